@@ -65,12 +65,13 @@ typedef enum {
   MOE_OK = 0,
   MOE_ERR_ARG = -1,     /* NULL pointer, non-positive size, k > E, unknown name */
   MOE_ERR_SHAPE = -2,   /* shape outside what the kernels tile (see moe_config) */
-  MOE_ERR_ALIGN = -3,   /* a pointer is not 16-byte aligned */
+  MOE_ERR_ALIGN = -3,   /* a pointer is not 16-byte aligned (around the layer: not as its entry point says) */
   MOE_ERR_CUDA = -4,    /* a CUDA runtime / driver call or a launch failed */
   MOE_ERR_DEVICE = -5,  /* current device is not sm_103 / sm_100 family */
   MOE_ERR_TIMEOUT = -6, /* device side: a bounded wait inside a kernel ran out */
-  MOE_ERR_BOUNDS = -7   /* device side, debug builds only (compiled with -DMOE_DEBUG): an index
-                           read from a buffer fell outside its range; the access was skipped */
+  MOE_ERR_BOUNDS = -7   /* device side: an index read from a buffer fell outside its range; the
+                           access was skipped (the layer: debug builds only, compiled with
+                           -DMOE_DEBUG; the grouped products' offsets: every build) */
 } moe_status;
 
 /* moe_config.flags bits */
@@ -378,9 +379,141 @@ int moe_backward(const moe_config *cfg, const void *dy, const void *x, const moe
 int moe_route_noalloc(const moe_config *cfg, const float *logits, int32_t *idx, float *w,
                       int32_t *counts, int32_t *offsets, int32_t *perm, moe_stream_t stream);
 
+/*
+ * ======================================================================
+ * Around the layer: what a model needs next to the block.  The pages have no
+ * counterpart; these entry points are additions of this library.
+ * ======================================================================
+ * They follow the conventions at the top with these differences, which hold
+ * for every entry point below: element types are moe_elem values; the rows of
+ * a matrix may be strided (ld_* in elements, 0 = contiguous; the elements of a
+ * row are always adjacent); pointers need only their element's alignment
+ * (MOE_ERR_ALIGN otherwise; offsets, ids and fp32 statistics 4 bytes or their
+ * own size, workspaces 16 bytes), and 16-byte aligned rows take the faster
+ * kernels; a call over zero rows is valid and writes what does not depend on
+ * rows (zero weight gradients).  Sums, norms and statistics are fp32; each
+ * output is rounded once.
+ */
+typedef enum { MOE_ELEM_BF16 = 0, MOE_ELEM_FP16 = 1, MOE_ELEM_FP32 = 2 } moe_elem;
+
+/*
+ * Matrix products grouped by expert, ragged sizes.  Rows r of expert e are
+ * [offsets[e], offsets[e+1]) (int32 [E+1] on the device, ascending, as
+ * moe_route writes them; no padding); w [E, N, K].
+ *   forward:   y[r] = x[r] w[e]^T              x [rows, K] -> y [rows, N]
+ *   backward:  dx[r] = dy[r] w[e]              dy [rows, N] -> dx [rows, K]
+ *              dw[e] = sum_r dy[r]^T x[r]      -> dw [E, N, K] contiguous
+ * Rows below offsets[0] or at and above offsets[E] belong to no expert: their
+ * y and dx are written as zeros and what x and dy hold there (NaN included)
+ * is not used.  An expert without rows gets dw[e] = 0.
+ * dtype is the type of x, w, dy and dx (BF16 or FP16); out_dtype that of y or
+ * dw: dtype, or FP32.  accumulate = 1 adds to what dw holds instead of
+ * overwriting it (FP32 dw only; an expert without rows is left alone).
+ * ld_x: row stride of x and dx; ld_y: of y and dy; ld_w: of w's rows;
+ * ld_e: elements from one expert's matrix to the next.
+ * Offsets that descend or leave [0, rows] never cause an access out of range;
+ * moe_get_status(ws) then reports MOE_ERR_BOUNDS (in every build) and the
+ * outputs are unspecified.
+ * Limits: 1 <= E <= 65535, 1 <= N, K <= 2^20, rows < 2^31 - 256, strides below 2^31
+ * (MOE_ERR_SHAPE).  16-byte aligned rows and pointers run on the tensor cores
+ * through TMA, few rows in all (a generated token) on a kernel that streams
+ * the experts' weights, everything else on a plain tiled kernel.
+ */
+typedef struct {
+  int64_t rows;
+  int32_t E, N, K;
+  int32_t dtype, out_dtype; /* moe_elem */
+  int32_t accumulate;
+  int64_t ld_x, ld_y, ld_w, ld_e; /* 0 = contiguous */
+} moe_grouped_config;
+
+/* Bytes of scratch for one grouped call (0 on an invalid config). */
+size_t moe_grouped_workspace_bytes(const moe_grouped_config *cfg);
+int moe_grouped_forward(const moe_grouped_config *cfg, const void *x, const void *w, const int32_t *offsets, void *y,
+                        void *ws, moe_stream_t stream);
+/* dx or dw may be NULL (not both); x is not read without dw, w not without dx. */
+int moe_grouped_backward(const moe_grouped_config *cfg, const void *dy, const void *x, const void *w,
+                         const int32_t *offsets, void *dx, void *dw, void *ws, moe_stream_t stream);
+
+/*
+ * The norms around a block, fused with its gate and the residual:
+ *   n = w_post * f / rms(f)   with MOE_NORM_POST, else n = f
+ *   z = alpha * x + g * n     (z = alpha * x when f is NULL)
+ *   h = w_pre * z / rms(z)    with MOE_NORM_PRE: the next block's input
+ *   rms(v) = sqrt(mean(v^2) + eps) over the d elements of a row
+ * x is the residual stream, f the block's output; the gate g is none (1), one
+ * value per channel [d], per row [rows] or per element [rows, d].  w_post and
+ * w_pre are [d] or NULL (ones).  All of dtype (BF16, FP16 or FP32), ld_x of x
+ * and dx, ld_f of f and df, ld_z of z and dz, ld_h of h and dh, ld_g of a
+ * full gate and its gradient.
+ * forward writes z (may be NULL with MOE_NORM_PRE), h, and the reciprocal roots
+ * r_post = 1 / rms(f), r_pre = 1 / rms(z) [rows] fp32 that a backward needs
+ * (each may be NULL).  h comes from z before z is rounded.
+ * backward takes the gradients dz (NULL = none, with MOE_NORM_PRE) and dh, the
+ * forward's z, f, r_post and r_pre, and writes
+ *   dx = alpha * t, df, dgate (in the gate's shape), dw_post, dw_pre,
+ *   t = dz + the pre norm's gradient; any output may be NULL.
+ * Sums over rows run in a fixed order (bitwise reproducible).  z and r_pre are
+ * needed with MOE_NORM_PRE, f for df / dgate / dw_post, r_post with
+ * MOE_NORM_POST.  dx may be dz's buffer and df f's.
+ * Limits: 1 <= d <= 65536, rows < 2^31, eps >= 0 (MOE_ERR_SHAPE, MOE_ERR_ARG).
+ */
+#define MOE_NORM_POST 1
+#define MOE_NORM_PRE 2
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_ROW = 2, MOE_GATE_FULL = 3 } moe_gate;
+typedef struct {
+  int64_t rows;
+  int32_t d;
+  int32_t dtype; /* moe_elem */
+  int32_t flags; /* MOE_NORM_POST | MOE_NORM_PRE */
+  int32_t gate;  /* moe_gate */
+  float alpha, eps;
+  int64_t ld_x, ld_f, ld_z, ld_h, ld_g; /* 0 = d */
+} moe_norm_config;
+
+int moe_norm_forward(const moe_norm_config *cfg, const void *x, const void *f, const void *gate, const void *w_post,
+                     const void *w_pre, void *z, void *h, float *r_post, float *r_pre, moe_stream_t stream);
+/* Bytes of scratch of one moe_norm_backward call (0 on an invalid config). */
+size_t moe_norm_workspace_bytes(const moe_norm_config *cfg);
+int moe_norm_backward(const moe_norm_config *cfg, const void *dz, const void *dh, const void *z, const void *f,
+                      const void *gate, const void *w_post, const void *w_pre, const float *r_post,
+                      const float *r_pre, void *dx, void *df, void *dgate, void *dw_post, void *dw_pre, void *ws,
+                      moe_stream_t stream);
+
+/*
+ * Token embedding: out[t] = scale * table[ids[t]], a zero row for an id outside
+ * [0, V) (padding), and its gradient
+ *   dtable[v] = scale * sum of dout[t] over the t with ids[t] = v
+ * by sorting the tokens: each table row's sum runs over ascending t in fp32 in a
+ * fixed order and is rounded once (bitwise reproducible).  Ids outside [0, V)
+ * take no gradient.  accumulate = 0 writes every row of dtable (zeros where no
+ * token points); accumulate = 1 adds to the rows that tokens point to and
+ * leaves the others alone.
+ * ids: int32 or (ids64 = 1) int64 [rows].  table and out / dout are of dtype
+ * (BF16, FP16, FP32), dtable of grad_dtype (dtype or FP32).  ld_t: row stride
+ * of table and dtable; ld_o: of out and dout.
+ * Limits: rows < 2^30, 1 <= V < 2^31 - 1, 1 <= d <= 2^20 (MOE_ERR_SHAPE).
+ */
+typedef struct {
+  int64_t rows;
+  int64_t V;
+  int32_t d;
+  int32_t dtype, grad_dtype; /* moe_elem */
+  int32_t ids64, accumulate;
+  float scale;
+  int64_t ld_t, ld_o; /* 0 = d */
+} moe_embed_config;
+
+int moe_embed_forward(const moe_embed_config *cfg, const void *ids, const void *table, void *out,
+                      moe_stream_t stream);
+/* Bytes of scratch of one moe_embed_backward call (0 on an invalid config). */
+size_t moe_embed_workspace_bytes(const moe_embed_config *cfg);
+int moe_embed_backward(const moe_embed_config *cfg, const void *ids, const void *dout, void *dtable, void *ws,
+                       moe_stream_t stream);
+
 /* Synchronises `stream`, returns the device status word recorded in `ws`
- * (MOE_OK, MOE_ERR_TIMEOUT, or in a debug build MOE_ERR_BOUNDS; a timeout is
- * reported first when both happened) and clears it.  Returns MOE_ERR_CUDA if
+ * (MOE_OK, MOE_ERR_TIMEOUT, or MOE_ERR_BOUNDS -- from the layer only in a debug
+ * build; a timeout is reported first when both happened) and clears it.  Returns MOE_ERR_CUDA if
  * the stream reports a CUDA error. */
 int moe_get_status(void *ws, moe_stream_t stream);
 

@@ -25,6 +25,11 @@ STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported shape", -3: "pointer
           -4: "CUDA error", -5: "device is not sm_103", -6: "a device-side wait timed out",
           -7: "a device-side bounds check failed (debug build)"}
 
+MOE_ELEM_BF16, MOE_ELEM_FP16, MOE_ELEM_FP32 = 0, 1, 2
+MOE_NORM_POST, MOE_NORM_PRE = 1, 2
+MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_ROW, MOE_GATE_FULL = 0, 1, 2, 3
+GATES = {"none": MOE_GATE_NONE, "channel": MOE_GATE_CHANNEL, "row": MOE_GATE_ROW, "full": MOE_GATE_FULL}
+
 WEIGHT_FIELDS = ["gu", "gu_scale", "dn", "dn_scale", "gu_t", "gu_t_scale", "dn_t", "dn_t_scale",
                  "s_gu", "s_dn", "s_gu_t", "s_dn_t", "gu_gscale", "dn_gscale"]
 
@@ -38,6 +43,24 @@ class MoeWeights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in WEIGHT_FIELDS]
 
 
+class MoeGroupedConfig(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in ("E", "N", "K", "dtype", "out_dtype",
+                                                                          "accumulate")] + \
+               [(n, ctypes.c_int64) for n in ("ld_x", "ld_y", "ld_w", "ld_e")]
+
+
+class MoeNormConfig(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in ("d", "dtype", "flags", "gate")] + \
+               [("alpha", ctypes.c_float), ("eps", ctypes.c_float)] + \
+               [(n, ctypes.c_int64) for n in ("ld_x", "ld_f", "ld_z", "ld_h", "ld_g")]
+
+
+class MoeEmbedConfig(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("V", ctypes.c_int64)] + \
+               [(n, ctypes.c_int32) for n in ("d", "dtype", "grad_dtype", "ids64", "accumulate")] + \
+               [("scale", ctypes.c_float), ("ld_t", ctypes.c_int64), ("ld_o", ctypes.c_int64)]
+
+
 _lib = None
 EXPORTS = ["moe_workspace_bytes", "moe_saved_bytes", "moe_buffer_info", "moe_padded_rows",
            "moe_quantize_weights", "moe_quantize_mx", "moe_quantize_mx_both", "moe_prepare_weights",
@@ -45,7 +68,10 @@ EXPORTS = ["moe_workspace_bytes", "moe_saved_bytes", "moe_buffer_info", "moe_pad
            "moe_canonical_scales", "moe_transpose_bf16", "moe_route",
            "moe_forward", "moe_backward",
            "moe_get_status", "moe_status_string", "moe_trace_enable", "moe_trace_clear", "moe_trace_count",
-           "moe_trace_name", "moe_trace_ms", "moe_route_noalloc", "moe_router_forward", "moe_router_backward"]
+           "moe_trace_name", "moe_trace_ms", "moe_route_noalloc", "moe_router_forward", "moe_router_backward",
+           "moe_grouped_workspace_bytes", "moe_grouped_forward", "moe_grouped_backward", "moe_norm_forward",
+           "moe_norm_workspace_bytes", "moe_norm_backward", "moe_embed_forward", "moe_embed_workspace_bytes",
+           "moe_embed_backward"]
 
 
 def lib():
@@ -87,6 +113,14 @@ def lib():
         L.moe_trace_count.argtypes, L.moe_trace_count.restype = [], I
         L.moe_trace_name.argtypes, L.moe_trace_name.restype = [I], ctypes.c_char_p
         L.moe_trace_ms.argtypes, L.moe_trace_ms.restype = [I], ctypes.c_float
+        gp, npp, ep = (ctypes.POINTER(c) for c in (MoeGroupedConfig, MoeNormConfig, MoeEmbedConfig))
+        for fn, cp in ((L.moe_grouped_workspace_bytes, gp), (L.moe_norm_workspace_bytes, npp),
+                       (L.moe_embed_workspace_bytes, ep)):
+            fn.argtypes, fn.restype = [cp], Z
+        for fn, cp, n in ((L.moe_grouped_forward, gp, 5), (L.moe_grouped_backward, gp, 7), (L.moe_norm_forward, npp, 9),
+                          (L.moe_norm_backward, npp, 15), (L.moe_embed_forward, ep, 3),
+                          (L.moe_embed_backward, ep, 4)):
+            fn.argtypes, fn.restype = [cp] + [P] * n + [S], I
         _lib = L
     return _lib
 
@@ -208,6 +242,49 @@ def moe_backward(cfg, dy, x, W, saved, dx, dlogits, dW_gu, dW_dn, dWs_gu, dWs_dn
     return lib().moe_backward(ctypes.byref(cfg), _ptr(dy), _ptr(x), ctypes.byref(W), _ptr(saved), _ptr(dx),
                               _ptr(dlogits), _ptr(dW_gu), _ptr(dW_dn), _ptr(dWs_gu), _ptr(dWs_dn), _ptr(ws),
                               _stream(stream))
+
+
+def moe_grouped_workspace_bytes(cfg):
+    return lib().moe_grouped_workspace_bytes(ctypes.byref(cfg))
+
+
+def moe_grouped_forward(cfg, x, w, offsets, y, ws, stream=None):
+    return lib().moe_grouped_forward(ctypes.byref(cfg), _ptr(x), _ptr(w), _ptr(offsets), _ptr(y), _ptr(ws),
+                                     _stream(stream))
+
+
+def moe_grouped_backward(cfg, dy, x, w, offsets, dx, dw, ws, stream=None):
+    return lib().moe_grouped_backward(ctypes.byref(cfg), _ptr(dy), _ptr(x), _ptr(w), _ptr(offsets), _ptr(dx),
+                                      _ptr(dw), _ptr(ws), _stream(stream))
+
+
+def moe_norm_forward(cfg, x, f, gate, w_post, w_pre, z, h, r_post, r_pre, stream=None):
+    return lib().moe_norm_forward(ctypes.byref(cfg), _ptr(x), _ptr(f), _ptr(gate), _ptr(w_post), _ptr(w_pre),
+                                  _ptr(z), _ptr(h), _ptr(r_post), _ptr(r_pre), _stream(stream))
+
+
+def moe_norm_workspace_bytes(cfg):
+    return lib().moe_norm_workspace_bytes(ctypes.byref(cfg))
+
+
+def moe_norm_backward(cfg, dz, dh, z, f, gate, w_post, w_pre, r_post, r_pre, dx, df, dgate, dw_post, dw_pre, ws,
+                      stream=None):
+    return lib().moe_norm_backward(ctypes.byref(cfg), _ptr(dz), _ptr(dh), _ptr(z), _ptr(f), _ptr(gate),
+                                   _ptr(w_post), _ptr(w_pre), _ptr(r_post), _ptr(r_pre), _ptr(dx), _ptr(df),
+                                   _ptr(dgate), _ptr(dw_post), _ptr(dw_pre), _ptr(ws), _stream(stream))
+
+
+def moe_embed_forward(cfg, ids, table, out, stream=None):
+    return lib().moe_embed_forward(ctypes.byref(cfg), _ptr(ids), _ptr(table), _ptr(out), _stream(stream))
+
+
+def moe_embed_workspace_bytes(cfg):
+    return lib().moe_embed_workspace_bytes(ctypes.byref(cfg))
+
+
+def moe_embed_backward(cfg, ids, dout, dtable, ws, stream=None):
+    return lib().moe_embed_backward(ctypes.byref(cfg), _ptr(ids), _ptr(dout), _ptr(dtable), _ptr(ws),
+                                    _stream(stream))
 
 
 def moe_get_status(ws, stream=None):

@@ -1,0 +1,301 @@
+"""What a model needs around the MoE layer, on torch tensors: ragged matrix
+products grouped by expert, the norms around a block with its gate and
+residual scale, and the token embedding with its gradient (include/moe.h:
+moe_grouped_*, moe_norm_*, moe_embed_*).
+
+Plain functions: they check their arguments, allocate outputs and workspaces
+from torch and call the library; all arithmetic runs in its kernels.  They run
+on torch's current stream, or on `stream`, and do not synchronise.  The
+autograd functions and modules over them are in module.py.
+"""
+from functools import lru_cache
+
+import torch
+
+from . import (GATES, MOE_ELEM_BF16, MOE_ELEM_FP16, MOE_ELEM_FP32, MOE_NORM_POST, MOE_NORM_PRE, MoeEmbedConfig,
+               MoeGroupedConfig, MoeNormConfig, check, moe_embed_backward, moe_embed_forward,
+               moe_embed_workspace_bytes, moe_get_status, moe_grouped_backward, moe_grouped_forward,
+               moe_grouped_workspace_bytes, moe_norm_backward, moe_norm_forward, moe_norm_workspace_bytes)
+
+_ELEM = {torch.bfloat16: MOE_ELEM_BF16, torch.float16: MOE_ELEM_FP16, torch.float32: MOE_ELEM_FP32}
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _rows(t, name, cols, dtype=None, rows=None):
+    """A 2-D matrix on the current GPU whose rows are contiguous; its row stride."""
+    _need(t.dim() == 2 and t.shape[1] == cols and (rows is None or t.shape[0] == rows),
+          "%s has shape %s, expected [%s, %d]" % (name, tuple(t.shape), "rows" if rows is None else rows, cols))
+    _need(dtype is None or t.dtype == dtype, "%s is %s, expected %s" % (name, t.dtype, dtype))
+    _need(t.is_cuda, "%s is not on the GPU" % name)
+    if t.stride(1) != 1 and cols > 1 or (t.shape[0] > 1 and t.stride(0) < cols):
+        t = t.contiguous()
+    return t, (t.stride(0) if t.shape[0] > 1 else cols)
+
+
+def _out(t, name, rows, cols, dtype, device):
+    """The caller's output matrix (rows contiguous), or a new one; its row stride."""
+    if t is None:
+        return torch.empty((rows, cols), dtype=dtype, device=device), cols
+    _need(t.shape == (rows, cols) and t.dtype == dtype and t.is_cuda and (cols == 1 or t.stride(1) == 1) and
+          (rows <= 1 or t.stride(0) >= cols),
+          "%s must be a %s GPU matrix [%d, %d] with contiguous rows" % (name, dtype, rows, cols))
+    return t, (t.stride(0) if rows > 1 else cols)
+
+
+def _vector(t, name, n, dtype):
+    if t is None:
+        return None
+    _need(t.dim() == 1 and t.shape[0] == n and t.dtype == dtype and t.is_cuda,
+          "%s must be a %s GPU vector of %d" % (name, dtype, n))
+    return t.contiguous()
+
+
+def _ws(nbytes, device):
+    _need(nbytes > 0, "the library does not take these sizes")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _used_on(stream, *tensors):
+    """Memory from the current stream's pool that a call on another stream uses."""
+    if stream is None:
+        return
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+
+
+# ---------------------------------------------------------------- grouped products
+@lru_cache(maxsize=512)
+def _grouped_config(*fields):
+    return MoeGroupedConfig(*fields)
+
+
+def _grouped(x_rows, x_dtype, w, offsets, name):
+    _need(x_dtype in (torch.bfloat16, torch.float16), "%s must be bfloat16 or float16" % name)
+    _need(w.dim() == 3 and w.dtype == x_dtype and w.is_cuda, "w must be a %s GPU tensor [E, N, K]" % x_dtype)
+    E, N, K = w.shape
+    _need(offsets.dim() == 1 and offsets.shape[0] == E + 1 and offsets.dtype == torch.int32 and offsets.is_cuda,
+          "offsets must be an int32 GPU vector of E + 1 = %d" % (E + 1))
+    if (K > 1 and w.stride(2) != 1) or (N > 1 and w.stride(1) < K) or \
+            (E > 1 and w.stride(0) < (N - 1) * w.stride(1) + K):
+        w = w.contiguous()
+    return w, offsets.contiguous(), E, N, K, (w.stride(1) if N > 1 else K)
+
+
+def grouped_forward(x, w, offsets, *, out=None, out_dtype=None, return_workspace=False, stream=None):
+    """y [rows, N]: y[r] = x[r] w[e]^T for the rows offsets[e] <= r < offsets[e + 1]
+    of expert e (0 for a row of no expert).  x [rows, K] and w [E, N, K] bf16 or
+    fp16, offsets int32 [E + 1] on the GPU as moe_route writes them; y of x's
+    type or fp32 (out_dtype, or out's)."""
+    w, offsets, E, N, K, ld_w = _grouped(None, x.dtype, w, offsets, "x")
+    x, ld_x = _rows(x, "x", K)
+    out_dtype = out_dtype or (out.dtype if out is not None else x.dtype)
+    _need(out_dtype in (x.dtype, torch.float32), "y is of x's type or float32")
+    y, ld_y = _out(out, "out", x.shape[0], N, out_dtype, x.device)
+    ld_e = w.stride(0) if E > 1 else 0
+    cfg = _grouped_config(x.shape[0], E, N, K, _ELEM[x.dtype], _ELEM[out_dtype], 0, ld_x, ld_y, ld_w, ld_e)
+    ws = _ws(moe_grouped_workspace_bytes(cfg), x.device)
+    check(moe_grouped_forward(cfg, x, w, offsets, y, ws, stream))
+    _used_on(stream, x, w, offsets, y, ws)
+    return (y, ws) if return_workspace else y
+
+
+def grouped_backward(dy, x, w, offsets, *, dx=None, dw=None, need_dx=True, need_dw=True, dw_dtype=None,
+                     accumulate=False, return_workspace=False, stream=None):
+    """(dx [rows, K], dw [E, N, K]) of grouped_forward: dx[r] = dy[r] w[e], dw[e] =
+    sum of dy[r]^T x[r] over e's rows (zeros for an expert without rows), either
+    None when not needed.  dw is of x's type or fp32 (dw_dtype, or dw's); with
+    accumulate it must be given, fp32, and is added to."""
+    w, offsets, E, N, K, ld_w = _grouped(None, dy.dtype, w, offsets, "dy")
+    rows = dy.shape[0]
+    dy, ld_y = _rows(dy, "dy", N)
+    x, ld_x = _rows(x, "x", K, dy.dtype, rows)
+    dw_dtype = dw_dtype or (dw.dtype if dw is not None else dy.dtype)
+    _need(dw_dtype in (dy.dtype, torch.float32), "dw is of dy's type or float32")
+    _need(not accumulate or (dw is not None and dw_dtype == torch.float32), "accumulate adds to a given float32 dw")
+    _need(need_dx or need_dw, "nothing to compute")
+    if need_dx:
+        if dx is None:      # of x's row stride, which the library shares between the two
+            dx = torch.empty((rows, ld_x), dtype=dy.dtype, device=dy.device)[:, :K]
+        _need(dx.shape == (rows, K) and dx.dtype == dy.dtype and dx.is_cuda and (K == 1 or dx.stride(1) == 1),
+              "dx must be a %s GPU matrix [%d, %d] with contiguous rows" % (dy.dtype, rows, K))
+        if rows > 1 and dx.stride(0) != ld_x:
+            x, ld_x = x.contiguous(), K
+            _need(dx.stride(0) == K, "dx must have x's row stride or be contiguous")
+    if need_dw:
+        if dw is None:
+            dw = torch.empty((E, N, K), dtype=dw_dtype, device=dy.device)
+        _need(dw.shape == (E, N, K) and dw.dtype == dw_dtype and dw.is_cuda and dw.is_contiguous(),
+              "dw must be a contiguous %s GPU tensor [%d, %d, %d]" % (dw_dtype, E, N, K))
+    ld_e = w.stride(0) if E > 1 else 0
+    cfg = _grouped_config(rows, E, N, K, _ELEM[dy.dtype], _ELEM[dw_dtype], int(accumulate), ld_x, ld_y, ld_w, ld_e)
+    ws = _ws(moe_grouped_workspace_bytes(cfg), dy.device)
+    out = (dx if need_dx else None, dw if need_dw else None)
+    check(moe_grouped_backward(cfg, dy, x, w, offsets, out[0], out[1], ws, stream))
+    _used_on(stream, dy, x, w, offsets, out[0], out[1], ws)
+    return out + (ws,) if return_workspace else out
+
+
+def grouped_status(ws, stream=None):
+    """Synchronises; the device status of the call that used workspace `ws`
+    (return_workspace=True): 0, or -7 when its offsets descend or leave the rows."""
+    return moe_get_status(ws, stream)
+
+
+# ---------------------------------------------------------------- block norms
+@lru_cache(maxsize=512)
+def _norm_config(*fields):
+    return MoeNormConfig(*fields)
+
+
+def _gate(gate, kind, rows, d, dtype):
+    _need(kind in GATES, "gate_kind is one of %s" % sorted(GATES))
+    _need((gate is None) == (kind == "none"), "a gate goes with its kind (channel, row or full)")
+    if kind == "none":
+        return None, d
+    if kind == "full":
+        return _rows(gate, "gate", d, dtype, rows)
+    return _vector(gate, "gate", d if kind == "channel" else rows, dtype), d
+
+
+def norm_forward(x, f=None, gate=None, w_post=None, w_pre=None, *, gate_kind="none", post=True, pre=True, alpha=1.0,
+                 eps=1e-6, need_z=True, z=None, h=None, stream=None):
+    """(z, h, r_post, r_pre):
+        z = alpha x + g n,  n = w_post f / rms(f) (post) or f,  h = w_pre z / rms(z) (pre).
+    x [rows, d] is the residual stream, f [rows, d] the block's output (None: z =
+    alpha x), gate [d], [rows] or [rows, d] by gate_kind "channel", "row" or
+    "full"; w_post and w_pre [d] or None (ones); all of one type (bf16, fp16,
+    fp32).  r_post, r_pre [rows] fp32 are the reciprocal roots for the backward;
+    what is not computed comes back as None."""
+    _need(x.dim() == 2 and x.dtype in _ELEM, "x must be a bf16, fp16 or fp32 matrix [rows, d]")
+    rows, d = x.shape
+    x, ld_x = _rows(x, "x", d)
+    ld_f, post = d, post and f is not None
+    if f is not None:
+        f, ld_f = _rows(f, "f", d, x.dtype, rows)
+    _need(f is not None or gate is None, "a gate needs the block's output f")
+    _need(pre or need_z, "nothing to compute")
+    gate, ld_g = _gate(gate, gate_kind, rows, d, x.dtype)
+    w_post = _vector(w_post, "w_post", d, x.dtype) if post else None
+    w_pre = _vector(w_pre, "w_pre", d, x.dtype) if pre else None
+    dev, ld_z, ld_h, r_post, r_pre = x.device, d, d, None, None
+    if need_z:
+        z, ld_z = _out(z, "z", rows, d, x.dtype, dev)
+    if pre:
+        h, ld_h = _out(h, "h", rows, d, x.dtype, dev)
+        r_pre = torch.empty(rows, dtype=torch.float32, device=dev)
+    if post:
+        r_post = torch.empty(rows, dtype=torch.float32, device=dev)
+    cfg = _norm_config(rows, d, _ELEM[x.dtype], (MOE_NORM_POST if post else 0) | (MOE_NORM_PRE if pre else 0),
+                       GATES[gate_kind], alpha, eps, ld_x, ld_f, ld_z, ld_h, ld_g)
+    z, h = z if need_z else None, h if pre else None
+    check(moe_norm_forward(cfg, x, f, gate, w_post, w_pre, z, h, r_post, r_pre, stream))
+    _used_on(stream, x, f, gate, w_post, w_pre, z, h, r_post, r_pre)
+    return z, h, r_post, r_pre
+
+
+def norm_backward(dz, dh, z, f=None, gate=None, w_post=None, w_pre=None, r_post=None, r_pre=None, *, gate_kind="none",
+                  post=True, pre=True, alpha=1.0, need_dx=True, need_df=True, need_dgate=True, need_dw=True,
+                  stream=None):
+    """(dx, df, dgate, dw_post, dw_pre) of norm_forward from the gradients dz
+    (None: nothing but h is used) and dh, its z, f and reciprocal roots; what
+    does not exist or is not needed comes back as None."""
+    like = dz if dz is not None else dh
+    _need(like is not None and like.dim() == 2 and like.dtype in _ELEM, "dz or dh must be a bf16, fp16 or fp32 matrix")
+    rows, d = like.shape
+    dt, dev, post = like.dtype, like.device, post and f is not None
+    _need(pre or dz is not None, "without the pre norm the gradient arrives in dz")
+    ld_z, ld_h, ld_f = d, d, d
+    if dz is not None:
+        dz, ld_z = _rows(dz, "dz", d, dt, rows)
+    if pre:
+        _need(dh is not None and z is not None and r_pre is not None, "the pre norm needs dh, z and r_pre")
+        dh, ld_h = _rows(dh, "dh", d, dt, rows)
+        z, ld = _rows(z, "z", d, dt, rows)
+        if dz is not None and ld != ld_z and rows > 1:      # the library has one stride for the two
+            dz, z, ld = dz.contiguous(), z.contiguous(), d
+        ld_z = ld
+        r_pre = _vector(r_pre, "r_pre", rows, torch.float32)
+    if f is not None:
+        f, ld_f = _rows(f, "f", d, dt, rows)
+    if post:
+        _need(r_post is not None, "the post norm needs r_post")
+        r_post = _vector(r_post, "r_post", rows, torch.float32)
+    gate, ld_g = _gate(gate, gate_kind, rows, d, dt)
+    w_post = _vector(w_post, "w_post", d, dt) if post else None
+    w_pre = _vector(w_pre, "w_pre", d, dt) if pre else None
+
+    def new(need, *shape):
+        return torch.empty(shape, dtype=dt, device=dev) if need else None
+
+    dx = new(need_dx, rows, d)
+    df = dgate = None
+    if f is not None and need_df:       # shares f's row stride
+        df = torch.empty((rows, ld_f), dtype=dt, device=dev)[:, :d]
+    if gate is not None and need_dgate:
+        dgate = torch.empty((rows, ld_g), dtype=dt, device=dev)[:, :d] if gate_kind == "full" else \
+            torch.empty_like(gate)
+    dw_post, dw_pre = new(need_dw and w_post is not None, d), new(need_dw and w_pre is not None, d)
+    cfg = _norm_config(rows, d, _ELEM[dt], (MOE_NORM_POST if post else 0) | (MOE_NORM_PRE if pre else 0),
+                       GATES[gate_kind], alpha, 0.0, d, ld_f, ld_z, ld_h, ld_g)
+    ws = _ws(moe_norm_workspace_bytes(cfg), dev)
+    check(moe_norm_backward(cfg, dz, dh, z, f, gate, w_post, w_pre, r_post, r_pre, dx, df, dgate, dw_post, dw_pre, ws,
+                            stream))
+    _used_on(stream, dz, dh, z, f, gate, w_post, w_pre, r_post, r_pre, dx, df, dgate, dw_post, dw_pre, ws)
+    return dx, df, dgate, dw_post, dw_pre
+
+
+# ---------------------------------------------------------------- embedding
+@lru_cache(maxsize=512)
+def _embed_config(*fields):
+    return MoeEmbedConfig(*fields)
+
+
+def _ids(ids):
+    _need(ids.dtype in (torch.int32, torch.int64) and ids.is_cuda, "ids must be int32 or int64 on the GPU")
+    return ids.reshape(-1).contiguous()
+
+
+def embed_forward(ids, table, *, scale=1.0, out=None, stream=None):
+    """scale * table[ids] [*ids.shape, d]; an id outside [0, V) (padding) gives a
+    zero row.  table [V, d] bf16, fp16 or fp32; ids int32 or int64 of any shape.
+    `out` [ids.numel(), d] may be given."""
+    _need(table.dim() == 2 and table.dtype in _ELEM, "table must be a bf16, fp16 or fp32 matrix [V, d]")
+    V, d = table.shape
+    table, ld_t = _rows(table, "table", d)
+    flat = _ids(ids)
+    rows, el = flat.shape[0], _ELEM[table.dtype]
+    res, ld_o = _out(out, "out", rows, d, table.dtype, table.device)
+    cfg = _embed_config(rows, V, d, el, el, int(flat.dtype == torch.int64), 0, scale, ld_t, ld_o)
+    check(moe_embed_forward(cfg, flat, table, res, stream))
+    _used_on(stream, flat, table, res)
+    return res if out is not None else res.view(*ids.shape, d)
+
+
+def embed_backward(ids, dout, V, *, scale=1.0, dtable=None, grad_dtype=None, accumulate=False, stream=None):
+    """dtable [V, d]: dtable[v] = scale * sum of dout[t] over ids[t] = v, in
+    ascending t.  dout [ids.numel(), d] (or [*ids.shape, d]); dtable of dout's
+    type or fp32 (grad_dtype, or dtable's).  accumulate adds to the given
+    dtable's rows that occur and leaves the others alone."""
+    flat = _ids(ids)
+    _need(dout.dtype in _ELEM and dout.dim() >= 2, "dout must be bf16, fp16 or fp32 [rows, d]")
+    d = dout.shape[-1]
+    if dout.dim() != 2:
+        dout = dout.reshape(-1, d)
+    dout, ld_o = _rows(dout, "dout", d, None, flat.shape[0])
+    _need(not accumulate or dtable is not None, "accumulate adds to a given dtable")
+    grad_dtype = grad_dtype or (dtable.dtype if dtable is not None else dout.dtype)
+    _need(grad_dtype in (dout.dtype, torch.float32), "dtable is of dout's type or float32")
+    dtable, ld_t = _out(dtable, "dtable", V, d, grad_dtype, dout.device)
+    cfg = _embed_config(flat.shape[0], V, d, _ELEM[dout.dtype], _ELEM[grad_dtype], int(flat.dtype == torch.int64),
+                        int(accumulate), scale, ld_t, ld_o)
+    ws = _ws(moe_embed_workspace_bytes(cfg), dout.device)
+    check(moe_embed_backward(cfg, flat, dout, dtable, ws, stream))
+    _used_on(stream, flat, dout, dtable, ws)
+    return dtable

@@ -17,6 +17,7 @@
 #include <mutex>
 
 #include "../../include/moe.h"
+#include "block.h"
 #include "kernels.h"
 
 namespace {
@@ -1395,3 +1396,44 @@ const char *moe_status_string(int status) {
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------- host services of block_api.cu
+namespace moe {
+
+int host_device(int *num_sms) {
+  DeviceInfo d;
+  const int rc = device_info(&d);
+  if (rc == MOE_OK) *num_sms = d.num_sms;
+  return rc;
+}
+
+bool host_encode_map(CUtensorMap *m, int elem, const void *base, int rank, const uint64_t *dims,
+                     const uint64_t *strides_bytes, const uint32_t *box) {
+  cuuint64_t d[5], st[4];
+  cuuint32_t b[5], es[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    b[i] = box[i];
+    es[i] = 1;
+    if (i + 1 < rank) st[i] = strides_bytes[i];
+  }
+  const CUtensorMapDataType t = elem == MOE_ELEM_FP32   ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                : elem == MOE_ELEM_FP16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                        : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  return g_encode(m, t, rank, const_cast<void *>(base), d, st, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+HostTrace::HostTrace(const char *name, cudaStream_t stream) : slot(-1), s(stream) {
+  if (g_trace.count < g_trace.capacity) {
+    slot = g_trace.count++;
+    g_trace.name[slot] = name;
+    cudaEventRecord(g_trace.start[slot], s);
+  }
+}
+HostTrace::~HostTrace() {
+  if (slot >= 0) cudaEventRecord(g_trace.end[slot], s);
+}
+
+}  // namespace moe

@@ -1,0 +1,88 @@
+// Internal launchers of the operators around the layer (ragged grouped
+// products, block norms, token embedding).  All launches are asynchronous on
+// the given stream and return the launch error.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "../../include/moe.h"
+
+namespace moe {
+
+// ---------------------------------------------------------------- host services (api.cu)
+// The current device's SM count after checking that it is an sm_103 part and
+// that the tensor-map encoder is there: MOE_OK or a moe_status.
+int host_device(int *num_sms);
+// A tiled tensor map, 128-byte swizzle, zero fill out of bounds.
+bool host_encode_map(CUtensorMap *m, int elem, const void *base, int rank, const uint64_t *dims,
+                     const uint64_t *strides_bytes, const uint32_t *box);
+// Brackets a launch with the trace's events when tracing is on (moe_trace_enable).
+struct HostTrace {
+  int slot;
+  cudaStream_t s;
+  HostTrace(const char *name, cudaStream_t stream);
+  ~HostTrace();
+};
+
+// ---------------------------------------------------------------- grouped products
+// One product of the three directions as a strided matrix product per group:
+//   out[m, n] (+)= sum_k a[m, k] b[n, k]
+// with element (i, k) of an operand at base + i * s_i + k * s_k.
+enum GroupedDir { GROUPED_FWD = 0, GROUPED_DGRAD = 1, GROUPED_WGRAD = 2 };
+
+struct GroupedArgs {
+  int E, N, K;
+  int rows;
+  int dtype, out_dtype;  // moe_elem; out_dtype of y / dw (dx has dtype)
+  int accumulate;
+  long ld_x, ld_y, ld_w, ld_e;
+  const int *offsets;  // [E + 1]
+  const void *x, *w, *dy;
+  void *y, *dx, *dw;
+  int *status;   // workspace status word
+  int *tiles;    // workspace: [E + 1] first token tile of every expert
+  uint8_t *maps; // workspace: 2 E tensor maps of 128 bytes (weight gradient)
+};
+
+// Status word and, where `tiles` / map templates are given, the tile table and
+// the experts' tensor maps; zeroes the rows of `out` that belong to no expert.
+cudaError_t launch_grouped_plan(const GroupedArgs &g, int tile_rows, void *out, int out_elem, int out_cols,
+                                long ld_out, cudaStream_t s);
+int grouped_plain_tile_rows();
+cudaError_t launch_grouped_plain(const GroupedArgs &g, int dir, cudaStream_t s);
+
+// ---------------------------------------------------------------- block norms
+struct NormArgs {
+  int rows, d, dtype, flags, gate;
+  float alpha, eps;
+  long ld_x, ld_f, ld_z, ld_h, ld_g;
+  const void *x, *f, *g, *w_post, *w_pre;
+  void *z, *h;
+  float *r_post, *r_pre;
+  // backward
+  const void *dz, *dh, *zin;
+  const float *r_post_in, *r_pre_in;
+  void *dx, *df, *dg, *dw_post, *dw_pre;
+  float *part;  // workspace: [blocks][2][d] column sums of a block's rows
+};
+constexpr int kNormMaxBlocks = 152 * 4;
+cudaError_t launch_norm_forward(const NormArgs &a, int num_sms, cudaStream_t s);
+cudaError_t launch_norm_backward(const NormArgs &a, int num_sms, cudaStream_t s);
+
+// ---------------------------------------------------------------- embedding
+struct EmbedArgs {
+  int rows, V, d, dtype, grad_dtype, ids64, accumulate;
+  float scale;
+  long ld_t, ld_o;
+  const void *ids, *table, *dout;
+  void *out, *dtable;
+  // workspace of the backward (offsets from embed_workspace)
+  uint8_t *ws;
+};
+size_t embed_workspace(int rows, long V, int d);
+cudaError_t launch_embed_forward(const EmbedArgs &a, cudaStream_t s);
+cudaError_t launch_embed_backward(const EmbedArgs &a, int num_sms, cudaStream_t s);
+
+}  // namespace moe

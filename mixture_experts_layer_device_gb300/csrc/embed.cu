@@ -1,0 +1,482 @@
+// Token embedding and its gradient.
+//   out[t] = scale table[ids[t]];   dtable[v] = scale sum over ids[t] = v of dout[t]
+// The gradient sorts the tokens by id (stable), so that the rows of one id lie
+// next to each other in ascending token order, and cuts the sorted list into
+// pieces of kPiece tokens.  A block sums a piece's runs in fp32; a run that lies
+// inside its piece is final, one that crosses into others leaves a partial row,
+// and a last pass joins the partial rows of such a run in order.  A frequent id
+// is so spread over many blocks, and every sum has one fixed order.
+//
+// HBM bound: forward one row in, one out per token; backward one row in per
+// token and the whole table out (or, accumulating, the rows that occur, twice).
+#include "block.h"
+#include "elem.cuh"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kPiece = 32;      // sorted tokens per block of the sums
+constexpr int kSmallSort = 2048;  // up to here every token counts its rank
+constexpr int kSortBlock = 256;   // threads of a radix block
+constexpr int kSortItems = 8;     // keys per thread and block
+constexpr int kSortChunk = kSortBlock * kSortItems;
+constexpr int kMaxDigits = 1024;  // 10-bit digits at most
+
+// Table row of token t, or V for an id outside the table.
+MOE_DEV int key_of(const EmbedArgs &a, long t) {
+  if (a.ids64) {
+    const long long v = static_cast<const long long *>(a.ids)[t];
+    return (v >= 0 && v < a.V) ? static_cast<int>(v) : a.V;
+  }
+  const int v = static_cast<const int *>(a.ids)[t];
+  return (v >= 0 && v < a.V) ? v : a.V;
+}
+
+// ---------------------------------------------------------------- forward
+// A warp takes 32 x UN chunks (16 bytes each) of one row at a time, all its
+// loads in flight before the first store.
+template <typename T, int VEC, int UN>
+__global__ void __launch_bounds__(256) embed_fwd_kernel(const EmbedArgs a, int spans) {
+  const int lane = threadIdx.x & 31;
+  const long warps = static_cast<long>(gridDim.x) * (blockDim.x >> 5);
+  const long total = static_cast<long>(a.rows) * spans;
+  for (long u = static_cast<long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); u < total; u += warps) {
+    const long row = u / spans;
+    const int c0 = static_cast<int>(u - row * spans) * 32 * UN * VEC + lane * VEC;
+    const int key = key_of(a, row);
+    T *dst = static_cast<T *>(a.out) + row * a.ld_o;
+    const T *src = static_cast<const T *>(a.table) + static_cast<long>(key) * a.ld_t;
+    if constexpr (VEC > 1) {
+      uint4 q[UN];
+#pragma unroll
+      for (int i = 0; i < UN; ++i) {
+        q[i] = make_uint4(0, 0, 0, 0);
+        if (key < a.V && c0 + i * 32 * VEC < a.d) q[i] = __ldg(reinterpret_cast<const uint4 *>(src + c0 + i * 32 * VEC));
+      }
+#pragma unroll
+      for (int i = 0; i < UN; ++i) {
+        if (c0 + i * 32 * VEC >= a.d) continue;
+        float v[VEC];
+        Elem<T>::unpack(q[i], v);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) v[k] = key < a.V ? v[k] * a.scale : 0.f;
+        st_stream(dst + c0 + i * 32 * VEC, Elem<T>::pack(v));
+      }
+    } else {
+      T q[UN];
+#pragma unroll
+      for (int i = 0; i < UN; ++i) {
+        q[i] = Elem<T>::from(0.f);
+        if (key < a.V && c0 + i * 32 < a.d) q[i] = src[c0 + i * 32];
+      }
+#pragma unroll
+      for (int i = 0; i < UN; ++i)
+        if (c0 + i * 32 < a.d) dst[c0 + i * 32] = Elem<T>::from(key < a.V ? Elem<T>::to(q[i]) * a.scale : 0.f);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- sort
+// Few tokens: a token's place is the number of tokens that come before it.
+// One launch instead of a radix pass' three per digit; 2,048 comparisons a
+// thread at most.  Also marks the table rows that occur.
+__global__ void __launch_bounds__(256) embed_rank_kernel(const EmbedArgs a, int *keys, int *pos, uint8_t *used) {
+  __shared__ int sk[kSmallSort];
+  for (int i = threadIdx.x; i < a.rows; i += blockDim.x) sk[i] = key_of(a, i);
+  __syncthreads();
+  const int t = blockIdx.x * blockDim.x + threadIdx.x;
+  if (t >= a.rows) return;
+  const int key = sk[t];
+  int rank = 0;
+  for (int i = 0; i < a.rows; ++i) rank += (sk[i] < key) || (sk[i] == key && i < t);
+  keys[rank] = key;
+  pos[rank] = t;
+  if (used && key < a.V) used[key] = 1;
+}
+
+// One digit of the least-significant-digit radix sort: histogram per block,
+// prefix over the blocks of every digit, stable scatter.  `keys` NULL: the ids.
+__global__ void __launch_bounds__(kSortBlock) embed_hist_kernel(const EmbedArgs a, const int *keys, int shift,
+                                                                int digits, int *hist, uint8_t *used) {
+  __shared__ int h[kMaxDigits];
+  for (int i = threadIdx.x; i < digits; i += kSortBlock) h[i] = 0;
+  __syncthreads();
+  const long base = static_cast<long>(blockIdx.x) * kSortChunk;
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k) {
+    const long i = base + k * kSortBlock + threadIdx.x;
+    if (i < a.rows) {
+      const int key = keys ? keys[i] : key_of(a, i);
+      atomicAdd(&h[(key >> shift) & (digits - 1)], 1);
+      if (used && key < a.V) used[key] = 1;
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < digits; i += kSortBlock) hist[static_cast<long>(i) * gridDim.x + blockIdx.x] = h[i];
+}
+
+// Exclusive prefix of one digit's block counts (a warp per digit), its total.
+__global__ void __launch_bounds__(256) embed_scan_kernel(int *hist, int blocks, int digits, int *total) {
+  const int digit = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (digit >= digits) return;
+  int *h = hist + static_cast<long>(digit) * blocks;
+  int run = 0;
+  for (int b = 0; b < blocks; b += 32) {
+    const int v = b + lane < blocks ? h[b + lane] : 0;
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += n;
+    }
+    if (b + lane < blocks) h[b + lane] = run + inc - v;
+    run += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  if (lane == 0) total[digit] = run;
+}
+
+// Block offset of `digits` totals: exclusive prefix into out[] by one warp.
+MOE_DEV void warp_prefix(const int *total, int digits, int *out) {
+  const int lane = threadIdx.x & 31;
+  int run = 0;
+  for (int i = 0; i < digits; i += 32) {
+    const int v = i + lane < digits ? total[i + lane] : 0;
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += n;
+    }
+    if (i + lane < digits) out[i + lane] = run + inc - v;
+    run += __shfl_sync(0xffffffffu, inc, 31);
+  }
+}
+
+__global__ void __launch_bounds__(kSortBlock) embed_scatter_kernel(const EmbedArgs a, const int *keys, const int *pos,
+                                                                   int shift, int digits, const int *hist,
+                                                                   const int *total, int *keys_out, int *pos_out) {
+  // next[w][digit]: where warp w's next key of a digit goes
+  extern __shared__ int next[];
+  __shared__ int base[kMaxDigits];
+  constexpr int W = kSortBlock / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < W * digits; i += kSortBlock) next[i] = 0;
+  if (warp == 0) warp_prefix(total, digits, base);
+  __syncthreads();
+  // a warp owns kSortItems consecutive groups of 32 keys
+  const long first = static_cast<long>(blockIdx.x) * kSortChunk + warp * 32 * kSortItems + lane;
+  int key[kSortItems], ps[kSortItems];
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k) {
+    const long i = first + k * 32;
+    key[k] = -1;
+    if (i < a.rows) {
+      key[k] = keys ? keys[i] : key_of(a, i);
+      ps[k] = pos ? pos[i] : static_cast<int>(i);
+      atomicAdd(&next[warp * digits + ((key[k] >> shift) & (digits - 1))], 1);
+    }
+  }
+  __syncthreads();
+  for (int dg = threadIdx.x; dg < digits; dg += kSortBlock) {
+    int at = base[dg] + hist[static_cast<long>(dg) * gridDim.x + blockIdx.x];
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const int n = next[w * digits + dg];
+      next[w * digits + dg] = at;
+      at += n;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kSortItems; ++k) {
+    const bool in = key[k] >= 0;
+    const int dg = in ? (key[k] >> shift) & (digits - 1) : digits;  // keys out of range form their own group
+    const unsigned same = __match_any_sync(0xffffffffu, dg);
+    const int before = __popc(same & ((1u << lane) - 1));
+    int at = 0;
+    if (in) at = next[warp * digits + dg] + before;
+    __syncwarp();
+    if (in && before == 0) next[warp * digits + dg] += __popc(same);
+    __syncwarp();
+    if (in) {
+      keys_out[at] = key[k];
+      pos_out[at] = ps[k];
+    }
+  }
+}
+
+// ---------------------------------------------------------------- sums
+// Writes (or adds) a finished fp32 sum of VEC columns to the table.
+template <typename G, int VEC>
+MOE_DEV void put_grad(const EmbedArgs &a, int key, int c, const float *acc) {
+  G *dst = static_cast<G *>(a.dtable) + static_cast<long>(key) * a.ld_t + c;
+  float v[VEC];
+#pragma unroll
+  for (int k = 0; k < VEC; ++k) {
+    v[k] = acc[k] * a.scale;
+    if (a.accumulate) v[k] += Elem<G>::to(dst[k]);
+  }
+  if constexpr (VEC == Elem<G>::VEC) {
+    st_stream(dst, Elem<G>::pack(v));
+  } else if constexpr (VEC == 2 * Elem<G>::VEC) {
+    st_stream(dst, Elem<G>::pack(v));
+    st_stream(dst + VEC / 2, Elem<G>::pack(v + VEC / 2));
+  } else {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) dst[k] = Elem<G>::from(v[k]);
+  }
+}
+
+// Rows of one piece (blockIdx.y) x 128 threads' columns.  part[2 p] takes the
+// run that comes in from piece p - 1, part[2 p + 1] the one that starts here
+// and goes on in piece p + 1.
+template <typename T, typename G, int VEC>
+__global__ void __launch_bounds__(128) embed_sum_kernel(const EmbedArgs a, const int *keys, const int *pos, float *part) {
+  __shared__ int sk[kPiece], sp[kPiece];
+  const int piece = blockIdx.x;
+  const int first = piece * kPiece;
+  const int n = a.rows - first < kPiece ? a.rows - first : kPiece;
+  if (threadIdx.x < n) {
+    sk[threadIdx.x] = keys[first + threadIdx.x];
+    sp[threadIdx.x] = pos[first + threadIdx.x];
+  }
+  const int before = first > 0 ? keys[first - 1] : -1;
+  const int after = first + n < a.rows ? keys[first + n] : -1;
+  __syncthreads();
+  const int c = (blockIdx.y * 128 + threadIdx.x) * VEC;
+  if (c >= a.d) return;
+  float acc[VEC];
+#pragma unroll
+  for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
+  constexpr int U = VEC > 1 ? 8 : 16;
+  int run = 0;  // first token of the current run
+  for (int j0 = 0; j0 < n; j0 += U) {
+    uint4 q[U];
+    T q1[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (j0 + u < n && sk[j0 + u] < a.V) {
+        const T *p = static_cast<const T *>(a.dout) + static_cast<long>(sp[j0 + u]) * a.ld_o + c;
+        if constexpr (VEC > 1) q[u] = ld_stream(p);
+        else q1[u] = *p;
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + u;
+      if (j >= n) break;
+      const int key = sk[j];
+      if (key >= a.V) break;  // padding sorts last
+      float v[VEC];
+      if constexpr (VEC > 1) Elem<T>::unpack(q[u], v);
+      else v[0] = Elem<T>::to(q1[u]);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) acc[k] += v[k];
+      const int nextkey = j + 1 < n ? sk[j + 1] : after;
+      const bool ends = j + 1 == n || nextkey != key;
+      if (ends) {
+        const bool came = run == 0 && before == key, goes = nextkey == key;
+        if (!came && !goes) {
+          put_grad<G, VEC>(a, key, c, acc);
+        } else {
+          float *p = part + (static_cast<long>(piece) * 2 + (came ? 0 : 1)) * a.d + c;
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) p[k] = acc[k];
+        }
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
+        run = j + 1;
+      }
+    }
+  }
+}
+
+// Joins the runs that cross pieces: the block of the piece where such a run
+// starts adds the following pieces' partial rows in order.
+template <typename G>
+__global__ void __launch_bounds__(128) embed_join_kernel(const EmbedArgs a, const int *keys, int pieces, const float *part) {
+  const int piece = blockIdx.x;
+  const int last = piece * kPiece + kPiece - 1;
+  if (last + 1 >= a.rows) return;
+  const int key = keys[last];
+  if (key >= a.V || keys[last + 1] != key) return;          // no run goes on
+  if (piece > 0 && keys[piece * kPiece] == key && keys[piece * kPiece - 1] == key) return;  // it did not start here
+  // the last piece that the run reaches: the first token of a piece has its key
+  int lo = piece + 1, hi = pieces - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (keys[mid * kPiece] == key) lo = mid;
+    else hi = mid - 1;
+  }
+  const int c = blockIdx.y * 128 + threadIdx.x;
+  if (c >= a.d) return;
+  float acc = part[(static_cast<long>(piece) * 2 + 1) * a.d + c];
+  int p = piece + 1;
+  for (; p + 7 <= lo; p += 8) {
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = part[static_cast<long>(p + u) * 2 * a.d + c];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) acc += v[u];
+  }
+  for (; p <= lo; ++p) acc += part[static_cast<long>(p) * 2 * a.d + c];
+  put_grad<G, 1>(a, key, c, &acc);
+}
+
+// Zeros for the table rows that no token points to.
+template <typename G, int VEC>
+__global__ void __launch_bounds__(256) embed_zero_kernel(const EmbedArgs a, const uint8_t *used) {
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  for (long v = static_cast<long>(blockIdx.x) * warps + (threadIdx.x >> 5); v < a.V;
+       v += static_cast<long>(gridDim.x) * warps) {
+    if (used[v]) continue;
+    G *dst = static_cast<G *>(a.dtable) + v * a.ld_t;
+    if constexpr (VEC > 1) {
+      for (int c = lane * VEC; c < a.d; c += 32 * VEC) st_stream(dst + c, make_uint4(0, 0, 0, 0));
+    } else {
+      for (int c = lane; c < a.d; c += 32) dst[c] = Elem<G>::from(0.f);
+    }
+  }
+}
+
+struct EmbedWs {
+  size_t keys[2], pos[2], hist, total, used, part, bytes;
+};
+
+EmbedWs ws_layout(int rows, long V, int d) {
+  EmbedWs w;
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t o = at;
+    at += (n + 255) / 256 * 256;
+    return o;
+  };
+  const size_t T = rows, blocks = (T + kSortChunk - 1) / kSortChunk, pieces = (T + kPiece - 1) / kPiece;
+  for (int i = 0; i < 2; ++i) {
+    w.keys[i] = take(T * 4);
+    w.pos[i] = take(T * 4);
+  }
+  w.hist = take(blocks * kMaxDigits * 4);
+  w.total = take(kMaxDigits * 4);
+  w.used = take(V);
+  w.part = take(pieces * 2 * d * 4);
+  w.bytes = at;
+  return w;
+}
+
+bool vec16(const void *p, long ld, int esz) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * esz) % 16 == 0;
+}
+
+template <typename T>
+cudaError_t fwd_type(const EmbedArgs &a, cudaStream_t s) {
+  const int e = sizeof(T);
+  const bool vec = vec16(a.table, a.ld_t, e) && vec16(a.out, a.ld_o, e) && (static_cast<long>(a.d) * e) % 16 == 0;
+  constexpr int UN = 4;
+  const int cols = 32 * UN * (vec ? Elem<T>::VEC : 1);
+  const int spans = (a.d + cols - 1) / cols;
+  const long blocks = (static_cast<long>(a.rows) * spans + 7) / 8;
+  const int grid = static_cast<int>(blocks < 152 * 64 ? blocks : 152 * 64);
+  if (vec) embed_fwd_kernel<T, Elem<T>::VEC, UN><<<grid, 256, 0, s>>>(a, spans);
+  else embed_fwd_kernel<T, 1, UN><<<grid, 256, 0, s>>>(a, spans);
+  return cudaGetLastError();
+}
+
+template <typename T, typename G>
+cudaError_t sums(const EmbedArgs &a, const int *keys, const int *pos, float *part, const uint8_t *used, int num_sms,
+                 cudaStream_t s) {
+  const int pieces = (a.rows + kPiece - 1) / kPiece;
+  const bool vec = vec16(a.dout, a.ld_o, sizeof(T)) && vec16(a.dtable, a.ld_t, sizeof(G)) &&
+                   a.d % Elem<T>::VEC == 0 && a.d % Elem<G>::VEC == 0;
+  if (pieces) {
+    HostTrace t("embed_sum", s);
+    const int cols = 128 * (vec ? Elem<T>::VEC : 1);
+    const dim3 grid(pieces, (a.d + cols - 1) / cols);
+    if (vec) embed_sum_kernel<T, G, Elem<T>::VEC><<<grid, 128, 0, s>>>(a, keys, pos, part);
+    else embed_sum_kernel<T, G, 1><<<grid, 128, 0, s>>>(a, keys, pos, part);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  if (pieces > 1) {
+    HostTrace t("embed_join", s);
+    embed_join_kernel<G><<<dim3(pieces - 1, (a.d + 127) / 128), 128, 0, s>>>(a, keys, pieces, part);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  if (!a.accumulate) {
+    HostTrace t("embed_zero", s);
+    const bool zv = vec16(a.dtable, a.ld_t, sizeof(G)) && a.d % Elem<G>::VEC == 0;
+    const long want = (static_cast<long>(a.V) + 7) / 8;
+    const int grid = static_cast<int>(want < num_sms * 16L ? want : num_sms * 16L);
+    if (zv) embed_zero_kernel<G, Elem<G>::VEC><<<grid, 256, 0, s>>>(a, used);
+    else embed_zero_kernel<G, 1><<<grid, 256, 0, s>>>(a, used);
+    return cudaGetLastError();
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+size_t embed_workspace(int rows, long V, int d) { return ws_layout(rows, V, d).bytes; }
+
+cudaError_t launch_embed_forward(const EmbedArgs &a, cudaStream_t s) {
+  if (a.rows <= 0) return cudaSuccess;
+  HostTrace t("embed_forward", s);
+  switch (a.dtype) {
+    case MOE_ELEM_BF16: return fwd_type<__nv_bfloat16>(a, s);
+    case MOE_ELEM_FP16: return fwd_type<__half>(a, s);
+    default: return fwd_type<float>(a, s);
+  }
+}
+
+cudaError_t launch_embed_backward(const EmbedArgs &a, int num_sms, cudaStream_t s) {
+  const EmbedWs w = ws_layout(a.rows, a.V, a.d);
+  int *keys[2], *pos[2];
+  for (int i = 0; i < 2; ++i) {
+    keys[i] = reinterpret_cast<int *>(a.ws + w.keys[i]);
+    pos[i] = reinterpret_cast<int *>(a.ws + w.pos[i]);
+  }
+  uint8_t *used = a.accumulate ? nullptr : a.ws + w.used;
+  float *part = reinterpret_cast<float *>(a.ws + w.part);
+  cudaError_t e = cudaSuccess;
+  if (used && (e = cudaMemsetAsync(used, 0, a.V, s)) != cudaSuccess) return e;
+  int at = 0;
+  if (a.rows > 0 && a.rows <= kSmallSort) {
+    HostTrace t("embed_rank", s);
+    embed_rank_kernel<<<(a.rows + 255) / 256, 256, 0, s>>>(a, keys[0], pos[0], used);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  } else if (a.rows > 0) {
+    int bits = 1;
+    while ((1L << bits) <= a.V) ++bits;  // keys 0 .. V
+    const int passes = (bits + 9) / 10;
+    const int per = (bits + passes - 1) / passes;
+    const int blocks = (a.rows + kSortChunk - 1) / kSortChunk;
+    int *hist = reinterpret_cast<int *>(a.ws + w.hist), *total = reinterpret_cast<int *>(a.ws + w.total);
+    const int digits = 1 << per;
+    for (int p = 0; p < passes; ++p) {
+      const int *kin = p ? keys[at] : nullptr, *pin = p ? pos[at] : nullptr;
+      const int to = p ? at ^ 1 : 0;
+      HostTrace t("embed_sort", s);
+      embed_hist_kernel<<<blocks, kSortBlock, 0, s>>>(a, kin, p * per, digits, hist, p ? nullptr : used);
+      embed_scan_kernel<<<(digits + 7) / 8, 256, 0, s>>>(hist, blocks, digits, total);
+      embed_scatter_kernel<<<blocks, kSortBlock, static_cast<size_t>(digits) * (kSortBlock / 32) * 4, s>>>(
+          a, kin, pin, p * per, digits, hist, total, keys[to], pos[to]);
+      if ((e = cudaGetLastError()) != cudaSuccess) return e;
+      at = to;
+    }
+  }
+  const int *k = keys[at], *ps = pos[at];
+  const bool wide = a.grad_dtype == MOE_ELEM_FP32;
+  switch (a.dtype) {
+    case MOE_ELEM_BF16:
+      return wide ? sums<__nv_bfloat16, float>(a, k, ps, part, used, num_sms, s)
+                  : sums<__nv_bfloat16, __nv_bfloat16>(a, k, ps, part, used, num_sms, s);
+    case MOE_ELEM_FP16:
+      return wide ? sums<__half, float>(a, k, ps, part, used, num_sms, s)
+                  : sums<__half, __half>(a, k, ps, part, used, num_sms, s);
+    default: return sums<float, float>(a, k, ps, part, used, num_sms, s);
+  }
+}
+
+}  // namespace moe

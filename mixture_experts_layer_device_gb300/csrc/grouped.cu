@@ -1,0 +1,281 @@
+// Matrix products grouped by expert with ragged sizes: the plan that every
+// direction starts with, and the plain tiled kernel that takes any size,
+// stride and alignment.
+//   y[r] = x[r] w[e]^T,   dx[r] = dy[r] w[e],   dw[e] = sum over e's rows of dy[r]^T x[r]
+// Each direction is one matrix product per expert, out[m, n] = sum_k a[m, k] b[n, k],
+// whose operands are addressed by two strides; only which index is ragged
+// differs (m for y and dx, k for dw).
+#include "block.h"
+#include "elem.cuh"
+#include "grouped.cuh"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+// ---------------------------------------------------------------- plan
+// Block 0: the status word, and the first tile of every expert.  The other
+// blocks: zeros for the rows of `out` that belong to no expert.
+__global__ void __launch_bounds__(1024) grouped_plan_kernel(const GroupedArgs g, int tile_rows, uint8_t *out,
+                                                            long row_bytes, long ld_bytes) {
+  if (blockIdx.x > 0) {
+    int lo, hi, lo_last, hi_last;
+    group_rows(g, 0, lo, hi);
+    group_rows(g, g.E - 1, lo_last, hi_last);
+    const long outside = lo + static_cast<long>(g.rows - hi_last);
+    for (long i = blockIdx.x - 1; i < outside; i += gridDim.x - 1) {
+      const long row = i < lo ? i : hi_last + (i - lo);
+      uint8_t *p = out + row * ld_bytes;
+      for (long b = threadIdx.x * 2L; b < row_bytes; b += blockDim.x * 2L) *reinterpret_cast<uint16_t *>(p + b) = 0;
+    }
+    return;
+  }
+  __shared__ int warp_sum[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int run = 0;
+  bool bad = false;
+  for (int e = threadIdx.x; e < g.E; e += 1024) {
+    int lo, hi;
+    bad |= !group_rows(g, e, lo, hi);
+  }
+  const int any = __syncthreads_or(bad);  // bad offsets: no tiles at all
+  for (int base = 0; base < g.E; base += 1024) {
+    const int e = base + threadIdx.x;
+    int n = 0;
+    if (e < g.E && !any) {
+      int lo, hi;
+      group_rows(g, e, lo, hi);
+      n = (hi - lo + tile_rows - 1) / tile_rows;
+    }
+    int inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int w = 0; w < 32; ++w) {
+      if (w < warp) before += warp_sum[w];
+      all += warp_sum[w];
+    }
+    if (e < g.E) g.tiles[e] = run + before + inc - n;
+    run += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    g.tiles[g.E] = run;
+    *g.status = any ? kStatusBounds : 0;
+  }
+}
+
+// ---------------------------------------------------------------- plain kernel
+// 64 x 64 output tiles, 32 of the reduction at a time: loads by element along
+// the operand's contiguous index, the next step's in registers while
+// mma.sync works on this one's.  It exists for sizes and alignments that TMA
+// cannot address, where calls are small.
+constexpr int PT = 64, PK = 32, PLD = PK + 8;
+
+template <typename T>
+MOE_DEV void mma_16816(float *c, const uint32_t *a, const uint32_t *b);
+template <>
+MOE_DEV void mma_16816<__nv_bfloat16>(float *c, const uint32_t *a, const uint32_t *b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+template <>
+MOE_DEV void mma_16816<__half>(float *c, const uint32_t *a, const uint32_t *b) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+
+MOE_DEV void ldmatrix4(uint32_t *r, const void *p) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(smem_u32(p)));
+}
+
+// One operand tile [PT, PK] of 128 threads: element (i, k) at p + i s_i + k s_k.
+struct Side {
+  const uint16_t *p;
+  long s_i, s_k;
+  int ni, nk;  // valid i and k from p on
+  MOE_DEV void load(uint16_t *r, int k0) const {
+#pragma unroll
+    for (int j = 0; j < PT * PK / 128; ++j) {
+      const int t = threadIdx.x + j * 128;
+      const int i = s_k == 1 ? t / PK : t % PT, k = s_k == 1 ? t % PK : t / PT;
+      r[j] = (i < ni && k0 + k < nk) ? p[i * s_i + (k0 + k) * s_k] : static_cast<uint16_t>(0);
+    }
+  }
+  MOE_DEV void put(uint16_t (*sm)[PLD], const uint16_t *r) const {
+#pragma unroll
+    for (int j = 0; j < PT * PK / 128; ++j) {
+      const int t = threadIdx.x + j * 128;
+      const int i = s_k == 1 ? t / PK : t % PT, k = s_k == 1 ? t % PK : t / PT;
+      sm[i][k] = r[j];
+    }
+  }
+};
+
+template <typename T>
+MOE_DEV void plain_tile(const Side &a, const Side &b, int nk, float acc[2][4][4]) {
+  __shared__ uint16_t sa[PT][PLD], sb[PT][PLD];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int wm = (warp & 1) * 32, wn = (warp >> 1) * 32;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[i][j][k] = 0.f;
+  uint16_t ra[PT * PK / 128], rb[PT * PK / 128];
+  if (nk > 0) {
+    a.load(ra, 0);
+    b.load(rb, 0);
+  }
+  for (int k0 = 0; k0 < nk; k0 += PK) {
+    __syncthreads();
+    a.put(sa, ra);
+    b.put(sb, rb);
+    __syncthreads();
+    if (k0 + PK < nk) {
+      a.load(ra, k0 + PK);
+      b.load(rb, k0 + PK);
+    }
+#pragma unroll
+    for (int kk = 0; kk < PK; kk += 16) {
+      uint32_t fa[2][4], fb[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) ldmatrix4(fa[i], &sa[wm + i * 16 + (lane & 15)][kk + (lane >> 4) * 8]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        ldmatrix4(fb[j], &sb[wn + j * 16 + (lane & 7) + ((lane >> 4) << 3)][kk + ((lane >> 3) & 1) * 8]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mma_16816<T>(acc[i][j], fa[i], &fb[j >> 1][(j & 1) * 2]);
+    }
+  }
+}
+
+template <typename T>
+MOE_DEV void store_elem(void *out, long at, float v, bool wide, bool add) {
+  if (wide) {
+    float *p = static_cast<float *>(out) + at;
+    *p = add ? *p + v : v;
+  } else {
+    static_cast<T *>(out)[at] = Elem<T>::from(v);
+  }
+}
+
+// Accumulator element (i, j, k) of a warp's 32 x 32 part -> row and column.
+MOE_DEV void acc_place(int warp, int lane, int i, int j, int k, int &m, int &n) {
+  m = (warp & 1) * 32 + i * 16 + (lane >> 2) + (k >> 1) * 8;
+  n = (warp >> 1) * 32 + j * 8 + (lane & 3) * 2 + (k & 1);
+}
+
+template <typename T, int DIR>
+__global__ void __launch_bounds__(128) grouped_plain_kernel(const GroupedArgs g) {
+  Side a, b;
+  int lo, hi, n0, m0, mn, nn, nk;
+  void *out;
+  long ldo;
+  bool wide, add = false;
+  if constexpr (DIR == GROUPED_WGRAD) {
+    const int nt = (g.K + PT - 1) / PT, e = blockIdx.y;
+    m0 = static_cast<int>(blockIdx.x) / nt * PT;
+    n0 = static_cast<int>(blockIdx.x) % nt * PT;
+    group_rows(g, e, lo, hi);
+    if (lo == hi && g.accumulate) return;
+    nk = hi - lo;
+    mn = g.N - m0;
+    nn = g.K - n0;
+    a = Side{static_cast<const uint16_t *>(g.dy) + lo * g.ld_y + m0, 1, g.ld_y, mn, nk};
+    b = Side{static_cast<const uint16_t *>(g.x) + lo * g.ld_x + n0, 1, g.ld_x, nn, nk};
+    wide = g.out_dtype == MOE_ELEM_FP32;
+    add = g.accumulate != 0;
+    out = static_cast<uint8_t *>(g.dw) +
+          (static_cast<long>(e) * g.N * g.K + static_cast<long>(m0) * g.K + n0) * (wide ? 4 : 2);
+    ldo = g.K;
+  } else {
+    if (static_cast<int>(blockIdx.x) >= __ldg(g.tiles + g.E)) return;
+    const int e = group_of_tile(g.tiles, g.E, blockIdx.x);
+    group_rows(g, e, lo, hi);
+    m0 = lo + (blockIdx.x - __ldg(g.tiles + e)) * PT;
+    n0 = blockIdx.y * PT;
+    mn = hi - m0;
+    const uint16_t *w = static_cast<const uint16_t *>(g.w) + static_cast<long>(e) * g.ld_e;
+    if constexpr (DIR == GROUPED_FWD) {
+      nk = g.K;
+      nn = g.N - n0;
+      a = Side{static_cast<const uint16_t *>(g.x) + m0 * g.ld_x, g.ld_x, 1, mn, nk};
+      b = Side{w + n0 * g.ld_w, g.ld_w, 1, nn, nk};
+      wide = g.out_dtype == MOE_ELEM_FP32;
+      out = static_cast<uint8_t *>(g.y) + (m0 * g.ld_y + n0) * (wide ? 4 : 2);
+      ldo = g.ld_y;
+    } else {
+      nk = g.N;
+      nn = g.K - n0;
+      a = Side{static_cast<const uint16_t *>(g.dy) + m0 * g.ld_y, g.ld_y, 1, mn, nk};
+      b = Side{w + n0, 1, g.ld_w, nn, nk};
+      wide = false;
+      out = static_cast<uint8_t *>(g.dx) + (m0 * g.ld_x + n0) * 2;
+      ldo = g.ld_x;
+    }
+  }
+  float acc[2][4][4];
+  plain_tile<T>(a, b, nk, acc);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        int m, n;
+        acc_place(warp, lane, i, j, k, m, n);
+        if (m < mn && n < nn) store_elem<T>(out, m * ldo + n, acc[i][j][k], wide, add);
+      }
+}
+
+template <typename T>
+cudaError_t plain_type(const GroupedArgs &g, int dir, cudaStream_t s) {
+  const long slots = (g.rows + PT - 1L) / PT + (g.E < g.rows ? g.E : g.rows);
+  if (dir == GROUPED_WGRAD) {
+    const dim3 grid(((g.N + PT - 1) / PT) * ((g.K + PT - 1) / PT), g.E);
+    grouped_plain_kernel<T, GROUPED_WGRAD><<<grid, 128, 0, s>>>(g);
+  } else if (dir == GROUPED_FWD) {
+    if (slots) grouped_plain_kernel<T, GROUPED_FWD><<<dim3(slots, (g.N + PT - 1) / PT), 128, 0, s>>>(g);
+  } else {
+    if (slots) grouped_plain_kernel<T, GROUPED_DGRAD><<<dim3(slots, (g.K + PT - 1) / PT), 128, 0, s>>>(g);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int grouped_plain_tile_rows() { return PT; }
+
+cudaError_t launch_grouped_plan(const GroupedArgs &g, int tile_rows, void *out, int out_elem, int out_cols,
+                                long ld_out, cudaStream_t s) {
+  HostTrace t("grouped_plan", s);
+  const long esz = elem_bytes(out_elem);
+  const int zero_blocks = out && g.rows > 0 ? (g.rows < 64 ? g.rows : 64) : 0;
+  grouped_plan_kernel<<<1 + zero_blocks, 1024, 0, s>>>(g, tile_rows, static_cast<uint8_t *>(out), out_cols * esz,
+                                                       ld_out * esz);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_grouped_plain(const GroupedArgs &g, int dir, cudaStream_t s) {
+  HostTrace t(dir == GROUPED_FWD ? "grouped_fwd_plain" : dir == GROUPED_DGRAD ? "grouped_dgrad_plain" : "grouped_wgrad_plain", s);
+  return g.dtype == MOE_ELEM_BF16 ? plain_type<__nv_bfloat16>(g, dir, s) : plain_type<__half>(g, dir, s);
+}
+
+}  // namespace moe

@@ -1,0 +1,553 @@
+// The norms around a block, fused with its gate and the residual:
+//   n = w_post f / rms(f),  z = alpha x + g n,  h = w_pre z / rms(z),
+// and their backward.  With r = 1 / rms and u = r v, du pulls back to
+//   dv = r du - v r^3 <du, v> / d,
+// so with t = dz + r_pre (w_pre dh) - z r_pre^3 <w_pre dh, z> / d (the gradient
+// that reaches z from both sides)
+//   dx = alpha t,   dn = g t,   df = r_post (w_post dn) - f r_post^3 <w_post dn, f> / d,
+//   dw_pre = sum_rows dh z r_pre,   dw_post = sum_rows dn f r_post,   dg = t n.
+// <w_post dn, f> needs t, and t needs <w_pre dh, z>.  Expanding t makes it one
+// round of sums over the row:
+//   <t, q> = <dz, q> + r_pre <w_pre dh, q> - c <z, q>,  q = w_post g f,
+// so the row is read once and a block waits for one reduction per row.
+//
+// HBM bound: forward 4 elements moved per column (f, x in; z, h out), backward 6
+// (dz, dh, z, f in; dx, df out).
+#include "block.h"
+#include "elem.cuh"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kMaxWarps = 32;
+
+// Sum over the threads that share a row: a warp (WARP), or the block through
+// red[2][N][32] (two buffers in turn: one barrier per sum).  Fixed order.
+template <bool WARP, int N>
+MOE_DEV void row_sum(float *v, float (*red)[N][kMaxWarps], int &turn) {
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  if constexpr (!WARP) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    if (lane == 0)
+#pragma unroll
+      for (int k = 0; k < N; ++k) red[turn][k][warp] = v[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      float t = lane < nw ? red[turn][k][lane] : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      v[k] = t;
+    }
+    turn ^= 1;
+  }
+}
+
+// VEC elements of a row at p (16 bytes at once when VEC > 1).
+template <typename T, int VEC>
+struct Chunk {
+  uint4 q;
+  MOE_DEV void load(const T *p) { q = ld_stream(p); }
+  MOE_DEV void load_cached(const T *p) { q = __ldg(reinterpret_cast<const uint4 *>(p)); }
+  MOE_DEV void clear() { q = make_uint4(0, 0, 0, 0); }
+  MOE_DEV void get(float *v) const { Elem<T>::unpack(q, v); }
+  MOE_DEV static void store(T *p, const float *v) { st_stream(p, Elem<T>::pack(v)); }
+};
+template <typename T>
+struct Chunk<T, 1> {
+  T q;
+  MOE_DEV void load(const T *p) { q = *p; }
+  MOE_DEV void load_cached(const T *p) { q = *p; }
+  MOE_DEV void clear() { q = Elem<T>::from(0.f); }
+  MOE_DEV void get(float *v) const { v[0] = Elem<T>::to(q); }
+  MOE_DEV static void store(T *p, const float *v) { *p = Elem<T>::from(v[0]); }
+};
+
+template <typename T, int VEC>
+MOE_DEV void weight_chunk(const void *w, long at, float *v) {
+  if (w) {
+    Chunk<T, VEC> q;
+    q.load_cached(static_cast<const T *>(w) + at);
+    q.get(v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) v[k] = 1.f;
+  }
+}
+
+// The gate of VEC columns of a row (ROW's value comes in as `row_gate`).
+template <typename T, int VEC>
+MOE_DEV void gate_chunk(const NormArgs &a, long row, int c, float row_gate, float *v) {
+  if (a.gate == MOE_GATE_CHANNEL) {
+    weight_chunk<T, VEC>(a.g, c, v);
+  } else if (a.gate == MOE_GATE_FULL) {
+    Chunk<T, VEC> q;
+    q.load(static_cast<const T *>(a.g) + row * a.ld_g + c);
+    q.get(v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) v[k] = row_gate;
+  }
+}
+
+template <typename T>
+MOE_DEV float row_gate_of(const NormArgs &a, long row) {
+  return a.gate == MOE_GATE_ROW ? Elem<T>::to(static_cast<const T *>(a.g)[row]) : 1.f;
+}
+
+// ---------------------------------------------------------------- forward
+// A row stays in the registers of its threads (NCH chunks of VEC columns each)
+// from the loads to the stores; the rows of the grid's blocks follow each other.
+template <typename T, int VEC, int NCH, bool WARP, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_fwd_kernel(const NormArgs a) {
+  __shared__ float red[2][1][kMaxWarps];
+  const int tpr = WARP ? 32 : blockDim.x;
+  const int tid = WARP ? (threadIdx.x & 31) : threadIdx.x;
+  const int rpb = WARP ? (blockDim.x >> 5) : 1;
+  const float inv_d = 1.f / static_cast<float>(a.d);
+  int turn = 0;
+  for (long row = static_cast<long>(blockIdx.x) * rpb + (WARP ? (threadIdx.x >> 5) : 0); row < a.rows;
+       row += static_cast<long>(gridDim.x) * rpb) {
+    Chunk<T, VEC> xq[NCH], fq[NCH];
+    const T *xr = static_cast<const T *>(a.x) + row * a.ld_x;
+    const T *fr = static_cast<const T *>(a.f) + row * a.ld_f;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int c = (tid + i * tpr) * VEC;
+      xq[i].clear();
+      fq[i].clear();
+      if (c < a.d) {
+        xq[i].load(xr + c);
+        if (a.f) fq[i].load(fr + c);
+      }
+    }
+    float r = 1.f;
+    if (a.flags & MOE_NORM_POST) {
+      float ss[1] = {0.f};
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) {
+        float v[VEC];
+        fq[i].get(v);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) ss[0] = fmaf(v[k], v[k], ss[0]);
+      }
+      row_sum<WARP, 1>(ss, red, turn);
+      r = rsqrtf(ss[0] * inv_d + a.eps);
+      if (tid == 0 && a.r_post) a.r_post[row] = r;
+    }
+    const float rg = row_gate_of<T>(a, row);
+    float z[NCH][VEC];
+    float ss[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int c = (tid + i * tpr) * VEC;
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) z[i][k] = 0.f;
+      if (c < a.d) {
+        xq[i].get(z[i]);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) z[i][k] *= a.alpha;
+        if (a.f) {
+          float v[VEC], w[VEC], g[VEC];
+          fq[i].get(v);
+          weight_chunk<T, VEC>(a.w_post, c, w);
+          gate_chunk<T, VEC>(a, row, c, rg, g);
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) z[i][k] = fmaf(g[k], v[k] * r * w[k], z[i][k]);
+        }
+        if (a.z) Chunk<T, VEC>::store(static_cast<T *>(a.z) + row * a.ld_z + c, z[i]);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) ss[0] = fmaf(z[i][k], z[i][k], ss[0]);
+      }
+    }
+    if (a.flags & MOE_NORM_PRE) {
+      row_sum<WARP, 1>(ss, red, turn);
+      r = rsqrtf(ss[0] * inv_d + a.eps);
+      if (tid == 0 && a.r_pre) a.r_pre[row] = r;
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) {
+        const int c = (tid + i * tpr) * VEC;
+        if (c < a.d) {
+          float w[VEC];
+          weight_chunk<T, VEC>(a.w_pre, c, w);
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) z[i][k] *= r * w[k];
+          Chunk<T, VEC>::store(static_cast<T *>(a.h) + row * a.ld_h + c, z[i]);
+        }
+      }
+    }
+  }
+}
+
+// Rows that do not fit the registers of a block: each pass reads the row again
+// (from L1 / L2).
+template <typename T>
+__global__ void __launch_bounds__(1024) norm_fwd_long_kernel(const NormArgs a) {
+  __shared__ float red[2][1][kMaxWarps];
+  const float inv_d = 1.f / static_cast<float>(a.d);
+  int turn = 0;
+  for (long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    const T *xr = static_cast<const T *>(a.x) + row * a.ld_x;
+    const T *fr = a.f ? static_cast<const T *>(a.f) + row * a.ld_f : nullptr;
+    float r = 1.f, ss[1] = {0.f};
+    if (a.flags & MOE_NORM_POST) {
+      for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
+        const float v = Elem<T>::to(fr[c]);
+        ss[0] = fmaf(v, v, ss[0]);
+      }
+      row_sum<false, 1>(ss, red, turn);
+      r = rsqrtf(ss[0] * inv_d + a.eps);
+      if (threadIdx.x == 0 && a.r_post) a.r_post[row] = r;
+    }
+    const float rg = row_gate_of<T>(a, row);
+    auto z_at = [&](int c) {
+      float z = a.alpha * Elem<T>::to(xr[c]);
+      if (fr) {
+        float w, g;
+        weight_chunk<T, 1>(a.w_post, c, &w);
+        gate_chunk<T, 1>(a, row, c, rg, &g);
+        z = fmaf(g, Elem<T>::to(fr[c]) * r * w, z);
+      }
+      return z;
+    };
+    ss[0] = 0.f;
+    if (a.flags & MOE_NORM_PRE) {
+      for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
+        const float z = z_at(c);
+        ss[0] = fmaf(z, z, ss[0]);
+      }
+      row_sum<false, 1>(ss, red, turn);
+    }
+    const float rp = rsqrtf(ss[0] * inv_d + a.eps);
+    if ((a.flags & MOE_NORM_PRE) && threadIdx.x == 0 && a.r_pre) a.r_pre[row] = rp;
+    for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
+      const float z = z_at(c);   // before the stores: z may be x's or f's buffer
+      if (a.z) static_cast<T *>(a.z)[row * a.ld_z + c] = Elem<T>::from(z);
+      if (a.flags & MOE_NORM_PRE) {
+        float w;
+        weight_chunk<T, 1>(a.w_pre, c, &w);
+        static_cast<T *>(a.h)[row * a.ld_h + c] = Elem<T>::from(z * (rp * w));
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- backward
+// What one row's columns need after its sums are known.
+struct RowTerms {
+  float rp, rq, rg;  // r_pre, r_post, row gate
+  float c1;          // rp^3 <w_pre dh, z> / d
+  float c2;          // rq^3 <w_post dn, f> / d
+};
+
+// Row sums: [0] <w_pre dh, z>, [1] <dz, q>, [2] <w_pre dh, q>, [3] <z, q> with
+// q = w_post g f, g without a row gate.
+MOE_DEV void add_sums(float dz, float dhw, float z, float q, float *s) {
+  s[0] = fmaf(dhw, z, s[0]);
+  s[1] = fmaf(dz, q, s[1]);
+  s[2] = fmaf(dhw, q, s[2]);
+  s[3] = fmaf(z, q, s[3]);
+}
+
+template <typename T>
+MOE_DEV RowTerms row_terms(const NormArgs &a, long row, const float *s, float inv_d, bool first) {
+  RowTerms t;
+  t.rp = (a.flags & MOE_NORM_PRE) ? a.r_pre_in[row] : 0.f;
+  t.rq = (a.flags & MOE_NORM_POST) ? a.r_post_in[row] : 1.f;
+  t.rg = row_gate_of<T>(a, row);
+  t.c1 = t.rp * t.rp * t.rp * s[0] * inv_d;
+  const float tq = s[1] + t.rp * s[2] - t.c1 * s[3];  // <t, q>
+  t.c2 = (a.flags & MOE_NORM_POST) ? t.rq * t.rq * t.rq * t.rg * tq * inv_d : 0.f;
+  if (a.gate == MOE_GATE_ROW && a.dg && first) static_cast<T *>(a.dg)[row] = Elem<T>::from(tq * t.rq);  // <t, n>
+  return t;
+}
+
+// Column sums: [0] dh z r_pre (dw_pre), [1] t f r_post with the gates that are
+// not per channel (dw_post; dgate per channel).
+template <typename T, int VEC, int NCH, bool WARP, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_bwd_kernel(const NormArgs a) {
+  __shared__ float red[2][4][kMaxWarps];
+  const int tpr = WARP ? 32 : blockDim.x;
+  const int tid = WARP ? (threadIdx.x & 31) : threadIdx.x;
+  const int rpb = WARP ? (blockDim.x >> 5) : 1;
+  const int slot = WARP ? blockIdx.x * rpb + (threadIdx.x >> 5) : blockIdx.x;
+  const float inv_d = 1.f / static_cast<float>(a.d);
+  const bool pre = (a.flags & MOE_NORM_PRE) != 0;
+  float acc0[NCH][VEC], acc1[NCH][VEC];
+#pragma unroll
+  for (int i = 0; i < NCH; ++i)
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) acc0[i][k] = acc1[i][k] = 0.f;
+  int turn = 0;
+  for (long row = slot; row < a.rows; row += static_cast<long>(gridDim.x) * rpb) {
+    Chunk<T, VEC> dzq[NCH], dhq[NCH], zq[NCH], fq[NCH];
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int c = (tid + i * tpr) * VEC;
+      dzq[i].clear();
+      dhq[i].clear();
+      zq[i].clear();
+      fq[i].clear();
+      if (c < a.d) {
+        if (a.dz) dzq[i].load(static_cast<const T *>(a.dz) + row * a.ld_z + c);
+        if (pre) dhq[i].load(static_cast<const T *>(a.dh) + row * a.ld_h + c);
+        if (pre) zq[i].load(static_cast<const T *>(a.zin) + row * a.ld_z + c);
+        if (a.f) fq[i].load(static_cast<const T *>(a.f) + row * a.ld_f + c);
+      }
+    }
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int c = (tid + i * tpr) * VEC;
+      if (c < a.d) {
+        float dz[VEC], dh[VEC], z[VEC], f[VEC], wq[VEC], wp[VEC], g[VEC];
+        dzq[i].get(dz);
+        dhq[i].get(dh);
+        zq[i].get(z);
+        fq[i].get(f);
+        weight_chunk<T, VEC>(a.w_pre, c, wp);
+        weight_chunk<T, VEC>(a.w_post, c, wq);
+        gate_chunk<T, VEC>(a, row, c, 1.f, g);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) add_sums(dz[k], dh[k] * wp[k], z[k], wq[k] * g[k] * f[k], s);
+      }
+    }
+    row_sum<WARP, 4>(s, red, turn);
+    const RowTerms t = row_terms<T>(a, row, s, inv_d, tid == 0);
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int c = (tid + i * tpr) * VEC;
+      if (c < a.d) {
+        float dz[VEC], dh[VEC], z[VEC], f[VEC], wq[VEC], wp[VEC], g[VEC], o[VEC];
+        dzq[i].get(dz);
+        dhq[i].get(dh);
+        zq[i].get(z);
+        fq[i].get(f);
+        weight_chunk<T, VEC>(a.w_pre, c, wp);
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          acc0[i][k] = fmaf(dh[k] * t.rp, z[k], acc0[i][k]);
+          dz[k] = fmaf(t.rp * wp[k], dh[k], fmaf(-t.c1, z[k], dz[k]));  // t
+          o[k] = a.alpha * dz[k];
+        }
+        if (a.dx) Chunk<T, VEC>::store(static_cast<T *>(a.dx) + row * a.ld_x + c, o);
+        weight_chunk<T, VEC>(a.w_post, c, wq);
+        gate_chunk<T, VEC>(a, row, c, t.rg, g);
+        if (a.gate == MOE_GATE_FULL && a.dg) {
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) o[k] = dz[k] * (wq[k] * f[k] * t.rq);
+          Chunk<T, VEC>::store(static_cast<T *>(a.dg) + row * a.ld_g + c, o);
+        }
+        const bool chan = a.gate == MOE_GATE_CHANNEL;
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          acc1[i][k] = fmaf(dz[k] * (chan ? 1.f : g[k]), f[k] * t.rq, acc1[i][k]);
+          o[k] = fmaf(t.rq * wq[k] * g[k], dz[k], -t.c2 * f[k]);
+        }
+        if (a.df) Chunk<T, VEC>::store(static_cast<T *>(a.df) + row * a.ld_f + c, o);
+      }
+    }
+  }
+  if (a.part) {
+    float *p = a.part + static_cast<long>(slot) * 2 * a.d;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+      const int c = (tid + i * tpr) * VEC;
+      if (c < a.d)
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) {
+          p[c + k] = acc0[i][k];
+          p[a.d + c + k] = acc1[i][k];
+        }
+    }
+  }
+}
+
+// Long rows: two passes over the row, the column sums in the block's own
+// workspace rows (each thread adds to its own columns).
+template <typename T>
+__global__ void __launch_bounds__(1024) norm_bwd_long_kernel(const NormArgs a) {
+  __shared__ float red[2][4][kMaxWarps];
+  const float inv_d = 1.f / static_cast<float>(a.d);
+  const bool pre = (a.flags & MOE_NORM_PRE) != 0;
+  float *part = a.part ? a.part + static_cast<long>(blockIdx.x) * 2 * a.d : nullptr;
+  if (part)
+    for (int c = threadIdx.x; c < a.d; c += blockDim.x) part[c] = part[a.d + c] = 0.f;
+  int turn = 0;
+  for (long row = blockIdx.x; row < a.rows; row += gridDim.x) {
+    auto at = [&](const void *p, long ld, int c) { return p ? Elem<T>::to(static_cast<const T *>(p)[row * ld + c]) : 0.f; };
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
+      float wp, wq, g;
+      weight_chunk<T, 1>(a.w_pre, c, &wp);
+      weight_chunk<T, 1>(a.w_post, c, &wq);
+      gate_chunk<T, 1>(a, row, c, 1.f, &g);
+      add_sums(at(a.dz, a.ld_z, c), pre ? at(a.dh, a.ld_h, c) * wp : 0.f, pre ? at(a.zin, a.ld_z, c) : 0.f,
+               wq * g * at(a.f, a.ld_f, c), s);
+    }
+    row_sum<false, 4>(s, red, turn);
+    const RowTerms t = row_terms<T>(a, row, s, inv_d, threadIdx.x == 0);
+    for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
+      float wp, wq, g;
+      weight_chunk<T, 1>(a.w_pre, c, &wp);
+      weight_chunk<T, 1>(a.w_post, c, &wq);
+      gate_chunk<T, 1>(a, row, c, t.rg, &g);
+      const float dh = pre ? at(a.dh, a.ld_h, c) : 0.f, z = pre ? at(a.zin, a.ld_z, c) : 0.f;
+      const float f = at(a.f, a.ld_f, c);
+      const float tt = fmaf(t.rp * wp, dh, fmaf(-t.c1, z, at(a.dz, a.ld_z, c)));
+      if (a.dx) static_cast<T *>(a.dx)[row * a.ld_x + c] = Elem<T>::from(a.alpha * tt);
+      if (a.gate == MOE_GATE_FULL && a.dg)
+        static_cast<T *>(a.dg)[row * a.ld_g + c] = Elem<T>::from(tt * (wq * f * t.rq));
+      if (a.df) static_cast<T *>(a.df)[row * a.ld_f + c] = Elem<T>::from(fmaf(t.rq * wq * g, tt, -t.c2 * f));
+      if (part) {
+        part[c] = fmaf(dh * t.rp, z, part[c]);
+        part[a.d + c] = fmaf(tt * (a.gate == MOE_GATE_CHANNEL ? 1.f : g), f * t.rq, part[a.d + c]);
+      }
+    }
+  }
+}
+
+// dw_pre, dw_post and a channel gate's gradient from the blocks' column sums:
+// 32 columns per block, the partial rows in 8 interleaved runs joined in order.
+template <typename T>
+__global__ void __launch_bounds__(256) norm_columns_kernel(const NormArgs a, int slots) {
+  __shared__ float sh[8][32];
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), run = threadIdx.x >> 5, k = blockIdx.y;
+  float v = 0.f;
+  if (c < a.d)
+    for (int b = run; b < slots; b += 8) v += a.part[(static_cast<long>(b) * 2 + k) * a.d + c];
+  sh[run][threadIdx.x & 31] = v;
+  __syncthreads();
+  if (run || c >= a.d) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) v += sh[i][threadIdx.x];
+  if (k == 0) {
+    if (a.dw_pre) static_cast<T *>(a.dw_pre)[c] = Elem<T>::from(v);
+    return;
+  }
+  float w = 1.f, g = 1.f;
+  if (a.w_post) w = Elem<T>::to(static_cast<const T *>(a.w_post)[c]);
+  if (a.gate == MOE_GATE_CHANNEL) g = Elem<T>::to(static_cast<const T *>(a.g)[c]);
+  if (a.dw_post) static_cast<T *>(a.dw_post)[c] = Elem<T>::from(g * v);
+  if (a.gate == MOE_GATE_CHANNEL && a.dg) static_cast<T *>(a.dg)[c] = Elem<T>::from(w * v);
+}
+
+bool vec16(const void *p, long ld, int esz) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * esz) % 16 == 0;
+}
+
+int round32(int n) { return (n + 31) / 32 * 32; }
+
+// Rows of 16-byte chunks only when every tensor of the call has them.
+template <typename T>
+bool all_vec(const NormArgs &a) {
+  const int e = sizeof(T);
+  return (a.d * e) % 16 == 0 && vec16(a.x, a.ld_x, e) && vec16(a.dx, a.ld_x, e) && vec16(a.f, a.ld_f, e) &&
+         vec16(a.df, a.ld_f, e) && vec16(a.z, a.ld_z, e) && vec16(a.zin, a.ld_z, e) && vec16(a.dz, a.ld_z, e) &&
+         vec16(a.h, a.ld_h, e) && vec16(a.dh, a.ld_h, e) && vec16(a.w_pre, 0, e) && vec16(a.w_post, 0, e) &&
+         (a.gate == MOE_GATE_NONE || a.gate == MOE_GATE_ROW ||
+          (vec16(a.g, a.gate == MOE_GATE_FULL ? a.ld_g : 0, e) &&
+           (a.gate == MOE_GATE_CHANNEL || vec16(a.dg, a.ld_g, e))));
+}
+
+template <typename T, int VEC, int NCH, bool WARP, int THREADS>
+cudaError_t fwd_one(const NormArgs &a, int threads, int num_sms, cudaStream_t s) {
+  const int rpb = WARP ? threads / 32 : 1;
+  const long blocks = (a.rows + rpb - 1) / rpb;
+  const int per_sm = threads >= 1024 ? 2 : 2048 / threads;
+  const int grid = static_cast<int>(blocks < static_cast<long>(num_sms) * per_sm ? blocks : num_sms * per_sm);
+  norm_fwd_kernel<T, VEC, NCH, WARP, THREADS><<<grid, threads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+// Elements per thread: 16, in a warp up to 512 columns, else a block of up to
+// 1024 threads (16384 columns).
+template <typename T, int VEC>
+cudaError_t fwd_vec(const NormArgs &a, int num_sms, cudaStream_t s) {
+  constexpr int NCH = 16 / VEC;
+  if (a.d <= 512) return fwd_one<T, VEC, NCH, true, 256>(a, 256, num_sms, s);
+  const int threads = round32((a.d + 15) / 16);
+  if (threads <= 512) return fwd_one<T, VEC, NCH, false, 512>(a, threads, num_sms, s);
+  return fwd_one<T, VEC, NCH, false, 1024>(a, threads, num_sms, s);
+}
+
+template <typename T>
+cudaError_t fwd_type(const NormArgs &a, int num_sms, cudaStream_t s) {
+  if (a.d > 16384) {
+    const int grid = a.rows < 2 * num_sms ? a.rows : 2 * num_sms;
+    norm_fwd_long_kernel<T><<<grid, 1024, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+  return all_vec<T>(a) ? fwd_vec<T, Elem<T>::VEC>(a, num_sms, s) : fwd_vec<T, 1>(a, num_sms, s);
+}
+
+template <typename T, int VEC, int NCH, bool WARP, int THREADS>
+cudaError_t bwd_one(const NormArgs &a, int threads, int per_sm, int num_sms, int *slots, cudaStream_t s) {
+  const int rpb = WARP ? threads / 32 : 1;
+  const long blocks = (a.rows + rpb - 1) / rpb;
+  long grid = static_cast<long>(num_sms) * per_sm;
+  if (grid * rpb > kNormMaxBlocks) grid = kNormMaxBlocks / rpb;
+  if (blocks < grid) grid = blocks;
+  *slots = static_cast<int>(grid) * rpb;
+  norm_bwd_kernel<T, VEC, NCH, WARP, THREADS><<<static_cast<int>(grid), threads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int VEC>
+cudaError_t bwd_vec(const NormArgs &a, int num_sms, int *slots, cudaStream_t s) {
+  constexpr int NCH = 8 / VEC;
+  if (a.d <= 256) return bwd_one<T, VEC, NCH, true, 256>(a, 128, 1, num_sms, slots, s);
+  const int threads = round32((a.d + 7) / 8);
+  if (threads <= 256) return bwd_one<T, VEC, NCH, false, 256>(a, threads, 4, num_sms, slots, s);
+  if (threads <= 512) return bwd_one<T, VEC, NCH, false, 512>(a, threads, 2, num_sms, slots, s);
+  return bwd_one<T, VEC, NCH, false, 1024>(a, threads, 1, num_sms, slots, s);
+}
+
+template <typename T>
+cudaError_t bwd_type(const NormArgs &a, int num_sms, cudaStream_t s) {
+  int slots = 0;
+  if (a.rows > 0) {
+    cudaError_t e;
+    HostTrace t("norm_backward", s);
+    if (a.d > 8192) {
+      slots = a.rows < 2 * num_sms ? a.rows : 2 * num_sms;
+      if (slots > kNormMaxBlocks) slots = kNormMaxBlocks;
+      norm_bwd_long_kernel<T><<<slots, 1024, 0, s>>>(a);
+      e = cudaGetLastError();
+    } else {
+      e = all_vec<T>(a) ? bwd_vec<T, Elem<T>::VEC>(a, num_sms, &slots, s) : bwd_vec<T, 1>(a, num_sms, &slots, s);
+    }
+    if (e != cudaSuccess) return e;
+  }
+  if (!a.part) return cudaSuccess;
+  HostTrace t("norm_columns", s);
+  norm_columns_kernel<T><<<dim3((a.d + 31) / 32, 2), 256, 0, s>>>(a, slots);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_norm_forward(const NormArgs &a, int num_sms, cudaStream_t s) {
+  if (a.rows <= 0) return cudaSuccess;
+  HostTrace t("norm_forward", s);
+  switch (a.dtype) {
+    case MOE_ELEM_BF16: return fwd_type<__nv_bfloat16>(a, num_sms, s);
+    case MOE_ELEM_FP16: return fwd_type<__half>(a, num_sms, s);
+    default: return fwd_type<float>(a, num_sms, s);
+  }
+}
+
+cudaError_t launch_norm_backward(const NormArgs &a, int num_sms, cudaStream_t s) {
+  switch (a.dtype) {
+    case MOE_ELEM_BF16: return bwd_type<__nv_bfloat16>(a, num_sms, s);
+    case MOE_ELEM_FP16: return bwd_type<__half>(a, num_sms, s);
+    default: return bwd_type<float>(a, num_sms, s);
+  }
+}
+
+}  // namespace moe
