@@ -52,6 +52,9 @@ cudaError_t launch_grouped_plan(const GroupedArgs &g, int tile_rows, void *out, 
                                 long ld_out, cudaStream_t s);
 int grouped_plain_tile_rows();
 cudaError_t launch_grouped_plain(const GroupedArgs &g, int dir, cudaStream_t s);
+// Tensor-core path: every pointer and row stride a multiple of 16 bytes.
+int grouped_tc_tile_rows();
+cudaError_t launch_grouped_tc(const GroupedArgs &g, int dir, cudaStream_t s);
 
 // ---------------------------------------------------------------- block norms
 struct NormArgs {

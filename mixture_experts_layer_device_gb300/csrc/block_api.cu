@@ -29,7 +29,7 @@ GroupedWs grouped_ws(int E) {
   w.status = 0;
   w.tiles = 256;
   w.maps = w.tiles + round256((static_cast<size_t>(E) + 1) * 4);
-  w.bytes = w.maps + static_cast<size_t>(E) * 2 * 128;
+  w.bytes = w.maps + static_cast<size_t>(E) * 2 * 128 + 128;  // aligned to 128 bytes in place
   return w;
 }
 
@@ -63,7 +63,26 @@ void grouped_bind(moe::GroupedArgs *g, const int32_t *offsets, void *ws) {
   g->offsets = offsets;
   g->status = reinterpret_cast<int *>(b + w.status);
   g->tiles = reinterpret_cast<int *>(b + w.tiles);
-  g->maps = b + w.maps;
+  g->maps = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(b + w.maps) + 127) & ~static_cast<uintptr_t>(127));
+}
+
+// TMA addresses rows of whole 16-byte units; the sizes that the products share
+// decide for all of them, the pointers for each.
+bool tma_rows(const void *p, long ld) { return aligned(p, 16) && ld % 8 == 0; }
+
+bool grouped_tensor(const moe::GroupedArgs &g, int dir) {
+  if (g.rows == 0 || g.N % 8 || g.K % 8) return false;
+  const bool w = tma_rows(g.w, g.ld_w) && g.ld_e % 8 == 0;
+  if (dir == moe::GROUPED_FWD) return w && tma_rows(g.x, g.ld_x) && tma_rows(g.y, g.ld_y);
+  if (dir == moe::GROUPED_DGRAD) return w && tma_rows(g.dy, g.ld_y) && tma_rows(g.dx, g.ld_x);
+  return tma_rows(g.dy, g.ld_y) && tma_rows(g.x, g.ld_x) && aligned(g.dw, 16);
+}
+
+int grouped_product(const moe::GroupedArgs &g, int dir, cudaStream_t s) {
+  return status_of(grouped_tensor(g, dir) ? moe::launch_grouped_tc(g, dir, s) : moe::launch_grouped_plain(g, dir, s));
+}
+int grouped_tile_rows(const moe::GroupedArgs &g, int dir) {
+  return grouped_tensor(g, dir) ? moe::grouped_tc_tile_rows() : moe::grouped_plain_tile_rows();
 }
 
 // ---------------------------------------------------------------- norm
@@ -136,10 +155,10 @@ int moe_grouped_forward(const moe_grouped_config *cfg, const void *x, const void
   g.x = x;
   g.w = w;
   g.y = y;
-  if ((rc = status_of(moe::launch_grouped_plan(g, moe::grouped_plain_tile_rows(), y, g.out_dtype, g.N, g.ld_y,
-                                               stream))) != MOE_OK)
+  if ((rc = status_of(moe::launch_grouped_plan(g, grouped_tile_rows(g, moe::GROUPED_FWD), y, g.out_dtype, g.N,
+                                               g.ld_y, stream))) != MOE_OK)
     return rc;
-  return status_of(moe::launch_grouped_plain(g, moe::GROUPED_FWD, stream));
+  return grouped_product(g, moe::GROUPED_FWD, stream);
 }
 
 int moe_grouped_backward(const moe_grouped_config *cfg, const void *dy, const void *x, const void *w,
@@ -161,11 +180,11 @@ int moe_grouped_backward(const moe_grouped_config *cfg, const void *dy, const vo
   g.w = w;
   g.dx = dx;
   g.dw = dw;
-  if ((rc = status_of(moe::launch_grouped_plan(g, moe::grouped_plain_tile_rows(), dx, g.dtype, g.K, g.ld_x,
+  if ((rc = status_of(moe::launch_grouped_plan(g, grouped_tile_rows(g, moe::GROUPED_DGRAD), dx, g.dtype, g.K, g.ld_x,
                                                stream))) != MOE_OK)
     return rc;
-  if (dx && (rc = status_of(moe::launch_grouped_plain(g, moe::GROUPED_DGRAD, stream))) != MOE_OK) return rc;
-  if (dw && (rc = status_of(moe::launch_grouped_plain(g, moe::GROUPED_WGRAD, stream))) != MOE_OK) return rc;
+  if (dx && (rc = grouped_product(g, moe::GROUPED_DGRAD, stream)) != MOE_OK) return rc;
+  if (dw && (rc = grouped_product(g, moe::GROUPED_WGRAD, stream)) != MOE_OK) return rc;
   return MOE_OK;
 }
 

@@ -1,0 +1,554 @@
+// Ragged grouped products on CTA pairs (tcgen05, cta_group::2).
+//
+// The tokens are the N side of the tensor-core product: y^T = w x^T with 256
+// output features (M, 128 per CTA) by up to 256 tokens, and N is set per tile in
+// steps of 32.  An expert's rows start and end anywhere, so with the tokens on
+// M every expert would cost whole 128-row tiles; on N its last tile costs what
+// it holds.  Rows past the expert's last one are computed with whatever lies
+// there (another expert's rows) and not stored: a token is a column of its own.
+//
+//   forward   A = w [N, K] K-major             B = x K-major     columns: tokens
+//   dgrad     A = w^T: w read MN-major         B = dy K-major    columns: tokens
+//   wgrad     A = dy^T, B = x^T: both read MN-major, the reduction runs over the
+//             expert's rows.  Rows past its last one must not enter the sum
+//             (0 * NaN is NaN), so each expert has its own pair of tensor maps
+//             that end at its last row: TMA fills zeros beyond it.
+//
+// No operand is transposed in memory: the MN-major operands are 64 x 64 boxes
+// (64 features wide, 64 reduction steps deep) in the 128-byte swizzle, which the
+// shared-memory descriptors address directly.
+//
+// Roles per CTA (192 threads): TMA producer, MMA issuer (leader CTA), four
+// epilogue warps; six 32 KB stages; two accumulators of 256 TMEM columns, so a
+// tile's epilogue runs beside the next one's MMAs.  Persistent: pair c takes
+// tiles c, c + pairs, ...  Every wait is bounded (mbar_wait).
+#include "elem.cuh"
+#include "gemm_common.cuh"
+#include "grouped.cuh"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kStages = 6;
+constexpr int kStageBytes = 32768;           // 16 KB of A, up to 16 KB of B
+constexpr int kStaging = 8192;               // per epilogue warp: two 4 KB pieces
+constexpr int kTileTokens = 256;
+constexpr size_t kSmem = 1024 + kStages * kStageBytes + 4 * kStaging + (2 * kStages + 5) * 8 + 16;
+static_assert(kSmem <= 232448, "shared memory");
+
+struct TcMaps {
+  CUtensorMap a;        // forward, dgrad: w
+  CUtensorMap b[4];     // token rows, boxes of 16, 32, 64 and 128 rows
+  CUtensorMap out;      // wgrad: dw
+};
+
+MOE_DEV void tma_load_3d_pair(const CUtensorMap *map, uint32_t mbar, void *dst, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(mbar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+MOE_DEV void tma_store_3d(const CUtensorMap *map, const void *src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+MOE_DEV void tma_add_3d(const CUtensorMap *map, const void *src, int c0, int c1, int c2) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   map),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+
+// Descriptor of an MN-major operand in the 128-byte swizzle: rows of 64 features
+// (128 bytes), one per reduction step; 8 steps (1024 bytes) to the next group
+// of 8, 64 steps (8192 bytes) to the next 64 features.
+MOE_DEV uint64_t mn_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(8192u >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+// Instruction descriptor of kind::f16 with fp32 accumulation, M = 256 over the
+// pair: operand format (1 bf16, 0 fp16) at [7,10) and [10,13), MN-major A / B at
+// bits 15 / 16, N >> 3 at [17,23), M >> 4 at [24,29).
+template <int DIR>
+MOE_DEV uint32_t tc_idesc(int dtype, int n) {
+  const uint32_t f = dtype == MOE_ELEM_BF16 ? 1u : 0u;
+  return (1u << 4) | (f << 7) | (f << 10) | (DIR != GROUPED_FWD ? 1u << 15 : 0u) |
+         (DIR == GROUPED_WGRAD ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (16u << 24);
+}
+
+struct TcTile {
+  int e;
+  int f0;     // first output feature of the pair (A's rows)
+  int c0;     // first column: token row (forward, dgrad) or feature (wgrad)
+  int n;      // columns of the product: a multiple of 32 (wgrad: 128)
+  int valid;  // columns that are stored
+  int k0;     // first reduction step (wgrad: the expert's first row)
+  int klen;   // reduction length
+};
+
+template <int DIR>
+MOE_DEV long tc_units(const GroupedArgs &g) {
+  const int F = DIR == GROUPED_DGRAD ? g.K : g.N;
+  const long nf = (F + 255) >> 8;
+  if (DIR == GROUPED_WGRAD) return g.E * nf * ((g.K + 255) >> 8);
+  return nf * __ldg(g.tiles + g.E);
+}
+
+template <int DIR>
+MOE_DEV TcTile tc_tile(const GroupedArgs &g, long u) {
+  TcTile t;
+  int lo, hi;
+  if constexpr (DIR == GROUPED_WGRAD) {
+    const int nf = (g.N + 255) >> 8, nc = (g.K + 255) >> 8;
+    t.e = static_cast<int>(u / (nf * nc));
+    const int r = static_cast<int>(u - static_cast<long>(t.e) * (nf * nc));
+    t.f0 = (r / nc) * 256;
+    t.c0 = (r % nc) * 256;
+    t.valid = g.K - t.c0 < 256 ? g.K - t.c0 : 256;
+    group_rows(g, t.e, lo, hi);
+    t.k0 = lo;
+    t.klen = hi - lo;
+  } else {
+    const int nf = ((DIR == GROUPED_DGRAD ? g.K : g.N) + 255) >> 8;
+    t.e = group_of_tile(g.tiles, g.E, static_cast<int>(u / nf));
+    const int first = __ldg(g.tiles + t.e), mt = __ldg(g.tiles + t.e + 1) - first;
+    const int local = static_cast<int>(u - static_cast<long>(first) * nf);
+    t.f0 = (local / mt) * 256;
+    const int tt = local % mt;
+    group_rows(g, t.e, lo, hi);
+    // whole tiles, the last two share what is left evenly
+    int from = tt * kTileTokens, to = from + kTileTokens;
+    if (mt > 1 && tt >= mt - 2) {
+      const int base = (mt - 2) * kTileTokens, left = hi - lo - base;
+      const int half = ((left + 1) / 2 + 31) & ~31;
+      from = tt == mt - 1 ? base + half : base;
+      to = tt == mt - 1 ? base + left : base + half;
+    }
+    if (to > hi - lo) to = hi - lo;
+    t.c0 = lo + from;
+    t.valid = to - from;
+    t.k0 = 0;
+    t.klen = DIR == GROUPED_DGRAD ? g.N : g.K;
+  }
+  // MN-major columns come in whole 64-feature blocks per CTA
+  t.n = DIR == GROUPED_WGRAD ? (t.valid > 128 ? 256 : 128) : (t.valid + 31) & ~31;
+  return t;
+}
+
+// A piece of 32 tokens x 32 features from one warp's accumulator columns (lane =
+// feature): neighbouring lanes swap so that each holds two features of one
+// token, and the piece leaves through shared memory as 16-byte stores.
+template <typename T>
+MOE_DEV void put_tokens(const float *v, uint8_t *buf, T *out, long ld, int tokens, int features, int lane) {
+  const bool odd = lane & 1;
+  __syncwarp();
+#pragma unroll
+  for (int t = 0; t < 32; t += 2) {
+    const float mine = odd ? v[t + 1] : v[t];
+    const float other = __shfl_xor_sync(0xffffffffu, odd ? v[t] : v[t + 1], 1);
+    const uint32_t w = odd ? Elem<T>::pack2(other, mine) : Elem<T>::pack2(mine, other);
+    *reinterpret_cast<uint32_t *>(buf + (t + (odd ? 1 : 0)) * 64 + (lane >> 1) * 4) = w;
+  }
+  __syncwarp();
+  const int c = (lane & 3) * 8;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = (lane >> 2) + 8 * i;
+    if (t < tokens && c < features)
+      *reinterpret_cast<uint4 *>(out + t * ld + c) = *reinterpret_cast<const uint4 *>(buf + t * 64 + c * 2);
+  }
+}
+
+// A piece of 32 rows x 128 bytes of dw (lane = row) into 128-byte-swizzled shared
+// memory and out by TMA, which clips it to the expert's matrix.
+MOE_DEV void put_rows(const uint32_t *w, uint8_t *buf, const CUtensorMap *map, bool add, int col, int row, int e,
+                      bool inside, int lane) {
+  if (lane == 0) bulk_wait_read<1>();  // the piece before last has left this buffer
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<uint4 *>(buf + lane * 128 + ((j ^ (lane & 7)) * 16)) =
+        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    if (inside) {
+      if (add) tma_add_3d(map, buf, col, row, e);
+      else tma_store_3d(map, buf, col, row, e);
+    }
+    bulk_commit();
+  }
+}
+
+template <int DIR>
+__global__ void __launch_bounds__(192, 1) grouped_tc_kernel(const __grid_constant__ TcMaps maps, const GroupedArgs g) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  uint8_t *staging = smem + kStages * kStageBytes;
+  uint64_t *full = reinterpret_cast<uint64_t *>(staging + 4 * kStaging);
+  uint64_t *empty = full + kStages;
+  uint64_t *tfull = empty + kStages;
+  uint64_t *tempty = tfull + 2;
+  uint64_t *done = tempty + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const long pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 256);  // epilogue threads of both CTAs
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+    tc_fence_before();
+  }
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const long total = tc_units<DIR>(g);
+
+  if (warp == 0) {
+    // ------------------------------------------------ TMA producer (both CTAs)
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t ph = 0;
+      int fenced = -1;
+      for (long u = pair; u < total && !*abort_flag; u += pairs) {
+        const TcTile t = tc_tile<DIR>(g, u);
+        const int half = t.n >> 1;
+        const int fr = t.f0 + static_cast<int>(rank) * 128, cr = t.c0 + static_cast<int>(rank) * half;
+        const int level = half > 64 ? 3 : (half > 32 ? 2 : (half > 16 ? 1 : 0));
+        const uint32_t b_bytes = DIR == GROUPED_WGRAD ? (half > 64 ? 16384u : 8192u) : 2048u << level;
+        const CUtensorMap *ma = &maps.a, *mb = &maps.b[level];
+        if constexpr (DIR == GROUPED_WGRAD) {
+          if (t.klen == 0) continue;
+          ma = reinterpret_cast<const CUtensorMap *>(g.maps + static_cast<long>(t.e) * 256);
+          mb = reinterpret_cast<const CUtensorMap *>(g.maps + static_cast<long>(t.e) * 256 + 128);
+          if (fenced != t.e) {  // the maps were written by an earlier launch
+            asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(ma) : "memory");
+            asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(mb) : "memory");
+            fenced = t.e;
+          }
+        }
+        bool ok = true;
+        for (int kb = 0; kb < t.klen; kb += 64) {
+          if (!mbar_wait(&empty[stage], ph ^ 1u, abort_flag, g.status)) {
+            ok = false;
+            break;
+          }
+          uint8_t *sa = smem + stage * kStageBytes, *sb = sa + 16384;
+          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * (16384u + b_bytes));
+          const uint32_t bar = peer_smem(smem_u32(&full[stage]), 0);
+          const int k = t.k0 + kb;
+          if constexpr (DIR == GROUPED_FWD) {
+            tma_load_3d_pair(ma, bar, sa, k, fr, t.e);
+            tma_load_2d_pair(mb, bar, sb, k, cr);
+          } else if constexpr (DIR == GROUPED_DGRAD) {
+            tma_load_3d_pair(ma, bar, sa, fr, k, t.e);
+            tma_load_3d_pair(ma, bar, sa + 8192, fr + 64, k, t.e);
+            tma_load_2d_pair(mb, bar, sb, k, cr);
+          } else {
+            tma_load_2d_pair(ma, bar, sa, fr, k);
+            tma_load_2d_pair(ma, bar, sa + 8192, fr + 64, k);
+            tma_load_2d_pair(mb, bar, sb, cr, k);
+            if (half > 64) tma_load_2d_pair(mb, bar, sb + 8192, cr + 64, k);
+          }
+          if (++stage == kStages) {
+            stage = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA issuer (pair leader)
+    if (leader && lane == 0) {
+      int stage = 0, acc = 0;
+      uint32_t ph = 0, aph = 0;
+      bool ok = true;
+      for (long u = pair; u < total && ok; u += pairs) {
+        const TcTile t = tc_tile<DIR>(g, u);
+        if (t.klen == 0) continue;
+        if (!mbar_wait(&tempty[acc], aph ^ 1u, abort_flag, g.status)) break;
+        tc_fence_after();
+        const uint32_t dt = tmem + static_cast<uint32_t>(acc * 256);
+        const uint32_t idesc = tc_idesc<DIR>(g.dtype, t.n);
+        for (int kb = 0; kb < t.klen; kb += 64) {
+          if (!mbar_wait(&full[stage], ph, abort_flag, g.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + stage * kStageBytes), sb = sa + 16384;
+          const int left = t.klen - kb;  // steps past the end hold zeros in both operands
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (k * 16 < left) {
+              const uint64_t ad = DIR == GROUPED_FWD ? sw128_desc(sa + 32 * k) : mn_desc(sa + 2048 * k);
+              const uint64_t bd = DIR == GROUPED_WGRAD ? mn_desc(sb + 2048 * k) : sw128_desc(sb + 32 * k);
+              mma_bf16_pair(dt, ad, bd, idesc, (kb | k) ? 1u : 0u);
+            }
+          }
+          mma_commit_pair_mc(&empty[stage], 3);
+          if (++stage == kStages) {
+            stage = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+        mma_commit_pair_mc(&tfull[acc], 3);
+        if (++acc == 2) {
+          acc = 0;
+          aph ^= 1u;
+        }
+      }
+      mma_commit_pair_mc(done, 1);
+      volatile int no_abort = 0;
+      mbar_wait(done, 0, &no_abort, g.status);
+    }
+  } else {
+    // ------------------------------------------------ epilogue (warps 2..5, both CTAs)
+    const int q = warp & 3;
+    uint8_t *buf = staging + (warp - 2) * kStaging;
+    int acc = 0, piece = 0;
+    uint32_t aph = 0;
+    for (long u = pair; u < total; u += pairs) {
+      const TcTile t = tc_tile<DIR>(g, u);
+      const int fr = t.f0 + static_cast<int>(rank) * 128 + q * 32;  // this warp's first feature
+      const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * 256);
+      if (t.klen > 0) {
+        if (!mbar_wait(&tfull[acc], aph, abort_flag, g.status)) break;
+        tc_fence_after();
+      } else if (g.accumulate) {
+        continue;
+      }
+      const uint32_t tempty_addr = smem_u32(&tempty[acc]);
+      auto release = [&]() {
+        tc_fence_before();
+        if (leader) mbar_arrive(&tempty[acc]);
+        else mbar_arrive_remote(peer_smem(tempty_addr, 0));
+      };
+      if constexpr (DIR == GROUPED_WGRAD) {
+        const bool wide = g.out_dtype == MOE_ELEM_FP32;
+        const int step = wide ? 32 : 64;
+        for (int j = 0; j < t.n; j += step) {
+          uint32_t r[64], w[32];
+          if (t.klen > 0) {
+            tmem_ld32_async(tb + j, r);
+            if (!wide) tmem_ld32_async(tb + j + 32, r + 32);
+            tmem_ld_wait();
+            reg_fence<64>(r);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) r[i] = 0;
+          }
+          if (j + step >= t.n && t.klen > 0) release();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const float a = __uint_as_float(r[2 * i]), b = __uint_as_float(r[2 * i + 1]);
+            if (wide) w[i] = r[i];
+            else w[i] = g.dtype == MOE_ELEM_BF16 ? Elem<__nv_bfloat16>::pack2(a, b) : Elem<__half>::pack2(a, b);
+          }
+          put_rows(w, buf + (piece & 1) * 4096, &maps.out, g.accumulate != 0, t.c0 + j, fr, t.e,
+                   fr < g.N && t.c0 + j < g.K, lane);
+          ++piece;
+        }
+      } else {
+        const int F = DIR == GROUPED_DGRAD ? g.K : g.N;
+        const long ld = DIR == GROUPED_DGRAD ? g.ld_x : g.ld_y;
+        for (int j = 0; j < t.n; j += 32) {
+          uint32_t r[32];
+          tmem_ld32_async(tb + j, r);
+          tmem_ld_wait();
+          reg_fence<32>(r);
+          if (j + 32 >= t.n) release();
+          const float *v = reinterpret_cast<const float *>(r);
+          const long row = t.c0 + j;
+          const int tokens = t.valid - j;
+          if (fr >= F) continue;
+          if (DIR == GROUPED_FWD && g.out_dtype == MOE_ELEM_FP32) {
+            float *out = static_cast<float *>(g.y) + row * ld + fr + lane;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i < tokens && fr + lane < F) out[i * ld] = v[i];
+          } else {
+            uint16_t *out = static_cast<uint16_t *>(DIR == GROUPED_DGRAD ? g.dx : g.y) + row * ld + fr;
+            if (g.dtype == MOE_ELEM_BF16)
+              put_tokens(v, buf, reinterpret_cast<__nv_bfloat16 *>(out), ld, tokens, F - fr, lane);
+            else
+              put_tokens(v, buf, reinterpret_cast<__half *>(out), ld, tokens, F - fr, lane);
+          }
+        }
+      }
+      if (t.klen > 0 && ++acc == 2) {
+        acc = 0;
+        aph ^= 1u;
+      }
+    }
+    if (DIR == GROUPED_WGRAD && lane == 0) bulk_wait<0>();
+  }
+
+  __syncthreads();
+  cluster_sync();  // no CTA leaves while its peer may still signal it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+// The experts' tensor maps of the weight gradient: dy's and x's map with the row
+// extent cut to the expert's last row.  One warp per map; the copy to global
+// memory makes it visible to later TMA accesses.
+__global__ void __launch_bounds__(128) grouped_maps_kernel(const __grid_constant__ CUtensorMap dy,
+                                                           const __grid_constant__ CUtensorMap x, const GroupedArgs g) {
+  __shared__ __align__(128) uint32_t sm[4][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int i = blockIdx.x * 4 + warp;
+  if (i >= 2 * g.E) return;
+  sm[warp][lane] = reinterpret_cast<const uint32_t *>((i & 1) ? &x : &dy)[lane];
+  __syncwarp();
+  if (lane == 0) {
+    int lo, hi;
+    group_rows(g, i >> 1, lo, hi);
+    const uint64_t at = smem_u32(sm[warp]);
+    asm volatile("tensormap.replace.tile.global_dim.shared::cta.b1024.b32 [%0], 1, %1;" ::"l"(at), "r"(hi > 0 ? hi : 1)
+                 : "memory");
+  }
+  __syncwarp();
+  asm volatile(
+      "tensormap.cp_fenceproxy.global.shared::cta.tensormap::generic.release.gpu.sync.aligned [%0], [%1], 128;" ::"l"(
+          g.maps + static_cast<long>(i) * 128),
+      "r"(smem_u32(sm[warp]))
+      : "memory");
+}
+
+template <int DIR>
+int tc_clusters_query() {
+  if (cudaFuncSetAttribute(grouped_tc_kernel<DIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(kSmem)) != cudaSuccess)
+    return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2, 1, 1);
+  cfg.blockDim = dim3(192, 1, 1);
+  cfg.dynamicSmemBytes = kSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  return cudaOccupancyMaxActiveClusters(&n, grouped_tc_kernel<DIR>, &cfg) == cudaSuccess ? n : 0;
+}
+
+template <int DIR>
+cudaError_t launch_tc(const TcMaps &maps, const GroupedArgs &g, long units, cudaStream_t s) {
+  static int memo[64] = {};
+  const int most = per_device_memo(memo, tc_clusters_query<DIR>);
+  if (most <= 0) return cudaErrorInvalidConfiguration;
+  if (units <= 0) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(units < most ? units : most), 1, 1);
+  cfg.blockDim = dim3(192, 1, 1);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<DIR>, maps, g);
+}
+
+// Token rows [rows, cols] with boxes of 64 columns x 16 << i rows.
+bool row_maps(CUtensorMap *m, int elem, const void *p, long rows, int cols, long ld) {
+  const uint64_t dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)};
+  const uint64_t strides[1] = {static_cast<uint64_t>(ld) * 2};
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t box[2] = {64, 16u << i};
+    if (!host_encode_map(&m[i], elem, p, 2, dims, strides, box)) return false;
+  }
+  return true;
+}
+
+bool expert_map(CUtensorMap *m, int elem, const void *p, const GroupedArgs &g, long ld, long ld_e, uint32_t c, uint32_t r) {
+  const uint64_t e = elem_bytes(elem);
+  const uint64_t dims[3] = {static_cast<uint64_t>(g.K), static_cast<uint64_t>(g.N), static_cast<uint64_t>(g.E)};
+  const uint64_t strides[2] = {static_cast<uint64_t>(ld) * e, static_cast<uint64_t>(ld_e) * e};
+  const uint32_t box[3] = {c, r, 1};
+  return host_encode_map(m, elem, p, 3, dims, strides, box);
+}
+
+}  // namespace
+
+int grouped_tc_tile_rows() { return kTileTokens; }
+
+cudaError_t launch_grouped_tc(const GroupedArgs &g, int dir, cudaStream_t s) {
+  TcMaps m;
+  const long tokens = (g.rows + kTileTokens - 1L) / kTileTokens + (g.E < g.rows ? g.E : g.rows);
+  if (dir == GROUPED_WGRAD) {
+    CUtensorMap dy, x;
+    const uint64_t n[2] = {static_cast<uint64_t>(g.N), static_cast<uint64_t>(g.rows > 0 ? g.rows : 1)};
+    const uint64_t k[2] = {static_cast<uint64_t>(g.K), n[1]};
+    const uint64_t sn[1] = {static_cast<uint64_t>(g.ld_y) * 2}, sk[1] = {static_cast<uint64_t>(g.ld_x) * 2};
+    const uint32_t box[2] = {64, 64};
+    if (!host_encode_map(&dy, g.dtype, g.dy, 2, n, sn, box) || !host_encode_map(&x, g.dtype, g.x, 2, k, sk, box) ||
+        !expert_map(&m.out, g.out_dtype, g.dw, g, g.K, static_cast<long>(g.N) * g.K, g.out_dtype == MOE_ELEM_FP32 ? 32 : 64,
+                    32))
+      return cudaErrorInvalidValue;
+    m.a = dy;
+    for (int i = 0; i < 4; ++i) m.b[i] = x;
+    {
+      HostTrace t("grouped_maps", s);
+      grouped_maps_kernel<<<(2 * g.E + 3) / 4, 128, 0, s>>>(dy, x, g);
+      const cudaError_t e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+    }
+    HostTrace t("grouped_wgrad", s);
+    return launch_tc<GROUPED_WGRAD>(m, g, static_cast<long>(g.E) * ((g.N + 255) / 256) * ((g.K + 255) / 256), s);
+  }
+  if (g.rows <= 0) return cudaSuccess;
+  if (dir == GROUPED_FWD) {
+    if (!row_maps(m.b, g.dtype, g.x, g.rows, g.K, g.ld_x) || !expert_map(&m.a, g.dtype, g.w, g, g.ld_w, g.ld_e, 64, 128))
+      return cudaErrorInvalidValue;
+    m.out = m.a;
+    HostTrace t("grouped_forward", s);
+    return launch_tc<GROUPED_FWD>(m, g, tokens * ((g.N + 255) / 256), s);
+  }
+  if (!row_maps(m.b, g.dtype, g.dy, g.rows, g.N, g.ld_y) || !expert_map(&m.a, g.dtype, g.w, g, g.ld_w, g.ld_e, 64, 64))
+    return cudaErrorInvalidValue;
+  m.out = m.a;
+  HostTrace t("grouped_dgrad", s);
+  return launch_tc<GROUPED_DGRAD>(m, g, tokens * ((g.K + 255) / 256), s);
+}
+
+}  // namespace moe
