@@ -46,14 +46,16 @@ struct GroupedArgs {
   uint8_t *maps; // workspace: 2 E tensor maps of 128 bytes (weight gradient)
 };
 
-// Status word and, where `tiles` / map templates are given, the tile table and
-// the experts' tensor maps; zeroes the rows of `out` that belong to no expert.
+// The first launch of a call writes the status word (bad offsets) and zeroes the
+// output rows of no expert: the plan does it for the plain kernel, whose tile
+// table it also makes, the others do it themselves.
 cudaError_t launch_grouped_plan(const GroupedArgs &g, int tile_rows, void *out, int out_elem, int out_cols,
                                 long ld_out, cudaStream_t s);
-int grouped_plain_tile_rows();
-cudaError_t launch_grouped_plain(const GroupedArgs &g, int dir, cudaStream_t s);
+// Any size, stride and alignment; `first`: with the plan in front.
+cudaError_t launch_grouped_plain(const GroupedArgs &g, int dir, bool first, cudaStream_t s);
+// Forward of a few rows (no plan needed): 16-byte aligned rows of x and w.
+cudaError_t launch_grouped_few(const GroupedArgs &g, cudaStream_t s);
 // Tensor-core path: every pointer and row stride a multiple of 16 bytes.
-int grouped_tc_tile_rows();
 cudaError_t launch_grouped_tc(const GroupedArgs &g, int dir, cudaStream_t s);
 
 // ---------------------------------------------------------------- block norms

@@ -78,11 +78,16 @@ bool grouped_tensor(const moe::GroupedArgs &g, int dir) {
   return tma_rows(g.dy, g.ld_y) && tma_rows(g.x, g.ld_x) && aligned(g.dw, 16);
 }
 
-int grouped_product(const moe::GroupedArgs &g, int dir, cudaStream_t s) {
-  return status_of(grouped_tensor(g, dir) ? moe::launch_grouped_tc(g, dir, s) : moe::launch_grouped_plain(g, dir, s));
+// Few rows that mostly have an expert of their own: reading the weights bounds
+// the call and the tensor cores have nothing to reuse.
+bool grouped_few(const moe::GroupedArgs &g) {
+  return g.rows > 0 && g.rows <= 64 && g.rows <= 4L * g.E && g.K % 8 == 0 && tma_rows(g.x, g.ld_x) &&
+         tma_rows(g.w, g.ld_w) && g.ld_e % 8 == 0;
 }
-int grouped_tile_rows(const moe::GroupedArgs &g, int dir) {
-  return grouped_tensor(g, dir) ? moe::grouped_tc_tile_rows() : moe::grouped_plain_tile_rows();
+
+int grouped_product(const moe::GroupedArgs &g, int dir, bool first, cudaStream_t s) {
+  return status_of(grouped_tensor(g, dir) ? moe::launch_grouped_tc(g, dir, s)
+                                          : moe::launch_grouped_plain(g, dir, first, s));
 }
 
 // ---------------------------------------------------------------- norm
@@ -155,10 +160,8 @@ int moe_grouped_forward(const moe_grouped_config *cfg, const void *x, const void
   g.x = x;
   g.w = w;
   g.y = y;
-  if ((rc = status_of(moe::launch_grouped_plan(g, grouped_tile_rows(g, moe::GROUPED_FWD), y, g.out_dtype, g.N,
-                                               g.ld_y, stream))) != MOE_OK)
-    return rc;
-  return grouped_product(g, moe::GROUPED_FWD, stream);
+  if (grouped_few(g)) return status_of(moe::launch_grouped_few(g, stream));
+  return grouped_product(g, moe::GROUPED_FWD, true, stream);
 }
 
 int moe_grouped_backward(const moe_grouped_config *cfg, const void *dy, const void *x, const void *w,
@@ -180,11 +183,8 @@ int moe_grouped_backward(const moe_grouped_config *cfg, const void *dy, const vo
   g.w = w;
   g.dx = dx;
   g.dw = dw;
-  if ((rc = status_of(moe::launch_grouped_plan(g, grouped_tile_rows(g, moe::GROUPED_DGRAD), dx, g.dtype, g.K, g.ld_x,
-                                               stream))) != MOE_OK)
-    return rc;
-  if (dx && (rc = grouped_product(g, moe::GROUPED_DGRAD, stream)) != MOE_OK) return rc;
-  if (dw && (rc = grouped_product(g, moe::GROUPED_WGRAD, stream)) != MOE_OK) return rc;
+  if (dx && (rc = grouped_product(g, moe::GROUPED_DGRAD, true, stream)) != MOE_OK) return rc;
+  if (dw && (rc = grouped_product(g, moe::GROUPED_WGRAD, !dx, stream)) != MOE_OK) return rc;
   return MOE_OK;
 }
 

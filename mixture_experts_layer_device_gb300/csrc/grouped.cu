@@ -259,9 +259,121 @@ cudaError_t plain_type(const GroupedArgs &g, int dir, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// ---------------------------------------------------------------- few rows
+// A generated token: few rows, nearly each with an expert of its own, so the
+// work is reading those experts' weights once.  A warp forms FEW_F features of
+// up to FEW_R rows of one expert; its lanes split K in 16-byte pieces, FEW_F x
+// UNROLL of them in flight each, and join by shuffles in a fixed order.  Block
+// (features, row): the first row of every FEW_R rows of an expert does the
+// work, the others leave at once.
+constexpr int FEW_F = 4, FEW_R = 4, FEW_WARPS = 4;
+
+template <typename T, int R>
+MOE_DEV void few_dot(const GroupedArgs &g, const T *x, const T *w, int nf, float acc[R][FEW_F]) {
+  const int lane = threadIdx.x & 31, chunks = g.K >> 3;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int f = 0; f < FEW_F; ++f) acc[r][f] = 0.f;
+  constexpr int UNROLL = 4;
+  for (int c0 = lane; c0 < chunks; c0 += 32 * UNROLL) {
+    uint4 q[UNROLL][FEW_F];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+      for (int f = 0; f < FEW_F; ++f) {
+        q[u][f] = make_uint4(0, 0, 0, 0);
+        if (c0 + 32 * u < chunks && f < nf) q[u][f] = ld_stream(w + f * g.ld_w + (c0 + 32 * u) * 8L);
+      }
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+      if (c0 + 32 * u >= chunks) break;
+      float xv[R][8];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        Elem<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(x + r * g.ld_x + (c0 + 32 * u) * 8L)), xv[r]);
+#pragma unroll
+      for (int f = 0; f < FEW_F; ++f) {
+        float wv[8];
+        Elem<T>::unpack(q[u][f], wv);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) acc[r][f] = fmaf(xv[r][k], wv[k], acc[r][f]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int f = 0; f < FEW_F; ++f)
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) acc[r][f] += __shfl_xor_sync(0xffffffffu, acc[r][f], o);
+}
+
+template <typename T, int R>
+MOE_DEV void few_rows(const GroupedArgs &g, int row, int e, int n0, int nf) {
+  const int lane = threadIdx.x & 31;
+  float acc[R][FEW_F];
+  few_dot<T, R>(g, static_cast<const T *>(g.x) + row * g.ld_x,
+                static_cast<const T *>(g.w) + e * g.ld_e + n0 * g.ld_w, nf, acc);
+  // lane r * FEW_F + f stores element (r, f)
+  float v = 0.f;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int f = 0; f < FEW_F; ++f)
+      if (lane == r * FEW_F + f) v = acc[r][f];
+  const int r = lane / FEW_F, f = lane % FEW_F;
+  if (r < R && f < nf)
+    store_elem<T>(g.y, (row + r) * g.ld_y + n0 + f, v, g.out_dtype == MOE_ELEM_FP32, false);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(FEW_WARPS * 32) grouped_few_kernel(const GroupedArgs g) {
+  const int row = blockIdx.y;
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    bool bad = false;
+    int lo, hi;
+    for (int e = threadIdx.x; e < g.E; e += blockDim.x) bad |= !group_rows(g, e, lo, hi);
+    const int any = __syncthreads_or(bad);
+    if (threadIdx.x == 0) *g.status = any ? kStatusBounds : 0;
+  }
+  // experts that end at or before this row = the expert of the row
+  int before = 0;
+  for (int base = 0; base < g.E; base += blockDim.x) {
+    const int e = base + threadIdx.x;
+    before += __syncthreads_count(e < g.E && __ldg(g.offsets + e + 1) <= row);
+  }
+  const int e = before < g.E ? before : g.E - 1;
+  int lo, hi;
+  group_rows(g, e, lo, hi);
+  const int n0 = (blockIdx.x * FEW_WARPS + (threadIdx.x >> 5)) * FEW_F;
+  if (n0 >= g.N) return;
+  const int nf = g.N - n0 < FEW_F ? g.N - n0 : FEW_F;
+  if (row < lo || row >= hi) {  // a row of no expert
+    if (static_cast<int>(threadIdx.x & 31) < nf)
+      store_elem<T>(g.y, row * g.ld_y + n0 + (threadIdx.x & 31), 0.f, g.out_dtype == MOE_ELEM_FP32, false);
+    return;
+  }
+  if ((row - lo) % FEW_R) return;
+  switch (hi - row) {
+    case 1: few_rows<T, 1>(g, row, e, n0, nf); break;
+    case 2: few_rows<T, 2>(g, row, e, n0, nf); break;
+    case 3: few_rows<T, 3>(g, row, e, n0, nf); break;
+    default: few_rows<T, 4>(g, row, e, n0, nf); break;
+  }
+}
+
 }  // namespace
 
-int grouped_plain_tile_rows() { return PT; }
+cudaError_t launch_grouped_few(const GroupedArgs &g, cudaStream_t s) {
+  HostTrace t("grouped_few", s);
+  const dim3 grid((g.N + FEW_WARPS * FEW_F - 1) / (FEW_WARPS * FEW_F), g.rows);
+  if (g.dtype == MOE_ELEM_BF16) grouped_few_kernel<__nv_bfloat16><<<grid, FEW_WARPS * 32, 0, s>>>(g);
+  else grouped_few_kernel<__half><<<grid, FEW_WARPS * 32, 0, s>>>(g);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_grouped_plan(const GroupedArgs &g, int tile_rows, void *out, int out_elem, int out_cols,
                                 long ld_out, cudaStream_t s) {
@@ -273,7 +385,13 @@ cudaError_t launch_grouped_plan(const GroupedArgs &g, int tile_rows, void *out, 
   return cudaGetLastError();
 }
 
-cudaError_t launch_grouped_plain(const GroupedArgs &g, int dir, cudaStream_t s) {
+cudaError_t launch_grouped_plain(const GroupedArgs &g, int dir, bool first, cudaStream_t s) {
+  if (first) {
+    const bool fwd = dir == GROUPED_FWD;
+    const cudaError_t e = launch_grouped_plan(g, PT, fwd ? g.y : (dir == GROUPED_DGRAD ? g.dx : nullptr),
+                                              fwd ? g.out_dtype : g.dtype, fwd ? g.N : g.K, fwd ? g.ld_y : g.ld_x, s);
+    if (e != cudaSuccess) return e;
+  }
   HostTrace t(dir == GROUPED_FWD ? "grouped_fwd_plain" : dir == GROUPED_DGRAD ? "grouped_dgrad_plain" : "grouped_wgrad_plain", s);
   return g.dtype == MOE_ELEM_BF16 ? plain_type<__nv_bfloat16>(g, dir, s) : plain_type<__half>(g, dir, s);
 }

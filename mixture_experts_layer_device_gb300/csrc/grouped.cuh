@@ -21,7 +21,7 @@ MOE_DEV int group_of_tile(const int *tiles, int E, int u) {
   int lo = 0, hi = E - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(tiles + mid) <= u) lo = mid;
+    if (tiles[mid] <= u) lo = mid;
     else hi = mid - 1;
   }
   return lo;

@@ -37,6 +37,10 @@ constexpr int kStaging = 8192;               // per epilogue warp: two 4 KB piec
 constexpr int kTileTokens = 256;
 constexpr size_t kSmem = 1024 + kStages * kStageBytes + 4 * kStaging + (2 * kStages + 5) * 8 + 16;
 static_assert(kSmem <= 232448, "shared memory");
+// Forward and dgrad stage 2 KB per warp and keep the tile table in the rest;
+// more experts than it holds take the plan launch's table in the workspace.
+constexpr int kTablePlace = 4 * 2048;
+constexpr int kTableExperts = (4 * kStaging - kTablePlace) / 4 - 1;
 
 struct TcMaps {
   CUtensorMap a;        // forward, dgrad: w
@@ -96,12 +100,49 @@ struct TcTile {
   int klen;   // reduction length
 };
 
+// First token tile of every expert into tiles[0 .. E], by all 192 threads; no
+// tiles at all when the offsets are bad.
+MOE_DEV bool tile_table(const GroupedArgs &g, int *tiles, int *warp_sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int run = 0;
+  bool bad = false;
+  for (int base = 0; base < g.E; base += 192) {
+    const int e = base + threadIdx.x;
+    int n = 0;
+    if (e < g.E) {
+      int lo, hi;
+      bad |= !group_rows(g, e, lo, hi);
+      n = (hi - lo + kTileTokens - 1) / kTileTokens;
+    }
+    int inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    int before = run;
+#pragma unroll
+    for (int w = 0; w < 6; ++w) {
+      if (w < warp) before += warp_sum[w];
+      run += warp_sum[w];
+    }
+    if (e < g.E) tiles[e] = before + inc - n;
+    __syncthreads();
+  }
+  const bool any = __syncthreads_or(bad);
+  if (threadIdx.x == 0) tiles[g.E] = any ? 0 : run;
+  __syncthreads();
+  return any;
+}
+
 template <int DIR>
 MOE_DEV long tc_units(const GroupedArgs &g) {
   const int F = DIR == GROUPED_DGRAD ? g.K : g.N;
   const long nf = (F + 255) >> 8;
   if (DIR == GROUPED_WGRAD) return g.E * nf * ((g.K + 255) >> 8);
-  return nf * __ldg(g.tiles + g.E);
+  return nf * g.tiles[g.E];
 }
 
 template <int DIR>
@@ -121,7 +162,7 @@ MOE_DEV TcTile tc_tile(const GroupedArgs &g, long u) {
   } else {
     const int nf = ((DIR == GROUPED_DGRAD ? g.K : g.N) + 255) >> 8;
     t.e = group_of_tile(g.tiles, g.E, static_cast<int>(u / nf));
-    const int first = __ldg(g.tiles + t.e), mt = __ldg(g.tiles + t.e + 1) - first;
+    const int first = g.tiles[t.e], mt = g.tiles[t.e + 1] - first;
     const int local = static_cast<int>(u - static_cast<long>(first) * nf);
     t.f0 = (local / mt) * 256;
     const int tt = local % mt;
@@ -191,7 +232,8 @@ MOE_DEV void put_rows(const uint32_t *w, uint8_t *buf, const CUtensorMap *map, b
 }
 
 template <int DIR>
-__global__ void __launch_bounds__(192, 1) grouped_tc_kernel(const __grid_constant__ TcMaps maps, const GroupedArgs g) {
+__global__ void __launch_bounds__(192, 1) grouped_tc_kernel(const __grid_constant__ TcMaps maps, const GroupedArgs ga) {
+  GroupedArgs g = ga;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
@@ -225,6 +267,13 @@ __global__ void __launch_bounds__(192, 1) grouped_tc_kernel(const __grid_constan
     tmem_alloc_pair(tmem_slot, 512);
     tmem_relinquish_pair();
     tc_fence_before();
+  }
+  if constexpr (DIR != GROUPED_WGRAD) {
+    if (g.E <= kTableExperts) {
+      g.tiles = reinterpret_cast<int *>(staging + kTablePlace);
+      const bool bad = tile_table(g, g.tiles, reinterpret_cast<int *>(staging));
+      if (blockIdx.x == 0 && threadIdx.x == 0) *g.status = bad ? kStatusBounds : 0;
+    }
   }
   __syncthreads();
   cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
@@ -335,9 +384,23 @@ __global__ void __launch_bounds__(192, 1) grouped_tc_kernel(const __grid_constan
   } else {
     // ------------------------------------------------ epilogue (warps 2..5, both CTAs)
     const int q = warp & 3;
-    uint8_t *buf = staging + (warp - 2) * kStaging;
+    uint8_t *buf = staging + (warp - 2) * (DIR == GROUPED_WGRAD ? kStaging : 2048);
     int acc = 0, piece = 0;
     uint32_t aph = 0;
+    if constexpr (DIR != GROUPED_WGRAD) {
+      // zeros for the rows of no expert (the plan launch has done it otherwise)
+      int lo, hi, lo_last, hi_last;
+      group_rows(g, 0, lo, hi);
+      group_rows(g, g.E - 1, lo_last, hi_last);
+      const int outside = g.E <= kTableExperts ? lo + (g.rows - hi_last) : 0;
+      const bool wide = DIR == GROUPED_FWD && g.out_dtype == MOE_ELEM_FP32;
+      const long ld = (DIR == GROUPED_DGRAD ? g.ld_x : g.ld_y) * (wide ? 4 : 2);
+      const int bytes = (DIR == GROUPED_DGRAD ? g.K : g.N) * (wide ? 4 : 2);
+      uint8_t *out = static_cast<uint8_t *>(DIR == GROUPED_DGRAD ? g.dx : g.y);
+      for (long i = blockIdx.x; i < outside; i += gridDim.x)
+        for (int b = (threadIdx.x - 64) * 16; b < bytes; b += 128 * 16)
+          *reinterpret_cast<uint4 *>(out + (i < lo ? i : hi_last + (i - lo)) * ld + b) = make_uint4(0, 0, 0, 0);
+    }
     for (long u = pair; u < total; u += pairs) {
       const TcTile t = tc_tile<DIR>(g, u);
       const int fr = t.f0 + static_cast<int>(rank) * 128 + q * 32;  // this warp's first feature
@@ -430,6 +493,13 @@ __global__ void __launch_bounds__(128) grouped_maps_kernel(const __grid_constant
   __shared__ __align__(128) uint32_t sm[4][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int i = blockIdx.x * 4 + warp;
+  if (blockIdx.x == 0 && !g.dx) {  // the first launch of the call writes the status word
+    bool bad = false;
+    int lo, hi;
+    for (int e = threadIdx.x; e < g.E; e += 128) bad |= !group_rows(g, e, lo, hi);
+    const int any = __syncthreads_or(bad);
+    if (threadIdx.x == 0) *g.status = any ? kStatusBounds : 0;
+  }
   if (i >= 2 * g.E) return;
   sm[warp][lane] = reinterpret_cast<const uint32_t *>((i & 1) ? &x : &dy)[lane];
   __syncwarp();
@@ -510,8 +580,6 @@ bool expert_map(CUtensorMap *m, int elem, const void *p, const GroupedArgs &g, l
 
 }  // namespace
 
-int grouped_tc_tile_rows() { return kTileTokens; }
-
 cudaError_t launch_grouped_tc(const GroupedArgs &g, int dir, cudaStream_t s) {
   TcMaps m;
   const long tokens = (g.rows + kTileTokens - 1L) / kTileTokens + (g.E < g.rows ? g.E : g.rows);
@@ -537,6 +605,12 @@ cudaError_t launch_grouped_tc(const GroupedArgs &g, int dir, cudaStream_t s) {
     return launch_tc<GROUPED_WGRAD>(m, g, static_cast<long>(g.E) * ((g.N + 255) / 256) * ((g.K + 255) / 256), s);
   }
   if (g.rows <= 0) return cudaSuccess;
+  if (g.E > kTableExperts) {
+    const bool fwd = dir == GROUPED_FWD;
+    const cudaError_t e = launch_grouped_plan(g, kTileTokens, fwd ? g.y : g.dx, fwd ? g.out_dtype : g.dtype,
+                                              fwd ? g.N : g.K, fwd ? g.ld_y : g.ld_x, s);
+    if (e != cudaSuccess) return e;
+  }
   if (dir == GROUPED_FWD) {
     if (!row_maps(m.b, g.dtype, g.x, g.rows, g.K, g.ld_x) || !expert_map(&m.a, g.dtype, g.w, g, g.ld_w, g.ld_e, 64, 128))
       return cudaErrorInvalidValue;

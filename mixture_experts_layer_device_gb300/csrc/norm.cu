@@ -15,6 +15,7 @@
 // (dz, dh, z, f in; dx, df out).
 #include "block.h"
 #include "elem.cuh"
+#include "gemm_common.cuh"
 #include "kernels.h"
 
 namespace moe {
@@ -101,30 +102,46 @@ MOE_DEV float row_gate_of(const NormArgs &a, long row) {
 }
 
 // ---------------------------------------------------------------- forward
+// Chunks of one row of a tensor (NULL: zeros).
+template <typename T, int VEC, int NCH>
+MOE_DEV void load_row(Chunk<T, VEC> *q, const void *base, long row, long ld, int d, int tid, int tpr) {
+  const T *p = static_cast<const T *>(base) + row * ld;
+#pragma unroll
+  for (int i = 0; i < NCH; ++i) {
+    const int c = (tid + i * tpr) * VEC;
+    if (base && c < d) q[i].load(p + c);
+    else q[i].clear();
+  }
+}
+
 // A row stays in the registers of its threads (NCH chunks of VEC columns each)
-// from the loads to the stores; the rows of the grid's blocks follow each other.
-template <typename T, int VEC, int NCH, bool WARP, int THREADS>
-__global__ void __launch_bounds__(THREADS) norm_fwd_kernel(const NormArgs a) {
+// from the loads to the stores.  The blocks are persistent, and the next row's
+// loads are issued before this row's sums: the reductions' waits would
+// otherwise leave the memory idle.
+template <typename T, int VEC, int NCH, bool WARP, int THREADS, int MINB>
+__global__ void __launch_bounds__(THREADS, MINB) norm_fwd_kernel(const NormArgs a) {
   __shared__ float red[2][1][kMaxWarps];
   const int tpr = WARP ? 32 : blockDim.x;
   const int tid = WARP ? (threadIdx.x & 31) : threadIdx.x;
   const int rpb = WARP ? (blockDim.x >> 5) : 1;
   const float inv_d = 1.f / static_cast<float>(a.d);
+  const long step = static_cast<long>(gridDim.x) * rpb;
   int turn = 0;
-  for (long row = static_cast<long>(blockIdx.x) * rpb + (WARP ? (threadIdx.x >> 5) : 0); row < a.rows;
-       row += static_cast<long>(gridDim.x) * rpb) {
+  long row = static_cast<long>(blockIdx.x) * rpb + (WARP ? (threadIdx.x >> 5) : 0);
+  if (row >= a.rows) return;
+  Chunk<T, VEC> xn[NCH], fn[NCH];
+  load_row<T, VEC, NCH>(xn, a.x, row, a.ld_x, a.d, tid, tpr);
+  load_row<T, VEC, NCH>(fn, a.f, row, a.ld_f, a.d, tid, tpr);
+  for (; row < a.rows; row += step) {
     Chunk<T, VEC> xq[NCH], fq[NCH];
-    const T *xr = static_cast<const T *>(a.x) + row * a.ld_x;
-    const T *fr = static_cast<const T *>(a.f) + row * a.ld_f;
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const int c = (tid + i * tpr) * VEC;
-      xq[i].clear();
-      fq[i].clear();
-      if (c < a.d) {
-        xq[i].load(xr + c);
-        if (a.f) fq[i].load(fr + c);
-      }
+      xq[i] = xn[i];
+      fq[i] = fn[i];
+    }
+    if (row + step < a.rows) {
+      load_row<T, VEC, NCH>(xn, a.x, row + step, a.ld_x, a.d, tid, tpr);
+      load_row<T, VEC, NCH>(fn, a.f, row + step, a.ld_f, a.d, tid, tpr);
     }
     float r = 1.f;
     if (a.flags & MOE_NORM_POST) {
@@ -269,37 +286,39 @@ MOE_DEV RowTerms row_terms(const NormArgs &a, long row, const float *s, float in
 
 // Column sums: [0] dh z r_pre (dw_pre), [1] t f r_post with the gates that are
 // not per channel (dw_post; dgate per channel).
-template <typename T, int VEC, int NCH, bool WARP, int THREADS>
-__global__ void __launch_bounds__(THREADS) norm_bwd_kernel(const NormArgs a) {
+template <typename T, int VEC, int NCH, bool WARP, int THREADS, int MINB>
+__global__ void __launch_bounds__(THREADS, MINB) norm_bwd_kernel(const NormArgs a) {
   __shared__ float red[2][4][kMaxWarps];
   const int tpr = WARP ? 32 : blockDim.x;
   const int tid = WARP ? (threadIdx.x & 31) : threadIdx.x;
   const int rpb = WARP ? (blockDim.x >> 5) : 1;
   const int slot = WARP ? blockIdx.x * rpb + (threadIdx.x >> 5) : blockIdx.x;
   const float inv_d = 1.f / static_cast<float>(a.d);
-  const bool pre = (a.flags & MOE_NORM_PRE) != 0;
+  const long step = static_cast<long>(gridDim.x) * rpb;
   float acc0[NCH][VEC], acc1[NCH][VEC];
 #pragma unroll
   for (int i = 0; i < NCH; ++i)
 #pragma unroll
     for (int k = 0; k < VEC; ++k) acc0[i][k] = acc1[i][k] = 0.f;
   int turn = 0;
-  for (long row = slot; row < a.rows; row += static_cast<long>(gridDim.x) * rpb) {
+  Chunk<T, VEC> next[4][NCH];
+  auto fetch = [&](long row) {
+    load_row<T, VEC, NCH>(next[0], a.dz, row, a.ld_z, a.d, tid, tpr);
+    load_row<T, VEC, NCH>(next[1], a.dh, row, a.ld_h, a.d, tid, tpr);
+    load_row<T, VEC, NCH>(next[2], a.zin, row, a.ld_z, a.d, tid, tpr);
+    load_row<T, VEC, NCH>(next[3], a.f, row, a.ld_f, a.d, tid, tpr);
+  };
+  if (slot < a.rows) fetch(slot);
+  for (long row = slot; row < a.rows; row += step) {
     Chunk<T, VEC> dzq[NCH], dhq[NCH], zq[NCH], fq[NCH];
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
-      const int c = (tid + i * tpr) * VEC;
-      dzq[i].clear();
-      dhq[i].clear();
-      zq[i].clear();
-      fq[i].clear();
-      if (c < a.d) {
-        if (a.dz) dzq[i].load(static_cast<const T *>(a.dz) + row * a.ld_z + c);
-        if (pre) dhq[i].load(static_cast<const T *>(a.dh) + row * a.ld_h + c);
-        if (pre) zq[i].load(static_cast<const T *>(a.zin) + row * a.ld_z + c);
-        if (a.f) fq[i].load(static_cast<const T *>(a.f) + row * a.ld_f + c);
-      }
+      dzq[i] = next[0][i];
+      dhq[i] = next[1][i];
+      zq[i] = next[2][i];
+      fq[i] = next[3][i];
     }
+    if (row + step < a.rows) fetch(row + step);
     float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
@@ -455,57 +474,85 @@ bool all_vec(const NormArgs &a) {
            (a.gate == MOE_GATE_CHANNEL || vec16(a.dg, a.ld_g, e))));
 }
 
-template <typename T, int VEC, int NCH, bool WARP, int THREADS>
+// Blocks of `threads` of a kernel that fit an SM, asked once per device and size.
+template <typename K>
+int resident(K kernel, int threads, int (&memo)[33][64]) {
+  return per_device_memo(memo[threads >> 5], [&]() {
+    int n = 0;
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) == cudaSuccess && n > 0 ? n : 1;
+  });
+}
+
+template <typename T, int VEC, int NCH, bool WARP, int THREADS, int MINB>
 cudaError_t fwd_one(const NormArgs &a, int threads, int num_sms, cudaStream_t s) {
+  static int memo[33][64] = {};
+  const auto kernel = norm_fwd_kernel<T, VEC, NCH, WARP, THREADS, MINB>;
   const int rpb = WARP ? threads / 32 : 1;
-  const long blocks = (a.rows + rpb - 1) / rpb;
-  const int per_sm = threads >= 1024 ? 2 : 2048 / threads;
-  const int grid = static_cast<int>(blocks < static_cast<long>(num_sms) * per_sm ? blocks : num_sms * per_sm);
-  norm_fwd_kernel<T, VEC, NCH, WARP, THREADS><<<grid, threads, 0, s>>>(a);
+  const long blocks = (a.rows + rpb - 1) / rpb, most = static_cast<long>(num_sms) * resident(kernel, threads, memo);
+  kernel<<<static_cast<int>(blocks < most ? blocks : most), threads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
-// Elements per thread: 16, in a warp up to 512 columns, else a block of up to
-// 1024 threads (16384 columns).
+// Columns per thread: 16 of a 16-byte chunked row, 8 of one that is not (each
+// takes a register of its own).  Up to 512 columns a warp holds a row, beyond
+// a block.
 template <typename T, int VEC>
 cudaError_t fwd_vec(const NormArgs &a, int num_sms, cudaStream_t s) {
-  constexpr int NCH = 16 / VEC;
-  if (a.d <= 512) return fwd_one<T, VEC, NCH, true, 256>(a, 256, num_sms, s);
-  const int threads = round32((a.d + 15) / 16);
-  if (threads <= 512) return fwd_one<T, VEC, NCH, false, 512>(a, threads, num_sms, s);
-  return fwd_one<T, VEC, NCH, false, 1024>(a, threads, num_sms, s);
+  constexpr int EPT = VEC > 1 ? 16 : 8, NCH = EPT / VEC;
+  if (a.d <= 32 * EPT) return fwd_one<T, VEC, NCH, true, 256, 2>(a, 256, num_sms, s);
+  const int threads = round32((a.d + EPT - 1) / EPT);
+  if (threads <= 256) return fwd_one<T, VEC, NCH, false, 256, 3>(a, threads, num_sms, s);
+  if (threads <= 512) return fwd_one<T, VEC, NCH, false, 512, 2>(a, threads, num_sms, s);
+  return fwd_one<T, VEC, NCH, false, 1024, 1>(a, threads, num_sms, s);
 }
 
 template <typename T>
 cudaError_t fwd_type(const NormArgs &a, int num_sms, cudaStream_t s) {
-  if (a.d > 16384) {
+  const bool vec = all_vec<T>(a);
+  if (a.d > (vec ? 16384 : 8192)) {
     const int grid = a.rows < 2 * num_sms ? a.rows : 2 * num_sms;
     norm_fwd_long_kernel<T><<<grid, 1024, 0, s>>>(a);
     return cudaGetLastError();
   }
-  return all_vec<T>(a) ? fwd_vec<T, Elem<T>::VEC>(a, num_sms, s) : fwd_vec<T, 1>(a, num_sms, s);
+  return vec ? fwd_vec<T, Elem<T>::VEC>(a, num_sms, s) : fwd_vec<T, 1>(a, num_sms, s);
 }
 
-template <typename T, int VEC, int NCH, bool WARP, int THREADS>
-cudaError_t bwd_one(const NormArgs &a, int threads, int per_sm, int num_sms, int *slots, cudaStream_t s) {
+template <typename T, int VEC, int NCH, bool WARP, int THREADS, int MINB>
+cudaError_t bwd_one(const NormArgs &a, int threads, int num_sms, int *slots, cudaStream_t s) {
+  static int memo[33][64] = {};
+  const auto kernel = norm_bwd_kernel<T, VEC, NCH, WARP, THREADS, MINB>;
   const int rpb = WARP ? threads / 32 : 1;
   const long blocks = (a.rows + rpb - 1) / rpb;
-  long grid = static_cast<long>(num_sms) * per_sm;
+  long grid = static_cast<long>(num_sms) * resident(kernel, threads, memo);
   if (grid * rpb > kNormMaxBlocks) grid = kNormMaxBlocks / rpb;
   if (blocks < grid) grid = blocks;
   *slots = static_cast<int>(grid) * rpb;
-  norm_bwd_kernel<T, VEC, NCH, WARP, THREADS><<<static_cast<int>(grid), threads, 0, s>>>(a);
+  kernel<<<static_cast<int>(grid), threads, 0, s>>>(a);
   return cudaGetLastError();
 }
 
 template <typename T, int VEC>
 cudaError_t bwd_vec(const NormArgs &a, int num_sms, int *slots, cudaStream_t s) {
-  constexpr int NCH = 8 / VEC;
-  if (a.d <= 256) return bwd_one<T, VEC, NCH, true, 256>(a, 128, 1, num_sms, slots, s);
-  const int threads = round32((a.d + 7) / 8);
-  if (threads <= 256) return bwd_one<T, VEC, NCH, false, 256>(a, threads, 4, num_sms, slots, s);
-  if (threads <= 512) return bwd_one<T, VEC, NCH, false, 512>(a, threads, 2, num_sms, slots, s);
-  return bwd_one<T, VEC, NCH, false, 1024>(a, threads, 1, num_sms, slots, s);
+  if constexpr (VEC > 1) {
+    constexpr int NCH = 16 / VEC;
+    if (a.d <= 512) return bwd_one<T, VEC, NCH, true, 128, 1>(a, 128, num_sms, slots, s);
+    if (sizeof(T) == 4 && a.d <= 4096) {  // fp32 rows take twice the registers
+      const int threads = round32((a.d + 7) / 8);
+      if (threads <= 256) return bwd_one<T, VEC, NCH / 2, false, 256, 2>(a, threads, num_sms, slots, s);
+      return bwd_one<T, VEC, NCH / 2, false, 512, 1>(a, threads, num_sms, slots, s);
+    }
+    const int threads = round32((a.d + 15) / 16);
+    if (threads <= 192) return bwd_one<T, VEC, NCH, false, 192, 2>(a, threads, num_sms, slots, s);
+    if (threads <= 384) return bwd_one<T, VEC, NCH, false, 384, 1>(a, threads, num_sms, slots, s);
+    return bwd_one<T, VEC, NCH, false, 512, 1>(a, threads, num_sms, slots, s);
+  } else {
+    if (a.d <= 128) return bwd_one<T, 1, 4, true, 128, 4>(a, 128, num_sms, slots, s);
+    const int threads = round32((a.d + 3) / 4);
+    if (threads <= 256) return bwd_one<T, 1, 4, false, 256, 4>(a, threads, num_sms, slots, s);
+    if (threads <= 512) return bwd_one<T, 1, 4, false, 512, 2>(a, threads, num_sms, slots, s);
+    if (threads <= 1024) return bwd_one<T, 1, 4, false, 1024, 1>(a, threads, num_sms, slots, s);
+    return bwd_one<T, 1, 8, false, 1024, 1>(a, round32((a.d + 7) / 8), num_sms, slots, s);
+  }
 }
 
 template <typename T>
