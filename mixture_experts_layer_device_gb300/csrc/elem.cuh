@@ -10,8 +10,50 @@
 
 namespace moe {
 
+// Two fp32 values in one 64-bit register pair: one instruction works on both
+// (fma / mul / add.rn.f32x2), each half rounded as its scalar form.
+typedef unsigned long long f32x2;
+MOE_DEV f32x2 f2_of(float lo, float hi) {
+  f32x2 v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+MOE_DEV f32x2 f2_both(float x) { return f2_of(x, x); }
+MOE_DEV void f2_split(f32x2 v, float &lo, float &hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+MOE_DEV float f2_sum(f32x2 v) {
+  float lo, hi;
+  f2_split(v, lo, hi);
+  return lo + hi;
+}
+MOE_DEV f32x2 f2_fma(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+MOE_DEV f32x2 f2_mul(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 template <typename T>
 struct Elem;
+
+// 16 bytes as fp32 pairs (VEC / 2 of them) and back.
+template <typename T>
+MOE_DEV void unpack_pairs(const uint4 &q, f32x2 *p) {
+  float v[Elem<T>::VEC];
+  Elem<T>::unpack(q, v);
+#pragma unroll
+  for (int k = 0; k < Elem<T>::VEC / 2; ++k) p[k] = f2_of(v[2 * k], v[2 * k + 1]);
+}
+template <typename T>
+MOE_DEV uint4 pack_pairs(const f32x2 *p) {
+  float v[Elem<T>::VEC];
+#pragma unroll
+  for (int k = 0; k < Elem<T>::VEC / 2; ++k) f2_split(p[k], v[2 * k], v[2 * k + 1]);
+  return Elem<T>::pack(v);
+}
 
 template <>
 struct Elem<__nv_bfloat16> {

@@ -13,93 +13,13 @@
 //
 // HBM bound: forward 4 elements moved per column (f, x in; z, h out), backward 6
 // (dz, dh, z, f in; dx, df out).
-#include "block.h"
-#include "elem.cuh"
 #include "gemm_common.cuh"
 #include "kernels.h"
+#include "norm.cuh"
 
 namespace moe {
 
 namespace {
-
-constexpr int kMaxWarps = 32;
-
-// Sum over the threads that share a row: a warp (WARP), or the block through
-// red[2][N][32] (two buffers in turn: one barrier per sum).  Fixed order.
-template <bool WARP, int N>
-MOE_DEV void row_sum(float *v, float (*red)[N][kMaxWarps], int &turn) {
-#pragma unroll
-  for (int k = 0; k < N; ++k)
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  if constexpr (!WARP) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
-    if (lane == 0)
-#pragma unroll
-      for (int k = 0; k < N; ++k) red[turn][k][warp] = v[k];
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      float t = lane < nw ? red[turn][k][lane] : 0.f;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-      v[k] = t;
-    }
-    turn ^= 1;
-  }
-}
-
-// VEC elements of a row at p (16 bytes at once when VEC > 1).
-template <typename T, int VEC>
-struct Chunk {
-  uint4 q;
-  MOE_DEV void load(const T *p) { q = ld_stream(p); }
-  MOE_DEV void load_cached(const T *p) { q = __ldg(reinterpret_cast<const uint4 *>(p)); }
-  MOE_DEV void clear() { q = make_uint4(0, 0, 0, 0); }
-  MOE_DEV void get(float *v) const { Elem<T>::unpack(q, v); }
-  MOE_DEV static void store(T *p, const float *v) { st_stream(p, Elem<T>::pack(v)); }
-};
-template <typename T>
-struct Chunk<T, 1> {
-  T q;
-  MOE_DEV void load(const T *p) { q = *p; }
-  MOE_DEV void load_cached(const T *p) { q = *p; }
-  MOE_DEV void clear() { q = Elem<T>::from(0.f); }
-  MOE_DEV void get(float *v) const { v[0] = Elem<T>::to(q); }
-  MOE_DEV static void store(T *p, const float *v) { *p = Elem<T>::from(v[0]); }
-};
-
-template <typename T, int VEC>
-MOE_DEV void weight_chunk(const void *w, long at, float *v) {
-  if (w) {
-    Chunk<T, VEC> q;
-    q.load_cached(static_cast<const T *>(w) + at);
-    q.get(v);
-  } else {
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) v[k] = 1.f;
-  }
-}
-
-// The gate of VEC columns of a row (ROW's value comes in as `row_gate`).
-template <typename T, int VEC>
-MOE_DEV void gate_chunk(const NormArgs &a, long row, int c, float row_gate, float *v) {
-  if (a.gate == MOE_GATE_CHANNEL) {
-    weight_chunk<T, VEC>(a.g, c, v);
-  } else if (a.gate == MOE_GATE_FULL) {
-    Chunk<T, VEC> q;
-    q.load(static_cast<const T *>(a.g) + row * a.ld_g + c);
-    q.get(v);
-  } else {
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) v[k] = row_gate;
-  }
-}
-
-template <typename T>
-MOE_DEV float row_gate_of(const NormArgs &a, long row) {
-  return a.gate == MOE_GATE_ROW ? Elem<T>::to(static_cast<const T *>(a.g)[row]) : 1.f;
-}
 
 // ---------------------------------------------------------------- forward
 // Chunks of one row of a tensor (NULL: zeros).
@@ -255,37 +175,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(const NormArgs a) {
 }
 
 // ---------------------------------------------------------------- backward
-// What one row's columns need after its sums are known.
-struct RowTerms {
-  float rp, rq, rg;  // r_pre, r_post, row gate
-  float c1;          // rp^3 <w_pre dh, z> / d
-  float c2;          // rq^3 <w_post dn, f> / d
-};
-
-// Row sums: [0] <w_pre dh, z>, [1] <dz, q>, [2] <w_pre dh, q>, [3] <z, q> with
-// q = w_post g f, g without a row gate.
-MOE_DEV void add_sums(float dz, float dhw, float z, float q, float *s) {
-  s[0] = fmaf(dhw, z, s[0]);
-  s[1] = fmaf(dz, q, s[1]);
-  s[2] = fmaf(dhw, q, s[2]);
-  s[3] = fmaf(z, q, s[3]);
-}
-
-template <typename T>
-MOE_DEV RowTerms row_terms(const NormArgs &a, long row, const float *s, float inv_d, bool first) {
-  RowTerms t;
-  t.rp = (a.flags & MOE_NORM_PRE) ? a.r_pre_in[row] : 0.f;
-  t.rq = (a.flags & MOE_NORM_POST) ? a.r_post_in[row] : 1.f;
-  t.rg = row_gate_of<T>(a, row);
-  t.c1 = t.rp * t.rp * t.rp * s[0] * inv_d;
-  const float tq = s[1] + t.rp * s[2] - t.c1 * s[3];  // <t, q>
-  t.c2 = (a.flags & MOE_NORM_POST) ? t.rq * t.rq * t.rq * t.rg * tq * inv_d : 0.f;
-  if (a.gate == MOE_GATE_ROW && a.dg && first) static_cast<T *>(a.dg)[row] = Elem<T>::from(tq * t.rq);  // <t, n>
-  return t;
-}
-
-// Column sums: [0] dh z r_pre (dw_pre), [1] t f r_post with the gates that are
-// not per channel (dw_post; dgate per channel).
+// Rows in registers, the next row's loads in flight (as the forward).
 template <typename T, int VEC, int NCH, bool WARP, int THREADS, int MINB>
 __global__ void __launch_bounds__(THREADS, MINB) norm_bwd_kernel(const NormArgs a) {
   __shared__ float red[2][4][kMaxWarps];
@@ -295,85 +185,109 @@ __global__ void __launch_bounds__(THREADS, MINB) norm_bwd_kernel(const NormArgs 
   const int slot = WARP ? blockIdx.x * rpb + (threadIdx.x >> 5) : blockIdx.x;
   const float inv_d = 1.f / static_cast<float>(a.d);
   const long step = static_cast<long>(gridDim.x) * rpb;
+  const bool full = a.gate == MOE_GATE_FULL;
   float acc0[NCH][VEC], acc1[NCH][VEC];
 #pragma unroll
   for (int i = 0; i < NCH; ++i)
 #pragma unroll
     for (int k = 0; k < VEC; ++k) acc0[i][k] = acc1[i][k] = 0.f;
   int turn = 0;
-  Chunk<T, VEC> next[4][NCH];
+  Chunk<T, VEC> next[5][NCH];
+  RowIn next_in = {};
   auto fetch = [&](long row) {
     load_row<T, VEC, NCH>(next[0], a.dz, row, a.ld_z, a.d, tid, tpr);
     load_row<T, VEC, NCH>(next[1], a.dh, row, a.ld_h, a.d, tid, tpr);
     load_row<T, VEC, NCH>(next[2], a.zin, row, a.ld_z, a.d, tid, tpr);
     load_row<T, VEC, NCH>(next[3], a.f, row, a.ld_f, a.d, tid, tpr);
+    if (full) load_row<T, VEC, NCH>(next[4], a.g, row, a.ld_g, a.d, tid, tpr);
+    next_in = row_in<T>(a, row);
   };
   if (slot < a.rows) fetch(slot);
   for (long row = slot; row < a.rows; row += step) {
-    Chunk<T, VEC> dzq[NCH], dhq[NCH], zq[NCH], fq[NCH];
+    Chunk<T, VEC> q[5][NCH];
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) {
-      dzq[i] = next[0][i];
-      dhq[i] = next[1][i];
-      zq[i] = next[2][i];
-      fq[i] = next[3][i];
-    }
+    for (int k = 0; k < 5; ++k)
+#pragma unroll
+      for (int i = 0; i < NCH; ++i) q[k][i] = next[k][i];
+    const RowIn in = next_in;
     if (row + step < a.rows) fetch(row + step);
     float s[4] = {0.f, 0.f, 0.f, 0.f};
+    // w_post times a channel gate, and a full gate's values
+    auto gates = [&](int i, int c, float *w, float *g) {
+      weight_chunk<T, VEC>(a.w_post, c, w);
+      weight_chunk<T, VEC>(a.gate == MOE_GATE_CHANNEL ? a.g : nullptr, c, g);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        w[k] *= g[k];
+        g[k] = 1.f;
+      }
+      if (full) q[4][i].get(g);
+    };
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
       const int c = (tid + i * tpr) * VEC;
       if (c < a.d) {
-        float dz[VEC], dh[VEC], z[VEC], f[VEC], wq[VEC], wp[VEC], g[VEC];
-        dzq[i].get(dz);
-        dhq[i].get(dh);
-        zq[i].get(z);
-        fq[i].get(f);
+        float dz[VEC], dh[VEC], z[VEC], f[VEC], w[VEC], wp[VEC], g[VEC];
+        q[0][i].get(dz);
+        q[1][i].get(dh);
+        q[2][i].get(z);
+        q[3][i].get(f);
         weight_chunk<T, VEC>(a.w_pre, c, wp);
-        weight_chunk<T, VEC>(a.w_post, c, wq);
-        gate_chunk<T, VEC>(a, row, c, 1.f, g);
+        gates(i, c, w, g);
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) add_sums(dz[k], dh[k] * wp[k], z[k], wq[k] * g[k] * f[k], s);
+        for (int k = 0; k < VEC; ++k) add_sums(dz[k], dh[k] * wp[k], z[k], w[k] * g[k] * f[k], s);
       }
     }
     row_sum<WARP, 4>(s, red, turn);
-    const RowTerms t = row_terms<T>(a, row, s, inv_d, tid == 0);
+    const RowTerms t = row_terms<T>(a, row, in, s, inv_d, tid == 0);
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
       const int c = (tid + i * tpr) * VEC;
       if (c < a.d) {
-        float dz[VEC], dh[VEC], z[VEC], f[VEC], wq[VEC], wp[VEC], g[VEC], o[VEC];
-        dzq[i].get(dz);
-        dhq[i].get(dh);
-        zq[i].get(z);
-        fq[i].get(f);
+        float dz[VEC], dh[VEC], z[VEC], f[VEC], w[VEC], wp[VEC], g[VEC];
+        q[0][i].get(dz);
+        q[1][i].get(dh);
+        q[2][i].get(z);
+        q[3][i].get(f);
         weight_chunk<T, VEC>(a.w_pre, c, wp);
+        gates(i, c, w, g);
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
-          acc0[i][k] = fmaf(dh[k] * t.rp, z[k], acc0[i][k]);
-          dz[k] = fmaf(t.rp * wp[k], dh[k], fmaf(-t.c1, z[k], dz[k]));  // t
-          o[k] = a.alpha * dz[k];
+          const ElemOut o =
+              elem_out(t, a.alpha, dz[k], dh[k], z[k], f[k], wp[k], w[k], g[k], acc0[i][k], acc1[i][k]);
+          dz[k] = o.dx;
+          dh[k] = o.df;
+          z[k] = o.dg;
         }
-        if (a.dx) Chunk<T, VEC>::store(static_cast<T *>(a.dx) + row * a.ld_x + c, o);
-        weight_chunk<T, VEC>(a.w_post, c, wq);
-        gate_chunk<T, VEC>(a, row, c, t.rg, g);
-        if (a.gate == MOE_GATE_FULL && a.dg) {
-#pragma unroll
-          for (int k = 0; k < VEC; ++k) o[k] = dz[k] * (wq[k] * f[k] * t.rq);
-          Chunk<T, VEC>::store(static_cast<T *>(a.dg) + row * a.ld_g + c, o);
-        }
-        const bool chan = a.gate == MOE_GATE_CHANNEL;
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-          acc1[i][k] = fmaf(dz[k] * (chan ? 1.f : g[k]), f[k] * t.rq, acc1[i][k]);
-          o[k] = fmaf(t.rq * wq[k] * g[k], dz[k], -t.c2 * f[k]);
-        }
-        if (a.df) Chunk<T, VEC>::store(static_cast<T *>(a.df) + row * a.ld_f + c, o);
+        if (a.dx) Chunk<T, VEC>::store(static_cast<T *>(a.dx) + row * a.ld_x + c, dz);
+        if (a.df) Chunk<T, VEC>::store(static_cast<T *>(a.df) + row * a.ld_f + c, dh);
+        if (full && a.dg) Chunk<T, VEC>::store(static_cast<T *>(a.dg) + row * a.ld_g + c, z);
       }
     }
   }
-  if (a.part) {
-    float *p = a.part + static_cast<long>(slot) * 2 * a.d;
+  if (!a.part) return;
+  float *p = a.part + static_cast<long>(blockIdx.x) * 2 * a.d;
+  if constexpr (WARP) {
+    // the block's warps join their column sums in order
+    __shared__ float join[2][32 * VEC * NCH];
+    for (int turn_of = 0; turn_of < rpb; ++turn_of) {
+      if (turn_of == static_cast<int>(threadIdx.x >> 5)) {
+#pragma unroll
+        for (int i = 0; i < NCH; ++i)
+#pragma unroll
+          for (int k = 0; k < VEC; ++k) {
+            const int c = (tid + i * tpr) * VEC + k;
+            join[0][c] = turn_of ? join[0][c] + acc0[i][k] : acc0[i][k];
+            join[1][c] = turn_of ? join[1][c] + acc1[i][k] : acc1[i][k];
+          }
+      }
+      __syncthreads();
+    }
+    for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
+      p[c] = join[0][c];
+      p[a.d + c] = join[1][c];
+    }
+  } else {
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
       const int c = (tid + i * tpr) * VEC;
@@ -410,41 +324,43 @@ __global__ void __launch_bounds__(1024) norm_bwd_long_kernel(const NormArgs a) {
                wq * g * at(a.f, a.ld_f, c), s);
     }
     row_sum<false, 4>(s, red, turn);
-    const RowTerms t = row_terms<T>(a, row, s, inv_d, threadIdx.x == 0);
+    const RowTerms t = row_terms<T>(a, row, row_in<T>(a, row), s, inv_d, threadIdx.x == 0);
     for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
-      float wp, wq, g;
+      float wp, w, g, acc0 = 0.f, acc1 = 0.f;
       weight_chunk<T, 1>(a.w_pre, c, &wp);
-      weight_chunk<T, 1>(a.w_post, c, &wq);
-      gate_chunk<T, 1>(a, row, c, t.rg, &g);
-      const float dh = pre ? at(a.dh, a.ld_h, c) : 0.f, z = pre ? at(a.zin, a.ld_z, c) : 0.f;
-      const float f = at(a.f, a.ld_f, c);
-      const float tt = fmaf(t.rp * wp, dh, fmaf(-t.c1, z, at(a.dz, a.ld_z, c)));
-      if (a.dx) static_cast<T *>(a.dx)[row * a.ld_x + c] = Elem<T>::from(a.alpha * tt);
-      if (a.gate == MOE_GATE_FULL && a.dg)
-        static_cast<T *>(a.dg)[row * a.ld_g + c] = Elem<T>::from(tt * (wq * f * t.rq));
-      if (a.df) static_cast<T *>(a.df)[row * a.ld_f + c] = Elem<T>::from(fmaf(t.rq * wq * g, tt, -t.c2 * f));
+      weight_chunk<T, 1>(a.w_post, c, &w);
+      gate_chunk<T, 1>(a, row, c, 1.f, &g);
+      if (a.gate == MOE_GATE_CHANNEL) {
+        w *= g;
+        g = 1.f;
+      }
+      const ElemOut o = elem_out(t, a.alpha, at(a.dz, a.ld_z, c), pre ? at(a.dh, a.ld_h, c) : 0.f,
+                                 pre ? at(a.zin, a.ld_z, c) : 0.f, at(a.f, a.ld_f, c), wp, w, g, acc0, acc1);
+      if (a.dx) static_cast<T *>(a.dx)[row * a.ld_x + c] = Elem<T>::from(o.dx);
+      if (a.gate == MOE_GATE_FULL && a.dg) static_cast<T *>(a.dg)[row * a.ld_g + c] = Elem<T>::from(o.dg);
+      if (a.df) static_cast<T *>(a.df)[row * a.ld_f + c] = Elem<T>::from(o.df);
       if (part) {
-        part[c] = fmaf(dh * t.rp, z, part[c]);
-        part[a.d + c] = fmaf(tt * (a.gate == MOE_GATE_CHANNEL ? 1.f : g), f * t.rq, part[a.d + c]);
+        part[c] += acc0;
+        part[a.d + c] += acc1;
       }
     }
   }
 }
 
 // dw_pre, dw_post and a channel gate's gradient from the blocks' column sums:
-// 32 columns per block, the partial rows in 8 interleaved runs joined in order.
+// 32 columns per block, the partial rows in 32 interleaved runs joined in order.
 template <typename T>
-__global__ void __launch_bounds__(256) norm_columns_kernel(const NormArgs a, int slots) {
-  __shared__ float sh[8][32];
+__global__ void __launch_bounds__(1024) norm_columns_kernel(const NormArgs a, int slots) {
+  __shared__ float sh[32][32];
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), run = threadIdx.x >> 5, k = blockIdx.y;
   float v = 0.f;
   if (c < a.d)
-    for (int b = run; b < slots; b += 8) v += a.part[(static_cast<long>(b) * 2 + k) * a.d + c];
+    for (int b = run; b < slots; b += 32) v += a.part[(static_cast<long>(b) * 2 + k) * a.d + c];
   sh[run][threadIdx.x & 31] = v;
   __syncthreads();
   if (run || c >= a.d) return;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) v += sh[i][threadIdx.x];
+  for (int i = 1; i < 32; ++i) v += sh[i][threadIdx.x];
   if (k == 0) {
     if (a.dw_pre) static_cast<T *>(a.dw_pre)[c] = Elem<T>::from(v);
     return;
@@ -509,6 +425,7 @@ cudaError_t fwd_vec(const NormArgs &a, int num_sms, cudaStream_t s) {
 template <typename T>
 cudaError_t fwd_type(const NormArgs &a, int num_sms, cudaStream_t s) {
   const bool vec = all_vec<T>(a);
+  if (a.rows > num_sms && norm_ring_fits(a, false)) return launch_norm_fwd_ring(a, num_sms, s);
   if (a.d > (vec ? 16384 : 8192)) {
     const int grid = a.rows < 2 * num_sms ? a.rows : 2 * num_sms;
     norm_fwd_long_kernel<T><<<grid, 1024, 0, s>>>(a);
@@ -524,9 +441,9 @@ cudaError_t bwd_one(const NormArgs &a, int threads, int num_sms, int *slots, cud
   const int rpb = WARP ? threads / 32 : 1;
   const long blocks = (a.rows + rpb - 1) / rpb;
   long grid = static_cast<long>(num_sms) * resident(kernel, threads, memo);
-  if (grid * rpb > kNormMaxBlocks) grid = kNormMaxBlocks / rpb;
+  if (grid > kNormMaxBlocks) grid = kNormMaxBlocks;
   if (blocks < grid) grid = blocks;
-  *slots = static_cast<int>(grid) * rpb;
+  *slots = static_cast<int>(grid);
   kernel<<<static_cast<int>(grid), threads, 0, s>>>(a);
   return cudaGetLastError();
 }
@@ -535,7 +452,7 @@ template <typename T, int VEC>
 cudaError_t bwd_vec(const NormArgs &a, int num_sms, int *slots, cudaStream_t s) {
   if constexpr (VEC > 1) {
     constexpr int NCH = 16 / VEC;
-    if (a.d <= 512) return bwd_one<T, VEC, NCH, true, 128, 1>(a, 128, num_sms, slots, s);
+    if (a.d <= 512) return bwd_one<T, VEC, NCH, true, 256, 1>(a, 256, num_sms, slots, s);
     if (sizeof(T) == 4 && a.d <= 4096) {  // fp32 rows take twice the registers
       const int threads = round32((a.d + 7) / 8);
       if (threads <= 256) return bwd_one<T, VEC, NCH / 2, false, 256, 2>(a, threads, num_sms, slots, s);
@@ -546,7 +463,7 @@ cudaError_t bwd_vec(const NormArgs &a, int num_sms, int *slots, cudaStream_t s) 
     if (threads <= 384) return bwd_one<T, VEC, NCH, false, 384, 1>(a, threads, num_sms, slots, s);
     return bwd_one<T, VEC, NCH, false, 512, 1>(a, threads, num_sms, slots, s);
   } else {
-    if (a.d <= 128) return bwd_one<T, 1, 4, true, 128, 4>(a, 128, num_sms, slots, s);
+    if (a.d <= 128) return bwd_one<T, 1, 4, true, 256, 2>(a, 256, num_sms, slots, s);
     const int threads = round32((a.d + 3) / 4);
     if (threads <= 256) return bwd_one<T, 1, 4, false, 256, 4>(a, threads, num_sms, slots, s);
     if (threads <= 512) return bwd_one<T, 1, 4, false, 512, 2>(a, threads, num_sms, slots, s);
@@ -561,19 +478,22 @@ cudaError_t bwd_type(const NormArgs &a, int num_sms, cudaStream_t s) {
   if (a.rows > 0) {
     cudaError_t e;
     HostTrace t("norm_backward", s);
-    if (a.d > 8192) {
+    const bool vec = all_vec<T>(a);
+    if (a.rows > num_sms && norm_ring_fits(a, true)) {
+      e = launch_norm_bwd_ring(a, num_sms, &slots, s);
+    } else if (a.d > 8192) {
       slots = a.rows < 2 * num_sms ? a.rows : 2 * num_sms;
       if (slots > kNormMaxBlocks) slots = kNormMaxBlocks;
       norm_bwd_long_kernel<T><<<slots, 1024, 0, s>>>(a);
       e = cudaGetLastError();
     } else {
-      e = all_vec<T>(a) ? bwd_vec<T, Elem<T>::VEC>(a, num_sms, &slots, s) : bwd_vec<T, 1>(a, num_sms, &slots, s);
+      e = vec ? bwd_vec<T, Elem<T>::VEC>(a, num_sms, &slots, s) : bwd_vec<T, 1>(a, num_sms, &slots, s);
     }
     if (e != cudaSuccess) return e;
   }
   if (!a.part) return cudaSuccess;
   HostTrace t("norm_columns", s);
-  norm_columns_kernel<T><<<dim3((a.d + 31) / 32, 2), 256, 0, s>>>(a, slots);
+  norm_columns_kernel<T><<<dim3((a.d + 31) / 32, 2), 1024, 0, s>>>(a, slots);
   return cudaGetLastError();
 }
 

@@ -223,7 +223,8 @@ def test_grouped_follows_the_routers_offsets(blk):
 
 # ---------------------------------------------------------------- norms
 NORM = [(1, 1), (1, 7168), (2, 8), (5, 33), (17, 512), (9, 520), (33, 1000), (3, 2883), (40, 4096), (2, 8200), (3, 16392),
-        (700, 264)]
+        (700, 264), (400, 1024), (333, 4104), (160, 7168), (157, 8192), (170, 13000), (300, 2883), (200, 515), (161, 777),
+        (1000, 40), (5000, 256)]
 
 
 def norm_inputs(rows, d, dtype, kind, seed):
@@ -276,7 +277,7 @@ def test_norm_sizes(blk, rows, d, dtype):
 
 @pytest.mark.parametrize("kind", ["none", "channel", "row", "full"])
 @pytest.mark.parametrize("post,pre", [(True, True), (True, False), (False, True), (False, False)])
-@pytest.mark.parametrize("rows,d", [(37, 264), (37, 1027), (5, 9000)])
+@pytest.mark.parametrize("rows,d", [(37, 264), (37, 1027), (5, 9000), (333, 1032), (311, 1027)])
 def test_norm_gates_and_halves(blk, kind, post, pre, rows, d):
     check_norm(blk, rows, d, BF, kind, post, pre, 1.0, seed=7)
 
