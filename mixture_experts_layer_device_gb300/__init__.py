@@ -133,10 +133,18 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_current_stream = None
+
+
 def _stream(stream):
+    global _current_stream
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _current_stream is None:
+            import torch
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the same handle, without the Stream object
+            _current_stream = (lambda: raw(torch.cuda.current_device())) if raw else \
+                (lambda: torch.cuda.current_stream().cuda_stream)
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

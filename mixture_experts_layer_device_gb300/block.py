@@ -20,42 +20,47 @@ from . import (GATES, MOE_ELEM_BF16, MOE_ELEM_FP16, MOE_ELEM_FP32, MOE_NORM_POST
 _ELEM = {torch.bfloat16: MOE_ELEM_BF16, torch.float16: MOE_ELEM_FP16, torch.float32: MOE_ELEM_FP32}
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
+def _bad(what, *args):
+    raise ValueError(what % args if args else what)
 
 
 def _rows(t, name, cols, dtype=None, rows=None):
     """A 2-D matrix on the current GPU whose rows are contiguous; its row stride."""
-    _need(t.dim() == 2 and t.shape[1] == cols and (rows is None or t.shape[0] == rows),
-          "%s has shape %s, expected [%s, %d]" % (name, tuple(t.shape), "rows" if rows is None else rows, cols))
-    _need(dtype is None or t.dtype == dtype, "%s is %s, expected %s" % (name, t.dtype, dtype))
-    _need(t.is_cuda, "%s is not on the GPU" % name)
-    if t.stride(1) != 1 and cols > 1 or (t.shape[0] > 1 and t.stride(0) < cols):
-        t = t.contiguous()
-    return t, (t.stride(0) if t.shape[0] > 1 else cols)
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols or (rows is not None and shape[0] != rows):
+        _bad("%s has shape %s, expected [%s, %d]", name, tuple(shape), "rows" if rows is None else rows, cols)
+    if dtype is not None and t.dtype != dtype:
+        _bad("%s is %s, expected %s", name, t.dtype, dtype)
+    if not t.is_cuda:
+        _bad("%s is not on the GPU", name)
+    if t.is_contiguous():
+        return t, cols
+    if (t.stride(1) != 1 and cols > 1) or (shape[0] > 1 and t.stride(0) < cols):
+        return t.contiguous(), cols
+    return t, (t.stride(0) if shape[0] > 1 else cols)
 
 
 def _out(t, name, rows, cols, dtype, device):
     """The caller's output matrix (rows contiguous), or a new one; its row stride."""
     if t is None:
         return torch.empty((rows, cols), dtype=dtype, device=device), cols
-    _need(t.shape == (rows, cols) and t.dtype == dtype and t.is_cuda and (cols == 1 or t.stride(1) == 1) and
-          (rows <= 1 or t.stride(0) >= cols),
-          "%s must be a %s GPU matrix [%d, %d] with contiguous rows" % (name, dtype, rows, cols))
+    if not (t.shape == (rows, cols) and t.dtype == dtype and t.is_cuda and (cols == 1 or t.stride(1) == 1) and
+            (rows <= 1 or t.stride(0) >= cols)):
+        _bad("%s must be a %s GPU matrix [%d, %d] with contiguous rows", name, dtype, rows, cols)
     return t, (t.stride(0) if rows > 1 else cols)
 
 
 def _vector(t, name, n, dtype):
     if t is None:
         return None
-    _need(t.dim() == 1 and t.shape[0] == n and t.dtype == dtype and t.is_cuda,
-          "%s must be a %s GPU vector of %d" % (name, dtype, n))
+    if t.shape != (n,) or t.dtype != dtype or not t.is_cuda:
+        _bad("%s must be a %s GPU vector of %d", name, dtype, n)
     return t.contiguous()
 
 
 def _ws(nbytes, device):
-    _need(nbytes > 0, "the library does not take these sizes")
+    if nbytes <= 0:
+        _bad("the library does not take these sizes")
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
@@ -77,11 +82,13 @@ def _grouped_config(*fields):
 
 
 def _grouped(x_rows, x_dtype, w, offsets, name):
-    _need(x_dtype in (torch.bfloat16, torch.float16), "%s must be bfloat16 or float16" % name)
-    _need(w.dim() == 3 and w.dtype == x_dtype and w.is_cuda, "w must be a %s GPU tensor [E, N, K]" % x_dtype)
+    if not (x_dtype in (torch.bfloat16, torch.float16)):
+        _bad("%s must be bfloat16 or float16", name)
+    if not (w.dim() == 3 and w.dtype == x_dtype and w.is_cuda):
+        _bad("w must be a %s GPU tensor [E, N, K]", x_dtype)
     E, N, K = w.shape
-    _need(offsets.dim() == 1 and offsets.shape[0] == E + 1 and offsets.dtype == torch.int32 and offsets.is_cuda,
-          "offsets must be an int32 GPU vector of E + 1 = %d" % (E + 1))
+    if not (offsets.dim() == 1 and offsets.shape[0] == E + 1 and offsets.dtype == torch.int32 and offsets.is_cuda):
+        _bad("offsets must be an int32 GPU vector of E + 1 = %d", E + 1)
     if (K > 1 and w.stride(2) != 1) or (N > 1 and w.stride(1) < K) or \
             (E > 1 and w.stride(0) < (N - 1) * w.stride(1) + K):
         w = w.contiguous()
@@ -96,7 +103,8 @@ def grouped_forward(x, w, offsets, *, out=None, out_dtype=None, return_workspace
     w, offsets, E, N, K, ld_w = _grouped(None, x.dtype, w, offsets, "x")
     x, ld_x = _rows(x, "x", K)
     out_dtype = out_dtype or (out.dtype if out is not None else x.dtype)
-    _need(out_dtype in (x.dtype, torch.float32), "y is of x's type or float32")
+    if not (out_dtype in (x.dtype, torch.float32)):
+        _bad("y is of x's type or float32")
     y, ld_y = _out(out, "out", x.shape[0], N, out_dtype, x.device)
     ld_e = w.stride(0) if E > 1 else 0
     cfg = _grouped_config(x.shape[0], E, N, K, _ELEM[x.dtype], _ELEM[out_dtype], 0, ld_x, ld_y, ld_w, ld_e)
@@ -117,22 +125,26 @@ def grouped_backward(dy, x, w, offsets, *, dx=None, dw=None, need_dx=True, need_
     dy, ld_y = _rows(dy, "dy", N)
     x, ld_x = _rows(x, "x", K, dy.dtype, rows)
     dw_dtype = dw_dtype or (dw.dtype if dw is not None else dy.dtype)
-    _need(dw_dtype in (dy.dtype, torch.float32), "dw is of dy's type or float32")
-    _need(not accumulate or (dw is not None and dw_dtype == torch.float32), "accumulate adds to a given float32 dw")
-    _need(need_dx or need_dw, "nothing to compute")
+    if not (dw_dtype in (dy.dtype, torch.float32)):
+        _bad("dw is of dy's type or float32")
+    if not (not accumulate or (dw is not None and dw_dtype == torch.float32)):
+        _bad("accumulate adds to a given float32 dw")
+    if not (need_dx or need_dw):
+        _bad("nothing to compute")
     if need_dx:
         if dx is None:      # of x's row stride, which the library shares between the two
             dx = torch.empty((rows, ld_x), dtype=dy.dtype, device=dy.device)[:, :K]
-        _need(dx.shape == (rows, K) and dx.dtype == dy.dtype and dx.is_cuda and (K == 1 or dx.stride(1) == 1),
-              "dx must be a %s GPU matrix [%d, %d] with contiguous rows" % (dy.dtype, rows, K))
+        if not (dx.shape == (rows, K) and dx.dtype == dy.dtype and dx.is_cuda and (K == 1 or dx.stride(1) == 1)):
+            _bad("dx must be a %s GPU matrix [%d, %d] with contiguous rows", dy.dtype, rows, K)
         if rows > 1 and dx.stride(0) != ld_x:
             x, ld_x = x.contiguous(), K
-            _need(dx.stride(0) == K, "dx must have x's row stride or be contiguous")
+            if not (dx.stride(0) == K):
+                _bad("dx must have x's row stride or be contiguous")
     if need_dw:
         if dw is None:
             dw = torch.empty((E, N, K), dtype=dw_dtype, device=dy.device)
-        _need(dw.shape == (E, N, K) and dw.dtype == dw_dtype and dw.is_cuda and dw.is_contiguous(),
-              "dw must be a contiguous %s GPU tensor [%d, %d, %d]" % (dw_dtype, E, N, K))
+        if not (dw.shape == (E, N, K) and dw.dtype == dw_dtype and dw.is_cuda and dw.is_contiguous()):
+            _bad("dw must be a contiguous %s GPU tensor [%d, %d, %d]", dw_dtype, E, N, K)
     ld_e = w.stride(0) if E > 1 else 0
     cfg = _grouped_config(rows, E, N, K, _ELEM[dy.dtype], _ELEM[dw_dtype], int(accumulate), ld_x, ld_y, ld_w, ld_e)
     ws = _ws(moe_grouped_workspace_bytes(cfg), dy.device)
@@ -155,8 +167,10 @@ def _norm_config(*fields):
 
 
 def _gate(gate, kind, rows, d, dtype):
-    _need(kind in GATES, "gate_kind is one of %s" % sorted(GATES))
-    _need((gate is None) == (kind == "none"), "a gate goes with its kind (channel, row or full)")
+    if not (kind in GATES):
+        _bad("gate_kind is one of %s", sorted(GATES))
+    if not ((gate is None) == (kind == "none")):
+        _bad("a gate goes with its kind (channel, row or full)")
     if kind == "none":
         return None, d
     if kind == "full":
@@ -173,14 +187,17 @@ def norm_forward(x, f=None, gate=None, w_post=None, w_pre=None, *, gate_kind="no
     "full"; w_post and w_pre [d] or None (ones); all of one type (bf16, fp16,
     fp32).  r_post, r_pre [rows] fp32 are the reciprocal roots for the backward;
     what is not computed comes back as None."""
-    _need(x.dim() == 2 and x.dtype in _ELEM, "x must be a bf16, fp16 or fp32 matrix [rows, d]")
+    if not (x.dim() == 2 and x.dtype in _ELEM):
+        _bad("x must be a bf16, fp16 or fp32 matrix [rows, d]")
     rows, d = x.shape
     x, ld_x = _rows(x, "x", d)
     ld_f, post = d, post and f is not None
     if f is not None:
         f, ld_f = _rows(f, "f", d, x.dtype, rows)
-    _need(f is not None or gate is None, "a gate needs the block's output f")
-    _need(pre or need_z, "nothing to compute")
+    if not (f is not None or gate is None):
+        _bad("a gate needs the block's output f")
+    if not (pre or need_z):
+        _bad("nothing to compute")
     gate, ld_g = _gate(gate, gate_kind, rows, d, x.dtype)
     w_post = _vector(w_post, "w_post", d, x.dtype) if post else None
     w_pre = _vector(w_pre, "w_pre", d, x.dtype) if pre else None
@@ -207,15 +224,18 @@ def norm_backward(dz, dh, z, f=None, gate=None, w_post=None, w_pre=None, r_post=
     (None: nothing but h is used) and dh, its z, f and reciprocal roots; what
     does not exist or is not needed comes back as None."""
     like = dz if dz is not None else dh
-    _need(like is not None and like.dim() == 2 and like.dtype in _ELEM, "dz or dh must be a bf16, fp16 or fp32 matrix")
+    if not (like is not None and like.dim() == 2 and like.dtype in _ELEM):
+        _bad("dz or dh must be a bf16, fp16 or fp32 matrix")
     rows, d = like.shape
     dt, dev, post = like.dtype, like.device, post and f is not None
-    _need(pre or dz is not None, "without the pre norm the gradient arrives in dz")
+    if not (pre or dz is not None):
+        _bad("without the pre norm the gradient arrives in dz")
     ld_z, ld_h, ld_f = d, d, d
     if dz is not None:
         dz, ld_z = _rows(dz, "dz", d, dt, rows)
     if pre:
-        _need(dh is not None and z is not None and r_pre is not None, "the pre norm needs dh, z and r_pre")
+        if not (dh is not None and z is not None and r_pre is not None):
+            _bad("the pre norm needs dh, z and r_pre")
         dh, ld_h = _rows(dh, "dh", d, dt, rows)
         z, ld = _rows(z, "z", d, dt, rows)
         if dz is not None and ld != ld_z and rows > 1:      # the library has one stride for the two
@@ -225,7 +245,8 @@ def norm_backward(dz, dh, z, f=None, gate=None, w_post=None, w_pre=None, r_post=
     if f is not None:
         f, ld_f = _rows(f, "f", d, dt, rows)
     if post:
-        _need(r_post is not None, "the post norm needs r_post")
+        if not (r_post is not None):
+            _bad("the post norm needs r_post")
         r_post = _vector(r_post, "r_post", rows, torch.float32)
     gate, ld_g = _gate(gate, gate_kind, rows, d, dt)
     w_post = _vector(w_post, "w_post", d, dt) if post else None
@@ -258,7 +279,8 @@ def _embed_config(*fields):
 
 
 def _ids(ids):
-    _need(ids.dtype in (torch.int32, torch.int64) and ids.is_cuda, "ids must be int32 or int64 on the GPU")
+    if not (ids.dtype in (torch.int32, torch.int64) and ids.is_cuda):
+        _bad("ids must be int32 or int64 on the GPU")
     return ids.reshape(-1).contiguous()
 
 
@@ -266,7 +288,8 @@ def embed_forward(ids, table, *, scale=1.0, out=None, stream=None):
     """scale * table[ids] [*ids.shape, d]; an id outside [0, V) (padding) gives a
     zero row.  table [V, d] bf16, fp16 or fp32; ids int32 or int64 of any shape.
     `out` [ids.numel(), d] may be given."""
-    _need(table.dim() == 2 and table.dtype in _ELEM, "table must be a bf16, fp16 or fp32 matrix [V, d]")
+    if not (table.dim() == 2 and table.dtype in _ELEM):
+        _bad("table must be a bf16, fp16 or fp32 matrix [V, d]")
     V, d = table.shape
     table, ld_t = _rows(table, "table", d)
     flat = _ids(ids)
@@ -284,14 +307,17 @@ def embed_backward(ids, dout, V, *, scale=1.0, dtable=None, grad_dtype=None, acc
     type or fp32 (grad_dtype, or dtable's).  accumulate adds to the given
     dtable's rows that occur and leaves the others alone."""
     flat = _ids(ids)
-    _need(dout.dtype in _ELEM and dout.dim() >= 2, "dout must be bf16, fp16 or fp32 [rows, d]")
+    if not (dout.dtype in _ELEM and dout.dim() >= 2):
+        _bad("dout must be bf16, fp16 or fp32 [rows, d]")
     d = dout.shape[-1]
     if dout.dim() != 2:
         dout = dout.reshape(-1, d)
     dout, ld_o = _rows(dout, "dout", d, None, flat.shape[0])
-    _need(not accumulate or dtable is not None, "accumulate adds to a given dtable")
+    if not (not accumulate or dtable is not None):
+        _bad("accumulate adds to a given dtable")
     grad_dtype = grad_dtype or (dtable.dtype if dtable is not None else dout.dtype)
-    _need(grad_dtype in (dout.dtype, torch.float32), "dtable is of dout's type or float32")
+    if not (grad_dtype in (dout.dtype, torch.float32)):
+        _bad("dtable is of dout's type or float32")
     dtable, ld_t = _out(dtable, "dtable", V, d, grad_dtype, dout.device)
     cfg = _embed_config(flat.shape[0], V, d, _ELEM[dout.dtype], _ELEM[grad_dtype], int(flat.dtype == torch.int64),
                         int(accumulate), scale, ld_t, ld_o)

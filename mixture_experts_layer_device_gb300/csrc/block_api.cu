@@ -81,7 +81,7 @@ bool grouped_tensor(const moe::GroupedArgs &g, int dir) {
 // Few rows that mostly have an expert of their own: reading the weights bounds
 // the call and the tensor cores have nothing to reuse.
 bool grouped_few(const moe::GroupedArgs &g) {
-  return g.rows > 0 && g.rows <= 64 && g.rows <= 4L * g.E && g.K % 8 == 0 && tma_rows(g.x, g.ld_x) &&
+  return g.rows > 0 && g.rows <= 64 && g.rows <= 2L * g.E && g.K % 8 == 0 && tma_rows(g.x, g.ld_x) &&
          tma_rows(g.w, g.ld_w) && g.ld_e % 8 == 0;
 }
 

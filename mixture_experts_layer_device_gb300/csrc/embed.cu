@@ -2,7 +2,7 @@
 //   out[t] = scale table[ids[t]];   dtable[v] = scale sum over ids[t] = v of dout[t]
 // The gradient sorts the tokens by id (stable), so that the rows of one id lie
 // next to each other in ascending token order, and cuts the sorted list into
-// pieces of kPiece tokens.  A block sums a piece's runs in fp32; a run that lies
+// pieces.  A block sums a piece's runs in fp32; a run that lies
 // inside its piece is final, one that crosses into others leaves a partial row,
 // and a last pass joins the partial rows of such a run in order.  A frequent id
 // is so spread over many blocks, and every sum has one fixed order.
@@ -17,10 +17,11 @@ namespace moe {
 
 namespace {
 
-constexpr int kPiece = 32;      // sorted tokens per block of the sums
+constexpr int kMaxPiece = 64;   // sorted tokens per block of the sums: 64, or 16 of few
+__host__ __device__ inline int piece_of(long rows) { return rows > 8192 ? kMaxPiece : 16; }
 constexpr int kSmallSort = 2048;  // up to here every token counts its rank
 constexpr int kSortBlock = 256;   // threads of a radix block
-constexpr int kSortItems = 8;     // keys per thread and block
+constexpr int kSortItems = 2;     // keys per thread and block: the passes are short, so more blocks
 constexpr int kSortChunk = kSortBlock * kSortItems;
 constexpr int kMaxDigits = 1024;  // 10-bit digits at most
 
@@ -78,19 +79,49 @@ __global__ void __launch_bounds__(256) embed_fwd_kernel(const EmbedArgs a, int s
   }
 }
 
+// ---------------------------------------------------------------- fill
+// Zeros for the table rows of [from, to) that no token points to, a warp per row,
+// in the sums' launch.  (Filling slices beside the sort's launches too, which
+// leave the memory idle, measured 247 us where this is 250: not kept.)
+struct Fill {
+  const uint8_t *used;
+  uint8_t *table;
+  long row_bytes, ld_bytes;
+  int unit;  // bytes per store: 16, or an element of unaligned rows
+  int from, to;
+};
+MOE_DEV void fill_rows(const Fill &f, long block, long blocks) {
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  for (long v = f.from + block * warps + (threadIdx.x >> 5); v < f.to; v += blocks * warps) {
+    if (f.used[v]) continue;
+    uint8_t *dst = f.table + v * f.ld_bytes;
+    if (f.unit == 16) {
+      for (long b = lane * 16; b < f.row_bytes; b += 512) st_stream(dst + b, make_uint4(0, 0, 0, 0));
+    } else if (f.unit == 4) {
+      for (long b = lane * 4; b < f.row_bytes; b += 128) *reinterpret_cast<uint32_t *>(dst + b) = 0;
+    } else {
+      for (long b = lane * 2; b < f.row_bytes; b += 64) *reinterpret_cast<uint16_t *>(dst + b) = 0;
+    }
+  }
+}
+
 // ---------------------------------------------------------------- sort
 // Few tokens: a token's place is the number of tokens that come before it.
 // One launch instead of a radix pass' three per digit; 2,048 comparisons a
 // thread at most.  Also marks the table rows that occur.
-__global__ void __launch_bounds__(256) embed_rank_kernel(const EmbedArgs a, int *keys, int *pos, uint8_t *used) {
+constexpr int kRankBlock = 128;
+__global__ void __launch_bounds__(kRankBlock) embed_rank_kernel(const EmbedArgs a, int *keys, int *pos, uint8_t *used) {
   __shared__ int sk[kSmallSort];
-  for (int i = threadIdx.x; i < a.rows; i += blockDim.x) sk[i] = key_of(a, i);
+  for (int i = threadIdx.x; i < a.rows; i += kRankBlock) sk[i] = key_of(a, i);
   __syncthreads();
-  const int t = blockIdx.x * blockDim.x + threadIdx.x;
+  const int t = blockIdx.x * kRankBlock + threadIdx.x;
   if (t >= a.rows) return;
   const int key = sk[t];
   int rank = 0;
-  for (int i = 0; i < a.rows; ++i) rank += (sk[i] < key) || (sk[i] == key && i < t);
+#pragma unroll 8
+  for (int i = 0; i < t; ++i) rank += sk[i] <= key;
+#pragma unroll 8
+  for (int i = t + 1; i < a.rows; ++i) rank += sk[i] < key;
   keys[rank] = key;
   pos[rank] = t;
   if (used && key < a.V) used[key] = 1;
@@ -223,21 +254,33 @@ MOE_DEV void put_grad(const EmbedArgs &a, int key, int c, const float *acc) {
   } else if constexpr (VEC == 2 * Elem<G>::VEC) {
     st_stream(dst, Elem<G>::pack(v));
     st_stream(dst + VEC / 2, Elem<G>::pack(v + VEC / 2));
+  } else if constexpr (2 * VEC == Elem<G>::VEC) {
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(Elem<G>::pack2(v[0], v[1]), Elem<G>::pack2(v[2], v[3]));
   } else {
 #pragma unroll
     for (int k = 0; k < VEC; ++k) dst[k] = Elem<G>::from(v[k]);
   }
 }
 
-// Rows of one piece (blockIdx.y) x 128 threads' columns.  part[2 p] takes the
-// run that comes in from piece p - 1, part[2 p + 1] the one that starts here
-// and goes on in piece p + 1.
+// Blocks below pieces * slabs: the rows of one piece x 128 threads' columns.
+// part[2 p] takes the run that comes in from piece p - 1, part[2 p + 1] the one
+// that starts here and goes on in piece p + 1; such runs enter the list cross
+// (16 bytes each from the second on: first piece, last piece, table row; their
+// number in the first word; the order does not matter, each is joined by
+// itself).  The other blocks write the rows of zeros beside it.
 template <typename T, typename G, int VEC>
-__global__ void __launch_bounds__(128) embed_sum_kernel(const EmbedArgs a, const int *keys, const int *pos, float *part) {
-  __shared__ int sk[kPiece], sp[kPiece];
-  const int piece = blockIdx.x;
-  const int first = piece * kPiece;
-  const int n = a.rows - first < kPiece ? a.rows - first : kPiece;
+__global__ void __launch_bounds__(128) embed_sum_kernel(const EmbedArgs a, const int *keys, const int *pos, float *part,
+                                                        int *cross, int pieces, int slabs, const Fill fill) {
+  __shared__ int sk[kMaxPiece], sp[kMaxPiece];
+  const long work = static_cast<long>(pieces) * slabs;
+  if (blockIdx.x >= work) {
+    fill_rows(fill, blockIdx.x - work, gridDim.x - work);
+    return;
+  }
+  const int slab = blockIdx.x % slabs;
+  const int piece = blockIdx.x / slabs;
+  const int len = piece_of(a.rows), first = piece * len;
+  const int n = a.rows - first < len ? a.rows - first : len;
   if (threadIdx.x < n) {
     sk[threadIdx.x] = keys[first + threadIdx.x];
     sp[threadIdx.x] = pos[first + threadIdx.x];
@@ -245,7 +288,20 @@ __global__ void __launch_bounds__(128) embed_sum_kernel(const EmbedArgs a, const
   const int before = first > 0 ? keys[first - 1] : -1;
   const int after = first + n < a.rows ? keys[first + n] : -1;
   __syncthreads();
-  const int c = (blockIdx.y * 128 + threadIdx.x) * VEC;
+  if (slab == 0 && threadIdx.x == 0) {
+    const int last = sk[n - 1];
+    if (last < a.V && after == last && !(before == last && sk[0] == last)) {
+      // the last piece that the run reaches: the first token of a piece has its key
+      int lo = piece + 1, hi = pieces - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (keys[mid * len] == last) lo = mid;
+        else hi = mid - 1;
+      }
+      reinterpret_cast<int4 *>(cross)[1 + atomicAdd(cross, 1)] = make_int4(piece, lo, last, 0);
+    }
+  }
+  const int c = (slab * 128 + threadIdx.x) * VEC;
   if (c >= a.d) return;
   float acc[VEC];
 #pragma unroll
@@ -292,56 +348,52 @@ __global__ void __launch_bounds__(128) embed_sum_kernel(const EmbedArgs a, const
   }
 }
 
-// Joins the runs that cross pieces: the block of the piece where such a run
-// starts adds the following pieces' partial rows in order.
-template <typename G>
-__global__ void __launch_bounds__(128) embed_join_kernel(const EmbedArgs a, const int *keys, int pieces, const float *part) {
-  const int piece = blockIdx.x;
-  const int last = piece * kPiece + kPiece - 1;
-  if (last + 1 >= a.rows) return;
-  const int key = keys[last];
-  if (key >= a.V || keys[last + 1] != key) return;          // no run goes on
-  if (piece > 0 && keys[piece * kPiece] == key && keys[piece * kPiece - 1] == key) return;  // it did not start here
-  // the last piece that the run reaches: the first token of a piece has its key
-  int lo = piece + 1, hi = pieces - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (keys[mid * kPiece] == key) lo = mid;
-    else hi = mid - 1;
-  }
-  const int c = blockIdx.y * 128 + threadIdx.x;
-  if (c >= a.d) return;
-  float acc = part[(static_cast<long>(piece) * 2 + 1) * a.d + c];
-  int p = piece + 1;
-  for (; p + 7 <= lo; p += 8) {
-    float v[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = part[static_cast<long>(p + u) * 2 * a.d + c];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) acc += v[u];
-  }
-  for (; p <= lo; ++p) acc += part[static_cast<long>(p) * 2 * a.d + c];
-  put_grad<G, 1>(a, key, c, &acc);
-}
-
-// Zeros for the table rows that no token points to.
+// Joins the runs that cross pieces: 256 x VEC columns of one run per block, its
+// partial rows in order.
 template <typename G, int VEC>
-__global__ void __launch_bounds__(256) embed_zero_kernel(const EmbedArgs a, const uint8_t *used) {
-  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
-  for (long v = static_cast<long>(blockIdx.x) * warps + (threadIdx.x >> 5); v < a.V;
-       v += static_cast<long>(gridDim.x) * warps) {
-    if (used[v]) continue;
-    G *dst = static_cast<G *>(a.dtable) + v * a.ld_t;
-    if constexpr (VEC > 1) {
-      for (int c = lane * VEC; c < a.d; c += 32 * VEC) st_stream(dst + c, make_uint4(0, 0, 0, 0));
-    } else {
-      for (int c = lane; c < a.d; c += 32) dst[c] = Elem<G>::from(0.f);
+__global__ void __launch_bounds__(256) embed_join_kernel(const EmbedArgs a, const float *part, const int *cross, int slabs) {
+  const long total = static_cast<long>(cross[0]) * slabs;
+  for (long u = blockIdx.x; u < total; u += gridDim.x) {
+    const int4 run = reinterpret_cast<const int4 *>(cross)[1 + u / slabs];
+    const int c = (static_cast<int>(u % slabs) * 256 + threadIdx.x) * VEC;
+    if (c >= a.d) continue;
+    // the starting piece's second row, then the first rows of those after it
+    float acc[VEC];
+    auto load = [&](long row, float *v) {
+      const float *p = part + row * a.d + c;
+      if constexpr (VEC == 4) {
+        const float4 q = *reinterpret_cast<const float4 *>(p);
+        v[0] = q.x;
+        v[1] = q.y;
+        v[2] = q.z;
+        v[3] = q.w;
+      } else {
+        v[0] = *p;
+      }
+    };
+    load(2L * run.x + 1, acc);
+    int i = run.x + 1;
+    for (; i + 7 <= run.y; i += 8) {
+      float v[8][VEC];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) load(2L * (i + k), v[k]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) acc[j] += v[k][j];
     }
+    for (; i <= run.y; ++i) {
+      float v[VEC];
+      load(2L * i, v);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) acc[j] += v[j];
+    }
+    put_grad<G, VEC>(a, run.z, c, acc);
   }
 }
 
 struct EmbedWs {
-  size_t keys[2], pos[2], hist, total, used, part, bytes;
+  size_t keys[2], pos[2], hist, total, cross, used, part, bytes;
 };
 
 EmbedWs ws_layout(int rows, long V, int d) {
@@ -352,7 +404,7 @@ EmbedWs ws_layout(int rows, long V, int d) {
     at += (n + 255) / 256 * 256;
     return o;
   };
-  const size_t T = rows, blocks = (T + kSortChunk - 1) / kSortChunk, pieces = (T + kPiece - 1) / kPiece;
+  const size_t T = rows, blocks = (T + kSortChunk - 1) / kSortChunk, pieces = (T + piece_of(rows) - 1) / piece_of(rows);
   for (int i = 0; i < 2; ++i) {
     w.keys[i] = take(T * 4);
     w.pos[i] = take(T * 4);
@@ -360,6 +412,7 @@ EmbedWs ws_layout(int rows, long V, int d) {
   w.hist = take(blocks * kMaxDigits * 4);
   w.total = take(kMaxDigits * 4);
   w.used = take(V);
+  w.cross = take((pieces + 1) * 16);
   w.part = take(pieces * 2 * d * 4);
   w.bytes = at;
   return w;
@@ -384,33 +437,32 @@ cudaError_t fwd_type(const EmbedArgs &a, cudaStream_t s) {
 }
 
 template <typename T, typename G>
-cudaError_t sums(const EmbedArgs &a, const int *keys, const int *pos, float *part, const uint8_t *used, int num_sms,
-                 cudaStream_t s) {
-  const int pieces = (a.rows + kPiece - 1) / kPiece;
+cudaError_t sums(const EmbedArgs &a, const int *keys, const int *pos, float *part, int *cross, const Fill &fill,
+                 int num_sms, cudaStream_t s) {
+  const int pieces = (a.rows + piece_of(a.rows) - 1) / piece_of(a.rows);
   const bool vec = vec16(a.dout, a.ld_o, sizeof(T)) && vec16(a.dtable, a.ld_t, sizeof(G)) &&
                    a.d % Elem<T>::VEC == 0 && a.d % Elem<G>::VEC == 0;
-  if (pieces) {
+  const int cols = 128 * (vec ? Elem<T>::VEC : 1), slabs = (a.d + cols - 1) / cols;
+  // a fill block's four warps take a table row each, so many rows a block
+  const long rows_left = (static_cast<long>(fill.to) - fill.from + 3) / 4, most = num_sms * 32L;
+  const long grid = static_cast<long>(pieces) * slabs + (rows_left < most ? rows_left : most);
+  if (grid > 2147483647L) return cudaErrorInvalidConfiguration;
+  if (grid) {
     HostTrace t("embed_sum", s);
-    const int cols = 128 * (vec ? Elem<T>::VEC : 1);
-    const dim3 grid(pieces, (a.d + cols - 1) / cols);
-    if (vec) embed_sum_kernel<T, G, Elem<T>::VEC><<<grid, 128, 0, s>>>(a, keys, pos, part);
-    else embed_sum_kernel<T, G, 1><<<grid, 128, 0, s>>>(a, keys, pos, part);
+    if (vec)
+      embed_sum_kernel<T, G, Elem<T>::VEC><<<static_cast<unsigned>(grid), 128, 0, s>>>(a, keys, pos, part, cross, pieces, slabs, fill);
+    else
+      embed_sum_kernel<T, G, 1><<<static_cast<unsigned>(grid), 128, 0, s>>>(a, keys, pos, part, cross, pieces, slabs, fill);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   if (pieces > 1) {
     HostTrace t("embed_join", s);
-    embed_join_kernel<G><<<dim3(pieces - 1, (a.d + 127) / 128), 128, 0, s>>>(a, keys, pieces, part);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  if (!a.accumulate) {
-    HostTrace t("embed_zero", s);
-    const bool zv = vec16(a.dtable, a.ld_t, sizeof(G)) && a.d % Elem<G>::VEC == 0;
-    const long want = (static_cast<long>(a.V) + 7) / 8;
-    const int grid = static_cast<int>(want < num_sms * 16L ? want : num_sms * 16L);
-    if (zv) embed_zero_kernel<G, Elem<G>::VEC><<<grid, 256, 0, s>>>(a, used);
-    else embed_zero_kernel<G, 1><<<grid, 256, 0, s>>>(a, used);
+    const int join_cols = 256 * (vec ? 4 : 1), join_slabs = (a.d + join_cols - 1) / join_cols;
+    const long want = static_cast<long>(pieces) * join_slabs;
+    const unsigned blocks = static_cast<unsigned>(want < num_sms * 8L ? want : num_sms * 8L);
+    if (vec) embed_join_kernel<G, 4><<<blocks, 256, 0, s>>>(a, part, cross, join_slabs);
+    else embed_join_kernel<G, 1><<<blocks, 256, 0, s>>>(a, part, cross, join_slabs);
     return cudaGetLastError();
   }
   return cudaSuccess;
@@ -439,12 +491,18 @@ cudaError_t launch_embed_backward(const EmbedArgs &a, int num_sms, cudaStream_t 
   }
   uint8_t *used = a.accumulate ? nullptr : a.ws + w.used;
   float *part = reinterpret_cast<float *>(a.ws + w.part);
-  cudaError_t e = cudaSuccess;
-  if (used && (e = cudaMemsetAsync(used, 0, a.V, s)) != cudaSuccess) return e;
+  int *cross = reinterpret_cast<int *>(a.ws + w.cross);
+  // the flags of the table rows and the number of crossing runs lie together
+  cudaError_t e = used ? cudaMemsetAsync(used, 0, w.cross + 4 - w.used, s) : cudaMemsetAsync(cross, 0, 4, s);
+  if (e != cudaSuccess) return e;
+  const long gsz = elem_bytes(a.grad_dtype);
+  Fill fill = {used, static_cast<uint8_t *>(a.dtable), a.d * gsz, a.ld_t * gsz, static_cast<int>(gsz), 0,
+               a.accumulate ? 0 : a.V};
+  if (vec16(a.dtable, a.ld_t, static_cast<int>(gsz)) && fill.row_bytes % 16 == 0) fill.unit = 16;
   int at = 0;
   if (a.rows > 0 && a.rows <= kSmallSort) {
     HostTrace t("embed_rank", s);
-    embed_rank_kernel<<<(a.rows + 255) / 256, 256, 0, s>>>(a, keys[0], pos[0], used);
+    embed_rank_kernel<<<(a.rows + kRankBlock - 1) / kRankBlock, kRankBlock, 0, s>>>(a, keys[0], pos[0], used);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   } else if (a.rows > 0) {
     int bits = 1;
@@ -470,12 +528,12 @@ cudaError_t launch_embed_backward(const EmbedArgs &a, int num_sms, cudaStream_t 
   const bool wide = a.grad_dtype == MOE_ELEM_FP32;
   switch (a.dtype) {
     case MOE_ELEM_BF16:
-      return wide ? sums<__nv_bfloat16, float>(a, k, ps, part, used, num_sms, s)
-                  : sums<__nv_bfloat16, __nv_bfloat16>(a, k, ps, part, used, num_sms, s);
+      return wide ? sums<__nv_bfloat16, float>(a, k, ps, part, cross, fill, num_sms, s)
+                  : sums<__nv_bfloat16, __nv_bfloat16>(a, k, ps, part, cross, fill, num_sms, s);
     case MOE_ELEM_FP16:
-      return wide ? sums<__half, float>(a, k, ps, part, used, num_sms, s)
-                  : sums<__half, __half>(a, k, ps, part, used, num_sms, s);
-    default: return sums<float, float>(a, k, ps, part, used, num_sms, s);
+      return wide ? sums<__half, float>(a, k, ps, part, cross, fill, num_sms, s)
+                  : sums<__half, __half>(a, k, ps, part, cross, fill, num_sms, s);
+    default: return sums<float, float>(a, k, ps, part, cross, fill, num_sms, s);
   }
 }
 

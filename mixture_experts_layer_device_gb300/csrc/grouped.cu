@@ -275,7 +275,7 @@ MOE_DEV void few_dot(const GroupedArgs &g, const T *x, const T *w, int nf, float
   for (int r = 0; r < R; ++r)
 #pragma unroll
     for (int f = 0; f < FEW_F; ++f) acc[r][f] = 0.f;
-  constexpr int UNROLL = 4;
+  constexpr int UNROLL = 2;
   for (int c0 = lane; c0 < chunks; c0 += 32 * UNROLL) {
     uint4 q[UNROLL][FEW_F];
 #pragma unroll

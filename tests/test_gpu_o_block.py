@@ -367,7 +367,8 @@ def test_norm_gradient_against_differences(blk):
 
 # ---------------------------------------------------------------- embedding
 EMBED = [(1, 1, 1), (1, 50, 64), (7, 3, 33), (64, 10, 128), (300, 1000, 72), (513, 97, 40), (2048, 5000, 24), (2049, 5000, 24),
-         (5000, 70000, 16), (4097, 2, 264), (3000, 1, 8), (6000, 1100000, 3)]
+         (5000, 70000, 16), (4097, 2, 264), (3000, 1, 8), (6000, 1100000, 3), (9000, 20000, 64),
+         (9001, 300, 37)]
 
 
 @pytest.mark.parametrize("rows,V,d", EMBED)
