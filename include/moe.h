@@ -414,7 +414,7 @@ typedef enum { MOE_ELEM_BF16 = 0, MOE_ELEM_FP16 = 1, MOE_ELEM_FP32 = 2 } moe_ele
  * Offsets that descend or leave [0, rows] never cause an access out of range;
  * moe_get_status(ws) then reports MOE_ERR_BOUNDS (in every build) and the
  * outputs are unspecified.
- * Limits: 1 <= E <= 65535, 1 <= N, K <= 2^20, rows < 2^31 - 256, strides below 2^31
+ * Limits: 1 <= E <= 32767, 1 <= N, K <= 2^20, rows < 2^31 - 256, strides below 2^31
  * (MOE_ERR_SHAPE).  16-byte aligned rows and pointers run on the tensor cores
  * through TMA, few rows in all (a generated token) on a kernel that streams
  * the experts' weights, everything else on a plain tiled kernel.

@@ -42,13 +42,16 @@ struct GroupedArgs {
   const void *x, *w, *dy;
   void *y, *dx, *dw;
   int *status;   // workspace status word
-  int *tiles;    // workspace: [E + 1] first token tile of every expert
+  int *tiles;    // workspace: the plan's tile table (4 E + 4 ints)
+  int *order;    // workspace: the experts by descending rows (weight gradient)
   uint8_t *maps; // workspace: 2 E tensor maps of 128 bytes (weight gradient)
 };
 
 // The first launch of a call writes the status word (bad offsets) and zeroes the
 // output rows of no expert: the plan does it for the plain kernel, whose tile
-// table it also makes, the others do it themselves.
+// table (first tile of `tile_rows` rows of every expert) it also makes, and for
+// the tensor-core kernel with more experts than its shared memory holds
+// (tile_rows 0: grouped.cuh's table); otherwise the kernels do it themselves.
 cudaError_t launch_grouped_plan(const GroupedArgs &g, int tile_rows, void *out, int out_elem, int out_cols,
                                 long ld_out, cudaStream_t s);
 // Any size, stride and alignment; `first`: with the plan in front.

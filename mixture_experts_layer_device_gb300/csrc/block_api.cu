@@ -22,13 +22,14 @@ bool stride(int64_t given, int64_t least, long *out) {
 
 // ---------------------------------------------------------------- grouped
 struct GroupedWs {
-  size_t status, tiles, maps, bytes;
+  size_t status, tiles, order, maps, bytes;
 };
 GroupedWs grouped_ws(int E) {
   GroupedWs w;
   w.status = 0;
   w.tiles = 256;
-  w.maps = w.tiles + round256((static_cast<size_t>(E) + 1) * 4);
+  w.order = w.tiles + round256((4 * static_cast<size_t>(E) + 4) * 4);
+  w.maps = w.order + round256(static_cast<size_t>(E) * 4);
   w.bytes = w.maps + static_cast<size_t>(E) * 2 * 128 + 128;  // aligned to 128 bytes in place
   return w;
 }
@@ -39,10 +40,12 @@ int grouped_check(const moe_grouped_config *c, moe::GroupedArgs *g) {
   if (c->dtype != MOE_ELEM_BF16 && c->dtype != MOE_ELEM_FP16) return MOE_ERR_ARG;
   if (c->out_dtype != c->dtype && c->out_dtype != MOE_ELEM_FP32) return MOE_ERR_ARG;
   if (c->accumulate != 0 && (c->accumulate != 1 || c->out_dtype != MOE_ELEM_FP32)) return MOE_ERR_ARG;
-  if (c->E > 65535 || c->N > (1 << 20) || c->K > (1 << 20) || c->rows >= (1LL << 31) - 256) return MOE_ERR_SHAPE;
+  if (c->E > 32767 || c->N > (1 << 20) || c->K > (1 << 20) || c->rows >= (1LL << 31) - 256) return MOE_ERR_SHAPE;
   *g = moe::GroupedArgs();
   if (!stride(c->ld_x, c->K, &g->ld_x) || !stride(c->ld_y, c->N, &g->ld_y) || !stride(c->ld_w, c->K, &g->ld_w))
     return MOE_ERR_SHAPE;
+  // tiles of the weight gradient are counted in 32 bits
+  if (static_cast<int64_t>(c->E) * ((c->N + 255) / 256) * ((c->K + 255) / 256) >= (1LL << 30)) return MOE_ERR_SHAPE;
   // a matrix's extent may pass 2^31: only the strides of rows are held below it
   const int64_t extent = static_cast<int64_t>(c->N - 1) * g->ld_w + c->K;
   if (c->ld_e != 0 && (c->ld_e < extent || c->ld_e > (1LL << 40))) return MOE_ERR_SHAPE;
@@ -63,6 +66,7 @@ void grouped_bind(moe::GroupedArgs *g, const int32_t *offsets, void *ws) {
   g->offsets = offsets;
   g->status = reinterpret_cast<int *>(b + w.status);
   g->tiles = reinterpret_cast<int *>(b + w.tiles);
+  g->order = reinterpret_cast<int *>(b + w.order);
   g->maps = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(b + w.maps) + 127) & ~static_cast<uintptr_t>(127));
 }
 
@@ -72,6 +76,8 @@ bool tma_rows(const void *p, long ld) { return aligned(p, 16) && ld % 8 == 0; }
 
 bool grouped_tensor(const moe::GroupedArgs &g, int dir) {
   if (g.rows == 0 || g.N % 8 || g.K % 8) return false;
+  const long widest = ((g.N > g.K ? g.N : g.K) + 255L) / 256;
+  if ((g.rows / 256 + 2L * g.E) * widest >= (1L << 30)) return false;  // tiles are counted in 32 bits
   const bool w = tma_rows(g.w, g.ld_w) && g.ld_e % 8 == 0;
   if (dir == moe::GROUPED_FWD) return w && tma_rows(g.x, g.ld_x) && tma_rows(g.y, g.ld_y);
   if (dir == moe::GROUPED_DGRAD) return w && tma_rows(g.dy, g.ld_y) && tma_rows(g.dx, g.ld_x);

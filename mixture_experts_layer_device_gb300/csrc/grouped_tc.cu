@@ -18,8 +18,9 @@
 // (64 features wide, 64 reduction steps deep) in the 128-byte swizzle, which the
 // shared-memory descriptors address directly.
 //
-// Roles per CTA (192 threads): TMA producer, MMA issuer (leader CTA), four
-// epilogue warps; six 32 KB stages; two accumulators of 256 TMEM columns, so a
+// Roles per CTA (320 threads): TMA producer, MMA issuer (leader CTA), eight
+// epilogue warps (two per quarter of the accumulator's rows: one alone works on
+// its instructions' latencies); six 32 KB stages; two accumulators of 256 TMEM columns, so a
 // tile's epilogue runs beside the next one's MMAs.  Persistent: pair c takes
 // tiles c, c + pairs, ...  Every wait is bounded (mbar_wait).
 #include "elem.cuh"
@@ -31,16 +32,21 @@ namespace moe {
 
 namespace {
 
-constexpr int kStages = 6;
 constexpr int kStageBytes = 32768;           // 16 KB of A, up to 16 KB of B
-constexpr int kStaging = 8192;               // per epilogue warp: two 4 KB pieces
-constexpr int kTileTokens = 256;
-constexpr size_t kSmem = 1024 + kStages * kStageBytes + 4 * kStaging + (2 * kStages + 5) * 8 + 16;
-static_assert(kSmem <= 232448, "shared memory");
-// Forward and dgrad stage 2 KB per warp and keep the tile table in the rest;
-// more experts than it holds take the plan launch's table in the workspace.
-constexpr int kTablePlace = 4 * 2048;
-constexpr int kTableExperts = (4 * kStaging - kTablePlace) / 4 - 1;
+constexpr int kThreads = 320;
+constexpr int kEpilogueWarps = 8;
+
+template <int DIR>
+struct TcShape {
+  static constexpr int STAGES = DIR == GROUPED_WGRAD ? 5 : 6;
+  static constexpr int STAGING = DIR == GROUPED_WGRAD ? 8192 : 4096;  // per epilogue warp
+  static constexpr size_t SMEM = 1024 + STAGES * kStageBytes + kEpilogueWarps * STAGING + (2 * STAGES + 5) * 8 + 16;
+  static_assert(SMEM <= 232448, "shared memory");
+};
+// Forward and dgrad stage 2 KB per warp and keep the tile table in the rest of
+// the staging; more experts than it holds take the plan launch's table.
+constexpr int kTablePlace = kEpilogueWarps * 2048;
+constexpr int kTableExperts = ((kEpilogueWarps * TcShape<GROUPED_FWD>::STAGING - kTablePlace) / 4 - 4) / 4;
 
 struct TcMaps {
   CUtensorMap a;        // forward, dgrad: w
@@ -65,6 +71,21 @@ MOE_DEV void tma_add_3d(const CUtensorMap *map, const void *src, int c0, int c1,
                    map),
                "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
                : "memory");
+}
+
+// `half` token rows (a multiple of 16, up to 128) in boxes of 128, 64, 32 and 16.
+MOE_DEV void load_tokens(const CUtensorMap *maps, uint32_t bar, uint8_t *dst, int k, int row, int half) {
+  if (half == 128) {
+    tma_load_2d_pair(&maps[3], bar, dst, k, row);
+    return;
+  }
+#pragma unroll
+  for (int i = 2; i >= 0; --i)
+    if (half & (16 << i)) {
+      tma_load_2d_pair(&maps[i], bar, dst, k, row);
+      dst += 2048 << i;
+      row += 16 << i;
+    }
 }
 
 // Descriptor of an MN-major operand in the 128-byte swizzle: rows of 64 features
@@ -100,91 +121,68 @@ struct TcTile {
   int klen;   // reduction length
 };
 
-// First token tile of every expert into tiles[0 .. E], by all 192 threads; no
-// tiles at all when the offsets are bad.
-MOE_DEV bool tile_table(const GroupedArgs &g, int *tiles, int *warp_sum) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int run = 0;
-  bool bad = false;
-  for (int base = 0; base < g.E; base += 192) {
-    const int e = base + threadIdx.x;
-    int n = 0;
-    if (e < g.E) {
+// The tiles of a call in the order in which the pairs take them.
+template <int DIR>
+struct TcTiles {
+  const GroupedArgs &g;
+  TileTable t;
+  int nf, nc, total;
+  MOE_DEV TcTiles(const GroupedArgs &args, int *table) : g(args) {
+    nf = ((DIR == GROUPED_DGRAD ? g.K : g.N) + 255) >> 8;
+    if constexpr (DIR == GROUPED_WGRAD) {
+      nc = (g.K + 255) >> 8;
+      total = g.E * nf * nc;
+    } else {
+      t = tile_table_at(table, g.E);
+      nc = 1;
+      total = (t.n_whole + t.n_rest) * nf;
+    }
+  }
+  // The same without the end: whatever lies past it is not used.
+  MOE_DEV TcTile ahead(int u) const { return u < total ? at(u) : TcTile(); }
+  // Pair p's i-th tile: back and forth over the pairs, so that in a descending
+  // order of sizes no pair always gets the larger one.
+  MOE_DEV int unit(int i, int p, int pairs) const { return i * pairs + ((i & 1) ? pairs - 1 - p : p); }
+  MOE_DEV TcTile at(int u) const {
+    TcTile r;
+    if constexpr (DIR == GROUPED_WGRAD) {
+      const int per = nf * nc, q = u / per, w = u - q * per;
+      r.e = __ldg(g.order + q);
+      r.f0 = (w / nc) * 256;
+      r.c0 = (w % nc) * 256;
+      r.valid = g.K - r.c0 < 256 ? g.K - r.c0 : 256;
+      // MN-major columns come in whole 64-feature blocks per CTA
+      r.n = r.valid > 128 ? 256 : 128;
       int lo, hi;
-      bad |= !group_rows(g, e, lo, hi);
-      n = (hi - lo + kTileTokens - 1) / kTileTokens;
+      group_rows(g, r.e, lo, hi);
+      r.k0 = lo;
+      r.klen = hi - lo;
+    } else {
+      const int whole = t.n_whole * nf;
+      if (u < whole) {
+        r.e = group_of_tile(t.whole, g.E, u / nf);
+        const int first = t.whole[r.e], mt = t.whole[r.e + 1] - first, local = u - first * nf;
+        r.f0 = (local / mt) * 256;
+        r.c0 = t.off[r.e] + (local % mt) * kTileTokens;
+        r.valid = kTileTokens;
+      } else {
+        const int i = (u - whole) / nf, id = t.rest[i];
+        r.e = id >> 1;
+        r.f0 = (u - whole - i * nf) * 256;
+        const int lo = t.off[r.e], rows = t.off[r.e + 1] - lo;
+        const TokenCut c = cut_tokens(rows);
+        const int done = c.whole * kTileTokens;
+        r.c0 = lo + done + ((id & 1) ? c.size : 0);
+        r.valid = (id & 1) ? rows - done - c.size : c.size;
+        if (c.rest == 1) r.valid = rows;
+      }
+      r.n = (r.valid + 31) & ~31;
+      r.k0 = 0;
+      r.klen = DIR == GROUPED_DGRAD ? g.N : g.K;
     }
-    int inc = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
-    if (lane == 31) warp_sum[warp] = inc;
-    __syncthreads();
-    int before = run;
-#pragma unroll
-    for (int w = 0; w < 6; ++w) {
-      if (w < warp) before += warp_sum[w];
-      run += warp_sum[w];
-    }
-    if (e < g.E) tiles[e] = before + inc - n;
-    __syncthreads();
+    return r;
   }
-  const bool any = __syncthreads_or(bad);
-  if (threadIdx.x == 0) tiles[g.E] = any ? 0 : run;
-  __syncthreads();
-  return any;
-}
-
-template <int DIR>
-MOE_DEV long tc_units(const GroupedArgs &g) {
-  const int F = DIR == GROUPED_DGRAD ? g.K : g.N;
-  const long nf = (F + 255) >> 8;
-  if (DIR == GROUPED_WGRAD) return g.E * nf * ((g.K + 255) >> 8);
-  return nf * g.tiles[g.E];
-}
-
-template <int DIR>
-MOE_DEV TcTile tc_tile(const GroupedArgs &g, long u) {
-  TcTile t;
-  int lo, hi;
-  if constexpr (DIR == GROUPED_WGRAD) {
-    const int nf = (g.N + 255) >> 8, nc = (g.K + 255) >> 8;
-    t.e = static_cast<int>(u / (nf * nc));
-    const int r = static_cast<int>(u - static_cast<long>(t.e) * (nf * nc));
-    t.f0 = (r / nc) * 256;
-    t.c0 = (r % nc) * 256;
-    t.valid = g.K - t.c0 < 256 ? g.K - t.c0 : 256;
-    group_rows(g, t.e, lo, hi);
-    t.k0 = lo;
-    t.klen = hi - lo;
-  } else {
-    const int nf = ((DIR == GROUPED_DGRAD ? g.K : g.N) + 255) >> 8;
-    t.e = group_of_tile(g.tiles, g.E, static_cast<int>(u / nf));
-    const int first = g.tiles[t.e], mt = g.tiles[t.e + 1] - first;
-    const int local = static_cast<int>(u - static_cast<long>(first) * nf);
-    t.f0 = (local / mt) * 256;
-    const int tt = local % mt;
-    group_rows(g, t.e, lo, hi);
-    // whole tiles, the last two share what is left evenly
-    int from = tt * kTileTokens, to = from + kTileTokens;
-    if (mt > 1 && tt >= mt - 2) {
-      const int base = (mt - 2) * kTileTokens, left = hi - lo - base;
-      const int half = ((left + 1) / 2 + 31) & ~31;
-      from = tt == mt - 1 ? base + half : base;
-      to = tt == mt - 1 ? base + left : base + half;
-    }
-    if (to > hi - lo) to = hi - lo;
-    t.c0 = lo + from;
-    t.valid = to - from;
-    t.k0 = 0;
-    t.klen = DIR == GROUPED_DGRAD ? g.N : g.K;
-  }
-  // MN-major columns come in whole 64-feature blocks per CTA
-  t.n = DIR == GROUPED_WGRAD ? (t.valid > 128 ? 256 : 128) : (t.valid + 31) & ~31;
-  return t;
-}
+};
 
 // A piece of 32 tokens x 32 features from one warp's accumulator columns (lane =
 // feature): neighbouring lanes swap so that each holds two features of one
@@ -211,10 +209,11 @@ MOE_DEV void put_tokens(const float *v, uint8_t *buf, T *out, long ld, int token
 }
 
 // A piece of 32 rows x 128 bytes of dw (lane = row) into 128-byte-swizzled shared
-// memory and out by TMA, which clips it to the expert's matrix.
-MOE_DEV void put_rows(const uint32_t *w, uint8_t *buf, const CUtensorMap *map, bool add, int col, int row, int e,
-                      bool inside, int lane) {
-  if (lane == 0) bulk_wait_read<1>();  // the piece before last has left this buffer
+// memory and out by TMA (or added to what is there), which clips it to the
+// expert's matrix.  Two buffers per warp: the piece before last has left when
+// this one is written.
+MOE_DEV void put_rows(const uint32_t *w, uint8_t *buf, const CUtensorMap *map, bool add, int col, int row, int e, int lane) {
+  if (lane == 0) bulk_wait_read<1>();
   __syncwarp();
 #pragma unroll
   for (int j = 0; j < 8; ++j)
@@ -223,22 +222,21 @@ MOE_DEV void put_rows(const uint32_t *w, uint8_t *buf, const CUtensorMap *map, b
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) {
-    if (inside) {
-      if (add) tma_add_3d(map, buf, col, row, e);
-      else tma_store_3d(map, buf, col, row, e);
-    }
+    if (add) tma_add_3d(map, buf, col, row, e);
+    else tma_store_3d(map, buf, col, row, e);
     bulk_commit();
   }
 }
 
-template <int DIR>
-__global__ void __launch_bounds__(192, 1) grouped_tc_kernel(const __grid_constant__ TcMaps maps, const GroupedArgs ga) {
-  GroupedArgs g = ga;
+// T: the operands' type; WIDE: fp32 output (y or dw).
+template <int DIR, typename T, bool WIDE>
+__global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_constant__ TcMaps maps, const GroupedArgs g) {
+  constexpr int kStages = TcShape<DIR>::STAGES, kStaging = TcShape<DIR>::STAGING;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   uint8_t *staging = smem + kStages * kStageBytes;
-  uint64_t *full = reinterpret_cast<uint64_t *>(staging + 4 * kStaging);
+  uint64_t *full = reinterpret_cast<uint64_t *>(staging + kEpilogueWarps * kStaging);
   uint64_t *empty = full + kStages;
   uint64_t *tfull = empty + kStages;
   uint64_t *tempty = tfull + 2;
@@ -249,7 +247,7 @@ __global__ void __launch_bounds__(192, 1) grouped_tc_kernel(const __grid_constan
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
-  const long pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -257,7 +255,7 @@ __global__ void __launch_bounds__(192, 1) grouped_tc_kernel(const __grid_constan
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 256);  // epilogue threads of both CTAs
+      mbar_init(&tempty[a], 2 * 32 * kEpilogueWarps);  // epilogue threads of both CTAs
     }
     mbar_init(done, 1);
     *abort_flag = 0;
@@ -268,10 +266,11 @@ __global__ void __launch_bounds__(192, 1) grouped_tc_kernel(const __grid_constan
     tmem_relinquish_pair();
     tc_fence_before();
   }
+  int *table = g.tiles;
   if constexpr (DIR != GROUPED_WGRAD) {
     if (g.E <= kTableExperts) {
-      g.tiles = reinterpret_cast<int *>(staging + kTablePlace);
-      const bool bad = tile_table(g, g.tiles, reinterpret_cast<int *>(staging));
+      table = reinterpret_cast<int *>(staging + kTablePlace);
+      const bool bad = build_tile_table<kThreads>(g, table, reinterpret_cast<unsigned long long *>(staging));
       if (blockIdx.x == 0 && threadIdx.x == 0) *g.status = bad ? kStatusBounds : 0;
     }
   }
@@ -279,7 +278,7 @@ __global__ void __launch_bounds__(192, 1) grouped_tc_kernel(const __grid_constan
   cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const long total = tc_units<DIR>(g);
+  const TcTiles<DIR> tiles(g, table);
 
   if (warp == 0) {
     // ------------------------------------------------ TMA producer (both CTAs)
@@ -287,13 +286,14 @@ __global__ void __launch_bounds__(192, 1) grouped_tc_kernel(const __grid_constan
       int stage = 0;
       uint32_t ph = 0;
       int fenced = -1;
-      for (long u = pair; u < total && !*abort_flag; u += pairs) {
-        const TcTile t = tc_tile<DIR>(g, u);
+      TcTile next = tiles.ahead(pair);  // looked up one tile early: the look-up is a chain of loads
+      for (int i = 0; tiles.unit(i, pair, pairs) < tiles.total && !*abort_flag; ++i) {
+        const TcTile t = next;
+        next = tiles.ahead(tiles.unit(i + 1, pair, pairs));
         const int half = t.n >> 1;
         const int fr = t.f0 + static_cast<int>(rank) * 128, cr = t.c0 + static_cast<int>(rank) * half;
-        const int level = half > 64 ? 3 : (half > 32 ? 2 : (half > 16 ? 1 : 0));
-        const uint32_t b_bytes = DIR == GROUPED_WGRAD ? (half > 64 ? 16384u : 8192u) : 2048u << level;
-        const CUtensorMap *ma = &maps.a, *mb = &maps.b[level];
+        const uint32_t b_bytes = 128u * static_cast<uint32_t>(half);
+        const CUtensorMap *ma = &maps.a, *mb = &maps.b[3];
         if constexpr (DIR == GROUPED_WGRAD) {
           if (t.klen == 0) continue;
           ma = reinterpret_cast<const CUtensorMap *>(g.maps + static_cast<long>(t.e) * 256);
@@ -316,11 +316,11 @@ __global__ void __launch_bounds__(192, 1) grouped_tc_kernel(const __grid_constan
           const int k = t.k0 + kb;
           if constexpr (DIR == GROUPED_FWD) {
             tma_load_3d_pair(ma, bar, sa, k, fr, t.e);
-            tma_load_2d_pair(mb, bar, sb, k, cr);
+            load_tokens(maps.b, bar, sb, k, cr, half);
           } else if constexpr (DIR == GROUPED_DGRAD) {
             tma_load_3d_pair(ma, bar, sa, fr, k, t.e);
             tma_load_3d_pair(ma, bar, sa + 8192, fr + 64, k, t.e);
-            tma_load_2d_pair(mb, bar, sb, k, cr);
+            load_tokens(maps.b, bar, sb, k, cr, half);
           } else {
             tma_load_2d_pair(ma, bar, sa, fr, k);
             tma_load_2d_pair(ma, bar, sa + 8192, fr + 64, k);
@@ -341,8 +341,10 @@ __global__ void __launch_bounds__(192, 1) grouped_tc_kernel(const __grid_constan
       int stage = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
       bool ok = true;
-      for (long u = pair; u < total && ok; u += pairs) {
-        const TcTile t = tc_tile<DIR>(g, u);
+      TcTile next = tiles.ahead(pair);
+      for (int i = 0; tiles.unit(i, pair, pairs) < tiles.total && ok; ++i) {
+        const TcTile t = next;
+        next = tiles.ahead(tiles.unit(i + 1, pair, pairs));
         if (t.klen == 0) continue;
         if (!mbar_wait(&tempty[acc], aph ^ 1u, abort_flag, g.status)) break;
         tc_fence_after();
@@ -382,8 +384,8 @@ __global__ void __launch_bounds__(192, 1) grouped_tc_kernel(const __grid_constan
       mbar_wait(done, 0, &no_abort, g.status);
     }
   } else {
-    // ------------------------------------------------ epilogue (warps 2..5, both CTAs)
-    const int q = warp & 3;
+    // ------------------------------------------------ epilogue (warps 2..9, both CTAs)
+    const int q = warp & 3, half = (warp - 2) >> 2;  // accumulator rows; which of the pieces of 32 columns
     uint8_t *buf = staging + (warp - 2) * (DIR == GROUPED_WGRAD ? kStaging : 2048);
     int acc = 0, piece = 0;
     uint32_t aph = 0;
@@ -393,16 +395,17 @@ __global__ void __launch_bounds__(192, 1) grouped_tc_kernel(const __grid_constan
       group_rows(g, 0, lo, hi);
       group_rows(g, g.E - 1, lo_last, hi_last);
       const int outside = g.E <= kTableExperts ? lo + (g.rows - hi_last) : 0;
-      const bool wide = DIR == GROUPED_FWD && g.out_dtype == MOE_ELEM_FP32;
-      const long ld = (DIR == GROUPED_DGRAD ? g.ld_x : g.ld_y) * (wide ? 4 : 2);
-      const int bytes = (DIR == GROUPED_DGRAD ? g.K : g.N) * (wide ? 4 : 2);
+      const long ld = (DIR == GROUPED_DGRAD ? g.ld_x : g.ld_y) * (WIDE ? 4 : 2);
+      const int bytes = (DIR == GROUPED_DGRAD ? g.K : g.N) * (WIDE ? 4 : 2);
       uint8_t *out = static_cast<uint8_t *>(DIR == GROUPED_DGRAD ? g.dx : g.y);
       for (long i = blockIdx.x; i < outside; i += gridDim.x)
-        for (int b = (threadIdx.x - 64) * 16; b < bytes; b += 128 * 16)
+        for (int b = (threadIdx.x - 64) * 16; b < bytes; b += 32 * kEpilogueWarps * 16)
           *reinterpret_cast<uint4 *>(out + (i < lo ? i : hi_last + (i - lo)) * ld + b) = make_uint4(0, 0, 0, 0);
     }
-    for (long u = pair; u < total; u += pairs) {
-      const TcTile t = tc_tile<DIR>(g, u);
+    TcTile next = tiles.ahead(pair);
+    for (int i = 0; tiles.unit(i, pair, pairs) < tiles.total; ++i) {
+      const TcTile t = next;
+      next = tiles.ahead(tiles.unit(i + 1, pair, pairs));
       const int fr = t.f0 + static_cast<int>(rank) * 128 + q * 32;  // this warp's first feature
       const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * 256);
       if (t.klen > 0) {
@@ -417,58 +420,60 @@ __global__ void __launch_bounds__(192, 1) grouped_tc_kernel(const __grid_constan
         if (leader) mbar_arrive(&tempty[acc]);
         else mbar_arrive_remote(peer_smem(tempty_addr, 0));
       };
+      bool held = t.klen > 0;  // this warp has not released the accumulator yet
       if constexpr (DIR == GROUPED_WGRAD) {
-        const bool wide = g.out_dtype == MOE_ELEM_FP32;
-        const int step = wide ? 32 : 64;
-        for (int j = 0; j < t.n; j += step) {
-          uint32_t r[64], w[32];
+        constexpr int STEP = WIDE ? 32 : 64;  // columns of a 128-byte piece
+        for (int j = half * STEP; j < t.n; j += 2 * STEP) {
+          uint32_t r[STEP], w[32];
           if (t.klen > 0) {
             tmem_ld32_async(tb + j, r);
-            if (!wide) tmem_ld32_async(tb + j + 32, r + 32);
+            if (!WIDE) tmem_ld32_async(tb + j + 32, r + STEP - 32);
             tmem_ld_wait();
-            reg_fence<64>(r);
+            reg_fence<STEP>(r);
           } else {
 #pragma unroll
-            for (int i = 0; i < 64; ++i) r[i] = 0;
+            for (int i = 0; i < STEP; ++i) r[i] = 0;
           }
-          if (j + step >= t.n && t.klen > 0) release();
+          if (held && j + 2 * STEP >= t.n) {
+            release();
+            held = false;
+          }
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float a = __uint_as_float(r[2 * i]), b = __uint_as_float(r[2 * i + 1]);
-            if (wide) w[i] = r[i];
-            else w[i] = g.dtype == MOE_ELEM_BF16 ? Elem<__nv_bfloat16>::pack2(a, b) : Elem<__half>::pack2(a, b);
-          }
-          put_rows(w, buf + (piece & 1) * 4096, &maps.out, g.accumulate != 0, t.c0 + j, fr, t.e,
-                   fr < g.N && t.c0 + j < g.K, lane);
+          for (int i = 0; i < 32; ++i)
+            if constexpr (WIDE) w[i] = r[i];
+            else w[i] = Elem<T>::pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+          if (fr >= g.N || t.c0 + j >= g.K) continue;
+          put_rows(w, buf + (piece & 1) * 4096, &maps.out, WIDE && g.accumulate, t.c0 + j, fr, t.e, lane);
           ++piece;
         }
       } else {
         const int F = DIR == GROUPED_DGRAD ? g.K : g.N;
         const long ld = DIR == GROUPED_DGRAD ? g.ld_x : g.ld_y;
-        for (int j = 0; j < t.n; j += 32) {
+        for (int j = half * 32; j < t.n; j += 64) {
           uint32_t r[32];
           tmem_ld32_async(tb + j, r);
           tmem_ld_wait();
           reg_fence<32>(r);
-          if (j + 32 >= t.n) release();
+          if (j + 64 >= t.n) {
+            release();
+            held = false;
+          }
           const float *v = reinterpret_cast<const float *>(r);
           const long row = t.c0 + j;
           const int tokens = t.valid - j;
           if (fr >= F) continue;
-          if (DIR == GROUPED_FWD && g.out_dtype == MOE_ELEM_FP32) {
+          if constexpr (WIDE) {
             float *out = static_cast<float *>(g.y) + row * ld + fr + lane;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (i < tokens && fr + lane < F) out[i * ld] = v[i];
           } else {
-            uint16_t *out = static_cast<uint16_t *>(DIR == GROUPED_DGRAD ? g.dx : g.y) + row * ld + fr;
-            if (g.dtype == MOE_ELEM_BF16)
-              put_tokens(v, buf, reinterpret_cast<__nv_bfloat16 *>(out), ld, tokens, F - fr, lane);
-            else
-              put_tokens(v, buf, reinterpret_cast<__half *>(out), ld, tokens, F - fr, lane);
+            put_tokens(v, buf, static_cast<T *>(DIR == GROUPED_DGRAD ? g.dx : g.y) + row * ld + fr, ld, tokens, F - fr,
+                       lane);
           }
         }
       }
+      if (held) release();  // a narrow tile has no piece for this half
       if (t.klen > 0 && ++acc == 2) {
         acc = 0;
         aph ^= 1u;
@@ -485,21 +490,56 @@ __global__ void __launch_bounds__(192, 1) grouped_tc_kernel(const __grid_constan
   }
 }
 
-// The experts' tensor maps of the weight gradient: dy's and x's map with the row
-// extent cut to the expert's last row.  One warp per map; the copy to global
-// memory makes it visible to later TMA accesses.
+// Before the weight gradient, by its last block the experts in descending order of
+// rows (by buckets, an eighth of an octave wide), by the others their tensor maps:
+// dy's and x's with the row extent cut to the expert's last row.  One warp per
+// map; the copy to global memory makes it visible to later TMA accesses.
+constexpr int kBuckets = 256;
+MOE_DEV int size_bucket(int rows) {  // descending
+  if (rows <= 0) return kBuckets - 1;
+  const unsigned f = __float_as_uint(static_cast<float>(rows));
+  const int b = static_cast<int>((f >> 20) - (127u << 3));  // eight steps per octave: 0 .. 247
+  return kBuckets - 2 - b;
+}
 __global__ void __launch_bounds__(128) grouped_maps_kernel(const __grid_constant__ CUtensorMap dy,
                                                            const __grid_constant__ CUtensorMap x, const GroupedArgs g) {
   __shared__ __align__(128) uint32_t sm[4][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int i = blockIdx.x * 4 + warp;
-  if (blockIdx.x == 0 && !g.dx) {  // the first launch of the call writes the status word
+  if (blockIdx.x == gridDim.x - 1) {
+    __shared__ int count[kBuckets];
+    for (int i = threadIdx.x; i < kBuckets; i += 128) count[i] = 0;
+    __syncthreads();
     bool bad = false;
     int lo, hi;
-    for (int e = threadIdx.x; e < g.E; e += 128) bad |= !group_rows(g, e, lo, hi);
+    for (int e = threadIdx.x; e < g.E; e += 128) {
+      bad |= !group_rows(g, e, lo, hi);
+      atomicAdd(&count[size_bucket(hi - lo)], 1);
+    }
     const int any = __syncthreads_or(bad);
-    if (threadIdx.x == 0) *g.status = any ? kStatusBounds : 0;
+    if (threadIdx.x == 0 && !g.dx) *g.status = any ? kStatusBounds : 0;  // the call's first launch
+    if (warp == 0) {
+      int run = 0;
+      for (int i = 0; i < kBuckets; i += 32) {
+        const int v = count[i + lane];
+        int inc = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int n = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += n;
+        }
+        count[i + lane] = run + inc - v;
+        run += __shfl_sync(0xffffffffu, inc, 31);
+      }
+    }
+    __syncthreads();
+    // places inside a bucket do not matter: an expert's tiles are computed alike wherever they stand
+    for (int e = threadIdx.x; e < g.E; e += 128) {
+      group_rows(g, e, lo, hi);
+      g.order[atomicAdd(&count[size_bucket(hi - lo)], 1)] = e;
+    }
+    return;
   }
+  const int i = blockIdx.x * 4 + warp;
   if (i >= 2 * g.E) return;
   sm[warp][lane] = reinterpret_cast<const uint32_t *>((i & 1) ? &x : &dy)[lane];
   __syncwarp();
@@ -518,15 +558,16 @@ __global__ void __launch_bounds__(128) grouped_maps_kernel(const __grid_constant
       : "memory");
 }
 
-template <int DIR>
+template <int DIR, typename T, bool WIDE>
 int tc_clusters_query() {
-  if (cudaFuncSetAttribute(grouped_tc_kernel<DIR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(kSmem)) != cudaSuccess)
+  const auto kernel = grouped_tc_kernel<DIR, T, WIDE>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(TcShape<DIR>::SMEM)) != cudaSuccess)
     return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2, 1, 1);
-  cfg.blockDim = dim3(192, 1, 1);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = TcShape<DIR>::SMEM;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
@@ -535,19 +576,19 @@ int tc_clusters_query() {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  return cudaOccupancyMaxActiveClusters(&n, grouped_tc_kernel<DIR>, &cfg) == cudaSuccess ? n : 0;
+  return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
 }
 
-template <int DIR>
-cudaError_t launch_tc(const TcMaps &maps, const GroupedArgs &g, long units, cudaStream_t s) {
+template <int DIR, typename T, bool WIDE>
+cudaError_t launch_tc_one(const TcMaps &maps, const GroupedArgs &g, long units, cudaStream_t s) {
   static int memo[64] = {};
-  const int most = per_device_memo(memo, tc_clusters_query<DIR>);
+  const int most = per_device_memo(memo, tc_clusters_query<DIR, T, WIDE>);
   if (most <= 0) return cudaErrorInvalidConfiguration;
   if (units <= 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * static_cast<unsigned>(units < most ? units : most), 1, 1);
-  cfg.blockDim = dim3(192, 1, 1);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = TcShape<DIR>::SMEM;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -556,7 +597,17 @@ cudaError_t launch_tc(const TcMaps &maps, const GroupedArgs &g, long units, cuda
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<DIR>, maps, g);
+  return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<DIR, T, WIDE>, maps, g);
+}
+
+template <int DIR>
+cudaError_t launch_tc(const TcMaps &maps, const GroupedArgs &g, long units, cudaStream_t s) {
+  const bool bf = g.dtype == MOE_ELEM_BF16;
+  if constexpr (DIR != GROUPED_DGRAD) {
+    if (g.out_dtype == MOE_ELEM_FP32)
+      return bf ? launch_tc_one<DIR, __nv_bfloat16, true>(maps, g, units, s) : launch_tc_one<DIR, __half, true>(maps, g, units, s);
+  }
+  return bf ? launch_tc_one<DIR, __nv_bfloat16, false>(maps, g, units, s) : launch_tc_one<DIR, __half, false>(maps, g, units, s);
 }
 
 // Token rows [rows, cols] with boxes of 64 columns x 16 << i rows.
@@ -593,11 +644,11 @@ cudaError_t launch_grouped_tc(const GroupedArgs &g, int dir, cudaStream_t s) {
         !expert_map(&m.out, g.out_dtype, g.dw, g, g.K, static_cast<long>(g.N) * g.K, g.out_dtype == MOE_ELEM_FP32 ? 32 : 64,
                     32))
       return cudaErrorInvalidValue;
-    m.a = dy;
+    m.a = dy;  // the kernel takes its experts' maps from the workspace
     for (int i = 0; i < 4; ++i) m.b[i] = x;
     {
       HostTrace t("grouped_maps", s);
-      grouped_maps_kernel<<<(2 * g.E + 3) / 4, 128, 0, s>>>(dy, x, g);
+      grouped_maps_kernel<<<(2 * g.E + 3) / 4 + 1, 128, 0, s>>>(dy, x, g);
       const cudaError_t e = cudaGetLastError();
       if (e != cudaSuccess) return e;
     }
@@ -607,14 +658,14 @@ cudaError_t launch_grouped_tc(const GroupedArgs &g, int dir, cudaStream_t s) {
   if (g.rows <= 0) return cudaSuccess;
   if (g.E > kTableExperts) {
     const bool fwd = dir == GROUPED_FWD;
-    const cudaError_t e = launch_grouped_plan(g, kTileTokens, fwd ? g.y : g.dx, fwd ? g.out_dtype : g.dtype,
+    const cudaError_t e = launch_grouped_plan(g, 0, fwd ? g.y : g.dx, fwd ? g.out_dtype : g.dtype,
                                               fwd ? g.N : g.K, fwd ? g.ld_y : g.ld_x, s);
     if (e != cudaSuccess) return e;
   }
   if (dir == GROUPED_FWD) {
     if (!row_maps(m.b, g.dtype, g.x, g.rows, g.K, g.ld_x) || !expert_map(&m.a, g.dtype, g.w, g, g.ld_w, g.ld_e, 64, 128))
       return cudaErrorInvalidValue;
-    m.out = m.a;
+      m.out = m.a;
     HostTrace t("grouped_forward", s);
     return launch_tc<GROUPED_FWD>(m, g, tokens * ((g.N + 255) / 256), s);
   }

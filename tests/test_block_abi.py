@@ -24,7 +24,7 @@ def grouped(pkg, **kw):
 
 @pytest.mark.parametrize("bad,code", [
     (dict(rows=-1), -1), (dict(E=0), -1), (dict(N=0), -1), (dict(K=-3), -1), (dict(dtype=2), -1), (dict(dtype=7), -1),
-    (dict(out_dtype=1), -1), (dict(accumulate=1), -1), (dict(accumulate=2, out_dtype=2), -1), (dict(E=65536), -2),
+    (dict(out_dtype=1), -1), (dict(accumulate=1), -1), (dict(accumulate=2, out_dtype=2), -1), (dict(E=32768), -2),
     (dict(N=(1 << 20) + 1), -2), (dict(rows=1 << 31), -2), (dict(ld_x=23), -2), (dict(ld_y=15), -2), (dict(ld_w=8), -2),
     (dict(ld_x=1 << 31), -2), (dict(ld_x=-24), -2), (dict(ld_e=16 * 24 - 1), -2), (dict(ld_w=32, ld_e=16 * 24), -2)])
 def test_grouped_refusals(pkg, bad, code):

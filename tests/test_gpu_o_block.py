@@ -82,6 +82,9 @@ GROUPED = [
     (1500, 3, 1000, 640, "even", 0, 0),
     (2000, 130, 264, 328, "skew", 0, 0),
     (5, 1024, 40, 512, "even", 0, 0),
+    (3000, 1, 64, 64, "one", 1, 2),
+    (2600, 2000, 16, 64, "skew", 0, 0),
+    (4000, 5, 72, 80, "skew", 0, 5),
 ]
 
 
