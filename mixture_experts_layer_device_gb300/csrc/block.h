@@ -42,7 +42,7 @@ struct GroupedArgs {
   const void *x, *w, *dy;
   void *y, *dx, *dw;
   int *status;   // workspace status word
-  int *tiles;    // workspace: the plan's tile table (4 E + 4 ints)
+  int *tiles;    // workspace: the plan's tile table (3 E + 3 ints)
   int *order;    // workspace: the experts by descending rows (weight gradient)
   uint8_t *maps; // workspace: 2 E tensor maps of 128 bytes (weight gradient)
 };

@@ -28,7 +28,7 @@ GroupedWs grouped_ws(int E) {
   GroupedWs w;
   w.status = 0;
   w.tiles = 256;
-  w.order = w.tiles + round256((4 * static_cast<size_t>(E) + 4) * 4);
+  w.order = w.tiles + round256((3 * static_cast<size_t>(E) + 3) * 4);
   w.maps = w.order + round256(static_cast<size_t>(E) * 4);
   w.bytes = w.maps + static_cast<size_t>(E) * 2 * 128 + 128;  // aligned to 128 bytes in place
   return w;

@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(1024) grouped_plan_kernel(const GroupedArgs g,
     }
     return;
   }
-  __shared__ unsigned long long scratch[128];
+  __shared__ int scratch[256];
   if (tile_rows == 0) {
     const bool bad_offsets = build_tile_table<1024>(g, g.tiles, scratch);
     if (threadIdx.x == 0) *g.status = bad_offsets ? kStatusBounds : 0;

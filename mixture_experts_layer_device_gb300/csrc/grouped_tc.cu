@@ -46,11 +46,11 @@ struct TcShape {
 // Forward and dgrad stage 2 KB per warp and keep the tile table in the rest of
 // the staging; more experts than it holds take the plan launch's table.
 constexpr int kTablePlace = kEpilogueWarps * 2048;
-constexpr int kTableExperts = ((kEpilogueWarps * TcShape<GROUPED_FWD>::STAGING - kTablePlace) / 4 - 4) / 4;
+constexpr int kTableExperts = ((kEpilogueWarps * TcShape<GROUPED_FWD>::STAGING - kTablePlace) / 4 - 3) / 3;
 
 struct TcMaps {
   CUtensorMap a;        // forward, dgrad: w
-  CUtensorMap b[4];     // token rows, boxes of 16, 32, 64 and 128 rows
+  CUtensorMap b[8];     // token rows, boxes of 16, 32, .. 128 rows
   CUtensorMap out;      // wgrad: dw
 };
 
@@ -71,21 +71,6 @@ MOE_DEV void tma_add_3d(const CUtensorMap *map, const void *src, int c0, int c1,
                    map),
                "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
                : "memory");
-}
-
-// `half` token rows (a multiple of 16, up to 128) in boxes of 128, 64, 32 and 16.
-MOE_DEV void load_tokens(const CUtensorMap *maps, uint32_t bar, uint8_t *dst, int k, int row, int half) {
-  if (half == 128) {
-    tma_load_2d_pair(&maps[3], bar, dst, k, row);
-    return;
-  }
-#pragma unroll
-  for (int i = 2; i >= 0; --i)
-    if (half & (16 << i)) {
-      tma_load_2d_pair(&maps[i], bar, dst, k, row);
-      dst += 2048 << i;
-      row += 16 << i;
-    }
 }
 
 // Descriptor of an MN-major operand in the 128-byte swizzle: rows of 64 features
@@ -135,7 +120,7 @@ struct TcTiles {
     } else {
       t = tile_table_at(table, g.E);
       nc = 1;
-      total = (t.n_whole + t.n_rest) * nf;
+      total = t.tiles * nf;
     }
   }
   // The same without the end: whatever lies past it is not used.
@@ -158,24 +143,14 @@ struct TcTiles {
       r.k0 = lo;
       r.klen = hi - lo;
     } else {
-      const int whole = t.n_whole * nf;
-      if (u < whole) {
-        r.e = group_of_tile(t.whole, g.E, u / nf);
-        const int first = t.whole[r.e], mt = t.whole[r.e + 1] - first, local = u - first * nf;
-        r.f0 = (local / mt) * 256;
-        r.c0 = t.off[r.e] + (local % mt) * kTileTokens;
-        r.valid = kTileTokens;
-      } else {
-        const int i = (u - whole) / nf, id = t.rest[i];
-        r.e = id >> 1;
-        r.f0 = (u - whole - i * nf) * 256;
-        const int lo = t.off[r.e], rows = t.off[r.e + 1] - lo;
-        const TokenCut c = cut_tokens(rows);
-        const int done = c.whole * kTileTokens;
-        r.c0 = lo + done + ((id & 1) ? c.size : 0);
-        r.valid = (id & 1) ? rows - done - c.size : c.size;
-        if (c.rest == 1) r.valid = rows;
-      }
+      const int i = group_of_tile(t.first, t.n, u / nf);
+      const int first = t.first[i], mt = t.first[i + 1] - first, local = u - first * nf;
+      r.e = t.order[i];
+      const int lo = t.off[r.e], rows = t.off[r.e + 1] - lo, size = tile_tokens(rows);
+      r.f0 = (local / mt) * 256;
+      const int from = (local % mt) * size;
+      r.c0 = lo + from;
+      r.valid = rows - from < size ? rows - from : size;
       r.n = (r.valid + 31) & ~31;
       r.k0 = 0;
       r.klen = DIR == GROUPED_DGRAD ? g.N : g.K;
@@ -270,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
   if constexpr (DIR != GROUPED_WGRAD) {
     if (g.E <= kTableExperts) {
       table = reinterpret_cast<int *>(staging + kTablePlace);
-      const bool bad = build_tile_table<kThreads>(g, table, reinterpret_cast<unsigned long long *>(staging));
+      const bool bad = build_tile_table<kThreads>(g, table, reinterpret_cast<int *>(staging));
       if (blockIdx.x == 0 && threadIdx.x == 0) *g.status = bad ? kStatusBounds : 0;
     }
   }
@@ -292,8 +267,12 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
         next = tiles.ahead(tiles.unit(i + 1, pair, pairs));
         const int half = t.n >> 1;
         const int fr = t.f0 + static_cast<int>(rank) * 128, cr = t.c0 + static_cast<int>(rank) * half;
-        const uint32_t b_bytes = 128u * static_cast<uint32_t>(half);
-        const CUtensorMap *ma = &maps.a, *mb = &maps.b[3];
+        // a box of just the CTA's tokens: one request costs less than several that make
+        // it up (32768 rows, 64 experts of [4096, 4096]: 811 us with boxes of 16, 32, 64
+        // or 128 rows, 855 with sums of them)
+        const int level = (half >> 4) - 1;
+        const uint32_t b_bytes = DIR == GROUPED_WGRAD ? (half > 64 ? 16384u : 8192u) : 128u * static_cast<uint32_t>(half);
+        const CUtensorMap *ma = &maps.a, *mb = &maps.b[level];
         if constexpr (DIR == GROUPED_WGRAD) {
           if (t.klen == 0) continue;
           ma = reinterpret_cast<const CUtensorMap *>(g.maps + static_cast<long>(t.e) * 256);
@@ -316,11 +295,11 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
           const int k = t.k0 + kb;
           if constexpr (DIR == GROUPED_FWD) {
             tma_load_3d_pair(ma, bar, sa, k, fr, t.e);
-            load_tokens(maps.b, bar, sb, k, cr, half);
+            tma_load_2d_pair(mb, bar, sb, k, cr);
           } else if constexpr (DIR == GROUPED_DGRAD) {
             tma_load_3d_pair(ma, bar, sa, fr, k, t.e);
             tma_load_3d_pair(ma, bar, sa + 8192, fr + 64, k, t.e);
-            load_tokens(maps.b, bar, sb, k, cr, half);
+            tma_load_2d_pair(mb, bar, sb, k, cr);
           } else {
             tma_load_2d_pair(ma, bar, sa, fr, k);
             tma_load_2d_pair(ma, bar, sa + 8192, fr + 64, k);
@@ -610,12 +589,12 @@ cudaError_t launch_tc(const TcMaps &maps, const GroupedArgs &g, long units, cuda
   return bf ? launch_tc_one<DIR, __nv_bfloat16, false>(maps, g, units, s) : launch_tc_one<DIR, __half, false>(maps, g, units, s);
 }
 
-// Token rows [rows, cols] with boxes of 64 columns x 16 << i rows.
+// Token rows [rows, cols] with boxes of 64 columns x 16 (i + 1) rows.
 bool row_maps(CUtensorMap *m, int elem, const void *p, long rows, int cols, long ld) {
   const uint64_t dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows)};
   const uint64_t strides[1] = {static_cast<uint64_t>(ld) * 2};
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t box[2] = {64, 16u << i};
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t box[2] = {64, 16u * (i + 1)};
     if (!host_encode_map(&m[i], elem, p, 2, dims, strides, box)) return false;
   }
   return true;
@@ -636,8 +615,8 @@ cudaError_t launch_grouped_tc(const GroupedArgs &g, int dir, cudaStream_t s) {
   const long tokens = (g.rows + kTileTokens - 1L) / kTileTokens + (g.E < g.rows ? g.E : g.rows);
   if (dir == GROUPED_WGRAD) {
     CUtensorMap dy, x;
-    const uint64_t n[2] = {static_cast<uint64_t>(g.N), static_cast<uint64_t>(g.rows > 0 ? g.rows : 1)};
-    const uint64_t k[2] = {static_cast<uint64_t>(g.K), n[1]};
+    const uint64_t n[2] = {static_cast<uint64_t>(g.N), static_cast<uint64_t>(g.rows)};
+    const uint64_t k[2] = {static_cast<uint64_t>(g.K), static_cast<uint64_t>(g.rows)};
     const uint64_t sn[1] = {static_cast<uint64_t>(g.ld_y) * 2}, sk[1] = {static_cast<uint64_t>(g.ld_x) * 2};
     const uint32_t box[2] = {64, 64};
     if (!host_encode_map(&dy, g.dtype, g.dy, 2, n, sn, box) || !host_encode_map(&x, g.dtype, g.x, 2, k, sk, box) ||
@@ -645,7 +624,7 @@ cudaError_t launch_grouped_tc(const GroupedArgs &g, int dir, cudaStream_t s) {
                     32))
       return cudaErrorInvalidValue;
     m.a = dy;  // the kernel takes its experts' maps from the workspace
-    for (int i = 0; i < 4; ++i) m.b[i] = x;
+    for (CUtensorMap &b : m.b) b = x;
     {
       HostTrace t("grouped_maps", s);
       grouped_maps_kernel<<<(2 * g.E + 3) / 4 + 1, 128, 0, s>>>(dy, x, g);
