@@ -32,15 +32,17 @@ namespace moe {
 
 namespace {
 
-constexpr int kStageBytes = 32768;           // 16 KB of A, up to 16 KB of B
+constexpr int kBlockBytes = 32768;           // 64 reduction steps: 16 KB of A, up to 16 KB of B
 constexpr int kThreads = 320;
 constexpr int kEpilogueWarps = 8;
 
 template <int DIR>
 struct TcShape {
-  static constexpr int STAGES = DIR == GROUPED_WGRAD ? 5 : 6;
+  static constexpr int BLOCKS = DIR == GROUPED_WGRAD ? 1 : 2;  // blocks of 64 reduction steps per stage
+  static constexpr int STAGES = DIR == GROUPED_WGRAD ? 5 : 3;
+  static constexpr int STAGE_BYTES = BLOCKS * kBlockBytes;
   static constexpr int STAGING = DIR == GROUPED_WGRAD ? 8192 : 4096;  // per epilogue warp
-  static constexpr size_t SMEM = 1024 + STAGES * kStageBytes + kEpilogueWarps * STAGING + (2 * STAGES + 5) * 8 + 16;
+  static constexpr size_t SMEM = 1024 + STAGES * STAGE_BYTES + kEpilogueWarps * STAGING + (2 * STAGES + 5) * 8 + 16;
   static_assert(SMEM <= 232448, "shared memory");
 };
 // Forward and dgrad stage 2 KB per warp and keep the tile table in the rest of
@@ -206,7 +208,8 @@ MOE_DEV void put_rows(const uint32_t *w, uint8_t *buf, const CUtensorMap *map, b
 // T: the operands' type; WIDE: fp32 output (y or dw).
 template <int DIR, typename T, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_constant__ TcMaps maps, const GroupedArgs g) {
-  constexpr int kStages = TcShape<DIR>::STAGES, kStaging = TcShape<DIR>::STAGING;
+  constexpr int kStages = TcShape<DIR>::STAGES, kStaging = TcShape<DIR>::STAGING, kBlocks = TcShape<DIR>::BLOCKS,
+                kStageBytes = TcShape<DIR>::STAGE_BYTES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
@@ -284,27 +287,32 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
           }
         }
         bool ok = true;
-        for (int kb = 0; kb < t.klen; kb += 64) {
+        for (int kb = 0; kb < t.klen; kb += 64 * kBlocks) {
           if (!mbar_wait(&empty[stage], ph ^ 1u, abort_flag, g.status)) {
             ok = false;
             break;
           }
-          uint8_t *sa = smem + stage * kStageBytes, *sb = sa + 16384;
-          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * (16384u + b_bytes));
+          const int blocks = t.klen - kb > 64 ? kBlocks : 1;
+          if (leader) mbar_arrive_expect_tx(&full[stage], 2u * blocks * (16384u + b_bytes));
           const uint32_t bar = peer_smem(smem_u32(&full[stage]), 0);
-          const int k = t.k0 + kb;
-          if constexpr (DIR == GROUPED_FWD) {
-            tma_load_3d_pair(ma, bar, sa, k, fr, t.e);
-            tma_load_2d_pair(mb, bar, sb, k, cr);
-          } else if constexpr (DIR == GROUPED_DGRAD) {
-            tma_load_3d_pair(ma, bar, sa, fr, k, t.e);
-            tma_load_3d_pair(ma, bar, sa + 8192, fr + 64, k, t.e);
-            tma_load_2d_pair(mb, bar, sb, k, cr);
-          } else {
-            tma_load_2d_pair(ma, bar, sa, fr, k);
-            tma_load_2d_pair(ma, bar, sa + 8192, fr + 64, k);
-            tma_load_2d_pair(mb, bar, sb, cr, k);
-            if (half > 64) tma_load_2d_pair(mb, bar, sb + 8192, cr + 64, k);
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b) {
+            if (b >= blocks) break;
+            uint8_t *sa = smem + stage * kStageBytes + b * kBlockBytes, *sb = sa + 16384;
+            const int k = t.k0 + kb + 64 * b;
+            if constexpr (DIR == GROUPED_FWD) {
+              tma_load_3d_pair(ma, bar, sa, k, fr, t.e);
+              tma_load_2d_pair(mb, bar, sb, k, cr);
+            } else if constexpr (DIR == GROUPED_DGRAD) {
+              tma_load_3d_pair(ma, bar, sa, fr, k, t.e);
+              tma_load_3d_pair(ma, bar, sa + 8192, fr + 64, k, t.e);
+              tma_load_2d_pair(mb, bar, sb, k, cr);
+            } else {
+              tma_load_2d_pair(ma, bar, sa, fr, k);
+              tma_load_2d_pair(ma, bar, sa + 8192, fr + 64, k);
+              tma_load_2d_pair(mb, bar, sb, cr, k);
+              if (half > 64) tma_load_2d_pair(mb, bar, sb + 8192, cr + 64, k);
+            }
           }
           if (++stage == kStages) {
             stage = 0;
@@ -329,19 +337,20 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
         tc_fence_after();
         const uint32_t dt = tmem + static_cast<uint32_t>(acc * 256);
         const uint32_t idesc = tc_idesc<DIR>(g.dtype, t.n);
-        for (int kb = 0; kb < t.klen; kb += 64) {
+        for (int kb = 0; kb < t.klen; kb += 64 * kBlocks) {
           if (!mbar_wait(&full[stage], ph, abort_flag, g.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * kStageBytes), sb = sa + 16384;
+          const uint32_t sa0 = smem_u32(smem + stage * kStageBytes);
           const int left = t.klen - kb;  // steps past the end hold zeros in both operands
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < 4 * kBlocks; ++k) {
             if (k * 16 < left) {
-              const uint64_t ad = DIR == GROUPED_FWD ? sw128_desc(sa + 32 * k) : mn_desc(sa + 2048 * k);
-              const uint64_t bd = DIR == GROUPED_WGRAD ? mn_desc(sb + 2048 * k) : sw128_desc(sb + 32 * k);
+              const uint32_t sa = sa0 + (k >> 2) * kBlockBytes, sb = sa + 16384;
+              const uint64_t ad = DIR == GROUPED_FWD ? sw128_desc(sa + 32 * (k & 3)) : mn_desc(sa + 2048 * (k & 3));
+              const uint64_t bd = DIR == GROUPED_WGRAD ? mn_desc(sb + 2048 * (k & 3)) : sw128_desc(sb + 32 * (k & 3));
               mma_bf16_pair(dt, ad, bd, idesc, (kb | k) ? 1u : 0u);
             }
           }
