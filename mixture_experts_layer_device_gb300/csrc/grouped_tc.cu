@@ -20,7 +20,7 @@
 //
 // Roles per CTA (320 threads): TMA producer, MMA issuer (leader CTA), eight
 // epilogue warps (two per quarter of the accumulator's rows: one alone works on
-// its instructions' latencies); six 32 KB stages; two accumulators of 256 TMEM columns, so a
+// its instructions' latencies); three 64 KB stages; two accumulators of 256 TMEM columns, so a
 // tile's epilogue runs beside the next one's MMAs.  Persistent: pair c takes
 // tiles c, c + pairs, ...  Every wait is bounded (mbar_wait).
 #include "elem.cuh"
@@ -35,20 +35,17 @@ namespace {
 constexpr int kBlockBytes = 32768;           // 64 reduction steps: 16 KB of A, up to 16 KB of B
 constexpr int kThreads = 320;
 constexpr int kEpilogueWarps = 8;
+constexpr int kStaging = 4096;               // per epilogue warp
 
-template <int DIR>
-struct TcShape {
-  static constexpr int BLOCKS = DIR == GROUPED_WGRAD ? 1 : 2;  // blocks of 64 reduction steps per stage
-  static constexpr int STAGES = DIR == GROUPED_WGRAD ? 5 : 3;
-  static constexpr int STAGE_BYTES = BLOCKS * kBlockBytes;
-  static constexpr int STAGING = DIR == GROUPED_WGRAD ? 8192 : 4096;  // per epilogue warp
-  static constexpr size_t SMEM = 1024 + STAGES * STAGE_BYTES + kEpilogueWarps * STAGING + (2 * STAGES + 5) * 8 + 16;
-  static_assert(SMEM <= 232448, "shared memory");
-};
+constexpr int kBlocks = 2;                   // blocks per stage: a stage's barriers cost some 300 cycles whatever it holds
+constexpr int kStages = 3;
+constexpr int kStageBytes = kBlocks * kBlockBytes;
+constexpr size_t kSmem = 1024 + kStages * kStageBytes + kEpilogueWarps * kStaging + (2 * kStages + 5) * 8 + 16;
+static_assert(kSmem <= 232448, "shared memory");
 // Forward and dgrad stage 2 KB per warp and keep the tile table in the rest of
 // the staging; more experts than it holds take the plan launch's table.
 constexpr int kTablePlace = kEpilogueWarps * 2048;
-constexpr int kTableExperts = ((kEpilogueWarps * TcShape<GROUPED_FWD>::STAGING - kTablePlace) / 4 - 3) / 3;
+constexpr int kTableExperts = ((kEpilogueWarps * kStaging - kTablePlace) / 4 - 3) / 3;
 
 struct TcMaps {
   CUtensorMap a;        // forward, dgrad: w
@@ -187,10 +184,11 @@ MOE_DEV void put_tokens(const float *v, uint8_t *buf, T *out, long ld, int token
 
 // A piece of 32 rows x 128 bytes of dw (lane = row) into 128-byte-swizzled shared
 // memory and out by TMA (or added to what is there), which clips it to the
-// expert's matrix.  Two buffers per warp: the piece before last has left when
-// this one is written.
+// expert's matrix.  (As 16-byte stores of the lanes instead: 572 us where this is 506,
+// 8192 rows and 128 experts of [2048, 4096].  A second buffer per warp in place of
+// the third stage: 809 us where this is 768, 32768 skewed rows, 64 of [7168, 2048].)
 MOE_DEV void put_rows(const uint32_t *w, uint8_t *buf, const CUtensorMap *map, bool add, int col, int row, int e, int lane) {
-  if (lane == 0) bulk_wait_read<1>();
+  if (lane == 0) bulk_wait_read<0>();  // the last piece has left the buffer
   __syncwarp();
 #pragma unroll
   for (int j = 0; j < 8; ++j)
@@ -208,8 +206,6 @@ MOE_DEV void put_rows(const uint32_t *w, uint8_t *buf, const CUtensorMap *map, b
 // T: the operands' type; WIDE: fp32 output (y or dw).
 template <int DIR, typename T, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_constant__ TcMaps maps, const GroupedArgs g) {
-  constexpr int kStages = TcShape<DIR>::STAGES, kStaging = TcShape<DIR>::STAGING, kBlocks = TcShape<DIR>::BLOCKS,
-                kStageBytes = TcShape<DIR>::STAGE_BYTES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
@@ -375,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
     // ------------------------------------------------ epilogue (warps 2..9, both CTAs)
     const int q = warp & 3, half = (warp - 2) >> 2;  // accumulator rows; which of the pieces of 32 columns
     uint8_t *buf = staging + (warp - 2) * (DIR == GROUPED_WGRAD ? kStaging : 2048);
-    int acc = 0, piece = 0;
+    int acc = 0;
     uint32_t aph = 0;
     if constexpr (DIR != GROUPED_WGRAD) {
       // zeros for the rows of no expert (the plan launch has done it otherwise)
@@ -431,8 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
             if constexpr (WIDE) w[i] = r[i];
             else w[i] = Elem<T>::pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
           if (fr >= g.N || t.c0 + j >= g.K) continue;
-          put_rows(w, buf + (piece & 1) * 4096, &maps.out, WIDE && g.accumulate, t.c0 + j, fr, t.e, lane);
-          ++piece;
+          put_rows(w, buf, &maps.out, WIDE && g.accumulate, t.c0 + j, fr, t.e, lane);
         }
       } else {
         const int F = DIR == GROUPED_DGRAD ? g.K : g.N;
@@ -550,12 +545,12 @@ template <int DIR, typename T, bool WIDE>
 int tc_clusters_query() {
   const auto kernel = grouped_tc_kernel<DIR, T, WIDE>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(TcShape<DIR>::SMEM)) != cudaSuccess)
+                           static_cast<int>(kSmem)) != cudaSuccess)
     return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = TcShape<DIR>::SMEM;
+  cfg.dynamicSmemBytes = kSmem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
@@ -576,7 +571,7 @@ cudaError_t launch_tc_one(const TcMaps &maps, const GroupedArgs &g, long units, 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * static_cast<unsigned>(units < most ? units : most), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = TcShape<DIR>::SMEM;
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
