@@ -142,8 +142,8 @@ def _stream(stream):
         if _current_stream is None:
             import torch
             raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # the same handle, without the Stream object
-            _current_stream = (lambda: raw(torch.cuda.current_device())) if raw else \
-                (lambda: torch.cuda.current_stream().cuda_stream)
+            device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+            _current_stream = (lambda: raw(device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
         return _current_stream()
     if isinstance(stream, int):
         return stream

@@ -8,14 +8,13 @@ from torch and call the library; all arithmetic runs in its kernels.  They run
 on torch's current stream, or on `stream`, and do not synchronise.  The
 autograd functions and modules over them are in module.py.
 """
+import ctypes
 from functools import lru_cache
 
 import torch
 
 from . import (GATES, MOE_ELEM_BF16, MOE_ELEM_FP16, MOE_ELEM_FP32, MOE_NORM_POST, MOE_NORM_PRE, MoeEmbedConfig,
-               MoeGroupedConfig, MoeNormConfig, check, moe_embed_backward, moe_embed_forward,
-               moe_embed_workspace_bytes, moe_get_status, moe_grouped_backward, moe_grouped_forward,
-               moe_grouped_workspace_bytes, moe_norm_backward, moe_norm_forward, moe_norm_workspace_bytes)
+               MoeGroupedConfig, MoeNormConfig, _stream, check, lib, moe_get_status)
 
 _ELEM = {torch.bfloat16: MOE_ELEM_BF16, torch.float16: MOE_ELEM_FP16, torch.float32: MOE_ELEM_FP32}
 
@@ -58,16 +57,25 @@ def _vector(t, name, n, dtype):
     return t.contiguous()
 
 
-def _ws(nbytes, device):
-    if nbytes <= 0:
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _plan(cfg, workspace_bytes):
+    """(the config, a reference to it for the library's calls, the call's workspace
+    bytes): what depends on sizes, types and strides alone, kept for the next call."""
+    ref = ctypes.byref(cfg)
+    return cfg, ref, workspace_bytes(ref) if workspace_bytes else 0
+
+
+def _ws(plan, device):
+    if plan[2] <= 0:
         _bad("the library does not take these sizes")
-    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return torch.empty(plan[2], dtype=torch.uint8, device=device)
 
 
 def _used_on(stream, *tensors):
     """Memory from the current stream's pool that a call on another stream uses."""
-    if stream is None:
-        return
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream)
     for t in tensors:
@@ -77,11 +85,11 @@ def _used_on(stream, *tensors):
 
 # ---------------------------------------------------------------- grouped products
 @lru_cache(maxsize=512)
-def _grouped_config(*fields):
-    return MoeGroupedConfig(*fields)
+def _grouped_plan(*fields):
+    return _plan(MoeGroupedConfig(*fields), lib().moe_grouped_workspace_bytes)
 
 
-def _grouped(x_rows, x_dtype, w, offsets, name):
+def _grouped(x_dtype, w, offsets, name):
     if not (x_dtype in (torch.bfloat16, torch.float16)):
         _bad("%s must be bfloat16 or float16", name)
     if not (w.dim() == 3 and w.dtype == x_dtype and w.is_cuda):
@@ -100,17 +108,19 @@ def grouped_forward(x, w, offsets, *, out=None, out_dtype=None, return_workspace
     of expert e (0 for a row of no expert).  x [rows, K] and w [E, N, K] bf16 or
     fp16, offsets int32 [E + 1] on the GPU as moe_route writes them; y of x's
     type or fp32 (out_dtype, or out's)."""
-    w, offsets, E, N, K, ld_w = _grouped(None, x.dtype, w, offsets, "x")
+    w, offsets, E, N, K, ld_w = _grouped(x.dtype, w, offsets, "x")
     x, ld_x = _rows(x, "x", K)
     out_dtype = out_dtype or (out.dtype if out is not None else x.dtype)
     if not (out_dtype in (x.dtype, torch.float32)):
         _bad("y is of x's type or float32")
     y, ld_y = _out(out, "out", x.shape[0], N, out_dtype, x.device)
     ld_e = w.stride(0) if E > 1 else 0
-    cfg = _grouped_config(x.shape[0], E, N, K, _ELEM[x.dtype], _ELEM[out_dtype], 0, ld_x, ld_y, ld_w, ld_e)
-    ws = _ws(moe_grouped_workspace_bytes(cfg), x.device)
-    check(moe_grouped_forward(cfg, x, w, offsets, y, ws, stream))
-    _used_on(stream, x, w, offsets, y, ws)
+    plan = _grouped_plan(x.shape[0], E, N, K, _ELEM[x.dtype], _ELEM[out_dtype], 0, ld_x, ld_y, ld_w, ld_e)
+    ws = _ws(plan, x.device)
+    check(lib().moe_grouped_forward(plan[1], x.data_ptr(), w.data_ptr(), offsets.data_ptr(), y.data_ptr(),
+                                    ws.data_ptr(), _stream(stream)))
+    if stream is not None:
+        _used_on(stream, x, w, offsets, y, ws)
     return (y, ws) if return_workspace else y
 
 
@@ -120,7 +130,7 @@ def grouped_backward(dy, x, w, offsets, *, dx=None, dw=None, need_dx=True, need_
     sum of dy[r]^T x[r] over e's rows (zeros for an expert without rows), either
     None when not needed.  dw is of x's type or fp32 (dw_dtype, or dw's); with
     accumulate it must be given, fp32, and is added to."""
-    w, offsets, E, N, K, ld_w = _grouped(None, dy.dtype, w, offsets, "dy")
+    w, offsets, E, N, K, ld_w = _grouped(dy.dtype, w, offsets, "dy")
     rows = dy.shape[0]
     dy, ld_y = _rows(dy, "dy", N)
     x, ld_x = _rows(x, "x", K, dy.dtype, rows)
@@ -133,7 +143,8 @@ def grouped_backward(dy, x, w, offsets, *, dx=None, dw=None, need_dx=True, need_
         _bad("nothing to compute")
     if need_dx:
         if dx is None:      # of x's row stride, which the library shares between the two
-            dx = torch.empty((rows, ld_x), dtype=dy.dtype, device=dy.device)[:, :K]
+            dx = torch.empty((rows, ld_x), dtype=dy.dtype, device=dy.device)
+            dx = dx if ld_x == K else dx[:, :K]
         if not (dx.shape == (rows, K) and dx.dtype == dy.dtype and dx.is_cuda and (K == 1 or dx.stride(1) == 1)):
             _bad("dx must be a %s GPU matrix [%d, %d] with contiguous rows", dy.dtype, rows, K)
         if rows > 1 and dx.stride(0) != ld_x:
@@ -146,11 +157,13 @@ def grouped_backward(dy, x, w, offsets, *, dx=None, dw=None, need_dx=True, need_
         if not (dw.shape == (E, N, K) and dw.dtype == dw_dtype and dw.is_cuda and dw.is_contiguous()):
             _bad("dw must be a contiguous %s GPU tensor [%d, %d, %d]", dw_dtype, E, N, K)
     ld_e = w.stride(0) if E > 1 else 0
-    cfg = _grouped_config(rows, E, N, K, _ELEM[dy.dtype], _ELEM[dw_dtype], int(accumulate), ld_x, ld_y, ld_w, ld_e)
-    ws = _ws(moe_grouped_workspace_bytes(cfg), dy.device)
+    plan = _grouped_plan(rows, E, N, K, _ELEM[dy.dtype], _ELEM[dw_dtype], int(accumulate), ld_x, ld_y, ld_w, ld_e)
+    ws = _ws(plan, dy.device)
     out = (dx if need_dx else None, dw if need_dw else None)
-    check(moe_grouped_backward(cfg, dy, x, w, offsets, out[0], out[1], ws, stream))
-    _used_on(stream, dy, x, w, offsets, out[0], out[1], ws)
+    check(lib().moe_grouped_backward(plan[1], dy.data_ptr(), x.data_ptr(), w.data_ptr(), offsets.data_ptr(),
+                                     _ptr(out[0]), _ptr(out[1]), ws.data_ptr(), _stream(stream)))
+    if stream is not None:
+        _used_on(stream, dy, x, w, offsets, out[0], out[1], ws)
     return out + (ws,) if return_workspace else out
 
 
@@ -162,8 +175,8 @@ def grouped_status(ws, stream=None):
 
 # ---------------------------------------------------------------- block norms
 @lru_cache(maxsize=512)
-def _norm_config(*fields):
-    return MoeNormConfig(*fields)
+def _norm_plan(*fields):
+    return _plan(MoeNormConfig(*fields), lib().moe_norm_workspace_bytes)
 
 
 def _gate(gate, kind, rows, d, dtype):
@@ -209,11 +222,13 @@ def norm_forward(x, f=None, gate=None, w_post=None, w_pre=None, *, gate_kind="no
         r_pre = torch.empty(rows, dtype=torch.float32, device=dev)
     if post:
         r_post = torch.empty(rows, dtype=torch.float32, device=dev)
-    cfg = _norm_config(rows, d, _ELEM[x.dtype], (MOE_NORM_POST if post else 0) | (MOE_NORM_PRE if pre else 0),
-                       GATES[gate_kind], alpha, eps, ld_x, ld_f, ld_z, ld_h, ld_g)
+    plan = _norm_plan(rows, d, _ELEM[x.dtype], (MOE_NORM_POST if post else 0) | (MOE_NORM_PRE if pre else 0),
+                      GATES[gate_kind], alpha, eps, ld_x, ld_f, ld_z, ld_h, ld_g)
     z, h = z if need_z else None, h if pre else None
-    check(moe_norm_forward(cfg, x, f, gate, w_post, w_pre, z, h, r_post, r_pre, stream))
-    _used_on(stream, x, f, gate, w_post, w_pre, z, h, r_post, r_pre)
+    check(lib().moe_norm_forward(plan[1], x.data_ptr(), _ptr(f), _ptr(gate), _ptr(w_post), _ptr(w_pre), _ptr(z),
+                                 _ptr(h), _ptr(r_post), _ptr(r_pre), _stream(stream)))
+    if stream is not None:
+        _used_on(stream, x, f, gate, w_post, w_pre, z, h, r_post, r_pre)
     return z, h, r_post, r_pre
 
 
@@ -252,36 +267,38 @@ def norm_backward(dz, dh, z, f=None, gate=None, w_post=None, w_pre=None, r_post=
     w_post = _vector(w_post, "w_post", d, dt) if post else None
     w_pre = _vector(w_pre, "w_pre", d, dt) if pre else None
 
-    def new(need, *shape):
-        return torch.empty(shape, dtype=dt, device=dev) if need else None
-
-    dx = new(need_dx, rows, d)
+    dx = torch.empty((rows, d), dtype=dt, device=dev) if need_dx else None
     df = dgate = None
     if f is not None and need_df:       # shares f's row stride
-        df = torch.empty((rows, ld_f), dtype=dt, device=dev)[:, :d]
+        df = torch.empty((rows, ld_f), dtype=dt, device=dev)
+        if ld_f != d:
+            df = df[:, :d]
     if gate is not None and need_dgate:
-        dgate = torch.empty((rows, ld_g), dtype=dt, device=dev)[:, :d] if gate_kind == "full" else \
+        dgate = torch.empty((rows, ld_g), dtype=dt, device=dev)[:, :d] if gate_kind == "full" and ld_g != d else \
             torch.empty_like(gate)
-    dw_post, dw_pre = new(need_dw and w_post is not None, d), new(need_dw and w_pre is not None, d)
-    cfg = _norm_config(rows, d, _ELEM[dt], (MOE_NORM_POST if post else 0) | (MOE_NORM_PRE if pre else 0),
-                       GATES[gate_kind], alpha, 0.0, d, ld_f, ld_z, ld_h, ld_g)
-    ws = _ws(moe_norm_workspace_bytes(cfg), dev)
-    check(moe_norm_backward(cfg, dz, dh, z, f, gate, w_post, w_pre, r_post, r_pre, dx, df, dgate, dw_post, dw_pre, ws,
-                            stream))
-    _used_on(stream, dz, dh, z, f, gate, w_post, w_pre, r_post, r_pre, dx, df, dgate, dw_post, dw_pre, ws)
+    dw_post = torch.empty_like(w_post) if need_dw and w_post is not None else None
+    dw_pre = torch.empty_like(w_pre) if need_dw and w_pre is not None else None
+    plan = _norm_plan(rows, d, _ELEM[dt], (MOE_NORM_POST if post else 0) | (MOE_NORM_PRE if pre else 0),
+                      GATES[gate_kind], alpha, 0.0, d, ld_f, ld_z, ld_h, ld_g)
+    ws = _ws(plan, dev)
+    check(lib().moe_norm_backward(plan[1], _ptr(dz), _ptr(dh), _ptr(z), _ptr(f), _ptr(gate), _ptr(w_post),
+                                  _ptr(w_pre), _ptr(r_post), _ptr(r_pre), _ptr(dx), _ptr(df), _ptr(dgate),
+                                  _ptr(dw_post), _ptr(dw_pre), ws.data_ptr(), _stream(stream)))
+    if stream is not None:
+        _used_on(stream, dz, dh, z, f, gate, w_post, w_pre, r_post, r_pre, dx, df, dgate, dw_post, dw_pre, ws)
     return dx, df, dgate, dw_post, dw_pre
 
 
 # ---------------------------------------------------------------- embedding
 @lru_cache(maxsize=512)
-def _embed_config(*fields):
-    return MoeEmbedConfig(*fields)
+def _embed_plan(*fields):
+    return _plan(MoeEmbedConfig(*fields), lib().moe_embed_workspace_bytes)
 
 
 def _ids(ids):
     if not (ids.dtype in (torch.int32, torch.int64) and ids.is_cuda):
         _bad("ids must be int32 or int64 on the GPU")
-    return ids.reshape(-1).contiguous()
+    return ids if ids.dim() == 1 and ids.is_contiguous() else ids.reshape(-1).contiguous()
 
 
 def embed_forward(ids, table, *, scale=1.0, out=None, stream=None):
@@ -295,10 +312,11 @@ def embed_forward(ids, table, *, scale=1.0, out=None, stream=None):
     flat = _ids(ids)
     rows, el = flat.shape[0], _ELEM[table.dtype]
     res, ld_o = _out(out, "out", rows, d, table.dtype, table.device)
-    cfg = _embed_config(rows, V, d, el, el, int(flat.dtype == torch.int64), 0, scale, ld_t, ld_o)
-    check(moe_embed_forward(cfg, flat, table, res, stream))
-    _used_on(stream, flat, table, res)
-    return res if out is not None else res.view(*ids.shape, d)
+    plan = _embed_plan(rows, V, d, el, el, int(flat.dtype == torch.int64), 0, scale, ld_t, ld_o)
+    check(lib().moe_embed_forward(plan[1], flat.data_ptr(), table.data_ptr(), res.data_ptr(), _stream(stream)))
+    if stream is not None:
+        _used_on(stream, flat, table, res)
+    return res if out is not None or ids.dim() == 1 else res.view(*ids.shape, d)
 
 
 def embed_backward(ids, dout, V, *, scale=1.0, dtable=None, grad_dtype=None, accumulate=False, stream=None):
@@ -319,9 +337,11 @@ def embed_backward(ids, dout, V, *, scale=1.0, dtable=None, grad_dtype=None, acc
     if not (grad_dtype in (dout.dtype, torch.float32)):
         _bad("dtable is of dout's type or float32")
     dtable, ld_t = _out(dtable, "dtable", V, d, grad_dtype, dout.device)
-    cfg = _embed_config(flat.shape[0], V, d, _ELEM[dout.dtype], _ELEM[grad_dtype], int(flat.dtype == torch.int64),
-                        int(accumulate), scale, ld_t, ld_o)
-    ws = _ws(moe_embed_workspace_bytes(cfg), dout.device)
-    check(moe_embed_backward(cfg, flat, dout, dtable, ws, stream))
-    _used_on(stream, flat, dout, dtable, ws)
+    plan = _embed_plan(flat.shape[0], V, d, _ELEM[dout.dtype], _ELEM[grad_dtype], int(flat.dtype == torch.int64),
+                       int(accumulate), scale, ld_t, ld_o)
+    ws = _ws(plan, dout.device)
+    check(lib().moe_embed_backward(plan[1], flat.data_ptr(), dout.data_ptr(), dtable.data_ptr(), ws.data_ptr(),
+                                   _stream(stream)))
+    if stream is not None:
+        _used_on(stream, flat, dout, dtable, ws)
     return dtable
