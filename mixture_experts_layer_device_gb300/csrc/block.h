@@ -38,9 +38,11 @@ struct GroupedArgs {
   int dtype, out_dtype;  // moe_elem; out_dtype of y / dw (dx has dtype)
   int accumulate;
   long ld_x, ld_y, ld_w, ld_e;
+  long in_x, in_y;     // tensor-core path: row strides of the inputs x and dy (padded copies have their own)
   const int *offsets;  // [E + 1]
   const void *x, *w, *dy;
   void *y, *dx, *dw;
+  bool vec_out;  // tensor-core path: the output's rows are whole 16-byte pieces
   int *status;   // workspace status word
   int *tiles;    // workspace: the plan's tile table (3 E + 3 ints)
   int *order;    // workspace: the experts by descending rows (weight gradient)
@@ -58,7 +60,12 @@ cudaError_t launch_grouped_plan(const GroupedArgs &g, int tile_rows, void *out, 
 cudaError_t launch_grouped_plain(const GroupedArgs &g, int dir, bool first, cudaStream_t s);
 // Forward of a few rows (no plan needed): 16-byte aligned rows of x and w.
 cudaError_t launch_grouped_few(const GroupedArgs &g, cudaStream_t s);
-// Tensor-core path: every pointer and row stride a multiple of 16 bytes.
+// dst [n rows of `cols`, stride ld_dst >= cols] = src with its row stride, zeros
+// beyond cols; `experts`: rows of w (N per expert, ld_e apart), experts without
+// rows left out.  2-byte elements.
+cudaError_t launch_grouped_pad(const GroupedArgs &g, const void *src, long rows, int cols, long ld, bool experts,
+                               void *dst, long ld_dst, cudaStream_t s);
+// Tensor-core path: the operands' pointers and row strides multiples of 16 bytes.
 cudaError_t launch_grouped_tc(const GroupedArgs &g, int dir, cudaStream_t s);
 
 // ---------------------------------------------------------------- block norms

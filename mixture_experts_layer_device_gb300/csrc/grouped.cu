@@ -371,7 +371,44 @@ __global__ void __launch_bounds__(FEW_WARPS * 32) grouped_few_kernel(const Group
   }
 }
 
+// ---------------------------------------------------------------- padded copies
+// Rows at odd strides into rows that TMA can address: a thread per 8 elements.
+__global__ void __launch_bounds__(256) grouped_pad_kernel(const GroupedArgs g, const uint16_t *src, long rows, int cols,
+                                                          long ld, bool experts, uint16_t *dst, long ld_dst) {
+  const int chunks = static_cast<int>(ld_dst >> 3);
+  const long total = rows * chunks;
+  for (long u = static_cast<long>(blockIdx.x) * blockDim.x + threadIdx.x; u < total;
+       u += static_cast<long>(gridDim.x) * blockDim.x) {
+    const long row = u / chunks;
+    const int c = static_cast<int>(u - row * chunks) * 8;
+    const uint16_t *p = src + row * ld + c;
+    if (experts) {
+      const int e = static_cast<int>(row / g.N);
+      int lo, hi;
+      group_rows(g, e, lo, hi);
+      if (lo == hi) continue;
+      p = src + e * g.ld_e + (row - static_cast<long>(e) * g.N) * ld + c;
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t a = c + 2 * k < cols ? p[2 * k] : 0u, b = c + 2 * k + 1 < cols ? p[2 * k + 1] : 0u;
+      w[k] = a | (b << 16);
+    }
+    *reinterpret_cast<uint4 *>(dst + row * ld_dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_grouped_pad(const GroupedArgs &g, const void *src, long rows, int cols, long ld, bool experts,
+                               void *dst, long ld_dst, cudaStream_t s) {
+  HostTrace t("grouped_pad", s);
+  const long want = (rows * (ld_dst >> 3) + 255) / 256;
+  grouped_pad_kernel<<<static_cast<unsigned>(want < 152 * 32 ? want : 152 * 32), 256, 0, s>>>(
+      g, static_cast<const uint16_t *>(src), rows, cols, ld, experts, static_cast<uint16_t *>(dst), ld_dst);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_grouped_few(const GroupedArgs &g, cudaStream_t s) {
   HostTrace t("grouped_few", s);

@@ -23,6 +23,8 @@
 // its instructions' latencies); three 64 KB stages; two accumulators of 256 TMEM columns, so a
 // tile's epilogue runs beside the next one's MMAs.  Persistent: pair c takes
 // tiles c, c + pairs, ...  Every wait is bounded (mbar_wait).
+#include <type_traits>
+
 #include "elem.cuh"
 #include "gemm_common.cuh"
 #include "grouped.cuh"
@@ -201,6 +203,29 @@ MOE_DEV void put_rows(const uint32_t *w, uint8_t *buf, const CUtensorMap *map, b
     else tma_store_3d(map, buf, col, row, e);
     bulk_commit();
   }
+}
+
+// The same piece element by element, for matrices whose rows are no whole 16-byte
+// pieces: each store takes neighbouring columns of one row.
+template <typename O>
+MOE_DEV void put_elements(const uint32_t *w, uint8_t *buf, O *out, long ld, int rows, int cols, bool add, int lane) {
+  constexpr int COLS = 128 / sizeof(O);
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<uint4 *>(buf + lane * 128 + ((j ^ (lane & 7)) * 16)) =
+        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  __syncwarp();
+  for (int r = 0; r < 32 && r < rows; ++r)
+#pragma unroll
+    for (int c = lane; c < COLS; c += 32) {
+      const int byte = c * static_cast<int>(sizeof(O));
+      const O v = *reinterpret_cast<const O *>(buf + r * 128 + (((byte >> 4) ^ (r & 7)) * 16) + (byte & 15));
+      if (c < cols) {
+        if constexpr (sizeof(O) == 4) out[r * ld + c] = add ? out[r * ld + c] + v : v;
+        else out[r * ld + c] = v;
+      }
+    }
 }
 
 // T: the operands' type; WIDE: fp32 output (y or dw).
@@ -382,9 +407,15 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
       const long ld = (DIR == GROUPED_DGRAD ? g.ld_x : g.ld_y) * (WIDE ? 4 : 2);
       const int bytes = (DIR == GROUPED_DGRAD ? g.K : g.N) * (WIDE ? 4 : 2);
       uint8_t *out = static_cast<uint8_t *>(DIR == GROUPED_DGRAD ? g.dx : g.y);
-      for (long i = blockIdx.x; i < outside; i += gridDim.x)
-        for (int b = (threadIdx.x - 64) * 16; b < bytes; b += 32 * kEpilogueWarps * 16)
-          *reinterpret_cast<uint4 *>(out + (i < lo ? i : hi_last + (i - lo)) * ld + b) = make_uint4(0, 0, 0, 0);
+      for (long i = blockIdx.x; i < outside; i += gridDim.x) {
+        uint8_t *row = out + (i < lo ? i : hi_last + (i - lo)) * ld;
+        if (g.vec_out) {
+          for (int b = (threadIdx.x - 64) * 16; b < bytes; b += 32 * kEpilogueWarps * 16)
+            *reinterpret_cast<uint4 *>(row + b) = make_uint4(0, 0, 0, 0);
+        } else {
+          for (int b = (threadIdx.x - 64) * 2; b < bytes; b += 32 * kEpilogueWarps * 2) *reinterpret_cast<uint16_t *>(row + b) = 0;
+        }
+      }
     }
     TcTile next = tiles.ahead(pair);
     for (int i = 0; tiles.unit(i, pair, pairs) < tiles.total; ++i) {
@@ -427,7 +458,13 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
             if constexpr (WIDE) w[i] = r[i];
             else w[i] = Elem<T>::pack2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
           if (fr >= g.N || t.c0 + j >= g.K) continue;
-          put_rows(w, buf, &maps.out, WIDE && g.accumulate, t.c0 + j, fr, t.e, lane);
+          if (g.vec_out) {
+            put_rows(w, buf, &maps.out, WIDE && g.accumulate, t.c0 + j, fr, t.e, lane);
+          } else {
+            using O = typename std::conditional<WIDE, float, T>::type;
+            put_elements<O>(w, buf, static_cast<O *>(g.dw) + (static_cast<long>(t.e) * g.N + fr) * g.K + t.c0 + j, g.K,
+                            g.N - fr, g.K - t.c0 - j, g.accumulate != 0, lane);
+          }
         }
       } else {
         const int F = DIR == GROUPED_DGRAD ? g.K : g.N;
@@ -451,8 +488,14 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
             for (int i = 0; i < 32; ++i)
               if (i < tokens && fr + lane < F) out[i * ld] = v[i];
           } else {
-            put_tokens(v, buf, static_cast<T *>(DIR == GROUPED_DGRAD ? g.dx : g.y) + row * ld + fr, ld, tokens, F - fr,
-                       lane);
+            T *out = static_cast<T *>(DIR == GROUPED_DGRAD ? g.dx : g.y) + row * ld + fr;
+            if (g.vec_out) {
+              put_tokens(v, buf, out, ld, tokens, F - fr, lane);
+            } else {  // rows that are no whole 16-byte pieces: 32 features of a token per store
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i < tokens && fr + lane < F) out[i * ld + lane] = Elem<T>::from(v[i]);
+            }
           }
         }
       }
@@ -462,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
         aph ^= 1u;
       }
     }
-    if (DIR == GROUPED_WGRAD && lane == 0) bulk_wait<0>();
+    if (DIR == GROUPED_WGRAD && g.vec_out && lane == 0) bulk_wait<0>();
   }
 
   __syncthreads();
@@ -621,12 +664,13 @@ cudaError_t launch_grouped_tc(const GroupedArgs &g, int dir, cudaStream_t s) {
     CUtensorMap dy, x;
     const uint64_t n[2] = {static_cast<uint64_t>(g.N), static_cast<uint64_t>(g.rows)};
     const uint64_t k[2] = {static_cast<uint64_t>(g.K), static_cast<uint64_t>(g.rows)};
-    const uint64_t sn[1] = {static_cast<uint64_t>(g.ld_y) * 2}, sk[1] = {static_cast<uint64_t>(g.ld_x) * 2};
+    const uint64_t sn[1] = {static_cast<uint64_t>(g.in_y) * 2}, sk[1] = {static_cast<uint64_t>(g.in_x) * 2};
     const uint32_t box[2] = {64, 64};
     if (!host_encode_map(&dy, g.dtype, g.dy, 2, n, sn, box) || !host_encode_map(&x, g.dtype, g.x, 2, k, sk, box) ||
-        !expert_map(&m.out, g.out_dtype, g.dw, g, g.K, static_cast<long>(g.N) * g.K, g.out_dtype == MOE_ELEM_FP32 ? 32 : 64,
-                    32))
+        (g.vec_out && !expert_map(&m.out, g.out_dtype, g.dw, g, g.K, static_cast<long>(g.N) * g.K, g.out_dtype == MOE_ELEM_FP32 ? 32 : 64,
+                                  32)))
       return cudaErrorInvalidValue;
+    if (!g.vec_out) m.out = dy;
     m.a = dy;  // the kernel takes its experts' maps from the workspace
     for (CUtensorMap &b : m.b) b = x;
     {
@@ -646,13 +690,13 @@ cudaError_t launch_grouped_tc(const GroupedArgs &g, int dir, cudaStream_t s) {
     if (e != cudaSuccess) return e;
   }
   if (dir == GROUPED_FWD) {
-    if (!row_maps(m.b, g.dtype, g.x, g.rows, g.K, g.ld_x) || !expert_map(&m.a, g.dtype, g.w, g, g.ld_w, g.ld_e, 64, 128))
+    if (!row_maps(m.b, g.dtype, g.x, g.rows, g.K, g.in_x) || !expert_map(&m.a, g.dtype, g.w, g, g.ld_w, g.ld_e, 64, 128))
       return cudaErrorInvalidValue;
       m.out = m.a;
     HostTrace t("grouped_forward", s);
     return launch_tc<GROUPED_FWD>(m, g, tokens * ((g.N + 255) / 256), s);
   }
-  if (!row_maps(m.b, g.dtype, g.dy, g.rows, g.N, g.ld_y) || !expert_map(&m.a, g.dtype, g.w, g, g.ld_w, g.ld_e, 64, 64))
+  if (!row_maps(m.b, g.dtype, g.dy, g.rows, g.N, g.in_y) || !expert_map(&m.a, g.dtype, g.w, g, g.ld_w, g.ld_e, 64, 64))
     return cudaErrorInvalidValue;
   m.out = m.a;
   HostTrace t("grouped_dgrad", s);

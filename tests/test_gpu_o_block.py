@@ -85,6 +85,9 @@ GROUPED = [
     (3000, 1, 64, 64, "one", 1, 2),
     (2600, 2000, 16, 64, "skew", 0, 0),
     (4000, 5, 72, 80, "skew", 0, 5),
+    (4000, 4, 301, 305, "skew", 2, 3),      # large and odd: padded copies
+    (4000, 4, 304, 305, "ends", 0, 1),
+    (4001, 5, 301, 304, "skew", 1, 0),
 ]
 
 
