@@ -9,9 +9,14 @@ weight preparation step of a training update.  Gradients pass straight through
 the MXFP8 quantisers, so the masters receive the gradients the library
 computes for the quantised layer.  Each training forward keeps its activations
 in its own buffer, so several forwards may precede their backwards.
+
+Around the layer: GroupedLinear (ragged products grouped by expert), BlockNorm
+(the norms around a block with its gate and residual scale) and TokenEmbedding,
+each an nn.Module over an autograd.Function over block.py.
 """
 import torch
 
+from . import block
 from .layer import MoELayer
 
 
@@ -92,3 +97,116 @@ class MoE(torch.nn.Module):
     def aux_loss(self):
         """The load-balancing loss of the last forward (0-d fp32 device tensor)."""
         return self.layer.view(1, "aux", "f32", (1,))[0]
+
+
+# ---------------------------------------------------------------- around the layer
+class GroupedFunction(torch.autograd.Function):
+    """y[r] = x[r] w[e]^T for the rows r of expert e (block.grouped_forward)."""
+
+    @staticmethod
+    def forward(ctx, x, w, offsets):
+        ctx.save_for_backward(x, w, offsets)
+        return block.grouped_forward(x, w, offsets)
+
+    @staticmethod
+    def backward(ctx, dy):
+        x, w, offsets = ctx.saved_tensors
+        need_dx, need_dw = ctx.needs_input_grad[:2]
+        dx = dw = None
+        if need_dx or need_dw:
+            dx, dw = block.grouped_backward(dy, x, w, offsets, need_dx=need_dx, need_dw=need_dw)
+        return dx, dw, None
+
+
+class GroupedLinear(torch.nn.Module):
+    """E bias-free linear maps K -> N over expert-sorted rows: forward(x [rows, K],
+    offsets int32 [E + 1]) -> [rows, N]; rows outside the offsets give zeros and
+    take no gradient.  Weight [E, N, K] bf16 (or fp16)."""
+
+    def __init__(self, E, N, K, dtype=torch.bfloat16, device="cuda"):
+        super().__init__()
+        self.weight = torch.nn.Parameter(torch.empty(E, N, K, dtype=dtype, device=device).normal_(0.0, K ** -0.5))
+
+    def forward(self, x, offsets):
+        return GroupedFunction.apply(x, self.weight, offsets)
+
+
+class BlockNormFunction(torch.autograd.Function):
+    """(z, h) of block.norm_forward; z is None without need_z, h without pre."""
+
+    @staticmethod
+    def forward(ctx, x, f, gate, w_post, w_pre, gate_kind, post, pre, alpha, eps):
+        post = post and f is not None
+        z, h, r_post, r_pre = block.norm_forward(x, f, gate, w_post, w_pre, gate_kind=gate_kind, post=post, pre=pre,
+                                                 alpha=alpha, eps=eps)
+        ctx.opts = dict(gate_kind=gate_kind, post=post, pre=pre, alpha=alpha)
+        ctx.save_for_backward(z if pre else None, f, gate, w_post, w_pre, r_post, r_pre)
+        ctx.set_materialize_grads(False)
+        return z, h
+
+    @staticmethod
+    def backward(ctx, dz, dh):
+        z, f, gate, w_post, w_pre, r_post, r_pre = ctx.saved_tensors
+        need, opts = ctx.needs_input_grad, dict(ctx.opts)
+        if dz is None and dh is None:
+            return (None,) * 10
+        if dh is None and opts["pre"]:      # only z was used: the pre norm has no part in it
+            opts["pre"], z, r_pre = False, None, None
+        dx, df, dgate, dw_post, dw_pre = block.norm_backward(
+            dz, dh, z, f, gate, w_post, w_pre if opts["pre"] else None, r_post, r_pre, need_dx=need[0], need_df=need[1],
+            need_dgate=need[2], need_dw=need[3] or need[4], **opts)
+        return (dx, df, dgate, dw_post if need[3] else None, dw_pre if need[4] else None) + (None,) * 5
+
+
+class BlockNorm(torch.nn.Module):
+    """What stands between two blocks, in one pass over the tokens:
+
+        z = alpha x + g * (w_post * f / rms(f)),   h = w_pre * z / rms(z)
+
+    forward(x, f=None, gate=None) -> (z, h): x [T, d] the residual stream, f [T,
+    d] the block's output (None: z = alpha x), h the next block's input.  post
+    and pre leave the norms in; gate "none", "channel" (a parameter [d], ones at
+    the start), "row" or "full" (given to forward, [T] or [T, d])."""
+
+    def __init__(self, d, post=True, pre=True, gate="none", alpha=1.0, eps=1e-6, dtype=torch.bfloat16, device="cuda"):
+        super().__init__()
+        ones = lambda on: torch.nn.Parameter(torch.ones(d, dtype=dtype, device=device)) if on else None  # noqa: E731
+        self.w_post, self.w_pre, self.w_gate = ones(post), ones(pre), ones(gate == "channel")
+        self.post, self.pre, self.gate, self.alpha, self.eps = post, pre, gate, alpha, eps
+
+    def forward(self, x, f=None, gate=None):
+        kind = self.gate if f is not None else "none"
+        if (gate is not None) != (kind in ("row", "full")):
+            raise ValueError("pass a gate exactly when the module's kind is row or full and f is given")
+        if kind == "channel":
+            gate = self.w_gate
+        return BlockNormFunction.apply(x, f, gate, self.w_post if f is not None else None, self.w_pre, kind, self.post,
+                                       self.pre, self.alpha, self.eps)
+
+
+class EmbeddingFunction(torch.autograd.Function):
+    """scale * table[ids] (block.embed_forward), its gradient by sorted tokens."""
+
+    @staticmethod
+    def forward(ctx, ids, table, scale):
+        ctx.save_for_backward(ids)
+        ctx.V, ctx.scale = table.shape[0], scale
+        return block.embed_forward(ids, table, scale=scale)
+
+    @staticmethod
+    def backward(ctx, dout):
+        ids, = ctx.saved_tensors
+        return None, block.embed_backward(ids, dout, ctx.V, scale=ctx.scale), None
+
+
+class TokenEmbedding(torch.nn.Module):
+    """forward(ids) = scale * weight[ids]; an id outside [0, V) (padding) gives zeros
+    and takes no gradient.  Weight [V, d]; the gradient is dense."""
+
+    def __init__(self, V, d, scale=1.0, dtype=torch.bfloat16, device="cuda"):
+        super().__init__()
+        self.weight = torch.nn.Parameter(torch.empty(V, d, dtype=dtype, device=device).normal_(0.0, 0.02))
+        self.scale = scale
+
+    def forward(self, ids):
+        return EmbeddingFunction.apply(ids, self.weight, self.scale)
