@@ -11,6 +11,7 @@
 // token and the whole table out (or, accumulating, the rows that occur, twice).
 #include "block.h"
 #include "elem.cuh"
+#include "gemm_common.cuh"
 #include "kernels.h"
 
 namespace moe {
@@ -125,6 +126,134 @@ __global__ void __launch_bounds__(kRankBlock) embed_rank_kernel(const EmbedArgs 
   keys[rank] = key;
   pos[rank] = t;
   if (used && key < a.V) used[key] = 1;
+}
+
+// Up to 65,536 tokens: the whole radix sort in one launch of one cluster.  Each of
+// its eight blocks holds a consecutive piece of the list in shared memory; a pass
+// ranks the piece's keys (stable), adds up the digits' counts of all blocks
+// through distributed shared memory, and writes every key to its place in the
+// block that holds it.  One launch of 27 us in place of six of 31 us together, at
+// 32768 tokens and 18-bit keys.
+constexpr int kClusterBlocks = 8, kClusterThreads = 1024, kClusterItems = 8, kClusterDigits = 512;
+constexpr int kClusterSort = kClusterBlocks * kClusterThreads * kClusterItems;
+
+struct ClusterSmem {
+  int keys[2][kClusterThreads * kClusterItems], pos[2][kClusterThreads * kClusterItems];
+  uint16_t count[kClusterThreads / 32][kClusterDigits];  // per warp and digit: keys so far, then keys of the warps before
+  int total[kClusterDigits];                              // this block's keys of a digit
+  int base[kClusterDigits];                               // first place of this block's keys of a digit
+  int warp_sum[kClusterDigits / 32];
+};
+static_assert(sizeof(ClusterSmem) <= 232448, "shared memory");
+
+MOE_DEV int ld_cluster(uint32_t at) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+MOE_DEV void st_cluster(uint32_t at, int v) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+
+__global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kClusterThreads, 1)
+    embed_cluster_sort_kernel(const EmbedArgs a, int items, int passes, int bits, int *keys_out, int *pos_out, uint8_t *used) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  ClusterSmem &sm = *reinterpret_cast<ClusterSmem *>(smem_raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, digits = 1 << bits;
+  const uint32_t rank = cluster_rank();
+  const int piece = kClusterThreads * items, first = static_cast<int>(rank) * piece;
+  const int mine = warp * 32 * items + lane;  // a warp ranks 32 x items consecutive keys
+  for (int i = 0; i < items; ++i) {
+    const int at = mine + 32 * i, t = first + at;
+    int key = -1;
+    if (t < a.rows) {
+      key = key_of(a, t);
+      if (used && key < a.V) used[key] = 1;
+    }
+    sm.keys[0][at] = key;
+    sm.pos[0][at] = t;
+  }
+  for (int p = 0; p < passes; ++p) {
+    const int in = p & 1, shift = p * bits;
+    for (int i = threadIdx.x; i < (kClusterThreads / 32) * digits; i += kClusterThreads)
+      sm.count[i >> bits][i & (digits - 1)] = 0;
+    __syncthreads();
+    int key[kClusterItems], local[kClusterItems];
+#pragma unroll
+    for (int i = 0; i < kClusterItems; ++i) {
+      if (i >= items) break;
+      key[i] = sm.keys[in][mine + 32 * i];
+      const int dg = key[i] >= 0 ? (key[i] >> shift) & (digits - 1) : digits;  // places past the end: a group of their own
+      const unsigned same = __match_any_sync(0xffffffffu, dg);
+      const int before = __popc(same & ((1u << lane) - 1));
+      if (key[i] >= 0) local[i] = sm.count[warp][dg] + before;
+      __syncwarp();
+      if (key[i] >= 0 && before == 0) sm.count[warp][dg] += static_cast<uint16_t>(__popc(same));
+      __syncwarp();
+    }
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) < digits) {
+      int run = 0;
+#pragma unroll 8
+      for (int w = 0; w < kClusterThreads / 32; ++w) {
+        const int n = sm.count[w][threadIdx.x];
+        sm.count[w][threadIdx.x] = static_cast<uint16_t>(run);
+        run += n;
+      }
+      sm.total[threadIdx.x] = run;
+    }
+    cluster_sync();
+    // places of this block's keys: those of smaller digits anywhere, and of the same digit in the blocks before
+    int all = 0, before = 0;
+    if (static_cast<int>(threadIdx.x) < digits) {
+      const uint32_t at = smem_u32(&sm.total[threadIdx.x]);
+#pragma unroll
+      for (int c = 0; c < kClusterBlocks; ++c) {
+        const int n = ld_cluster(peer_smem(at, c));
+        all += n;
+        if (c < static_cast<int>(rank)) before += n;
+      }
+    }
+    int inc = all;
+    if (threadIdx.x < kClusterDigits) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int n = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += n;
+      }
+      if (lane == 31) sm.warp_sum[warp] = inc;
+    }
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) < digits) {
+      int at = before + inc - all;
+      for (int w = 0; w < warp; ++w) at += sm.warp_sum[w];
+      sm.base[threadIdx.x] = at;
+    }
+    __syncthreads();
+    const bool last = p + 1 == passes;
+#pragma unroll
+    for (int i = 0; i < kClusterItems; ++i) {
+      if (i >= items) break;
+      if (key[i] < 0) continue;
+      const int dg = (key[i] >> shift) & (digits - 1);
+      const int to = sm.base[dg] + sm.count[warp][dg] + local[i], ps = sm.pos[in][mine + 32 * i];
+      if (last) {
+        keys_out[to] = key[i];
+        pos_out[to] = ps;
+      } else {
+        const int block = to / piece, slot = to - block * piece;
+        st_cluster(peer_smem(smem_u32(&sm.keys[in ^ 1][slot]), block), key[i]);
+        st_cluster(peer_smem(smem_u32(&sm.pos[in ^ 1][slot]), block), ps);
+      }
+    }
+    if (!last) {
+      // places that no key takes: past the end of the list
+#pragma unroll
+      for (int i = 0; i < kClusterItems; ++i)
+        if (i < items && first + mine + 32 * i >= a.rows) sm.keys[in ^ 1][mine + 32 * i] = -1;
+    }
+    cluster_sync();  // the keys have arrived; no block leaves or reuses its counts while another reads them
+  }
 }
 
 // One digit of the least-significant-digit radix sort: histogram per block,
@@ -392,6 +521,13 @@ __global__ void __launch_bounds__(256) embed_join_kernel(const EmbedArgs a, cons
   }
 }
 
+// Bits of the keys 0 .. V.
+int key_bits(long V) {
+  int bits = 1;
+  while ((1L << bits) <= V) ++bits;
+  return bits;
+}
+
 struct EmbedWs {
   size_t keys[2], pos[2], hist, total, cross, used, part, bytes;
 };
@@ -504,9 +640,23 @@ cudaError_t launch_embed_backward(const EmbedArgs &a, int num_sms, cudaStream_t 
     HostTrace t("embed_rank", s);
     embed_rank_kernel<<<(a.rows + kRankBlock - 1) / kRankBlock, kRankBlock, 0, s>>>(a, keys[0], pos[0], used);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  } else if (a.rows > 0 && a.rows <= kClusterSort) {
+    HostTrace t("embed_sort", s);
+    const int bits = key_bits(a.V), passes = (bits + 8) / 9, per = (bits + passes - 1) / passes;
+    const int items = (a.rows + kClusterBlocks * kClusterThreads - 1) / (kClusterBlocks * kClusterThreads);
+    static int memo[64] = {};
+    if (per_device_memo(memo, []() {
+          return cudaFuncSetAttribute(embed_cluster_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      static_cast<int>(sizeof(ClusterSmem))) == cudaSuccess
+                     ? 1
+                     : 0;
+        }) <= 0)
+      return cudaErrorInvalidConfiguration;
+    embed_cluster_sort_kernel<<<kClusterBlocks, kClusterThreads, sizeof(ClusterSmem), s>>>(a, items, passes, per, keys[0], pos[0],
+                                                                                         used);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
   } else if (a.rows > 0) {
-    int bits = 1;
-    while ((1L << bits) <= a.V) ++bits;  // keys 0 .. V
+    const int bits = key_bits(a.V);
     const int passes = (bits + 9) / 10;
     const int per = (bits + passes - 1) / passes;
     const int blocks = (a.rows + kSortChunk - 1) / kSortChunk;

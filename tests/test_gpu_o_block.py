@@ -374,7 +374,7 @@ def test_norm_gradient_against_differences(blk):
 # ---------------------------------------------------------------- embedding
 EMBED = [(1, 1, 1), (1, 50, 64), (7, 3, 33), (64, 10, 128), (300, 1000, 72), (513, 97, 40), (2048, 5000, 24), (2049, 5000, 24),
          (5000, 70000, 16), (4097, 2, 264), (3000, 1, 8), (6000, 1100000, 3), (9000, 20000, 64),
-         (9001, 300, 37)]
+         (9001, 300, 37), (65536, 131, 8), (65537, 3000, 8), (70001, 1100000, 5)]
 
 
 @pytest.mark.parametrize("rows,V,d", EMBED)
@@ -454,3 +454,95 @@ def test_calls_run_on_the_given_stream(blk):
     s.synchronize()
     assert torch.equal(got[0], want) and all(torch.equal(a, b) for a, b in zip(got[1], nz))
     assert torch.equal(ee, e) and torch.equal(gg, ge)
+
+
+def test_calls_are_captured_in_a_graph(blk):
+    """One capture of every operator, replayed on new contents of its inputs."""
+    g = gen(1)
+    off = torch.tensor([0, 100, 100, 300], dtype=torch.int32, device="cuda")
+    x, dy, w = draw((300, 128), BF, g), draw((300, 64), BF, g), draw((3, 64, 128), BF, g)
+    wn, ids = draw((128,), BF, g), torch.randint(0, 40, (300,), generator=g, device="cuda")
+
+    def calls():
+        z, h, rq, rp = blk.norm_forward(x, x, None, wn, wn)
+        return (blk.grouped_forward(x, w, off), *blk.grouped_backward(dy, x, w, off), z, h,
+                *(t for t in blk.norm_backward(h, z, z, x, None, wn, wn, rq, rp) if t is not None),
+                blk.embed_forward(ids, x), blk.embed_backward(ids, x, 40))
+
+    calls()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = calls()
+    for seed in (5, 6):
+        g = gen(seed)
+        for t in (x, dy, w, wn):
+            t.copy_(draw(t.shape, t.dtype, g))
+        ids.copy_(torch.randint(-1, 41, (300,), generator=g, device="cuda"))
+        off.copy_(torch.tensor([[0, 7, 250, 290], [3, 3, 200, 300]][seed - 5], dtype=torch.int32))
+        graph.replay()
+        for a, b in zip(out, calls()):
+            assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- offsets past 32 bits
+def test_norm_past_32_bits(blk):
+    rows, d = 270000, 8192          # 2.2e9 elements a tensor
+    g = gen(2)
+    x = torch.empty((rows, d), dtype=BF, device="cuda").normal_(generator=g)
+    w = draw((d,), BF, g)
+    z, h, rq, rp = blk.norm_forward(x, x, None, w, w, eps=1e-5)
+    pick = torch.tensor([0, 1, 131071, 131072, 262143, 262144, 269999], device="cuda")
+    o = ob.norm_forward(f64(x[pick]), f64(x[pick]), None, f64(w), f64(w), eps=1e-5)
+    close(z[pick], o["z"], o["z_size"], d)
+    close(h[pick], o["h"], o["h_size"] * 4, d)
+    dx, df, _, _, _ = blk.norm_backward(x, h, z, x, None, w, w, rq, rp)
+    ref, size = ob.norm_backward(*(f64(t[pick]) for t in (x, h, z, x)), None, f64(w), f64(w), f64(rq[pick]), f64(rp[pick]))
+    close(dx[pick], ref["dx"], size["dx"], d)
+    close(df[pick], ref["df"], size["df"], d)
+
+
+def test_embedding_past_32_bits(blk):
+    V, d, rows = 300000, 8192, 3000
+    g = gen(3)
+    table = torch.empty((V, d), dtype=BF, device="cuda").normal_(generator=g)
+    ids = torch.randint(V - 1000, V, (rows,), generator=g, device="cuda")
+    out = blk.embed_forward(ids, table)
+    assert torch.equal(out, table[ids])
+    grad = blk.embed_backward(ids, out, V, dtable=table.fill_(3.0))
+    want = torch.zeros((1000, d), dtype=torch.float64, device="cuda").index_add_(0, ids - (V - 1000), out.double())
+    size = torch.zeros((1000, d), dtype=torch.float64, device="cuda").index_add_(0, ids - (V - 1000), out.double().abs())
+    close(grad[V - 1000:], f64(want), f64(size), 40)
+    assert not grad[:V - 1000].any()
+
+
+def test_grouped_past_32_bits(blk):
+    rows, K, N = 270000, 8192, 64
+    g = gen(4)
+    x = torch.empty((rows, K), dtype=BF, device="cuda").normal_(generator=g)
+    w = draw((2, N, K), BF, g, K ** -0.5)
+    off = torch.tensor([0, 135000, rows], dtype=torch.int32, device="cuda")
+    y = blk.grouped_forward(x, w, off)
+    pick = torch.tensor([0, 134999, 135000, 262143, 262144, 269999], device="cuda")
+    e = (pick >= 135000).long()
+    ref = np.einsum("rk,rnk->rn", f64(x[pick]), f64(w[e]))
+    size = np.einsum("rk,rnk->rn", np.abs(f64(x[pick])), np.abs(f64(w[e])))
+    close(y[pick], ref, size, K)
+    dx, _ = blk.grouped_backward(y, x, w, off, need_dw=False)
+    close(dx[pick], np.einsum("rn,rnk->rk", f64(y[pick]), f64(w[e])), np.einsum("rn,rnk->rk", np.abs(f64(y[pick])), np.abs(f64(w[e]))), N)
+    del dx, x, y
+    # many experts: w itself past 32 bits, on few rows and on the tensor cores
+    E, N, K = 600, 1024, 4096
+    w = torch.empty((E, N, K), dtype=BF, device="cuda").normal_(generator=g)
+    for rows in (8, 300):
+        x = draw((rows, K), BF, g, K ** -0.5)
+        off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+        off[E] = rows
+        off[E - 1] = rows // 2
+        y = blk.grouped_forward(x, w, off)
+        for lo, hi, e in ((0, rows // 2, E - 2), (rows // 2, rows, E - 1)):
+            close(y[lo:hi], f64(x[lo:hi]) @ f64(w[e]).T, np.abs(f64(x[lo:hi])) @ np.abs(f64(w[e])).T, K)
