@@ -80,9 +80,12 @@ struct NormArgs {
   const void *dz, *dh, *zin;
   const float *r_post_in, *r_pre_in;
   void *dx, *df, *dg, *dw_post, *dw_pre;
-  float *part;  // workspace: [blocks][2][d] column sums of a block's rows
+  float *part;   // workspace: [blocks][2][d] column sums of a block's rows (NULL: none wanted)
+  float *terms;  // workspace: [rows][4] terms of long rows
 };
-constexpr int kNormMaxBlocks = 152 * 4;
+// Blocks that leave column sums: four per SM of the part, more where rows are short.
+inline __host__ __device__ int norm_max_blocks(int d) { return 152 * (d >= 2048 ? 4 : (d >= 1024 ? 8 : 16)); }
+constexpr int kNormLong = 8192;  // columns from which the backward takes two launches
 cudaError_t launch_norm_forward(const NormArgs &a, int num_sms, cudaStream_t s);
 cudaError_t launch_norm_backward(const NormArgs &a, int num_sms, cudaStream_t s);
 

@@ -192,6 +192,12 @@ int norm_check(const moe_norm_config *c, moe::NormArgs *a) {
   return MOE_OK;
 }
 
+size_t norm_part_bytes(const moe::NormArgs &a) {
+  const int most = moe::norm_max_blocks(a.d);
+  const size_t slots = a.rows < most ? (a.rows > 0 ? a.rows : 1) : most;
+  return round256(slots * 2 * a.d * 4);
+}
+
 // ---------------------------------------------------------------- embedding
 int embed_check(const moe_embed_config *c, moe::EmbedArgs *a) {
   if (!c) return MOE_ERR_ARG;
@@ -299,8 +305,7 @@ int moe_norm_forward(const moe_norm_config *cfg, const void *x, const void *f, c
 size_t moe_norm_workspace_bytes(const moe_norm_config *cfg) {
   moe::NormArgs a;
   if (norm_check(cfg, &a) != MOE_OK) return 0;
-  const size_t slots = a.rows < moe::kNormMaxBlocks ? (a.rows > 0 ? a.rows + 3 : 1) : moe::kNormMaxBlocks;
-  return slots * 2 * a.d * 4;
+  return norm_part_bytes(a) + (a.d > moe::kNormLong ? static_cast<size_t>(a.rows) * 16 : 0);
 }
 
 int moe_norm_backward(const moe_norm_config *cfg, const void *dz, const void *dh, const void *z, const void *f,
@@ -318,7 +323,7 @@ int moe_norm_backward(const moe_norm_config *cfg, const void *dz, const void *dh
     if (needs_f && (!f || (post && !r_post) || (a.gate != MOE_GATE_NONE && !gate))) return MOE_ERR_ARG;
   }
   const bool columns = dw_post || dw_pre || (dgate && a.gate == MOE_GATE_CHANNEL);
-  if (columns && !ws) return MOE_ERR_ARG;
+  if (!ws) return MOE_ERR_ARG;
   if (columns && needs_f && a.gate == MOE_GATE_CHANNEL && !gate) return MOE_ERR_ARG;
   const int e = moe::elem_bytes(a.dtype);
   const void *elems[] = {dz, dh, z, f, gate, w_post, w_pre, dx, df, dgate, dw_post, dw_pre};
@@ -347,6 +352,7 @@ int moe_norm_backward(const moe_norm_config *cfg, const void *dz, const void *dh
   a.dw_post = dw_post;
   a.dw_pre = dw_pre;
   a.part = columns ? static_cast<float *>(ws) : nullptr;
+  a.terms = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + norm_part_bytes(a));
   return status_of(moe::launch_norm_backward(a, sms, stream));
 }
 

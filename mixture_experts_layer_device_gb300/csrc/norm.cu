@@ -301,50 +301,122 @@ __global__ void __launch_bounds__(THREADS, MINB) norm_bwd_kernel(const NormArgs 
   }
 }
 
-// Long rows: two passes over the row, the column sums in the block's own
-// workspace rows (each thread adds to its own columns).
-template <typename T>
-__global__ void __launch_bounds__(1024) norm_bwd_long_kernel(const NormArgs a) {
+// Long rows in two launches that each read the row: the first leaves every row's
+// terms in the workspace, the second has no sums over rows left to wait for, so a
+// thread keeps its columns for many rows.  10 instead of 6 elements move per
+// column, but a row need not fit a block.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(512) norm_bwd_rows_kernel(const NormArgs a) {
   __shared__ float red[2][4][kMaxWarps];
   const float inv_d = 1.f / static_cast<float>(a.d);
-  const bool pre = (a.flags & MOE_NORM_PRE) != 0;
-  float *part = a.part ? a.part + static_cast<long>(blockIdx.x) * 2 * a.d : nullptr;
-  if (part)
-    for (int c = threadIdx.x; c < a.d; c += blockDim.x) part[c] = part[a.d + c] = 0.f;
   int turn = 0;
   for (long row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    auto at = [&](const void *p, long ld, int c) { return p ? Elem<T>::to(static_cast<const T *>(p)[row * ld + c]) : 0.f; };
+    const RowIn in = row_in<T>(a, row);
     float s[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
-      float wp, wq, g;
-      weight_chunk<T, 1>(a.w_pre, c, &wp);
-      weight_chunk<T, 1>(a.w_post, c, &wq);
-      gate_chunk<T, 1>(a, row, c, 1.f, &g);
-      add_sums(at(a.dz, a.ld_z, c), pre ? at(a.dh, a.ld_h, c) * wp : 0.f, pre ? at(a.zin, a.ld_z, c) : 0.f,
-               wq * g * at(a.f, a.ld_f, c), s);
+    for (int c = threadIdx.x * VEC; c < a.d; c += blockDim.x * VEC) {
+      float v[4][VEC], w[VEC], wp[VEC], g[VEC];
+      const void *base[4] = {a.dz, a.dh, a.zin, a.f};
+      const long ld[4] = {a.ld_z, a.ld_h, a.ld_z, a.ld_f};
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        Chunk<T, VEC> q;
+        q.clear();
+        if (base[t]) q.load(static_cast<const T *>(base[t]) + row * ld[t] + c);
+        q.get(v[t]);
+      }
+      weight_chunk<T, VEC>(a.w_pre, c, wp);
+      weight_chunk<T, VEC>(a.w_post, c, w);
+      gate_chunk<T, VEC>(a, row, c, 1.f, g);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) add_sums(v[0][k], v[1][k] * wp[k], v[2][k], w[k] * g[k] * v[3][k], s);
     }
     row_sum<false, 4>(s, red, turn);
-    const RowTerms t = row_terms<T>(a, row, row_in<T>(a, row), s, inv_d, threadIdx.x == 0);
-    for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
-      float wp, w, g, acc0 = 0.f, acc1 = 0.f;
-      weight_chunk<T, 1>(a.w_pre, c, &wp);
-      weight_chunk<T, 1>(a.w_post, c, &w);
-      gate_chunk<T, 1>(a, row, c, 1.f, &g);
-      if (a.gate == MOE_GATE_CHANNEL) {
-        w *= g;
-        g = 1.f;
+    const RowTerms t = row_terms<T>(a, row, in, s, inv_d, threadIdx.x == 0);
+    if (threadIdx.x == 0) reinterpret_cast<float4 *>(a.terms)[row] = make_float4(t.rp, t.c1, t.a1, t.c2);
+  }
+}
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(128) norm_bwd_apply_kernel(const NormArgs a, int rows_each) {
+  const int c = (blockIdx.x * 128 + threadIdx.x) * VEC;
+  if (c >= a.d) return;
+  const bool full = a.gate == MOE_GATE_FULL;
+  float w[VEC], wp[VEC], acc0[VEC], acc1[VEC];
+  weight_chunk<T, VEC>(a.w_pre, c, wp);
+  weight_chunk<T, VEC>(a.w_post, c, w);
+  if (a.gate == MOE_GATE_CHANNEL) {
+    float g[VEC];
+    weight_chunk<T, VEC>(a.g, c, g);
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) w[k] *= g[k];
+  }
+#pragma unroll
+  for (int k = 0; k < VEC; ++k) acc0[k] = acc1[k] = 0.f;
+  const long first = static_cast<long>(blockIdx.y) * rows_each;
+  const long end = first + rows_each < a.rows ? first + rows_each : a.rows;
+  constexpr int U = 2;  // rows in flight
+  for (long r0 = first; r0 < end; r0 += U) {
+    Chunk<T, VEC> q[U][5];
+    float4 term[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int t = 0; t < 5; ++t) q[u][t].clear();
+      const long row = r0 + u;
+      if (row >= end) continue;
+      term[u] = reinterpret_cast<const float4 *>(a.terms)[row];
+      if (a.dz) q[u][0].load(static_cast<const T *>(a.dz) + row * a.ld_z + c);
+      if (a.dh) q[u][1].load(static_cast<const T *>(a.dh) + row * a.ld_h + c);
+      if (a.zin) q[u][2].load(static_cast<const T *>(a.zin) + row * a.ld_z + c);
+      if (a.f) q[u][3].load(static_cast<const T *>(a.f) + row * a.ld_f + c);
+      if (full) q[u][4].load(static_cast<const T *>(a.g) + row * a.ld_g + c);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long row = r0 + u;
+      if (row >= end) break;
+      const RowTerms t = {term[u].x, term[u].y, term[u].z, term[u].w};
+      float dz[VEC], dh[VEC], z[VEC], f[VEC], g[VEC];
+      q[u][0].get(dz);
+      q[u][1].get(dh);
+      q[u][2].get(z);
+      q[u][3].get(f);
+      q[u][4].get(g);
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        const ElemOut o =
+            elem_out(t, a.alpha, dz[k], dh[k], z[k], f[k], wp[k], w[k], full ? g[k] : 1.f, acc0[k], acc1[k]);
+        dz[k] = o.dx;
+        f[k] = o.df;
+        z[k] = o.dg;
       }
-      const ElemOut o = elem_out(t, a.alpha, at(a.dz, a.ld_z, c), pre ? at(a.dh, a.ld_h, c) : 0.f,
-                                 pre ? at(a.zin, a.ld_z, c) : 0.f, at(a.f, a.ld_f, c), wp, w, g, acc0, acc1);
-      if (a.dx) static_cast<T *>(a.dx)[row * a.ld_x + c] = Elem<T>::from(o.dx);
-      if (a.gate == MOE_GATE_FULL && a.dg) static_cast<T *>(a.dg)[row * a.ld_g + c] = Elem<T>::from(o.dg);
-      if (a.df) static_cast<T *>(a.df)[row * a.ld_f + c] = Elem<T>::from(o.df);
-      if (part) {
-        part[c] += acc0;
-        part[a.d + c] += acc1;
-      }
+      if (a.dx) Chunk<T, VEC>::store(static_cast<T *>(a.dx) + row * a.ld_x + c, dz);
+      if (a.df) Chunk<T, VEC>::store(static_cast<T *>(a.df) + row * a.ld_f + c, f);
+      if (full && a.dg) Chunk<T, VEC>::store(static_cast<T *>(a.dg) + row * a.ld_g + c, z);
     }
   }
+  if (a.part) {
+    float *p = a.part + static_cast<long>(blockIdx.y) * 2 * a.d + c;
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+      p[k] = acc0[k];
+      p[a.d + k] = acc1[k];
+    }
+  }
+}
+
+template <typename T, int VEC>
+cudaError_t bwd_long(const NormArgs &a, int num_sms, int *slots, cudaStream_t s) {
+  norm_bwd_rows_kernel<T, VEC><<<a.rows < num_sms * 4L ? a.rows : num_sms * 4, 512, 0, s>>>(a);
+  const int tiles = (a.d + 128 * VEC - 1) / (128 * VEC);
+  long groups = (num_sms * 16L + tiles - 1) / tiles;
+  if (groups > norm_max_blocks(a.d)) groups = norm_max_blocks(a.d);
+  if (groups > a.rows) groups = a.rows;
+  const int each = static_cast<int>((a.rows + groups - 1) / groups);
+  groups = (a.rows + each - 1) / each;
+  *slots = static_cast<int>(groups);
+  norm_bwd_apply_kernel<T, VEC><<<dim3(tiles, static_cast<unsigned>(groups)), 128, 0, s>>>(a, each);
+  return cudaGetLastError();
 }
 
 // dw_pre, dw_post and a channel gate's gradient from the blocks' column sums:
@@ -441,7 +513,7 @@ cudaError_t bwd_one(const NormArgs &a, int threads, int num_sms, int *slots, cud
   const int rpb = WARP ? threads / 32 : 1;
   const long blocks = (a.rows + rpb - 1) / rpb;
   long grid = static_cast<long>(num_sms) * resident(kernel, threads, memo);
-  if (grid > kNormMaxBlocks) grid = kNormMaxBlocks;
+  if (grid > norm_max_blocks(a.d)) grid = norm_max_blocks(a.d);
   if (blocks < grid) grid = blocks;
   *slots = static_cast<int>(grid);
   kernel<<<static_cast<int>(grid), threads, 0, s>>>(a);
@@ -452,7 +524,7 @@ template <typename T, int VEC>
 cudaError_t bwd_vec(const NormArgs &a, int num_sms, int *slots, cudaStream_t s) {
   if constexpr (VEC > 1) {
     constexpr int NCH = 16 / VEC;
-    if (a.d <= 512) return bwd_one<T, VEC, NCH, true, 256, 1>(a, 256, num_sms, slots, s);
+    if (a.d <= 256) return bwd_one<T, VEC, NCH / 2, true, 256, 2>(a, 256, num_sms, slots, s);
     if (sizeof(T) == 4 && a.d <= 4096) {  // fp32 rows take twice the registers
       const int threads = round32((a.d + 7) / 8);
       if (threads <= 256) return bwd_one<T, VEC, NCH / 2, false, 256, 2>(a, threads, num_sms, slots, s);
@@ -481,11 +553,8 @@ cudaError_t bwd_type(const NormArgs &a, int num_sms, cudaStream_t s) {
     const bool vec = all_vec<T>(a);
     if (a.rows > num_sms && norm_ring_fits(a, true)) {
       e = launch_norm_bwd_ring(a, num_sms, &slots, s);
-    } else if (a.d > 8192) {
-      slots = a.rows < 2 * num_sms ? a.rows : 2 * num_sms;
-      if (slots > kNormMaxBlocks) slots = kNormMaxBlocks;
-      norm_bwd_long_kernel<T><<<slots, 1024, 0, s>>>(a);
-      e = cudaGetLastError();
+    } else if (a.d > kNormLong) {
+      e = vec ? bwd_long<T, Elem<T>::VEC>(a, num_sms, &slots, s) : bwd_long<T, 1>(a, num_sms, &slots, s);
     } else {
       e = vec ? bwd_vec<T, Elem<T>::VEC>(a, num_sms, &slots, s) : bwd_vec<T, 1>(a, num_sms, &slots, s);
     }

@@ -19,7 +19,10 @@ namespace moe {
 
 namespace {
 
-constexpr int kFwdRows = 2;   // rows that share the forward's two barriers
+// Rows that share the forward's two barriers: three where a row takes most of a
+// block's registers and shared memory (16384 x 7168: 154 us, 171 with two), else two
+// (16384 x 4096: 93 us, 98 with three).
+__host__ __device__ constexpr int fwd_rows(int threads) { return threads > 384 && threads <= 512 ? 3 : 2; }
 constexpr int kRingSmem = 232448 - 2048;
 
 // 16-byte chunks of a row per thread: 16 columns of a 2-byte type, 8 of fp32 (in
@@ -121,13 +124,13 @@ MOE_DEV int row_shift(long ld, long row) {
 }
 
 // ---------------------------------------------------------------- forward
-// kFwdRows rows at a time (a grid apart): their sums share the barriers.  Shared
+// fwd_rows() rows at a time (a grid apart): their sums share the barriers.  Shared
 // memory: [stage][row][x, f, full gate][chunk][thread] of 16 bytes.
 template <typename T, bool FULL, bool EDGES, int THREADS>
 __global__ void __launch_bounds__(THREADS) norm_fwd_ring_kernel(const NormArgs a, int stages) {
-  constexpr int P = Elem<T>::VEC / 2, NT = FULL ? 3 : 2, R = kFwdRows;
+  constexpr int P = Elem<T>::VEC / 2, NT = FULL ? 3 : 2, R = fwd_rows(THREADS), SUMS = R > 2 ? 4 : R;
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float red[2][R][kMaxWarps];
+  __shared__ float red[2][SUMS][kMaxWarps];
   const Columns<T, EDGES> col(a.d, row_shift<T>(a.ld_x, blockIdx.x));
   const uint32_t place = 16 * blockDim.x, stage_bytes = R * NT * kChunks * place;
   const uint32_t base = smem_u32(smem) + 16 * threadIdx.x;
@@ -166,7 +169,8 @@ __global__ void __launch_bounds__(THREADS) norm_fwd_ring_kernel(const NormArgs a
     copy_wait(stages - 1);
     const uint32_t at = base + stage * stage_bytes;
     uint4 fq[R][kChunks];
-    float ss[R];
+    float ss[SUMS];
+    for (int r = R; r < SUMS; ++r) ss[r] = 0.f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       f32x2 sum = 0;
@@ -182,7 +186,7 @@ __global__ void __launch_bounds__(THREADS) norm_fwd_ring_kernel(const NormArgs a
       ss[r] = f2_sum(sum);
     }
     if (post) {
-      row_sum<false, R>(ss, red, turn);
+      row_sum<false, SUMS>(ss, red, turn);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         const float rp = rsqrtf(ss[r] * inv_d + a.eps);
@@ -218,7 +222,7 @@ __global__ void __launch_bounds__(THREADS) norm_fwd_ring_kernel(const NormArgs a
       ss[r] = f2_sum(sum);
     }
     if (pre) {
-      row_sum<false, R>(ss, red, turn);
+      row_sum<false, SUMS>(ss, red, turn);
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         if (row + r * G >= a.rows) break;
@@ -245,7 +249,7 @@ __global__ void __launch_bounds__(THREADS) norm_fwd_ring_kernel(const NormArgs a
 // One step sums row i + 1 and finishes row i, so the barrier and the joining of
 // the sums have the other row's work beside them.
 template <typename T, bool FULL, bool EDGES, int THREADS>
-__global__ void __launch_bounds__(THREADS) norm_bwd_ring_kernel(const NormArgs a, int stages) {
+__global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) norm_bwd_ring_kernel(const NormArgs a, int stages) {
   constexpr int VEC = Elem<T>::VEC, P = VEC / 2, NT = FULL ? 5 : 4;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float red[2][4][kMaxWarps];
@@ -421,7 +425,7 @@ RingShape ring_shape(const NormArgs &a, bool backward) {
   const int per = kChunks * vec;
   r.threads = ((a.d + (m ? vec - 1 : 0) + per - 1) / per + 31) / 32 * 32;
   if (r.threads > (backward ? 512 : 1024)) return r;
-  const size_t stage = static_cast<size_t>(r.threads) * kChunks * 16 * nt * (backward ? 1 : kFwdRows);
+  const size_t stage = static_cast<size_t>(r.threads) * kChunks * 16 * nt * (backward ? 1 : fwd_rows(r.threads));
   // short rows: three stages and more blocks
   for (int s = r.threads <= 256 ? 3 : 4; s >= 2; --s)
     if (stage * s <= kRingSmem) {
@@ -460,10 +464,11 @@ cudaError_t fwd_shape(const NormArgs &a, const RingShape &r, int num_sms, cudaSt
 template <typename T, bool FULL, bool EDGES, int THREADS>
 cudaError_t bwd_shape(const NormArgs &a, const RingShape &r, int num_sms, int *slots, cudaStream_t s) {
   static int memo[33][64] = {};
-  return ring_launch(norm_bwd_ring_kernel<T, FULL, EDGES, THREADS>, a, r, num_sms, kNormMaxBlocks, slots, memo, s);
+  return ring_launch(norm_bwd_ring_kernel<T, FULL, EDGES, THREADS>, a, r, num_sms, norm_max_blocks(a.d), slots, memo, s);
 }
 
-// Block sizes by the registers that they leave a thread: 384 (168), 512 (128), 1024 (64).
+// Block sizes by the registers that they leave a thread: up to 256 threads two
+// blocks (128), 384 (168), 512 (128), 1024 (64).
 template <typename T, bool FULL, bool EDGES>
 cudaError_t fwd_block(const NormArgs &a, const RingShape &r, int num_sms, cudaStream_t s) {
   if (r.threads <= 384) return fwd_shape<T, FULL, EDGES, 384>(a, r, num_sms, s);
@@ -472,6 +477,7 @@ cudaError_t fwd_block(const NormArgs &a, const RingShape &r, int num_sms, cudaSt
 }
 template <typename T, bool FULL, bool EDGES>
 cudaError_t bwd_block(const NormArgs &a, const RingShape &r, int num_sms, int *slots, cudaStream_t s) {
+  if (r.threads <= 256) return bwd_shape<T, FULL, EDGES, 256>(a, r, num_sms, slots, s);
   if (r.threads <= 384) return bwd_shape<T, FULL, EDGES, 384>(a, r, num_sms, slots, s);
   return bwd_shape<T, FULL, EDGES, 512>(a, r, num_sms, slots, s);
 }
