@@ -42,10 +42,11 @@ struct GroupedArgs {
   const int *offsets;  // [E + 1]
   const void *x, *w, *dy;
   void *y, *dx, *dw;
+  bool zeroed;   // weight gradient: launch_grouped_zero has written the experts without rows
   bool vec_out;  // tensor-core path: the output's rows are whole 16-byte pieces
   int *status;   // workspace status word
   int *tiles;    // workspace: the plan's tile table (3 E + 3 ints)
-  int *order;    // workspace: the experts by descending rows (weight gradient)
+  int *order;    // workspace: the experts by descending rows, and how many have any (weight gradient)
   uint8_t *maps; // workspace: 2 E tensor maps of 128 bytes (weight gradient)
 };
 
@@ -60,6 +61,8 @@ cudaError_t launch_grouped_plan(const GroupedArgs &g, int tile_rows, void *out, 
 cudaError_t launch_grouped_plain(const GroupedArgs &g, int dir, bool first, cudaStream_t s);
 // Forward of a few rows (no plan needed): 16-byte aligned rows of x and w.
 cudaError_t launch_grouped_few(const GroupedArgs &g, cudaStream_t s);
+// Zeros for the weight gradients of experts without rows.
+cudaError_t launch_grouped_zero(const GroupedArgs &g, int num_sms, cudaStream_t s);
 // dst [n rows of `cols`, stride ld_dst >= cols] = src with its row stride, zeros
 // beyond cols; `experts`: rows of w (N per expert, ld_e apart), experts without
 // rows left out.  2-byte elements.
@@ -85,7 +88,8 @@ struct NormArgs {
 };
 // Blocks that leave column sums: four per SM of the part, more where rows are short.
 inline __host__ __device__ int norm_max_blocks(int d) { return 152 * (d >= 2048 ? 4 : (d >= 1024 ? 8 : 16)); }
-constexpr int kNormLong = 8192;  // columns from which the backward takes two launches
+// Columns from which the backward takes two launches.
+inline __host__ __device__ int norm_long(int dtype) { return dtype == MOE_ELEM_FP32 ? 4096 : 8192; }
 cudaError_t launch_norm_forward(const NormArgs &a, int num_sms, cudaStream_t s);
 cudaError_t launch_norm_backward(const NormArgs &a, int num_sms, cudaStream_t s);
 

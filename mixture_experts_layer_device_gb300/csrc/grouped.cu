@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(128) grouped_plain_kernel(const GroupedArgs g)
     m0 = static_cast<int>(blockIdx.x) / nt * PT;
     n0 = static_cast<int>(blockIdx.x) % nt * PT;
     group_rows(g, e, lo, hi);
-    if (lo == hi && g.accumulate) return;
+    if (lo == hi && (g.accumulate || g.zeroed)) return;
     nk = hi - lo;
     mn = g.N - m0;
     nn = g.K - n0;
@@ -371,6 +371,31 @@ __global__ void __launch_bounds__(FEW_WARPS * 32) grouped_few_kernel(const Group
   }
 }
 
+// ---------------------------------------------------------------- zeros
+// Pieces of 64 KB of the experts' matrices, taken in turns; those of experts with
+// rows are passed over.  Whole 16-byte units between a piece's ragged ends.
+constexpr long kZeroPiece = 64 << 10;
+__global__ void __launch_bounds__(256) grouped_zero_kernel(const GroupedArgs g, long bytes, int pieces) {
+  const long total = static_cast<long>(g.E) * pieces;
+  for (long u = blockIdx.x; u < total; u += gridDim.x) {
+    const int e = static_cast<int>(u / pieces);
+    int lo, hi;
+    group_rows(g, e, lo, hi);
+    if (lo != hi) continue;
+    const long from = (u - static_cast<long>(e) * pieces) * kZeroPiece;
+    const long to = from + kZeroPiece < bytes ? from + kZeroPiece : bytes;
+    uint8_t *p = static_cast<uint8_t *>(g.dw) + e * bytes + from;
+    const long n = to - from;
+    long head = (16 - static_cast<long>(reinterpret_cast<uintptr_t>(p) & 15u)) & 15;
+    if (head > n) head = n;
+    const long body = (n - head) / 16 * 16;
+    for (long b = threadIdx.x * 16L; b < body; b += 256 * 16) st_stream(p + head + b, make_uint4(0, 0, 0, 0));
+    // ends: a few elements, 2 bytes at a time
+    for (long b = threadIdx.x * 2L; b < head; b += 512) *reinterpret_cast<uint16_t *>(p + b) = 0;
+    for (long b = head + body + threadIdx.x * 2L; b < n; b += 512) *reinterpret_cast<uint16_t *>(p + b) = 0;
+  }
+}
+
 // ---------------------------------------------------------------- padded copies
 // Rows at odd strides into rows that TMA can address: a thread per 8 elements.
 __global__ void __launch_bounds__(256) grouped_pad_kernel(const GroupedArgs g, const uint16_t *src, long rows, int cols,
@@ -400,6 +425,16 @@ __global__ void __launch_bounds__(256) grouped_pad_kernel(const GroupedArgs g, c
 }
 
 }  // namespace
+
+cudaError_t launch_grouped_zero(const GroupedArgs &g, int num_sms, cudaStream_t s) {
+  HostTrace t("grouped_zero", s);
+  const long bytes = static_cast<long>(g.N) * g.K * elem_bytes(g.out_dtype);
+  const int pieces = static_cast<int>((bytes + kZeroPiece - 1) / kZeroPiece);
+  const long want = static_cast<long>(g.E) * pieces;
+  grouped_zero_kernel<<<static_cast<unsigned>(want < num_sms * 16L ? want : num_sms * 16L), 256, 0, s>>>(
+      g, bytes, pieces);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_grouped_pad(const GroupedArgs &g, const void *src, long rows, int cols, long ld, bool experts,
                                void *dst, long ld_dst, cudaStream_t s) {

@@ -117,7 +117,7 @@ struct TcTiles {
     nf = ((DIR == GROUPED_DGRAD ? g.K : g.N) + 255) >> 8;
     if constexpr (DIR == GROUPED_WGRAD) {
       nc = (g.K + 255) >> 8;
-      total = g.E * nf * nc;
+      total = (g.zeroed || g.accumulate ? __ldg(g.order + g.E) : g.E) * nf * nc;  // the experts without rows stand last
     } else {
       t = tile_table_at(table, g.E);
       nc = 1;
@@ -426,8 +426,6 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
       if (t.klen > 0) {
         if (!mbar_wait(&tfull[acc], aph, abort_flag, g.status)) break;
         tc_fence_after();
-      } else if (g.accumulate) {
-        continue;
       }
       const uint32_t tempty_addr = smem_u32(&tempty[acc]);
       auto release = [&]() {
@@ -554,6 +552,7 @@ __global__ void __launch_bounds__(128) grouped_maps_kernel(const __grid_constant
           if (lane >= o) inc += n;
         }
         count[i + lane] = run + inc - v;
+        if (i + lane == kBuckets - 1) g.order[g.E] = run + inc - v;  // experts that have rows
         run += __shfl_sync(0xffffffffu, inc, 31);
       }
     }

@@ -553,7 +553,7 @@ cudaError_t bwd_type(const NormArgs &a, int num_sms, cudaStream_t s) {
     const bool vec = all_vec<T>(a);
     if (a.rows > num_sms && norm_ring_fits(a, true)) {
       e = launch_norm_bwd_ring(a, num_sms, &slots, s);
-    } else if (a.d > kNormLong) {
+    } else if (a.d > norm_long(a.dtype)) {
       e = vec ? bwd_long<T, Elem<T>::VEC>(a, num_sms, &slots, s) : bwd_long<T, 1>(a, num_sms, &slots, s);
     } else {
       e = vec ? bwd_vec<T, Elem<T>::VEC>(a, num_sms, &slots, s) : bwd_vec<T, 1>(a, num_sms, &slots, s);

@@ -88,6 +88,8 @@ GROUPED = [
     (4000, 4, 301, 305, "skew", 2, 3),      # large and odd: padded copies
     (4000, 4, 304, 305, "ends", 0, 1),
     (4001, 5, 301, 304, "skew", 1, 0),
+    (3, 300, 264, 256, "even", 0, 0),       # mostly experts without rows: their zeros written apart
+    (3, 300, 263, 257, "even", 0, 0),
 ]
 
 
