@@ -131,18 +131,21 @@ __global__ void __launch_bounds__(kRankBlock) embed_rank_kernel(const EmbedArgs 
 // Up to 65,536 tokens: the whole radix sort in one launch of one cluster.  Each of
 // its eight blocks holds a consecutive piece of the list in shared memory; a pass
 // ranks the piece's keys (stable), adds up the digits' counts of all blocks
-// through distributed shared memory, and writes every key to its place in the
-// block that holds it.  One launch of 27 us in place of six of 31 us together, at
-// 32768 tokens and 18-bit keys.
+// through distributed shared memory, orders the piece by digit in place, and
+// writes it out from there: neighbouring threads then mostly write neighbouring
+// places of one block (written straight from the ranking, every lane's store
+// goes somewhere else: 27 us where this takes 21, and the six launches of the
+// larger sort 31, at 32768 tokens and 18-bit keys).
 constexpr int kClusterBlocks = 8, kClusterThreads = 1024, kClusterItems = 8, kClusterDigits = 512;
 constexpr int kClusterSort = kClusterBlocks * kClusterThreads * kClusterItems;
 
 struct ClusterSmem {
-  int keys[2][kClusterThreads * kClusterItems], pos[2][kClusterThreads * kClusterItems];
+  int2 list[2][kClusterThreads * kClusterItems];          // key, position
   uint16_t count[kClusterThreads / 32][kClusterDigits];  // per warp and digit: keys so far, then keys of the warps before
   int total[kClusterDigits];                              // this block's keys of a digit
   int base[kClusterDigits];                               // first place of this block's keys of a digit
-  int warp_sum[kClusterDigits / 32];
+  int start[kClusterDigits];                              // the same within the block
+  int2 warp_sum[kClusterDigits / 32];
 };
 static_assert(sizeof(ClusterSmem) <= 232448, "shared memory");
 
@@ -151,8 +154,8 @@ MOE_DEV int ld_cluster(uint32_t at) {
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
   return v;
 }
-MOE_DEV void st_cluster(uint32_t at, int v) {
-  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+MOE_DEV void st_cluster(uint32_t at, int2 v) {
+  asm volatile("st.shared::cluster.v2.s32 [%0], {%1, %2};" ::"r"(at), "r"(v.x), "r"(v.y) : "memory");
 }
 
 __global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kClusterThreads, 1)
@@ -162,95 +165,101 @@ __global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kCluste
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, digits = 1 << bits;
   const uint32_t rank = cluster_rank();
   const int piece = kClusterThreads * items, first = static_cast<int>(rank) * piece;
+  const int held = a.rows - first < piece ? (a.rows > first ? a.rows - first : 0) : piece;  // places of the piece in the list
   const int mine = warp * 32 * items + lane;  // a warp ranks 32 x items consecutive keys
   for (int i = 0; i < items; ++i) {
-    const int at = mine + 32 * i, t = first + at;
-    int key = -1;
-    if (t < a.rows) {
-      key = key_of(a, t);
+    const int at = mine + 32 * i;
+    if (at < held) {
+      const int key = key_of(a, first + at);
       if (used && key < a.V) used[key] = 1;
+      sm.list[0][at] = make_int2(key, first + at);
     }
-    sm.keys[0][at] = key;
-    sm.pos[0][at] = t;
   }
   for (int p = 0; p < passes; ++p) {
     const int in = p & 1, shift = p * bits;
-    for (int i = threadIdx.x; i < (kClusterThreads / 32) * digits; i += kClusterThreads)
-      sm.count[i >> bits][i & (digits - 1)] = 0;
+    for (int i = threadIdx.x; i < (kClusterThreads / 32) * kClusterDigits / 8; i += kClusterThreads)
+      reinterpret_cast<uint4 *>(sm.count)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
-    int key[kClusterItems], local[kClusterItems];
+    int2 kv[kClusterItems];
+    int local[kClusterItems];
 #pragma unroll
     for (int i = 0; i < kClusterItems; ++i) {
       if (i >= items) break;
-      key[i] = sm.keys[in][mine + 32 * i];
-      const int dg = key[i] >= 0 ? (key[i] >> shift) & (digits - 1) : digits;  // places past the end: a group of their own
+      const bool has = mine + 32 * i < held;
+      int dg = digits;  // places past the end: a group of their own
+      if (has) {
+        kv[i] = sm.list[in][mine + 32 * i];
+        dg = (kv[i].x >> shift) & (digits - 1);
+      }
       const unsigned same = __match_any_sync(0xffffffffu, dg);
       const int before = __popc(same & ((1u << lane) - 1));
-      if (key[i] >= 0) local[i] = sm.count[warp][dg] + before;
+      if (has) local[i] = sm.count[warp][dg] + before;
       __syncwarp();
-      if (key[i] >= 0 && before == 0) sm.count[warp][dg] += static_cast<uint16_t>(__popc(same));
+      if (has && before == 0) sm.count[warp][dg] += static_cast<uint16_t>(__popc(same));
       __syncwarp();
     }
     __syncthreads();
-    if (static_cast<int>(threadIdx.x) < digits) {
-      int run = 0;
+    int own = 0, all = 0, before = 0;
+    const bool digit = static_cast<int>(threadIdx.x) < digits;
+    if (digit) {
 #pragma unroll 8
       for (int w = 0; w < kClusterThreads / 32; ++w) {
         const int n = sm.count[w][threadIdx.x];
-        sm.count[w][threadIdx.x] = static_cast<uint16_t>(run);
-        run += n;
+        sm.count[w][threadIdx.x] = static_cast<uint16_t>(own);
+        own += n;
       }
-      sm.total[threadIdx.x] = run;
+      sm.total[threadIdx.x] = own;
     }
     cluster_sync();
     // places of this block's keys: those of smaller digits anywhere, and of the same digit in the blocks before
-    int all = 0, before = 0;
-    if (static_cast<int>(threadIdx.x) < digits) {
+    if (digit) {
       const uint32_t at = smem_u32(&sm.total[threadIdx.x]);
+      int n[kClusterBlocks];
+#pragma unroll
+      for (int c = 0; c < kClusterBlocks; ++c) n[c] = ld_cluster(peer_smem(at, c));
 #pragma unroll
       for (int c = 0; c < kClusterBlocks; ++c) {
-        const int n = ld_cluster(peer_smem(at, c));
-        all += n;
-        if (c < static_cast<int>(rank)) before += n;
+        all += n[c];
+        if (c < static_cast<int>(rank)) before += n[c];
       }
     }
-    int inc = all;
+    int inc = all, inc_own = own;
     if (threadIdx.x < kClusterDigits) {
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int n = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += n;
+        const int n = __shfl_up_sync(0xffffffffu, inc, o), m = __shfl_up_sync(0xffffffffu, inc_own, o);
+        if (lane >= o) {
+          inc += n;
+          inc_own += m;
+        }
       }
-      if (lane == 31) sm.warp_sum[warp] = inc;
+      if (lane == 31) sm.warp_sum[warp] = make_int2(inc, inc_own);
     }
     __syncthreads();
-    if (static_cast<int>(threadIdx.x) < digits) {
-      int at = before + inc - all;
-      for (int w = 0; w < warp; ++w) at += sm.warp_sum[w];
-      sm.base[threadIdx.x] = at;
+    if (threadIdx.x < kClusterDigits) {  // whole warps, whatever the number of digits
+      const int2 v = lane < warp ? sm.warp_sum[lane] : make_int2(0, 0);  // warp <= 15: the warps before
+      sm.base[threadIdx.x] = __reduce_add_sync(0xffffffffu, v.x) + before + inc - all;
+      sm.start[threadIdx.x] = __reduce_add_sync(0xffffffffu, v.y) + inc_own - own;
     }
     __syncthreads();
-    const bool last = p + 1 == passes;
+    // the piece in order of digits, where the pass read it from
 #pragma unroll
     for (int i = 0; i < kClusterItems; ++i) {
-      if (i >= items) break;
-      if (key[i] < 0) continue;
-      const int dg = (key[i] >> shift) & (digits - 1);
-      const int to = sm.base[dg] + sm.count[warp][dg] + local[i], ps = sm.pos[in][mine + 32 * i];
-      if (last) {
-        keys_out[to] = key[i];
-        pos_out[to] = ps;
-      } else {
-        const int block = to / piece, slot = to - block * piece;
-        st_cluster(peer_smem(smem_u32(&sm.keys[in ^ 1][slot]), block), key[i]);
-        st_cluster(peer_smem(smem_u32(&sm.pos[in ^ 1][slot]), block), ps);
-      }
+      if (i >= items || mine + 32 * i >= held) break;
+      const int dg = (kv[i].x >> shift) & (digits - 1);
+      sm.list[in][sm.start[dg] + sm.count[warp][dg] + local[i]] = kv[i];
     }
-    if (!last) {
-      // places that no key takes: past the end of the list
-#pragma unroll
-      for (int i = 0; i < kClusterItems; ++i)
-        if (i < items && first + mine + 32 * i >= a.rows) sm.keys[in ^ 1][mine + 32 * i] = -1;
+    __syncthreads();
+    for (int at = threadIdx.x; at < held; at += kClusterThreads) {
+      const int2 v = sm.list[in][at];
+      const int dg = (v.x >> shift) & (digits - 1), to = sm.base[dg] + at - sm.start[dg];
+      if (p + 1 == passes) {
+        keys_out[to] = v.x;
+        pos_out[to] = v.y;
+      } else {
+        const int block = to / piece;
+        st_cluster(peer_smem(smem_u32(&sm.list[in ^ 1][to - block * piece]), block), v);
+      }
     }
     cluster_sync();  // the keys have arrived; no block leaves or reuses its counts while another reads them
   }
