@@ -26,6 +26,23 @@ struct HostTrace {
   ~HostTrace();
 };
 
+// A launch that may begin while the kernel in front on the stream, which has to call
+// pdl_trigger(), still runs: its blocks take their places and stop at pdl_wait() until
+// that kernel has ended.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---------------------------------------------------------------- grouped products
 // One product of the three directions as a strided matrix product per group:
 //   out[m, n] (+)= sum_k a[m, k] b[n, k]
@@ -43,6 +60,7 @@ struct GroupedArgs {
   const void *x, *w, *dy;
   void *y, *dx, *dw;
   bool zeroed;   // weight gradient: launch_grouped_zero has written the experts without rows
+  bool chained;  // tensor-core path: dgrad and wgrad of one call, each started before the launch in front has ended
   bool vec_out;  // tensor-core path: the output's rows are whole 16-byte pieces
   int *status;   // workspace status word
   int *tiles;    // workspace: the plan's tile table (3 E + 3 ints)
@@ -70,6 +88,8 @@ cudaError_t launch_grouped_pad(const GroupedArgs &g, const void *src, long rows,
                                void *dst, long ld_dst, cudaStream_t s);
 // Tensor-core path: the operands' pointers and row strides multiples of 16 bytes.
 cudaError_t launch_grouped_tc(const GroupedArgs &g, int dir, cudaStream_t s);
+// Both products of a backward on it.
+cudaError_t launch_grouped_tc_pair(GroupedArgs dgrad, GroupedArgs wgrad, cudaStream_t s);
 
 // ---------------------------------------------------------------- block norms
 struct NormArgs {

@@ -109,7 +109,7 @@ void grouped_bind(moe::GroupedArgs *g, const int32_t *offsets, void *ws) {
 bool tma_rows(const void *p, long ld) { return aligned(p, 16) && ld % 8 == 0; }
 
 // Brings the operands of one product into TMA's form: true when the tensor-core
-// kernel can run on *t (copies launched where needed).
+// kernel can run on *t (copies launched where needed; `have_dy`: dy's has been made).
 struct Padded {
   bool ok;
   int rc;
@@ -161,11 +161,9 @@ bool grouped_few(const moe::GroupedArgs &g) {
          tma_rows(g.w, g.ld_w) && g.ld_e % 8 == 0;
 }
 
-// One product; `have_dy`: an earlier one of the call has made dy's padded copy.
-int grouped_product(const moe::GroupedArgs &g, int dir, bool first, void *ws, bool *have_dy, cudaStream_t s) {
-  moe::GroupedArgs t;
-  const Padded p = grouped_tensor(g, dir, static_cast<uint8_t *>(ws), &t, have_dy, s);
-  if (p.rc != MOE_OK) return p.rc;
+// One product: t on the tensor cores when that can be, else g on the plain kernel.
+int grouped_product(const Padded &p, const moe::GroupedArgs &t, const moe::GroupedArgs &g, int dir, bool first,
+                    cudaStream_t s) {
   return status_of(p.ok ? moe::launch_grouped_tc(t, dir, s) : moe::launch_grouped_plain(g, dir, first, s));
 }
 
@@ -247,7 +245,9 @@ int moe_grouped_forward(const moe_grouped_config *cfg, const void *x, const void
   g.y = y;
   if (grouped_few(g)) return status_of(moe::launch_grouped_few(g, stream));
   bool have_dy = false;
-  return grouped_product(g, moe::GROUPED_FWD, true, ws, &have_dy, stream);
+  moe::GroupedArgs t;
+  const Padded p = grouped_tensor(g, moe::GROUPED_FWD, static_cast<uint8_t *>(ws), &t, &have_dy, stream);
+  return p.rc != MOE_OK ? p.rc : grouped_product(p, t, g, moe::GROUPED_FWD, true, stream);
 }
 
 int moe_grouped_backward(const moe_grouped_config *cfg, const void *dy, const void *x, const void *w,
@@ -272,10 +272,16 @@ int moe_grouped_backward(const moe_grouped_config *cfg, const void *dy, const vo
   // Large weight gradients: the experts without rows are written by plain stores (6.9
   // TB/s) and left out of the product, whose epilogue reaches 2.8 to 6.1 TB/s on zeros.
   g.zeroed = dw && !g.accumulate && static_cast<double>(g.E) * g.N * g.K >= 16e6;
-  if (g.zeroed && (rc = status_of(moe::launch_grouped_zero(g, sms, stream))) != MOE_OK) return rc;
   bool have_dy = false;
-  if (dx && (rc = grouped_product(g, moe::GROUPED_DGRAD, true, ws, &have_dy, stream)) != MOE_OK) return rc;
-  if (dw && (rc = grouped_product(g, moe::GROUPED_WGRAD, !dx, ws, &have_dy, stream)) != MOE_OK) return rc;
+  moe::GroupedArgs dg, wg;
+  Padded pd = {false, MOE_OK}, pw = {false, MOE_OK};
+  if (dx) pd = grouped_tensor(g, moe::GROUPED_DGRAD, static_cast<uint8_t *>(ws), &dg, &have_dy, stream);
+  if (pd.rc == MOE_OK && dw) pw = grouped_tensor(g, moe::GROUPED_WGRAD, static_cast<uint8_t *>(ws), &wg, &have_dy, stream);
+  if (pd.rc != MOE_OK || pw.rc != MOE_OK) return pd.rc != MOE_OK ? pd.rc : pw.rc;
+  if (g.zeroed && (rc = status_of(moe::launch_grouped_zero(g, sms, stream))) != MOE_OK) return rc;
+  if (pd.ok && pw.ok) return status_of(moe::launch_grouped_tc_pair(dg, wg, stream));
+  if (dx && (rc = grouped_product(pd, dg, g, moe::GROUPED_DGRAD, true, stream)) != MOE_OK) return rc;
+  if (dw && (rc = grouped_product(pw, wg, g, moe::GROUPED_WGRAD, !dx, stream)) != MOE_OK) return rc;
   return MOE_OK;
 }
 

@@ -10,6 +10,11 @@
 
 namespace moe {
 
+// Programmatic dependent launch: lets the next launch begin, and waits for the end
+// of the one in front (at once where the launches are not chained).
+MOE_DEV void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+MOE_DEV void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Two fp32 values in one 64-bit register pair: one instruction works on both
 // (fma / mul / add.rn.f32x2), each half rounded as its scalar form.
 typedef unsigned long long f32x2;

@@ -112,6 +112,7 @@ MOE_DEV void fill_rows(const Fill &f, long block, long blocks) {
 // thread at most.  Also marks the table rows that occur.
 constexpr int kRankBlock = 128;
 __global__ void __launch_bounds__(kRankBlock) embed_rank_kernel(const EmbedArgs a, int *keys, int *pos, uint8_t *used) {
+  pdl_trigger();
   __shared__ int sk[kSmallSort];
   for (int i = threadIdx.x; i < a.rows; i += kRankBlock) sk[i] = key_of(a, i);
   __syncthreads();
@@ -160,6 +161,7 @@ MOE_DEV void st_cluster(uint32_t at, int2 v) {
 
 __global__ void __cluster_dims__(kClusterBlocks, 1, 1) __launch_bounds__(kClusterThreads, 1)
     embed_cluster_sort_kernel(const EmbedArgs a, int items, int passes, int bits, int *keys_out, int *pos_out, uint8_t *used) {
+  pdl_trigger();
   extern __shared__ __align__(16) uint8_t smem_raw[];
   ClusterSmem &sm = *reinterpret_cast<ClusterSmem *>(smem_raw);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, digits = 1 << bits;
@@ -326,6 +328,7 @@ MOE_DEV void warp_prefix(const int *total, int digits, int *out) {
 __global__ void __launch_bounds__(kSortBlock) embed_scatter_kernel(const EmbedArgs a, const int *keys, const int *pos,
                                                                    int shift, int digits, const int *hist,
                                                                    const int *total, int *keys_out, int *pos_out) {
+  pdl_trigger();
   // next[w][digit]: where warp w's next key of a digit goes
   extern __shared__ int next[];
   __shared__ int base[kMaxDigits];
@@ -410,6 +413,8 @@ template <typename T, typename G, int VEC>
 __global__ void __launch_bounds__(128) embed_sum_kernel(const EmbedArgs a, const int *keys, const int *pos, float *part,
                                                         int *cross, int pieces, int slabs, const Fill fill) {
   __shared__ int sk[kMaxPiece], sp[kMaxPiece];
+  pdl_wait();
+  pdl_trigger();
   const long work = static_cast<long>(pieces) * slabs;
   if (blockIdx.x >= work) {
     fill_rows(fill, blockIdx.x - work, gridDim.x - work);
@@ -490,6 +495,7 @@ __global__ void __launch_bounds__(128) embed_sum_kernel(const EmbedArgs a, const
 // partial rows in order.
 template <typename G, int VEC>
 __global__ void __launch_bounds__(256) embed_join_kernel(const EmbedArgs a, const float *part, const int *cross, int slabs) {
+  pdl_wait();
   const long total = static_cast<long>(cross[0]) * slabs;
   for (long u = blockIdx.x; u < total; u += gridDim.x) {
     const int4 run = reinterpret_cast<const int4 *>(cross)[1 + u / slabs];
@@ -594,11 +600,14 @@ cudaError_t sums(const EmbedArgs &a, const int *keys, const int *pos, float *par
   if (grid > 2147483647L) return cudaErrorInvalidConfiguration;
   if (grid) {
     HostTrace t("embed_sum", s);
-    if (vec)
-      embed_sum_kernel<T, G, Elem<T>::VEC><<<static_cast<unsigned>(grid), 128, 0, s>>>(a, keys, pos, part, cross, pieces, slabs, fill);
-    else
-      embed_sum_kernel<T, G, 1><<<static_cast<unsigned>(grid), 128, 0, s>>>(a, keys, pos, part, cross, pieces, slabs, fill);
-    cudaError_t e = cudaGetLastError();
+    const auto kernel = vec ? embed_sum_kernel<T, G, Elem<T>::VEC> : embed_sum_kernel<T, G, 1>;
+    cudaError_t e;
+    if (a.rows > 0) {  // behind the sort
+      e = launch_early(kernel, static_cast<unsigned>(grid), 128, s, a, keys, pos, part, cross, pieces, slabs, fill);
+    } else {
+      kernel<<<static_cast<unsigned>(grid), 128, 0, s>>>(a, keys, pos, part, cross, pieces, slabs, fill);
+      e = cudaGetLastError();
+    }
     if (e != cudaSuccess) return e;
   }
   if (pieces > 1) {
@@ -606,9 +615,7 @@ cudaError_t sums(const EmbedArgs &a, const int *keys, const int *pos, float *par
     const int join_cols = 256 * (vec ? 4 : 1), join_slabs = (a.d + join_cols - 1) / join_cols;
     const long want = static_cast<long>(pieces) * join_slabs;
     const unsigned blocks = static_cast<unsigned>(want < num_sms * 8L ? want : num_sms * 8L);
-    if (vec) embed_join_kernel<G, 4><<<blocks, 256, 0, s>>>(a, part, cross, join_slabs);
-    else embed_join_kernel<G, 1><<<blocks, 256, 0, s>>>(a, part, cross, join_slabs);
-    return cudaGetLastError();
+    return launch_early(vec ? embed_join_kernel<G, 4> : embed_join_kernel<G, 1>, blocks, 256, s, a, part, cross, join_slabs);
   }
   return cudaSuccess;
 }

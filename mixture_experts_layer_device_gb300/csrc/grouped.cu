@@ -19,6 +19,7 @@ namespace {
 // blocks: zeros for the rows of `out` that belong to no expert.
 __global__ void __launch_bounds__(1024) grouped_plan_kernel(const GroupedArgs g, int tile_rows, uint8_t *out,
                                                             long row_bytes, long ld_bytes) {
+  pdl_trigger();
   if (blockIdx.x > 0) {
     int lo, hi, lo_last, hi_last;
     group_rows(g, 0, lo, hi);
@@ -189,6 +190,7 @@ MOE_DEV void acc_place(int warp, int lane, int i, int j, int k, int &m, int &n) 
 
 template <typename T, int DIR>
 __global__ void __launch_bounds__(128) grouped_plain_kernel(const GroupedArgs g) {
+  pdl_wait();  // the plan's tile table
   Side a, b;
   int lo, hi, n0, m0, mn, nn, nk;
   void *out;
@@ -252,15 +254,18 @@ __global__ void __launch_bounds__(128) grouped_plain_kernel(const GroupedArgs g)
 }
 
 template <typename T>
-cudaError_t plain_type(const GroupedArgs &g, int dir, cudaStream_t s) {
+cudaError_t plain_type(const GroupedArgs &g, int dir, bool planned, cudaStream_t s) {
   const long slots = (g.rows + PT - 1L) / PT + (g.E < g.rows ? g.E : g.rows);
   if (dir == GROUPED_WGRAD) {
     const dim3 grid(((g.N + PT - 1) / PT) * ((g.K + PT - 1) / PT), g.E);
+    if (planned) return launch_early(grouped_plain_kernel<T, GROUPED_WGRAD>, grid, 128, s, g);
     grouped_plain_kernel<T, GROUPED_WGRAD><<<grid, 128, 0, s>>>(g);
   } else if (dir == GROUPED_FWD) {
-    if (slots) grouped_plain_kernel<T, GROUPED_FWD><<<dim3(slots, (g.N + PT - 1) / PT), 128, 0, s>>>(g);
+    const dim3 grid(slots, (g.N + PT - 1) / PT);
+    if (slots) return launch_early(grouped_plain_kernel<T, GROUPED_FWD>, grid, 128, s, g);
   } else {
-    if (slots) grouped_plain_kernel<T, GROUPED_DGRAD><<<dim3(slots, (g.K + PT - 1) / PT), 128, 0, s>>>(g);
+    const dim3 grid(slots, (g.K + PT - 1) / PT);
+    if (slots) return launch_early(grouped_plain_kernel<T, GROUPED_DGRAD>, grid, 128, s, g);
   }
   return cudaGetLastError();
 }
@@ -471,7 +476,7 @@ cudaError_t launch_grouped_plain(const GroupedArgs &g, int dir, bool first, cuda
     if (e != cudaSuccess) return e;
   }
   HostTrace t(dir == GROUPED_FWD ? "grouped_fwd_plain" : dir == GROUPED_DGRAD ? "grouped_dgrad_plain" : "grouped_wgrad_plain", s);
-  return g.dtype == MOE_ELEM_BF16 ? plain_type<__nv_bfloat16>(g, dir, s) : plain_type<__half>(g, dir, s);
+  return g.dtype == MOE_ELEM_BF16 ? plain_type<__nv_bfloat16>(g, dir, first, s) : plain_type<__half>(g, dir, first, s);
 }
 
 }  // namespace moe

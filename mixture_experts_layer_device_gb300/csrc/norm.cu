@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_long_kernel(const NormArgs a) {
 // Rows in registers, the next row's loads in flight (as the forward).
 template <typename T, int VEC, int NCH, bool WARP, int THREADS, int MINB>
 __global__ void __launch_bounds__(THREADS, MINB) norm_bwd_kernel(const NormArgs a) {
+  pdl_trigger();
   __shared__ float red[2][4][kMaxWarps];
   const int tpr = WARP ? 32 : blockDim.x;
   const int tid = WARP ? (threadIdx.x & 31) : threadIdx.x;
@@ -338,6 +339,7 @@ __global__ void __launch_bounds__(512) norm_bwd_rows_kernel(const NormArgs a) {
 
 template <typename T, int VEC>
 __global__ void __launch_bounds__(128) norm_bwd_apply_kernel(const NormArgs a, int rows_each) {
+  pdl_trigger();
   const int c = (blockIdx.x * 128 + threadIdx.x) * VEC;
   if (c >= a.d) return;
   const bool full = a.gate == MOE_GATE_FULL;
@@ -424,6 +426,7 @@ cudaError_t bwd_long(const NormArgs &a, int num_sms, int *slots, cudaStream_t s)
 template <typename T>
 __global__ void __launch_bounds__(1024) norm_columns_kernel(const NormArgs a, int slots) {
   __shared__ float sh[32][32];
+  pdl_wait();
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), run = threadIdx.x >> 5, k = blockIdx.y;
   float v = 0.f;
   if (c < a.d)
@@ -562,7 +565,9 @@ cudaError_t bwd_type(const NormArgs &a, int num_sms, cudaStream_t s) {
   }
   if (!a.part) return cudaSuccess;
   HostTrace t("norm_columns", s);
-  norm_columns_kernel<T><<<dim3((a.d + 31) / 32, 2), 1024, 0, s>>>(a, slots);
+  const dim3 grid((a.d + 31) / 32, 2);
+  if (a.rows > 0) return launch_early(norm_columns_kernel<T>, grid, 1024, s, a, slots);
+  norm_columns_kernel<T><<<grid, 1024, 0, s>>>(a, slots);
   return cudaGetLastError();
 }
 

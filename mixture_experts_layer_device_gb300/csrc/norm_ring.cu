@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(THREADS) norm_fwd_ring_kernel(const NormArgs a
 // the sums have the other row's work beside them.
 template <typename T, bool FULL, bool EDGES, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) norm_bwd_ring_kernel(const NormArgs a, int stages) {
+  pdl_trigger();
   constexpr int VEC = Elem<T>::VEC, P = VEC / 2, NT = FULL ? 5 : 4;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float red[2][4][kMaxWarps];
