@@ -59,8 +59,8 @@ struct GroupedArgs {
   const int *offsets;  // [E + 1]
   const void *x, *w, *dy;
   void *y, *dx, *dw;
-  bool zeroed;   // weight gradient: launch_grouped_zero has written the experts without rows
-  bool chained;  // tensor-core path: dgrad and wgrad of one call, each started before the launch in front has ended
+  bool zeroed;   // weight gradient: launch_grouped_zero writes the experts without rows
+  bool chained;  // tensor-core path: starts before the launch in front has ended (dgrad and wgrad of one call)
   bool vec_out;  // tensor-core path: the output's rows are whole 16-byte pieces
   int *status;   // workspace status word
   int *tiles;    // workspace: the plan's tile table (3 E + 3 ints)
@@ -79,7 +79,11 @@ cudaError_t launch_grouped_plan(const GroupedArgs &g, int tile_rows, void *out, 
 cudaError_t launch_grouped_plain(const GroupedArgs &g, int dir, bool first, cudaStream_t s);
 // Forward of a few rows (no plan needed): 16-byte aligned rows of x and w.
 cudaError_t launch_grouped_few(const GroupedArgs &g, cudaStream_t s);
-// Zeros for the weight gradients of experts without rows.
+// Puts the experts in order (g.order) for launch_grouped_zero; the tensor-core
+// path's own launch does it there.
+cudaError_t launch_grouped_order(const GroupedArgs &g, cudaStream_t s);
+// Zeros for the weight gradients of experts without rows, right behind the launch
+// that has put the experts in order.
 cudaError_t launch_grouped_zero(const GroupedArgs &g, int num_sms, cudaStream_t s);
 // dst [n rows of `cols`, stride ld_dst >= cols] = src with its row stride, zeros
 // beyond cols; `experts`: rows of w (N per expert, ld_e apart), experts without
@@ -87,9 +91,9 @@ cudaError_t launch_grouped_zero(const GroupedArgs &g, int num_sms, cudaStream_t 
 cudaError_t launch_grouped_pad(const GroupedArgs &g, const void *src, long rows, int cols, long ld, bool experts,
                                void *dst, long ld_dst, cudaStream_t s);
 // Tensor-core path: the operands' pointers and row strides multiples of 16 bytes.
-cudaError_t launch_grouped_tc(const GroupedArgs &g, int dir, cudaStream_t s);
+cudaError_t launch_grouped_tc(const GroupedArgs &g, int dir, int num_sms, cudaStream_t s);
 // Both products of a backward on it.
-cudaError_t launch_grouped_tc_pair(GroupedArgs dgrad, GroupedArgs wgrad, cudaStream_t s);
+cudaError_t launch_grouped_tc_pair(GroupedArgs dgrad, GroupedArgs wgrad, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- block norms
 struct NormArgs {

@@ -163,8 +163,14 @@ bool grouped_few(const moe::GroupedArgs &g) {
 
 // One product: t on the tensor cores when that can be, else g on the plain kernel.
 int grouped_product(const Padded &p, const moe::GroupedArgs &t, const moe::GroupedArgs &g, int dir, bool first,
-                    cudaStream_t s) {
-  return status_of(p.ok ? moe::launch_grouped_tc(t, dir, s) : moe::launch_grouped_plain(g, dir, first, s));
+                    int sms, cudaStream_t s) {
+  if (p.ok) return status_of(moe::launch_grouped_tc(t, dir, sms, s));
+  if (dir == moe::GROUPED_WGRAD && g.zeroed) {
+    int rc = status_of(moe::launch_grouped_order(g, s));
+    if (rc == MOE_OK) rc = status_of(moe::launch_grouped_zero(g, sms, s));
+    if (rc != MOE_OK) return rc;
+  }
+  return status_of(moe::launch_grouped_plain(g, dir, first, s));
 }
 
 // ---------------------------------------------------------------- norm
@@ -247,7 +253,7 @@ int moe_grouped_forward(const moe_grouped_config *cfg, const void *x, const void
   bool have_dy = false;
   moe::GroupedArgs t;
   const Padded p = grouped_tensor(g, moe::GROUPED_FWD, static_cast<uint8_t *>(ws), &t, &have_dy, stream);
-  return p.rc != MOE_OK ? p.rc : grouped_product(p, t, g, moe::GROUPED_FWD, true, stream);
+  return p.rc != MOE_OK ? p.rc : grouped_product(p, t, g, moe::GROUPED_FWD, true, sms, stream);
 }
 
 int moe_grouped_backward(const moe_grouped_config *cfg, const void *dy, const void *x, const void *w,
@@ -278,10 +284,9 @@ int moe_grouped_backward(const moe_grouped_config *cfg, const void *dy, const vo
   if (dx) pd = grouped_tensor(g, moe::GROUPED_DGRAD, static_cast<uint8_t *>(ws), &dg, &have_dy, stream);
   if (pd.rc == MOE_OK && dw) pw = grouped_tensor(g, moe::GROUPED_WGRAD, static_cast<uint8_t *>(ws), &wg, &have_dy, stream);
   if (pd.rc != MOE_OK || pw.rc != MOE_OK) return pd.rc != MOE_OK ? pd.rc : pw.rc;
-  if (g.zeroed && (rc = status_of(moe::launch_grouped_zero(g, sms, stream))) != MOE_OK) return rc;
-  if (pd.ok && pw.ok) return status_of(moe::launch_grouped_tc_pair(dg, wg, stream));
-  if (dx && (rc = grouped_product(pd, dg, g, moe::GROUPED_DGRAD, true, stream)) != MOE_OK) return rc;
-  if (dw && (rc = grouped_product(pw, wg, g, moe::GROUPED_WGRAD, !dx, stream)) != MOE_OK) return rc;
+  if (pd.ok && pw.ok) return status_of(moe::launch_grouped_tc_pair(dg, wg, sms, stream));
+  if (dx && (rc = grouped_product(pd, dg, g, moe::GROUPED_DGRAD, true, sms, stream)) != MOE_OK) return rc;
+  if (dw && (rc = grouped_product(pw, wg, g, moe::GROUPED_WGRAD, !dx, sms, stream)) != MOE_OK) return rc;
   return MOE_OK;
 }
 

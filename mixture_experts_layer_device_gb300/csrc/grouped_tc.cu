@@ -710,24 +710,34 @@ cudaError_t launch_product(const GroupedArgs &g, int dir, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_grouped_tc(const GroupedArgs &g, int dir, cudaStream_t s) {
+cudaError_t launch_grouped_order(const GroupedArgs &g, cudaStream_t s) {
+  HostTrace t("grouped_order", s);
+  grouped_maps_kernel<<<1, 128, 0, s>>>(CUtensorMap(), CUtensorMap(), g);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_grouped_tc(const GroupedArgs &g, int dir, int num_sms, cudaStream_t s) {
   if (dir != GROUPED_WGRAD && g.rows <= 0) return cudaSuccess;
-  const cudaError_t e = dir == GROUPED_WGRAD ? launch_maps(g, s) : plan_first(g, dir, s);
+  cudaError_t e = dir == GROUPED_WGRAD ? launch_maps(g, s) : plan_first(g, dir, s);
+  if (e == cudaSuccess && dir == GROUPED_WGRAD && g.zeroed) e = launch_grouped_zero(g, num_sms, s);
   return e == cudaSuccess ? launch_product(g, dir, s) : e;
 }
 
-// Programmatic dependent launches: dgrad needs nothing of the maps' launch and starts
-// with it; wgrad starts when dgrad's blocks all run and the maps are written, on the
-// SMs that dgrad does not fill or has left, and ends after dgrad.  2043 rows, 8
-// experts of [512, 768]: 24 us where launches in turn take 33; 16384 rows, 32 of
-// [1024, 1024]: 83 and 93; 8192 rows, 8 of [4096, 4096]: 344 and 354.  Not for the
-// longest products, where 10 us are nothing and pairs that start wgrad at different
-// times find less of each other's tiles in L2: 32768 rows, 64 of [7168, 2048], 1432 and
-// 1482 us with two draws of the offsets where launches in turn take 1441 and 1443.
-cudaError_t launch_grouped_tc_pair(GroupedArgs dgrad, GroupedArgs wgrad, cudaStream_t s) {
-  dgrad.chained = wgrad.chained = static_cast<double>(dgrad.rows) * dgrad.N * dgrad.K <= 274877906944.0;
+// Programmatic dependent launches.  dgrad needs nothing of the launch in front (the
+// maps, or the zeros) and starts with it; wgrad starts when dgrad's blocks all run and
+// the maps are written, on the SMs that dgrad does not fill or has left, and ends
+// after dgrad.  2043 rows, 8 experts of [512, 768]: 24 us where launches in turn take
+// 33; 16384 rows, 32 of [1024, 1024]: 83 and 93; 8192 rows, 8 of [4096, 4096]: 344 and
+// 354.  Not wgrad's of the longest products, where 10 us are nothing and pairs that
+// start it at different times find less of each other's tiles in L2: 32768 rows, 64 of
+// [7168, 2048], 1432 and 1482 us with two draws of the offsets where launches in turn
+// take 1441 and 1443.
+cudaError_t launch_grouped_tc_pair(GroupedArgs dgrad, GroupedArgs wgrad, int num_sms, cudaStream_t s) {
+  dgrad.chained = true;
+  wgrad.chained = static_cast<double>(dgrad.rows) * dgrad.N * dgrad.K <= 274877906944.0;
   cudaError_t e = plan_first(dgrad, GROUPED_DGRAD, s);
   if (e == cudaSuccess) e = launch_maps(wgrad, s);
+  if (e == cudaSuccess && wgrad.zeroed) e = launch_grouped_zero(wgrad, num_sms, s);
   if (e == cudaSuccess) e = launch_product(dgrad, GROUPED_DGRAD, s);
   if (e == cudaSuccess) e = launch_product(wgrad, GROUPED_WGRAD, s);
   return e;
