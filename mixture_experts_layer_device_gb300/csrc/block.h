@@ -107,9 +107,12 @@ struct NormArgs {
   const void *dz, *dh, *zin;
   const float *r_post_in, *r_pre_in;
   void *dx, *df, *dg, *dw_post, *dw_pre;
-  float *part;   // workspace: [blocks][2][d] column sums of a block's rows (NULL: none wanted)
+  float *part;   // workspace: [blocks][2][norm_part_row(d)] column sums of a block's rows (NULL: none wanted)
   float *terms;  // workspace: [rows][4] terms of long rows
 };
+// Floats of one row of column sums: 16-byte pieces, and room for rows that start
+// inside one.
+inline __host__ __device__ long norm_part_row(int d) { return (d + 15L) & ~7L; }
 // Blocks that leave column sums: four per SM of the part, more where rows are short.
 inline __host__ __device__ int norm_max_blocks(int d) { return 152 * (d >= 2048 ? 4 : (d >= 1024 ? 8 : 16)); }
 // Columns from which the backward takes two launches.

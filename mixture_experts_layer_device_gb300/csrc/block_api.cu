@@ -199,7 +199,7 @@ int norm_check(const moe_norm_config *c, moe::NormArgs *a) {
 size_t norm_part_bytes(const moe::NormArgs &a) {
   const int most = moe::norm_max_blocks(a.d);
   const size_t slots = a.rows < most ? (a.rows > 0 ? a.rows : 1) : most;
-  return round256(slots * 2 * a.d * 4);
+  return round256(slots * 2 * moe::norm_part_row(a.d) * 4);
 }
 
 // ---------------------------------------------------------------- embedding

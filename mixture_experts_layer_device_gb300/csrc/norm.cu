@@ -267,7 +267,8 @@ __global__ void __launch_bounds__(THREADS, MINB) norm_bwd_kernel(const NormArgs 
     }
   }
   if (!a.part) return;
-  float *p = a.part + static_cast<long>(blockIdx.x) * 2 * a.d;
+  const long ld_p = norm_part_row(a.d);
+  float *p = a.part + blockIdx.x * 2 * ld_p;
   if constexpr (WARP) {
     // the block's warps join their column sums in order
     __shared__ float join[2][32 * VEC * NCH];
@@ -286,18 +287,16 @@ __global__ void __launch_bounds__(THREADS, MINB) norm_bwd_kernel(const NormArgs 
     }
     for (int c = threadIdx.x; c < a.d; c += blockDim.x) {
       p[c] = join[0][c];
-      p[a.d + c] = join[1][c];
+      p[ld_p + c] = join[1][c];
     }
   } else {
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
       const int c = (tid + i * tpr) * VEC;
-      if (c < a.d)
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-          p[c + k] = acc0[i][k];
-          p[a.d + c + k] = acc1[i][k];
-        }
+      if (c < a.d) {
+        put_sums<VEC>(p + c, acc0[i]);
+        put_sums<VEC>(p + ld_p + c, acc1[i]);
+      }
     }
   }
 }
@@ -398,12 +397,10 @@ __global__ void __launch_bounds__(128) norm_bwd_apply_kernel(const NormArgs a, i
     }
   }
   if (a.part) {
-    float *p = a.part + static_cast<long>(blockIdx.y) * 2 * a.d + c;
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-      p[k] = acc0[k];
-      p[a.d + k] = acc1[k];
-    }
+    const long ld_p = norm_part_row(a.d);
+    float *p = a.part + blockIdx.y * 2 * ld_p + c;
+    put_sums<VEC>(p, acc0);
+    put_sums<VEC>(p + ld_p, acc1);
   }
 }
 
@@ -423,14 +420,17 @@ cudaError_t bwd_long(const NormArgs &a, int num_sms, int *slots, cudaStream_t s)
 
 // dw_pre, dw_post and a channel gate's gradient from the blocks' column sums:
 // 32 columns per block, the partial rows in 32 interleaved runs joined in order.
+// Where the rows start inside a 16-byte chunk (`mod` elements further into one with
+// every row), so do the partial rows, block b's like row b.
 template <typename T>
-__global__ void __launch_bounds__(1024) norm_columns_kernel(const NormArgs a, int slots) {
+__global__ void __launch_bounds__(1024) norm_columns_kernel(const NormArgs a, int slots, int mod) {
   __shared__ float sh[32][32];
+  const long ld_p = norm_part_row(a.d);
   pdl_wait();
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), run = threadIdx.x >> 5, k = blockIdx.y;
   float v = 0.f;
   if (c < a.d)
-    for (int b = run; b < slots; b += 32) v += a.part[(static_cast<long>(b) * 2 + k) * a.d + c];
+    for (int b = run; b < slots; b += 32) v += a.part[(b * 2L + k) * ld_p + c + row_shift<T>(mod, b)];
   sh[run][threadIdx.x & 31] = v;
   __syncthreads();
   if (run || c >= a.d) return;
@@ -549,13 +549,14 @@ cudaError_t bwd_vec(const NormArgs &a, int num_sms, int *slots, cudaStream_t s) 
 
 template <typename T>
 cudaError_t bwd_type(const NormArgs &a, int num_sms, cudaStream_t s) {
-  int slots = 0;
+  int slots = 0, mod = 0;
   if (a.rows > 0) {
     cudaError_t e;
     HostTrace t("norm_backward", s);
     const bool vec = all_vec<T>(a);
     if (a.rows > num_sms && norm_ring_fits(a, true)) {
       e = launch_norm_bwd_ring(a, num_sms, &slots, s);
+      mod = static_cast<int>(a.ld_z % Elem<T>::VEC);
     } else if (a.d > norm_long(a.dtype)) {
       e = vec ? bwd_long<T, Elem<T>::VEC>(a, num_sms, &slots, s) : bwd_long<T, 1>(a, num_sms, &slots, s);
     } else {
@@ -566,8 +567,8 @@ cudaError_t bwd_type(const NormArgs &a, int num_sms, cudaStream_t s) {
   if (!a.part) return cudaSuccess;
   HostTrace t("norm_columns", s);
   const dim3 grid((a.d + 31) / 32, 2);
-  if (a.rows > 0) return launch_early(norm_columns_kernel<T>, grid, 1024, s, a, slots);
-  norm_columns_kernel<T><<<grid, 1024, 0, s>>>(a, slots);
+  if (a.rows > 0) return launch_early(norm_columns_kernel<T>, grid, 1024, s, a, slots, mod);
+  norm_columns_kernel<T><<<grid, 1024, 0, s>>>(a, slots, mod);
   return cudaGetLastError();
 }
 

@@ -195,4 +195,22 @@ bool norm_ring_fits(const NormArgs &a, bool backward);
 cudaError_t launch_norm_fwd_ring(const NormArgs &a, int num_sms, cudaStream_t s);
 cudaError_t launch_norm_bwd_ring(const NormArgs &a, int num_sms, int *slots, cudaStream_t s);
 
+// How far into a 16-byte chunk the rows of block b start, in elements.
+template <typename T>
+MOE_DEV int row_shift(long ld, long row) {
+  return static_cast<int>((row % Elem<T>::VEC) * (ld % Elem<T>::VEC) % Elem<T>::VEC);
+}
+
+// One thread's column sums into a partial row.
+template <int VEC>
+MOE_DEV void put_sums(float *p, const float *v) {
+  if constexpr (VEC % 4 == 0) {
+#pragma unroll
+    for (int k = 0; k < VEC; k += 4) *reinterpret_cast<float4 *>(p + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) p[k] = v[k];
+  }
+}
+
 }  // namespace moe

@@ -54,7 +54,14 @@ template <typename T, bool EDGES>
 struct Columns {
   static constexpr int VEC = Elem<T>::VEC;
   int c0, step, d;
-  MOE_DEV Columns(int cols, int shift) : c0(threadIdx.x * VEC - (EDGES ? shift : 0)), step(blockDim.x * VEC), d(cols) {}
+  uint32_t head[4];  // bits of the first chunk that are the row's
+  MOE_DEV Columns(int cols, int shift) : c0(threadIdx.x * VEC - (EDGES ? shift : 0)), step(blockDim.x * VEC), d(cols) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int out = lo(0) * static_cast<int>(sizeof(T)) - 4 * k;  // bytes of the word in front of the row
+      head[k] = out >= 4 ? 0u : (out == 2 ? 0xffff0000u : 0xffffffffu);
+    }
+  }
   MOE_DEV int at(int i) const { return c0 + i * step; }
   MOE_DEV bool has(int i) const { return at(i) < d; }
   MOE_DEV int lo(int i) const { return EDGES && at(i) < 0 ? -at(i) : 0; }
@@ -63,18 +70,16 @@ struct Columns {
   // bytes of the chunk that lie in the row or before it
   MOE_DEV int bytes(int i) const { return EDGES ? hi(i) * static_cast<int>(sizeof(T)) : 16; }
 
-  MOE_DEV void unpack(int i, const uint4 &q, f32x2 *p) const {
-    if (whole(i)) {
-      unpack_pairs<T>(q, p);
-    } else {
-      float v[VEC];
-      Elem<T>::unpack(q, v);
-#pragma unroll
-      for (int k = 0; k < VEC; ++k)
-        if (k < lo(i) || k >= hi(i)) v[k] = 0.f;
-#pragma unroll
-      for (int k = 0; k < VEC / 2; ++k) p[k] = f2_of(v[2 * k], v[2 * k + 1]);
+  // what the copy left in shared memory: it filled up with zeros behind the row's end; in
+  // front of its start (thread 0's first chunk) stands the end of the row before
+  MOE_DEV void unpack(int i, uint4 q, f32x2 *p) const {
+    if (EDGES && i == 0) {
+      q.x &= head[0];
+      q.y &= head[1];
+      q.z &= head[2];
+      q.w &= head[3];
     }
+    unpack_pairs<T>(q, p);
   }
   // at column at(0) + i * step of the row that `row0` points at column at(0) of
   MOE_DEV void store(int i, T *row0, const f32x2 *p) const {
@@ -115,12 +120,6 @@ MOE_DEV void own_weights(const NormArgs &a, const Columns<T, EDGES> &col, f32x2 
       w[i][k] = f2_of(v[2 * k] * g[2 * k], v[2 * k + 1] * g[2 * k + 1]);
     }
   }
-}
-
-// How far into a 16-byte chunk the rows of block b start, in elements.
-template <typename T>
-MOE_DEV int row_shift(long ld, long row) {
-  return static_cast<int>((row % Elem<T>::VEC) * (ld % Elem<T>::VEC) % Elem<T>::VEC);
 }
 
 // ---------------------------------------------------------------- forward
@@ -388,20 +387,21 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) norm_bwd_ring
     __syncthreads();
   }
   if (a.part) {
-    float *p = a.part + static_cast<long>(blockIdx.x) * 2 * a.d;
+    // by place in the chunks: columns that are not the row's hold zeros and are not read
+    const long ld_p = norm_part_row(a.d);
+    float *p = a.part + blockIdx.x * 2 * ld_p + threadIdx.x * VEC;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i)
-      if (col.has(i))
+      if (col.has(i)) {
+        float u[VEC], v[VEC];
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) {
-          float u[2], v[2];
-          f2_split(acc0[i][k / 2], u[0], u[1]);
-          f2_split(acc1[i][k / 2], v[0], v[1]);
-          if (k >= col.lo(i) && k < col.hi(i)) {
-            p[col.at(i) + k] = u[k & 1];
-            p[a.d + col.at(i) + k] = v[k & 1];
-          }
+        for (int k = 0; k < P; ++k) {
+          f2_split(acc0[i][k], u[2 * k], u[2 * k + 1]);
+          f2_split(acc1[i][k], v[2 * k], v[2 * k + 1]);
         }
+        put_sums<VEC>(p + i * col.step, u);
+        put_sums<VEC>(p + ld_p + i * col.step, v);
+      }
   }
 }
 
