@@ -44,8 +44,14 @@ MOE_DEV void copy_wait(int n) {
 }
 MOE_DEV uint4 lds16(uint32_t at) {
   uint4 q;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(at) : "memory");
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w) : "r"(at));
   return q;
+}
+MOE_DEV void sts_zero16(uint32_t at) { asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0)); }
+// st_stream under a predicate, without a branch.
+MOE_DEV void st_stream_if(bool on, void *p, const uint4 &q) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n @p st.global.cs.v4.b32 [%0], {%1, %2, %3, %4};\n}\n" ::"l"(p),
+               "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w), "r"(static_cast<uint32_t>(on)));
 }
 
 // One thread's columns of a row: chunk i covers the VEC columns from at(i) on, of
@@ -66,7 +72,15 @@ struct Columns {
   MOE_DEV bool has(int i) const { return at(i) < d; }
   MOE_DEV int lo(int i) const { return EDGES && at(i) < 0 ? -at(i) : 0; }
   MOE_DEV int hi(int i) const { return EDGES && d - at(i) < VEC ? d - at(i) : VEC; }
-  MOE_DEV bool whole(int i) const { return !EDGES || (at(i) >= 0 && at(i) + VEC <= d); }
+  MOE_DEV bool whole(int i) const { return EDGES ? at(i) >= 0 && at(i) + VEC <= d : has(i); }
+  // the chunk (ring_shape: at most one) that the row has a part of, or -1
+  MOE_DEV int part() const {
+    int c = -1;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i)
+      if (has(i) && !whole(i)) c = i;
+    return c;
+  }
   // bytes of the chunk that lie in the row or before it
   MOE_DEV int bytes(int i) const { return EDGES ? hi(i) * static_cast<int>(sizeof(T)) : 16; }
 
@@ -83,17 +97,18 @@ struct Columns {
   }
   // at column at(0) + i * step of the row that `row0` points at column at(0) of
   MOE_DEV void store(int i, T *row0, const f32x2 *p) const {
+    const uint4 q = pack_pairs<T>(p);
+    if (whole(i)) st_stream(row0 + i * step, q);
+    else store_part(i, row0, q);
+  }
+  MOE_DEV void store_part(int i, T *row0, const uint4 &q) const {
     T *dst = row0 + i * step;
-    if (whole(i)) {
-      st_stream(dst, pack_pairs<T>(p));
-    } else {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-      for (int k = 0; k < VEC / 2; ++k) {
-        float v[2];
-        f2_split(p[k], v[0], v[1]);
-        if (2 * k >= lo(i) && 2 * k < hi(i)) dst[2 * k] = Elem<T>::from(v[0]);
-        if (2 * k + 1 >= lo(i) && 2 * k + 1 < hi(i)) dst[2 * k + 1] = Elem<T>::from(v[1]);
-      }
+    for (int k = 0; k < VEC; ++k) {
+      if (k < lo(i) || k >= hi(i)) continue;
+      if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t *>(dst)[k] = w[k];
+      else reinterpret_cast<uint16_t *>(dst)[k] = static_cast<uint16_t>(w[k / 2] >> (k % 2 * 16));
     }
   }
   MOE_DEV void weights(int i, const void *w, float *v) const {
@@ -287,10 +302,14 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) norm_bwd_ring
     coming += step;
     copy_commit();
   };
-  // a tensor that is not there reads as zeros
-  auto take = [&](uint32_t at, int t, int i, f32x2 *p) {
-    col.unpack(i, src[t] && col.has(i) ? lds16(at + (t * kChunks + i) * place) : make_uint4(0, 0, 0, 0), p);
-  };
+  // a tensor or chunk that is not there reads as zeros
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i)
+      if (!src[t] || !col.has(i))
+        for (int k = 0; k < stages; ++k) sts_zero16(base + k * stage_bytes + (t * kChunks + i) * place);
+  auto take = [&](uint32_t at, int t, int i, f32x2 *p) { col.unpack(i, lds16(at + (t * kChunks + i) * place), p); };
   for (int k = 0; k + 1 < stages; ++k) fetch(base + k * stage_bytes);
   f32x2 wp[kChunks][P], w[kChunks][P], acc0[kChunks][P], acc1[kChunks][P];
   own_weights<T, EDGES>(a, col, wp, w);
@@ -328,6 +347,16 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) norm_bwd_ring
     for (int k = 0; k < 4; ++k) s[k] = f2_sum(s2[k]);
     block_sums_put<4>(s, out);
   };
+  // straight-line code: the chunks' arithmetic then runs side by side.  A chunk that the
+  // row has a part of waits for the end of the row (8000 x 2883: 117 us with its stores
+  // in a branch of each chunk)
+  uint4 edge[3];
+  const int part = EDGES ? col.part() : -1;
+  auto put = [&](T *dst, int i, const f32x2 *p, uint4 &e) {
+    const uint4 q = pack_pairs<T>(p);
+    st_stream_if(dst && col.whole(i), dst + i * col.step, q);
+    if (EDGES && (i == 0 || part == i)) e = q;
+  };
   int turn = 0, stage = 0, ahead = stages - 1;
   RowIn in = {}, next = {};
   if (row < a.rows) {
@@ -349,34 +378,38 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) norm_bwd_ring
     const f32x2 rp = f2_both(t.rp), c1 = f2_both(-t.c1), a1 = f2_both(t.a1), c2 = f2_both(-t.c2);
     const uint32_t at = base + stage * stage_bytes;
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i)
-      if (col.has(i)) {
-        f32x2 dz[P], dh[P], z[P], f[P], g[P], o[P];
-        take(at, 0, i, dz);
-        take(at, 1, i, dh);
-        take(at, 2, i, z);
-        take(at, 3, i, f);
-        if (FULL) take(at, NT - 1, i, g);
+    for (int i = 0; i < kChunks; ++i) {
+      f32x2 dz[P], dh[P], z[P], f[P], g[P], o[P];
+      take(at, 0, i, dz);
+      take(at, 1, i, dh);
+      take(at, 2, i, z);
+      take(at, 3, i, f);
+      if (FULL) take(at, NT - 1, i, g);
 #pragma unroll
-        for (int k = 0; k < P; ++k) {
-          const f32x2 y = f2_mul(rp, z[k]);
-          const f32x2 tt = f2_fma(rp, f2_mul(dh[k], wp[i][k]), f2_fma(c1, y, dz[k]));
-          acc0[i][k] = f2_fma(dh[k], y, acc0[i][k]);
-          const f32x2 nh = f2_mul(f[k], a1);
-          f32x2 tg = tt, tw = f2_mul(tt, w[i][k]);
-          if (FULL) {
-            o[k] = f2_mul(tw, nh);
-            tg = f2_mul(tg, g[k]);
-            tw = f2_mul(tw, g[k]);
-          }
-          acc1[i][k] = f2_fma(tg, nh, acc1[i][k]);
-          dz[k] = f2_mul(alpha, tt);
-          f[k] = f2_fma(a1, tw, f2_mul(c2, f[k]));
+      for (int k = 0; k < P; ++k) {
+        const f32x2 y = f2_mul(rp, z[k]);
+        const f32x2 tt = f2_fma(rp, f2_mul(dh[k], wp[i][k]), f2_fma(c1, y, dz[k]));
+        acc0[i][k] = f2_fma(dh[k], y, acc0[i][k]);
+        const f32x2 nh = f2_mul(f[k], a1);
+        f32x2 tg = tt, tw = f2_mul(tt, w[i][k]);
+        if (FULL) {
+          o[k] = f2_mul(tw, nh);
+          tg = f2_mul(tg, g[k]);
+          tw = f2_mul(tw, g[k]);
         }
-        if (dx) col.store(i, dx, dz);
-        if (df) col.store(i, df, f);
-        if (FULL && dg) col.store(i, dg, o);
+        acc1[i][k] = f2_fma(tg, nh, acc1[i][k]);
+        dz[k] = f2_mul(alpha, tt);
+        f[k] = f2_fma(a1, tw, f2_mul(c2, f[k]));
       }
+      put(dx, i, dz, edge[0]);
+      put(df, i, f, edge[1]);
+      if (FULL) put(dg, i, o, edge[2]);
+    }
+    if (EDGES && part >= 0) {
+      if (dx) col.store_part(part, dx, edge[0]);
+      if (df) col.store_part(part, df, edge[1]);
+      if (FULL && dg) col.store_part(part, dg, edge[2]);
+    }
     if (dx) dx += step * a.ld_x;
     if (df) df += step * a.ld_f;
     if (FULL && dg) dg += step * a.ld_g;
@@ -425,6 +458,8 @@ RingShape ring_shape(const NormArgs &a, bool backward) {
   const int nt = (backward ? 4 : 2) + (a.gate == MOE_GATE_FULL ? 1 : 0);
   const int per = kChunks * vec;
   r.threads = ((a.d + (m ? vec - 1 : 0) + per - 1) / per + 31) / 32 * 32;
+  // no thread has parts of two chunks: thread 0's second one would be the row's last
+  if (m && a.d > r.threads * vec - vec && a.d < r.threads * vec + vec) r.threads += 32;
   if (r.threads > (backward ? 512 : 1024)) return r;
   const size_t stage = static_cast<size_t>(r.threads) * kChunks * 16 * nt * (backward ? 1 : fwd_rows(r.threads));
   // short rows: three stages and more blocks
