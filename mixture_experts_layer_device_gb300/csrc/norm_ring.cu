@@ -48,7 +48,12 @@ MOE_DEV uint4 lds16(uint32_t at) {
   return q;
 }
 MOE_DEV void sts_zero16(uint32_t at) { asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0)); }
-// st_stream under a predicate, without a branch.
+// Under a predicate, without a branch: 16 bytes to shared memory, and st_stream.
+MOE_DEV void sts16_if(bool on, uint32_t at, const uint4 &q) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n @p st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n}\n" ::"r"(at),
+               "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w), "r"(static_cast<uint32_t>(on))
+               : "memory");
+}
 MOE_DEV void st_stream_if(bool on, void *p, const uint4 &q) {
   asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %5, 0;\n @p st.global.cs.v4.b32 [%0], {%1, %2, %3, %4};\n}\n" ::"l"(p),
                "r"(q.x), "r"(q.y), "r"(q.z), "r"(q.w), "r"(static_cast<uint32_t>(on)));
@@ -73,14 +78,6 @@ struct Columns {
   MOE_DEV int lo(int i) const { return EDGES && at(i) < 0 ? -at(i) : 0; }
   MOE_DEV int hi(int i) const { return EDGES && d - at(i) < VEC ? d - at(i) : VEC; }
   MOE_DEV bool whole(int i) const { return EDGES ? at(i) >= 0 && at(i) + VEC <= d : has(i); }
-  // the chunk (ring_shape: at most one) that the row has a part of, or -1
-  MOE_DEV int part() const {
-    int c = -1;
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i)
-      if (has(i) && !whole(i)) c = i;
-    return c;
-  }
   // bytes of the chunk that lie in the row or before it
   MOE_DEV int bytes(int i) const { return EDGES ? hi(i) * static_cast<int>(sizeof(T)) : 16; }
 
@@ -97,18 +94,18 @@ struct Columns {
   }
   // at column at(0) + i * step of the row that `row0` points at column at(0) of
   MOE_DEV void store(int i, T *row0, const f32x2 *p) const {
-    const uint4 q = pack_pairs<T>(p);
-    if (whole(i)) st_stream(row0 + i * step, q);
-    else store_part(i, row0, q);
-  }
-  MOE_DEV void store_part(int i, T *row0, const uint4 &q) const {
     T *dst = row0 + i * step;
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    const uint4 q = pack_pairs<T>(p);
+    if (whole(i)) {
+      st_stream(dst, q);
+    } else {
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) {
-      if (k < lo(i) || k >= hi(i)) continue;
-      if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t *>(dst)[k] = w[k];
-      else reinterpret_cast<uint16_t *>(dst)[k] = static_cast<uint16_t>(w[k / 2] >> (k % 2 * 16));
+      for (int k = 0; k < VEC; ++k) {
+        if (k < lo(i) || k >= hi(i)) continue;
+        if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t *>(dst)[k] = w[k];
+        else reinterpret_cast<uint16_t *>(dst)[k] = static_cast<uint16_t>(w[k / 2] >> (k % 2 * 16));
+      }
     }
   }
   MOE_DEV void weights(int i, const void *w, float *v) const {
@@ -347,17 +344,27 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) norm_bwd_ring
     for (int k = 0; k < 4; ++k) s[k] = f2_sum(s2[k]);
     block_sums_put<4>(s, out);
   };
-  // straight-line code: the chunks' arithmetic then runs side by side.  A chunk that the
-  // row has a part of waits for the end of the row (8000 x 2883: 117 us with its stores
-  // in a branch of each chunk)
-  uint4 edge[3];
-  const int part = EDGES ? col.part() : -1;
-  auto put = [&](T *dst, int i, const f32x2 *p, uint4 &e) {
+  // Straight-line code: the chunks' arithmetic then runs side by side.  The chunks that
+  // the row has a part of, its first and last, go to shared memory and leave after the
+  // row's barrier, an element per thread (from the one thread that has them, 8000 x 2883:
+  // 118 us where this takes 97).
+  __shared__ __align__(16) uint4 parts[2][3][2];  // [turn][dx, df, dg][first, last]
+  int turn = 0;
+  auto put = [&](T *dst, int t, int i, const f32x2 *p) {
     const uint4 q = pack_pairs<T>(p);
     st_stream_if(dst && col.whole(i), dst + i * col.step, q);
-    if (EDGES && (i == 0 || part == i)) e = q;
+    if (EDGES) sts16_if(col.has(i) && !col.whole(i), smem_u32(&parts[turn][t][col.at(i) < 0 ? 0 : 1]), q);
   };
-  int turn = 0, stage = 0, ahead = stages - 1;
+  auto put_parts = [&](int of, long r) {
+    const int shift = row_shift<T>(a.ld_z, blockIdx.x), last = (a.d + shift) / VEC * VEC - shift;
+    for (int j = threadIdx.x; j < 3 * 2 * VEC; j += blockDim.x) {
+      const int t = j / (2 * VEC), side = j / VEC % 2, k = j % VEC, c = side ? last + k : k - shift;
+      T *out = static_cast<T *>(t == 0 ? a.dx : (t == 1 ? a.df : (FULL ? a.dg : nullptr)));
+      if (out && (side ? c < a.d : c >= 0 && shift > 0))
+        out[r * (t == 0 ? a.ld_x : (t == 1 ? a.ld_f : a.ld_g)) + c] = reinterpret_cast<const T *>(&parts[of][t][side])[k];
+    }
+  };
+  int stage = 0, ahead = stages - 1;
   RowIn in = {}, next = {};
   if (row < a.rows) {
     in = row_in<T>(a, row);
@@ -367,6 +374,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) norm_bwd_ring
   __syncthreads();
   for (; row < a.rows; row += step) {
     const bool more = row + step < a.rows;
+    if (EDGES && row > blockIdx.x) put_parts(turn ^ 1, row - step);
     if (more) next = row_in<T>(a, row + step);
     fetch(base + ahead * stage_bytes);
     copy_wait(stages - 2);
@@ -401,14 +409,9 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) norm_bwd_ring
         dz[k] = f2_mul(alpha, tt);
         f[k] = f2_fma(a1, tw, f2_mul(c2, f[k]));
       }
-      put(dx, i, dz, edge[0]);
-      put(df, i, f, edge[1]);
-      if (FULL) put(dg, i, o, edge[2]);
-    }
-    if (EDGES && part >= 0) {
-      if (dx) col.store_part(part, dx, edge[0]);
-      if (df) col.store_part(part, df, edge[1]);
-      if (FULL && dg) col.store_part(part, dg, edge[2]);
+      put(dx, 0, i, dz);
+      put(df, 1, i, f);
+      if (FULL) put(dg, 2, i, o);
     }
     if (dx) dx += step * a.ld_x;
     if (df) df += step * a.ld_f;
@@ -419,6 +422,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) norm_bwd_ring
     if (++ahead == stages) ahead = 0;
     __syncthreads();
   }
+  if (EDGES && row > blockIdx.x) put_parts(turn ^ 1, row - step);
   if (a.part) {
     // by place in the chunks: columns that are not the row's hold zeros and are not read
     const long ld_p = norm_part_row(a.d);
@@ -458,8 +462,6 @@ RingShape ring_shape(const NormArgs &a, bool backward) {
   const int nt = (backward ? 4 : 2) + (a.gate == MOE_GATE_FULL ? 1 : 0);
   const int per = kChunks * vec;
   r.threads = ((a.d + (m ? vec - 1 : 0) + per - 1) / per + 31) / 32 * 32;
-  // no thread has parts of two chunks: thread 0's second one would be the row's last
-  if (m && a.d > r.threads * vec - vec && a.d < r.threads * vec + vec) r.threads += 32;
   if (r.threads > (backward ? 512 : 1024)) return r;
   const size_t stage = static_cast<size_t>(r.threads) * kChunks * 16 * nt * (backward ? 1 : fwd_rows(r.threads));
   // short rows: three stages and more blocks
