@@ -19,10 +19,10 @@ namespace moe {
 
 namespace {
 
-// Rows that share the forward's two barriers: three where a row takes most of a
-// block's registers and shared memory (16384 x 7168: 154 us, 171 with two), else two
-// (16384 x 4096: 93 us, 98 with three).
-__host__ __device__ constexpr int fwd_rows(int threads) { return threads > 384 && threads <= 512 ? 3 : 2; }
+// Rows that share the forward's two barriers: two where two blocks fit an SM (16384 x
+// 4096: 88 us, 98 with three), three where one takes most of its registers and shared
+// memory (16384 x 7168: 150 us, 171 with two; x 5120: 121 and 138).
+__host__ __device__ constexpr int fwd_rows(int threads) { return threads > 288 && threads <= 512 ? 3 : 2; }
 constexpr int kRingSmem = 232448 - 2048;
 
 // 16-byte chunks of a row per thread: 16 columns of a 2-byte type, 8 of fp32 (in
@@ -138,7 +138,7 @@ MOE_DEV void own_weights(const NormArgs &a, const Columns<T, EDGES> &col, f32x2 
 // fwd_rows() rows at a time (a grid apart): their sums share the barriers.  Shared
 // memory: [stage][row][x, f, full gate][chunk][thread] of 16 bytes.
 template <typename T, bool FULL, bool EDGES, int THREADS>
-__global__ void __launch_bounds__(THREADS) norm_fwd_ring_kernel(const NormArgs a, int stages) {
+__global__ void __launch_bounds__(THREADS, THREADS <= 288 ? 2 : 1) norm_fwd_ring_kernel(const NormArgs a, int stages) {
   constexpr int P = Elem<T>::VEC / 2, NT = FULL ? 3 : 2, R = fwd_rows(THREADS), SUMS = R > 2 ? 4 : R;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float red[2][SUMS][kMaxWarps];
@@ -465,7 +465,7 @@ RingShape ring_shape(const NormArgs &a, bool backward) {
   if (r.threads > (backward ? 512 : 1024)) return r;
   const size_t stage = static_cast<size_t>(r.threads) * kChunks * 16 * nt * (backward ? 1 : fwd_rows(r.threads));
   // short rows: three stages and more blocks
-  for (int s = r.threads <= 256 ? 3 : 4; s >= 2; --s)
+  for (int s = r.threads <= (backward ? 256 : 288) ? 3 : 4; s >= 2; --s)
     if (stage * s <= kRingSmem) {
       r.stages = s;
       r.smem = stage * s;
@@ -506,10 +506,12 @@ cudaError_t bwd_shape(const NormArgs &a, const RingShape &r, int num_sms, int *s
 }
 
 // Block sizes by the registers that they leave a thread: up to 256 threads two
-// blocks (128), 384 (168), 512 (128), 1024 (64).
+// blocks (128), the forward's 288 too (112; 16384 x 4608: 97 us, 134 with one block),
+// the backward's 384 one (168), 512 (128), 1024 (64).
 template <typename T, bool FULL, bool EDGES>
 cudaError_t fwd_block(const NormArgs &a, const RingShape &r, int num_sms, cudaStream_t s) {
-  if (r.threads <= 384) return fwd_shape<T, FULL, EDGES, 384>(a, r, num_sms, s);
+  if (r.threads <= 256) return fwd_shape<T, FULL, EDGES, 256>(a, r, num_sms, s);
+  if (r.threads <= 288) return fwd_shape<T, FULL, EDGES, 288>(a, r, num_sms, s);
   if (r.threads <= 512) return fwd_shape<T, FULL, EDGES, 512>(a, r, num_sms, s);
   return fwd_shape<T, FULL, EDGES, 1024>(a, r, num_sms, s);
 }
