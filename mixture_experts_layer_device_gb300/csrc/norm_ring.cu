@@ -108,6 +108,13 @@ struct Columns {
       }
     }
   }
+  // The same without a branch; a chunk that the row has only a part of goes to parts[0]
+  // (its first) or parts[1] (its last), for put_part after a barrier.
+  MOE_DEV void store_or_keep(bool on, int i, T *row0, const f32x2 *p, uint4 *parts) const {
+    const uint4 q = pack_pairs<T>(p);
+    st_stream_if(on && whole(i), row0 + i * step, q);
+    if (EDGES) sts16_if(has(i) && !whole(i), smem_u32(parts + (at(i) < 0 ? 0 : 1)), q);
+  }
   MOE_DEV void weights(int i, const void *w, float *v) const {
     const T *p = static_cast<const T *>(w);
 #pragma unroll
@@ -134,6 +141,14 @@ MOE_DEV void own_weights(const NormArgs &a, const Columns<T, EDGES> &col, f32x2 
   }
 }
 
+// Element j of a row's first and last chunk (Columns::store_or_keep) to the row; j < 2 VEC.
+template <typename T>
+MOE_DEV void put_part(T *row, int d, int shift, int j, const uint4 *parts) {
+  constexpr int VEC = Elem<T>::VEC;
+  const int last = j / VEC, k = j % VEC, c = last ? (d + shift) / VEC * VEC - shift + k : k - shift;
+  if (last ? c < d : c >= 0 && shift > 0) row[c] = reinterpret_cast<const T *>(parts + last)[k];
+}
+
 // ---------------------------------------------------------------- forward
 // fwd_rows() rows at a time (a grid apart): their sums share the barriers.  Shared
 // memory: [stage][row][x, f, full gate][chunk][thread] of 16 bytes.
@@ -142,7 +157,14 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 288 ? 2 : 1) norm_fwd_ring
   constexpr int P = Elem<T>::VEC / 2, NT = FULL ? 3 : 2, R = fwd_rows(THREADS), SUMS = R > 2 ? 4 : R;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float red[2][SUMS][kMaxWarps];
-  const Columns<T, EDGES> col(a.d, row_shift<T>(a.ld_x, blockIdx.x));
+  // as in the backward, the rows' first and last chunks leave after a barrier (8000 x 2883
+  // with a full gate: 48 us, 53 from the threads that have them), but where registers are
+  // short (16384 x 4095: 128 us so, 113)
+  constexpr bool KEEP = EDGES && THREADS <= 256;
+  __shared__ __align__(16) uint4 parts[2][R][2][2];  // [turn][row][z, h][first, last]
+  int part_turn = 0;
+  const int shift = row_shift<T>(a.ld_x, blockIdx.x);
+  const Columns<T, EDGES> col(a.d, shift);
   const uint32_t place = 16 * blockDim.x, stage_bytes = R * NT * kChunks * place;
   const uint32_t base = smem_u32(smem) + 16 * threadIdx.x;
   const float inv_d = 1.f / static_cast<float>(a.d);
@@ -165,6 +187,10 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 288 ? 2 : 1) norm_fwd_ring
       }
     }
     copy_commit();
+  };
+  auto put = [&](int i, T *row0, const f32x2 *p, uint4 *parts_of) {
+    if (KEEP) col.store_or_keep(true, i, row0, p, parts_of);
+    else col.store(i, row0, p);
   };
   long row = blockIdx.x;
   for (int k = 0; k + 1 < stages; ++k) fetch(row + k * step, base + k * stage_bytes);
@@ -227,7 +253,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 288 ? 2 : 1) norm_fwd_ring
             sum = f2_fma(z[r][i][k], z[r][i][k], sum);
           }
           if (a.z && row + r * G < a.rows)
-            col.store(i, static_cast<T *>(a.z) + (row + r * G) * a.ld_z + col.at(0), z[r][i]);
+            put(i, static_cast<T *>(a.z) + (row + r * G) * a.ld_z + col.at(0), z[r][i], parts[part_turn][r][0]);
         }
       }
       ss[r] = f2_sum(sum);
@@ -245,9 +271,20 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 288 ? 2 : 1) norm_fwd_ring
           if (col.has(i)) {
 #pragma unroll
             for (int k = 0; k < P; ++k) z[r][i][k] = f2_mul(z[r][i][k], f2_mul(rr, wp[i][k]));
-            col.store(i, static_cast<T *>(a.h) + (row + r * G) * a.ld_h + col.at(0), z[r][i]);
+            put(i, static_cast<T *>(a.h) + (row + r * G) * a.ld_h + col.at(0), z[r][i], parts[part_turn][r][1]);
           }
       }
+    }
+    if (KEEP) {
+      constexpr int N = 2 * Elem<T>::VEC;
+      __syncthreads();
+      for (int j = threadIdx.x; j < R * 2 * N; j += blockDim.x) {
+        const int r = j / (2 * N), t = j / N % 2;
+        T *out = static_cast<T *>(t ? a.h : a.z);
+        if (out && row + r * G < a.rows)
+          put_part(out + (row + r * G) * (t ? a.ld_h : a.ld_z), a.d, shift, j % N, parts[part_turn][r][t]);
+      }
+      part_turn ^= 1;
     }
     if (++stage == stages) stage = 0;
     if (++ahead == stages) ahead = 0;
@@ -266,7 +303,8 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) norm_bwd_ring
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float red[2][4][kMaxWarps];
   long row = blockIdx.x;
-  const Columns<T, EDGES> col(a.d, row_shift<T>(a.ld_z, row));
+  const int shift = row_shift<T>(a.ld_z, row);
+  const Columns<T, EDGES> col(a.d, shift);
   const uint32_t place = 16 * blockDim.x, stage_bytes = NT * kChunks * place;
   const uint32_t base = smem_u32(smem) + 16 * threadIdx.x;
   const float inv_d = 1.f / static_cast<float>(a.d);
@@ -350,18 +388,11 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) norm_bwd_ring
   // 118 us where this takes 97).
   __shared__ __align__(16) uint4 parts[2][3][2];  // [turn][dx, df, dg][first, last]
   int turn = 0;
-  auto put = [&](T *dst, int t, int i, const f32x2 *p) {
-    const uint4 q = pack_pairs<T>(p);
-    st_stream_if(dst && col.whole(i), dst + i * col.step, q);
-    if (EDGES) sts16_if(col.has(i) && !col.whole(i), smem_u32(&parts[turn][t][col.at(i) < 0 ? 0 : 1]), q);
-  };
   auto put_parts = [&](int of, long r) {
-    const int shift = row_shift<T>(a.ld_z, blockIdx.x), last = (a.d + shift) / VEC * VEC - shift;
     for (int j = threadIdx.x; j < 3 * 2 * VEC; j += blockDim.x) {
-      const int t = j / (2 * VEC), side = j / VEC % 2, k = j % VEC, c = side ? last + k : k - shift;
+      const int t = j / (2 * VEC);
       T *out = static_cast<T *>(t == 0 ? a.dx : (t == 1 ? a.df : (FULL ? a.dg : nullptr)));
-      if (out && (side ? c < a.d : c >= 0 && shift > 0))
-        out[r * (t == 0 ? a.ld_x : (t == 1 ? a.ld_f : a.ld_g)) + c] = reinterpret_cast<const T *>(&parts[of][t][side])[k];
+      if (out) put_part(out + r * (t == 0 ? a.ld_x : (t == 1 ? a.ld_f : a.ld_g)), a.d, shift, j % (2 * VEC), parts[of][t]);
     }
   };
   int stage = 0, ahead = stages - 1;
@@ -409,9 +440,9 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) norm_bwd_ring
         dz[k] = f2_mul(alpha, tt);
         f[k] = f2_fma(a1, tw, f2_mul(c2, f[k]));
       }
-      put(dx, 0, i, dz);
-      put(df, 1, i, f);
-      if (FULL) put(dg, 2, i, o);
+      col.store_or_keep(dx, i, dx, dz, parts[turn][0]);
+      col.store_or_keep(df, i, df, f, parts[turn][1]);
+      if (FULL) col.store_or_keep(dg, i, dg, o, parts[turn][2]);
     }
     if (dx) dx += step * a.ld_x;
     if (df) df += step * a.ld_f;
@@ -506,7 +537,7 @@ cudaError_t bwd_shape(const NormArgs &a, const RingShape &r, int num_sms, int *s
 }
 
 // Block sizes by the registers that they leave a thread: up to 256 threads two
-// blocks (128), the forward's 288 too (112; 16384 x 4608: 97 us, 134 with one block),
+// blocks (128), the forward's 288 too (96; 16384 x 4608: 97 us, 134 with one block),
 // the backward's 384 one (168), 512 (128), 1024 (64).
 template <typename T, bool FULL, bool EDGES>
 cudaError_t fwd_block(const NormArgs &a, const RingShape &r, int num_sms, cudaStream_t s) {

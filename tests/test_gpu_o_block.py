@@ -548,3 +548,72 @@ def test_grouped_past_32_bits(blk):
         y = blk.grouped_forward(x, w, off)
         for lo, hi, e in ((0, rows // 2, E - 2), (rows // 2, rows, E - 1)):
             close(y[lo:hi], f64(x[lo:hi]) @ f64(w[e]).T, np.abs(f64(x[lo:hi])) @ np.abs(f64(w[e])).T, K)
+
+
+# ---------------------------------------------------------------- rows that share chunks, launches that overlap
+@pytest.mark.parametrize("rows,d", [(2000, 515), (1700, 1027), (1100, 2883), (700, 4095), (700, 4604)])
+@pytest.mark.parametrize("kind,post,pre", [("full", True, True), ("row", False, True), ("channel", True, False),
+                                           ("none", False, False)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_norm_many_rows_of_odd_width(blk, rows, d, kind, post, pre, dtype):
+    check_norm(blk, rows, d, dtype, kind, post, pre, 0.75, seed=d)
+
+
+@pytest.mark.parametrize("d", [515, 2883, 4095, 7167])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_norm_neighbours_stay_apart(blk, d, dtype):
+    """A row's chunks hold columns of the rows beside it: what is not finite there stays there."""
+    rows = 700
+    x, f, gate, w_post, w_pre = norm_inputs(rows, d, dtype, "full", 3)
+    g = gen(4)
+    dz, dh = draw((rows, d), dtype, g), draw((rows, d), dtype, g)
+    kw = dict(gate_kind="full", alpha=0.5)
+
+    def run(bad):
+        t = [v.clone() for v in (x, f, gate, dz, dh)]
+        if bad:
+            for i, v in enumerate(t):
+                v[1::2] = (float("nan"), float("inf"), float("-inf"))[i % 3]
+        z, h, r_post, r_pre = blk.norm_forward(t[0], t[1], t[2], w_post, w_pre, **kw)
+        dx, df, dg = blk.norm_backward(t[3], t[4], z, t[1], t[2], w_post, w_pre, r_post, r_pre, **kw)[:3]
+        return [v[::2] for v in (z, h, r_post, r_pre, dx, df, dg)]
+
+    for a, b in zip(run(False), run(True)):
+        assert torch.equal(a, b)
+
+
+def test_overlapping_launches(blk):
+    """Calls back to back, each read by a kernel right behind it, give what calls one at a time give."""
+    g = gen(9)
+    sizes = [(2043, 8, 512, 768), (900, 24, 128, 256), (3000, 5, 264, 520), (600, 300, 64, 72)]
+    calls = []
+    for rows, E, N, K in sizes:
+        counts = split(rows, E, "skew", rows)
+        counts[0], counts[-1] = 0, counts[-1] + counts[0]
+        off = offsets_of(counts, 0)
+        x, dy, w = draw((rows, K), BF, g), draw((rows, N), BF, g), draw((E, N, K), BF, g, K ** -0.5)
+        calls.append(lambda dy=dy, x=x, w=w, off=off: blk.grouped_backward(dy, x, w, off))
+    big = draw((64, 512, 768), BF, g)  # experts enough that those without rows are written apart
+    few = torch.zeros(65, dtype=torch.int32)
+    few[30:] = 700
+    few = few.cuda()
+    dy, x = draw((700, 512), BF, g), draw((700, 768), BF, g)
+    calls.append(lambda: blk.grouped_backward(dy, x, big, few))
+    for rows, V, d in [(515, 5001, 33), (5000, 700, 128), (70000, 300, 40)]:
+        ids, dout = torch.randint(0, V, (rows,), generator=g, device="cuda"), draw((rows, d), BF, g)
+        calls.append(lambda ids=ids, dout=dout, V=V: (blk.embed_backward(ids, dout, V),))
+    for rows, d in [(700, 2883), (300, 9000), (40, 512)]:
+        x_, f, gate, w_post, w_pre = norm_inputs(rows, d, BF, "channel", d)
+        z, _, r_post, r_pre = blk.norm_forward(x_, f, gate, w_post, w_pre, gate_kind="channel")
+        calls.append(lambda z=z, f=f, gate=gate, a=w_post, b=w_pre, p=r_post, q=r_pre, x_=x_: blk.norm_backward(
+            x_, f, z, f, gate, a, b, p, q, gate_kind="channel"))
+    alone = []
+    for call in calls:
+        out = call()
+        torch.cuda.synchronize()
+        alone.append([t.clone() for t in out])
+        torch.cuda.synchronize()
+    for _ in range(4):
+        copies = [[t.clone() for t in call()] for call in calls]
+        for a, b in zip(alone, copies):
+            assert all(torch.equal(s, t) for s, t in zip(a, b))
