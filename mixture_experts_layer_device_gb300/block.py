@@ -5,8 +5,10 @@ moe_grouped_*, moe_norm_*, moe_embed_*).
 
 Plain functions: they check their arguments, allocate outputs and workspaces
 from torch and call the library; all arithmetic runs in its kernels.  They run
-on torch's current stream, or on `stream`, and do not synchronise.  The
-autograd functions and modules over them are in module.py.
+on torch's current stream and do not synchronise; with `stream` (a stream or its
+handle) they run as under `torch.cuda.stream(stream)`: what they read has to be
+ready on it, and what they return is.  The autograd functions and modules over
+them are in module.py.
 """
 import ctypes
 from functools import lru_cache
@@ -74,13 +76,23 @@ def _ws(plan, device):
     return torch.empty(plan[2], dtype=torch.uint8, device=device)
 
 
-def _used_on(stream, *tensors):
-    """Memory from the current stream's pool that a call on another stream uses."""
+def _on(stream, call, *args, **kw):
+    """The whole call with `stream` as the current one, so that the copies it makes,
+    its outputs and its workspace are in order with its kernels.  The caller's
+    tensors are kept until `stream` has used them, the results until the caller's
+    current stream has."""
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream)
-    for t in tensors:
-        if t is not None:
+    caller = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        out = call(*args, **kw)
+    for t in (*args, *kw.values()):
+        if isinstance(t, torch.Tensor):
             t.record_stream(stream)
+    for t in out if isinstance(out, tuple) else (out,):
+        if t is not None:
+            t.record_stream(caller)
+    return out
 
 
 # ---------------------------------------------------------------- grouped products
@@ -108,6 +120,8 @@ def grouped_forward(x, w, offsets, *, out=None, out_dtype=None, return_workspace
     of expert e (0 for a row of no expert).  x [rows, K] and w [E, N, K] bf16 or
     fp16, offsets int32 [E + 1] on the GPU as moe_route writes them; y of x's
     type or fp32 (out_dtype, or out's)."""
+    if stream is not None:
+        return _on(stream, grouped_forward, x, w, offsets, out=out, out_dtype=out_dtype, return_workspace=return_workspace)
     w, offsets, E, N, K, ld_w = _grouped(x.dtype, w, offsets, "x")
     x, ld_x = _rows(x, "x", K)
     out_dtype = out_dtype or (out.dtype if out is not None else x.dtype)
@@ -118,9 +132,7 @@ def grouped_forward(x, w, offsets, *, out=None, out_dtype=None, return_workspace
     plan = _grouped_plan(x.shape[0], E, N, K, _ELEM[x.dtype], _ELEM[out_dtype], 0, ld_x, ld_y, ld_w, ld_e)
     ws = _ws(plan, x.device)
     check(lib().moe_grouped_forward(plan[1], x.data_ptr(), w.data_ptr(), offsets.data_ptr(), y.data_ptr(),
-                                    ws.data_ptr(), _stream(stream)))
-    if stream is not None:
-        _used_on(stream, x, w, offsets, y, ws)
+                                    ws.data_ptr(), _stream(None)))
     return (y, ws) if return_workspace else y
 
 
@@ -130,6 +142,9 @@ def grouped_backward(dy, x, w, offsets, *, dx=None, dw=None, need_dx=True, need_
     sum of dy[r]^T x[r] over e's rows (zeros for an expert without rows), either
     None when not needed.  dw is of x's type or fp32 (dw_dtype, or dw's); with
     accumulate it must be given, fp32, and is added to."""
+    if stream is not None:
+        return _on(stream, grouped_backward, dy, x, w, offsets, dx=dx, dw=dw, need_dx=need_dx, need_dw=need_dw,
+                   dw_dtype=dw_dtype, accumulate=accumulate, return_workspace=return_workspace)
     w, offsets, E, N, K, ld_w = _grouped(dy.dtype, w, offsets, "dy")
     rows = dy.shape[0]
     dy, ld_y = _rows(dy, "dy", N)
@@ -161,9 +176,7 @@ def grouped_backward(dy, x, w, offsets, *, dx=None, dw=None, need_dx=True, need_
     ws = _ws(plan, dy.device)
     out = (dx if need_dx else None, dw if need_dw else None)
     check(lib().moe_grouped_backward(plan[1], dy.data_ptr(), x.data_ptr(), w.data_ptr(), offsets.data_ptr(),
-                                     _ptr(out[0]), _ptr(out[1]), ws.data_ptr(), _stream(stream)))
-    if stream is not None:
-        _used_on(stream, dy, x, w, offsets, out[0], out[1], ws)
+                                     _ptr(out[0]), _ptr(out[1]), ws.data_ptr(), _stream(None)))
     return out + (ws,) if return_workspace else out
 
 
@@ -200,6 +213,9 @@ def norm_forward(x, f=None, gate=None, w_post=None, w_pre=None, *, gate_kind="no
     "full"; w_post and w_pre [d] or None (ones); all of one type (bf16, fp16,
     fp32).  r_post, r_pre [rows] fp32 are the reciprocal roots for the backward;
     what is not computed comes back as None."""
+    if stream is not None:
+        return _on(stream, norm_forward, x, f, gate, w_post, w_pre, gate_kind=gate_kind, post=post, pre=pre, alpha=alpha,
+                   eps=eps, need_z=need_z, z=z, h=h)
     if not (x.dim() == 2 and x.dtype in _ELEM):
         _bad("x must be a bf16, fp16 or fp32 matrix [rows, d]")
     rows, d = x.shape
@@ -226,9 +242,7 @@ def norm_forward(x, f=None, gate=None, w_post=None, w_pre=None, *, gate_kind="no
                       GATES[gate_kind], alpha, eps, ld_x, ld_f, ld_z, ld_h, ld_g)
     z, h = z if need_z else None, h if pre else None
     check(lib().moe_norm_forward(plan[1], x.data_ptr(), _ptr(f), _ptr(gate), _ptr(w_post), _ptr(w_pre), _ptr(z),
-                                 _ptr(h), _ptr(r_post), _ptr(r_pre), _stream(stream)))
-    if stream is not None:
-        _used_on(stream, x, f, gate, w_post, w_pre, z, h, r_post, r_pre)
+                                 _ptr(h), _ptr(r_post), _ptr(r_pre), _stream(None)))
     return z, h, r_post, r_pre
 
 
@@ -238,6 +252,9 @@ def norm_backward(dz, dh, z, f=None, gate=None, w_post=None, w_pre=None, r_post=
     """(dx, df, dgate, dw_post, dw_pre) of norm_forward from the gradients dz
     (None: nothing but h is used) and dh, its z, f and reciprocal roots; what
     does not exist or is not needed comes back as None."""
+    if stream is not None:
+        return _on(stream, norm_backward, dz, dh, z, f, gate, w_post, w_pre, r_post, r_pre, gate_kind=gate_kind, post=post,
+                   pre=pre, alpha=alpha, need_dx=need_dx, need_df=need_df, need_dgate=need_dgate, need_dw=need_dw)
     like = dz if dz is not None else dh
     if not (like is not None and like.dim() == 2 and like.dtype in _ELEM):
         _bad("dz or dh must be a bf16, fp16 or fp32 matrix")
@@ -283,9 +300,7 @@ def norm_backward(dz, dh, z, f=None, gate=None, w_post=None, w_pre=None, r_post=
     ws = _ws(plan, dev)
     check(lib().moe_norm_backward(plan[1], _ptr(dz), _ptr(dh), _ptr(z), _ptr(f), _ptr(gate), _ptr(w_post),
                                   _ptr(w_pre), _ptr(r_post), _ptr(r_pre), _ptr(dx), _ptr(df), _ptr(dgate),
-                                  _ptr(dw_post), _ptr(dw_pre), ws.data_ptr(), _stream(stream)))
-    if stream is not None:
-        _used_on(stream, dz, dh, z, f, gate, w_post, w_pre, r_post, r_pre, dx, df, dgate, dw_post, dw_pre, ws)
+                                  _ptr(dw_post), _ptr(dw_pre), ws.data_ptr(), _stream(None)))
     return dx, df, dgate, dw_post, dw_pre
 
 
@@ -305,6 +320,8 @@ def embed_forward(ids, table, *, scale=1.0, out=None, stream=None):
     """scale * table[ids] [*ids.shape, d]; an id outside [0, V) (padding) gives a
     zero row.  table [V, d] bf16, fp16 or fp32; ids int32 or int64 of any shape.
     `out` [ids.numel(), d] may be given."""
+    if stream is not None:
+        return _on(stream, embed_forward, ids, table, scale=scale, out=out)
     if not (table.dim() == 2 and table.dtype in _ELEM):
         _bad("table must be a bf16, fp16 or fp32 matrix [V, d]")
     V, d = table.shape
@@ -313,9 +330,7 @@ def embed_forward(ids, table, *, scale=1.0, out=None, stream=None):
     rows, el = flat.shape[0], _ELEM[table.dtype]
     res, ld_o = _out(out, "out", rows, d, table.dtype, table.device)
     plan = _embed_plan(rows, V, d, el, el, int(flat.dtype == torch.int64), 0, scale, ld_t, ld_o)
-    check(lib().moe_embed_forward(plan[1], flat.data_ptr(), table.data_ptr(), res.data_ptr(), _stream(stream)))
-    if stream is not None:
-        _used_on(stream, flat, table, res)
+    check(lib().moe_embed_forward(plan[1], flat.data_ptr(), table.data_ptr(), res.data_ptr(), _stream(None)))
     return res if out is not None or ids.dim() == 1 else res.view(*ids.shape, d)
 
 
@@ -324,6 +339,9 @@ def embed_backward(ids, dout, V, *, scale=1.0, dtable=None, grad_dtype=None, acc
     ascending t.  dout [ids.numel(), d] (or [*ids.shape, d]); dtable of dout's
     type or fp32 (grad_dtype, or dtable's).  accumulate adds to the given
     dtable's rows that occur and leaves the others alone."""
+    if stream is not None:
+        return _on(stream, embed_backward, ids, dout, V, scale=scale, dtable=dtable, grad_dtype=grad_dtype,
+                   accumulate=accumulate)
     flat = _ids(ids)
     if not (dout.dtype in _ELEM and dout.dim() >= 2):
         _bad("dout must be bf16, fp16 or fp32 [rows, d]")
@@ -341,7 +359,5 @@ def embed_backward(ids, dout, V, *, scale=1.0, dtable=None, grad_dtype=None, acc
                        int(accumulate), scale, ld_t, ld_o)
     ws = _ws(plan, dout.device)
     check(lib().moe_embed_backward(plan[1], flat.data_ptr(), dout.data_ptr(), dtable.data_ptr(), ws.data_ptr(),
-                                   _stream(stream)))
-    if stream is not None:
-        _used_on(stream, flat, dout, dtable, ws)
+                                   _stream(None)))
     return dtable

@@ -1,0 +1,150 @@
+"""CPU-only checks of what block.py does around the library's calls: in which
+stream's order its copies, allocations and launches stand, which GPUs its
+tensors are on, what it allocates.  CPU tensors pose as GPU tensors, and a
+stand-in for the library records its calls."""
+import contextlib
+import types
+
+import pytest
+import torch
+
+from mixture_experts_layer_device_gb300 import block
+
+BF = torch.bfloat16
+
+
+class Gpu(torch.Tensor):
+    """A CPU tensor that says it is on GPU 0 and records what is done with it."""
+    log, index = [], 0
+    is_cuda = property(lambda t: True)
+    device = property(lambda t: torch.device("cuda", t.index))
+
+    def get_device(t):
+        return t.index
+
+    def data_ptr(t):
+        return 1 << 12
+
+    def contiguous(t):
+        if t.is_contiguous():
+            return t
+        Gpu.log.append(("copy", torch.cuda.current_stream()))
+        return super().contiguous()
+
+    def reshape(t, *shape):
+        r = super().reshape(*shape)
+        if r.untyped_storage().data_ptr() != t.untyped_storage().data_ptr():
+            Gpu.log.append(("copy", torch.cuda.current_stream()))
+        return r
+
+    def record_stream(t, stream):
+        Gpu.log.append(("kept", stream, t.untyped_storage().data_ptr()))
+
+
+class OtherGpu(Gpu):
+    index = 1
+
+
+class Stream:
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+MAIN, SIDE = Stream(11), Stream(22)
+
+
+class Library:
+    def __getattr__(self, name):
+        def call(*args):
+            if name.endswith("workspace_bytes"):
+                return 512
+            Gpu.log.append(("launch", name, args[-1]))
+            return 0
+        return call
+
+
+@pytest.fixture
+def gpu(monkeypatch):
+    """The recorded calls; `gpu.current` is the current GPU's index."""
+    state = types.SimpleNamespace(log=[], stream=MAIN, current=0, allocated=0)
+    Gpu.log = state.log
+
+    @contextlib.contextmanager
+    def within(stream):
+        before, state.stream = state.stream, stream
+        yield
+        state.stream = before
+
+    def stand_in(make):
+        def call(*args, device=None, **kw):
+            state.log.append(("new", state.stream))
+            t = make(*args, **kw).as_subclass(Gpu)
+            state.allocated = max(state.allocated, t.untyped_storage().nbytes())
+            return t
+        return call
+
+    monkeypatch.setattr(torch, "empty", stand_in(torch.empty))
+    monkeypatch.setattr(torch.cuda, "stream", within)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: state.stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: {11: MAIN, 22: SIDE}[handle])
+    monkeypatch.setattr(block, "_stream", lambda s: s if isinstance(s, int) else (s or state.stream).cuda_stream)
+    monkeypatch.setattr(block, "lib", Library)
+    plans = (block._grouped_plan, block._norm_plan, block._embed_plan)
+    for p in plans:
+        p.cache_clear()
+    yield state
+    for p in plans:
+        p.cache_clear()
+
+
+def on(kind, *shape, dtype=BF):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(kind)
+
+
+def crooked(kind, *shape, dtype=BF):
+    """The same whose last two dimensions lie in the other order: the call copies it."""
+    return on(kind, *shape[:-2], shape[-1], shape[-2], dtype=dtype).transpose(-1, -2)
+
+
+def spread(kind, n, dtype):
+    return on(kind, 2 * n, dtype=dtype)[::2]
+
+
+def calls(make, vec):
+    """(operator, its tensors, its options): matrices by make(*shape), vectors by vec(n, dtype)."""
+    R, E, N, K, V = 6, 3, 4, 5, 7
+    x, w, off, dy = make(R, K), make(E, N, K), vec(E + 1, torch.int32), make(R, N)
+    f, g, wq, r, ids = make(R, K), make(R, K), vec(K, BF), vec(R, torch.float32), vec(R, torch.int64)
+    return [
+        (block.grouped_forward, dict(x=x, w=w, offsets=off), {}),
+        (block.grouped_backward, dict(dy=dy, x=x, w=w, offsets=off), {}),
+        (block.norm_forward, dict(x=x, f=f, gate=g, w_post=wq, w_pre=wq), dict(gate_kind="full")),
+        (block.norm_backward, dict(dz=x, dh=f, z=f, f=f, gate=g, w_post=wq, w_pre=wq, r_post=r, r_pre=r),
+         dict(gate_kind="full")),
+        (block.embed_forward, dict(ids=ids, table=make(V, K)), {}),
+        (block.embed_backward, dict(ids=ids, dout=x), dict(V=V)),
+    ]
+
+
+CALLS = ["grouped_forward", "grouped_backward", "norm_forward", "norm_backward", "embed_forward", "embed_backward"]
+
+
+@pytest.mark.parametrize("i", range(6), ids=CALLS)
+@pytest.mark.parametrize("given", [None, SIDE, 22], ids=["current", "stream", "handle"])
+def test_copies_and_memory_belong_to_the_stream_of_the_launch(gpu, i, given):
+    fn, tensors, opts = calls(lambda *s: crooked(Gpu, *s), lambda n, dt: spread(Gpu, n, dt))[i]
+    out = fn(**tensors, **opts, stream=given)
+    stream = MAIN if given is None else SIDE
+    launches = [e for e in gpu.log if e[0] == "launch"]
+    assert len(launches) == 1 and launches[0][2] == stream.cuda_stream
+    made = [e for e in gpu.log if e[0] in ("copy", "new")]
+    assert {e[0] for e in made} == {"copy", "new"}
+    assert all(e[1] is stream for e in made), made
+    assert gpu.stream is MAIN
+    if given is not None:       # the caller's tensors outlive their use there, the results theirs on the caller's stream
+        kept = {e[1:] for e in gpu.log if e[0] == "kept"}
+        for t in tensors.values():
+            assert (SIDE, t.untyped_storage().data_ptr()) in kept
+        for t in out if isinstance(out, tuple) else (out,):
+            if t is not None:
+                assert (MAIN, t.untyped_storage().data_ptr()) in kept
