@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(THREADS, MINB) norm_bwd_kernel(const NormArgs 
   const int slot = WARP ? blockIdx.x * rpb + (threadIdx.x >> 5) : blockIdx.x;
   const float inv_d = 1.f / static_cast<float>(a.d);
   const long step = static_cast<long>(gridDim.x) * rpb;
-  const bool full = a.gate == MOE_GATE_FULL;
+  const bool full = a.gate == MOE_GATE_FULL, post = (a.flags & MOE_NORM_POST) != 0;
   float acc0[NCH][VEC], acc1[NCH][VEC];
 #pragma unroll
   for (int i = 0; i < NCH; ++i)
@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(THREADS, MINB) norm_bwd_kernel(const NormArgs 
       }
     }
     row_sum<WARP, 4>(s, red, turn);
-    const RowTerms t = row_terms<T>(a, row, in, s, inv_d, tid == 0);
+    const RowTerms t = row_terms<T>(a, post, row, in, s, inv_d, tid == 0);
 #pragma unroll
     for (int i = 0; i < NCH; ++i) {
       const int c = (tid + i * tpr) * VEC;
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(THREADS, MINB) norm_bwd_kernel(const NormArgs 
 #pragma unroll
         for (int k = 0; k < VEC; ++k) {
           const ElemOut o =
-              elem_out(t, a.alpha, dz[k], dh[k], z[k], f[k], wp[k], w[k], g[k], acc0[i][k], acc1[i][k]);
+              elem_out(t, post, a.alpha, dz[k], dh[k], z[k], f[k], wp[k], w[k], g[k], acc0[i][k], acc1[i][k]);
           dz[k] = o.dx;
           dh[k] = o.df;
           z[k] = o.dg;
@@ -309,6 +309,7 @@ template <typename T, int VEC>
 __global__ void __launch_bounds__(512) norm_bwd_rows_kernel(const NormArgs a) {
   __shared__ float red[2][4][kMaxWarps];
   const float inv_d = 1.f / static_cast<float>(a.d);
+  const bool post = (a.flags & MOE_NORM_POST) != 0;
   int turn = 0;
   for (long row = blockIdx.x; row < a.rows; row += gridDim.x) {
     const RowIn in = row_in<T>(a, row);
@@ -331,7 +332,7 @@ __global__ void __launch_bounds__(512) norm_bwd_rows_kernel(const NormArgs a) {
       for (int k = 0; k < VEC; ++k) add_sums(v[0][k], v[1][k] * wp[k], v[2][k], w[k] * g[k] * v[3][k], s);
     }
     row_sum<false, 4>(s, red, turn);
-    const RowTerms t = row_terms<T>(a, row, in, s, inv_d, threadIdx.x == 0);
+    const RowTerms t = row_terms<T>(a, post, row, in, s, inv_d, threadIdx.x == 0);
     if (threadIdx.x == 0) reinterpret_cast<float4 *>(a.terms)[row] = make_float4(t.rp, t.c1, t.a1, t.c2);
   }
 }
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(128) norm_bwd_apply_kernel(const NormArgs a, i
   pdl_trigger();
   const int c = (blockIdx.x * 128 + threadIdx.x) * VEC;
   if (c >= a.d) return;
-  const bool full = a.gate == MOE_GATE_FULL;
+  const bool full = a.gate == MOE_GATE_FULL, post = (a.flags & MOE_NORM_POST) != 0;
   float w[VEC], wp[VEC], acc0[VEC], acc1[VEC];
   weight_chunk<T, VEC>(a.w_pre, c, wp);
   weight_chunk<T, VEC>(a.w_post, c, w);
@@ -386,7 +387,7 @@ __global__ void __launch_bounds__(128) norm_bwd_apply_kernel(const NormArgs a, i
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
         const ElemOut o =
-            elem_out(t, a.alpha, dz[k], dh[k], z[k], f[k], wp[k], w[k], full ? g[k] : 1.f, acc0[k], acc1[k]);
+            elem_out(t, post, a.alpha, dz[k], dh[k], z[k], f[k], wp[k], w[k], full ? g[k] : 1.f, acc0[k], acc1[k]);
         dz[k] = o.dx;
         f[k] = o.df;
         z[k] = o.dg;

@@ -148,13 +148,15 @@ struct RowTerms {
   float rp, c1, a1, c2;
 };
 template <typename T>
-MOE_DEV RowTerms row_terms(const NormArgs &a, long row, const RowIn &in, const float *s, float inv_d, bool first) {
+MOE_DEV RowTerms row_terms(const NormArgs &a, bool post, long row, const RowIn &in, const float *s, float inv_d,
+                           bool first) {
   RowTerms t;
   t.rp = in.rp;
   t.c1 = in.rp * in.rp * s[0] * inv_d;
-  const float tq = s[1] + in.rp * (s[2] - t.c1 * s[3]);  // <t, q>
+  float tq = s[1] + in.rp * (s[2] - t.c1 * s[3]);  // <t, q>
+  if (!post && !(a.flags & MOE_NORM_PRE)) tq = s[1];  // f may be infinite: no 0 * inf of the terms that are not there
   t.a1 = in.rq * in.rg;
-  t.c2 = (a.flags & MOE_NORM_POST) ? in.rq * in.rq * in.rq * in.rg * tq * inv_d : 0.f;
+  t.c2 = post ? in.rq * in.rq * in.rq * in.rg * tq * inv_d : 0.f;
   if (a.gate == MOE_GATE_ROW && a.dg && first) static_cast<T *>(a.dg)[row] = Elem<T>::from(tq * in.rq);
   return t;
 }
@@ -169,12 +171,13 @@ MOE_DEV void add_sums(float dz, float dhw, float z, float q, float *s) {
 
 // One element after the sums.  w = w_post times a channel gate; g = a full
 // gate's value, else 1.  acc0 sums dh z r_pre (dw_pre); acc1 sums t f r_post
-// with a row or full gate (dw_post, and a channel gate's gradient).
+// with a row or full gate (dw_post, and a channel gate's gradient).  Without the
+// post norm df does not depend on f, which may be infinite then.
 struct ElemOut {
   float dx, df, dg;
 };
-MOE_DEV ElemOut elem_out(const RowTerms &t, float alpha, float dz, float dh, float z, float f, float wp, float w,
-                         float g, float &acc0, float &acc1) {
+MOE_DEV ElemOut elem_out(const RowTerms &t, bool post, float alpha, float dz, float dh, float z, float f, float wp,
+                         float w, float g, float &acc0, float &acc1) {
   ElemOut o;
   const float y = t.rp * z;
   const float tt = fmaf(t.rp, dh * wp, fmaf(-t.c1, y, dz));
@@ -183,7 +186,7 @@ MOE_DEV ElemOut elem_out(const RowTerms &t, float alpha, float dz, float dh, flo
   acc1 = fmaf(tg, nh, acc1);
   o.dx = alpha * tt;
   o.dg = tw * nh;
-  o.df = fmaf(t.a1, tw * g, -(t.c2 * f));
+  o.df = fmaf(t.a1, tw * g, post ? -(t.c2 * f) : 0.f);
   return o;
 }
 

@@ -295,8 +295,9 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 288 ? 2 : 1) norm_fwd_ring
 // Shared memory: [stage][dz, dh, z, f, full gate][chunk][thread] of 16 bytes.
 // The loops are those of add_sums and elem_out (norm.cuh), two columns at once.
 // One step sums row i + 1 and finishes row i, so the barrier and the joining of
-// the sums have the other row's work beside them.
-template <typename T, bool FULL, bool EDGES, int THREADS>
+// the sums have the other row's work beside them.  POST by kernel: asked per element,
+// whether f is in df costs 232 us where this takes 194 (16384 x 6144).
+template <typename T, bool POST, bool FULL, bool EDGES, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) norm_bwd_ring_kernel(const NormArgs a, int stages) {
   pdl_trigger();
   constexpr int VEC = Elem<T>::VEC, P = VEC / 2, NT = FULL ? 5 : 4;
@@ -413,7 +414,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) norm_bwd_ring
     if (more) sums(base + after * stage_bytes, red[turn ^ 1]);
     float s[4];
     block_sums_get<4>(s, red[turn]);
-    const RowTerms t = row_terms<T>(a, row, in, s, inv_d, threadIdx.x == 0);
+    const RowTerms t = row_terms<T>(a, POST, row, in, s, inv_d, threadIdx.x == 0);
     const f32x2 rp = f2_both(t.rp), c1 = f2_both(-t.c1), a1 = f2_both(t.a1), c2 = f2_both(-t.c2);
     const uint32_t at = base + stage * stage_bytes;
 #pragma unroll
@@ -438,7 +439,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) norm_bwd_ring
         }
         acc1[i][k] = f2_fma(tg, nh, acc1[i][k]);
         dz[k] = f2_mul(alpha, tt);
-        f[k] = f2_fma(a1, tw, f2_mul(c2, f[k]));
+        f[k] = f2_fma(a1, tw, POST ? f2_mul(c2, f[k]) : 0);
       }
       col.store_or_keep(dx, i, dx, dz, parts[turn][0]);
       col.store_or_keep(df, i, df, f, parts[turn][1]);
@@ -530,10 +531,10 @@ cudaError_t fwd_shape(const NormArgs &a, const RingShape &r, int num_sms, cudaSt
   int slots;
   return ring_launch(norm_fwd_ring_kernel<T, FULL, EDGES, THREADS>, a, r, num_sms, 1 << 30, &slots, memo, s);
 }
-template <typename T, bool FULL, bool EDGES, int THREADS>
+template <typename T, bool POST, bool FULL, bool EDGES, int THREADS>
 cudaError_t bwd_shape(const NormArgs &a, const RingShape &r, int num_sms, int *slots, cudaStream_t s) {
   static int memo[33][64] = {};
-  return ring_launch(norm_bwd_ring_kernel<T, FULL, EDGES, THREADS>, a, r, num_sms, norm_max_blocks(a.d), slots, memo, s);
+  return ring_launch(norm_bwd_ring_kernel<T, POST, FULL, EDGES, THREADS>, a, r, num_sms, norm_max_blocks(a.d), slots, memo, s);
 }
 
 // Block sizes by the registers that they leave a thread: up to 256 threads two
@@ -546,11 +547,11 @@ cudaError_t fwd_block(const NormArgs &a, const RingShape &r, int num_sms, cudaSt
   if (r.threads <= 512) return fwd_shape<T, FULL, EDGES, 512>(a, r, num_sms, s);
   return fwd_shape<T, FULL, EDGES, 1024>(a, r, num_sms, s);
 }
-template <typename T, bool FULL, bool EDGES>
+template <typename T, bool POST, bool FULL, bool EDGES>
 cudaError_t bwd_block(const NormArgs &a, const RingShape &r, int num_sms, int *slots, cudaStream_t s) {
-  if (r.threads <= 256) return bwd_shape<T, FULL, EDGES, 256>(a, r, num_sms, slots, s);
-  if (r.threads <= 384) return bwd_shape<T, FULL, EDGES, 384>(a, r, num_sms, slots, s);
-  return bwd_shape<T, FULL, EDGES, 512>(a, r, num_sms, slots, s);
+  if (r.threads <= 256) return bwd_shape<T, POST, FULL, EDGES, 256>(a, r, num_sms, slots, s);
+  if (r.threads <= 384) return bwd_shape<T, POST, FULL, EDGES, 384>(a, r, num_sms, slots, s);
+  return bwd_shape<T, POST, FULL, EDGES, 512>(a, r, num_sms, slots, s);
 }
 
 template <typename T>
@@ -560,12 +561,18 @@ cudaError_t fwd_type(const NormArgs &a, int num_sms, cudaStream_t s) {
     return r.edges ? fwd_block<T, true, true>(a, r, num_sms, s) : fwd_block<T, true, false>(a, r, num_sms, s);
   return r.edges ? fwd_block<T, false, true>(a, r, num_sms, s) : fwd_block<T, false, false>(a, r, num_sms, s);
 }
-template <typename T>
-cudaError_t bwd_type(const NormArgs &a, int num_sms, int *slots, cudaStream_t s) {
+template <typename T, bool POST>
+cudaError_t bwd_gate(const NormArgs &a, int num_sms, int *slots, cudaStream_t s) {
   const RingShape r = ring_shape(a, true);
   if (a.gate == MOE_GATE_FULL)
-    return r.edges ? bwd_block<T, true, true>(a, r, num_sms, slots, s) : bwd_block<T, true, false>(a, r, num_sms, slots, s);
-  return r.edges ? bwd_block<T, false, true>(a, r, num_sms, slots, s) : bwd_block<T, false, false>(a, r, num_sms, slots, s);
+    return r.edges ? bwd_block<T, POST, true, true>(a, r, num_sms, slots, s)
+                   : bwd_block<T, POST, true, false>(a, r, num_sms, slots, s);
+  return r.edges ? bwd_block<T, POST, false, true>(a, r, num_sms, slots, s)
+                 : bwd_block<T, POST, false, false>(a, r, num_sms, slots, s);
+}
+template <typename T>
+cudaError_t bwd_type(const NormArgs &a, int num_sms, int *slots, cudaStream_t s) {
+  return (a.flags & MOE_NORM_POST) ? bwd_gate<T, true>(a, num_sms, slots, s) : bwd_gate<T, false>(a, num_sms, slots, s);
 }
 
 }  // namespace

@@ -1,7 +1,10 @@
 """GPU tests of calls around the layer in the places where their inputs, streams
 and memory are not the usual ones."""
+import numpy as np
 import pytest
 import torch
+
+from oracle import block as ob
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +71,55 @@ def test_a_call_on_another_stream_does_not_wait_for_the_current_one(blk):
     side.synchronize()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(by_handle, want))
+
+
+# ---------------------------------------------------------------- what is not finite, and the ends of the range
+def f64(t):
+    return None if t is None else t.detach().double().cpu().numpy()
+
+
+U = {BF: 2.0 ** -8, HF: 2.0 ** -11, FP: 2.0 ** -24}
+
+
+def near(got, ref, size, n):
+    """Equal where the reference is not finite; elsewhere within a rounding of the output's
+    type and (n + 32) 2^-22 of the terms' sizes, as in test_gpu_o_block.py."""
+    got_, fin = f64(got), np.isfinite(ref)
+    assert np.array_equal(got_[~fin], ref[~fin], equal_nan=True)
+    tol = U[got.dtype] * np.abs(ref[fin]) + (n + 32) * 2.0 ** -22 * size[fin] + 2.0 ** -25
+    assert np.all(np.abs(got_[fin] - ref[fin]) <= tol)
+
+
+# both register kernels, rows in flight through shared memory (even and odd), long rows
+NORM_PATHS = [(37, 200), (37, 264), (37, 1027), (333, 1032), (311, 1027), (5, 9000), (5, 9001)]
+
+
+@pytest.mark.parametrize("kind", ["none", "channel", "row", "full"])
+@pytest.mark.parametrize("rows,d", NORM_PATHS)
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_norm_gradient_of_an_infinite_block_output_without_its_norm(blk, rows, d, kind, dtype):
+    """df = g t takes nothing from f, and without the pre norm t = dz: what f holds does not matter to df,
+    and a gate's gradient sum t f is infinite only where its own terms are."""
+    g = gen(d)
+    x, f, dz, dh = (draw((rows, d), dtype, g) for _ in range(4))
+    f[1, 3], f[2, d - 1], f[4, d // 2] = float("inf"), float("-inf"), float("nan")
+    shape = {"none": None, "channel": (d,), "row": (rows,), "full": (rows, d)}[kind]
+    gate = None if shape is None else draw(shape, dtype, g)
+    kw = dict(gate_kind=kind, post=False, pre=False, alpha=0.5)
+    got = blk.norm_backward(dz, None, None, f, gate, **kw)
+    with np.errstate(invalid="ignore"):
+        ref, size = ob.norm_backward(f64(dz), None, None, f64(f), f64(gate), None, None, None, None, kind, False, False, 0.5)
+    assert np.all(np.isfinite(ref["df"]))
+    for name, t in zip(("dx", "df", "dgate"), got):
+        assert (t is None) == (ref[name] is None)
+        if t is not None:
+            near(t, ref[name], size[name], d + rows)
+    # with the pre norm (over a z that is finite)
+    w_pre, r = draw((d,), dtype, g), (1 + draw((rows,), FP, g).abs())
+    dx, df, _, _, dw = blk.norm_backward(dz, dh, x, f, gate, None, w_pre, None, r, gate_kind=kind, post=False, alpha=0.5)
+    with np.errstate(invalid="ignore"):
+        ref, size = ob.norm_backward(f64(dz), f64(dh), f64(x), f64(f), f64(gate), None, f64(w_pre), None, f64(r), kind, False,
+                                     True, 0.5)
+    for name, t in (("dx", dx), ("df", df), ("dw_pre", dw)):
+        assert np.all(np.isfinite(ref[name]))
+        near(t, ref[name], size[name], d + rows)
