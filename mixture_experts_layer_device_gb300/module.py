@@ -13,11 +13,35 @@ in its own buffer, so several forwards may precede their backwards.
 Around the layer: GroupedLinear (ragged products grouped by expert), BlockNorm
 (the norms around a block with its gate and residual scale) and TokenEmbedding,
 each an nn.Module over an autograd.Function over block.py.
+
+Gradients have no second derivative: under create_graph they refuse one.
 """
 import torch
 
 from . import block
 from .layer import MoELayer
+
+
+class _FirstOrder(torch.autograd.Function):
+    """A gradient as it is, which cannot be differentiated."""
+
+    @staticmethod
+    def forward(ctx, grad, *depends):
+        return grad
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("the second derivative of the library's operators is not built: this gradient was computed "
+                           "under create_graph and is differentiated")
+
+
+def _first_order(grad, *depends):
+    """`grad`, computed out of autograd's sight from `depends`.  Where a graph is asked
+    for (create_graph), it refuses to be differentiated instead of passing for a
+    constant."""
+    if grad is None or not torch.is_grad_enabled() or not any(t is not None and t.requires_grad for t in depends):
+        return grad
+    return _FirstOrder.apply(grad, *depends)
 
 
 class MoEFunction(torch.autograd.Function):
@@ -56,8 +80,11 @@ class MoEFunction(torch.autograd.Function):
         if ctx.router:
             dW_r = torch.empty_like(W_r)
             layer.router_backward(g["dlogits"], x, W_r.contiguous(), g["dx"], dW_r)
-        return (g["dx"], None if ctx.router else g["dlogits"], dW_r, g["dW_gu"], g["dW_dn"], g["dWs_gu"],
-                g["dWs_dn"], None)
+        grads = (g["dx"], None if ctx.router else g["dlogits"], dW_r, g["dW_gu"], g["dW_dn"], g["dWs_gu"], g["dWs_dn"])
+        if torch.is_grad_enabled():     # every gradient depends on every input; the weights are not saved
+            some = torch.zeros((), device=x.device, requires_grad=True)
+            grads = tuple(_first_order(t, some) for t in grads)
+        return grads + (None,)
 
 
 class MoE(torch.nn.Module):
@@ -115,7 +142,7 @@ class GroupedFunction(torch.autograd.Function):
         dx = dw = None
         if need_dx or need_dw:
             dx, dw = block.grouped_backward(dy, x, w, offsets, need_dx=need_dx, need_dw=need_dw)
-        return dx, dw, None
+        return _first_order(dx, dy, w), _first_order(dw, dy, x), None
 
 
 class GroupedLinear(torch.nn.Module):
@@ -155,7 +182,8 @@ class BlockNormFunction(torch.autograd.Function):
         dx, df, dgate, dw_post, dw_pre = block.norm_backward(
             dz, dh, z, f, gate, w_post, w_pre if opts["pre"] else None, r_post, r_pre, need_dx=need[0], need_df=need[1],
             need_dgate=need[2], need_dw=need[3] or need[4], **opts)
-        return (dx, df, dgate, dw_post if need[3] else None, dw_pre if need[4] else None) + (None,) * 5
+        grads = (dx, df, dgate, dw_post if need[3] else None, dw_pre if need[4] else None)
+        return tuple(_first_order(t, dz, dh, z, f, gate, w_post, w_pre) for t in grads) + (None,) * 5
 
 
 class BlockNorm(torch.nn.Module):
@@ -196,7 +224,7 @@ class EmbeddingFunction(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dout):
         ids, = ctx.saved_tensors
-        return None, block.embed_backward(ids, dout, ctx.V, scale=ctx.scale), None
+        return None, _first_order(block.embed_backward(ids, dout, ctx.V, scale=ctx.scale), dout), None
 
 
 class TokenEmbedding(torch.nn.Module):
