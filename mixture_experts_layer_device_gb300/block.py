@@ -7,8 +7,8 @@ Plain functions: they check their arguments, allocate outputs and workspaces
 from torch and call the library; all arithmetic runs in its kernels.  They run
 on torch's current stream and do not synchronise; with `stream` (a stream or its
 handle) they run as under `torch.cuda.stream(stream)`: what they read has to be
-ready on it, and what they return is.  The autograd functions and modules over
-them are in module.py.
+ready on it, and what they return is.  All tensors of a call are on the current
+GPU.  The autograd functions and modules over them are in module.py.
 """
 import ctypes
 from functools import lru_cache
@@ -25,15 +25,26 @@ def _bad(what, *args):
     raise ValueError(what % args if args else what)
 
 
-def _rows(t, name, cols, dtype=None, rows=None):
-    """A 2-D matrix on the current GPU whose rows are contiguous; its row stride."""
+_current_gpu = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _gpu(t, name):
+    """The index of the GPU of a call's first tensor: the current one, on which the library launches."""
+    gpu = t.get_device()
+    if gpu < 0 or gpu != _current_gpu():
+        _bad("%s is on %s, not on the current GPU", name, t.device)
+    return gpu
+
+
+def _rows(t, name, cols, gpu, dtype=None, rows=None):
+    """A 2-D matrix on the call's GPU whose rows are contiguous; its row stride."""
     shape = t.shape
     if len(shape) != 2 or shape[1] != cols or (rows is not None and shape[0] != rows):
         _bad("%s has shape %s, expected [%s, %d]", name, tuple(shape), "rows" if rows is None else rows, cols)
     if dtype is not None and t.dtype != dtype:
         _bad("%s is %s, expected %s", name, t.dtype, dtype)
-    if not t.is_cuda:
-        _bad("%s is not on the GPU", name)
+    if t.get_device() != gpu:
+        _bad("%s is on %s, expected GPU %d", name, t.device, gpu)
     if t.is_contiguous():
         return t, cols
     if (t.stride(1) != 1 and cols > 1) or (shape[0] > 1 and t.stride(0) < cols):
@@ -41,21 +52,21 @@ def _rows(t, name, cols, dtype=None, rows=None):
     return t, (t.stride(0) if shape[0] > 1 else cols)
 
 
-def _out(t, name, rows, cols, dtype, device):
+def _out(t, name, rows, cols, dtype, device, gpu):
     """The caller's output matrix (rows contiguous), or a new one; its row stride."""
     if t is None:
         return torch.empty((rows, cols), dtype=dtype, device=device), cols
-    if not (t.shape == (rows, cols) and t.dtype == dtype and t.is_cuda and (cols == 1 or t.stride(1) == 1) and
-            (rows <= 1 or t.stride(0) >= cols)):
-        _bad("%s must be a %s GPU matrix [%d, %d] with contiguous rows", name, dtype, rows, cols)
+    if not (t.shape == (rows, cols) and t.dtype == dtype and t.get_device() == gpu and
+            (cols == 1 or t.stride(1) == 1) and (rows <= 1 or t.stride(0) >= cols)):
+        _bad("%s must be a %s matrix [%d, %d] with contiguous rows on GPU %d", name, dtype, rows, cols, gpu)
     return t, (t.stride(0) if rows > 1 else cols)
 
 
-def _vector(t, name, n, dtype):
+def _vector(t, name, n, dtype, gpu):
     if t is None:
         return None
-    if t.shape != (n,) or t.dtype != dtype or not t.is_cuda:
-        _bad("%s must be a %s GPU vector of %d", name, dtype, n)
+    if t.shape != (n,) or t.dtype != dtype or t.get_device() != gpu:
+        _bad("%s must be a %s vector of %d on GPU %d", name, dtype, n, gpu)
     return t.contiguous()
 
 
@@ -101,18 +112,21 @@ def _grouped_plan(*fields):
     return _plan(MoeGroupedConfig(*fields), lib().moe_grouped_workspace_bytes)
 
 
-def _grouped(x_dtype, w, offsets, name):
+def _grouped(x, w, offsets, name):
+    x_dtype = x.dtype
     if not (x_dtype in (torch.bfloat16, torch.float16)):
         _bad("%s must be bfloat16 or float16", name)
-    if not (w.dim() == 3 and w.dtype == x_dtype and w.is_cuda):
-        _bad("w must be a %s GPU tensor [E, N, K]", x_dtype)
+    gpu = _gpu(x, name)
+    if not (w.dim() == 3 and w.dtype == x_dtype and w.get_device() == gpu):
+        _bad("w must be a %s tensor [E, N, K] on GPU %d", x_dtype, gpu)
     E, N, K = w.shape
-    if not (offsets.dim() == 1 and offsets.shape[0] == E + 1 and offsets.dtype == torch.int32 and offsets.is_cuda):
-        _bad("offsets must be an int32 GPU vector of E + 1 = %d", E + 1)
+    if not (offsets.dim() == 1 and offsets.shape[0] == E + 1 and offsets.dtype == torch.int32 and
+            offsets.get_device() == gpu):
+        _bad("offsets must be an int32 vector of E + 1 = %d on GPU %d", E + 1, gpu)
     if (K > 1 and w.stride(2) != 1) or (N > 1 and w.stride(1) < K) or \
             (E > 1 and w.stride(0) < (N - 1) * w.stride(1) + K):
         w = w.contiguous()
-    return w, offsets.contiguous(), E, N, K, (w.stride(1) if N > 1 else K)
+    return gpu, w, offsets.contiguous(), E, N, K, (w.stride(1) if N > 1 else K)
 
 
 def grouped_forward(x, w, offsets, *, out=None, out_dtype=None, return_workspace=False, stream=None):
@@ -122,12 +136,12 @@ def grouped_forward(x, w, offsets, *, out=None, out_dtype=None, return_workspace
     type or fp32 (out_dtype, or out's)."""
     if stream is not None:
         return _on(stream, grouped_forward, x, w, offsets, out=out, out_dtype=out_dtype, return_workspace=return_workspace)
-    w, offsets, E, N, K, ld_w = _grouped(x.dtype, w, offsets, "x")
-    x, ld_x = _rows(x, "x", K)
+    gpu, w, offsets, E, N, K, ld_w = _grouped(x, w, offsets, "x")
+    x, ld_x = _rows(x, "x", K, gpu)
     out_dtype = out_dtype or (out.dtype if out is not None else x.dtype)
     if not (out_dtype in (x.dtype, torch.float32)):
         _bad("y is of x's type or float32")
-    y, ld_y = _out(out, "out", x.shape[0], N, out_dtype, x.device)
+    y, ld_y = _out(out, "out", x.shape[0], N, out_dtype, x.device, gpu)
     ld_e = w.stride(0) if E > 1 else 0
     plan = _grouped_plan(x.shape[0], E, N, K, _ELEM[x.dtype], _ELEM[out_dtype], 0, ld_x, ld_y, ld_w, ld_e)
     ws = _ws(plan, x.device)
@@ -145,10 +159,10 @@ def grouped_backward(dy, x, w, offsets, *, dx=None, dw=None, need_dx=True, need_
     if stream is not None:
         return _on(stream, grouped_backward, dy, x, w, offsets, dx=dx, dw=dw, need_dx=need_dx, need_dw=need_dw,
                    dw_dtype=dw_dtype, accumulate=accumulate, return_workspace=return_workspace)
-    w, offsets, E, N, K, ld_w = _grouped(dy.dtype, w, offsets, "dy")
+    gpu, w, offsets, E, N, K, ld_w = _grouped(dy, w, offsets, "dy")
     rows = dy.shape[0]
-    dy, ld_y = _rows(dy, "dy", N)
-    x, ld_x = _rows(x, "x", K, dy.dtype, rows)
+    dy, ld_y = _rows(dy, "dy", N, gpu)
+    x, ld_x = _rows(x, "x", K, gpu, dy.dtype, rows)
     dw_dtype = dw_dtype or (dw.dtype if dw is not None else dy.dtype)
     if not (dw_dtype in (dy.dtype, torch.float32)):
         _bad("dw is of dy's type or float32")
@@ -160,8 +174,9 @@ def grouped_backward(dy, x, w, offsets, *, dx=None, dw=None, need_dx=True, need_
         if dx is None:      # of x's row stride, which the library shares between the two
             dx = torch.empty((rows, ld_x), dtype=dy.dtype, device=dy.device)
             dx = dx if ld_x == K else dx[:, :K]
-        if not (dx.shape == (rows, K) and dx.dtype == dy.dtype and dx.is_cuda and (K == 1 or dx.stride(1) == 1)):
-            _bad("dx must be a %s GPU matrix [%d, %d] with contiguous rows", dy.dtype, rows, K)
+        if not (dx.shape == (rows, K) and dx.dtype == dy.dtype and dx.get_device() == gpu and
+                (K == 1 or dx.stride(1) == 1)):
+            _bad("dx must be a %s matrix [%d, %d] with contiguous rows on GPU %d", dy.dtype, rows, K, gpu)
         if rows > 1 and dx.stride(0) != ld_x:
             x, ld_x = x.contiguous(), K
             if not (dx.stride(0) == K):
@@ -169,8 +184,8 @@ def grouped_backward(dy, x, w, offsets, *, dx=None, dw=None, need_dx=True, need_
     if need_dw:
         if dw is None:
             dw = torch.empty((E, N, K), dtype=dw_dtype, device=dy.device)
-        if not (dw.shape == (E, N, K) and dw.dtype == dw_dtype and dw.is_cuda and dw.is_contiguous()):
-            _bad("dw must be a contiguous %s GPU tensor [%d, %d, %d]", dw_dtype, E, N, K)
+        if not (dw.shape == (E, N, K) and dw.dtype == dw_dtype and dw.get_device() == gpu and dw.is_contiguous()):
+            _bad("dw must be a contiguous %s tensor [%d, %d, %d] on GPU %d", dw_dtype, E, N, K, gpu)
     ld_e = w.stride(0) if E > 1 else 0
     plan = _grouped_plan(rows, E, N, K, _ELEM[dy.dtype], _ELEM[dw_dtype], int(accumulate), ld_x, ld_y, ld_w, ld_e)
     ws = _ws(plan, dy.device)
@@ -192,7 +207,7 @@ def _norm_plan(*fields):
     return _plan(MoeNormConfig(*fields), lib().moe_norm_workspace_bytes)
 
 
-def _gate(gate, kind, rows, d, dtype):
+def _gate(gate, kind, rows, d, dtype, gpu):
     if not (kind in GATES):
         _bad("gate_kind is one of %s", sorted(GATES))
     if not ((gate is None) == (kind == "none")):
@@ -200,8 +215,8 @@ def _gate(gate, kind, rows, d, dtype):
     if kind == "none":
         return None, d
     if kind == "full":
-        return _rows(gate, "gate", d, dtype, rows)
-    return _vector(gate, "gate", d if kind == "channel" else rows, dtype), d
+        return _rows(gate, "gate", d, gpu, dtype, rows)
+    return _vector(gate, "gate", d if kind == "channel" else rows, dtype, gpu), d
 
 
 def norm_forward(x, f=None, gate=None, w_post=None, w_pre=None, *, gate_kind="none", post=True, pre=True, alpha=1.0,
@@ -219,22 +234,23 @@ def norm_forward(x, f=None, gate=None, w_post=None, w_pre=None, *, gate_kind="no
     if not (x.dim() == 2 and x.dtype in _ELEM):
         _bad("x must be a bf16, fp16 or fp32 matrix [rows, d]")
     rows, d = x.shape
-    x, ld_x = _rows(x, "x", d)
+    gpu = _gpu(x, "x")
+    x, ld_x = _rows(x, "x", d, gpu)
     ld_f, post = d, post and f is not None
     if f is not None:
-        f, ld_f = _rows(f, "f", d, x.dtype, rows)
+        f, ld_f = _rows(f, "f", d, gpu, x.dtype, rows)
     if not (f is not None or gate is None):
         _bad("a gate needs the block's output f")
     if not (pre or need_z):
         _bad("nothing to compute")
-    gate, ld_g = _gate(gate, gate_kind, rows, d, x.dtype)
-    w_post = _vector(w_post, "w_post", d, x.dtype) if post else None
-    w_pre = _vector(w_pre, "w_pre", d, x.dtype) if pre else None
+    gate, ld_g = _gate(gate, gate_kind, rows, d, x.dtype, gpu)
+    w_post = _vector(w_post, "w_post", d, x.dtype, gpu) if post else None
+    w_pre = _vector(w_pre, "w_pre", d, x.dtype, gpu) if pre else None
     dev, ld_z, ld_h, r_post, r_pre = x.device, d, d, None, None
     if need_z:
-        z, ld_z = _out(z, "z", rows, d, x.dtype, dev)
+        z, ld_z = _out(z, "z", rows, d, x.dtype, dev, gpu)
     if pre:
-        h, ld_h = _out(h, "h", rows, d, x.dtype, dev)
+        h, ld_h = _out(h, "h", rows, d, x.dtype, dev, gpu)
         r_pre = torch.empty(rows, dtype=torch.float32, device=dev)
     if post:
         r_post = torch.empty(rows, dtype=torch.float32, device=dev)
@@ -259,30 +275,30 @@ def norm_backward(dz, dh, z, f=None, gate=None, w_post=None, w_pre=None, r_post=
     if not (like is not None and like.dim() == 2 and like.dtype in _ELEM):
         _bad("dz or dh must be a bf16, fp16 or fp32 matrix")
     rows, d = like.shape
-    dt, dev, post = like.dtype, like.device, post and f is not None
+    dt, dev, gpu, post = like.dtype, like.device, _gpu(like, "dz or dh"), post and f is not None
     if not (pre or dz is not None):
         _bad("without the pre norm the gradient arrives in dz")
     ld_z, ld_h, ld_f = d, d, d
     if dz is not None:
-        dz, ld_z = _rows(dz, "dz", d, dt, rows)
+        dz, ld_z = _rows(dz, "dz", d, gpu, dt, rows)
     if pre:
         if not (dh is not None and z is not None and r_pre is not None):
             _bad("the pre norm needs dh, z and r_pre")
-        dh, ld_h = _rows(dh, "dh", d, dt, rows)
-        z, ld = _rows(z, "z", d, dt, rows)
+        dh, ld_h = _rows(dh, "dh", d, gpu, dt, rows)
+        z, ld = _rows(z, "z", d, gpu, dt, rows)
         if dz is not None and ld != ld_z and rows > 1:      # the library has one stride for the two
             dz, z, ld = dz.contiguous(), z.contiguous(), d
         ld_z = ld
-        r_pre = _vector(r_pre, "r_pre", rows, torch.float32)
+        r_pre = _vector(r_pre, "r_pre", rows, torch.float32, gpu)
     if f is not None:
-        f, ld_f = _rows(f, "f", d, dt, rows)
+        f, ld_f = _rows(f, "f", d, gpu, dt, rows)
     if post:
         if not (r_post is not None):
             _bad("the post norm needs r_post")
-        r_post = _vector(r_post, "r_post", rows, torch.float32)
-    gate, ld_g = _gate(gate, gate_kind, rows, d, dt)
-    w_post = _vector(w_post, "w_post", d, dt) if post else None
-    w_pre = _vector(w_pre, "w_pre", d, dt) if pre else None
+        r_post = _vector(r_post, "r_post", rows, torch.float32, gpu)
+    gate, ld_g = _gate(gate, gate_kind, rows, d, dt, gpu)
+    w_post = _vector(w_post, "w_post", d, dt, gpu) if post else None
+    w_pre = _vector(w_pre, "w_pre", d, dt, gpu) if pre else None
 
     dx = torch.empty((rows, d), dtype=dt, device=dev) if need_dx else None
     df = dgate = None
@@ -310,9 +326,9 @@ def _embed_plan(*fields):
     return _plan(MoeEmbedConfig(*fields), lib().moe_embed_workspace_bytes)
 
 
-def _ids(ids):
-    if not (ids.dtype in (torch.int32, torch.int64) and ids.is_cuda):
-        _bad("ids must be int32 or int64 on the GPU")
+def _ids(ids, gpu):
+    if not (ids.dtype in (torch.int32, torch.int64) and ids.get_device() == gpu):
+        _bad("ids must be int32 or int64 on GPU %d", gpu)
     return ids if ids.dim() == 1 and ids.is_contiguous() else ids.reshape(-1).contiguous()
 
 
@@ -325,10 +341,11 @@ def embed_forward(ids, table, *, scale=1.0, out=None, stream=None):
     if not (table.dim() == 2 and table.dtype in _ELEM):
         _bad("table must be a bf16, fp16 or fp32 matrix [V, d]")
     V, d = table.shape
-    table, ld_t = _rows(table, "table", d)
-    flat = _ids(ids)
+    gpu = _gpu(table, "table")
+    table, ld_t = _rows(table, "table", d, gpu)
+    flat = _ids(ids, gpu)
     rows, el = flat.shape[0], _ELEM[table.dtype]
-    res, ld_o = _out(out, "out", rows, d, table.dtype, table.device)
+    res, ld_o = _out(out, "out", rows, d, table.dtype, table.device, gpu)
     plan = _embed_plan(rows, V, d, el, el, int(flat.dtype == torch.int64), 0, scale, ld_t, ld_o)
     check(lib().moe_embed_forward(plan[1], flat.data_ptr(), table.data_ptr(), res.data_ptr(), _stream(None)))
     return res if out is not None or ids.dim() == 1 else res.view(*ids.shape, d)
@@ -342,19 +359,20 @@ def embed_backward(ids, dout, V, *, scale=1.0, dtable=None, grad_dtype=None, acc
     if stream is not None:
         return _on(stream, embed_backward, ids, dout, V, scale=scale, dtable=dtable, grad_dtype=grad_dtype,
                    accumulate=accumulate)
-    flat = _ids(ids)
+    gpu = _gpu(dout, "dout")
+    flat = _ids(ids, gpu)
     if not (dout.dtype in _ELEM and dout.dim() >= 2):
         _bad("dout must be bf16, fp16 or fp32 [rows, d]")
     d = dout.shape[-1]
     if dout.dim() != 2:
         dout = dout.reshape(-1, d)
-    dout, ld_o = _rows(dout, "dout", d, None, flat.shape[0])
+    dout, ld_o = _rows(dout, "dout", d, gpu, None, flat.shape[0])
     if not (not accumulate or dtable is not None):
         _bad("accumulate adds to a given dtable")
     grad_dtype = grad_dtype or (dtable.dtype if dtable is not None else dout.dtype)
     if not (grad_dtype in (dout.dtype, torch.float32)):
         _bad("dtable is of dout's type or float32")
-    dtable, ld_t = _out(dtable, "dtable", V, d, grad_dtype, dout.device)
+    dtable, ld_t = _out(dtable, "dtable", V, d, grad_dtype, dout.device, gpu)
     plan = _embed_plan(flat.shape[0], V, d, _ELEM[dout.dtype], _ELEM[grad_dtype], int(flat.dtype == torch.int64),
                        int(accumulate), scale, ld_t, ld_o)
     ws = _ws(plan, dout.device)

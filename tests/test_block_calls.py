@@ -89,6 +89,7 @@ def gpu(monkeypatch):
     monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle: {11: MAIN, 22: SIDE}[handle])
     monkeypatch.setattr(block, "_stream", lambda s: s if isinstance(s, int) else (s or state.stream).cuda_stream)
     monkeypatch.setattr(block, "lib", Library)
+    monkeypatch.setattr(block, "_current_gpu", lambda: state.current, raising=False)
     plans = (block._grouped_plan, block._norm_plan, block._embed_plan)
     for p in plans:
         p.cache_clear()
@@ -148,3 +149,29 @@ def test_copies_and_memory_belong_to_the_stream_of_the_launch(gpu, i, given):
         for t in out if isinstance(out, tuple) else (out,):
             if t is not None:
                 assert (MAIN, t.untyped_storage().data_ptr()) in kept
+
+
+@pytest.mark.parametrize("i", range(6), ids=CALLS)
+def test_tensors_on_another_gpu_are_refused(gpu, i):
+    """All on the current GPU, or a ValueError before anything is launched."""
+    fn, tensors, opts = calls(lambda *s: on(Gpu, *s), lambda n, dt: on(Gpu, n, dtype=dt))[i]
+    fn(**tensors, **opts)
+    assert len([e for e in gpu.log if e[0] == "launch"]) == 1
+    for name, t in tensors.items():
+        with pytest.raises(ValueError):
+            fn(**{**tensors, name: t.as_subclass(OtherGpu)}, **opts)
+        with pytest.raises(ValueError):
+            fn(**{**tensors, name: t.as_subclass(torch.Tensor)}, **opts)
+    with pytest.raises(ValueError):
+        fn(**{k: t.as_subclass(OtherGpu) for k, t in tensors.items()}, **opts)
+    outputs = {"grouped_forward": dict(out=(6, 4)), "grouped_backward": dict(dx=(6, 5), dw=(3, 4, 5)),
+               "norm_forward": dict(z=(6, 5), h=(6, 5)), "embed_forward": dict(out=(6, 5)),
+               "embed_backward": dict(dtable=(7, 5))}
+    for name, shape in outputs.get(CALLS[i], {}).items():
+        fn(**tensors, **opts, **{name: on(Gpu, *shape)})
+        with pytest.raises(ValueError):
+            fn(**tensors, **opts, **{name: on(OtherGpu, *shape)})
+    assert len([e for e in gpu.log if e[0] == "launch"]) == 1 + len(outputs.get(CALLS[i], {}))
+    gpu.current = 1
+    with pytest.raises(ValueError):
+        fn(**tensors, **opts)
