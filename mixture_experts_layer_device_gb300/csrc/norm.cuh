@@ -142,8 +142,9 @@ MOE_DEV RowIn row_in(const NormArgs &a, long row) {
 //   s[0] <w_pre dh, z>, s[1] <dz, q>, s[2] <w_pre dh, q>, s[3] <z, q>
 // with q = w_post g f, g without a row gate:
 //   t = dz + rp (w_pre dh) - c1 (rp z),   c1 = rp^2 s[0] / d
-//   df = a1 (w_post g t) - c2 f,          a1 = rq rg, c2 = rq^3 rg <t, q> / d
-// Also writes a row gate's gradient <t, n>.
+//   df = a1 (w_post g t) - c2 (a1 f),     a1 = rq rg, c2 = rq^2 <t, q> / d
+// Multiplied in this order no factor leaves fp32 before the roots' own squares do
+// (rq^3 would at |f| of 1e13).  Also writes a row gate's gradient <t, n>.
 struct RowTerms {
   float rp, c1, a1, c2;
 };
@@ -152,11 +153,11 @@ MOE_DEV RowTerms row_terms(const NormArgs &a, bool post, long row, const RowIn &
                            bool first) {
   RowTerms t;
   t.rp = in.rp;
-  t.c1 = in.rp * in.rp * s[0] * inv_d;
+  t.c1 = in.rp * (in.rp * (s[0] * inv_d));
   float tq = s[1] + in.rp * (s[2] - t.c1 * s[3]);  // <t, q>
   if (!post && !(a.flags & MOE_NORM_PRE)) tq = s[1];  // f may be infinite: no 0 * inf of the terms that are not there
   t.a1 = in.rq * in.rg;
-  t.c2 = post ? in.rq * in.rq * in.rq * in.rg * tq * inv_d : 0.f;
+  t.c2 = post ? in.rq * (in.rq * (tq * inv_d)) : 0.f;
   if (a.gate == MOE_GATE_ROW && a.dg && first) static_cast<T *>(a.dg)[row] = Elem<T>::from(tq * in.rq);
   return t;
 }
@@ -186,7 +187,7 @@ MOE_DEV ElemOut elem_out(const RowTerms &t, bool post, float alpha, float dz, fl
   acc1 = fmaf(tg, nh, acc1);
   o.dx = alpha * tt;
   o.dg = tw * nh;
-  o.df = fmaf(t.a1, tw * g, post ? -(t.c2 * f) : 0.f);
+  o.df = fmaf(t.a1, tw * g, post ? -(t.c2 * nh) : 0.f);
   return o;
 }
 

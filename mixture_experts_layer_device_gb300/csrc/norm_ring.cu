@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(THREADS, THREADS <= 256 ? 2 : 1) norm_bwd_ring
         }
         acc1[i][k] = f2_fma(tg, nh, acc1[i][k]);
         dz[k] = f2_mul(alpha, tt);
-        f[k] = f2_fma(a1, tw, POST ? f2_mul(c2, f[k]) : 0);
+        f[k] = f2_fma(a1, tw, POST ? f2_mul(c2, nh) : 0);
       }
       col.store_or_keep(dx, i, dx, dz, parts[turn][0]);
       col.store_or_keep(df, i, df, f, parts[turn][1]);

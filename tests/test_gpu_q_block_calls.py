@@ -123,3 +123,21 @@ def test_norm_gradient_of_an_infinite_block_output_without_its_norm(blk, rows, d
     for name, t in (("dx", dx), ("df", df), ("dw_pre", dw)):
         assert np.all(np.isfinite(ref[name]))
         near(t, ref[name], size[name], d + rows)
+
+
+@pytest.mark.parametrize("rows,d", NORM_PATHS)
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("size", [2.0 ** 47, 2.0 ** -47])
+def test_norm_gradients_of_large_and_small_rows(blk, rows, d, dtype, size):
+    """rms(f) and rms(z) whose cubes leave fp32 while their squares do not: all gradients, relative to their
+    own terms (df and dx are of the size of t / rms)."""
+    g = gen(d + 1)
+    f, z, dz, dh = draw((rows, d), dtype, g, size), draw((rows, d), dtype, g, size), draw((rows, d), dtype, g, 1 / size), \
+        draw((rows, d), dtype, g)
+    wq, wp, gate = draw((d,), dtype, g), draw((d,), dtype, g), draw((rows,), dtype, g)
+    rq, rp = (torch.rsqrt(t.double().square().mean(1)).float() for t in (f, z))
+    got = blk.norm_backward(dz, dh, z, f, gate, wq, wp, rq, rp, gate_kind="row")
+    ref, sz = ob.norm_backward(*(f64(t) for t in (dz, dh, z, f, gate, wq, wp, rq, rp)), kind="row")
+    for name, t in zip(("dx", "df", "dgate", "dw_post", "dw_pre"), got):
+        tol = U[dtype] * np.abs(ref[name]) + (d + rows + 32) * 2.0 ** -22 * sz[name]
+        assert np.all(np.isfinite(f64(t))) and np.all(np.abs(f64(t) - ref[name]) <= tol), name
