@@ -175,3 +175,23 @@ def test_tensors_on_another_gpu_are_refused(gpu, i):
     gpu.current = 1
     with pytest.raises(ValueError):
         fn(**tensors, **opts)
+
+
+def test_gradients_of_narrow_slices_take_no_wide_memory(gpu):
+    """A gradient of a few columns of a wide buffer is not as wide as the buffer; one of a part
+    of a fused buffer shares its stride, without a copy."""
+    R, E, N, K = 64, 2, 40, 48
+
+    def backward(wide):
+        x, f, gate = (on(Gpu, R, wide * K)[:, :K] for _ in range(3))
+        dy, z, v, r = on(Gpu, R, N), on(Gpu, R, K), on(Gpu, K), on(Gpu, R, dtype=torch.float32)
+        gpu.log.clear()
+        gpu.allocated = 0
+        dx, dw = block.grouped_backward(dy, x, on(Gpu, E, N, K), on(Gpu, E + 1, dtype=torch.int32), need_dw=False)
+        assert dx.shape == (R, K) and dw is None
+        out = block.norm_backward(z, z, z, f, gate, v, v, r, r, gate_kind="full")
+        assert all(t.shape == (R, K) for t in out[:3])
+        return sum(e[0] == "copy" for e in gpu.log)
+
+    assert backward(64) == 3 and gpu.allocated <= 2 * R * K * 2
+    assert backward(8) == 0 and gpu.allocated <= 8 * R * K * 2

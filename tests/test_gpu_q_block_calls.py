@@ -141,3 +141,20 @@ def test_norm_gradients_of_large_and_small_rows(blk, rows, d, dtype, size):
     for name, t in zip(("dx", "df", "dgate", "dw_post", "dw_pre"), got):
         tol = U[dtype] * np.abs(ref[name]) + (d + rows + 32) * 2.0 ** -22 * sz[name]
         assert np.all(np.isfinite(f64(t))) and np.all(np.abs(f64(t) - ref[name]) <= tol), name
+
+
+# ---------------------------------------------------------------- memory
+def test_gradients_of_narrow_slices(blk):
+    """A few columns of a wide buffer: the gradients of the same columns by themselves."""
+    g = gen(3)
+    R, E, N, K = 300, 3, 64, 72
+    x, f, gate = (draw((R, 16 * K), BF, g)[:, i * K:(i + 1) * K] for i in (0, 1, 15))
+    dy, w, v = draw((R, N), BF, g), draw((E, N, K), BF, g), draw((K,), BF, g)
+    off = torch.tensor([0, 100, 100, R], dtype=torch.int32, device="cuda")
+    z, dz, dh = (draw((R, K), BF, g) for _ in range(3))
+    r = torch.rand(R, generator=g, device="cuda") + 0.5
+    got = (*blk.grouped_backward(dy, x, w, off), *blk.norm_backward(dz, dh, z, f, gate, v, v, r, r, gate_kind="full"))
+    c = [t.contiguous() for t in (x, f, gate)]
+    want = (*blk.grouped_backward(dy, c[0], w, off), *blk.norm_backward(dz, dh, z, c[1], c[2], v, v, r, r, gate_kind="full"))
+    assert len(got) == 7 and all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all(t.untyped_storage().nbytes() <= t.numel() * t.element_size() for t in got)
