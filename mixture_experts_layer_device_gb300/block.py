@@ -373,7 +373,7 @@ def embed_backward(ids, dout, V, *, scale=1.0, dtable=None, grad_dtype=None, acc
                    accumulate=accumulate)
     gpu = _gpu(dout, "dout")
     flat = _ids(ids, gpu)
-    if not (dout.dtype in _ELEM and dout.dim() >= 2):
+    if not (dout.dtype in _ELEM and dout.dim() >= min(2, 1 + ids.dim())):
         _bad("dout must be bf16, fp16 or fp32 [rows, d]")
     d = dout.shape[-1]
     if dout.dim() != 2:

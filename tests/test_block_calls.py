@@ -195,3 +195,13 @@ def test_gradients_of_narrow_slices_take_no_wide_memory(gpu):
 
     assert backward(64) == 3 and gpu.allocated <= 2 * R * K * 2
     assert backward(8) == 0 and gpu.allocated <= 8 * R * K * 2
+
+
+def test_an_embedding_of_one_id(gpu):
+    """ids of any shape, a single one without a dimension among them, in both directions."""
+    ids, table = torch.tensor(3).as_subclass(Gpu), on(Gpu, 7, 5)
+    out = block.embed_forward(ids, table)
+    assert out.shape == (5,)
+    assert block.embed_backward(ids, out, 7).shape == (7, 5)
+    with pytest.raises(ValueError):
+        block.embed_backward(on(Gpu, 2, dtype=torch.int64), out, 7)

@@ -158,3 +158,14 @@ def test_gradients_of_narrow_slices(blk):
     want = (*blk.grouped_backward(dy, c[0], w, off), *blk.norm_backward(dz, dh, z, c[1], c[2], v, v, r, r, gate_kind="full"))
     assert len(got) == 7 and all(torch.equal(a, b) for a, b in zip(got, want))
     assert all(t.untyped_storage().nbytes() <= t.numel() * t.element_size() for t in got)
+
+
+def test_embedding_of_a_single_id_trains(blk):
+    from mixture_experts_layer_device_gb300.module import TokenEmbedding
+    m = TokenEmbedding(7, 24, scale=2.0)
+    y = m(torch.tensor(3, device="cuda"))
+    assert torch.equal(y, 2.0 * m.weight[3])
+    y.sum().backward()
+    want = torch.zeros_like(m.weight)
+    want[3] = 2.0
+    assert torch.equal(m.weight.grad, want)
