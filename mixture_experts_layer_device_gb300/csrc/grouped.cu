@@ -190,7 +190,7 @@ MOE_DEV void acc_place(int warp, int lane, int i, int j, int k, int &m, int &n) 
 
 template <typename T, int DIR>
 __global__ void __launch_bounds__(128) grouped_plain_kernel(const GroupedArgs g) {
-  pdl_wait();  // the plan's tile table
+  pdl_wait();  // the plan's tile table, read by ordinary loads: it is written while this kernel may already run
   Side a, b;
   int lo, hi, n0, m0, mn, nn, nk;
   void *out;
@@ -213,10 +213,10 @@ __global__ void __launch_bounds__(128) grouped_plain_kernel(const GroupedArgs g)
           (static_cast<long>(e) * g.N * g.K + static_cast<long>(m0) * g.K + n0) * (wide ? 4 : 2);
     ldo = g.K;
   } else {
-    if (static_cast<int>(blockIdx.x) >= __ldg(g.tiles + g.E)) return;
+    if (static_cast<int>(blockIdx.x) >= g.tiles[g.E]) return;
     const int e = group_of_tile(g.tiles, g.E, blockIdx.x);
     group_rows(g, e, lo, hi);
-    m0 = lo + (blockIdx.x - __ldg(g.tiles + e)) * PT;
+    m0 = lo + (blockIdx.x - g.tiles[e]) * PT;
     n0 = blockIdx.y * PT;
     mn = hi - m0;
     const uint16_t *w = static_cast<const uint16_t *>(g.w) + static_cast<long>(e) * g.ld_e;
