@@ -21,9 +21,9 @@ DTYPES = {"bf16": MOE_BF16, "mxfp8": MOE_MXFP8, "nvfp4": MOE_NVFP4}
 MOE_FLAG_BACKWARD = 1
 MOE_FLAG_DEBUG_STARVE = 2
 MOE_FLAG_DEBUG_DUMP = 4
-STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported shape", -3: "pointer not 16-byte aligned",
+STATUS = {0: "ok", -1: "invalid argument", -2: "unsupported shape", -3: "pointer not aligned as its entry point requires",
           -4: "CUDA error", -5: "device is not sm_103", -6: "a device-side wait timed out",
-          -7: "a device-side bounds check failed (debug build)"}
+          -7: "a device-side bounds check failed: an index or offset out of range"}
 
 MOE_ELEM_BF16, MOE_ELEM_FP16, MOE_ELEM_FP32 = 0, 1, 2
 MOE_NORM_POST, MOE_NORM_PRE = 1, 2

@@ -1386,11 +1386,11 @@ const char *moe_status_string(int status) {
     case MOE_OK: return "ok";
     case MOE_ERR_ARG: return "invalid argument";
     case MOE_ERR_SHAPE: return "unsupported shape";
-    case MOE_ERR_ALIGN: return "pointer not 16-byte aligned";
+    case MOE_ERR_ALIGN: return "pointer not aligned as its entry point requires";
     case MOE_ERR_CUDA: return "CUDA error";
     case MOE_ERR_DEVICE: return "device is not sm_103";
     case MOE_ERR_TIMEOUT: return "a device-side wait timed out";
-    case MOE_ERR_BOUNDS: return "a device-side bounds check failed (debug build)";
+    case MOE_ERR_BOUNDS: return "a device-side bounds check failed: an index or offset out of range";
     default: return "unknown status";
   }
 }

@@ -10,7 +10,7 @@ namespace moe {
 
 // Device status word bits (kept in the workspace, read by moe_get_status).
 constexpr int kStatusTimeout = 1;
-constexpr int kStatusBounds = 2;  // a debug-build bounds check failed
+constexpr int kStatusBounds = 2;  // a bounds check failed (debug builds; the grouped products: every build)
 // Default limit of every device-side wait.
 constexpr unsigned long long kWaitTimeoutNs = 4000000000ull;
 

@@ -205,3 +205,13 @@ def test_an_embedding_of_one_id(gpu):
     assert block.embed_backward(ids, out, 7).shape == (7, 5)
     with pytest.raises(ValueError):
         block.embed_backward(on(Gpu, 2, dtype=torch.int64), out, 7)
+
+
+def test_status_texts_hold_for_every_entry_point():
+    """The grouped products report offsets out of range in every build, and around the
+    layer a pointer needs its element's alignment only."""
+    from mixture_experts_layer_device_gb300 import STATUS, build, lib
+    build.build()
+    for code in (-3, -7):
+        text = lib().moe_status_string(code).decode()
+        assert text == STATUS[code] and "debug" not in text and "16" not in text
