@@ -169,3 +169,75 @@ def test_embedding_of_a_single_id_trains(blk):
     want = torch.zeros_like(m.weight)
     want[3] = 2.0
     assert torch.equal(m.weight.grad, want)
+
+
+# ---------------------------------------------------------------- outputs in their inputs' place
+@pytest.mark.parametrize("kind", ["none", "channel", "row", "full"])
+@pytest.mark.parametrize("rows,d", [(40, 200), (40, 4096), (40, 2883), (700, 2883), (700, 4096), (2000, 515), (170, 13000)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_norm_backward_in_place(blk, rows, d, kind, dtype):
+    """dx in dz's buffer and df in f's, as the boundary allows: the numbers of separate buffers."""
+    import mixture_experts_layer_device_gb300 as pkg
+    g = gen(rows + d)
+    dz, dh, z, f = (draw((rows, d), dtype, g) for _ in range(4))
+    shape = {"none": None, "channel": (d,), "row": (rows,), "full": (rows, d)}[kind]
+    gate = None if shape is None else draw(shape, dtype, g)
+    wq, wp = draw((d,), dtype, g), draw((d,), dtype, g)
+    rq, rp = (torch.rand(rows, generator=g, device="cuda") + 0.5 for _ in range(2))
+    want = blk.norm_backward(dz, dh, z, f, gate, wq, wp, rq, rp, gate_kind=kind, alpha=0.5)
+    cfg = pkg.MoeNormConfig(rows, d, {BF: 0, FP: 2}[dtype], 3, pkg.GATES[kind], 0.5, 0.0, 0, 0, 0, 0, 0)
+    ws = torch.empty(pkg.moe_norm_workspace_bytes(cfg), dtype=torch.uint8, device="cuda")
+    dg, dwq, dwp = None if gate is None else torch.empty_like(gate), torch.empty_like(wq), torch.empty_like(wp)
+    pkg.check(pkg.moe_norm_backward(cfg, dz, dh, z, f, gate, wq, wp, rq, rp, dz, f, dg, dwq, dwp, ws))
+    for a, b in zip((dz, f, dg, dwq, dwp), want):
+        assert a is b or torch.equal(a, b)
+
+
+@pytest.mark.parametrize("rows,d", [(40, 200), (40, 4096), (700, 2883), (700, 4096), (170, 20000)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_norm_forward_into_the_residual_stream(blk, rows, d, dtype):
+    """z in x's buffer: the residual stream updated where it lies."""
+    g = gen(rows + d)
+    x, f, w = draw((rows, d), dtype, g), draw((rows, d), dtype, g), draw((d,), dtype, g)
+    want = blk.norm_forward(x, f, None, w, w)
+    got = blk.norm_forward(x, f, None, w, w, z=x)
+    assert got[0] is x and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ---------------------------------------------------------------- rows where the kernels change
+def products(blk, x, w, off):
+    with np.errstate(invalid="ignore"):
+        ref, size = ob.grouped_forward(f64(x), f64(w), off.cpu().numpy())
+    near(blk.grouped_forward(x, w, off), ref, size, x.shape[1])
+
+
+@pytest.mark.parametrize("rows", [1, 5, 64, 65])
+@pytest.mark.parametrize("at", [0, 17, 39])
+def test_grouped_all_rows_on_one_of_many_experts(blk, rows, at):
+    """The streaming kernel's rule looks at the average; all rows may be one expert's."""
+    g = gen(rows)
+    x, w = draw((rows, 136), BF, g), draw((40, 200, 136), BF, g)
+    off = torch.zeros(41, dtype=torch.int32, device="cuda")
+    off[at + 1:] = rows
+    products(blk, x, w, off)
+
+
+@pytest.mark.parametrize("shift", [1, 4, 8])
+@pytest.mark.parametrize("which", ["x", "w", "dy", "all"])
+def test_grouped_operands_off_16_bytes(blk, which, shift):
+    """Row strides that are whole 16-byte pieces, and rows that start inside one."""
+    g = gen(shift)
+    R, E, N, K = 400, 4, 128, 256
+    off = torch.tensor([0, 100, 100, 333, 398], dtype=torch.int32, device="cuda")
+
+    def make(name, *shape):
+        cut = which in (name, "all")
+        t = draw((*shape[:-1], shape[-1] + 16), BF, g)
+        return t[..., shift:shift + shape[-1]] if cut else t[..., :shape[-1]].contiguous()
+
+    x, w, dy = make("x", R, K), make("w", E, N, K), make("dy", R, N)
+    products(blk, x, w, off)
+    dx, dw = blk.grouped_backward(dy, x, w, off)
+    rx, rw, sx, sw = ob.grouped_backward(f64(dy), f64(x), f64(w), off.cpu().numpy())
+    near(dx, rx, sx, N)
+    near(dw, rw, sw, 233)
