@@ -264,7 +264,7 @@ def norm_forward(x, f=None, gate=None, w_post=None, w_pre=None, *, gate_kind="no
     if post:
         r_post = torch.empty(rows, dtype=torch.float32, device=dev)
     plan = _norm_plan(rows, d, _ELEM[x.dtype], (MOE_NORM_POST if post else 0) | (MOE_NORM_PRE if pre else 0),
-                      GATES[gate_kind], alpha, eps, ld_x, ld_f, ld_z, ld_h, ld_g)
+                      GATES[gate_kind], float(alpha), float(eps), ld_x, ld_f, ld_z, ld_h, ld_g)
     z, h = z if need_z else None, h if pre else None
     check(lib().moe_norm_forward(plan[1], x.data_ptr(), _ptr(f), _ptr(gate), _ptr(w_post), _ptr(w_pre), _ptr(z),
                                  _ptr(h), _ptr(r_post), _ptr(r_pre), _stream(None)))
@@ -324,7 +324,7 @@ def norm_backward(dz, dh, z, f=None, gate=None, w_post=None, w_pre=None, r_post=
     dw_post = torch.empty_like(w_post) if need_dw and w_post is not None else None
     dw_pre = torch.empty_like(w_pre) if need_dw and w_pre is not None else None
     plan = _norm_plan(rows, d, _ELEM[dt], (MOE_NORM_POST if post else 0) | (MOE_NORM_PRE if pre else 0),
-                      GATES[gate_kind], alpha, 0.0, d, ld_f, ld_z, ld_h, ld_g)
+                      GATES[gate_kind], float(alpha), 0.0, d, ld_f, ld_z, ld_h, ld_g)
     ws = _ws(plan, dev)
     check(lib().moe_norm_backward(plan[1], _ptr(dz), _ptr(dh), _ptr(z), _ptr(f), _ptr(gate), _ptr(w_post),
                                   _ptr(w_pre), _ptr(r_post), _ptr(r_pre), _ptr(dx), _ptr(df), _ptr(dgate),
@@ -358,7 +358,7 @@ def embed_forward(ids, table, *, scale=1.0, out=None, stream=None):
     flat = _ids(ids, gpu)
     rows, el = flat.shape[0], _ELEM[table.dtype]
     res, ld_o = _out(out, "out", rows, d, table.dtype, table.device, gpu)
-    plan = _embed_plan(rows, V, d, el, el, int(flat.dtype == torch.int64), 0, scale, ld_t, ld_o)
+    plan = _embed_plan(rows, V, d, el, el, int(flat.dtype == torch.int64), 0, float(scale), ld_t, ld_o)
     check(lib().moe_embed_forward(plan[1], flat.data_ptr(), table.data_ptr(), res.data_ptr(), _stream(None)))
     return res if out is not None or ids.dim() == 1 else res.view(*ids.shape, d)
 
@@ -386,7 +386,7 @@ def embed_backward(ids, dout, V, *, scale=1.0, dtable=None, grad_dtype=None, acc
         _bad("dtable is of dout's type or float32")
     dtable, ld_t = _out(dtable, "dtable", V, d, grad_dtype, dout.device, gpu)
     plan = _embed_plan(flat.shape[0], V, d, _ELEM[dout.dtype], _ELEM[grad_dtype], int(flat.dtype == torch.int64),
-                       int(accumulate), scale, ld_t, ld_o)
+                       int(accumulate), float(scale), ld_t, ld_o)
     ws = _ws(plan, dout.device)
     check(lib().moe_embed_backward(plan[1], flat.data_ptr(), dout.data_ptr(), dtable.data_ptr(), ws.data_ptr(),
                                    _stream(None)))

@@ -163,7 +163,7 @@ class BlockNormFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, f, gate, w_post, w_pre, gate_kind, post, pre, alpha, eps):
-        post = post and f is not None
+        post, alpha = post and f is not None, float(alpha)
         z, h, r_post, r_pre = block.norm_forward(x, f, gate, w_post, w_pre, gate_kind=gate_kind, post=post, pre=pre,
                                                  alpha=alpha, eps=eps)
         ctx.opts = dict(gate_kind=gate_kind, post=post, pre=pre, alpha=alpha)
@@ -218,8 +218,8 @@ class EmbeddingFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, ids, table, scale):
         ctx.save_for_backward(ids)
-        ctx.V, ctx.scale = table.shape[0], scale
-        return block.embed_forward(ids, table, scale=scale)
+        ctx.V, ctx.scale = table.shape[0], float(scale)
+        return block.embed_forward(ids, table, scale=ctx.scale)
 
     @staticmethod
     def backward(ctx, dout):

@@ -215,3 +215,30 @@ def test_status_texts_hold_for_every_entry_point():
     for code in (-3, -7):
         text = lib().moe_status_string(code).decode()
         assert text == STATUS[code] and "debug" not in text and "16" not in text
+
+
+def test_numbers_are_read_at_every_call(gpu, monkeypatch):
+    """alpha, eps and scale given as tensors that change in place: nothing is kept by which object came."""
+    seen = []
+
+    class Reading(Library):
+        def __getattr__(self, name):
+            def call(*args):
+                if name.endswith("workspace_bytes"):
+                    return 512
+                cfg = args[0]._obj
+                seen.append((cfg.alpha, cfg.eps) if "norm" in name else cfg.scale)
+                return 0
+            return call
+
+    monkeypatch.setattr(block, "lib", Reading)
+    x, ids, number = on(Gpu, 6, 5), on(Gpu, 6, dtype=torch.int64), torch.tensor(0.5)
+    r = on(Gpu, 6, dtype=torch.float32)
+    for value in (0.5, 0.25):
+        number.fill_(value)
+        seen.clear()
+        block.norm_forward(x, x, alpha=number, eps=number)
+        block.norm_backward(x, x, x, x, r_post=r, r_pre=r, alpha=number)
+        block.embed_forward(ids, x, scale=number)
+        block.embed_backward(ids, x, 7, scale=number)
+        assert seen == [(value, value), (value, 0.0), value, value]

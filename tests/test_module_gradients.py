@@ -100,3 +100,16 @@ def test_a_gradient_that_depends_on_nothing_stays_a_constant(plain):
     assert not g.requires_grad
     (y.sum() + g.square().sum()).backward()
     assert torch.allclose(x.grad, g)
+
+
+def test_the_backward_uses_the_forwards_numbers(plain, monkeypatch):
+    """A scale or alpha given as a tensor that changes in place in between."""
+    table, x, f, number = leaf(7, 3), leaf(5, 3), leaf(5, 3), torch.tensor(2.0)
+    seen = []
+    kept = module.block.norm_backward
+    monkeypatch.setattr(module.block, "norm_backward", lambda *a, **kw: seen.append(float(kw["alpha"])) or kept(*a, **kw))
+    y = module.EmbeddingFunction.apply(torch.tensor([0, 4]), table, number)
+    z, h = module.BlockNormFunction.apply(x, f, None, None, None, "none", False, True, number, 1e-6)
+    number.fill_(3.0)
+    (y.sum() + h.sum()).backward()
+    assert torch.equal(table.grad[4], torch.full((3,), 2.0)) and seen == [2.0]
