@@ -141,7 +141,9 @@ def grouped_forward(x, w, offsets, *, out=None, out_dtype=None, return_workspace
     """y [rows, N]: y[r] = x[r] w[e]^T for the rows offsets[e] <= r < offsets[e + 1]
     of expert e (0 for a row of no expert).  x [rows, K] and w [E, N, K] bf16 or
     fp16, offsets int32 [E + 1] on the GPU as moe_route writes them; y of x's
-    type or fp32 (out_dtype, or out's)."""
+    type or fp32 (out_dtype, or out's).  Rows of w (and of x, from a column on) may
+    be strided; a w whose last two dimensions lie in the other order is copied
+    whole in every call."""
     if stream is not None:
         return _on(stream, grouped_forward, x, w, offsets, out=out, out_dtype=out_dtype, return_workspace=return_workspace)
     gpu, w, offsets, E, N, K, ld_w = _grouped(x, w, offsets, "x")
@@ -205,8 +207,9 @@ def grouped_backward(dy, x, w, offsets, *, dx=None, dw=None, need_dx=True, need_
 
 
 def grouped_status(ws, stream=None):
-    """Synchronises; the device status of the call that used workspace `ws`
-    (return_workspace=True): 0, or -7 when its offsets descend or leave the rows."""
+    """Synchronises the current stream, or `stream`: the one that the call ran on.  The
+    device status of the call that used workspace `ws` (return_workspace=True): 0, or
+    -7 when its offsets descend or leave the rows."""
     return moe_get_status(ws, stream)
 
 

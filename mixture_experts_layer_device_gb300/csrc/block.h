@@ -44,9 +44,10 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream
 }
 
 // ---------------------------------------------------------------- grouped products
-// One product of the three directions as a strided matrix product per group:
-//   out[m, n] (+)= sum_k a[m, k] b[n, k]
-// with element (i, k) of an operand at base + i * s_i + k * s_k.
+// The three directions are one matrix product per expert, out[m, n] (+)= sum_k a[m, k]
+// b[n, k], with the expert's rows on m (forward, dgrad) or on k (wgrad).  The plain kernel
+// addresses both operands by two strides; the tensor-core kernel has the tokens on its
+// instruction's N side and reads each operand in the major in which it lies.
 enum GroupedDir { GROUPED_FWD = 0, GROUPED_DGRAD = 1, GROUPED_WGRAD = 2 };
 
 struct GroupedArgs {

@@ -51,9 +51,15 @@ int grouped_check(const moe_grouped_config *c, moe::GroupedArgs *g) {
 
 // Operands whose row strides TMA cannot address are first copied into padded rows
 // in the workspace, where the product is large against the copies.  Measured in
-// bf16 at experts of [1057, 2001], 8000 rows: 16 experts (500 rows each) forward 106
-// us with copies, 364 on the plain kernel; 150 experts (53 rows each) forward about
-// even, weight gradient (which copies no weights) 661 us, 1488.
+// bf16 at experts of [1057, 2001], us with copies / on the plain kernel, by the
+// multiply-adds per copied element that the rule asks for 64 of:
+//   forward   8000 rows, 16 experts (339): 97 / 352     100 experts (74): 282 / 517
+//             2000 rows, 40 experts (48): 122 / 157     8000, 150 experts (51): 400 / 418
+//             8000 rows, 300 experts (26): 763 / 747
+//   dgrad     8000 rows, 150 experts (52): 390 / 507    300 experts (26): 747 / 943
+//   wgrad     (copies no weights, 692)  2000 rows, 40 experts: 158 / 337
+// The host does not know which experts have rows, so all their weights count as
+// copied, though those of experts without rows are not.
 long pad8(long n) { return (n + 7) / 8 * 8; }
 struct GroupedPads {
   bool w, x, dy;  // the operands of the product whose strides need it
@@ -110,6 +116,8 @@ bool tma_rows(const void *p, long ld) { return aligned(p, 16) && ld % 8 == 0; }
 
 // Brings the operands of one product into TMA's form: true when the tensor-core
 // kernel can run on *t (copies launched where needed; `have_dy`: dy's has been made).
+// The copies mend strides only: an operand whose rows are whole 16-byte pieces but
+// start inside one (a view from a column on) goes to the plain kernel, whatever its size.
 struct Padded {
   bool ok;
   int rc;
@@ -154,8 +162,18 @@ Padded grouped_tensor(const moe::GroupedArgs &g, int dir, uint8_t *ws, moe::Grou
   return {true, MOE_OK};
 }
 
-// Few rows that mostly have an expert of their own: reading the weights bounds
-// the call and the tensor cores have nothing to reuse.
+// Few rows: reading the weights bounds the call, and the tensor cores have little to
+// reuse.  By the average over all experts, as the offsets are on the device.  Measured at
+// experts of [2048, 4096] in bf16, us here / on the tensor cores:
+//                            rows spread over the experts   all on one expert
+//   8 experts, 1 row         11 / 27
+//   8 experts, 16 rows       28 / 32                        19 / 27
+//   32 experts, 64 rows      84 / 102                       48 / 27
+//   512 experts, 10 rows     30 / 54                        17 / 27
+//   512 experts, 32 rows     82 / 103                       33 / 27
+//   512 experts, 64 rows     152 / 178                      53 / 27
+// An expert's weights are read again for every four of its rows: from some 25 rows of one
+// expert on (a call whose rows all take one adapter) the tensor cores would be faster.
 bool grouped_few(const moe::GroupedArgs &g) {
   return g.rows > 0 && g.rows <= 64 && g.rows <= 2L * g.E && g.K % 8 == 0 && tma_rows(g.x, g.ld_x) &&
          tma_rows(g.w, g.ld_w) && g.ld_e % 8 == 0;
