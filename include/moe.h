@@ -511,6 +511,104 @@ size_t moe_embed_workspace_bytes(const moe_embed_config *cfg);
 int moe_embed_backward(const moe_embed_config *cfg, const void *ids, const void *dout, void *dtable, void *ws,
                        moe_stream_t stream);
 
+/*
+ * Gated products grouped by expert, ragged sizes: the first half of a gated
+ * feed-forward block in one kernel.  Rows r of expert e as for moe_grouped_*;
+ * w [E, 2m, K]: an expert's m rows of the gate, then its m of the up projection.
+ *   forward:   g = x[r] w[e][0:m]^T, u = x[r] w[e][m:2m]^T,  h[r] = act(g) u
+ *              x [rows, K] -> h [rows, m], and gu [rows, 2m] = [g | u] unless NULL
+ *   backward:  dg = dh u act'(g), du = dh act(g) from the forward's gu,
+ *              dx[r] = dg w[e][0:m] + du w[e][m:2m]           -> dx [rows, K]
+ *              dw[e] = sum_r [dg | du][r]^T x[r]               -> dw [E, 2m, K] contiguous
+ * act: SiLU g / (1 + e^-g), GELU g Phi(g), its form by tanh, or ReLU.  h comes from
+ * g and u before they are rounded; dg and du are rounded to dtype in front of
+ * their products.  Rows of no expert: h, gu and dx zeros, what x, dh and gu hold
+ * there is not used; an expert without rows gets dw[e] = 0; bad offsets, dtype,
+ * grad_dtype (dw's), accumulate and limits (1 <= m <= 2^19) as for moe_grouped_*.
+ * ld_x: row stride of x and dx; ld_h: of h and dh; ld_gu: of gu; ld_w, ld_e of w.
+ */
+typedef enum { MOE_ACT_SILU = 0, MOE_ACT_GELU = 1, MOE_ACT_GELU_TANH = 2, MOE_ACT_RELU = 3 } moe_act;
+typedef struct {
+  int64_t rows;
+  int32_t E, m, K;
+  int32_t dtype, grad_dtype; /* moe_elem */
+  int32_t act;               /* moe_act */
+  int32_t accumulate;
+  int64_t ld_x, ld_h, ld_gu, ld_w, ld_e; /* 0 = contiguous */
+} moe_gated_config;
+
+/* Bytes of scratch of one call in each direction (0 on an invalid config). */
+size_t moe_gated_forward_workspace_bytes(const moe_gated_config *cfg);
+size_t moe_gated_backward_workspace_bytes(const moe_gated_config *cfg);
+int moe_gated_forward(const moe_gated_config *cfg, const void *x, const void *w, const int32_t *offsets, void *h,
+                      void *gu, void *ws, moe_stream_t stream);
+/* dx or dw may be NULL (not both); x is not read without dw, w not without dx. */
+int moe_gated_backward(const moe_gated_config *cfg, const void *dh, const void *x, const void *w, const int32_t *offsets,
+                       const void *gu, void *dx, void *dw, void *ws, moe_stream_t stream);
+
+/*
+ * The loss over a vocabulary straight from the last hidden rows, in pieces of the
+ * vocabulary: the logits z = x w^T are never in memory.
+ *   forward:   lse[t] = log sum_v exp z[t, v],  loss[t] = lse[t] - z[t, labels[t]]   (fp32)
+ *   backward:  dz[t, v] = (dloss[t] + dlse[t]) exp(z[t, v] - lse[t]) - dloss[t] [v = labels[t]]
+ *              dx[t] = sum_v dz[t, v] w[v]      -> dx [rows, d] of dtype
+ *              dw[v] = sum_t dz[t, v] x[t]      -> dw [V, d] contiguous, of grad_dtype
+ * x [rows, d] and w [V, d] of dtype (BF16 or FP16), labels int32 or (labels64 = 1)
+ * int64 [rows].  A row whose label lies outside [0, V) (padding) does not count:
+ * loss, lse and dx are zero and what x holds there (NaN included) is not used.
+ * So it is in the backward for rows whose dloss and dlse are both zero.
+ * dloss or dlse [rows] fp32 may be NULL (zeros), lse is the forward's.  With
+ * dlse the loss may hold terms in lse (a penalty lse^2).
+ * accumulate = 1 adds to dw (FP32 only).  dz is formed in fp32 and rounded to
+ * dtype relative to the largest coefficient of all rows, in front of its two
+ * products.  Sums run in a fixed order (bitwise reproducible).
+ * The tensor cores read w through TMA: w and its rows must start on 16-byte
+ * boundaries (MOE_ERR_ALIGN otherwise), or copy_w = 1 takes a padded copy in the
+ * workspace.  ld_x, ld_w, ld_dx: row strides.
+ * Workspace (256-byte aligned): a copy of the rows that count; forward 16 bytes
+ * per row and 256 vocabulary entries; backward about 512 MB for a piece of dz
+ * (4096 entries for all rows at least) and the fp32 sums of dx.
+ * moe_get_status(ws) reports a wait that timed out.
+ * Limits: rows, V < 2^30, 1 <= d <= 2^20, 2^30 tiles of 256 x 256 (MOE_ERR_SHAPE).
+ */
+typedef struct {
+  int64_t rows, V;
+  int32_t d;
+  int32_t dtype, grad_dtype; /* moe_elem */
+  int32_t labels64, accumulate, copy_w;
+  int64_t ld_x, ld_w, ld_dx; /* 0 = d */
+} moe_vocab_config;
+
+/* Bytes of scratch of one call in each direction (0 on an invalid config). */
+size_t moe_vocab_forward_workspace_bytes(const moe_vocab_config *cfg);
+size_t moe_vocab_backward_workspace_bytes(const moe_vocab_config *cfg);
+int moe_vocab_forward(const moe_vocab_config *cfg, const void *x, const void *w, const void *labels, float *loss,
+                      float *lse, void *ws, moe_stream_t stream);
+/* dx or dw may be NULL (not both). */
+int moe_vocab_backward(const moe_vocab_config *cfg, const float *dloss, const float *dlse, const void *x, const void *w,
+                       const void *labels, const float *lse, void *dx, void *dw, void *ws, moe_stream_t stream);
+
+/*
+ * The global norm of many gradients, and their clipping:
+ *   norm = sqrt(sum of all elements' squares),  c = min(1, max_norm / (norm + eps))
+ *   outs[i] = c grads[i]
+ * The arrays are host arrays of n entries, read before the call returns: device
+ * addresses, element counts, types (moe_elem; outs' type is the tensor's or FP32).
+ * An out may be its own gradient (of one type: in place; nothing is written when c = 1);
+ * otherwise outs share memory neither with one another nor with a gradient
+ * (MOE_ERR_ARG).  The same gradient twice counts twice in moe_grad_norm.
+ * norm: one fp32 on the device.  Sums are held in 64 bits over short fp32 sums, in
+ * a fixed order; no squares overflow or vanish.  A norm that is not finite makes
+ * c zero (infinite norm) or NaN, as the formula says.
+ * max_norm >= 0 (infinite: no limit), eps > 0; n <= 2^24, counts <= 2^42.
+ */
+size_t moe_grad_workspace_bytes(int32_t n);
+int moe_grad_norm(const void *const *grads, const int64_t *counts, const int32_t *dtypes, int32_t n, float *norm,
+                  void *ws, moe_stream_t stream);
+int moe_grad_clip(const void *const *grads, void *const *outs, const int64_t *counts, const int32_t *dtypes,
+                  const int32_t *out_dtypes, int32_t n, double max_norm, double eps, float *norm, void *ws,
+                  moe_stream_t stream);
+
 /* Synchronises `stream`, returns the device status word recorded in `ws`
  * (MOE_OK, MOE_ERR_TIMEOUT, or MOE_ERR_BOUNDS -- from the layer only in a debug
  * build; a timeout is reported first when both happened) and clears it.  Returns MOE_ERR_CUDA if

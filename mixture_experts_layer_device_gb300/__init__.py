@@ -30,6 +30,9 @@ MOE_NORM_POST, MOE_NORM_PRE = 1, 2
 MOE_GATE_NONE, MOE_GATE_CHANNEL, MOE_GATE_ROW, MOE_GATE_FULL = 0, 1, 2, 3
 GATES = {"none": MOE_GATE_NONE, "channel": MOE_GATE_CHANNEL, "row": MOE_GATE_ROW, "full": MOE_GATE_FULL}
 
+MOE_ACT_SILU, MOE_ACT_GELU, MOE_ACT_GELU_TANH, MOE_ACT_RELU = 0, 1, 2, 3
+ACTS = {"silu": MOE_ACT_SILU, "gelu": MOE_ACT_GELU, "gelu_tanh": MOE_ACT_GELU_TANH, "relu": MOE_ACT_RELU}
+
 WEIGHT_FIELDS = ["gu", "gu_scale", "dn", "dn_scale", "gu_t", "gu_t_scale", "dn_t", "dn_t_scale",
                  "s_gu", "s_dn", "s_gu_t", "s_dn_t", "gu_gscale", "dn_gscale"]
 
@@ -61,6 +64,18 @@ class MoeEmbedConfig(ctypes.Structure):
                [("scale", ctypes.c_float), ("ld_t", ctypes.c_int64), ("ld_o", ctypes.c_int64)]
 
 
+class MoeGatedConfig(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in ("E", "m", "K", "dtype", "grad_dtype", "act",
+                                                                          "accumulate")] + \
+               [(n, ctypes.c_int64) for n in ("ld_x", "ld_h", "ld_gu", "ld_w", "ld_e")]
+
+
+class MoeVocabConfig(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("V", ctypes.c_int64)] + \
+               [(n, ctypes.c_int32) for n in ("d", "dtype", "grad_dtype", "labels64", "accumulate", "copy_w")] + \
+               [(n, ctypes.c_int64) for n in ("ld_x", "ld_w", "ld_dx")]
+
+
 _lib = None
 EXPORTS = ["moe_workspace_bytes", "moe_saved_bytes", "moe_buffer_info", "moe_padded_rows",
            "moe_quantize_weights", "moe_quantize_mx", "moe_quantize_mx_both", "moe_prepare_weights",
@@ -71,7 +86,10 @@ EXPORTS = ["moe_workspace_bytes", "moe_saved_bytes", "moe_buffer_info", "moe_pad
            "moe_trace_name", "moe_trace_ms", "moe_route_noalloc", "moe_router_forward", "moe_router_backward",
            "moe_grouped_workspace_bytes", "moe_grouped_forward", "moe_grouped_backward", "moe_norm_forward",
            "moe_norm_workspace_bytes", "moe_norm_backward", "moe_embed_forward", "moe_embed_workspace_bytes",
-           "moe_embed_backward"]
+           "moe_embed_backward", "moe_gated_forward_workspace_bytes", "moe_gated_backward_workspace_bytes",
+           "moe_gated_forward", "moe_gated_backward", "moe_vocab_forward_workspace_bytes",
+           "moe_vocab_backward_workspace_bytes", "moe_vocab_forward", "moe_vocab_backward", "moe_grad_workspace_bytes",
+           "moe_grad_norm", "moe_grad_clip"]
 
 
 def lib():
@@ -121,6 +139,17 @@ def lib():
                           (L.moe_norm_backward, npp, 15), (L.moe_embed_forward, ep, 3),
                           (L.moe_embed_backward, ep, 4)):
             fn.argtypes, fn.restype = [cp] + [P] * n + [S], I
+        gap, vp = ctypes.POINTER(MoeGatedConfig), ctypes.POINTER(MoeVocabConfig)
+        for fn, cp in ((L.moe_gated_forward_workspace_bytes, gap), (L.moe_gated_backward_workspace_bytes, gap),
+                       (L.moe_vocab_forward_workspace_bytes, vp), (L.moe_vocab_backward_workspace_bytes, vp)):
+            fn.argtypes, fn.restype = [cp], Z
+        for fn, cp, n in ((L.moe_gated_forward, gap, 6), (L.moe_gated_backward, gap, 8), (L.moe_vocab_forward, vp, 6),
+                          (L.moe_vocab_backward, vp, 9)):
+            fn.argtypes, fn.restype = [cp] + [P] * n + [S], I
+        n32, f64 = ctypes.c_int32, ctypes.c_double
+        L.moe_grad_workspace_bytes.argtypes, L.moe_grad_workspace_bytes.restype = [n32], Z
+        L.moe_grad_norm.argtypes, L.moe_grad_norm.restype = [P, P, P, n32, P, P, S], I
+        L.moe_grad_clip.argtypes, L.moe_grad_clip.restype = [P, P, P, P, P, n32, f64, f64, P, P, S], I
         _lib = L
     return _lib
 
@@ -293,6 +322,56 @@ def moe_embed_workspace_bytes(cfg):
 def moe_embed_backward(cfg, ids, dout, dtable, ws, stream=None):
     return lib().moe_embed_backward(ctypes.byref(cfg), _ptr(ids), _ptr(dout), _ptr(dtable), _ptr(ws),
                                     _stream(stream))
+
+
+def moe_gated_forward_workspace_bytes(cfg):
+    return lib().moe_gated_forward_workspace_bytes(ctypes.byref(cfg))
+
+
+def moe_gated_backward_workspace_bytes(cfg):
+    return lib().moe_gated_backward_workspace_bytes(ctypes.byref(cfg))
+
+
+def moe_gated_forward(cfg, x, w, offsets, h, gu, ws, stream=None):
+    return lib().moe_gated_forward(ctypes.byref(cfg), _ptr(x), _ptr(w), _ptr(offsets), _ptr(h), _ptr(gu), _ptr(ws),
+                                   _stream(stream))
+
+
+def moe_gated_backward(cfg, dh, x, w, offsets, gu, dx, dw, ws, stream=None):
+    return lib().moe_gated_backward(ctypes.byref(cfg), _ptr(dh), _ptr(x), _ptr(w), _ptr(offsets), _ptr(gu), _ptr(dx),
+                                    _ptr(dw), _ptr(ws), _stream(stream))
+
+
+def moe_vocab_forward_workspace_bytes(cfg):
+    return lib().moe_vocab_forward_workspace_bytes(ctypes.byref(cfg))
+
+
+def moe_vocab_backward_workspace_bytes(cfg):
+    return lib().moe_vocab_backward_workspace_bytes(ctypes.byref(cfg))
+
+
+def moe_vocab_forward(cfg, x, w, labels, loss, lse, ws, stream=None):
+    return lib().moe_vocab_forward(ctypes.byref(cfg), _ptr(x), _ptr(w), _ptr(labels), _ptr(loss), _ptr(lse), _ptr(ws),
+                                   _stream(stream))
+
+
+def moe_vocab_backward(cfg, dloss, dlse, x, w, labels, lse, dx, dw, ws, stream=None):
+    return lib().moe_vocab_backward(ctypes.byref(cfg), _ptr(dloss), _ptr(dlse), _ptr(x), _ptr(w), _ptr(labels),
+                                    _ptr(lse), _ptr(dx), _ptr(dw), _ptr(ws), _stream(stream))
+
+
+def moe_grad_workspace_bytes(n):
+    return lib().moe_grad_workspace_bytes(n)
+
+
+def moe_grad_norm(grads, counts, dtypes, n, norm, ws, stream=None):
+    """grads, counts, dtypes: addresses of host arrays of n entries."""
+    return lib().moe_grad_norm(grads, counts, dtypes, n, _ptr(norm), _ptr(ws), _stream(stream))
+
+
+def moe_grad_clip(grads, outs, counts, dtypes, out_dtypes, n, max_norm, eps, norm, ws, stream=None):
+    return lib().moe_grad_clip(grads, outs, counts, dtypes, out_dtypes, n, max_norm, eps, _ptr(norm), _ptr(ws),
+                               _stream(stream))
 
 
 def moe_get_status(ws, stream=None):

@@ -1,7 +1,9 @@
 """What a model needs around the MoE layer, on torch tensors: ragged matrix
-products grouped by expert, the norms around a block with its gate and
-residual scale, and the token embedding with its gradient (include/moe.h:
-moe_grouped_*, moe_norm_*, moe_embed_*).
+products grouped by expert, plain and gated, the norms around a block with its
+gate and residual scale, the token embedding with its gradient, the loss over
+the vocabulary with its gradients, and the norm and clipping of all gradients
+(include/moe.h: moe_grouped_*, moe_gated_*, moe_norm_*, moe_embed_*,
+moe_vocab_*, moe_grad_*).
 
 Plain functions: they check their arguments, allocate outputs and workspaces
 from torch and call the library; all arithmetic runs in its kernels.  They run
@@ -11,12 +13,13 @@ ready on it, and what they return is.  All tensors of a call are on the current
 GPU.  The autograd functions and modules over them are in module.py.
 """
 import ctypes
+from array import array
 from functools import lru_cache
 
 import torch
 
-from . import (GATES, MOE_ELEM_BF16, MOE_ELEM_FP16, MOE_ELEM_FP32, MOE_NORM_POST, MOE_NORM_PRE, MoeEmbedConfig,
-               MoeGroupedConfig, MoeNormConfig, _stream, check, lib, moe_get_status)
+from . import (ACTS, GATES, MOE_ELEM_BF16, MOE_ELEM_FP16, MOE_ELEM_FP32, MOE_NORM_POST, MOE_NORM_PRE, MoeEmbedConfig,
+               MoeGatedConfig, MoeGroupedConfig, MoeNormConfig, MoeVocabConfig, _stream, check, lib, moe_get_status)
 
 _ELEM = {torch.bfloat16: MOE_ELEM_BF16, torch.float16: MOE_ELEM_FP16, torch.float32: MOE_ELEM_FP32}
 
@@ -105,9 +108,10 @@ def _on(stream, call, *args, **kw):
     caller = torch.cuda.current_stream()
     with torch.cuda.stream(stream):
         out = call(*args, **kw)
-    for t in (*args, *kw.values()):
-        if isinstance(t, torch.Tensor):
-            t.record_stream(stream)
+    for a in (*args, *kw.values()):
+        for t in a if isinstance(a, (list, tuple)) else (a,):
+            if isinstance(t, torch.Tensor):
+                t.record_stream(stream)
     for t in out if isinstance(out, tuple) else (out,):
         if t is not None:
             t.record_stream(caller)
@@ -160,6 +164,36 @@ def grouped_forward(x, w, offsets, *, out=None, out_dtype=None, return_workspace
     return (y, ws) if return_workspace else y
 
 
+def _product_grads(x, ld_x, rows, E, N, K, dtype, gpu, dx, dw, need_dx, need_dw, dw_dtype, accumulate, name):
+    """(x, its row stride, dx, dw) of a backward: the outputs checked or allocated, None
+    where not needed, x copied where dx cannot share its stride."""
+    dw_dtype = dw_dtype or (dw.dtype if dw is not None else dtype)
+    if not (dw_dtype in (dtype, torch.float32)):
+        _bad("dw is of %s's type or float32", name)
+    if not (not accumulate or (dw is not None and dw_dtype == torch.float32)):
+        _bad("accumulate adds to a given float32 dw")
+    if not (need_dx or need_dw):
+        _bad("nothing to compute")
+    if need_dx:
+        if dx is None:
+            x, ld_x = _narrow(x, ld_x)
+            dx = torch.empty((rows, ld_x), dtype=dtype, device=x.device)
+            dx = dx if ld_x == K else dx[:, :K]
+        if not (dx.shape == (rows, K) and dx.dtype == dtype and dx.get_device() == gpu and
+                (K == 1 or dx.stride(1) == 1)):
+            _bad("dx must be a %s matrix [%d, %d] with contiguous rows on GPU %d", dtype, rows, K, gpu)
+        if rows > 1 and dx.stride(0) != ld_x:
+            x, ld_x = x.contiguous(), K
+            if not (dx.stride(0) == K):
+                _bad("dx must have x's row stride or be contiguous")
+    if need_dw:
+        if dw is None:
+            dw = torch.empty((E, N, K), dtype=dw_dtype, device=x.device)
+        if not (dw.shape == (E, N, K) and dw.dtype == dw_dtype and dw.get_device() == gpu and dw.is_contiguous()):
+            _bad("dw must be a contiguous %s tensor [%d, %d, %d] on GPU %d", dw_dtype, E, N, K, gpu)
+    return x, ld_x, dx if need_dx else None, dw if need_dw else None
+
+
 def grouped_backward(dy, x, w, offsets, *, dx=None, dw=None, need_dx=True, need_dw=True, dw_dtype=None,
                      accumulate=False, return_workspace=False, stream=None):
     """(dx [rows, K], dw [E, N, K]) of grouped_forward: dx[r] = dy[r] w[e], dw[e] =
@@ -173,37 +207,15 @@ def grouped_backward(dy, x, w, offsets, *, dx=None, dw=None, need_dx=True, need_
     rows = dy.shape[0]
     dy, ld_y = _rows(dy, "dy", N, gpu)
     x, ld_x = _rows(x, "x", K, gpu, dy.dtype, rows)
-    dw_dtype = dw_dtype or (dw.dtype if dw is not None else dy.dtype)
-    if not (dw_dtype in (dy.dtype, torch.float32)):
-        _bad("dw is of dy's type or float32")
-    if not (not accumulate or (dw is not None and dw_dtype == torch.float32)):
-        _bad("accumulate adds to a given float32 dw")
-    if not (need_dx or need_dw):
-        _bad("nothing to compute")
-    if need_dx:
-        if dx is None:
-            x, ld_x = _narrow(x, ld_x)
-            dx = torch.empty((rows, ld_x), dtype=dy.dtype, device=dy.device)
-            dx = dx if ld_x == K else dx[:, :K]
-        if not (dx.shape == (rows, K) and dx.dtype == dy.dtype and dx.get_device() == gpu and
-                (K == 1 or dx.stride(1) == 1)):
-            _bad("dx must be a %s matrix [%d, %d] with contiguous rows on GPU %d", dy.dtype, rows, K, gpu)
-        if rows > 1 and dx.stride(0) != ld_x:
-            x, ld_x = x.contiguous(), K
-            if not (dx.stride(0) == K):
-                _bad("dx must have x's row stride or be contiguous")
-    if need_dw:
-        if dw is None:
-            dw = torch.empty((E, N, K), dtype=dw_dtype, device=dy.device)
-        if not (dw.shape == (E, N, K) and dw.dtype == dw_dtype and dw.get_device() == gpu and dw.is_contiguous()):
-            _bad("dw must be a contiguous %s tensor [%d, %d, %d] on GPU %d", dw_dtype, E, N, K, gpu)
+    x, ld_x, dx, dw = _product_grads(x, ld_x, rows, E, N, K, dy.dtype, gpu, dx, dw, need_dx, need_dw, dw_dtype, accumulate,
+                                     "dy")
     ld_e = w.stride(0) if E > 1 else 0
-    plan = _grouped_plan(rows, E, N, K, _ELEM[dy.dtype], _ELEM[dw_dtype], int(accumulate), ld_x, ld_y, ld_w, ld_e)
+    plan = _grouped_plan(rows, E, N, K, _ELEM[dy.dtype], _ELEM[dw.dtype if need_dw else dy.dtype], int(accumulate), ld_x,
+                         ld_y, ld_w, ld_e)
     ws = _ws(plan, dy.device)
-    out = (dx if need_dx else None, dw if need_dw else None)
-    check(lib().moe_grouped_backward(plan[1], dy.data_ptr(), x.data_ptr(), w.data_ptr(), offsets.data_ptr(),
-                                     _ptr(out[0]), _ptr(out[1]), ws.data_ptr(), _stream(None)))
-    return out + (ws,) if return_workspace else out
+    check(lib().moe_grouped_backward(plan[1], dy.data_ptr(), x.data_ptr(), w.data_ptr(), offsets.data_ptr(), _ptr(dx),
+                                     _ptr(dw), ws.data_ptr(), _stream(None)))
+    return (dx, dw, ws) if return_workspace else (dx, dw)
 
 
 def grouped_status(ws, stream=None):
@@ -211,6 +223,71 @@ def grouped_status(ws, stream=None):
     device status of the call that used workspace `ws` (return_workspace=True): 0, or
     -7 when its offsets descend or leave the rows."""
     return moe_get_status(ws, stream)
+
+
+# ---------------------------------------------------------------- gated products
+@lru_cache(maxsize=512)
+def _gated_plan(backward, *fields):
+    return _plan(MoeGatedConfig(*fields), lib().moe_gated_backward_workspace_bytes if backward
+                 else lib().moe_gated_forward_workspace_bytes)
+
+
+def _gated(x, w, offsets, act, name):
+    gpu, w, offsets, E, N, K, ld_w = _grouped(x, w, offsets, name)
+    if N % 2:
+        _bad("w has %d rows per expert, expected the gate's and as many of the up projection", N)
+    if not (act in ACTS):
+        _bad("act is one of %s", sorted(ACTS))
+    return gpu, w, offsets, E, N // 2, K, ld_w
+
+
+def gated_forward(x, w, offsets, *, act="silu", need_gu=True, out=None, gu=None, return_workspace=False, stream=None):
+    """(h [rows, m], gu [rows, 2m]): g = x[r] w[e][:m]^T, u = x[r] w[e][m:]^T, h = act(g) u
+    for the rows offsets[e] <= r < offsets[e + 1] of expert e (0 for a row of no
+    expert).  x [rows, K] and w [E, 2m, K] bf16 or fp16, offsets int32 [E + 1] as for
+    grouped_forward; gu = [g, u] is what a backward needs (None without need_gu).
+    act: "silu", "gelu", "gelu_tanh" or "relu"."""
+    if stream is not None:
+        return _on(stream, gated_forward, x, w, offsets, act=act, need_gu=need_gu, out=out, gu=gu,
+                   return_workspace=return_workspace)
+    gpu, w, offsets, E, m, K, ld_w = _gated(x, w, offsets, act, "x")
+    x, ld_x = _rows(x, "x", K, gpu)
+    rows, dt = x.shape[0], x.dtype
+    h, ld_h = _out(out, "out", rows, m, dt, x.device, gpu)
+    ld_gu = 2 * m
+    if need_gu:
+        gu, ld_gu = _out(gu, "gu", rows, 2 * m, dt, x.device, gpu)
+    elif gu is not None:
+        _bad("gu is given but not needed")
+    el = _ELEM[dt]
+    plan = _gated_plan(False, rows, E, m, K, el, el, ACTS[act], 0, ld_x, ld_h, ld_gu, ld_w, w.stride(0) if E > 1 else 0)
+    ws = _ws(plan, x.device)
+    check(lib().moe_gated_forward(plan[1], x.data_ptr(), w.data_ptr(), offsets.data_ptr(), h.data_ptr(), _ptr(gu),
+                                  ws.data_ptr(), _stream(None)))
+    return (h, gu, ws) if return_workspace else (h, gu)
+
+
+def gated_backward(dh, x, w, offsets, gu, *, act="silu", dx=None, dw=None, need_dx=True, need_dw=True, dw_dtype=None,
+                   accumulate=False, return_workspace=False, stream=None):
+    """(dx [rows, K], dw [E, 2m, K]) of gated_forward from its gu, either None when not
+    needed.  dw is of x's type or fp32 (dw_dtype, or dw's); with accumulate it must
+    be given, fp32, and is added to."""
+    if stream is not None:
+        return _on(stream, gated_backward, dh, x, w, offsets, gu, act=act, dx=dx, dw=dw, need_dx=need_dx, need_dw=need_dw,
+                   dw_dtype=dw_dtype, accumulate=accumulate, return_workspace=return_workspace)
+    gpu, w, offsets, E, m, K, ld_w = _gated(dh, w, offsets, act, "dh")
+    rows, dt = dh.shape[0], dh.dtype
+    dh, ld_h = _rows(dh, "dh", m, gpu)
+    x, ld_x = _rows(x, "x", K, gpu, dt, rows)
+    gu, ld_gu = _rows(gu, "gu", 2 * m, gpu, dt, rows)
+    x, ld_x, dx, dw = _product_grads(x, ld_x, rows, E, 2 * m, K, dt, gpu, dx, dw, need_dx, need_dw, dw_dtype, accumulate,
+                                     "dh")
+    plan = _gated_plan(True, rows, E, m, K, _ELEM[dt], _ELEM[dw.dtype if need_dw else dt], ACTS[act], int(accumulate),
+                       ld_x, ld_h, ld_gu, ld_w, w.stride(0) if E > 1 else 0)
+    ws = _ws(plan, dh.device)
+    check(lib().moe_gated_backward(plan[1], dh.data_ptr(), x.data_ptr(), w.data_ptr(), offsets.data_ptr(), gu.data_ptr(),
+                                   _ptr(dx), _ptr(dw), ws.data_ptr(), _stream(None)))
+    return (dx, dw, ws) if return_workspace else (dx, dw)
 
 
 # ---------------------------------------------------------------- block norms
@@ -341,9 +418,9 @@ def _embed_plan(*fields):
     return _plan(MoeEmbedConfig(*fields), lib().moe_embed_workspace_bytes)
 
 
-def _ids(ids, gpu):
+def _ids(ids, gpu, name="ids"):
     if not (ids.dtype in (torch.int32, torch.int64) and ids.get_device() == gpu):
-        _bad("ids must be int32 or int64 on GPU %d", gpu)
+        _bad("%s must be int32 or int64 on GPU %d", name, gpu)
     return ids if ids.dim() == 1 and ids.is_contiguous() else ids.reshape(-1).contiguous()
 
 
@@ -394,3 +471,175 @@ def embed_backward(ids, dout, V, *, scale=1.0, dtable=None, grad_dtype=None, acc
     check(lib().moe_embed_backward(plan[1], flat.data_ptr(), dout.data_ptr(), dtable.data_ptr(), ws.data_ptr(),
                                    _stream(None)))
     return dtable
+
+
+# ---------------------------------------------------------------- loss over a vocabulary
+@lru_cache(maxsize=512)
+def _vocab_plan(backward, *fields):
+    return _plan(MoeVocabConfig(*fields), lib().moe_vocab_backward_workspace_bytes if backward
+                 else lib().moe_vocab_forward_workspace_bytes)
+
+
+def _vocab(x, w, labels):
+    if not (x.dim() == 2 and x.dtype in (torch.bfloat16, torch.float16)):
+        _bad("x must be a bf16 or fp16 matrix [rows, d]")
+    gpu, (rows, d) = _gpu(x, "x"), x.shape
+    if w.dim() != 2:
+        _bad("w must be a matrix [V, %d]", d)
+    x, ld_x = _rows(x, "x", d, gpu)
+    w, ld_w = _rows(w, "w", d, gpu, x.dtype)
+    flat = _ids(labels, gpu, "labels")
+    if flat.shape[0] != rows:
+        _bad("labels has %d entries, expected %d", flat.shape[0], rows)
+    # TMA takes rows that start on 16-byte boundaries: others are copied in the call
+    copy_w = int(ld_w % 8 != 0 or w.data_ptr() % 16 != 0)
+    return gpu, x, ld_x, w, ld_w, flat, rows, w.shape[0], d, copy_w
+
+
+def _per_row(t, name, rows, gpu, device):
+    if t is None:
+        return torch.empty(rows, dtype=torch.float32, device=device)
+    if not (t.shape == (rows,) and t.dtype == torch.float32 and t.get_device() == gpu and t.is_contiguous()):
+        _bad("%s must be a contiguous float32 vector of %d on GPU %d", name, rows, gpu)
+    return t
+
+
+def vocab_loss_forward(x, w, labels, *, loss=None, lse=None, return_workspace=False, stream=None):
+    """(loss [rows], lse [rows]) fp32 of the logits z = x w^T, which are never in memory:
+    lse[t] = log sum_v exp z[t, v], loss[t] = lse[t] - z[t, labels[t]].  x [rows, d]
+    and w [V, d] bf16 or fp16, labels int32 or int64 of rows entries; a row whose
+    label lies outside [0, V) (padding) does not count: both are zero, whatever x
+    holds there."""
+    if stream is not None:
+        return _on(stream, vocab_loss_forward, x, w, labels, loss=loss, lse=lse, return_workspace=return_workspace)
+    gpu, x, ld_x, w, ld_w, flat, rows, V, d, copy_w = _vocab(x, w, labels)
+    loss, lse = _per_row(loss, "loss", rows, gpu, x.device), _per_row(lse, "lse", rows, gpu, x.device)
+    el = _ELEM[x.dtype]
+    plan = _vocab_plan(False, rows, V, d, el, el, int(flat.dtype == torch.int64), 0, copy_w, ld_x, ld_w, 0)
+    ws = _ws(plan, x.device)
+    check(lib().moe_vocab_forward(plan[1], x.data_ptr(), w.data_ptr(), flat.data_ptr(), loss.data_ptr(), lse.data_ptr(),
+                                  ws.data_ptr(), _stream(None)))
+    return (loss, lse, ws) if return_workspace else (loss, lse)
+
+
+def vocab_loss_backward(dloss, x, w, labels, lse, *, dlse=None, dx=None, dw=None, need_dx=True, need_dw=True,
+                        dw_dtype=None, accumulate=False, return_workspace=False, stream=None):
+    """(dx [rows, d], dw [V, d]) of vocab_loss_forward from the gradients dloss and dlse
+    [rows] fp32 of its two results (either may be None) and its lse; either output is
+    None when not needed.  A row that does not count, or whose gradients are both zero,
+    gets dx = 0 and adds nothing to dw.  dw is of x's type or fp32 (dw_dtype, or dw's);
+    with accumulate it must be given, fp32, and is added to."""
+    if stream is not None:
+        return _on(stream, vocab_loss_backward, dloss, x, w, labels, lse, dlse=dlse, dx=dx, dw=dw, need_dx=need_dx,
+                   need_dw=need_dw, dw_dtype=dw_dtype, accumulate=accumulate, return_workspace=return_workspace)
+    gpu, x, ld_x, w, ld_w, flat, rows, V, d, copy_w = _vocab(x, w, labels)
+    if dloss is None and dlse is None:
+        _bad("the gradient arrives in dloss, dlse or both")
+    dloss, dlse = _vector(dloss, "dloss", rows, torch.float32, gpu), _vector(dlse, "dlse", rows, torch.float32, gpu)
+    lse = _vector(lse, "lse", rows, torch.float32, gpu)
+    if lse is None:
+        _bad("the backward needs the forward's lse")
+    dw_dtype = dw_dtype or (dw.dtype if dw is not None else x.dtype)
+    if not (dw_dtype in (x.dtype, torch.float32)):
+        _bad("dw is of x's type or float32")
+    if not (not accumulate or (dw is not None and dw_dtype == torch.float32)):
+        _bad("accumulate adds to a given float32 dw")
+    if not (need_dx or need_dw):
+        _bad("nothing to compute")
+    ld_dx = 0
+    if need_dx:
+        dx, ld_dx = _out(dx, "dx", rows, d, x.dtype, x.device, gpu)
+    if need_dw:
+        if dw is None:
+            dw = torch.empty((V, d), dtype=dw_dtype, device=x.device)
+        if not (dw.shape == (V, d) and dw.dtype == dw_dtype and dw.get_device() == gpu and dw.is_contiguous()):
+            _bad("dw must be a contiguous %s matrix [%d, %d] on GPU %d", dw_dtype, V, d, gpu)
+    plan = _vocab_plan(True, rows, V, d, _ELEM[x.dtype], _ELEM[dw_dtype], int(flat.dtype == torch.int64), int(accumulate),
+                       copy_w, ld_x, ld_w, ld_dx)
+    ws = _ws(plan, x.device)
+    dx, dw = dx if need_dx else None, dw if need_dw else None
+    check(lib().moe_vocab_backward(plan[1], _ptr(dloss), _ptr(dlse), x.data_ptr(), w.data_ptr(), flat.data_ptr(),
+                                   lse.data_ptr(), _ptr(dx), _ptr(dw), ws.data_ptr(), _stream(None)))
+    return (dx, dw, ws) if return_workspace else (dx, dw)
+
+
+# ---------------------------------------------------------------- all gradients
+def _dense(t):
+    """Whether t's elements fill its memory, in whatever order of dimensions."""
+    if t.is_contiguous():
+        return True
+    order = sorted(range(t.dim()), key=lambda i: (t.stride(i), t.shape[i]), reverse=True)
+    return t.permute(order).is_contiguous()
+
+
+def _tensors(ts, gpu, name):
+    """(types, counts, addresses) of dense tensors on the current GPU, as host arrays."""
+    for t in ts:
+        if t.get_device() != gpu:
+            _bad("one of %s is on %s, not on the current GPU", name, t.device)
+        if not (t.is_contiguous() or _dense(t)):
+            _bad("one of %s (shape %s, strides %s) does not fill its memory", name, tuple(t.shape), t.stride())
+    try:
+        types = array("i", [_ELEM[t.dtype] for t in ts])
+    except KeyError:
+        _bad("%s are bf16, fp16 or fp32", name)
+    return types, array("q", [t.numel() for t in ts]), array("Q", [t.data_ptr() for t in ts])
+
+
+def _host(a):
+    return a.buffer_info()[0] if len(a) else None
+
+
+def _norm_out(norm, gpu):
+    if norm is None:
+        return torch.empty((), dtype=torch.float32, device=torch.device("cuda", gpu))
+    if not (norm.numel() == 1 and norm.dtype == torch.float32 and norm.get_device() == gpu):
+        _bad("norm must be one float32 on GPU %d", gpu)
+    return norm
+
+
+def grad_norm(grads, *, norm=None, stream=None):
+    """The 2-norm of all elements of the tensors in the list `grads` (bf16, fp16 or fp32,
+    any mix; each fills its memory): a 0-d fp32 tensor, zero for no tensors."""
+    if stream is not None:
+        return _on(stream, grad_norm, list(grads), norm=norm)
+    grads, gpu = list(grads), _current_gpu()
+    types, counts, at = _tensors(grads, gpu, "grads")
+    norm = _norm_out(norm, gpu)
+    ws = torch.empty(lib().moe_grad_workspace_bytes(len(grads)), dtype=torch.uint8, device=norm.device)
+    check(lib().moe_grad_norm(_host(at), _host(counts), _host(types), len(grads), norm.data_ptr(), ws.data_ptr(),
+                              _stream(None)))
+    return norm
+
+
+def grad_clip(grads, max_norm, *, out=None, eps=1e-6, norm=None, stream=None):
+    """Scales all tensors of the list `grads` by min(1, max_norm / (norm + eps)), in place
+    or into the list `out` of tensors of the same shapes and layouts (each of its
+    gradient's type or fp32, as an optimizer's masters take them); the norm of before
+    comes back as a 0-d fp32 tensor.  No output shares memory with another tensor of the
+    call (the same gradient twice, a view of another): refused."""
+    if stream is not None:
+        return _on(stream, grad_clip, list(grads), max_norm, out=None if out is None else list(out), eps=eps, norm=norm)
+    grads, gpu = list(grads), _current_gpu()
+    types, counts, at = _tensors(grads, gpu, "grads")
+    out_types, out_at = types, at
+    if out is not None:
+        out = list(out)
+        if len(out) != len(grads):
+            _bad("out has %d tensors, expected %d", len(out), len(grads))
+        out_types, _, out_at = _tensors(out, gpu, "out")
+        for g, o in zip(grads, out):
+            if o.shape != g.shape or o.dtype not in (g.dtype, torch.float32) or \
+                    not (g.stride() == o.stride() or (g.is_contiguous() and o.is_contiguous())):
+                _bad("out's tensors have their gradients' shapes and layouts, and their types or float32")
+    max_norm, eps = float(max_norm), float(eps)
+    if not (max_norm >= 0.0 and 0.0 < eps < float("inf")):
+        _bad("max_norm must not be negative, eps must be positive")
+    norm = _norm_out(norm, gpu)
+    ws = torch.empty(lib().moe_grad_workspace_bytes(len(grads)), dtype=torch.uint8, device=norm.device)
+    rc = lib().moe_grad_clip(_host(at), _host(out_at), _host(counts), _host(types), _host(out_types), len(grads), max_norm,
+                             eps, norm.data_ptr(), ws.data_ptr(), _stream(None))
+    if rc == -1:    # of the library's checks the only one that is not made above
+        _bad("tensors of the call overlap: no output shares memory with another tensor")
+    check(rc)
+    return norm

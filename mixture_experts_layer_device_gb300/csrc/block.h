@@ -48,7 +48,7 @@ cudaError_t launch_early(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream
 // b[n, k], with the expert's rows on m (forward, dgrad) or on k (wgrad).  The plain kernel
 // addresses both operands by two strides; the tensor-core kernel has the tokens on its
 // instruction's N side and reads each operand in the major in which it lies.
-enum GroupedDir { GROUPED_FWD = 0, GROUPED_DGRAD = 1, GROUPED_WGRAD = 2 };
+enum GroupedDir { GROUPED_FWD = 0, GROUPED_DGRAD = 1, GROUPED_WGRAD = 2, GROUPED_GATED = 3 };
 
 struct GroupedArgs {
   int E, N, K;
@@ -60,6 +60,11 @@ struct GroupedArgs {
   const int *offsets;  // [E + 1]
   const void *x, *w, *dy;
   void *y, *dx, *dw;
+  // gated forward: N = 2 m rows of w, the gate's and the up projection's; y (may be NULL) keeps both
+  // products, h [rows, m] = act(gate) up
+  void *h;
+  long ld_h;
+  int act;  // moe_act
   bool zeroed;   // weight gradient: launch_grouped_zero writes the experts without rows
   bool chained;  // tensor-core path: starts before the launch in front has ended (dgrad and wgrad of one call)
   bool vec_out;  // tensor-core path: the output's rows are whole 16-byte pieces
@@ -78,6 +83,8 @@ cudaError_t launch_grouped_plan(const GroupedArgs &g, int tile_rows, void *out, 
                                 long ld_out, cudaStream_t s);
 // Any size, stride and alignment; `first`: with the plan in front.
 cudaError_t launch_grouped_plain(const GroupedArgs &g, int dir, bool first, cudaStream_t s);
+// The gated forward for any size, stride and alignment, with its plans in front.
+cudaError_t launch_gated_plain(const GroupedArgs &g, cudaStream_t s);
 // Forward of a few rows (no plan needed): 16-byte aligned rows of x and w.
 cudaError_t launch_grouped_few(const GroupedArgs &g, cudaStream_t s);
 // Puts the experts in order (g.order) for launch_grouped_zero; the tensor-core
@@ -95,6 +102,15 @@ cudaError_t launch_grouped_pad(const GroupedArgs &g, const void *src, long rows,
 cudaError_t launch_grouped_tc(const GroupedArgs &g, int dir, int num_sms, cudaStream_t s);
 // Both products of a backward on it.
 cudaError_t launch_grouped_tc_pair(GroupedArgs dgrad, GroupedArgs wgrad, int num_sms, cudaStream_t s);
+
+// The gated products' backward in front of its two products: [dg | du] from dh and [g | u].
+struct GatedArgs {
+  int rows, m, dtype, act;
+  long ld_h, ld_gu, ld_dgu;
+  const void *dh, *gu;
+  void *dgu;
+};
+cudaError_t launch_gated_slope(const GatedArgs &a, int num_sms, cudaStream_t s);
 
 // ---------------------------------------------------------------- block norms
 struct NormArgs {
@@ -134,5 +150,55 @@ struct EmbedArgs {
 size_t embed_workspace(int rows, long V, int d);
 cudaError_t launch_embed_forward(const EmbedArgs &a, cudaStream_t s);
 cudaError_t launch_embed_backward(const EmbedArgs &a, int num_sms, cudaStream_t s);
+
+// ---------------------------------------------------------------- loss over a vocabulary
+// The rows that count (a label inside the vocabulary; backward: a gradient too)
+// stand first in a padded copy of x; everything after that works on the copy.
+// `pad` is rows rounded up to 256; width a multiple of 256.
+struct VocabArgs {
+  int rows, V, d, dtype, grad_dtype, labels64, accumulate;
+  long ld_x, ld_w, ld_dx;
+  const void *x, *w, *labels;
+  const float *dloss, *dlse, *lse_in;
+  float *loss, *lse;
+  void *dx, *dw;
+  // workspace
+  int *status, *count;   // rows that count
+  float *scale;          // what the backward's products are multiplied by in the end
+  int *row, *place;      // [pad] row of a place, [rows] place of a row (-1: none)
+  int *label;            // [pad]
+  float *hit;            // forward: [pad] the label's logit
+  float2 *part;          // forward: [pad][parts] (maximum, sum of exponentials) of 128 logits
+  int parts;
+  float *coef_p, *coef_l, *base;  // backward: [pad] dz = coef_p 2^(z log2 e - base) - coef_l [label]
+  void *xs;              // [rows][ld_xs] the copy of x
+  void *ws_w;            // the padded copy of w where TMA cannot address it (else unused)
+  void *dz;              // backward: [rows][width] one piece of the logits' gradient
+  float *sum;            // backward: [splits][rows][ld_sum] sums of dx
+  long ld_xs, ld_ws_w, ld_sum;
+  int width, splits;
+  bool pad_w, vec_dw;
+  // the piece at hand
+  int v0, wp;
+};
+cudaError_t launch_vocab_forward(const VocabArgs &a, int num_sms, cudaStream_t s);
+cudaError_t launch_vocab_backward(const VocabArgs &a, int num_sms, cudaStream_t s);
+// The tensor-core products (vocab_tc.cu).
+enum VocabMode { VOCAB_LOSS = 0, VOCAB_DZ = 1, VOCAB_DX = 2, VOCAB_DW = 3 };
+cudaError_t launch_vocab_tc(const VocabArgs &a, int mode, cudaStream_t s);
+
+// ---------------------------------------------------------------- norm of gradients, clipping
+// Host arrays: addresses, lengths and types of the tensors; outs with out_dtypes
+// (the tensor's type or fp32) for clipping.
+struct GradTensors {
+  int n;
+  const void *const *data;
+  void *const *outs;
+  const int64_t *counts;
+  const int32_t *dtypes, *out_dtypes;
+};
+size_t grad_workspace(int n);
+cudaError_t launch_grads(const GradTensors &g, bool clip, double max_norm, double eps, float *norm, void *ws, int num_sms,
+                         cudaStream_t s);
 
 }  // namespace moe

@@ -5,20 +5,15 @@
 
 #include "block.h"
 #include "elem.cuh"
+#include "host_check.h"
 #include "kernels.h"
 
 namespace {
 
-bool aligned(const void *p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
-int status_of(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
-size_t round256(size_t n) { return (n + 255) / 256 * 256; }
-constexpr int64_t kMaxStride = (1LL << 31) - 1;
-
-// A row stride: 0 means contiguous.  False when it is not one.
-bool stride(int64_t given, int64_t least, long *out) {
-  *out = static_cast<long>(given == 0 ? least : given);
-  return given == 0 || (given >= least && given <= kMaxStride);
-}
+using moe::aligned;
+using moe::round256;
+using moe::status_of;
+using moe::stride;
 
 // ---------------------------------------------------------------- grouped
 int grouped_check(const moe_grouped_config *c, moe::GroupedArgs *g) {
@@ -191,6 +186,47 @@ int grouped_product(const Padded &p, const moe::GroupedArgs &t, const moe::Group
   return status_of(moe::launch_grouped_plain(g, dir, first, s));
 }
 
+// Both gradients of a bound call (either output may be NULL).
+int grouped_backward_run(moe::GroupedArgs g, void *ws, int sms, cudaStream_t stream) {
+  int rc;
+  // Large weight gradients: the experts without rows are written by plain stores (6.9
+  // TB/s) and left out of the product, whose epilogue reaches 2.8 to 6.1 TB/s on zeros.
+  g.zeroed = g.dw && !g.accumulate && static_cast<double>(g.E) * g.N * g.K >= 16e6;
+  bool have_dy = false;
+  moe::GroupedArgs dg, wg;
+  Padded pd = {false, MOE_OK}, pw = {false, MOE_OK};
+  if (g.dx) pd = grouped_tensor(g, moe::GROUPED_DGRAD, static_cast<uint8_t *>(ws), &dg, &have_dy, stream);
+  if (pd.rc == MOE_OK && g.dw) pw = grouped_tensor(g, moe::GROUPED_WGRAD, static_cast<uint8_t *>(ws), &wg, &have_dy, stream);
+  if (pd.rc != MOE_OK || pw.rc != MOE_OK) return pd.rc != MOE_OK ? pd.rc : pw.rc;
+  if (pd.ok && pw.ok) return status_of(moe::launch_grouped_tc_pair(dg, wg, sms, stream));
+  if (g.dx && (rc = grouped_product(pd, dg, g, moe::GROUPED_DGRAD, true, sms, stream)) != MOE_OK) return rc;
+  if (g.dw && (rc = grouped_product(pw, wg, g, moe::GROUPED_WGRAD, !g.dx, sms, stream)) != MOE_OK) return rc;
+  return MOE_OK;
+}
+
+// ---------------------------------------------------------------- gated
+int gated_check(const moe_gated_config *c, moe::GroupedArgs *g) {
+  if (!c) return MOE_ERR_ARG;
+  if (c->act < MOE_ACT_SILU || c->act > MOE_ACT_RELU) return MOE_ERR_ARG;
+  if (c->m <= 0) return MOE_ERR_ARG;
+  if (c->m > (1 << 19)) return MOE_ERR_SHAPE;
+  const moe_grouped_config p = {c->rows, c->E, 2 * c->m, c->K, c->dtype, c->grad_dtype, c->accumulate, c->ld_x, c->ld_gu,
+                                c->ld_w, c->ld_e};
+  const int rc = grouped_check(&p, g);
+  if (rc != MOE_OK) return rc;
+  if (!stride(c->ld_h, c->m, &g->ld_h)) return MOE_ERR_SHAPE;
+  g->act = c->act;
+  return MOE_OK;
+}
+
+// The backward's products take [dg | du] from the workspace, in rows of its own stride.
+moe::GroupedArgs gated_products(const moe::GroupedArgs &g) {
+  moe::GroupedArgs p = g;
+  p.ld_y = p.in_y = pad8(g.N);
+  return p;
+}
+size_t gated_slope_place(const moe::GroupedArgs &products) { return round256(grouped_ws(products).bytes); }
+
 // ---------------------------------------------------------------- norm
 int norm_check(const moe_norm_config *c, moe::NormArgs *a) {
   if (!c) return MOE_ERR_ARG;
@@ -293,19 +329,75 @@ int moe_grouped_backward(const moe_grouped_config *cfg, const void *dy, const vo
   g.w = w;
   g.dx = dx;
   g.dw = dw;
-  // Large weight gradients: the experts without rows are written by plain stores (6.9
-  // TB/s) and left out of the product, whose epilogue reaches 2.8 to 6.1 TB/s on zeros.
-  g.zeroed = dw && !g.accumulate && static_cast<double>(g.E) * g.N * g.K >= 16e6;
-  bool have_dy = false;
-  moe::GroupedArgs dg, wg;
-  Padded pd = {false, MOE_OK}, pw = {false, MOE_OK};
-  if (dx) pd = grouped_tensor(g, moe::GROUPED_DGRAD, static_cast<uint8_t *>(ws), &dg, &have_dy, stream);
-  if (pd.rc == MOE_OK && dw) pw = grouped_tensor(g, moe::GROUPED_WGRAD, static_cast<uint8_t *>(ws), &wg, &have_dy, stream);
-  if (pd.rc != MOE_OK || pw.rc != MOE_OK) return pd.rc != MOE_OK ? pd.rc : pw.rc;
-  if (pd.ok && pw.ok) return status_of(moe::launch_grouped_tc_pair(dg, wg, sms, stream));
-  if (dx && (rc = grouped_product(pd, dg, g, moe::GROUPED_DGRAD, true, sms, stream)) != MOE_OK) return rc;
-  if (dw && (rc = grouped_product(pw, wg, g, moe::GROUPED_WGRAD, !dx, sms, stream)) != MOE_OK) return rc;
-  return MOE_OK;
+  return grouped_backward_run(g, ws, sms, stream);
+}
+
+size_t moe_gated_forward_workspace_bytes(const moe_gated_config *cfg) {
+  moe::GroupedArgs g;
+  return gated_check(cfg, &g) == MOE_OK ? grouped_ws(g).bytes : 0;
+}
+
+size_t moe_gated_backward_workspace_bytes(const moe_gated_config *cfg) {
+  moe::GroupedArgs g;
+  if (gated_check(cfg, &g) != MOE_OK) return 0;
+  const moe::GroupedArgs p = gated_products(g);
+  return gated_slope_place(p) + static_cast<size_t>(g.rows) * p.ld_y * 2 + 256;
+}
+
+int moe_gated_forward(const moe_gated_config *cfg, const void *x, const void *w, const int32_t *offsets, void *h,
+                      void *gu, void *ws, moe_stream_t stream) {
+  moe::GroupedArgs g;
+  int rc = gated_check(cfg, &g);
+  if (rc != MOE_OK) return rc;
+  if (g.accumulate) return MOE_ERR_ARG;  // a forward overwrites
+  if (!w || !offsets || !ws || (g.rows && (!x || !h))) return MOE_ERR_ARG;
+  if (!aligned(x, 2) || !aligned(w, 2) || !aligned(h, 2) || !aligned(gu, 2) || !aligned(offsets, 4) || !aligned(ws, 16))
+    return MOE_ERR_ALIGN;
+  int sms;
+  if ((rc = moe::host_device(&sms)) != MOE_OK) return rc;
+  grouped_bind(&g, offsets, ws);
+  g.x = x;
+  g.w = w;
+  g.h = h;
+  g.y = gu;
+  g.out_dtype = g.dtype;
+  return status_of(moe::launch_gated_plain(g, stream));
+}
+
+int moe_gated_backward(const moe_gated_config *cfg, const void *dh, const void *x, const void *w, const int32_t *offsets,
+                       const void *gu, void *dx, void *dw, void *ws, moe_stream_t stream) {
+  moe::GroupedArgs g;
+  int rc = gated_check(cfg, &g);
+  if (rc != MOE_OK) return rc;
+  if (!offsets || !ws || (g.rows && (!dh || !gu))) return MOE_ERR_ARG;
+  if (g.rows && !dx && !dw) return MOE_ERR_ARG;
+  if ((dx && !w) || (dw && g.rows && !x)) return MOE_ERR_ARG;
+  if (!aligned(dh, 2) || !aligned(gu, 2) || !aligned(x, 2) || !aligned(w, 2) || !aligned(dx, 2) ||
+      !aligned(dw, moe::elem_bytes(g.out_dtype)) || !aligned(offsets, 4) || !aligned(ws, 16))
+    return MOE_ERR_ALIGN;
+  int sms;
+  if ((rc = moe::host_device(&sms)) != MOE_OK) return rc;
+  moe::GroupedArgs p = gated_products(g);
+  const uintptr_t place = reinterpret_cast<uintptr_t>(ws) + gated_slope_place(p);
+  moe::GatedArgs a = {};
+  a.rows = g.rows;
+  a.m = g.N / 2;
+  a.dtype = g.dtype;
+  a.act = g.act;
+  a.ld_h = g.ld_h;
+  a.ld_gu = g.ld_y;
+  a.ld_dgu = p.ld_y;
+  a.dh = dh;
+  a.gu = gu;
+  a.dgu = reinterpret_cast<void *>((place + 255) & ~static_cast<uintptr_t>(255));
+  if ((rc = status_of(moe::launch_gated_slope(a, sms, stream))) != MOE_OK) return rc;
+  grouped_bind(&p, offsets, ws);
+  p.dy = a.dgu;
+  p.x = x;
+  p.w = w;
+  p.dx = dx;
+  p.dw = dw;
+  return grouped_backward_run(p, ws, sms, stream);
 }
 
 int moe_norm_forward(const moe_norm_config *cfg, const void *x, const void *f, const void *gate, const void *w_post,

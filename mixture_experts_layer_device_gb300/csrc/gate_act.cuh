@@ -1,0 +1,44 @@
+// The activations of the gated products and their derivatives, in fp32.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+// All by forms that keep their relative precision where the activation dies out (a
+// sum 1 + erf or 1 + tanh loses it): Phi(g) = erfc(-g / sqrt 2) / 2, and the form by tanh
+// is g times the logistic function of 2 sqrt(2 / pi) (g + 0.044715 g^3).  The hardware's
+// exponential as in the layer's SwiGLU: every use is rounded to 16 bits.
+constexpr float kTanhSlope = 1.5957691216057308f, kTanhCube = 0.044715f;
+
+// act(g).
+template <int ACT>
+MOE_DEV float act_value(float g) {
+  if constexpr (ACT == MOE_ACT_SILU) return silu(g);
+  if constexpr (ACT == MOE_ACT_GELU) return 0.5f * g * erfcf(g * -0.70710678118654752f);
+  if constexpr (ACT == MOE_ACT_GELU_TANH) return g * sigmoidf(kTanhSlope * g * (1.0f + kTanhCube * g * g));
+  return g <= 0.f ? 0.f : g;  // NaN stays
+}
+
+// act(g) and act'(g).
+template <int ACT>
+MOE_DEV void act_slope(float g, float &value, float &slope) {
+  if constexpr (ACT == MOE_ACT_SILU) {
+    const float s = sigmoidf(g);
+    value = g * s;
+    slope = s * (1.0f + g * (1.0f - s));
+  } else if constexpr (ACT == MOE_ACT_GELU) {
+    const float cdf = 0.5f * erfcf(g * -0.70710678118654752f);
+    value = g * cdf;
+    slope = cdf + g * __expf(-0.5f * g * g) * 0.39894228040143268f;
+  } else if constexpr (ACT == MOE_ACT_GELU_TANH) {
+    const float s = sigmoidf(kTanhSlope * g * (1.0f + kTanhCube * g * g));
+    value = g * s;
+    slope = s + value * (1.0f - s) * kTanhSlope * (1.0f + 3.0f * kTanhCube * g * g);
+  } else {
+    value = g <= 0.f ? 0.f : g;
+    slope = g <= 0.f ? 0.f : 1.f;
+  }
+}
+
+}  // namespace moe

@@ -1,0 +1,308 @@
+// The global norm of many gradients, and their clipping:
+//   norm = sqrt(sum over all tensors of g^2),  c = min(1, max_norm / (norm + eps)),  out = c g
+//
+// Two launches: blocks leave sums of squares, then the blocks of the next launch
+// each add those up in the same order (a few kilobytes from L2) and scale.  The
+// tensors' addresses and lengths travel as launch parameters, so nothing is
+// copied to the device and a captured graph keeps them.
+//
+// Bound by memory: the norm reads everything once.  Clipping reads it again,
+// from the end backwards, where L2 still holds what the norm read last; in place
+// and below the limit (c = 1) it reads and writes nothing.
+//
+// Sums: a thread squares up to 64 elements in fp32 and adds that to a 64-bit
+// sum.  Where fp32 overflows or its squares sink below the normal range, the
+// same 64 elements are squared again in 64 bits.
+#include "block.h"
+#include "elem.cuh"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kGradThreads = 256;
+constexpr int kVecs = 8;                                // 16-byte pieces per thread and chunk
+constexpr int kChunkVecs = kGradThreads * kVecs;        // 32 KB
+
+// The tensors of one launch: their first elements, lengths and types, and the
+// first chunk of each.  A chunk is kChunkVecs aligned 16-byte pieces; a tensor's
+// first and last piece may be cut.
+template <int MOST>
+struct GradTable {
+  int n, chunks;
+  const uint8_t *data[MOST];
+  uint8_t *out[MOST];
+  int64_t count[MOST];
+  int first[MOST + 1];
+  uint8_t type[MOST], out_type[MOST];
+};
+constexpr int kFewTensors = 64, kManyTensors = 1024;
+static_assert(sizeof(GradTable<kManyTensors>) + 64 <= 32764, "launch parameters");
+
+template <int MOST>
+MOE_DEV int tensor_of_chunk(const GradTable<MOST> &t, int c) {
+  int lo = 0, hi = t.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.first[mid] <= c) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// The elements of a chunk that one thread takes, as raw 16-byte pieces; absent ones
+// are zeros.  Elements in front of the tensor or behind it are not read.
+template <typename T>
+struct Piece {
+  static constexpr int VEC = Elem<T>::VEC;
+  const T *base;    // the aligned piece in which the tensor starts
+  int64_t lead;     // elements in front of the tensor in it
+  int64_t end;      // lead + count
+  MOE_DEV Piece(const uint8_t *data, int64_t count) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(data);
+    base = reinterpret_cast<const T *>(p & ~static_cast<uintptr_t>(15));
+    lead = static_cast<int64_t>((p & 15) / sizeof(T));
+    end = lead + count;
+  }
+  MOE_DEV bool whole(int64_t v) const { return v * VEC >= lead && v * VEC + VEC <= end; }
+  MOE_DEV uint4 load(int64_t v) const {
+    if (whole(v)) return ld_stream(base + v * VEC);
+    union {
+      uint4 q;
+      T e[VEC];
+    } u;
+    u.q = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) {
+      const int64_t i = v * VEC + k;
+      if (i >= lead && i < end) u.e[k] = base[i];
+    }
+    return u.q;
+  }
+};
+
+// Sum of the squares of kVecs pieces in 64 bits.
+template <typename T>
+MOE_DEV double squares(const uint4 (&q)[kVecs]) {
+  constexpr int VEC = Elem<T>::VEC;
+  float s0 = 0.f, s1 = 0.f;
+  uint32_t any = 0;
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    float v[VEC];
+    Elem<T>::unpack(q[j], v);
+#pragma unroll
+    for (int k = 0; k < VEC; k += 2) {
+      s0 = fmaf(v[k], v[k], s0);
+      s1 = fmaf(v[k + 1], v[k + 1], s1);
+    }
+    any |= q[j].x | q[j].y | q[j].z | q[j].w;
+  }
+  const float s = s0 + s1;
+  // from 2^-110 on, 64 squares that are each off by half of fp32's smallest step do not count
+  const uint32_t magnitude = sizeof(T) == 2 ? 0x7fff7fffu : 0x7fffffffu;
+  if ((s >= 7.7e-34f && s <= 3.0e38f) || (any & magnitude) == 0) return s;
+  double d = 0.0;
+#pragma unroll 1
+  for (int j = 0; j < kVecs; ++j) {
+    float v[VEC];
+    uint4 p = q[0];
+#pragma unroll
+    for (int i = 1; i < kVecs; ++i)
+      if (i == j) p = q[i];
+    Elem<T>::unpack(p, v);
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) d = fma(static_cast<double>(v[k]), static_cast<double>(v[k]), d);
+  }
+  return d;
+}
+
+template <typename T>
+MOE_DEV double chunk_squares(const uint8_t *data, int64_t count, int local) {
+  const Piece<T> p(data, count);
+  const int64_t v0 = static_cast<int64_t>(local) * kChunkVecs + threadIdx.x;
+  uint4 q[kVecs];
+  if (v0 * Piece<T>::VEC >= p.end) return 0.0;
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) q[j] = p.load(v0 + j * kGradThreads);
+  return squares<T>(q);
+}
+
+// A block's sum of its threads' values, in a fixed order; valid in thread 0.
+MOE_DEV double block_sum(double v) {
+  __shared__ double part[kGradThreads / 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  double s = 0.0;
+#pragma unroll
+  for (int w = 0; w < kGradThreads / 32; ++w) s += part[w];
+  return s;
+}
+
+template <int MOST>
+__global__ void __launch_bounds__(kGradThreads, 4) grad_squares_kernel(const __grid_constant__ GradTable<MOST> t,
+                                                                       double *part) {
+  pdl_trigger();
+  double sum = 0.0;
+  for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+    const int i = tensor_of_chunk(t, c), local = c - t.first[i];
+    if (t.type[i] == MOE_ELEM_BF16) sum += chunk_squares<__nv_bfloat16>(t.data[i], t.count[i], local);
+    else if (t.type[i] == MOE_ELEM_FP16) sum += chunk_squares<__half>(t.data[i], t.count[i], local);
+    else sum += chunk_squares<float>(t.data[i], t.count[i], local);
+  }
+  sum = block_sum(sum);
+  if (threadIdx.x == 0) part[blockIdx.x] = sum;
+}
+
+// The norm from all blocks' sums; every thread has it.
+MOE_DEV double norm_of(const double *part, int n) {
+  double v = 0.0;
+  for (int i = threadIdx.x; i < n; i += kGradThreads) v += part[i];
+  return sqrt(block_sum(v));
+}
+
+__global__ void __launch_bounds__(kGradThreads) grad_norm_kernel(const double *part, int n, float *norm) {
+  pdl_wait();
+  const double v = norm_of(part, n);
+  if (threadIdx.x == 0) *norm = static_cast<float>(v);
+}
+
+// One thread's pieces of a chunk, times c, to `out`.
+template <typename T, typename O>
+MOE_DEV void chunk_scale(const uint8_t *data, uint8_t *out, int64_t count, int local, float c) {
+  constexpr int VEC = Elem<T>::VEC;
+  const Piece<T> p(data, count);
+  O *o = reinterpret_cast<O *>(out) - p.lead;  // the place of piece 0's first element
+  const bool vec = (reinterpret_cast<uintptr_t>(o) & 15) == 0;
+  const int64_t v0 = static_cast<int64_t>(local) * kChunkVecs + threadIdx.x;
+  if (v0 * VEC >= p.end) return;
+  uint4 q[kVecs];
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) q[j] = p.load(v0 + j * kGradThreads);
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    const int64_t v = v0 + j * kGradThreads;
+    float f[VEC];
+    Elem<T>::unpack(q[j], f);
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) f[k] *= c;
+    if (vec && p.whole(v)) {
+      constexpr int OV = Elem<O>::VEC;
+#pragma unroll
+      for (int k = 0; k < VEC; k += OV) st_stream(o + v * VEC + k, Elem<O>::pack(f + k));
+    } else {
+#pragma unroll
+      for (int k = 0; k < VEC; ++k) {
+        const int64_t i = v * VEC + k;
+        if (i >= p.lead && i < p.end) o[i] = Elem<O>::from(f[k]);
+      }
+    }
+  }
+}
+
+template <typename T>
+MOE_DEV void chunk_scale_to(const uint8_t *data, uint8_t *out, int out_type, int64_t count, int local, float c) {
+  if (out_type == MOE_ELEM_FP32) chunk_scale<T, float>(data, out, count, local, c);
+  else chunk_scale<T, T>(data, out, count, local, c);
+}
+
+template <int MOST>
+__global__ void __launch_bounds__(kGradThreads, 4) grad_scale_kernel(const __grid_constant__ GradTable<MOST> t,
+                                                                     const double *part, int n, double max_norm,
+                                                                     double eps, float *norm) {
+  pdl_wait();
+  const double v = norm_of(part, n);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && norm) *norm = static_cast<float>(v);
+  const double r = max_norm / (v + eps);
+  const float c = r >= 1.0 ? 1.f : static_cast<float>(r);  // NaN stays
+  for (int k = blockIdx.x; k < t.chunks; k += gridDim.x) {
+    const int chunk = t.chunks - 1 - k, i = tensor_of_chunk(t, chunk), local = chunk - t.first[i];
+    if (c == 1.f && t.out[i] == t.data[i]) continue;
+    if (t.type[i] == MOE_ELEM_BF16) chunk_scale_to<__nv_bfloat16>(t.data[i], t.out[i], t.out_type[i], t.count[i], local, c);
+    else if (t.type[i] == MOE_ELEM_FP16) chunk_scale_to<__half>(t.data[i], t.out[i], t.out_type[i], t.count[i], local, c);
+    else chunk_scale_to<float>(t.data[i], t.out[i], t.out_type[i], t.count[i], local, c);
+  }
+}
+
+long tensor_chunks(const GradTensors &g, int i) {
+  const int64_t e = elem_bytes(g.dtypes[i]);
+  const int64_t lead = static_cast<int64_t>(reinterpret_cast<uintptr_t>(g.data[i]) & 15) / e;
+  const int64_t vecs = (lead + g.counts[i] + 16 / e - 1) / (16 / e);
+  return static_cast<long>((vecs + kChunkVecs - 1) / kChunkVecs);
+}
+
+// The next launch's tensors, from `at` on: as many as the table holds.  Empty ones are
+// left out.  (Their chunks, 32 KB each, are counted in 32 bits.)
+template <int MOST>
+int fill_table(GradTable<MOST> *t, const GradTensors &g, int at) {
+  t->n = 0;
+  long chunks = 0;
+  for (; at < g.n && t->n < MOST; ++at) {
+    if (g.counts[at] == 0) continue;
+    const long more = tensor_chunks(g, at);
+    const int i = t->n++;
+    t->data[i] = static_cast<const uint8_t *>(g.data[at]);
+    t->out[i] = g.outs ? static_cast<uint8_t *>(g.outs[at]) : nullptr;
+    t->count[i] = g.counts[at];
+    t->type[i] = static_cast<uint8_t>(g.dtypes[at]);
+    t->out_type[i] = static_cast<uint8_t>(g.outs ? g.out_dtypes[at] : 0);
+    t->first[i] = static_cast<int>(chunks);
+    chunks += more;
+  }
+  t->chunks = static_cast<int>(chunks);
+  t->first[t->n] = t->chunks;
+  return at;
+}
+
+// Four blocks per SM; the workspace has room for so many sums per launch.
+constexpr int kMostBlocks = 4 * 152;
+int grid_of(int chunks, int num_sms) {
+  const int most = num_sms * 4 < kMostBlocks ? num_sms * 4 : kMostBlocks;
+  return chunks < most ? chunks : most;
+}
+
+template <int MOST>
+cudaError_t grads(const GradTensors &g, bool clip, double max_norm, double eps, float *norm, double *part, int num_sms,
+                  cudaStream_t s) {
+  GradTable<MOST> t;
+  int sums = 0;
+  for (int at = 0; at < g.n;) {
+    at = fill_table(&t, g, at);
+    if (t.chunks == 0) break;
+    HostTrace trace("grad_squares", s);
+    const int grid = grid_of(t.chunks, num_sms);
+    grad_squares_kernel<MOST><<<grid, kGradThreads, 0, s>>>(t, part + sums);
+    sums += grid;
+  }
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  if (!clip || sums == 0) {
+    HostTrace trace("grad_norm", s);
+    return launch_early(grad_norm_kernel, 1, kGradThreads, s, static_cast<const double *>(part), sums, norm);
+  }
+  for (int at = 0; at < g.n;) {
+    at = fill_table(&t, g, at);
+    if (t.chunks == 0) break;
+    HostTrace trace("grad_scale", s);
+    e = launch_early(grad_scale_kernel<MOST>, grid_of(t.chunks, num_sms), kGradThreads, s, t,
+                     static_cast<const double *>(part), sums, max_norm, eps, norm);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+size_t grad_workspace(int n) { return (static_cast<size_t>(n) / kManyTensors + 1) * kMostBlocks * sizeof(double); }
+
+cudaError_t launch_grads(const GradTensors &g, bool clip, double max_norm, double eps, float *norm, void *ws, int num_sms,
+                         cudaStream_t s) {
+  double *part = static_cast<double *>(ws);
+  return g.n <= kFewTensors ? grads<kFewTensors>(g, clip, max_norm, eps, norm, part, num_sms, s)
+                            : grads<kManyTensors>(g, clip, max_norm, eps, norm, part, num_sms, s);
+}
+
+}  // namespace moe

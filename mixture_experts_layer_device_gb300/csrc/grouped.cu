@@ -7,6 +7,7 @@
 // differs (m for y and dx, k for dw).
 #include "block.h"
 #include "elem.cuh"
+#include "gate_act.cuh"
 #include "grouped.cuh"
 #include "kernels.h"
 
@@ -253,6 +254,52 @@ __global__ void __launch_bounds__(128) grouped_plain_kernel(const GroupedArgs g)
       }
 }
 
+// The gated forward: a tile of h from the tiles of both projections.
+template <typename T, int ACT>
+__global__ void __launch_bounds__(128) gated_plain_kernel(const GroupedArgs g) {
+  pdl_wait();  // the plan's tile table
+  if (static_cast<int>(blockIdx.x) >= g.tiles[g.E]) return;
+  const int e = group_of_tile(g.tiles, g.E, blockIdx.x), half = g.N >> 1;
+  int lo, hi;
+  group_rows(g, e, lo, hi);
+  const int m0 = lo + (blockIdx.x - g.tiles[e]) * PT, n0 = blockIdx.y * PT, mn = hi - m0, nn = half - n0;
+  const uint16_t *w = static_cast<const uint16_t *>(g.w) + static_cast<long>(e) * g.ld_e;
+  const Side a{static_cast<const uint16_t *>(g.x) + m0 * g.ld_x, g.ld_x, 1, mn, g.K};
+  float gate[2][4][4], up[2][4][4];
+  plain_tile<T>(a, Side{w + n0 * g.ld_w, g.ld_w, 1, nn, g.K}, g.K, gate);
+  plain_tile<T>(a, Side{w + (half + static_cast<long>(n0)) * g.ld_w, g.ld_w, 1, nn, g.K}, g.K, up);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  T *h = static_cast<T *>(g.h) + m0 * g.ld_h + n0, *y = g.y ? static_cast<T *>(g.y) + m0 * g.ld_y + n0 : nullptr;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        int m, n;
+        acc_place(warp, lane, i, j, k, m, n);
+        if (m < mn && n < nn) {
+          h[m * g.ld_h + n] = Elem<T>::from(act_value<ACT>(gate[i][j][k]) * up[i][j][k]);
+          if (y) {
+            y[m * g.ld_y + n] = Elem<T>::from(gate[i][j][k]);
+            y[m * g.ld_y + half + n] = Elem<T>::from(up[i][j][k]);
+          }
+        }
+      }
+}
+
+template <typename T>
+cudaError_t gated_plain_type(const GroupedArgs &g, cudaStream_t s) {
+  const long slots = (g.rows + PT - 1L) / PT + (g.E < g.rows ? g.E : g.rows);
+  const dim3 grid(slots, ((g.N >> 1) + PT - 1) / PT);
+  switch (g.act) {
+    case MOE_ACT_SILU: return launch_early(gated_plain_kernel<T, MOE_ACT_SILU>, grid, 128, s, g);
+    case MOE_ACT_GELU: return launch_early(gated_plain_kernel<T, MOE_ACT_GELU>, grid, 128, s, g);
+    case MOE_ACT_GELU_TANH: return launch_early(gated_plain_kernel<T, MOE_ACT_GELU_TANH>, grid, 128, s, g);
+    default: return launch_early(gated_plain_kernel<T, MOE_ACT_RELU>, grid, 128, s, g);
+  }
+}
+
 template <typename T>
 cudaError_t plain_type(const GroupedArgs &g, int dir, bool planned, cudaStream_t s) {
   const long slots = (g.rows + PT - 1L) / PT + (g.E < g.rows ? g.E : g.rows);
@@ -477,6 +524,16 @@ cudaError_t launch_grouped_plain(const GroupedArgs &g, int dir, bool first, cuda
   }
   HostTrace t(dir == GROUPED_FWD ? "grouped_fwd_plain" : dir == GROUPED_DGRAD ? "grouped_dgrad_plain" : "grouped_wgrad_plain", s);
   return g.dtype == MOE_ELEM_BF16 ? plain_type<__nv_bfloat16>(g, dir, first, s) : plain_type<__half>(g, dir, first, s);
+}
+
+cudaError_t launch_gated_plain(const GroupedArgs &g, cudaStream_t s) {
+  if (g.rows == 0) return launch_grouped_plan(g, PT, nullptr, g.dtype, 0, 0, s);
+  cudaError_t e = cudaSuccess;
+  if (g.y) e = launch_grouped_plan(g, PT, g.y, g.dtype, g.N, g.ld_y, s);
+  if (e == cudaSuccess) e = launch_grouped_plan(g, PT, g.h, g.dtype, g.N >> 1, g.ld_h, s);
+  if (e != cudaSuccess) return e;
+  HostTrace t("gated_plain", s);
+  return g.dtype == MOE_ELEM_BF16 ? gated_plain_type<__nv_bfloat16>(g, s) : gated_plain_type<__half>(g, s);
 }
 
 }  // namespace moe

@@ -1,0 +1,307 @@
+// The loss over a vocabulary, without its logits in memory: the rows that count,
+// the copy of x that the products read, and what joins the products' parts.
+//   z_tv = x_t . w_v,  lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_t[label_t]
+//   dz_tv = (dloss_t + dlse_t) exp(z_tv - lse_t) - dloss_t [v = label_t]
+//   dx_t = sum_v dz_tv w_v,  dw_v = sum_t dz_tv x_t
+// The products are in vocab_tc.cu.
+#include "block.h"
+#include "elem.cuh"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+MOE_DEV long label_of(const VocabArgs &a, int t) {
+  return a.labels64 ? static_cast<long>(static_cast<const long long *>(a.labels)[t])
+                    : static_cast<long>(static_cast<const int *>(a.labels)[t]);
+}
+
+// ---------------------------------------------------------------- rows that count
+// One block: the rows that count, in order.  Forward: those whose label lies in the
+// vocabulary; the others' loss and lse are zero.  Backward: of those, the ones that
+// have a gradient at all.  What is rounded to 16 bits, dz, is held relative to the
+// largest coefficient of all rows (times 2^14 in fp16, whose smallest steps
+// probabilities would sink below): equal coefficients, as a mean gives, are then 1
+// and lose nothing; *scale undoes it.
+constexpr int kRowThreads = 1024, kRowItems = 8;
+
+template <bool BACKWARD>
+MOE_DEV bool row_counts(const VocabArgs &a, int t, long &label, float &p, float &l) {
+  label = label_of(a, t);
+  p = l = 0.f;
+  if (label < 0 || label >= a.V) return false;
+  if constexpr (BACKWARD) {
+    l = a.dloss ? a.dloss[t] : 0.f;
+    p = l + (a.dlse ? a.dlse[t] : 0.f);
+    return p != 0.f || l != 0.f;  // NaN counts
+  }
+  return true;
+}
+
+template <bool BACKWARD>
+__global__ void __launch_bounds__(kRowThreads) vocab_rows_kernel(const VocabArgs a) {
+  pdl_trigger();
+  __shared__ int warps[32];
+  __shared__ float tops[32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float top = 0.f;
+  if constexpr (BACKWARD) {
+    for (int t = threadIdx.x; t < a.rows; t += kRowThreads) {
+      long label;
+      float p, l;
+      if (row_counts<true>(a, t, label, p, l)) {
+        const float m = fmaxf(fabsf(p), fabsf(l));  // one that is not finite keeps to its own row
+        if (m <= 3.402823466e38f) top = fmaxf(top, m);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) tops[warp] = top;
+    __syncthreads();
+    top = tops[lane];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (top == 0.f) top = 1.f;
+  }
+  const float up = a.dtype == MOE_ELEM_FP16 ? 16384.f : 1.f;
+  int done = 0;
+  for (int t0 = 0; t0 < a.rows; t0 += kRowThreads * kRowItems) {
+    const int first = t0 + threadIdx.x * kRowItems;
+    unsigned mask = 0;
+#pragma unroll
+    for (int k = 0; k < kRowItems; ++k) {
+      long label;
+      float p, l;
+      if (first + k < a.rows && row_counts<BACKWARD>(a, first + k, label, p, l)) mask |= 1u << k;
+    }
+    const int mine = __popc(mask);
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    __syncthreads();
+    if (lane == 31) warps[warp] = inc;
+    __syncthreads();
+    const int w = warps[lane];
+    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+    int at = done + before + inc - mine;
+    done += __reduce_add_sync(0xffffffffu, w);
+#pragma unroll
+    for (int k = 0; k < kRowItems; ++k) {
+      const int t = first + k;
+      if (t >= a.rows) break;
+      if (mask >> k & 1u) {
+        long label;
+        float p, l;
+        row_counts<BACKWARD>(a, t, label, p, l);
+        a.row[at] = t;
+        a.label[at] = static_cast<int>(label);
+        if constexpr (BACKWARD) {
+          a.place[t] = at;
+          a.coef_p[at] = p / top * up;
+          a.coef_l[at] = l / top * up;
+          a.base[at] = a.lse_in[t] * kLog2e;
+        }
+        ++at;
+      } else if constexpr (BACKWARD) {
+        a.place[t] = -1;
+      } else {
+        a.loss[t] = 0.f;
+        a.lse[t] = 0.f;
+      }
+    }
+  }
+  if (threadIdx.x == 0) {
+    *a.status = 0;
+    *a.count = done;
+    if constexpr (BACKWARD) *a.scale = top / up;
+  }
+  if constexpr (BACKWARD) {  // places behind the last one: no gradient
+    const int end = (done + 255) & ~255;
+    for (int i = done + threadIdx.x; i < end; i += kRowThreads) {
+      a.coef_p[i] = a.coef_l[i] = a.base[i] = 0.f;
+      a.label[i] = -1;
+    }
+  } else {
+    const int end = (done + 255) & ~255;
+    for (int i = done + threadIdx.x; i < end; i += kRowThreads) a.label[i] = -1;
+  }
+}
+
+// ---------------------------------------------------------------- copies
+// xs [count rounded up to 128 (or rows)][ld_xs] = x[row[i]], zeros beyond x's columns
+// and behind the last row: a sum over rows takes them in steps of up to 128.
+__global__ void __launch_bounds__(256) vocab_gather_kernel(const VocabArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int n = *a.count, chunks = static_cast<int>(a.ld_xs >> 3);
+  const int end = ((n + 127) & ~127) < a.rows ? ((n + 127) & ~127) : a.rows;
+  const long total = static_cast<long>(end) * chunks;
+  const bool vec = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && a.ld_x % 8 == 0 && a.d % 8 == 0;
+  uint16_t *xs = static_cast<uint16_t *>(a.xs);
+  for (long u = static_cast<long>(blockIdx.x) * 256 + threadIdx.x; u < total; u += static_cast<long>(gridDim.x) * 256) {
+    const int i = static_cast<int>(u / chunks), c = static_cast<int>(u - static_cast<long>(i) * chunks) * 8;
+    uint4 q = make_uint4(0, 0, 0, 0);
+    if (i < n) {
+      const uint16_t *p = static_cast<const uint16_t *>(a.x) + a.row[i] * a.ld_x + c;
+      if (vec) {
+        q = *reinterpret_cast<const uint4 *>(p);
+      } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t lo = c + 2 * k < a.d ? p[2 * k] : 0u, hi = c + 2 * k + 1 < a.d ? p[2 * k + 1] : 0u;
+          w[k] = lo | (hi << 16);
+        }
+        q = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    *reinterpret_cast<uint4 *>(xs + i * a.ld_xs + c) = q;
+  }
+}
+
+// w's rows into rows that TMA can address: a thread per 8 elements.
+__global__ void __launch_bounds__(256) vocab_pad_kernel(const VocabArgs a) {
+  const int chunks = static_cast<int>(a.ld_ws_w >> 3);
+  const long total = static_cast<long>(a.V) * chunks;
+  for (long u = static_cast<long>(blockIdx.x) * 256 + threadIdx.x; u < total; u += static_cast<long>(gridDim.x) * 256) {
+    const long v = u / chunks;
+    const int c = static_cast<int>(u - v * chunks) * 8;
+    const uint16_t *p = static_cast<const uint16_t *>(a.w) + v * a.ld_w + c;
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t lo = c + 2 * k < a.d ? p[2 * k] : 0u, hi = c + 2 * k + 1 < a.d ? p[2 * k + 1] : 0u;
+      w[k] = lo | (hi << 16);
+    }
+    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.ws_w) + v * a.ld_ws_w + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// ---------------------------------------------------------------- joins
+// (maximum, sum of 2^((z - maximum) log2 e)) of two sets of logits.  Where the larger
+// maximum is not finite, its exponentials were taken from zero.
+MOE_DEV float from_of(float m) { return fabsf(m) <= 3.402823466e38f ? m : 0.f; }
+MOE_DEV float2 join(float2 a, float2 b) {
+  const float m = fmaxf(a.x, b.x), f = from_of(m);
+  // a set without logits has sum 0, whatever its maximum's distance
+  const float sa = a.y == 0.f ? 0.f : a.y * exp2f((from_of(a.x) - f) * kLog2e);
+  const float sb = b.y == 0.f ? 0.f : b.y * exp2f((from_of(b.x) - f) * kLog2e);
+  return make_float2(m, sa + sb);
+}
+
+// One warp per row that counts.
+__global__ void __launch_bounds__(256) vocab_loss_kernel(const VocabArgs a) {
+  pdl_wait();
+  const int n = *a.count, lane = threadIdx.x & 31;
+  for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < n; i += gridDim.x * 8) {
+    const float2 *p = a.part + static_cast<long>(i) * a.parts;
+    float2 v = make_float2(-__int_as_float(0x7f800000), 0.f);
+    for (int k = lane; k < a.parts; k += 32) v = join(v, p[k]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float2 w = make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o));
+      v = join(v, w);
+    }
+    if (lane == 0) {
+      const float lse = from_of(v.x) + logf(v.y);
+      const int t = a.row[i];
+      a.lse[t] = lse;
+      a.loss[t] = lse - a.hit[i];
+    }
+  }
+}
+
+// dx of every row: the splits' sums in order, times *scale; zeros for rows that do not
+// count.
+template <typename T>
+__global__ void __launch_bounds__(256) vocab_dx_kernel(const VocabArgs a, bool vec) {
+  pdl_wait();
+  const float scale = *a.scale;
+  const int chunks = (a.d + 7) >> 3;
+  const long total = static_cast<long>(a.rows) * chunks, step = static_cast<long>(a.rows) * a.ld_sum;
+  for (long u = static_cast<long>(blockIdx.x) * 256 + threadIdx.x; u < total; u += static_cast<long>(gridDim.x) * 256) {
+    const int t = static_cast<int>(u / chunks), c = static_cast<int>(u - static_cast<long>(t) * chunks) * 8;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const int i = a.place[t];
+    if (i >= 0) {
+      const float *p = a.sum + i * a.ld_sum + c;
+      for (int k = 0; k < a.splits; ++k, p += step) {
+        const float4 lo = *reinterpret_cast<const float4 *>(p), hi = *reinterpret_cast<const float4 *>(p + 4);
+        v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+        v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] *= scale;
+    }
+    T *o = static_cast<T *>(a.dx) + t * a.ld_dx + c;
+    if (vec) {
+      *reinterpret_cast<uint4 *>(o) = Elem<T>::pack(v);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (c + k < a.d) o[k] = Elem<T>::from(v[k]);
+    }
+  }
+}
+
+unsigned blocks_of(long threads, int num_sms) {
+  const long want = (threads + 255) / 256, most = num_sms * 16L;
+  return static_cast<unsigned>(want < 1 ? 1 : want < most ? want : most);
+}
+
+cudaError_t copies(const VocabArgs &a, bool backward, int num_sms, cudaStream_t s) {
+  if (a.pad_w) {
+    HostTrace t("vocab_pad", s);
+    vocab_pad_kernel<<<blocks_of(static_cast<long>(a.V) * (a.ld_ws_w >> 3), num_sms), 256, 0, s>>>(a);
+  }
+  {
+    HostTrace t("vocab_rows", s);
+    if (backward) vocab_rows_kernel<true><<<1, kRowThreads, 0, s>>>(a);
+    else vocab_rows_kernel<false><<<1, kRowThreads, 0, s>>>(a);
+  }
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  HostTrace t("vocab_gather", s);
+  return launch_early(vocab_gather_kernel, blocks_of(static_cast<long>(a.rows) * (a.ld_xs >> 3), num_sms), 256, s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_vocab_forward(const VocabArgs &a, int num_sms, cudaStream_t s) {
+  if (a.rows == 0) return cudaSuccess;
+  cudaError_t e = copies(a, false, num_sms, s);
+  if (e == cudaSuccess) e = launch_vocab_tc(a, VOCAB_LOSS, s);
+  if (e != cudaSuccess) return e;
+  HostTrace t("vocab_loss", s);
+  return launch_early(vocab_loss_kernel, blocks_of(static_cast<long>(a.rows) * 32, num_sms), 256, s, a);
+}
+
+cudaError_t launch_vocab_backward(const VocabArgs &given, int num_sms, cudaStream_t s) {
+  VocabArgs a = given;
+  cudaError_t e = cudaSuccess;
+  if (a.rows > 0) {
+    e = copies(a, true, num_sms, s);
+  } else {
+    e = cudaMemsetAsync(a.status, 0, 256, s);  // status and count: no rows
+  }
+  for (a.v0 = 0; a.v0 < a.V && e == cudaSuccess; a.v0 += a.width) {
+    a.wp = a.V - a.v0 < a.width ? a.V - a.v0 : a.width;
+    if (a.rows > 0) e = launch_vocab_tc(a, VOCAB_DZ, s);
+    if (e == cudaSuccess && a.dx && a.rows > 0) e = launch_vocab_tc(a, VOCAB_DX, s);
+    if (e == cudaSuccess && a.dw) e = launch_vocab_tc(a, VOCAB_DW, s);
+  }
+  if (e != cudaSuccess || !a.dx || a.rows == 0) return e;
+  const bool vec = (reinterpret_cast<uintptr_t>(a.dx) & 15) == 0 && a.ld_dx % 8 == 0 && a.d % 8 == 0;
+  HostTrace t("vocab_dx", s);
+  const unsigned blocks = blocks_of(static_cast<long>(a.rows) * ((a.d + 7) / 8), num_sms);
+  return a.dtype == MOE_ELEM_BF16 ? launch_early(vocab_dx_kernel<__nv_bfloat16>, blocks, 256, s, a, vec)
+                                  : launch_early(vocab_dx_kernel<__half>, blocks, 256, s, a, vec);
+}
+
+}  // namespace moe

@@ -1,0 +1,575 @@
+// The products behind the loss over a vocabulary on CTA pairs (tcgen05, cta_group::2):
+//
+//   LOSS  logits z = xs w^T of 256 rows x 256 vocabulary entries; a row's maximum, sum of
+//         exponentials and label's logit leave, the logits do not
+//   DZ    the same logits again, out as dz = coef_p exp(z - lse) - coef_l [label] in
+//         16 bits, one piece of the vocabulary at a time
+//   DX    sum += dz w over a piece            A = dz K-major,  B = w read MN-major
+//   DW    dw = dz^T xs                        A and B read MN-major
+//
+// With the rows on the instruction's M side a thread of the epilogue owns one
+// row: maximum, sum and label stay in its registers, without a shuffle.  Rows are
+// dense here (those that do not count were left out by the copy), so tiles are
+// whole; what a tile has past the last row or column is computed on zeros that TMA
+// fills in and not stored.
+//
+// Bound by the tensor cores from some 512 rows on, by reading w below.
+//
+// Roles per CTA (320 threads) as in the grouped products: TMA producer, MMA issuer
+// (leader CTA), eight epilogue warps; three 64 KB stages of two blocks of 64
+// reduction steps; two accumulators of 256 TMEM columns.  Persistent over pairs.
+// Tiles are taken in bands of kBand row tiles, so that a band's rows stay in L2
+// while the other operand streams by.  Every wait is bounded (mbar_wait).
+#include <type_traits>
+
+#include "elem.cuh"
+#include "gemm_common.cuh"
+#include "kernels.h"
+
+#include "block.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kBlockBytes = 32768;  // 64 reduction steps: 16 KB of A, 16 KB of B
+constexpr int kThreads = 320;
+constexpr int kEpilogueWarps = 8;
+constexpr int kStaging = 4096;      // per epilogue warp
+constexpr int kBlocks = 2, kStages = 3;
+constexpr int kStageBytes = kBlocks * kBlockBytes;
+constexpr size_t kSmem = 1024 + kStages * kStageBytes + kEpilogueWarps * kStaging + (2 * kStages + 5) * 8 + 16;
+static_assert(kSmem <= 232448, "shared memory");
+constexpr int kBand = 8;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+struct VocabMaps {
+  CUtensorMap a, b, out;
+};
+
+MOE_DEV void tma_store_2d(const CUtensorMap *map, const void *src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1)
+               : "memory");
+}
+MOE_DEV void tma_add_2d(const CUtensorMap *map, const void *src, int c0, int c1) {
+  asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(map),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1)
+               : "memory");
+}
+MOE_DEV void tma_store_3d(const CUtensorMap *map, const void *src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+MOE_DEV void tma_add_3d(const CUtensorMap *map, const void *src, int c0, int c1, int c2) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   map),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
+
+// Descriptor of an MN-major operand in the 128-byte swizzle: rows of 64 features
+// (128 bytes), one per reduction step; 8 steps (1024 bytes) to the next group
+// of 8, 64 steps (8192 bytes) to the next 64 features.
+MOE_DEV uint64_t mn_desc(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(8192u >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+
+// kind::f16, fp32 accumulation, M = 256 over the pair, N = 256: operand format (1 bf16,
+// 0 fp16) at [7,10) and [10,13), MN-major A / B at bits 15 / 16.
+template <int MODE>
+MOE_DEV uint32_t vocab_idesc(int dtype) {
+  const uint32_t f = dtype == MOE_ELEM_BF16 ? 1u : 0u;
+  return (1u << 4) | (f << 7) | (f << 10) | (MODE == VOCAB_DW ? 1u << 15 : 0u) |
+         (MODE == VOCAB_DX || MODE == VOCAB_DW ? 1u << 16 : 0u) | (32u << 17) | (16u << 24);
+}
+
+// 2^x in the hardware's approximation (2 ulp), 0 below the normal range.
+MOE_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+struct VocabTile {
+  int m0, n0;       // first row and column of the product
+  int k0, klen;     // reduction
+  int split;
+};
+
+// LOSS, DZ: rows x vocabulary of the piece; DX: rows x d, the piece's reduction in
+// `splits` parts; DW: vocabulary of the piece x d.
+template <int MODE>
+struct VocabTiles {
+  int nm, nn, splits, k, per, total;
+  MOE_DEV VocabTiles(const VocabArgs &a, int count) {
+    nm = ((MODE == VOCAB_DW ? a.wp : count) + 255) >> 8;
+    nn = ((MODE == VOCAB_LOSS || MODE == VOCAB_DZ ? a.wp : a.d) + 255) >> 8;
+    splits = MODE == VOCAB_DX ? a.splits : 1;
+    k = MODE == VOCAB_DX ? a.wp : MODE == VOCAB_DW ? count : a.d;
+    per = ((k + 127) / 128 + splits - 1) / splits * 128;
+    total = nm * nn * splits;
+  }
+  MOE_DEV VocabTile at(int u) const {
+    VocabTile t;
+    const int plane = nm * nn;
+    t.split = u / plane;
+    u -= t.split * plane;
+    const int band = u / (kBand * nn), in = u - band * kBand * nn;
+    const int high = nm - band * kBand < kBand ? nm - band * kBand : kBand;
+    t.m0 = (band * kBand + in % high) * 256;
+    t.n0 = in / high * 256;
+    t.k0 = t.split * per;
+    t.klen = k - t.k0 < per ? k - t.k0 : per;
+    if (t.klen < 0) t.klen = 0;
+    return t;
+  }
+};
+
+// A piece of 32 rows x 128 bytes (lane = row) into 128-byte-swizzled shared memory, from
+// where TMA takes it.
+MOE_DEV void stage_rows(const uint32_t *w, uint8_t *buf, int lane) {
+  if (lane == 0) bulk_wait_read<0>();  // the last piece has left the buffer
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<uint4 *>(buf + lane * 128 + ((j ^ (lane & 7)) * 16)) =
+        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// The same piece element by element, for matrices whose rows are no whole 16-byte
+// pieces: each store takes neighbouring columns of one row.
+template <typename O>
+MOE_DEV void put_elements(const uint32_t *w, uint8_t *buf, O *out, long ld, int rows, int cols, bool add, int lane) {
+  constexpr int COLS = 128 / sizeof(O);
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    *reinterpret_cast<uint4 *>(buf + lane * 128 + ((j ^ (lane & 7)) * 16)) =
+        make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  __syncwarp();
+  for (int r = 0; r < 32 && r < rows; ++r)
+#pragma unroll
+    for (int c = lane; c < COLS; c += 32) {
+      const int byte = c * static_cast<int>(sizeof(O));
+      const O v = *reinterpret_cast<const O *>(buf + r * 128 + (((byte >> 4) ^ (r & 7)) * 16) + (byte & 15));
+      if (c < cols) {
+        if constexpr (sizeof(O) == 4) out[r * ld + c] = add ? out[r * ld + c] + v : v;
+        else out[r * ld + c] = v;
+      }
+    }
+}
+
+// T: the operands' type; WIDE: fp32 dw.
+template <int MODE, typename T, bool WIDE>
+__global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_constant__ VocabMaps maps, const VocabArgs g) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  uint8_t *staging = smem + kStages * kStageBytes;
+  uint64_t *full = reinterpret_cast<uint64_t *>(staging + kEpilogueWarps * kStaging);
+  uint64_t *empty = full + kStages;
+  uint64_t *tfull = empty + kStages;
+  uint64_t *tempty = tfull + 2;
+  uint64_t *done = tempty + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 2 * 32 * kEpilogueWarps);  // epilogue threads of both CTAs
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, 512);
+    tmem_relinquish_pair();
+    tc_fence_before();
+  }
+  pdl_wait();  // all that the launches in front have written, the rows that count among it
+  pdl_trigger();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers exist before any cross-CTA signal
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int count = *reinterpret_cast<const volatile int *>(g.count);
+  const VocabTiles<MODE> tiles(g, count);
+
+  if (warp == 0) {
+    // ------------------------------------------------ TMA producer (both CTAs)
+    if (lane == 0) {
+      fence_proxy_async_global();  // copies and dz were written by ordinary stores and by TMA
+      int stage = 0;
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int u = pair; u < tiles.total && ok && !*abort_flag; u += pairs) {
+        const VocabTile t = tiles.at(u);
+        const int ar = t.m0 + static_cast<int>(rank) * 128, br = t.n0 + static_cast<int>(rank) * 128;
+        for (int kb = 0; kb < t.klen; kb += 64 * kBlocks) {
+          if (!mbar_wait(&empty[stage], ph ^ 1u, abort_flag, g.status)) {
+            ok = false;
+            break;
+          }
+          const int blocks = t.klen - kb > 64 ? kBlocks : 1;
+          if (leader) mbar_arrive_expect_tx(&full[stage], 2u * blocks * kBlockBytes);
+          const uint32_t bar = peer_smem(smem_u32(&full[stage]), 0);
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b) {
+            if (b >= blocks) break;
+            uint8_t *sa = smem + stage * kStageBytes + b * kBlockBytes, *sb = sa + 16384;
+            const int k = t.k0 + kb + 64 * b;
+            if constexpr (MODE == VOCAB_DW) {
+              tma_load_2d_pair(&maps.a, bar, sa, ar, k);
+              tma_load_2d_pair(&maps.a, bar, sa + 8192, ar + 64, k);
+            } else {
+              tma_load_2d_pair(&maps.a, bar, sa, k, ar);
+            }
+            if constexpr (MODE == VOCAB_DX || MODE == VOCAB_DW) {
+              const int kr = MODE == VOCAB_DX ? g.v0 + k : k;
+              tma_load_2d_pair(&maps.b, bar, sb, br, kr);
+              tma_load_2d_pair(&maps.b, bar, sb + 8192, br + 64, kr);
+            } else {
+              tma_load_2d_pair(&maps.b, bar, sb, k, g.v0 + br);
+            }
+          }
+          if (++stage == kStages) {
+            stage = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA issuer (pair leader)
+    if (leader && lane == 0) {
+      int stage = 0, acc = 0;
+      uint32_t ph = 0, aph = 0;
+      bool ok = true;
+      const uint32_t idesc = vocab_idesc<MODE>(g.dtype);
+      for (int u = pair; u < tiles.total && ok; u += pairs) {
+        const VocabTile t = tiles.at(u);
+        if (t.klen == 0) continue;
+        if (!mbar_wait(&tempty[acc], aph ^ 1u, abort_flag, g.status)) break;
+        tc_fence_after();
+        const uint32_t dt = tmem + static_cast<uint32_t>(acc * 256);
+        for (int kb = 0; kb < t.klen; kb += 64 * kBlocks) {
+          if (!mbar_wait(&full[stage], ph, abort_flag, g.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa0 = smem_u32(smem + stage * kStageBytes);
+          const int left = t.klen - kb;  // steps past the end hold zeros in both operands
+#pragma unroll
+          for (int k = 0; k < 4 * kBlocks; ++k) {
+            if (k * 16 < left) {
+              const uint32_t sa = sa0 + (k >> 2) * kBlockBytes, sb = sa + 16384;
+              const uint64_t ad = MODE == VOCAB_DW ? mn_desc(sa + 2048 * (k & 3)) : sw128_desc(sa + 32 * (k & 3));
+              const uint64_t bd = MODE == VOCAB_DX || MODE == VOCAB_DW ? mn_desc(sb + 2048 * (k & 3))
+                                                                      : sw128_desc(sb + 32 * (k & 3));
+              mma_bf16_pair(dt, ad, bd, idesc, (kb | k) ? 1u : 0u);
+            }
+          }
+          mma_commit_pair_mc(&empty[stage], 3);
+          if (++stage == kStages) {
+            stage = 0;
+            ph ^= 1u;
+          }
+        }
+        if (!ok) break;
+        mma_commit_pair_mc(&tfull[acc], 3);
+        if (++acc == 2) {
+          acc = 0;
+          aph ^= 1u;
+        }
+      }
+      mma_commit_pair_mc(done, 1);
+      volatile int no_abort = 0;
+      mbar_wait(done, 0, &no_abort, g.status);
+    }
+  } else {
+    // ------------------------------------------------ epilogue (warps 2..9, both CTAs)
+    const int q = warp & 3, half = (warp - 2) >> 2;  // accumulator rows; which half of its columns
+    uint8_t *buf = staging + (warp - 2) * kStaging;
+    int acc = 0;
+    uint32_t aph = 0;
+    for (int u = pair; u < tiles.total; u += pairs) {
+      const VocabTile t = tiles.at(u);
+      const int row0 = t.m0 + static_cast<int>(rank) * 128 + q * 32, row = row0 + lane;
+      const int col0 = t.n0 + half * 128;
+      const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * 256 + half * 128);
+      if (t.klen > 0) {
+        if (!mbar_wait(&tfull[acc], aph, abort_flag, g.status)) break;
+        tc_fence_after();
+      }
+      const uint32_t tempty_addr = smem_u32(&tempty[acc]);
+      auto release = [&]() {
+        tc_fence_before();
+        if (leader) mbar_arrive(&tempty[acc]);
+        else mbar_arrive_remote(peer_smem(tempty_addr, 0));
+      };
+      if constexpr (MODE == VOCAB_LOSS) {
+        // d >= 1: klen > 0
+        const int hit = g.label[row] - (g.v0 + col0);  // rows are padded to whole tiles
+        float m = -__int_as_float(0x7f800000), s = 0.f;
+#pragma unroll
+        for (int j = 0; j < 128; j += 32) {
+          uint32_t r[32];
+          tmem_ld32_async(tb + j, r);
+          tmem_ld_wait();
+          reg_fence<32>(r);
+          if (j == 96) release();
+          float *z = reinterpret_cast<float *>(r);
+          const int left = g.wp - (col0 + j);  // columns that exist
+          if (left < 32) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i >= left) z[i] = -__int_as_float(0x7f800000);
+          }
+          if (__any_sync(0xffffffffu, hit >= j && hit < j + 32)) {
+            float v = 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (hit == j + i) v = z[i];
+            if (hit >= j && hit < j + 32) g.hit[row] = v;
+          }
+          float top = z[0];
+#pragma unroll
+          for (int i = 1; i < 32; ++i) top = fmaxf(top, z[i]);
+          const float now = fmaxf(m, top);
+          // a maximum that is not finite: exponentials from zero, as the join expects
+          const float from = fabsf(now) <= 3.402823466e38f ? now : 0.f;
+          const float was = fabsf(m) <= 3.402823466e38f ? m : 0.f;
+          const float base = from * kLog2e;
+          float s0 = s == 0.f ? 0.f : s * ex2(was * kLog2e - base), s1 = 0.f;
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            s0 += ex2(fmaf(z[i], kLog2e, -base));
+            s1 += ex2(fmaf(z[i + 1], kLog2e, -base));
+          }
+          s = s0 + s1;
+          m = now;
+        }
+        if (row < count) g.part[static_cast<long>(row) * g.parts + (t.n0 >> 7) + half] = make_float2(m, s);
+      } else if constexpr (MODE == VOCAB_DZ) {
+        const float cp = g.coef_p[row], cl = g.coef_l[row], base = g.base[row];
+        const int hit = g.label[row] - (g.v0 + col0);
+#pragma unroll
+        for (int j = 0; j < 128; j += 64) {
+          uint32_t r[64], w[32];
+          tmem_ld32_async(tb + j, r);
+          tmem_ld32_async(tb + j + 32, r + 32);
+          tmem_ld_wait();
+          reg_fence<64>(r);
+          if (j == 64) release();
+          float *z = reinterpret_cast<float *>(r);
+          // no coefficient, no term: what z holds there does not matter
+#pragma unroll
+          for (int i = 0; i < 64; ++i) z[i] = cp == 0.f ? 0.f : cp * ex2(fmaf(z[i], kLog2e, -base));
+          if (__any_sync(0xffffffffu, hit >= j && hit < j + 64)) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (hit == j + i) z[i] -= cl;
+          }
+#pragma unroll
+          for (int i = 0; i < 32; ++i) w[i] = Elem<T>::pack2(z[2 * i], z[2 * i + 1]);
+          if (col0 + j >= g.wp) continue;
+          stage_rows(w, buf, lane);
+          if (lane == 0) {
+            tma_store_2d(&maps.out, buf, col0 + j, row0);
+            bulk_commit();
+          }
+        }
+      } else if constexpr (MODE == VOCAB_DX) {
+#pragma unroll 1
+        for (int j = 0; j < 128; j += 32) {
+          uint32_t r[32];
+          if (t.klen > 0) {
+            tmem_ld32_async(tb + j, r);
+            tmem_ld_wait();
+            reg_fence<32>(r);
+            if (j == 96) release();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) r[i] = 0;
+          }
+          if (col0 + j >= g.d || row0 >= count || (t.klen == 0 && g.v0 > 0)) continue;
+          stage_rows(r, buf, lane);
+          if (lane == 0) {
+            if (g.v0 > 0) tma_add_3d(&maps.out, buf, col0 + j, row0, t.split);
+            else tma_store_3d(&maps.out, buf, col0 + j, row0, t.split);
+            bulk_commit();
+          }
+        }
+      } else {
+        constexpr int STEP = WIDE ? 32 : 64;  // columns of a 128-byte piece
+        const float scale = *reinterpret_cast<const volatile float *>(g.scale);
+#pragma unroll 1
+        for (int j = 0; j < 128; j += STEP) {
+          uint32_t r[STEP], w[32];
+          if (t.klen > 0) {
+            tmem_ld32_async(tb + j, r);
+            if (!WIDE) tmem_ld32_async(tb + j + 32, r + STEP - 32);
+            tmem_ld_wait();
+            reg_fence<STEP>(r);
+            if (j + STEP == 128) release();
+          } else {
+#pragma unroll
+            for (int i = 0; i < STEP; ++i) r[i] = 0;
+          }
+          if (row0 >= g.wp || col0 + j >= g.d || (t.klen == 0 && g.accumulate)) continue;
+          float *v = reinterpret_cast<float *>(r);
+          if (t.klen > 0)
+#pragma unroll
+            for (int i = 0; i < STEP; ++i) v[i] *= scale;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if constexpr (WIDE) w[i] = r[i];
+            else w[i] = Elem<T>::pack2(v[2 * i], v[2 * i + 1]);
+          if (g.vec_dw) {
+            stage_rows(w, buf, lane);
+            if (lane == 0) {
+              if (WIDE && g.accumulate) tma_add_2d(&maps.out, buf, col0 + j, g.v0 + row0);
+              else tma_store_2d(&maps.out, buf, col0 + j, g.v0 + row0);
+              bulk_commit();
+            }
+          } else {
+            using O = typename std::conditional<WIDE, float, T>::type;
+            put_elements<O>(w, buf, static_cast<O *>(g.dw) + static_cast<long>(g.v0 + row0) * g.d + col0 + j, g.d,
+                            g.wp - row0, g.d - col0 - j, g.accumulate != 0, lane);
+          }
+        }
+      }
+      if (t.klen > 0 && ++acc == 2) {
+        acc = 0;
+        aph ^= 1u;
+      }
+    }
+    if (MODE != VOCAB_LOSS && lane == 0) bulk_wait<0>();
+  }
+
+  __syncthreads();
+  cluster_sync();  // no CTA leaves while its peer may still signal it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <int MODE, typename T, bool WIDE>
+int vocab_clusters_query() {
+  const auto kernel = vocab_tc_kernel<MODE, T, WIDE>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem)) != cudaSuccess)
+    return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
+}
+
+template <int MODE, typename T, bool WIDE>
+cudaError_t launch_one(const VocabMaps &maps, const VocabArgs &g, long units, cudaStream_t s) {
+  static int memo[64] = {};
+  const int most = per_device_memo(memo, vocab_clusters_query<MODE, T, WIDE>);
+  if (most <= 0) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * static_cast<unsigned>(units < most ? units : most), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, vocab_tc_kernel<MODE, T, WIDE>, maps, g);
+}
+
+template <int MODE>
+cudaError_t launch_mode(const VocabMaps &m, const VocabArgs &g, long units, cudaStream_t s) {
+  const bool bf = g.dtype == MOE_ELEM_BF16;
+  if constexpr (MODE == VOCAB_DW) {
+    if (g.grad_dtype == MOE_ELEM_FP32)
+      return bf ? launch_one<MODE, __nv_bfloat16, true>(m, g, units, s) : launch_one<MODE, __half, true>(m, g, units, s);
+  }
+  return bf ? launch_one<MODE, __nv_bfloat16, false>(m, g, units, s) : launch_one<MODE, __half, false>(m, g, units, s);
+}
+
+bool map_2d(CUtensorMap *m, int elem, const void *p, long cols, long rows, long ld, uint32_t box_cols, uint32_t box_rows) {
+  const uint64_t e = elem_bytes(elem);
+  const uint64_t dims[2] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows > 0 ? rows : 1)};
+  const uint64_t strides[1] = {static_cast<uint64_t>(ld) * e};
+  const uint32_t box[2] = {box_cols, box_rows};
+  return host_encode_map(m, elem, p, 2, dims, strides, box);
+}
+
+}  // namespace
+
+cudaError_t launch_vocab_tc(const VocabArgs &g, int mode, cudaStream_t s) {
+  VocabMaps m = {};
+  const void *w = g.pad_w ? g.ws_w : g.w;
+  const long ld_w = g.pad_w ? g.ld_ws_w : g.ld_w;
+  const long rt = (g.rows + 255L) / 256, vt = (g.wp + 255L) / 256, dt = (g.d + 255L) / 256;
+  if (mode == VOCAB_LOSS || mode == VOCAB_DZ) {
+    if (!map_2d(&m.a, g.dtype, g.xs, g.d, g.rows, g.ld_xs, 64, 128) || !map_2d(&m.b, g.dtype, w, g.d, g.V, ld_w, 64, 128))
+      return cudaErrorInvalidValue;
+    if (mode == VOCAB_LOSS) {
+      HostTrace t("vocab_logits", s);
+      return launch_mode<VOCAB_LOSS>(m, g, rt * vt, s);
+    }
+    if (!map_2d(&m.out, g.dtype, g.dz, g.wp, g.rows, g.width, 64, 32)) return cudaErrorInvalidValue;
+    HostTrace t("vocab_dlogits", s);
+    return launch_mode<VOCAB_DZ>(m, g, rt * vt, s);
+  }
+  if (mode == VOCAB_DX) {
+    const uint64_t dims[3] = {static_cast<uint64_t>(g.ld_sum), static_cast<uint64_t>(g.rows), static_cast<uint64_t>(g.splits)};
+    const uint64_t strides[2] = {static_cast<uint64_t>(g.ld_sum) * 4, static_cast<uint64_t>(g.ld_sum) * 4 * g.rows};
+    const uint32_t box[3] = {32, 32, 1};
+    if (!map_2d(&m.a, g.dtype, g.dz, g.wp, g.rows, g.width, 64, 128) ||
+        !map_2d(&m.b, g.dtype, w, g.d, g.V, ld_w, 64, 64) || !host_encode_map(&m.out, MOE_ELEM_FP32, g.sum, 3, dims, strides, box))
+      return cudaErrorInvalidValue;
+    HostTrace t("vocab_dgrad", s);
+    return launch_mode<VOCAB_DX>(m, g, rt * dt * g.splits, s);
+  }
+  const bool wide = g.grad_dtype == MOE_ELEM_FP32;
+  if (!map_2d(&m.a, g.dtype, g.dz, g.wp, g.rows, g.width, 64, 64) || !map_2d(&m.b, g.dtype, g.xs, g.d, g.rows, g.ld_xs, 64, 64))
+    return cudaErrorInvalidValue;
+  if (g.vec_dw && !map_2d(&m.out, g.grad_dtype, g.dw, g.d, g.V, g.d, wide ? 32 : 64, 32)) return cudaErrorInvalidValue;
+  HostTrace t("vocab_wgrad", s);
+  return launch_mode<VOCAB_DW>(m, g, vt * dt, s);
+}
+
+}  // namespace moe

@@ -10,9 +10,11 @@ the MXFP8 quantisers, so the masters receive the gradients the library
 computes for the quantised layer.  Each training forward keeps its activations
 in its own buffer, so several forwards may precede their backwards.
 
-Around the layer: GroupedLinear (ragged products grouped by expert), BlockNorm
-(the norms around a block with its gate and residual scale) and TokenEmbedding,
-each an nn.Module over an autograd.Function over block.py.
+Around the layer: GroupedLinear (ragged products grouped by expert),
+GatedLinear (the same with a gate and its activation), BlockNorm (the norms
+around a block with its gate and residual scale), TokenEmbedding and VocabLoss
+(the loss over a vocabulary without its logits), each an nn.Module over an
+autograd.Function over block.py; clip_gradients for all of them.
 
 Gradients have no second derivative: under create_graph they refuse one.
 """
@@ -158,6 +160,42 @@ class GroupedLinear(torch.nn.Module):
         return GroupedFunction.apply(x, self.weight, offsets)
 
 
+class GatedFunction(torch.autograd.Function):
+    """h[r] = act(x[r] w[e][:m]^T) (x[r] w[e][m:]^T) for the rows r of expert e (block.gated_forward)."""
+
+    @staticmethod
+    def forward(ctx, x, w, offsets, act):
+        h, gu = block.gated_forward(x, w, offsets, act=act, need_gu=any(ctx.needs_input_grad[:2]))
+        ctx.act = act
+        ctx.save_for_backward(x, w, offsets, gu)
+        return h
+
+    @staticmethod
+    def backward(ctx, dh):
+        x, w, offsets, gu = ctx.saved_tensors
+        need_dx, need_dw = ctx.needs_input_grad[:2]
+        dx = dw = None
+        if need_dx or need_dw:
+            dx, dw = block.gated_backward(dh, x, w, offsets, gu, act=ctx.act, need_dx=need_dx, need_dw=need_dw)
+        return _first_order(dx, dh, x, w), _first_order(dw, dh, x, w), None, None
+
+
+class GatedLinear(torch.nn.Module):
+    """The first half of E gated feed-forward blocks K -> m over expert-sorted rows:
+    forward(x [rows, K], offsets int32 [E + 1]) -> act(x W_g^T) (x W_u^T) [rows, m]; rows
+    outside the offsets give zeros and take no gradient.  Weight [E, 2m, K] bf16 (or
+    fp16), an expert's W_g above its W_u; act "silu", "gelu", "gelu_tanh" or "relu".  A
+    GroupedLinear(E, N, m) behind it makes the block whole."""
+
+    def __init__(self, E, m, K, act="silu", dtype=torch.bfloat16, device="cuda"):
+        super().__init__()
+        self.weight = torch.nn.Parameter(torch.empty(E, 2 * m, K, dtype=dtype, device=device).normal_(0.0, K ** -0.5))
+        self.act = act
+
+    def forward(self, x, offsets):
+        return GatedFunction.apply(x, self.weight, offsets, self.act)
+
+
 class BlockNormFunction(torch.autograd.Function):
     """(z, h) of block.norm_forward; z is None without need_z, h without pre."""
 
@@ -238,3 +276,66 @@ class TokenEmbedding(torch.nn.Module):
 
     def forward(self, ids):
         return EmbeddingFunction.apply(ids, self.weight, self.scale)
+
+
+class VocabLossFunction(torch.autograd.Function):
+    """(loss, lse) of every row (block.vocab_loss_forward)."""
+
+    @staticmethod
+    def forward(ctx, x, w, labels):
+        loss, lse = block.vocab_loss_forward(x, w, labels)
+        ctx.save_for_backward(x, w, labels, lse)
+        ctx.set_materialize_grads(False)
+        return loss, lse
+
+    @staticmethod
+    def backward(ctx, dloss, dlse):
+        x, w, labels, lse = ctx.saved_tensors
+        need_dx, need_dw = ctx.needs_input_grad[:2]
+        dx = dw = None
+        if (need_dx or need_dw) and not (dloss is None and dlse is None):
+            dx, dw = block.vocab_loss_backward(dloss, x, w, labels, lse, dlse=dlse, need_dx=need_dx, need_dw=need_dw)
+        return _first_order(dx, dloss, dlse, x, w), _first_order(dw, dloss, dlse, x, w), None
+
+
+class VocabLoss(torch.nn.Module):
+    """Softmax cross entropy straight from the last hidden rows: forward(x [T, d],
+    labels [T]) -> (loss [T], lse [T]) fp32, the logits x W^T never in memory.  A row
+    whose label lies outside [0, V) (padding) gives zeros and takes no gradient; the
+    mean over the others is loss.sum() / their number.  lse is there for a term in the
+    logits' size (lse.square()).  Weight [V, d], or the given one (a TokenEmbedding's)."""
+
+    def __init__(self, V, d, weight=None, dtype=torch.bfloat16, device="cuda"):
+        super().__init__()
+        if weight is None:
+            weight = torch.nn.Parameter(torch.empty(V, d, dtype=dtype, device=device).normal_(0.0, d ** -0.5))
+        if weight.shape != (V, d):
+            raise ValueError("weight has shape %s, expected [%d, %d]" % (tuple(weight.shape), V, d))
+        self.weight = weight
+
+    def forward(self, x, labels):
+        return VocabLossFunction.apply(x, self.weight, labels)
+
+
+def clip_gradients(parameters, max_norm, masters=None, eps=1e-6):
+    """Scales the gradients of `parameters` so that their common norm is at most max_norm
+    (block.grad_clip) and returns the norm of before, a 0-d tensor.  With `masters`, a
+    list of fp32 tensors in the parameters' order, the gradients are left alone and the
+    masters' .grad get the scaled ones.  Parameters without a gradient are left out
+    (their master's .grad becomes None)."""
+    parameters = list(parameters)
+    grads = [p.grad for p in parameters if p.grad is not None]
+    if masters is None:
+        return block.grad_clip(grads, max_norm, eps=eps)
+    masters = list(masters)
+    if len(masters) != len(parameters):
+        raise ValueError("%d masters for %d parameters" % (len(masters), len(parameters)))
+    out = []
+    for p, m in zip(parameters, masters):
+        if p.grad is None:
+            m.grad = None
+            continue
+        if m.grad is None or m.grad.stride() != p.grad.stride():
+            m.grad = torch.empty_like(p.grad, dtype=torch.float32)
+        out.append(m.grad)
+    return block.grad_clip(grads, max_norm, out=out, eps=eps)
