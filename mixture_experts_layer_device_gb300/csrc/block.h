@@ -65,6 +65,7 @@ struct GroupedArgs {
   void *h;
   long ld_h;
   int act;  // moe_act
+  bool vec_h, by_16;  // tensor-core path: h's rows are whole 16-byte pieces; m is a multiple of 16
   bool zeroed;   // weight gradient: launch_grouped_zero writes the experts without rows
   bool chained;  // tensor-core path: starts before the launch in front has ended (dgrad and wgrad of one call)
   bool vec_out;  // tensor-core path: the output's rows are whole 16-byte pieces
@@ -87,6 +88,7 @@ cudaError_t launch_grouped_plain(const GroupedArgs &g, int dir, bool first, cuda
 cudaError_t launch_gated_plain(const GroupedArgs &g, cudaStream_t s);
 // Forward of a few rows (no plan needed): 16-byte aligned rows of x and w.
 cudaError_t launch_grouped_few(const GroupedArgs &g, cudaStream_t s);
+cudaError_t launch_gated_few(const GroupedArgs &g, cudaStream_t s);
 // Puts the experts in order (g.order) for launch_grouped_zero; the tensor-core
 // path's own launch does it there.
 cudaError_t launch_grouped_order(const GroupedArgs &g, cudaStream_t s);
@@ -167,10 +169,10 @@ struct VocabArgs {
   float *scale;          // what the backward's products are multiplied by in the end
   int *row, *place;      // [pad] row of a place, [rows] place of a row (-1: none)
   int *label;            // [pad]
-  float *hit;            // forward: [pad] the label's logit
+  float *hit;            // [pad] the label's logit; backward: its dz
   float2 *part;          // forward: [pad][parts] (maximum, sum of exponentials) of 128 logits
   int parts;
-  float *coef_p, *coef_l, *base;  // backward: [pad] dz = coef_p 2^(z log2 e - base) - coef_l [label]
+  float *coef_p, *coef_l, *base;  // backward: [pad] dz = coef_p 2^(z log2 e - base), less coef_l for the label
   void *xs;              // [rows][ld_xs] the copy of x
   void *ws_w;            // the padded copy of w where TMA cannot address it (else unused)
   void *dz;              // backward: [rows][width] one piece of the logits' gradient

@@ -64,7 +64,7 @@ GroupedPads grouped_pads(const moe::GroupedArgs &g, int dir) {
   GroupedPads p;
   p.w = dir != moe::GROUPED_WGRAD && (g.ld_w % 8 != 0 || g.ld_e % 8 != 0);
   p.x = dir != moe::GROUPED_DGRAD && g.ld_x % 8 != 0;
-  p.dy = dir != moe::GROUPED_FWD && g.ld_y % 8 != 0;
+  p.dy = (dir == moe::GROUPED_DGRAD || dir == moe::GROUPED_WGRAD) && g.ld_y % 8 != 0;
   const double work = static_cast<double>(g.rows) * g.N * g.K;
   const double copied = (p.w ? static_cast<double>(g.E) * g.N * g.K : 0.0) + (p.x ? static_cast<double>(g.rows) * g.K : 0.0) +
                         (p.dy ? static_cast<double>(g.rows) * g.N : 0.0);
@@ -122,7 +122,7 @@ Padded grouped_tensor(const moe::GroupedArgs &g, int dir, uint8_t *ws, moe::Grou
   if (g.rows == 0) return {false, MOE_OK};
   const long widest = ((g.N > g.K ? g.N : g.K) + 255L) / 256;
   if ((g.rows / 256 + 2L * g.E) * widest >= (1L << 30)) return {false, MOE_OK};  // tiles are counted in 32 bits
-  const bool uw = dir != moe::GROUPED_WGRAD, ux = dir != moe::GROUPED_DGRAD, uy = dir != moe::GROUPED_FWD;
+  const bool uw = dir != moe::GROUPED_WGRAD, ux = dir != moe::GROUPED_DGRAD, uy = dir == moe::GROUPED_DGRAD || dir == moe::GROUPED_WGRAD;
   const GroupedPads p = grouped_pads(g, dir);
   if ((p.w || p.x || p.dy) && !p.worth) return {false, MOE_OK};
   if ((uw && !p.w && !aligned(g.w, 16)) || (ux && !p.x && !aligned(g.x, 16)) || (uy && !p.dy && !aligned(g.dy, 16)))
@@ -151,6 +151,12 @@ Padded grouped_tensor(const moe::GroupedArgs &g, int dir, uint8_t *ws, moe::Grou
     *have_dy = true;
   }
   if (e != cudaSuccess) return {false, MOE_ERR_CUDA};
+  if (dir == moe::GROUPED_GATED) {
+    t->vec_out = tma_rows(g.y, g.ld_y) && g.N % 16 == 0;
+    t->vec_h = tma_rows(g.h, g.ld_h) && g.N % 16 == 0;
+    t->by_16 = g.N % 32 == 0;
+    return {true, MOE_OK};
+  }
   if (dir == moe::GROUPED_FWD) t->vec_out = tma_rows(g.y, g.ld_y) && g.N % 8 == 0;
   else if (dir == moe::GROUPED_DGRAD) t->vec_out = tma_rows(g.dx, g.ld_x) && g.K % 8 == 0;
   else t->vec_out = aligned(g.dw, 16) && g.K % 8 == 0;
@@ -361,7 +367,12 @@ int moe_gated_forward(const moe_gated_config *cfg, const void *x, const void *w,
   g.h = h;
   g.y = gu;
   g.out_dtype = g.dtype;
-  return status_of(moe::launch_gated_plain(g, stream));
+  if (grouped_few(g)) return status_of(moe::launch_gated_few(g, stream));
+  bool have_dy = false;
+  moe::GroupedArgs t;
+  const Padded p = grouped_tensor(g, moe::GROUPED_GATED, static_cast<uint8_t *>(ws), &t, &have_dy, stream);
+  if (p.rc != MOE_OK) return p.rc;
+  return status_of(p.ok ? moe::launch_grouped_tc(t, moe::GROUPED_GATED, sms, stream) : moe::launch_gated_plain(g, stream));
 }
 
 int moe_gated_backward(const moe_gated_config *cfg, const void *dh, const void *x, const void *w, const int32_t *offsets,

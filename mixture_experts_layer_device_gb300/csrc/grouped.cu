@@ -326,7 +326,17 @@ cudaError_t plain_type(const GroupedArgs &g, int dir, bool planned, cudaStream_t
 // work, the others leave at once.
 constexpr int FEW_F = 4, FEW_R = 4, FEW_WARPS = 4;
 
-template <typename T, int R>
+// GATED: the weights' rows are FEW_F / 2 of the gate and the same of the up projection.
+template <bool GATED>
+MOE_DEV int few_row(const GroupedArgs &g, int f) {
+  return GATED && f >= FEW_F / 2 ? (g.N >> 1) + f - FEW_F / 2 : f;
+}
+template <bool GATED>
+MOE_DEV bool few_has(int f, int nf) {
+  return (GATED ? f % (FEW_F / 2) : f) < nf;
+}
+
+template <typename T, int R, bool GATED>
 MOE_DEV void few_dot(const GroupedArgs &g, const T *x, const T *w, int nf, float acc[R][FEW_F]) {
   const int lane = threadIdx.x & 31, chunks = g.K >> 3;
 #pragma unroll
@@ -341,7 +351,7 @@ MOE_DEV void few_dot(const GroupedArgs &g, const T *x, const T *w, int nf, float
 #pragma unroll
       for (int f = 0; f < FEW_F; ++f) {
         q[u][f] = make_uint4(0, 0, 0, 0);
-        if (c0 + 32 * u < chunks && f < nf) q[u][f] = ld_stream(w + f * g.ld_w + (c0 + 32 * u) * 8L);
+        if (c0 + 32 * u < chunks && few_has<GATED>(f, nf)) q[u][f] = ld_stream(w + few_row<GATED>(g, f) * g.ld_w + (c0 + 32 * u) * 8L);
       }
 #pragma unroll
     for (int u = 0; u < UNROLL; ++u) {
@@ -373,8 +383,8 @@ template <typename T, int R>
 MOE_DEV void few_rows(const GroupedArgs &g, int row, int e, int n0, int nf) {
   const int lane = threadIdx.x & 31;
   float acc[R][FEW_F];
-  few_dot<T, R>(g, static_cast<const T *>(g.x) + row * g.ld_x,
-                static_cast<const T *>(g.w) + e * g.ld_e + n0 * g.ld_w, nf, acc);
+  few_dot<T, R, false>(g, static_cast<const T *>(g.x) + row * g.ld_x,
+                       static_cast<const T *>(g.w) + e * g.ld_e + n0 * g.ld_w, nf, acc);
   // lane r * FEW_F + f stores element (r, f)
   float v = 0.f;
 #pragma unroll
@@ -387,12 +397,38 @@ MOE_DEV void few_rows(const GroupedArgs &g, int row, int e, int n0, int nf) {
     store_elem<T>(g.y, (row + r) * g.ld_y + n0 + f, v, g.out_dtype == MOE_ELEM_FP32, false);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(FEW_WARPS * 32) grouped_few_kernel(const GroupedArgs g) {
-  const int row = blockIdx.y;
+template <typename T, int R, int ACT>
+MOE_DEV void few_gated_rows(const GroupedArgs &g, int row, int e, int n0, int nf) {
+  const int lane = threadIdx.x & 31, half = g.N >> 1;
+  float acc[R][FEW_F];
+  few_dot<T, R, true>(g, static_cast<const T *>(g.x) + row * g.ld_x,
+                      static_cast<const T *>(g.w) + e * g.ld_e + n0 * g.ld_w, nf, acc);
+  // lane r * FEW_F / 2 + f stores feature f of row r
+  float gate = 0.f, up = 0.f;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int f = 0; f < FEW_F / 2; ++f)
+      if (lane == r * (FEW_F / 2) + f) {
+        gate = acc[r][f];
+        up = acc[r][f + FEW_F / 2];
+      }
+  const int r = lane / (FEW_F / 2), f = lane % (FEW_F / 2);
+  if (r < R && f < nf) {
+    static_cast<T *>(g.h)[(row + r) * g.ld_h + n0 + f] = Elem<T>::from(act_value<ACT>(gate) * up);
+    if (g.y) {
+      T *y = static_cast<T *>(g.y) + (row + r) * g.ld_y + n0 + f;
+      y[0] = Elem<T>::from(gate);
+      y[half] = Elem<T>::from(up);
+    }
+  }
+}
+
+// The expert of a row, by the whole block; `lo`, `hi`: its rows (not around the row where
+// that belongs to no expert).
+MOE_DEV int few_expert(const GroupedArgs &g, int row, int &lo, int &hi) {
   if (blockIdx.x == 0 && blockIdx.y == 0) {
     bool bad = false;
-    int lo, hi;
     for (int e = threadIdx.x; e < g.E; e += blockDim.x) bad |= !group_rows(g, e, lo, hi);
     const int any = __syncthreads_or(bad);
     if (threadIdx.x == 0) *g.status = any ? kStatusBounds : 0;
@@ -404,8 +440,15 @@ __global__ void __launch_bounds__(FEW_WARPS * 32) grouped_few_kernel(const Group
     before += __syncthreads_count(e < g.E && __ldg(g.offsets + e + 1) <= row);
   }
   const int e = before < g.E ? before : g.E - 1;
-  int lo, hi;
   group_rows(g, e, lo, hi);
+  return e;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(FEW_WARPS * 32) grouped_few_kernel(const GroupedArgs g) {
+  const int row = blockIdx.y;
+  int lo, hi;
+  const int e = few_expert(g, row, lo, hi);
   const int n0 = (blockIdx.x * FEW_WARPS + (threadIdx.x >> 5)) * FEW_F;
   if (n0 >= g.N) return;
   const int nf = g.N - n0 < FEW_F ? g.N - n0 : FEW_F;
@@ -421,6 +464,47 @@ __global__ void __launch_bounds__(FEW_WARPS * 32) grouped_few_kernel(const Group
     case 3: few_rows<T, 3>(g, row, e, n0, nf); break;
     default: few_rows<T, 4>(g, row, e, n0, nf); break;
   }
+}
+
+template <typename T, int ACT>
+__global__ void __launch_bounds__(FEW_WARPS * 32) gated_few_kernel(const GroupedArgs g) {
+  const int row = blockIdx.y, half = g.N >> 1;
+  int lo, hi;
+  const int e = few_expert(g, row, lo, hi);
+  const int n0 = (blockIdx.x * FEW_WARPS + (threadIdx.x >> 5)) * (FEW_F / 2);
+  if (n0 >= half) return;
+  const int nf = half - n0 < FEW_F / 2 ? half - n0 : FEW_F / 2;
+  if (row < lo || row >= hi) {  // a row of no expert
+    const int f = threadIdx.x & 31;
+    if (f < nf) {
+      static_cast<T *>(g.h)[row * g.ld_h + n0 + f] = Elem<T>::from(0.f);
+      if (g.y) {
+        static_cast<T *>(g.y)[row * g.ld_y + n0 + f] = Elem<T>::from(0.f);
+        static_cast<T *>(g.y)[row * g.ld_y + half + n0 + f] = Elem<T>::from(0.f);
+      }
+    }
+    return;
+  }
+  if ((row - lo) % FEW_R) return;
+  switch (hi - row) {
+    case 1: few_gated_rows<T, 1, ACT>(g, row, e, n0, nf); break;
+    case 2: few_gated_rows<T, 2, ACT>(g, row, e, n0, nf); break;
+    case 3: few_gated_rows<T, 3, ACT>(g, row, e, n0, nf); break;
+    default: few_gated_rows<T, 4, ACT>(g, row, e, n0, nf); break;
+  }
+}
+
+template <typename T>
+cudaError_t gated_few_type(const GroupedArgs &g, cudaStream_t s) {
+  const int per = FEW_WARPS * FEW_F / 2;
+  const dim3 grid(((g.N >> 1) + per - 1) / per, g.rows);
+  switch (g.act) {
+    case MOE_ACT_SILU: gated_few_kernel<T, MOE_ACT_SILU><<<grid, FEW_WARPS * 32, 0, s>>>(g); break;
+    case MOE_ACT_GELU: gated_few_kernel<T, MOE_ACT_GELU><<<grid, FEW_WARPS * 32, 0, s>>>(g); break;
+    case MOE_ACT_GELU_TANH: gated_few_kernel<T, MOE_ACT_GELU_TANH><<<grid, FEW_WARPS * 32, 0, s>>>(g); break;
+    default: gated_few_kernel<T, MOE_ACT_RELU><<<grid, FEW_WARPS * 32, 0, s>>>(g); break;
+  }
+  return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------- zeros
@@ -495,6 +579,11 @@ cudaError_t launch_grouped_pad(const GroupedArgs &g, const void *src, long rows,
   grouped_pad_kernel<<<static_cast<unsigned>(want < 152 * 32 ? want : 152 * 32), 256, 0, s>>>(
       g, static_cast<const uint16_t *>(src), rows, cols, ld, experts, static_cast<uint16_t *>(dst), ld_dst);
   return cudaGetLastError();
+}
+
+cudaError_t launch_gated_few(const GroupedArgs &g, cudaStream_t s) {
+  HostTrace t("gated_few", s);
+  return g.dtype == MOE_ELEM_BF16 ? gated_few_type<__nv_bfloat16>(g, s) : gated_few_type<__half>(g, s);
 }
 
 cudaError_t launch_grouped_few(const GroupedArgs &g, cudaStream_t s) {

@@ -9,6 +9,8 @@
 //
 //   forward   A = w [N, K] K-major             B = x K-major     columns: tokens
 //   dgrad     A = w^T: w read MN-major         B = dy K-major    columns: tokens
+//   gated     A = w's rows [gate 16 | up 16 | gate 16 ..] K-major, B = x: 128 features of h
+//             per pair, both projections of a feature in one warp's 32 lanes
 //   wgrad     A = dy^T, B = x^T: both read MN-major, the reduction runs over the
 //             expert's rows.  Rows past its last one must not enter the sum
 //             (0 * NaN is NaN), so each expert has its own pair of tensor maps
@@ -26,6 +28,7 @@
 #include <type_traits>
 
 #include "elem.cuh"
+#include "gate_act.cuh"
 #include "gemm_common.cuh"
 #include "grouped.cuh"
 #include "kernels.h"
@@ -64,6 +67,20 @@ MOE_DEV void tma_load_3d_pair(const CUtensorMap *map, uint32_t mbar, void *dst, 
       "l"(map), "r"(mbar), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
+MOE_DEV void tma_load_4d_pair(const CUtensorMap *map, uint32_t mbar, void *dst, int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(mbar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+MOE_DEV void tma_load_5d_pair(const CUtensorMap *map, uint32_t mbar, void *dst, int c0, int c1, int c2, int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(map), "r"(mbar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
+}
 MOE_DEV void tma_store_3d(const CUtensorMap *map, const void *src, int c0, int c1, int c2) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(map),
                "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
@@ -95,7 +112,7 @@ MOE_DEV uint64_t mn_desc(uint32_t saddr) {
 template <int DIR>
 MOE_DEV uint32_t tc_idesc(int dtype, int n) {
   const uint32_t f = dtype == MOE_ELEM_BF16 ? 1u : 0u;
-  return (1u << 4) | (f << 7) | (f << 10) | (DIR != GROUPED_FWD ? 1u << 15 : 0u) |
+  return (1u << 4) | (f << 7) | (f << 10) | (DIR == GROUPED_DGRAD || DIR == GROUPED_WGRAD ? 1u << 15 : 0u) |
          (DIR == GROUPED_WGRAD ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (16u << 24);
 }
 
@@ -116,7 +133,7 @@ struct TcTiles {
   TileTable t;
   int nf, nc, total;
   MOE_DEV TcTiles(const GroupedArgs &args, int *table) : g(args) {
-    nf = ((DIR == GROUPED_DGRAD ? g.K : g.N) + 255) >> 8;
+    nf = DIR == GROUPED_GATED ? ((g.N >> 1) + 127) >> 7 : ((DIR == GROUPED_DGRAD ? g.K : g.N) + 255) >> 8;
     if constexpr (DIR == GROUPED_WGRAD) {
       nc = (g.K + 255) >> 8;
       total = (g.zeroed || g.accumulate ? __ldg(g.order + g.E) : g.E) * nf * nc;  // the experts without rows stand last
@@ -150,7 +167,7 @@ struct TcTiles {
       const int first = t.first[i], mt = t.first[i + 1] - first, local = u - first * nf;
       r.e = t.order[i];
       const int lo = t.off[r.e], rows = t.off[r.e + 1] - lo, size = tile_tokens(rows);
-      r.f0 = (local / mt) * 256;
+      r.f0 = (local / mt) * (DIR == GROUPED_GATED ? 128 : 256);
       const int from = (local % mt) * size;
       r.c0 = lo + from;
       r.valid = rows - from < size ? rows - from : size;
@@ -183,6 +200,85 @@ MOE_DEV void put_tokens(const float *v, uint8_t *buf, T *out, long ld, int token
     const int t = (lane >> 2) + 8 * i;
     if (t < tokens && c < features)
       *reinterpret_cast<uint4 *>(out + t * ld + c) = *reinterpret_cast<const uint4 *>(buf + t * 64 + c * 2);
+  }
+}
+
+// The same for a piece whose lanes 0 .. 15 hold 16 features of the gate and lanes 16 ..
+// 31 those of the up projection: [g | u] of each token, `half` elements apart.
+template <typename T>
+MOE_DEV void put_gate_up(const float *v, uint8_t *buf, T *out, long ld, int half, int tokens, int features, bool vec, int lane) {
+  if (!vec) {
+#pragma unroll
+    for (int t = 0; t < 32; ++t)
+      if (t < tokens && (lane & 15) < features) out[t * ld + (lane < 16 ? lane : half + lane - 16)] = Elem<T>::from(v[t]);
+    return;
+  }
+  const bool odd = lane & 1;
+  __syncwarp();
+#pragma unroll
+  for (int t = 0; t < 32; t += 2) {
+    const float mine = odd ? v[t + 1] : v[t];
+    const float other = __shfl_xor_sync(0xffffffffu, odd ? v[t] : v[t + 1], 1);
+    const uint32_t w = odd ? Elem<T>::pack2(other, mine) : Elem<T>::pack2(mine, other);
+    *reinterpret_cast<uint32_t *>(buf + (t + (odd ? 1 : 0)) * 64 + (lane >> 1) * 4) = w;
+  }
+  __syncwarp();
+  const int c = (lane & 1) * 8;
+  T *to = out + ((lane & 2) ? half : 0) + c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = (lane >> 2) + 8 * i;
+    if (t < tokens && c < features)
+      *reinterpret_cast<uint4 *>(to + t * ld) = *reinterpret_cast<const uint4 *>(buf + t * 64 + (lane & 3) * 16);
+  }
+}
+
+// h = act(g) u of that piece: a gate's lane and its up projection's, 16 apart, swap half of
+// their tokens, so that each has both for 16 of them (even ones below lane 16, odd ones above).
+template <typename T>
+MOE_DEV void put_gated(const float *v, uint8_t *buf, T *out, long ld, int act, int tokens, int features, bool vec, int lane) {
+  const bool up = lane & 16;
+  float gate[16], h[16];
+#pragma unroll
+  for (int t = 0; t < 16; ++t) {
+    const float other = __shfl_xor_sync(0xffffffffu, up ? v[2 * t] : v[2 * t + 1], 16);
+    gate[t] = up ? other : v[2 * t];
+    h[t] = up ? v[2 * t + 1] : other;
+  }
+  switch (act) {
+    case MOE_ACT_SILU:
+#pragma unroll
+      for (int t = 0; t < 16; ++t) h[t] *= act_value<MOE_ACT_SILU>(gate[t]);
+      break;
+    case MOE_ACT_GELU:
+#pragma unroll
+      for (int t = 0; t < 16; ++t) h[t] *= act_value<MOE_ACT_GELU>(gate[t]);
+      break;
+    case MOE_ACT_GELU_TANH:
+#pragma unroll
+      for (int t = 0; t < 16; ++t) h[t] *= act_value<MOE_ACT_GELU_TANH>(gate[t]);
+      break;
+    default:
+#pragma unroll
+      for (int t = 0; t < 16; ++t) h[t] *= act_value<MOE_ACT_RELU>(gate[t]);
+  }
+  const int f = lane & 15, first = up ? 1 : 0;
+  if (!vec) {
+#pragma unroll
+    for (int t = 0; t < 16; ++t)
+      if (2 * t + first < tokens && f < features) out[(2 * t + first) * ld + f] = Elem<T>::from(h[t]);
+    return;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int t = 0; t < 16; ++t) *reinterpret_cast<T *>(buf + (2 * t + first) * 32 + f * 2) = Elem<T>::from(h[t]);
+  __syncwarp();
+  const int c = (lane & 1) * 8;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int t = (lane >> 1) + 16 * i;
+    if (t < tokens && c < features)
+      *reinterpret_cast<uint4 *>(out + t * ld + c) = *reinterpret_cast<const uint4 *>(buf + t * 32 + c * 2);
   }
 }
 
@@ -326,6 +422,15 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
             if constexpr (DIR == GROUPED_FWD) {
               tma_load_3d_pair(ma, bar, sa, k, fr, t.e);
               tma_load_2d_pair(mb, bar, sb, k, cr);
+            } else if constexpr (DIR == GROUPED_GATED) {
+              const int f = t.f0 + static_cast<int>(rank) * 64;
+              if (g.by_16) {
+                tma_load_5d_pair(ma, bar, sa, k, 0, 0, f >> 4, t.e);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tma_load_4d_pair(ma, bar, sa + i * 4096, k, f + 16 * i, 0, t.e);
+              }
+              tma_load_2d_pair(mb, bar, sb, k, cr);
             } else if constexpr (DIR == GROUPED_DGRAD) {
               tma_load_3d_pair(ma, bar, sa, fr, k, t.e);
               tma_load_3d_pair(ma, bar, sa + 8192, fr + 64, k, t.e);
@@ -372,7 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
           for (int k = 0; k < 4 * kBlocks; ++k) {
             if (k * 16 < left) {
               const uint32_t sa = sa0 + (k >> 2) * kBlockBytes, sb = sa + 16384;
-              const uint64_t ad = DIR == GROUPED_FWD ? sw128_desc(sa + 32 * (k & 3)) : mn_desc(sa + 2048 * (k & 3));
+              const uint64_t ad = DIR == GROUPED_FWD || DIR == GROUPED_GATED ? sw128_desc(sa + 32 * (k & 3))
+                                                                              : mn_desc(sa + 2048 * (k & 3));
               const uint64_t bd = DIR == GROUPED_WGRAD ? mn_desc(sb + 2048 * (k & 3)) : sw128_desc(sb + 32 * (k & 3));
               mma_bf16_pair(dt, ad, bd, idesc, (kb | k) ? 1u : 0u);
             }
@@ -406,17 +512,24 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
       group_rows(g, 0, lo, hi);
       group_rows(g, g.E - 1, lo_last, hi_last);
       const int outside = g.E <= kTableExperts ? lo + (g.rows - hi_last) : 0;
-      const long ld = (DIR == GROUPED_DGRAD ? g.ld_x : g.ld_y) * (WIDE ? 4 : 2);
-      const int bytes = (DIR == GROUPED_DGRAD ? g.K : g.N) * (WIDE ? 4 : 2);
-      uint8_t *out = static_cast<uint8_t *>(DIR == GROUPED_DGRAD ? g.dx : g.y);
-      for (long i = blockIdx.x; i < outside; i += gridDim.x) {
-        uint8_t *row = out + (i < lo ? i : hi_last + (i - lo)) * ld;
-        if (g.vec_out) {
-          for (int b = (threadIdx.x - 64) * 16; b < bytes; b += 32 * kEpilogueWarps * 16)
-            *reinterpret_cast<uint4 *>(row + b) = make_uint4(0, 0, 0, 0);
-        } else {
-          for (int b = (threadIdx.x - 64) * 2; b < bytes; b += 32 * kEpilogueWarps * 2) *reinterpret_cast<uint16_t *>(row + b) = 0;
+      const auto zero = [&](void *to, long ld, int bytes, bool vec) {
+        uint8_t *out = static_cast<uint8_t *>(to);
+        for (long i = blockIdx.x; i < outside; i += gridDim.x) {
+          uint8_t *row = out + (i < lo ? i : hi_last + (i - lo)) * ld;
+          if (vec) {
+            for (int b = (threadIdx.x - 64) * 16; b < bytes; b += 32 * kEpilogueWarps * 16)
+              *reinterpret_cast<uint4 *>(row + b) = make_uint4(0, 0, 0, 0);
+          } else {
+            for (int b = (threadIdx.x - 64) * 2; b < bytes; b += 32 * kEpilogueWarps * 2) *reinterpret_cast<uint16_t *>(row + b) = 0;
+          }
         }
+      };
+      if constexpr (DIR == GROUPED_GATED) {
+        zero(g.h, g.ld_h * 2, g.N, g.vec_h);
+        if (g.y) zero(g.y, g.ld_y * 2, g.N * 2, g.vec_out);
+      } else {
+        zero(DIR == GROUPED_DGRAD ? g.dx : g.y, (DIR == GROUPED_DGRAD ? g.ld_x : g.ld_y) * (WIDE ? 4 : 2),
+             (DIR == GROUPED_DGRAD ? g.K : g.N) * (WIDE ? 4 : 2), g.vec_out);
       }
     }
     if (DIR == GROUPED_DGRAD && g.chained && warp == 2) {
@@ -469,6 +582,25 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
             put_elements<O>(w, buf, static_cast<O *>(g.dw) + (static_cast<long>(t.e) * g.N + fr) * g.K + t.c0 + j, g.K,
                             g.N - fr, g.K - t.c0 - j, g.accumulate != 0, lane);
           }
+        }
+      } else if constexpr (DIR == GROUPED_GATED) {
+        const int half_n = g.N >> 1, f = t.f0 + static_cast<int>(rank) * 64 + q * 16;  // this warp's first feature of h
+        for (int j = half * 32; j < t.n; j += 64) {
+          uint32_t r[32];
+          tmem_ld32_async(tb + j, r);
+          tmem_ld_wait();
+          reg_fence<32>(r);
+          if (j + 64 >= t.n) {
+            release();
+            held = false;
+          }
+          const int tokens = t.valid - j;
+          if (f >= half_n) continue;
+          const float *v = reinterpret_cast<const float *>(r);
+          const long row = t.c0 + j;
+          if (g.y)
+            put_gate_up<T>(v, buf, static_cast<T *>(g.y) + row * g.ld_y + f, g.ld_y, half_n, tokens, half_n - f, g.vec_out, lane);
+          put_gated<T>(v, buf, static_cast<T *>(g.h) + row * g.ld_h + f, g.ld_h, g.act, tokens, half_n - f, g.vec_h, lane);
         }
       } else {
         const int F = DIR == GROUPED_DGRAD ? g.K : g.N;
@@ -638,7 +770,7 @@ cudaError_t launch_tc_one(const TcMaps &maps, const GroupedArgs &g, long units, 
 template <int DIR>
 cudaError_t launch_tc(const TcMaps &maps, const GroupedArgs &g, long units, cudaStream_t s) {
   const bool bf = g.dtype == MOE_ELEM_BF16;
-  if constexpr (DIR != GROUPED_DGRAD) {
+  if constexpr (DIR == GROUPED_FWD || DIR == GROUPED_WGRAD) {
     if (g.out_dtype == MOE_ELEM_FP32)
       return bf ? launch_tc_one<DIR, __nv_bfloat16, true>(maps, g, units, s) : launch_tc_one<DIR, __half, true>(maps, g, units, s);
   }
@@ -664,9 +796,31 @@ bool expert_map(CUtensorMap *m, int elem, const void *p, const GroupedArgs &g, l
   return host_encode_map(m, elem, p, 3, dims, strides, box);
 }
 
+// w's rows as (column, 16 rows, gate or up, group of 16, expert), so that one box is 16 rows
+// of the gate, the same 16 of the up projection, and so on; where m is no multiple of 16
+// as (column, row, gate or up, expert), whose extent ends each projection, in boxes of
+// one group.
+bool gated_map(CUtensorMap *m, const GroupedArgs &g) {
+  const uint64_t k = g.K, half = g.N / 2, row = static_cast<uint64_t>(g.ld_w) * 2, e = static_cast<uint64_t>(g.ld_e) * 2;
+  if (g.by_16) {
+    const uint64_t dims[5] = {k, 16, 2, half / 16, static_cast<uint64_t>(g.E)};
+    const uint64_t strides[4] = {row, half * row, 16 * row, e};
+    const uint32_t box[5] = {64, 16, 2, 4, 1};
+    return host_encode_map(m, g.dtype, g.w, 5, dims, strides, box);
+  }
+  const uint64_t dims[4] = {k, half, 2, static_cast<uint64_t>(g.E)};
+  const uint64_t strides[3] = {row, half * row, e};
+  const uint32_t box[4] = {64, 16, 2, 1};
+  return host_encode_map(m, g.dtype, g.w, 4, dims, strides, box);
+}
+
 // Where the rows of no expert and the tile table are made by a launch of their own.
 cudaError_t plan_first(const GroupedArgs &g, int dir, cudaStream_t s) {
   if (g.E <= kTableExperts) return cudaSuccess;
+  if (dir == GROUPED_GATED) {
+    const cudaError_t e = g.y ? launch_grouped_plan(g, 0, g.y, g.dtype, g.N, g.ld_y, s) : cudaSuccess;
+    return e == cudaSuccess ? launch_grouped_plan(g, 0, g.h, g.dtype, g.N >> 1, g.ld_h, s) : e;
+  }
   const bool fwd = dir == GROUPED_FWD;
   return launch_grouped_plan(g, 0, fwd ? g.y : g.dx, fwd ? g.out_dtype : g.dtype, fwd ? g.N : g.K, fwd ? g.ld_y : g.ld_x, s);
 }
@@ -698,6 +852,11 @@ cudaError_t launch_product(const GroupedArgs &g, int dir, cudaStream_t s) {
     return launch_tc<GROUPED_WGRAD>(m, g, static_cast<long>(g.E) * ((g.N + 255) / 256) * ((g.K + 255) / 256), s);
   }
   const long tokens = (g.rows + kTileTokens - 1L) / kTileTokens + (g.E < g.rows ? g.E : g.rows);
+  if (dir == GROUPED_GATED) {
+    if (!row_maps(m.b, g.dtype, g.x, g.rows, g.K, g.in_x) || !gated_map(&m.a, g)) return cudaErrorInvalidValue;
+    HostTrace t("gated_forward", s);
+    return launch_tc<GROUPED_GATED>(m, g, tokens * ((g.N / 2 + 127) / 128), s);
+  }
   if (dir == GROUPED_FWD) {
     if (!row_maps(m.b, g.dtype, g.x, g.rows, g.K, g.in_x) || !expert_map(&m.a, g.dtype, g.w, g, g.ld_w, g.ld_e, 64, 128))
       return cudaErrorInvalidValue;

@@ -84,6 +84,7 @@ size_t vocab_bind(moe::VocabArgs *a, bool backward, void *ws) {
   a->scale = reinterpret_cast<float *>(head + 8);
   a->row = reinterpret_cast<int *>(take(pad * 4));
   a->label = reinterpret_cast<int *>(take(pad * 4));
+  a->hit = reinterpret_cast<float *>(take(pad * 4));
   a->xs = take(rows * a->ld_xs * 2);
   if (a->pad_w) a->ws_w = take(static_cast<size_t>(a->V) * a->ld_ws_w * 2);
   if (backward) {
@@ -95,7 +96,6 @@ size_t vocab_bind(moe::VocabArgs *a, bool backward, void *ws) {
     a->dz = take(rows * a->width * 2);
     a->sum = reinterpret_cast<float *>(take(a->splits * rows * a->ld_sum * 4));
   } else {
-    a->hit = reinterpret_cast<float *>(take(pad * 4));
     a->part = reinterpret_cast<float2 *>(take(pad * a->parts * 8));
   }
   return at + 256;

@@ -136,32 +136,75 @@ __global__ void __launch_bounds__(kRowThreads) vocab_rows_kernel(const VocabArgs
 // ---------------------------------------------------------------- copies
 // xs [count rounded up to 128 (or rows)][ld_xs] = x[row[i]], zeros beyond x's columns
 // and behind the last row: a sum over rows takes them in steps of up to 128.
+// On the way the label's logit, a dot product in fp32 whose terms are rounded to
+// nearest.  The tensor cores' sums truncate: at d = 7168 their logits are off by some
+// 4e-6 of their size, which the loss of a row that is sure of its label would consist of.
+// GROUP threads per row: 32, or the block's 256 from 2048 columns on.
+constexpr int kWideRow = 2048;
+
+template <typename T>
+MOE_DEV uint4 eight(const T *p, int left, bool vec) {
+  if (vec) return *reinterpret_cast<const uint4 *>(p);
+  const uint16_t *e = reinterpret_cast<const uint16_t *>(p);
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t lo = 2 * k < left ? e[2 * k] : 0u, hi = 2 * k + 1 < left ? e[2 * k + 1] : 0u;
+    w[k] = lo | (hi << 16);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+template <typename T, int GROUP, bool BACKWARD>
 __global__ void __launch_bounds__(256) vocab_gather_kernel(const VocabArgs a) {
+  __shared__ float part[8];
   pdl_wait();
   pdl_trigger();
   const int n = *a.count, chunks = static_cast<int>(a.ld_xs >> 3);
   const int end = ((n + 127) & ~127) < a.rows ? ((n + 127) & ~127) : a.rows;
-  const long total = static_cast<long>(end) * chunks;
-  const bool vec = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && a.ld_x % 8 == 0 && a.d % 8 == 0;
-  uint16_t *xs = static_cast<uint16_t *>(a.xs);
-  for (long u = static_cast<long>(blockIdx.x) * 256 + threadIdx.x; u < total; u += static_cast<long>(gridDim.x) * 256) {
-    const int i = static_cast<int>(u / chunks), c = static_cast<int>(u - static_cast<long>(i) * chunks) * 8;
-    uint4 q = make_uint4(0, 0, 0, 0);
-    if (i < n) {
-      const uint16_t *p = static_cast<const uint16_t *>(a.x) + a.row[i] * a.ld_x + c;
-      if (vec) {
-        q = *reinterpret_cast<const uint4 *>(p);
-      } else {
-        uint32_t w[4];
+  const bool vec_x = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && a.ld_x % 8 == 0 && a.d % 8 == 0;
+  const bool vec_w = (reinterpret_cast<uintptr_t>(a.w) & 15) == 0 && a.ld_w % 8 == 0 && a.d % 8 == 0;
+  const int me = threadIdx.x % GROUP, warp = threadIdx.x >> 5;
+  for (long i = static_cast<long>(blockIdx.x) * (256 / GROUP) + threadIdx.x / GROUP; i < end;
+       i += static_cast<long>(gridDim.x) * (256 / GROUP)) {
+    uint4 *to = reinterpret_cast<uint4 *>(static_cast<T *>(a.xs) + i * a.ld_xs);
+    if (i >= n) {
+      for (int c = me; c < chunks; c += GROUP) to[c] = make_uint4(0, 0, 0, 0);
+      continue;  // of whole groups; with GROUP 256 of the whole block
+    }
+    const int label = a.label[i];
+    const T *x = static_cast<const T *>(a.x) + a.row[i] * a.ld_x;
+    const T *w = static_cast<const T *>(a.w) + label * a.ld_w;
+    float s = 0.f;
+#pragma unroll 2
+    for (int c = me; c < chunks; c += GROUP) {
+      const uint4 q = eight(x + c * 8, a.d - c * 8, vec_x), r = eight(w + c * 8, a.d - c * 8, vec_w);
+      to[c] = q;
+      float u[8], v[8];
+      Elem<T>::unpack(q, u);
+      Elem<T>::unpack(r, v);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t lo = c + 2 * k < a.d ? p[2 * k] : 0u, hi = c + 2 * k + 1 < a.d ? p[2 * k + 1] : 0u;
-          w[k] = lo | (hi << 16);
-        }
-        q = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int k = 0; k < 8; ++k) s = fmaf(u[k], v[k], s);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if constexpr (GROUP == 256) {
+      __syncthreads();
+      if ((threadIdx.x & 31) == 0) part[warp] = s;
+      __syncthreads();
+      s = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += part[k];
+    }
+    if (me == 0) {
+      if constexpr (BACKWARD) {
+        // the label's dz: coef_p exp(z - lse) - coef_l, without losing it where exp is near 1
+        const float p = a.coef_p[i], l = a.coef_l[i];
+        a.hit[i] = p == 0.f ? -l : (p - l) + p * expm1f(s - a.lse_in[a.row[i]]);
+      } else {
+        a.hit[i] = s;
       }
     }
-    *reinterpret_cast<uint4 *>(xs + i * a.ld_xs + c) = q;
   }
 }
 
@@ -195,7 +238,9 @@ MOE_DEV float2 join(float2 a, float2 b) {
   return make_float2(m, sa + sb);
 }
 
-// One warp per row that counts.
+// One warp per row that counts.  The parts hold all logits but the label's, z:
+//   loss = log(1 + S exp(m - z)),  lse = z + loss
+// where that is in range, which keeps a small loss's precision.
 __global__ void __launch_bounds__(256) vocab_loss_kernel(const VocabArgs a) {
   pdl_wait();
   const int n = *a.count, lane = threadIdx.x & 31;
@@ -209,10 +254,18 @@ __global__ void __launch_bounds__(256) vocab_loss_kernel(const VocabArgs a) {
       v = join(v, w);
     }
     if (lane == 0) {
-      const float lse = from_of(v.x) + logf(v.y);
+      const float z = a.hit[i], others = from_of(v.x) + logf(v.y);  // -inf: the label is alone
+      float loss, lse;
+      if (others <= z) {
+        loss = log1pf(expf(others - z));
+        lse = z + loss;
+      } else {  // also where a logit is not finite
+        lse = others + log1pf(expf(z - others));
+        loss = lse - z;
+      }
       const int t = a.row[i];
       a.lse[t] = lse;
-      a.loss[t] = lse - a.hit[i];
+      a.loss[t] = loss;
     }
   }
 }
@@ -255,6 +308,12 @@ unsigned blocks_of(long threads, int num_sms) {
   return static_cast<unsigned>(want < 1 ? 1 : want < most ? want : most);
 }
 
+template <typename T, bool BACKWARD>
+cudaError_t gather_rows(const VocabArgs &a, int num_sms, cudaStream_t s) {
+  if (a.ld_xs >= kWideRow) return launch_early(vocab_gather_kernel<T, 256, BACKWARD>, blocks_of(a.rows * 256L, num_sms), 256, s, a);
+  return launch_early(vocab_gather_kernel<T, 32, BACKWARD>, blocks_of(a.rows * 32L, num_sms), 256, s, a);
+}
+
 cudaError_t copies(const VocabArgs &a, bool backward, int num_sms, cudaStream_t s) {
   if (a.pad_w) {
     HostTrace t("vocab_pad", s);
@@ -268,7 +327,9 @@ cudaError_t copies(const VocabArgs &a, bool backward, int num_sms, cudaStream_t 
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   HostTrace t("vocab_gather", s);
-  return launch_early(vocab_gather_kernel, blocks_of(static_cast<long>(a.rows) * (a.ld_xs >> 3), num_sms), 256, s, a);
+  if (a.dtype == MOE_ELEM_BF16)
+    return backward ? gather_rows<__nv_bfloat16, true>(a, num_sms, s) : gather_rows<__nv_bfloat16, false>(a, num_sms, s);
+  return backward ? gather_rows<__half, true>(a, num_sms, s) : gather_rows<__half, false>(a, num_sms, s);
 }
 
 }  // namespace

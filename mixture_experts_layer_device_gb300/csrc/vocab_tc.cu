@@ -1,14 +1,14 @@
 // The products behind the loss over a vocabulary on CTA pairs (tcgen05, cta_group::2):
 //
-//   LOSS  logits z = xs w^T of 256 rows x 256 vocabulary entries; a row's maximum, sum of
-//         exponentials and label's logit leave, the logits do not
-//   DZ    the same logits again, out as dz = coef_p exp(z - lse) - coef_l [label] in
-//         16 bits, one piece of the vocabulary at a time
+//   LOSS  logits z = xs w^T of 256 rows x 256 vocabulary entries; of a row's logits but its
+//         label's the maximum and the sum of exponentials leave, the logits do not
+//   DZ    the same logits again, out as dz = coef_p exp(z - lse) (the label's: its own
+//         value) in 16 bits, one piece of the vocabulary at a time
 //   DX    sum += dz w over a piece            A = dz K-major,  B = w read MN-major
 //   DW    dw = dz^T xs                        A and B read MN-major
 //
 // With the rows on the instruction's M side a thread of the epilogue owns one
-// row: maximum, sum and label stay in its registers, without a shuffle.  Rows are
+// row: maximum and sum stay in its registers, without a shuffle.  Rows are
 // dense here (those that do not count were left out by the copy), so tiles are
 // whole; what a tile has past the last row or column is computed on zeros that TMA
 // fills in and not stored.
@@ -346,12 +346,10 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
             for (int i = 0; i < 32; ++i)
               if (i >= left) z[i] = -__int_as_float(0x7f800000);
           }
-          if (__any_sync(0xffffffffu, hit >= j && hit < j + 32)) {
-            float v = 0.f;
+          if (__any_sync(0xffffffffu, hit >= j && hit < j + 32)) {  // the label's logit is formed apart
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (hit == j + i) v = z[i];
-            if (hit >= j && hit < j + 32) g.hit[row] = v;
+              if (hit == j + i) z[i] = -__int_as_float(0x7f800000);
           }
           float top = z[0];
 #pragma unroll
@@ -372,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
         }
         if (row < count) g.part[static_cast<long>(row) * g.parts + (t.n0 >> 7) + half] = make_float2(m, s);
       } else if constexpr (MODE == VOCAB_DZ) {
-        const float cp = g.coef_p[row], cl = g.coef_l[row], base = g.base[row];
+        const float cp = g.coef_p[row], own = g.hit[row], base = g.base[row];
         const int hit = g.label[row] - (g.v0 + col0);
 #pragma unroll
         for (int j = 0; j < 128; j += 64) {
@@ -389,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
           if (__any_sync(0xffffffffu, hit >= j && hit < j + 64)) {
 #pragma unroll
             for (int i = 0; i < 64; ++i)
-              if (hit == j + i) z[i] -= cl;
+              if (hit == j + i) z[i] = own;
           }
 #pragma unroll
           for (int i = 0; i < 32; ++i) w[i] = Elem<T>::pack2(z[2 * i], z[2 * i + 1]);
