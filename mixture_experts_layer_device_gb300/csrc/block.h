@@ -173,9 +173,9 @@ struct VocabArgs {
   float2 *part;          // forward: [pad][parts] (maximum, sum of exponentials) of 128 logits
   int parts;
   float *coef_p, *coef_l, *base;  // backward: [pad] dz = coef_p 2^(z log2 e - base), less coef_l for the label
-  void *xs;              // [rows][ld_xs] the copy of x
+  void *xs;              // [rows rounded up to 128][ld_xs] the copy of x
   void *ws_w;            // the padded copy of w where TMA cannot address it (else unused)
-  void *dz;              // backward: [rows][width] one piece of the logits' gradient
+  void *dz;              // backward: [rows rounded up to 128][width] one piece of the logits' gradient
   float *sum;            // backward: [splits][rows][ld_sum] sums of dx
   long ld_xs, ld_ws_w, ld_sum;
   int width, splits;

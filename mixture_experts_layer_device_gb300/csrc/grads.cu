@@ -10,9 +10,9 @@
 // from the end backwards, where L2 still holds what the norm read last; in place
 // and below the limit (c = 1) it reads and writes nothing.
 //
-// Sums: a thread squares up to 64 elements in fp32 and adds that to a 64-bit
+// Sums: a thread squares up to 32 elements in fp32 and adds that to a 64-bit
 // sum.  Where fp32 overflows or its squares sink below the normal range, the
-// same 64 elements are squared again in 64 bits.
+// same elements are squared again in 64 bits.
 #include "block.h"
 #include "elem.cuh"
 #include "kernels.h"
@@ -22,8 +22,9 @@ namespace moe {
 namespace {
 
 constexpr int kGradThreads = 256;
-constexpr int kVecs = 8;                                // 16-byte pieces per thread and chunk
-constexpr int kChunkVecs = kGradThreads * kVecs;        // 32 KB
+constexpr int kVecs = 4;                                // 16-byte pieces per thread and chunk
+constexpr int kChunkVecs = kGradThreads * kVecs;        // 16 KB
+constexpr int kBlocksPerSm = 6;
 
 // The tensors of one launch: their first elements, lengths and types, and the
 // first chunk of each.  A chunk is kChunkVecs aligned 16-byte pieces; a tensor's
@@ -66,8 +67,9 @@ struct Piece {
     end = lead + count;
   }
   MOE_DEV bool whole(int64_t v) const { return v * VEC >= lead && v * VEC + VEC <= end; }
+  template <bool STREAM>
   MOE_DEV uint4 load(int64_t v) const {
-    if (whole(v)) return ld_stream(base + v * VEC);
+    if (whole(v)) return STREAM ? ld_stream(base + v * VEC) : *reinterpret_cast<const uint4 *>(base + v * VEC);
     union {
       uint4 q;
       T e[VEC];
@@ -100,7 +102,7 @@ MOE_DEV double squares(const uint4 (&q)[kVecs]) {
     any |= q[j].x | q[j].y | q[j].z | q[j].w;
   }
   const float s = s0 + s1;
-  // from 2^-110 on, 64 squares that are each off by half of fp32's smallest step do not count
+  // from 2^-110 on, 32 squares that are each off by half of fp32's smallest step do not count
   const uint32_t magnitude = sizeof(T) == 2 ? 0x7fff7fffu : 0x7fffffffu;
   if ((s >= 7.7e-34f && s <= 3.0e38f) || (any & magnitude) == 0) return s;
   double d = 0.0;
@@ -125,7 +127,7 @@ MOE_DEV double chunk_squares(const uint8_t *data, int64_t count, int local) {
   uint4 q[kVecs];
   if (v0 * Piece<T>::VEC >= p.end) return 0.0;
 #pragma unroll
-  for (int j = 0; j < kVecs; ++j) q[j] = p.load(v0 + j * kGradThreads);
+  for (int j = 0; j < kVecs; ++j) q[j] = p.template load<false>(v0 + j * kGradThreads);
   return squares<T>(q);
 }
 
@@ -143,7 +145,7 @@ MOE_DEV double block_sum(double v) {
 }
 
 template <int MOST>
-__global__ void __launch_bounds__(kGradThreads, 4) grad_squares_kernel(const __grid_constant__ GradTable<MOST> t,
+__global__ void __launch_bounds__(kGradThreads, kBlocksPerSm) grad_squares_kernel(const __grid_constant__ GradTable<MOST> t,
                                                                        double *part) {
   pdl_trigger();
   double sum = 0.0;
@@ -170,18 +172,26 @@ __global__ void __launch_bounds__(kGradThreads) grad_norm_kernel(const double *p
   if (threadIdx.x == 0) *norm = static_cast<float>(v);
 }
 
+MOE_DEV void st_stream_32(void *p, const float *f) {
+  asm volatile("st.global.cs.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(f[0]), "f"(f[1]), "f"(f[2]),
+               "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7])
+               : "memory");
+}
+
 // One thread's pieces of a chunk, times c, to `out`.
 template <typename T, typename O>
 MOE_DEV void chunk_scale(const uint8_t *data, uint8_t *out, int64_t count, int local, float c) {
   constexpr int VEC = Elem<T>::VEC;
   const Piece<T> p(data, count);
   O *o = reinterpret_cast<O *>(out) - p.lead;  // the place of piece 0's first element
-  const bool vec = (reinterpret_cast<uintptr_t>(o) & 15) == 0;
+  // a piece leaves in one store: 16 bytes, or 32 as fp32 from 16-bit elements
+  constexpr int OUT = VEC * static_cast<int>(sizeof(O));
+  const bool vec = (reinterpret_cast<uintptr_t>(o) & (OUT - 1)) == 0;
   const int64_t v0 = static_cast<int64_t>(local) * kChunkVecs + threadIdx.x;
   if (v0 * VEC >= p.end) return;
   uint4 q[kVecs];
 #pragma unroll
-  for (int j = 0; j < kVecs; ++j) q[j] = p.load(v0 + j * kGradThreads);
+  for (int j = 0; j < kVecs; ++j) q[j] = p.template load<true>(v0 + j * kGradThreads);
 #pragma unroll
   for (int j = 0; j < kVecs; ++j) {
     const int64_t v = v0 + j * kGradThreads;
@@ -190,9 +200,8 @@ MOE_DEV void chunk_scale(const uint8_t *data, uint8_t *out, int64_t count, int l
 #pragma unroll
     for (int k = 0; k < VEC; ++k) f[k] *= c;
     if (vec && p.whole(v)) {
-      constexpr int OV = Elem<O>::VEC;
-#pragma unroll
-      for (int k = 0; k < VEC; k += OV) st_stream(o + v * VEC + k, Elem<O>::pack(f + k));
+      if constexpr (OUT == 32) st_stream_32(o + v * VEC, f);
+      else st_stream(o + v * VEC, Elem<O>::pack(f));
     } else {
 #pragma unroll
       for (int k = 0; k < VEC; ++k) {
@@ -210,14 +219,15 @@ MOE_DEV void chunk_scale_to(const uint8_t *data, uint8_t *out, int out_type, int
 }
 
 template <int MOST>
-__global__ void __launch_bounds__(kGradThreads, 4) grad_scale_kernel(const __grid_constant__ GradTable<MOST> t,
+__global__ void __launch_bounds__(kGradThreads, kBlocksPerSm) grad_scale_kernel(const __grid_constant__ GradTable<MOST> t,
                                                                      const double *part, int n, double max_norm,
-                                                                     double eps, float *norm) {
+                                                                     double eps, bool in_place, float *norm) {
   pdl_wait();
   const double v = norm_of(part, n);
   if (blockIdx.x == 0 && threadIdx.x == 0 && norm) *norm = static_cast<float>(v);
   const double r = max_norm / (v + eps);
   const float c = r >= 1.0 ? 1.f : static_cast<float>(r);  // NaN stays
+  if (c == 1.f && in_place) return;
   for (int k = blockIdx.x; k < t.chunks; k += gridDim.x) {
     const int chunk = t.chunks - 1 - k, i = tensor_of_chunk(t, chunk), local = chunk - t.first[i];
     if (c == 1.f && t.out[i] == t.data[i]) continue;
@@ -235,7 +245,7 @@ long tensor_chunks(const GradTensors &g, int i) {
 }
 
 // The next launch's tensors, from `at` on: as many as the table holds.  Empty ones are
-// left out.  (Their chunks, 32 KB each, are counted in 32 bits.)
+// left out.  (Their chunks, 16 KB each, are counted in 32 bits.)
 template <int MOST>
 int fill_table(GradTable<MOST> *t, const GradTensors &g, int at) {
   t->n = 0;
@@ -257,10 +267,10 @@ int fill_table(GradTable<MOST> *t, const GradTensors &g, int at) {
   return at;
 }
 
-// Four blocks per SM; the workspace has room for so many sums per launch.
-constexpr int kMostBlocks = 4 * 152;
+// The workspace has room for so many sums per launch.
+constexpr int kMostBlocks = kBlocksPerSm * 152;
 int grid_of(int chunks, int num_sms) {
-  const int most = num_sms * 4 < kMostBlocks ? num_sms * 4 : kMostBlocks;
+  const int most = num_sms * kBlocksPerSm < kMostBlocks ? num_sms * kBlocksPerSm : kMostBlocks;
   return chunks < most ? chunks : most;
 }
 
@@ -283,12 +293,14 @@ cudaError_t grads(const GradTensors &g, bool clip, double max_norm, double eps, 
     HostTrace trace("grad_norm", s);
     return launch_early(grad_norm_kernel, 1, kGradThreads, s, static_cast<const double *>(part), sums, norm);
   }
+  bool in_place = true;
+  for (int i = 0; i < g.n; ++i) in_place &= g.outs[i] == g.data[i];
   for (int at = 0; at < g.n;) {
-    at = fill_table(&t, g, at);
+    at = g.n > MOST ? fill_table(&t, g, at) : g.n;  // one table: it is still there
     if (t.chunks == 0) break;
     HostTrace trace("grad_scale", s);
     e = launch_early(grad_scale_kernel<MOST>, grid_of(t.chunks, num_sms), kGradThreads, s, t,
-                     static_cast<const double *>(part), sums, max_norm, eps, norm);
+                     static_cast<const double *>(part), sums, max_norm, eps, in_place, norm);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;

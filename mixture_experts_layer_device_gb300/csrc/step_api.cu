@@ -77,7 +77,7 @@ size_t vocab_bind(moe::VocabArgs *a, bool backward, void *ws) {
     at += round256(bytes);
     return p;
   };
-  const size_t rows = a->rows, pad = tiles(a->rows) * 256;
+  const size_t rows = a->rows, pad = tiles(a->rows) * 256, high = (rows + 127) / 128 * 128;
   uint8_t *head = take(256);
   a->status = reinterpret_cast<int *>(head);
   a->count = reinterpret_cast<int *>(head + 4);
@@ -85,7 +85,7 @@ size_t vocab_bind(moe::VocabArgs *a, bool backward, void *ws) {
   a->row = reinterpret_cast<int *>(take(pad * 4));
   a->label = reinterpret_cast<int *>(take(pad * 4));
   a->hit = reinterpret_cast<float *>(take(pad * 4));
-  a->xs = take(rows * a->ld_xs * 2);
+  a->xs = take(high * a->ld_xs * 2);
   if (a->pad_w) a->ws_w = take(static_cast<size_t>(a->V) * a->ld_ws_w * 2);
   if (backward) {
     vocab_pieces(a);
@@ -93,7 +93,7 @@ size_t vocab_bind(moe::VocabArgs *a, bool backward, void *ws) {
     a->coef_p = reinterpret_cast<float *>(take(pad * 4));
     a->coef_l = reinterpret_cast<float *>(take(pad * 4));
     a->base = reinterpret_cast<float *>(take(pad * 4));
-    a->dz = take(rows * a->width * 2);
+    a->dz = take(high * a->width * 2);
     a->sum = reinterpret_cast<float *>(take(a->splits * rows * a->ld_sum * 4));
   } else {
     a->part = reinterpret_cast<float2 *>(take(pad * a->parts * 8));

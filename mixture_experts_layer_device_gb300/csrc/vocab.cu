@@ -28,18 +28,34 @@ MOE_DEV long label_of(const VocabArgs &a, int t) {
 // and lose nothing; *scale undoes it.
 constexpr int kRowThreads = 1024, kRowItems = 8;
 
+// The labels (-1: a row that does not count) and coefficients of kRowItems rows, 32 apart
+// from `first` on (a warp has 32 kRowItems rows next to each other), all loads in flight
+// together; the rows that count as a mask.
 template <bool BACKWARD>
-MOE_DEV bool row_counts(const VocabArgs &a, int t, long &label, float &p, float &l) {
-  label = label_of(a, t);
-  p = l = 0.f;
-  if (label < 0 || label >= a.V) return false;
-  if constexpr (BACKWARD) {
-    l = a.dloss ? a.dloss[t] : 0.f;
-    p = l + (a.dlse ? a.dlse[t] : 0.f);
-    return p != 0.f || l != 0.f;  // NaN counts
+struct RowItems {
+  int label[kRowItems];
+  float p[kRowItems], l[kRowItems];
+  MOE_DEV unsigned load(const VocabArgs &a, int first) {
+    long lab[kRowItems];
+#pragma unroll
+    for (int k = 0; k < kRowItems; ++k) {
+      const int t = first + 32 * k;
+      const bool has = t < a.rows;
+      lab[k] = has ? label_of(a, t) : -1;
+      l[k] = BACKWARD && has && a.dloss ? a.dloss[t] : 0.f;
+      p[k] = BACKWARD && has && a.dlse ? a.dlse[t] : 0.f;
+    }
+    unsigned mask = 0;
+#pragma unroll
+    for (int k = 0; k < kRowItems; ++k) {
+      p[k] += l[k];
+      const bool counts = lab[k] >= 0 && lab[k] < a.V && (!BACKWARD || p[k] != 0.f || l[k] != 0.f);  // NaN counts
+      label[k] = counts ? static_cast<int>(lab[k]) : -1;
+      mask |= counts ? 1u << k : 0u;
+    }
+    return mask;
   }
-  return true;
-}
+};
 
 template <bool BACKWARD>
 __global__ void __launch_bounds__(kRowThreads) vocab_rows_kernel(const VocabArgs a) {
@@ -47,14 +63,15 @@ __global__ void __launch_bounds__(kRowThreads) vocab_rows_kernel(const VocabArgs
   __shared__ int warps[32];
   __shared__ float tops[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  RowItems<BACKWARD> r;
   float top = 0.f;
   if constexpr (BACKWARD) {
-    for (int t = threadIdx.x; t < a.rows; t += kRowThreads) {
-      long label;
-      float p, l;
-      if (row_counts<true>(a, t, label, p, l)) {
-        const float m = fmaxf(fabsf(p), fabsf(l));  // one that is not finite keeps to its own row
-        if (m <= 3.402823466e38f) top = fmaxf(top, m);
+    for (int t0 = 0; t0 < a.rows; t0 += kRowThreads * kRowItems) {
+      const unsigned mask = r.load(a, t0 + warp * 32 * kRowItems + lane);
+#pragma unroll
+      for (int k = 0; k < kRowItems; ++k) {
+        const float m = fmaxf(fabsf(r.p[k]), fabsf(r.l[k]));  // one that is not finite keeps to its own row
+        if ((mask >> k & 1u) && m <= 3.402823466e38f) top = fmaxf(top, m);
       }
     }
 #pragma unroll
@@ -69,45 +86,31 @@ __global__ void __launch_bounds__(kRowThreads) vocab_rows_kernel(const VocabArgs
   const float up = a.dtype == MOE_ELEM_FP16 ? 16384.f : 1.f;
   int done = 0;
   for (int t0 = 0; t0 < a.rows; t0 += kRowThreads * kRowItems) {
-    const int first = t0 + threadIdx.x * kRowItems;
-    unsigned mask = 0;
-#pragma unroll
-    for (int k = 0; k < kRowItems; ++k) {
-      long label;
-      float p, l;
-      if (first + k < a.rows && row_counts<BACKWARD>(a, first + k, label, p, l)) mask |= 1u << k;
-    }
-    const int mine = __popc(mask);
-    int inc = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
+    const int first = t0 + warp * 32 * kRowItems + lane;
+    const unsigned mask = r.load(a, first);
+    const int mine = __reduce_add_sync(0xffffffffu, __popc(mask));
     __syncthreads();
-    if (lane == 31) warps[warp] = inc;
+    if (lane == 0) warps[warp] = mine;
     __syncthreads();
     const int w = warps[lane];
-    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
-    int at = done + before + inc - mine;
+    int base = done + __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
     done += __reduce_add_sync(0xffffffffu, w);
 #pragma unroll
     for (int k = 0; k < kRowItems; ++k) {
-      const int t = first + k;
-      if (t >= a.rows) break;
+      const int t = first + 32 * k;
+      const unsigned same = __ballot_sync(0xffffffffu, mask >> k & 1u);
+      const int at = base + __popc(same & ((1u << lane) - 1));
+      base += __popc(same);
+      if (t >= a.rows) continue;
       if (mask >> k & 1u) {
-        long label;
-        float p, l;
-        row_counts<BACKWARD>(a, t, label, p, l);
         a.row[at] = t;
-        a.label[at] = static_cast<int>(label);
+        a.label[at] = r.label[k];
         if constexpr (BACKWARD) {
           a.place[t] = at;
-          a.coef_p[at] = p / top * up;
-          a.coef_l[at] = l / top * up;
+          a.coef_p[at] = r.p[k] / top * up;
+          a.coef_l[at] = r.l[k] / top * up;
           a.base[at] = a.lse_in[t] * kLog2e;
         }
-        ++at;
       } else if constexpr (BACKWARD) {
         a.place[t] = -1;
       } else {
@@ -121,21 +124,18 @@ __global__ void __launch_bounds__(kRowThreads) vocab_rows_kernel(const VocabArgs
     *a.count = done;
     if constexpr (BACKWARD) *a.scale = top / up;
   }
-  if constexpr (BACKWARD) {  // places behind the last one: no gradient
-    const int end = (done + 255) & ~255;
-    for (int i = done + threadIdx.x; i < end; i += kRowThreads) {
-      a.coef_p[i] = a.coef_l[i] = a.base[i] = 0.f;
-      a.label[i] = -1;
-    }
-  } else {
-    const int end = (done + 255) & ~255;
-    for (int i = done + threadIdx.x; i < end; i += kRowThreads) a.label[i] = -1;
+  // places behind the last one: no label, no gradient
+  for (int i = done + threadIdx.x; i < ((done + 255) & ~255); i += kRowThreads) {
+    a.label[i] = -1;
+    if constexpr (BACKWARD) a.coef_p[i] = a.coef_l[i] = a.base[i] = 0.f;
   }
 }
 
 // ---------------------------------------------------------------- copies
-// xs [count rounded up to 128 (or rows)][ld_xs] = x[row[i]], zeros beyond x's columns
-// and behind the last row: a sum over rows takes them in steps of up to 128.
+// xs [count rounded up to 128][ld_xs] = x[row[i]], zeros beyond x's columns and behind
+// the last row: a sum over rows takes them in steps of up to 128.  TMA could fill those
+// zeros in, but boxes that lie half outside their tensor cost it time: one row and 131072
+// entries of 7168 take 508 us with such boxes, 256 rows 338 us.
 // On the way the label's logit, a dot product in fp32 whose terms are rounded to
 // nearest.  The tensor cores' sums truncate: at d = 7168 their logits are off by some
 // 4e-6 of their size, which the loss of a row that is sure of its label would consist of.
@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(256) vocab_gather_kernel(const VocabArgs a) {
   pdl_wait();
   pdl_trigger();
   const int n = *a.count, chunks = static_cast<int>(a.ld_xs >> 3);
-  const int end = ((n + 127) & ~127) < a.rows ? ((n + 127) & ~127) : a.rows;
+  const int end = (n + 127) & ~127;
   const bool vec_x = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && a.ld_x % 8 == 0 && a.d % 8 == 0;
   const bool vec_w = (reinterpret_cast<uintptr_t>(a.w) & 15) == 0 && a.ld_w % 8 == 0 && a.d % 8 == 0;
   const int me = threadIdx.x % GROUP, warp = threadIdx.x >> 5;
@@ -310,8 +310,8 @@ unsigned blocks_of(long threads, int num_sms) {
 
 template <typename T, bool BACKWARD>
 cudaError_t gather_rows(const VocabArgs &a, int num_sms, cudaStream_t s) {
-  if (a.ld_xs >= kWideRow) return launch_early(vocab_gather_kernel<T, 256, BACKWARD>, blocks_of(a.rows * 256L, num_sms), 256, s, a);
-  return launch_early(vocab_gather_kernel<T, 32, BACKWARD>, blocks_of(a.rows * 32L, num_sms), 256, s, a);
+  if (a.ld_xs >= kWideRow) return launch_early(vocab_gather_kernel<T, 256, BACKWARD>, blocks_of((a.rows + 127L) * 256, num_sms), 256, s, a);
+  return launch_early(vocab_gather_kernel<T, 32, BACKWARD>, blocks_of((a.rows + 127L) * 32, num_sms), 256, s, a);
 }
 
 cudaError_t copies(const VocabArgs &a, bool backward, int num_sms, cudaStream_t s) {

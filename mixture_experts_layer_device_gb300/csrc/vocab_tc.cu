@@ -91,11 +91,29 @@ MOE_DEV uint32_t vocab_idesc(int dtype) {
          (MODE == VOCAB_DX || MODE == VOCAB_DW ? 1u << 16 : 0u) | (32u << 17) | (16u << 24);
 }
 
+MOE_DEV void tmem_ld16_async(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
 // 2^x in the hardware's approximation (2 ulp), 0 below the normal range.
 MOE_DEV float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// LOSS: how many reduction steps one accumulator takes; the epilogue adds those sums in
+// fp32.  An accumulator truncates at every instruction: a chain of 448 of them (d = 7168)
+// left logits 1.3e-5 too low, all alike, which lse and the loss inherit.
+constexpr int kChain = 2048;
+template <int MODE>
+MOE_DEV int chain_of(int klen) {
+  return MODE == VOCAB_LOSS ? kChain : (klen > 0 ? klen : 1);
 }
 
 struct VocabTile {
@@ -268,39 +286,44 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
       const uint32_t idesc = vocab_idesc<MODE>(g.dtype);
       for (int u = pair; u < tiles.total && ok; u += pairs) {
         const VocabTile t = tiles.at(u);
-        if (t.klen == 0) continue;
-        if (!mbar_wait(&tempty[acc], aph ^ 1u, abort_flag, g.status)) break;
-        tc_fence_after();
-        const uint32_t dt = tmem + static_cast<uint32_t>(acc * 256);
-        for (int kb = 0; kb < t.klen; kb += 64 * kBlocks) {
-          if (!mbar_wait(&full[stage], ph, abort_flag, g.status)) {
+        for (int from = 0, chain = chain_of<MODE>(t.klen); from < t.klen && ok; from += chain) {
+          const int to = t.klen - from < chain ? t.klen : from + chain;
+          if (!mbar_wait(&tempty[acc], aph ^ 1u, abort_flag, g.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa0 = smem_u32(smem + stage * kStageBytes);
-          const int left = t.klen - kb;  // steps past the end hold zeros in both operands
+          const uint32_t dt = tmem + static_cast<uint32_t>(acc * 256);
+          for (int kb = from; kb < to; kb += 64 * kBlocks) {
+            if (!mbar_wait(&full[stage], ph, abort_flag, g.status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sa0 = smem_u32(smem + stage * kStageBytes);
+            const int left = to - kb;  // steps past the end hold zeros in both operands
 #pragma unroll
-          for (int k = 0; k < 4 * kBlocks; ++k) {
-            if (k * 16 < left) {
-              const uint32_t sa = sa0 + (k >> 2) * kBlockBytes, sb = sa + 16384;
-              const uint64_t ad = MODE == VOCAB_DW ? mn_desc(sa + 2048 * (k & 3)) : sw128_desc(sa + 32 * (k & 3));
-              const uint64_t bd = MODE == VOCAB_DX || MODE == VOCAB_DW ? mn_desc(sb + 2048 * (k & 3))
-                                                                      : sw128_desc(sb + 32 * (k & 3));
-              mma_bf16_pair(dt, ad, bd, idesc, (kb | k) ? 1u : 0u);
+            for (int k = 0; k < 4 * kBlocks; ++k) {
+              if (k * 16 < left) {
+                const uint32_t sa = sa0 + (k >> 2) * kBlockBytes, sb = sa + 16384;
+                const uint64_t ad = MODE == VOCAB_DW ? mn_desc(sa + 2048 * (k & 3)) : sw128_desc(sa + 32 * (k & 3));
+                const uint64_t bd = MODE == VOCAB_DX || MODE == VOCAB_DW ? mn_desc(sb + 2048 * (k & 3))
+                                                                        : sw128_desc(sb + 32 * (k & 3));
+                mma_bf16_pair(dt, ad, bd, idesc, (kb - from | k) ? 1u : 0u);
+              }
+            }
+            mma_commit_pair_mc(&empty[stage], 3);
+            if (++stage == kStages) {
+              stage = 0;
+              ph ^= 1u;
             }
           }
-          mma_commit_pair_mc(&empty[stage], 3);
-          if (++stage == kStages) {
-            stage = 0;
-            ph ^= 1u;
+          if (!ok) break;
+          mma_commit_pair_mc(&tfull[acc], 3);
+          if (++acc == 2) {
+            acc = 0;
+            aph ^= 1u;
           }
-        }
-        if (!ok) break;
-        mma_commit_pair_mc(&tfull[acc], 3);
-        if (++acc == 2) {
-          acc = 0;
-          aph ^= 1u;
         }
       }
       mma_commit_pair_mc(done, 1);
@@ -313,6 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
     uint8_t *buf = staging + (warp - 2) * kStaging;
     int acc = 0;
     uint32_t aph = 0;
+    bool lost = false;
     for (int u = pair; u < tiles.total; u += pairs) {
       const VocabTile t = tiles.at(u);
       const int row0 = t.m0 + static_cast<int>(rank) * 128 + q * 32, row = row0 + lane;
@@ -329,46 +353,70 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
         else mbar_arrive_remote(peer_smem(tempty_addr, 0));
       };
       if constexpr (MODE == VOCAB_LOSS) {
-        // d >= 1: klen > 0
-        const int hit = g.label[row] - (g.v0 + col0);  // rows are padded to whole tiles
-        float m = -__int_as_float(0x7f800000), s = 0.f;
+        // d >= 1: klen > 0.  All 128 logits in registers: the chains' sums meet there.
+        float z[128];
+        bool first = true;
+        for (int from = kChain; ; from += kChain) {
+          uint32_t *r = reinterpret_cast<uint32_t *>(z);
+          const uint32_t at = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * 256 + half * 128);
+          if (first) {
 #pragma unroll
-        for (int j = 0; j < 128; j += 32) {
-          uint32_t r[32];
-          tmem_ld32_async(tb + j, r);
-          tmem_ld_wait();
-          reg_fence<32>(r);
-          if (j == 96) release();
-          float *z = reinterpret_cast<float *>(r);
-          const int left = g.wp - (col0 + j);  // columns that exist
-          if (left < 32) {
+            for (int j = 0; j < 128; j += 32) tmem_ld32_async(at + j, r + j);
+            tmem_ld_wait();
+            reg_fence<128>(r);
+          } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i >= left) z[i] = -__int_as_float(0x7f800000);
+            for (int j = 0; j < 128; j += 16) {
+              uint32_t more[16];
+              tmem_ld16_async(at + j, more);
+              tmem_ld_wait();
+              reg_fence<16>(more);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) z[j + i] += __uint_as_float(more[i]);
+            }
           }
-          if (__any_sync(0xffffffffu, hit >= j && hit < j + 32)) {  // the label's logit is formed apart
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (hit == j + i) z[i] = -__int_as_float(0x7f800000);
+          tc_fence_before();
+          if (leader) mbar_arrive(&tempty[acc]);
+          else mbar_arrive_remote(peer_smem(smem_u32(&tempty[acc]), 0));
+          if (from >= t.klen) break;
+          first = false;
+          if (++acc == 2) {
+            acc = 0;
+            aph ^= 1u;
           }
-          float top = z[0];
-#pragma unroll
-          for (int i = 1; i < 32; ++i) top = fmaxf(top, z[i]);
-          const float now = fmaxf(m, top);
-          // a maximum that is not finite: exponentials from zero, as the join expects
-          const float from = fabsf(now) <= 3.402823466e38f ? now : 0.f;
-          const float was = fabsf(m) <= 3.402823466e38f ? m : 0.f;
-          const float base = from * kLog2e;
-          float s0 = s == 0.f ? 0.f : s * ex2(was * kLog2e - base), s1 = 0.f;
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            s0 += ex2(fmaf(z[i], kLog2e, -base));
-            s1 += ex2(fmaf(z[i + 1], kLog2e, -base));
+          if (!mbar_wait(&tfull[acc], aph, abort_flag, g.status)) {
+            lost = true;
+            break;
           }
-          s = s0 + s1;
-          m = now;
+          tc_fence_after();
         }
-        if (row < count) g.part[static_cast<long>(row) * g.parts + (t.n0 >> 7) + half] = make_float2(m, s);
+        if (lost) break;
+        const int hit = g.label[row] - (g.v0 + col0);  // rows are padded to whole tiles
+        const int left = g.wp - col0;                  // columns that exist
+        if (left < 128) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i >= left) z[i] = -__int_as_float(0x7f800000);
+        }
+        if (__any_sync(0xffffffffu, hit >= 0 && hit < 128)) {  // the label's logit is formed apart
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (hit == i) z[i] = -__int_as_float(0x7f800000);
+        }
+        float m0 = z[0], m1 = z[1];
+#pragma unroll
+        for (int i = 2; i < 128; i += 2) {
+          m0 = fmaxf(m0, z[i]);
+          m1 = fmaxf(m1, z[i + 1]);
+        }
+        const float m = fmaxf(m0, m1);
+        // a maximum that is not finite: exponentials from zero, as the join expects
+        const float base = fabsf(m) <= 3.402823466e38f ? m * kLog2e : 0.f;
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 128; ++i) s[i & 3] += ex2(fmaf(z[i], kLog2e, -base));
+        if (row < count)
+          g.part[static_cast<long>(row) * g.parts + (t.n0 >> 7) + half] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
       } else if constexpr (MODE == VOCAB_DZ) {
         const float cp = g.coef_p[row], own = g.hit[row], base = g.base[row];
         const int hit = g.label[row] - (g.v0 + col0);
@@ -540,15 +588,16 @@ cudaError_t launch_vocab_tc(const VocabArgs &g, int mode, cudaStream_t s) {
   VocabMaps m = {};
   const void *w = g.pad_w ? g.ws_w : g.w;
   const long ld_w = g.pad_w ? g.ld_ws_w : g.ld_w;
+  const long high = (g.rows + 127L) / 128 * 128;  // rows of the workspace's operands
   const long rt = (g.rows + 255L) / 256, vt = (g.wp + 255L) / 256, dt = (g.d + 255L) / 256;
   if (mode == VOCAB_LOSS || mode == VOCAB_DZ) {
-    if (!map_2d(&m.a, g.dtype, g.xs, g.d, g.rows, g.ld_xs, 64, 128) || !map_2d(&m.b, g.dtype, w, g.d, g.V, ld_w, 64, 128))
+    if (!map_2d(&m.a, g.dtype, g.xs, g.d, high, g.ld_xs, 64, 128) || !map_2d(&m.b, g.dtype, w, g.d, g.V, ld_w, 64, 128))
       return cudaErrorInvalidValue;
     if (mode == VOCAB_LOSS) {
       HostTrace t("vocab_logits", s);
       return launch_mode<VOCAB_LOSS>(m, g, rt * vt, s);
     }
-    if (!map_2d(&m.out, g.dtype, g.dz, g.wp, g.rows, g.width, 64, 32)) return cudaErrorInvalidValue;
+    if (!map_2d(&m.out, g.dtype, g.dz, g.wp, high, g.width, 64, 32)) return cudaErrorInvalidValue;
     HostTrace t("vocab_dlogits", s);
     return launch_mode<VOCAB_DZ>(m, g, rt * vt, s);
   }
@@ -556,14 +605,14 @@ cudaError_t launch_vocab_tc(const VocabArgs &g, int mode, cudaStream_t s) {
     const uint64_t dims[3] = {static_cast<uint64_t>(g.ld_sum), static_cast<uint64_t>(g.rows), static_cast<uint64_t>(g.splits)};
     const uint64_t strides[2] = {static_cast<uint64_t>(g.ld_sum) * 4, static_cast<uint64_t>(g.ld_sum) * 4 * g.rows};
     const uint32_t box[3] = {32, 32, 1};
-    if (!map_2d(&m.a, g.dtype, g.dz, g.wp, g.rows, g.width, 64, 128) ||
+    if (!map_2d(&m.a, g.dtype, g.dz, g.wp, high, g.width, 64, 128) ||
         !map_2d(&m.b, g.dtype, w, g.d, g.V, ld_w, 64, 64) || !host_encode_map(&m.out, MOE_ELEM_FP32, g.sum, 3, dims, strides, box))
       return cudaErrorInvalidValue;
     HostTrace t("vocab_dgrad", s);
     return launch_mode<VOCAB_DX>(m, g, rt * dt * g.splits, s);
   }
   const bool wide = g.grad_dtype == MOE_ELEM_FP32;
-  if (!map_2d(&m.a, g.dtype, g.dz, g.wp, g.rows, g.width, 64, 64) || !map_2d(&m.b, g.dtype, g.xs, g.d, g.rows, g.ld_xs, 64, 64))
+  if (!map_2d(&m.a, g.dtype, g.dz, g.wp, high, g.width, 64, 64) || !map_2d(&m.b, g.dtype, g.xs, g.d, high, g.ld_xs, 64, 64))
     return cudaErrorInvalidValue;
   if (g.vec_dw && !map_2d(&m.out, g.grad_dtype, g.dw, g.d, g.V, g.d, wide ? 32 : 64, 32)) return cudaErrorInvalidValue;
   HostTrace t("vocab_wgrad", s);
