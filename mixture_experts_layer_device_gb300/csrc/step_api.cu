@@ -55,17 +55,29 @@ int vocab_check(const moe_vocab_config *c, moe::VocabArgs *a) {
 // A piece of the vocabulary: as many entries as the gradient of the logits of all rows
 // takes 512 MB for, 4096 at least.
 constexpr int64_t kPieceBytes = 512LL << 20;
-// DX: the piece's reduction is split where its tiles are fewer than two per SM pair.
+// DX: the piece's reduction is split so that the last round of tiles over the SM pairs is
+// full; a split costs a pass of its sums through memory, taken as 2 %.
 constexpr int kPairs = 76;
+int vocab_splits(int64_t units, int64_t most) {
+  int best = 1;
+  double least = 1e30;
+  for (int s = 1; s <= most && s <= 64; ++s) {
+    const double rounds = static_cast<double>((units * s + kPairs - 1) / kPairs) / s * (1.0 + 0.02 * (s - 1));
+    if (rounds < least) {
+      least = rounds;
+      best = s;
+    }
+    if (units * s >= 4 * kPairs) break;
+  }
+  return best;
+}
 void vocab_pieces(moe::VocabArgs *a) {
   const int64_t all = tiles(a->V) * 256;
   int64_t w = kPieceBytes / 2 / (a->rows > 0 ? a->rows : 1) / 256 * 256;
   if (w < 4096) w = 4096;
   a->width = static_cast<int>(w < all ? w : all);
   const int64_t units = tiles(a->rows > 0 ? a->rows : 1) * tiles(a->d);
-  int64_t s = units >= 2 * kPairs ? 1 : (2 * kPairs + units - 1) / units;
-  const int64_t most = a->width / 512 > 0 ? a->width / 512 : 1;
-  a->splits = static_cast<int>(s < most ? s : most);
+  a->splits = vocab_splits(units, std::max<int64_t>(1, a->width / 512));
 }
 
 // Carves the workspace; returns its bytes.

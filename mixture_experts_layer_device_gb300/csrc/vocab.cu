@@ -208,7 +208,8 @@ __global__ void __launch_bounds__(256) vocab_gather_kernel(const VocabArgs a) {
   }
 }
 
-// w's rows into rows that TMA can address: a thread per 8 elements.
+// w's rows into rows that TMA can address: a thread per 8 elements (50001 x 321: 20 us; a
+// warp per row, lanes on neighbouring words, 28 us).
 __global__ void __launch_bounds__(256) vocab_pad_kernel(const VocabArgs a) {
   const int chunks = static_cast<int>(a.ld_ws_w >> 3);
   const long total = static_cast<long>(a.V) * chunks;
@@ -227,34 +228,48 @@ __global__ void __launch_bounds__(256) vocab_pad_kernel(const VocabArgs a) {
 }
 
 // ---------------------------------------------------------------- joins
-// (maximum, sum of 2^((z - maximum) log2 e)) of two sets of logits.  Where the larger
-// maximum is not finite, its exponentials were taken from zero.
+// Parts are (maximum, sum of exponentials from it); where a maximum is not finite, from zero.
 MOE_DEV float from_of(float m) { return fabsf(m) <= 3.402823466e38f ? m : 0.f; }
-MOE_DEV float2 join(float2 a, float2 b) {
-  const float m = fmaxf(a.x, b.x), f = from_of(m);
-  // a set without logits has sum 0, whatever its maximum's distance
-  const float sa = a.y == 0.f ? 0.f : a.y * exp2f((from_of(a.x) - f) * kLog2e);
-  const float sb = b.y == 0.f ? 0.f : b.y * exp2f((from_of(b.x) - f) * kLog2e);
-  return make_float2(m, sa + sb);
-}
 
-// One warp per row that counts.  The parts hold all logits but the label's, z:
+// GROUP threads per row that counts: 32, or the block's 256 for few rows.  The parts hold
+// all logits but the label's, z:
 //   loss = log(1 + S exp(m - z)),  lse = z + loss
 // where that is in range, which keeps a small loss's precision.
+template <int GROUP>
 __global__ void __launch_bounds__(256) vocab_loss_kernel(const VocabArgs a) {
+  __shared__ float tops[8], sums[8];
   pdl_wait();
-  const int n = *a.count, lane = threadIdx.x & 31;
-  for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < n; i += gridDim.x * 8) {
+  const int n = *a.count, me = threadIdx.x % GROUP, warp = threadIdx.x >> 5;
+  for (int i = blockIdx.x * (256 / GROUP) + threadIdx.x / GROUP; i < n; i += gridDim.x * (256 / GROUP)) {
     const float2 *p = a.part + static_cast<long>(i) * a.parts;
-    float2 v = make_float2(-__int_as_float(0x7f800000), 0.f);
-    for (int k = lane; k < a.parts; k += 32) v = join(v, p[k]);
+    float top = -__int_as_float(0x7f800000), s = 0.f;
+#pragma unroll 4
+    for (int k = me; k < a.parts; k += GROUP) top = fmaxf(top, p[k].x);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float2 w = make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o));
-      v = join(v, w);
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if constexpr (GROUP == 256) {
+      if ((threadIdx.x & 31) == 0) tops[warp] = top;
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < 8; ++k) top = fmaxf(top, tops[k]);
     }
-    if (lane == 0) {
-      const float z = a.hit[i], others = from_of(v.x) + logf(v.y);  // -inf: the label is alone
+    const float from = from_of(top);
+#pragma unroll 4
+    for (int k = me; k < a.parts; k += GROUP) {
+      const float2 v = p[k];  // a part without logits has sum 0
+      s += v.y == 0.f ? 0.f : v.y * exp2f((from_of(v.x) - from) * kLog2e);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if constexpr (GROUP == 256) {
+      if ((threadIdx.x & 31) == 0) sums[warp] = s;
+      __syncthreads();
+      s = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += sums[k];
+    }
+    if (me == 0) {
+      const float z = a.hit[i], others = from + logf(s);  // -inf: the label is alone
       float loss, lse;
       if (others <= z) {
         loss = log1pf(expf(others - z));
@@ -267,6 +282,7 @@ __global__ void __launch_bounds__(256) vocab_loss_kernel(const VocabArgs a) {
       a.lse[t] = lse;
       a.loss[t] = loss;
     }
+    if constexpr (GROUP == 256) __syncthreads();  // the shared values have been read
   }
 }
 
@@ -284,6 +300,7 @@ __global__ void __launch_bounds__(256) vocab_dx_kernel(const VocabArgs a, bool v
     const int i = a.place[t];
     if (i >= 0) {
       const float *p = a.sum + i * a.ld_sum + c;
+#pragma unroll 4
       for (int k = 0; k < a.splits; ++k, p += step) {
         const float4 lo = *reinterpret_cast<const float4 *>(p), hi = *reinterpret_cast<const float4 *>(p + 4);
         v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
@@ -340,7 +357,8 @@ cudaError_t launch_vocab_forward(const VocabArgs &a, int num_sms, cudaStream_t s
   if (e == cudaSuccess) e = launch_vocab_tc(a, VOCAB_LOSS, s);
   if (e != cudaSuccess) return e;
   HostTrace t("vocab_loss", s);
-  return launch_early(vocab_loss_kernel, blocks_of(static_cast<long>(a.rows) * 32, num_sms), 256, s, a);
+  if (a.rows <= 8 * num_sms && a.parts > 64) return launch_early(vocab_loss_kernel<256>, a.rows, 256, s, a);
+  return launch_early(vocab_loss_kernel<32>, blocks_of(static_cast<long>(a.rows) * 32, num_sms), 256, s, a);
 }
 
 cudaError_t launch_vocab_backward(const VocabArgs &given, int num_sms, cudaStream_t s) {

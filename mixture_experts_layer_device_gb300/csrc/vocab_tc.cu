@@ -165,7 +165,8 @@ MOE_DEV void stage_rows(const uint32_t *w, uint8_t *buf, int lane) {
 }
 
 // The same piece element by element, for matrices whose rows are no whole 16-byte
-// pieces: each store takes neighbouring columns of one row.
+// pieces: each store takes neighbouring columns of one row.  (In words of 4 bytes, with
+// the odd ends apart: 74 us where this is 49, 515 rows and 50001 x 321.)
 template <typename O>
 MOE_DEV void put_elements(const uint32_t *w, uint8_t *buf, O *out, long ld, int rows, int cols, bool add, int lane) {
   constexpr int COLS = 128 / sizeof(O);
