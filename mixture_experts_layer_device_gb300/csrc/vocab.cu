@@ -55,7 +55,54 @@ struct RowItems {
     }
     return mask;
   }
+  // the largest coefficient; one that is not finite keeps to its own row
+  MOE_DEV float top(unsigned mask) const {
+    float t = 0.f;
+#pragma unroll
+    for (int k = 0; k < kRowItems; ++k) {
+      const float m = fmaxf(fabsf(p[k]), fabsf(l[k]));
+      if ((mask >> k & 1u) && m <= 3.402823466e38f) t = fmaxf(t, m);
+    }
+    return t;
+  }
+  // row t, item k, counts and stands at place `at`
+  MOE_DEV void write(const VocabArgs &a, int k, int t, int at, float top, float up) const {
+    a.row[at] = t;
+    a.label[at] = label[k];
+    if constexpr (BACKWARD) {
+      a.place[t] = at;
+      a.coef_p[at] = p[k] / top * up;
+      a.coef_l[at] = l[k] / top * up;
+      a.base[at] = a.lse_in[t] * kLog2e;
+    }
+  }
+  MOE_DEV void leave_out(const VocabArgs &a, int t) const {
+    if constexpr (BACKWARD) {
+      a.place[t] = -1;
+    } else {
+      a.loss[t] = 0.f;
+      a.lse[t] = 0.f;
+    }
+  }
 };
+
+MOE_DEV float scale_up(const VocabArgs &a) { return a.dtype == MOE_ELEM_FP16 ? 16384.f : 1.f; }
+
+template <bool BACKWARD>
+MOE_DEV void finish_rows(const VocabArgs &a, int n, float top, float up) {
+  *a.status = 0;
+  *a.count = n;
+  if constexpr (BACKWARD) *a.scale = top / up;
+}
+
+// Places behind the last one: no label, no gradient.
+template <bool BACKWARD, int THREADS>
+MOE_DEV void pad_rows(const VocabArgs &a, int n) {
+  for (int i = n + threadIdx.x; i < ((n + 255) & ~255); i += THREADS) {
+    a.label[i] = -1;
+    if constexpr (BACKWARD) a.coef_p[i] = a.coef_l[i] = a.base[i] = 0.f;
+  }
+}
 
 template <bool BACKWARD>
 __global__ void __launch_bounds__(kRowThreads) vocab_rows_kernel(const VocabArgs a) {
@@ -68,11 +115,7 @@ __global__ void __launch_bounds__(kRowThreads) vocab_rows_kernel(const VocabArgs
   if constexpr (BACKWARD) {
     for (int t0 = 0; t0 < a.rows; t0 += kRowThreads * kRowItems) {
       const unsigned mask = r.load(a, t0 + warp * 32 * kRowItems + lane);
-#pragma unroll
-      for (int k = 0; k < kRowItems; ++k) {
-        const float m = fmaxf(fabsf(r.p[k]), fabsf(r.l[k]));  // one that is not finite keeps to its own row
-        if ((mask >> k & 1u) && m <= 3.402823466e38f) top = fmaxf(top, m);
-      }
+      top = fmaxf(top, r.top(mask));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -83,7 +126,7 @@ __global__ void __launch_bounds__(kRowThreads) vocab_rows_kernel(const VocabArgs
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (top == 0.f) top = 1.f;
   }
-  const float up = a.dtype == MOE_ELEM_FP16 ? 16384.f : 1.f;
+  const float up = scale_up(a);
   int done = 0;
   for (int t0 = 0; t0 < a.rows; t0 += kRowThreads * kRowItems) {
     const int first = t0 + warp * 32 * kRowItems + lane;
@@ -102,33 +145,12 @@ __global__ void __launch_bounds__(kRowThreads) vocab_rows_kernel(const VocabArgs
       const int at = base + __popc(same & ((1u << lane) - 1));
       base += __popc(same);
       if (t >= a.rows) continue;
-      if (mask >> k & 1u) {
-        a.row[at] = t;
-        a.label[at] = r.label[k];
-        if constexpr (BACKWARD) {
-          a.place[t] = at;
-          a.coef_p[at] = r.p[k] / top * up;
-          a.coef_l[at] = r.l[k] / top * up;
-          a.base[at] = a.lse_in[t] * kLog2e;
-        }
-      } else if constexpr (BACKWARD) {
-        a.place[t] = -1;
-      } else {
-        a.loss[t] = 0.f;
-        a.lse[t] = 0.f;
-      }
+      if (mask >> k & 1u) r.write(a, k, t, at, top, up);
+      else r.leave_out(a, t);
     }
   }
-  if (threadIdx.x == 0) {
-    *a.status = 0;
-    *a.count = done;
-    if constexpr (BACKWARD) *a.scale = top / up;
-  }
-  // places behind the last one: no label, no gradient
-  for (int i = done + threadIdx.x; i < ((done + 255) & ~255); i += kRowThreads) {
-    a.label[i] = -1;
-    if constexpr (BACKWARD) a.coef_p[i] = a.coef_l[i] = a.base[i] = 0.f;
-  }
+  if (threadIdx.x == 0) finish_rows<BACKWARD>(a, done, top, up);
+  pad_rows<BACKWARD, kRowThreads>(a, done);
 }
 
 // ---------------------------------------------------------------- copies
@@ -155,12 +177,18 @@ MOE_DEV uint4 eight(const T *p, int left, bool vec) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// What a row needs of the rows kernel, in global memory or, where the gather has found the
+// rows itself, in shared memory.
+struct RowList {
+  const int *row, *label;
+  const float *p, *l;
+  int n;
+};
+
 template <typename T, int GROUP, bool BACKWARD>
-__global__ void __launch_bounds__(256) vocab_gather_kernel(const VocabArgs a) {
+MOE_DEV void gather_rows(const VocabArgs &a, const RowList &list) {
   __shared__ float part[8];
-  pdl_wait();
-  pdl_trigger();
-  const int n = *a.count, chunks = static_cast<int>(a.ld_xs >> 3);
+  const int n = list.n, chunks = static_cast<int>(a.ld_xs >> 3);
   const int end = (n + 127) & ~127;
   const bool vec_x = (reinterpret_cast<uintptr_t>(a.x) & 15) == 0 && a.ld_x % 8 == 0 && a.d % 8 == 0;
   const bool vec_w = (reinterpret_cast<uintptr_t>(a.w) & 15) == 0 && a.ld_w % 8 == 0 && a.d % 8 == 0;
@@ -172,8 +200,8 @@ __global__ void __launch_bounds__(256) vocab_gather_kernel(const VocabArgs a) {
       for (int c = me; c < chunks; c += GROUP) to[c] = make_uint4(0, 0, 0, 0);
       continue;  // of whole groups; with GROUP 256 of the whole block
     }
-    const int label = a.label[i];
-    const T *x = static_cast<const T *>(a.x) + a.row[i] * a.ld_x;
+    const int label = list.label[i], from = list.row[i];
+    const T *x = static_cast<const T *>(a.x) + from * a.ld_x;
     const T *w = static_cast<const T *>(a.w) + label * a.ld_w;
     float s = 0.f;
 #pragma unroll 2
@@ -199,8 +227,8 @@ __global__ void __launch_bounds__(256) vocab_gather_kernel(const VocabArgs a) {
     if (me == 0) {
       if constexpr (BACKWARD) {
         // the label's dz: coef_p exp(z - lse) - coef_l, without losing it where exp is near 1
-        const float p = a.coef_p[i], l = a.coef_l[i];
-        a.hit[i] = p == 0.f ? -l : (p - l) + p * expm1f(s - a.lse_in[a.row[i]]);
+        const float p = list.p[i], l = list.l[i];
+        a.hit[i] = p == 0.f ? -l : (p - l) + p * expm1f(s - a.lse_in[from]);
       } else {
         a.hit[i] = s;
       }
@@ -208,8 +236,74 @@ __global__ void __launch_bounds__(256) vocab_gather_kernel(const VocabArgs a) {
   }
 }
 
+template <typename T, int GROUP, bool BACKWARD>
+__global__ void __launch_bounds__(256) vocab_gather_kernel(const VocabArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  gather_rows<T, GROUP, BACKWARD>(a, RowList{a.row, a.label, a.coef_p, a.coef_l, *a.count});
+}
+
+// Up to 256 kRowItems rows: every block finds the rows that count itself (block 0 writes
+// them down), which saves a launch (31 rows, 1000 entries of 256: @@ us, @@ in two).
+template <typename T, int GROUP, bool BACKWARD>
+__global__ void __launch_bounds__(256) vocab_rows_gather_kernel(const VocabArgs a) {
+  constexpr int MOST = 256 * kRowItems;
+  __shared__ int row[MOST], label[MOST], warps[8];
+  __shared__ float p[BACKWARD ? MOST : 1], l[BACKWARD ? MOST : 1], tops[8];
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool writes = blockIdx.x == 0;
+  RowItems<BACKWARD> r;
+  const int first = warp * 32 * kRowItems + lane;
+  const unsigned mask = r.load(a, first);
+  float top = 0.f;
+  if constexpr (BACKWARD) top = r.top(mask);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const int mine = __reduce_add_sync(0xffffffffu, __popc(mask));
+  if (lane == 0) {
+    warps[warp] = mine;
+    tops[warp] = top;
+  }
+  __syncthreads();
+  int base = 0, n = 0;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    if (w < warp) base += warps[w];
+    n += warps[w];
+    top = fmaxf(top, tops[w]);
+  }
+  if (top == 0.f) top = 1.f;
+  const float up = scale_up(a);
+#pragma unroll
+  for (int k = 0; k < kRowItems; ++k) {
+    const int t = first + 32 * k;
+    const unsigned same = __ballot_sync(0xffffffffu, mask >> k & 1u);
+    const int at = base + __popc(same & ((1u << lane) - 1));
+    base += __popc(same);
+    if (t >= a.rows) continue;
+    if (mask >> k & 1u) {
+      row[at] = t;
+      label[at] = r.label[k];
+      if constexpr (BACKWARD) {
+        p[at] = r.p[k] / top * up;
+        l[at] = r.l[k] / top * up;
+      }
+      if (writes) r.write(a, k, t, at, top, up);
+    } else if (writes) {
+      r.leave_out(a, t);
+    }
+  }
+  if (writes) {
+    if (threadIdx.x == 0) finish_rows<BACKWARD>(a, n, top, up);
+    pad_rows<BACKWARD, 256>(a, n);
+  }
+  __syncthreads();
+  gather_rows<T, GROUP, BACKWARD>(a, RowList{row, label, p, l, n});
+}
+
 // w's rows into rows that TMA can address: a thread per 8 elements (50001 x 321: 20 us; a
-// warp per row, lanes on neighbouring words, 28 us).
+// warp per row, lanes on neighbouring words, 28 us; by way of shared memory 20 to 25).
 __global__ void __launch_bounds__(256) vocab_pad_kernel(const VocabArgs a) {
   const int chunks = static_cast<int>(a.ld_ws_w >> 3);
   const long total = static_cast<long>(a.V) * chunks;
@@ -325,28 +419,40 @@ unsigned blocks_of(long threads, int num_sms) {
   return static_cast<unsigned>(want < 1 ? 1 : want < most ? want : most);
 }
 
+template <typename T, int GROUP, bool BACKWARD>
+cudaError_t copy_group(const VocabArgs &a, int num_sms, cudaStream_t s) {
+  const unsigned blocks = blocks_of((a.rows + 127L) * GROUP, num_sms);
+  if (a.rows <= 256 * kRowItems) {
+    HostTrace t("vocab_rows_gather", s);
+    // every block reads all labels: no more blocks than give each a few rows
+    vocab_rows_gather_kernel<T, GROUP, BACKWARD><<<blocks < 2u * num_sms ? blocks : 2u * num_sms, 256, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+  {
+    HostTrace t("vocab_rows", s);
+    vocab_rows_kernel<BACKWARD><<<1, kRowThreads, 0, s>>>(a);
+  }
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  HostTrace t("vocab_gather", s);
+  return launch_early(vocab_gather_kernel<T, GROUP, BACKWARD>, blocks, 256, s, a);
+}
+
 template <typename T, bool BACKWARD>
-cudaError_t gather_rows(const VocabArgs &a, int num_sms, cudaStream_t s) {
-  if (a.ld_xs >= kWideRow) return launch_early(vocab_gather_kernel<T, 256, BACKWARD>, blocks_of((a.rows + 127L) * 256, num_sms), 256, s, a);
-  return launch_early(vocab_gather_kernel<T, 32, BACKWARD>, blocks_of((a.rows + 127L) * 32, num_sms), 256, s, a);
+cudaError_t copy_rows(const VocabArgs &a, int num_sms, cudaStream_t s) {
+  return a.ld_xs >= kWideRow ? copy_group<T, 256, BACKWARD>(a, num_sms, s) : copy_group<T, 32, BACKWARD>(a, num_sms, s);
 }
 
 cudaError_t copies(const VocabArgs &a, bool backward, int num_sms, cudaStream_t s) {
   if (a.pad_w) {
     HostTrace t("vocab_pad", s);
     vocab_pad_kernel<<<blocks_of(static_cast<long>(a.V) * (a.ld_ws_w >> 3), num_sms), 256, 0, s>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
   }
-  {
-    HostTrace t("vocab_rows", s);
-    if (backward) vocab_rows_kernel<true><<<1, kRowThreads, 0, s>>>(a);
-    else vocab_rows_kernel<false><<<1, kRowThreads, 0, s>>>(a);
-  }
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  HostTrace t("vocab_gather", s);
   if (a.dtype == MOE_ELEM_BF16)
-    return backward ? gather_rows<__nv_bfloat16, true>(a, num_sms, s) : gather_rows<__nv_bfloat16, false>(a, num_sms, s);
-  return backward ? gather_rows<__half, true>(a, num_sms, s) : gather_rows<__half, false>(a, num_sms, s);
+    return backward ? copy_rows<__nv_bfloat16, true>(a, num_sms, s) : copy_rows<__nv_bfloat16, false>(a, num_sms, s);
+  return backward ? copy_rows<__half, true>(a, num_sms, s) : copy_rows<__half, false>(a, num_sms, s);
 }
 
 }  // namespace

@@ -82,13 +82,13 @@ MOE_DEV uint64_t mn_desc(uint32_t saddr) {
   return d;
 }
 
-// kind::f16, fp32 accumulation, M = 256 over the pair, N = 256: operand format (1 bf16,
-// 0 fp16) at [7,10) and [10,13), MN-major A / B at bits 15 / 16.
+// kind::f16, fp32 accumulation, M = 256 over the pair: operand format (1 bf16, 0 fp16) at
+// [7,10) and [10,13), MN-major A / B at bits 15 / 16, N >> 3 at [17,23).
 template <int MODE>
-MOE_DEV uint32_t vocab_idesc(int dtype) {
+MOE_DEV uint32_t vocab_idesc(int dtype, int n) {
   const uint32_t f = dtype == MOE_ELEM_BF16 ? 1u : 0u;
   return (1u << 4) | (f << 7) | (f << 10) | (MODE == VOCAB_DW ? 1u << 15 : 0u) |
-         (MODE == VOCAB_DX || MODE == VOCAB_DW ? 1u << 16 : 0u) | (32u << 17) | (16u << 24);
+         (MODE == VOCAB_DX || MODE == VOCAB_DW ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (16u << 24);
 }
 
 MOE_DEV void tmem_ld16_async(uint32_t taddr, uint32_t *r) {
@@ -118,6 +118,7 @@ MOE_DEV int chain_of(int klen) {
 
 struct VocabTile {
   int m0, n0;       // first row and column of the product
+  int n;            // columns: 256, or 128 at the end of an MN-major B
   int k0, klen;     // reduction
   int split;
 };
@@ -126,10 +127,11 @@ struct VocabTile {
 // `splits` parts; DW: vocabulary of the piece x d.
 template <int MODE>
 struct VocabTiles {
-  int nm, nn, splits, k, per, total;
+  int nm, nn, cols, splits, k, per, total;
   MOE_DEV VocabTiles(const VocabArgs &a, int count) {
     nm = ((MODE == VOCAB_DW ? a.wp : count) + 255) >> 8;
-    nn = ((MODE == VOCAB_LOSS || MODE == VOCAB_DZ ? a.wp : a.d) + 255) >> 8;
+    cols = MODE == VOCAB_LOSS || MODE == VOCAB_DZ ? a.wp : a.d;
+    nn = (cols + 255) >> 8;
     splits = MODE == VOCAB_DX ? a.splits : 1;
     k = MODE == VOCAB_DX ? a.wp : MODE == VOCAB_DW ? count : a.d;
     per = ((k + 127) / 128 + splits - 1) / splits * 128;
@@ -144,6 +146,7 @@ struct VocabTiles {
     const int high = nm - band * kBand < kBand ? nm - band * kBand : kBand;
     t.m0 = (band * kBand + in % high) * 256;
     t.n0 = in / high * 256;
+    t.n = (MODE == VOCAB_DX || MODE == VOCAB_DW) && cols - t.n0 <= 128 ? 128 : 256;
     t.k0 = t.split * per;
     t.klen = k - t.k0 < per ? k - t.k0 : per;
     if (t.klen < 0) t.klen = 0;
@@ -207,6 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const bool turns = MODE == VOCAB_DZ || (MODE == VOCAB_LOSS && g.d <= kChain);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
@@ -214,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 2 * 32 * kEpilogueWarps);  // epilogue threads of both CTAs
+      mbar_init(&tempty[a], 2 * 32 * (turns ? kEpilogueWarps / 2 : kEpilogueWarps));  // epilogue threads of both CTAs
     }
     mbar_init(done, 1);
     *abort_flag = 0;
@@ -243,14 +247,15 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
       bool ok = true;
       for (int u = pair; u < tiles.total && ok && !*abort_flag; u += pairs) {
         const VocabTile t = tiles.at(u);
-        const int ar = t.m0 + static_cast<int>(rank) * 128, br = t.n0 + static_cast<int>(rank) * 128;
+        const int ar = t.m0 + static_cast<int>(rank) * 128, br = t.n0 + static_cast<int>(rank) * (t.n >> 1);
+        const uint32_t bytes = t.n == 256 ? 32768u : 24576u;  // of a block, per CTA
         for (int kb = 0; kb < t.klen; kb += 64 * kBlocks) {
           if (!mbar_wait(&empty[stage], ph ^ 1u, abort_flag, g.status)) {
             ok = false;
             break;
           }
           const int blocks = t.klen - kb > 64 ? kBlocks : 1;
-          if (leader) mbar_arrive_expect_tx(&full[stage], 2u * blocks * kBlockBytes);
+          if (leader) mbar_arrive_expect_tx(&full[stage], 2u * blocks * bytes);
           const uint32_t bar = peer_smem(smem_u32(&full[stage]), 0);
 #pragma unroll
           for (int b = 0; b < kBlocks; ++b) {
@@ -266,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
             if constexpr (MODE == VOCAB_DX || MODE == VOCAB_DW) {
               const int kr = MODE == VOCAB_DX ? g.v0 + k : k;
               tma_load_2d_pair(&maps.b, bar, sb, br, kr);
-              tma_load_2d_pair(&maps.b, bar, sb + 8192, br + 64, kr);
+              if (t.n == 256) tma_load_2d_pair(&maps.b, bar, sb + 8192, br + 64, kr);
             } else {
               tma_load_2d_pair(&maps.b, bar, sb, k, g.v0 + br);
             }
@@ -284,9 +289,9 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
       int stage = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
       bool ok = true;
-      const uint32_t idesc = vocab_idesc<MODE>(g.dtype);
       for (int u = pair; u < tiles.total && ok; u += pairs) {
         const VocabTile t = tiles.at(u);
+        const uint32_t idesc = vocab_idesc<MODE>(g.dtype, t.n);
         for (int from = 0, chain = chain_of<MODE>(t.klen); from < t.klen && ok; from += chain) {
           const int to = t.klen - from < chain ? t.klen : from + chain;
           if (!mbar_wait(&tempty[acc], aph ^ 1u, abort_flag, g.status)) {
@@ -333,124 +338,132 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
     }
   } else {
     // ------------------------------------------------ epilogue (warps 2..9, both CTAs)
-    const int q = warp & 3, half = (warp - 2) >> 2;  // accumulator rows; which half of its columns
+    // Two groups of four warps.  Where a tile is one accumulator (LOSS of rows up to kChain,
+    // DZ) they take tiles in turns, so that one's exponentials run beside the other's
+    // loads; else each takes half of the columns.
+    const int q = warp & 3, group = (warp - 2) >> 2;
     uint8_t *buf = staging + (warp - 2) * kStaging;
-    int acc = 0;
-    uint32_t aph = 0;
+    uint32_t seq = 0;  // accumulators that the pair has taken
     bool lost = false;
-    for (int u = pair; u < tiles.total; u += pairs) {
+    for (int u = pair, i = 0; u < tiles.total && !lost; u += pairs, ++i) {
+      if (turns && (i & 1) != group) {
+        ++seq;
+        continue;
+      }
       const VocabTile t = tiles.at(u);
       const int row0 = t.m0 + static_cast<int>(rank) * 128 + q * 32, row = row0 + lane;
-      const int col0 = t.n0 + half * 128;
-      const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * 256 + half * 128);
+      const int col0 = t.n0 + group * 128;
+      const uint32_t lanes = tmem + (static_cast<uint32_t>(q * 32) << 16);
+      uint32_t tb = lanes + (seq & 1) * 256 + group * 128;
       if (t.klen > 0) {
-        if (!mbar_wait(&tfull[acc], aph, abort_flag, g.status)) break;
+        if (!mbar_wait(&tfull[seq & 1], seq >> 1 & 1, abort_flag, g.status)) break;
         tc_fence_after();
       }
-      const uint32_t tempty_addr = smem_u32(&tempty[acc]);
       auto release = [&]() {
         tc_fence_before();
-        if (leader) mbar_arrive(&tempty[acc]);
-        else mbar_arrive_remote(peer_smem(tempty_addr, 0));
+        if (leader) mbar_arrive(&tempty[seq & 1]);
+        else mbar_arrive_remote(peer_smem(smem_u32(&tempty[seq & 1]), 0));
       };
       if constexpr (MODE == VOCAB_LOSS) {
-        // d >= 1: klen > 0.  All 128 logits in registers: the chains' sums meet there.
-        float z[128];
-        bool first = true;
-        for (int from = kChain; ; from += kChain) {
+        // d >= 1: klen > 0.  128 logits in registers at a time: the chains' sums meet there.
+        const int label = g.label[row] - g.v0;  // rows are padded to whole tiles
+        for (int part = turns ? 0 : group; part < (turns ? 2 : group + 1); ++part) {
+          float z[128];
           uint32_t *r = reinterpret_cast<uint32_t *>(z);
-          const uint32_t at = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * 256 + half * 128);
-          if (first) {
+          tb = lanes + (seq & 1) * 256 + part * 128;
 #pragma unroll
-            for (int j = 0; j < 128; j += 32) tmem_ld32_async(at + j, r + j);
-            tmem_ld_wait();
-            reg_fence<128>(r);
-          } else {
+          for (int j = 0; j < 128; j += 32) tmem_ld32_async(tb + j, r + j);
+          tmem_ld_wait();
+          reg_fence<128>(r);
+          if (!turns || part == 1) release();
+          for (int from = kChain; from < t.klen; from += kChain) {
+            ++seq;
+            if (!mbar_wait(&tfull[seq & 1], seq >> 1 & 1, abort_flag, g.status)) {
+              lost = true;
+              break;
+            }
+            tc_fence_after();
+            tb = lanes + (seq & 1) * 256 + part * 128;
 #pragma unroll
             for (int j = 0; j < 128; j += 16) {
               uint32_t more[16];
-              tmem_ld16_async(at + j, more);
+              tmem_ld16_async(tb + j, more);
               tmem_ld_wait();
               reg_fence<16>(more);
 #pragma unroll
               for (int i = 0; i < 16; ++i) z[j + i] += __uint_as_float(more[i]);
             }
+            release();
           }
-          tc_fence_before();
-          if (leader) mbar_arrive(&tempty[acc]);
-          else mbar_arrive_remote(peer_smem(smem_u32(&tempty[acc]), 0));
-          if (from >= t.klen) break;
-          first = false;
-          if (++acc == 2) {
-            acc = 0;
-            aph ^= 1u;
+          if (lost) break;
+          const int first = t.n0 + part * 128, hit = label - first;
+          const int left = g.wp - first;  // columns that exist
+          if (left < 128) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              if (i >= left) z[i] = -__int_as_float(0x7f800000);
           }
-          if (!mbar_wait(&tfull[acc], aph, abort_flag, g.status)) {
-            lost = true;
-            break;
+          if (__any_sync(0xffffffffu, hit >= 0 && hit < 128)) {  // the label's logit is formed apart
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              if (hit == i) z[i] = -__int_as_float(0x7f800000);
           }
-          tc_fence_after();
-        }
-        if (lost) break;
-        const int hit = g.label[row] - (g.v0 + col0);  // rows are padded to whole tiles
-        const int left = g.wp - col0;                  // columns that exist
-        if (left < 128) {
+          float m0 = z[0], m1 = z[1];
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i >= left) z[i] = -__int_as_float(0x7f800000);
-        }
-        if (__any_sync(0xffffffffu, hit >= 0 && hit < 128)) {  // the label's logit is formed apart
+          for (int i = 2; i < 128; i += 2) {
+            m0 = fmaxf(m0, z[i]);
+            m1 = fmaxf(m1, z[i + 1]);
+          }
+          const float m = fmaxf(m0, m1);
+          // a maximum that is not finite: exponentials from zero, as the join expects
+          const float base = fabsf(m) <= 3.402823466e38f ? m * kLog2e : 0.f;
+          float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (hit == i) z[i] = -__int_as_float(0x7f800000);
+          for (int i = 0; i < 128; ++i) s[i & 3] += ex2(fmaf(z[i], kLog2e, -base));
+          if (row < count)
+            g.part[static_cast<long>(row) * g.parts + (t.n0 >> 7) + part] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
         }
-        float m0 = z[0], m1 = z[1];
-#pragma unroll
-        for (int i = 2; i < 128; i += 2) {
-          m0 = fmaxf(m0, z[i]);
-          m1 = fmaxf(m1, z[i + 1]);
-        }
-        const float m = fmaxf(m0, m1);
-        // a maximum that is not finite: exponentials from zero, as the join expects
-        const float base = fabsf(m) <= 3.402823466e38f ? m * kLog2e : 0.f;
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 128; ++i) s[i & 3] += ex2(fmaf(z[i], kLog2e, -base));
-        if (row < count)
-          g.part[static_cast<long>(row) * g.parts + (t.n0 >> 7) + half] = make_float2(m, (s[0] + s[1]) + (s[2] + s[3]));
       } else if constexpr (MODE == VOCAB_DZ) {
+        // out through the staging by plain stores: nothing to wait for between pieces
         const float cp = g.coef_p[row], own = g.hit[row], base = g.base[row];
-        const int hit = g.label[row] - (g.v0 + col0);
-#pragma unroll
-        for (int j = 0; j < 128; j += 64) {
-          uint32_t r[64], w[32];
-          tmem_ld32_async(tb + j, r);
-          tmem_ld32_async(tb + j + 32, r + 32);
+        const int label = g.label[row] - (g.v0 + t.n0);
+        const gemm_detail::OutView out = gemm_detail::out_view(g.dz, g.width, (g.rows + 127L) / 128 * 128, 2);
+#pragma unroll 1
+        for (int j = 0; j < 256; j += 64) {
+          uint32_t r[64];
+          tb = lanes + (seq & 1) * 256 + j;
+          tmem_ld32_async(tb, r);
+          tmem_ld32_async(tb + 32, r + 32);
           tmem_ld_wait();
           reg_fence<64>(r);
-          if (j == 64) release();
+          if (j == 192) release();
+          if (t.n0 + j >= g.wp) continue;
           float *z = reinterpret_cast<float *>(r);
           // no coefficient, no term: what z holds there does not matter
 #pragma unroll
           for (int i = 0; i < 64; ++i) z[i] = cp == 0.f ? 0.f : cp * ex2(fmaf(z[i], kLog2e, -base));
-          if (__any_sync(0xffffffffu, hit >= j && hit < j + 64)) {
+          const int hit = label - j;
+          if (__any_sync(0xffffffffu, hit >= 0 && hit < 64)) {
 #pragma unroll
             for (int i = 0; i < 64; ++i)
-              if (hit == j + i) z[i] = own;
+              if (hit == i) z[i] = own;
           }
 #pragma unroll
-          for (int i = 0; i < 32; ++i) w[i] = Elem<T>::pack2(z[2 * i], z[2 * i + 1]);
-          if (col0 + j >= g.wp) continue;
-          stage_rows(w, buf, lane);
-          if (lane == 0) {
-            tma_store_2d(&maps.out, buf, col0 + j, row0);
-            bulk_commit();
+          for (int h = 0; h < 2; ++h) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = Elem<T>::pack2(z[32 * h + 2 * i], z[32 * h + 2 * i + 1]);
+            gemm_detail::Stager(buf + h * 2048).put(out, w, t.n0 + j + 32 * h, row0, lane);
           }
         }
       } else if constexpr (MODE == VOCAB_DX) {
 #pragma unroll 1
         for (int j = 0; j < 128; j += 32) {
           uint32_t r[32];
+          if (group * 128 >= t.n) {  // the narrow tile's columns are the first group's
+            if (t.klen > 0) release();
+            break;
+          }
           if (t.klen > 0) {
             tmem_ld32_async(tb + j, r);
             tmem_ld_wait();
@@ -474,6 +487,10 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
 #pragma unroll 1
         for (int j = 0; j < 128; j += STEP) {
           uint32_t r[STEP], w[32];
+          if (group * 128 >= t.n) {
+            if (t.klen > 0) release();
+            break;
+          }
           if (t.klen > 0) {
             tmem_ld32_async(tb + j, r);
             if (!WIDE) tmem_ld32_async(tb + j + 32, r + STEP - 32);
@@ -507,12 +524,9 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
           }
         }
       }
-      if (t.klen > 0 && ++acc == 2) {
-        acc = 0;
-        aph ^= 1u;
-      }
+      if (t.klen > 0) ++seq;
     }
-    if (MODE != VOCAB_LOSS && lane == 0) bulk_wait<0>();
+    if ((MODE == VOCAB_DX || MODE == VOCAB_DW) && lane == 0) bulk_wait<0>();
   }
 
   __syncthreads();
@@ -598,7 +612,6 @@ cudaError_t launch_vocab_tc(const VocabArgs &g, int mode, cudaStream_t s) {
       HostTrace t("vocab_logits", s);
       return launch_mode<VOCAB_LOSS>(m, g, rt * vt, s);
     }
-    if (!map_2d(&m.out, g.dtype, g.dz, g.wp, high, g.width, 64, 32)) return cudaErrorInvalidValue;
     HostTrace t("vocab_dlogits", s);
     return launch_mode<VOCAB_DZ>(m, g, rt * vt, s);
   }
