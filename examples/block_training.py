@@ -1,10 +1,12 @@
 """Trains a small mixture-of-experts token model with everything the library has
 around the layer: embedding -> [norm -> MoE layer -> norm, gate, residual] ->
-[ragged experts of another activation -> norm, gate, residual] -> logits.
+[ragged experts of another activation -> norm, gate, residual] -> [gated dense block
+-> norm, gate, residual] -> the loss over the vocabulary, and gradients clipped into
+the fp32 masters.
 
 Block 1 is the MoE layer itself (router, SwiGLU experts).  Block 2 is built by
 hand from moe_route's offsets and two GroupedLinear maps with a squared ReLU
-between them: experts of the user's own.  The task is to name the token itself,
+between them: experts of the user's own.  Block 3 is a dense GatedLinear of one group.  The task is to name the token itself,
 so the loss falls from log V as the model learns to pass it on.
 
     python examples/block_training.py [--steps 60] [--tokens 512]
@@ -19,7 +21,8 @@ import torch
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
 import mixture_experts_layer_device_gb300 as moe_lib  # noqa: E402
-from mixture_experts_layer_device_gb300.module import BlockNorm, GroupedLinear, MoE, TokenEmbedding  # noqa: E402
+from mixture_experts_layer_device_gb300.module import (BlockNorm, GatedLinear, GroupedLinear, MoE,  # noqa: E402
+                                                       TokenEmbedding, VocabLoss, clip_gradients)
 
 
 class RaggedExperts(torch.nn.Module):
@@ -58,16 +61,20 @@ class Model(torch.nn.Module):
         self.moe = MoE(T, d, m, E, k, fmt="bf16", router=True)
         self.between = BlockNorm(d, post=True, pre=True, gate="channel")       # x + g norm(f), and the next norm
         self.experts = RaggedExperts(T, d, m, E, k)
+        self.then = BlockNorm(d, post=True, pre=True, gate="channel")
+        self.up, self.down = GatedLinear(1, 2 * m, d, act="gelu"), GroupedLinear(1, d, 2 * m)   # one group of all tokens
         self.last = BlockNorm(d, post=True, pre=True, gate="channel")
-        self.head = GroupedLinear(1, V, d)                                     # logits: one group of all tokens
+        self.head = VocabLoss(V, d)
         self.all_rows = torch.tensor([0, T], dtype=torch.int32, device="cuda")
 
     def forward(self, ids):
         x = self.embed(ids)
         _, h = self.first(x)
         x, h = self.between(x, self.moe(h))
-        _, h = self.last(x, self.experts(h))
-        return self.head(h, self.all_rows)
+        x, h = self.then(x, self.experts(h))
+        _, h = self.last(x, self.down(self.up(h, self.all_rows), self.all_rows))
+        loss, _ = self.head(h, ids)                                            # padding does not count
+        return loss.sum() / (ids >= 0).sum()
 
 
 def train(steps=60, tokens=512, lr=0.002, seed=0, say=print):
@@ -82,11 +89,11 @@ def train(steps=60, tokens=512, lr=0.002, seed=0, say=print):
     for step in range(steps):
         ids = torch.randint(0, V // 8, (tokens,), device="cuda")
         ids[:: 17] = -1                                                        # padding
-        loss = torch.nn.functional.cross_entropy(model(ids).float(), ids, ignore_index=-1)
+        loss = model(ids)
         loss.backward()
         with torch.no_grad():
-            for p, m in zip(params, masters):
-                m.grad = None if p.grad is None else p.grad.float()
+            clip_gradients(params, 1.0, masters)                               # into the masters' .grad
+            for p in params:
                 p.grad = None
             opt.step()
             for p, m in zip(params, masters):

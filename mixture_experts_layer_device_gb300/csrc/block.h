@@ -70,6 +70,7 @@ struct GroupedArgs {
   bool chained;  // tensor-core path: starts before the launch in front has ended (dgrad and wgrad of one call)
   bool vec_out;  // tensor-core path: the output's rows are whole 16-byte pieces
   int *status;   // workspace status word
+  int most;      // tensor-core path: tokens of a tile at most
   int *tiles;    // workspace: the plan's tile table (3 E + 3 ints)
   int *order;    // workspace: the experts by descending rows, and how many have any (weight gradient)
   uint8_t *maps; // workspace: 2 E tensor maps of 128 bytes (weight gradient)

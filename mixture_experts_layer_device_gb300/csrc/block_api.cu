@@ -41,6 +41,7 @@ int grouped_check(const moe_grouped_config *c, moe::GroupedArgs *g) {
   g->dtype = c->dtype;
   g->out_dtype = c->out_dtype;
   g->accumulate = c->accumulate;
+  g->most = 256;
   return MOE_OK;
 }
 

@@ -28,11 +28,12 @@ MOE_DEV int group_of_tile(const int *tiles, int E, int u) {
 }
 
 // ---------------------------------------------------------------- token tiles
-// How the tensor-core kernel cuts an expert's rows: as few tiles of up to 256
-// tokens as hold them, all of one size (a multiple of 32) but the last.
+// How the tensor-core kernel cuts an expert's rows: as few tiles of up to `most`
+// tokens (256; fewer in small calls) as hold them, all of one size (a multiple of 32)
+// but the last.
 constexpr int kTileTokens = 256;
-MOE_DEV int tile_tokens(int rows) {
-  const int tiles = (rows + kTileTokens - 1) / kTileTokens;
+MOE_DEV int tile_tokens(int rows, int most) {
+  const int tiles = (rows + most - 1) / most;
   return ((rows + tiles - 1) / tiles + 31) & ~31;
 }
 
@@ -83,7 +84,7 @@ MOE_DEV bool build_tile_table(const GroupedArgs &g, int *p, int *scratch) {
   for (int c = 0; c < CLASSES; ++c) mine[c] = 0;
   auto cls_of = [&](int e) {
     const int rows = e < to && !any ? off[e + 1] - off[e] : 0;
-    return rows > 0 ? CLASSES - (tile_tokens(rows) >> 5) : -1;  // 0: the largest
+    return rows > 0 ? CLASSES - (tile_tokens(rows, g.most) >> 5) : -1;  // 0: the largest
   };
   for (int e0 = from; e0 < to; e0 += 32) {
     const int c = cls_of(e0 + lane);
@@ -121,7 +122,7 @@ MOE_DEV bool build_tile_table(const GroupedArgs &g, int *p, int *scratch) {
     const int i = i0 + threadIdx.x;
     int n = 0;
     if (i < total) {
-      const int e = order[i], rows = off[e + 1] - off[e], size = tile_tokens(rows);
+      const int e = order[i], rows = off[e + 1] - off[e], size = tile_tokens(rows, g.most);
       n = (rows + size - 1) / size;
     }
     int inc = n;

@@ -52,6 +52,7 @@ static_assert(kSmem <= 232448, "shared memory");
 // Forward and dgrad stage 2 KB per warp and keep the tile table in the rest of
 // the staging; more experts than it holds take the plan launch's table.
 constexpr int kTablePlace = kEpilogueWarps * 2048;
+constexpr int kPairs = 76;
 constexpr int kTableExperts = ((kEpilogueWarps * kStaging - kTablePlace) / 4 - 3) / 3;
 
 struct TcMaps {
@@ -166,7 +167,7 @@ struct TcTiles {
       const int i = group_of_tile(t.first, t.n, u / nf);
       const int first = t.first[i], mt = t.first[i + 1] - first, local = u - first * nf;
       r.e = t.order[i];
-      const int lo = t.off[r.e], rows = t.off[r.e + 1] - lo, size = tile_tokens(rows);
+      const int lo = t.off[r.e], rows = t.off[r.e + 1] - lo, size = tile_tokens(rows, g.most);
       r.f0 = (local / mt) * (DIR == GROUPED_GATED ? 128 : 256);
       const int from = (local % mt) * size;
       r.c0 = lo + from;
@@ -841,9 +842,24 @@ cudaError_t launch_maps(const GroupedArgs &g, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// Tiles of fewer tokens where even they all run in one round over the SM pairs: the
+// reduction's length bounds a small call, and half a tile takes half of it (gated forward,
+// 1500 rows of [256, 128]: 8.1 us, 12.6 with tiles of 256; 2043 rows, 8 experts of [512,
+// 768]: 12.8 and 15.7).  Not where the weight gradient runs beside the data gradient on the
+// pairs that it leaves (2043 rows of [3074, 768]: 42 us both, 30 with tiles of 256).  An
+// element's sum is the same in any tile.
+int most_tokens(const GroupedArgs &g, int dir) {
+  const long features = dir == GROUPED_GATED ? (g.N / 2 + 127) / 128 : ((dir == GROUPED_DGRAD ? g.K : g.N) + 255) / 256;
+  const long experts = g.E < g.rows ? g.E : g.rows;
+  int most = kTileTokens;
+  while (!g.chained && most > 64 && ((g.rows + most / 2 - 1L) / (most / 2) + experts) * features <= kPairs) most /= 2;
+  return most;
+}
+
 // The product itself, after plan_first or launch_maps.
-cudaError_t launch_product(const GroupedArgs &g, int dir, cudaStream_t s) {
+cudaError_t launch_product(const GroupedArgs &given, int dir, cudaStream_t s) {
   TcMaps m = {};
+  GroupedArgs g = given;
   if (dir == GROUPED_WGRAD) {
     const bool wide = g.out_dtype == MOE_ELEM_FP32;
     if (g.vec_out && !expert_map(&m.out, g.out_dtype, g.dw, g, g.K, static_cast<long>(g.N) * g.K, wide ? 32 : 64, 32))
@@ -851,7 +867,8 @@ cudaError_t launch_product(const GroupedArgs &g, int dir, cudaStream_t s) {
     HostTrace t("grouped_wgrad", s);
     return launch_tc<GROUPED_WGRAD>(m, g, static_cast<long>(g.E) * ((g.N + 255) / 256) * ((g.K + 255) / 256), s);
   }
-  const long tokens = (g.rows + kTileTokens - 1L) / kTileTokens + (g.E < g.rows ? g.E : g.rows);
+  g.most = most_tokens(g, dir);
+  const long tokens = (g.rows + g.most - 1L) / g.most + (g.E < g.rows ? g.E : g.rows);
   if (dir == GROUPED_GATED) {
     if (!row_maps(m.b, g.dtype, g.x, g.rows, g.K, g.in_x) || !gated_map(&m.a, g)) return cudaErrorInvalidValue;
     HostTrace t("gated_forward", s);
