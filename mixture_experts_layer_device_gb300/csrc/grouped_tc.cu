@@ -846,13 +846,14 @@ cudaError_t launch_maps(const GroupedArgs &g, cudaStream_t s) {
 // reduction's length bounds a small call, and half a tile takes half of it (gated forward,
 // 1500 rows of [256, 128]: 8.1 us, 12.6 with tiles of 256; 2043 rows, 8 experts of [512,
 // 768]: 12.8 and 15.7).  Not where the weight gradient runs beside the data gradient on the
-// pairs that it leaves (2043 rows of [3074, 768]: 42 us both, 30 with tiles of 256).  An
-// element's sum is the same in any tile.
+// pairs that it leaves (2043 rows of [3074, 768]: 42 us both, 30 with tiles of 256), and not
+// where the plan launch has made the table, with tiles of 256.  An element's sum is the
+// same in any tile.
 int most_tokens(const GroupedArgs &g, int dir) {
   const long features = dir == GROUPED_GATED ? (g.N / 2 + 127) / 128 : ((dir == GROUPED_DGRAD ? g.K : g.N) + 255) / 256;
   const long experts = g.E < g.rows ? g.E : g.rows;
   int most = kTileTokens;
-  while (!g.chained && most > 64 && ((g.rows + most / 2 - 1L) / (most / 2) + experts) * features <= kPairs) most /= 2;
+  while (!g.chained && g.E <= kTableExperts && most > 64 && ((g.rows + most / 2 - 1L) / (most / 2) + experts) * features <= kPairs) most /= 2;
   return most;
 }
 

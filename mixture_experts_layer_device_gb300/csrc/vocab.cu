@@ -458,7 +458,7 @@ cudaError_t copies(const VocabArgs &a, bool backward, int num_sms, cudaStream_t 
 }  // namespace
 
 cudaError_t launch_vocab_forward(const VocabArgs &a, int num_sms, cudaStream_t s) {
-  if (a.rows == 0) return cudaSuccess;
+  if (a.rows == 0) return cudaMemsetAsync(a.status, 0, 256, s);
   cudaError_t e = copies(a, false, num_sms, s);
   if (e == cudaSuccess) e = launch_vocab_tc(a, VOCAB_LOSS, s);
   if (e != cudaSuccess) return e;
