@@ -590,7 +590,7 @@ def _tensors(ts, gpu, name):
     types = list(map(_ELEM.get, map(_type_of, ts)))
     if None in types:
         _bad("%s are bf16, fp16 or fp32", name)
-    return array("i", types), array("q", map(_numel, ts)), array("Q", map(_address, ts))
+    return array("i", types), array("q", list(map(_numel, ts))), array("Q", list(map(_address, ts)))
 
 
 def _host(a):

@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 2 * 32 * kEpilogueWarps);  // epilogue threads of both CTAs
+      mbar_init(&tempty[a], 2 * kEpilogueWarps);  // epilogue warps of both CTAs
     }
     mbar_init(done, 1);
     *abort_flag = 0;
@@ -548,10 +548,14 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
         tc_fence_after();
       }
       const uint32_t tempty_addr = smem_u32(&tempty[acc]);
+      // one arrival per warp: one per thread took the other CTA's some 1600 cycles a tile
       auto release = [&]() {
         tc_fence_before();
-        if (leader) mbar_arrive(&tempty[acc]);
-        else mbar_arrive_remote(peer_smem(tempty_addr, 0));
+        __syncwarp();
+        if (lane == 0) {
+          if (leader) mbar_arrive(&tempty[acc]);
+          else mbar_arrive_remote(peer_smem(tempty_addr, 0));
+        }
       };
       bool held = t.klen > 0;  // this warp has not released the accumulator yet
       if constexpr (DIR == GROUPED_WGRAD) {

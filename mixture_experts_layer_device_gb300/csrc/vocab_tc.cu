@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 2 * 32 * (turns ? kEpilogueWarps / 2 : kEpilogueWarps));  // epilogue threads of both CTAs
+      mbar_init(&tempty[a], 2 * (turns ? kEpilogueWarps / 2 : kEpilogueWarps));  // epilogue warps of both CTAs
     }
     mbar_init(done, 1);
     *abort_flag = 0;
@@ -359,10 +359,15 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
         if (!mbar_wait(&tfull[seq & 1], seq >> 1 & 1, abort_flag, g.status)) break;
         tc_fence_after();
       }
+      // one arrival per warp: one per thread took the other CTA's 1600 cycles a tile (5 rows,
+      // 131072 x 4096: the weight gradient 264 us, @@ so)
       auto release = [&]() {
         tc_fence_before();
-        if (leader) mbar_arrive(&tempty[seq & 1]);
-        else mbar_arrive_remote(peer_smem(smem_u32(&tempty[seq & 1]), 0));
+        __syncwarp();
+        if (lane == 0) {
+          if (leader) mbar_arrive(&tempty[seq & 1]);
+          else mbar_arrive_remote(peer_smem(smem_u32(&tempty[seq & 1]), 0));
+        }
       };
       if constexpr (MODE == VOCAB_LOSS) {
         // d >= 1: klen > 0.  128 logits in registers at a time: the chains' sums meet there.
