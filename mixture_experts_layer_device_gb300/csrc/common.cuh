@@ -376,6 +376,13 @@ MOE_DEV void mbar_arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
 }
+// The same where no ordinary memory is handed over, only an accumulator whose TMEM loads
+// have been waited for (tcgen05.wait::ld, then tcgen05.fence::before_thread_sync): a
+// release at cluster scope first waits for the thread's earlier writes, some 1600 cycles
+// while an epilogue's stores are on their way.
+MOE_DEV void mbar_arrive_remote_tmem(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
 // TMA load into this CTA's shared memory whose completion is signalled on an
 // mbarrier of either CTA of the pair (here: the pair leader's).
 MOE_DEV void tma_load_2d_pair(const CUtensorMap *map, uint32_t mbar_cluster_addr, void *dst, int c0,

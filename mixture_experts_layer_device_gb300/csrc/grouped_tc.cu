@@ -554,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
         __syncwarp();
         if (lane == 0) {
           if (leader) mbar_arrive(&tempty[acc]);
-          else mbar_arrive_remote(peer_smem(tempty_addr, 0));
+          else mbar_arrive_remote_tmem(peer_smem(tempty_addr, 0));
         }
       };
       bool held = t.klen > 0;  // this warp has not released the accumulator yet

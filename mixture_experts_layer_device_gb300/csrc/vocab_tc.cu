@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
         __syncwarp();
         if (lane == 0) {
           if (leader) mbar_arrive(&tempty[seq & 1]);
-          else mbar_arrive_remote(peer_smem(smem_u32(&tempty[seq & 1]), 0));
+          else mbar_arrive_remote_tmem(peer_smem(smem_u32(&tempty[seq & 1]), 0));
         }
       };
       if constexpr (MODE == VOCAB_LOSS) {
