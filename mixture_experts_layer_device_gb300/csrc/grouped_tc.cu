@@ -548,7 +548,9 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
         tc_fence_after();
       }
       const uint32_t tempty_addr = smem_u32(&tempty[acc]);
-      // one arrival per warp: one per thread took the other CTA's some 1600 cycles a tile
+      // one arrival per warp, without an order of its own at cluster scope: one per thread that
+      // had it took the other CTA's warps some 1600 cycles a tile (60 experts of 128 rows, [4096,
+      // 7168]: the weight gradient 843 us, 567 so)
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();

@@ -18,7 +18,7 @@
 // Roles per CTA (320 threads) as in the grouped products: TMA producer, MMA issuer
 // (leader CTA), eight epilogue warps; three 64 KB stages of two blocks of 64
 // reduction steps; two accumulators of 256 TMEM columns.  Persistent over pairs.
-// Tiles are taken in bands of kBand row tiles, so that a band's rows stay in L2
+// Tiles are taken in bands of a few row tiles, so that a band's rows stay in L2
 // while the other operand streams by.  Every wait is bounded (mbar_wait).
 #include <type_traits>
 
@@ -40,7 +40,11 @@ constexpr int kBlocks = 2, kStages = 3;
 constexpr int kStageBytes = kBlocks * kBlockBytes;
 constexpr size_t kSmem = 1024 + kStages * kStageBytes + kEpilogueWarps * kStaging + (2 * kStages + 5) * 8 + 16;
 static_assert(kSmem <= 232448, "shared memory");
-constexpr int kBand = 8;
+// Row tiles of a band (16384 rows, 131072 x 4096, logits of the forward: 10.69 ms with 4,
+// 10.04 with 8, 9.99 with 12, 9.92 with 16, 10.0 with 32; the backward's products are best
+// with 8 to 12).
+template <int MODE>
+constexpr int kBand = MODE == VOCAB_LOSS ? 16 : 8;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 struct VocabMaps {
@@ -142,9 +146,10 @@ struct VocabTiles {
     const int plane = nm * nn;
     t.split = u / plane;
     u -= t.split * plane;
-    const int band = u / (kBand * nn), in = u - band * kBand * nn;
-    const int high = nm - band * kBand < kBand ? nm - band * kBand : kBand;
-    t.m0 = (band * kBand + in % high) * 256;
+    constexpr int tall = kBand<MODE>;
+    const int band = u / (tall * nn), in = u - band * tall * nn;
+    const int high = nm - band * tall < tall ? nm - band * tall : tall;
+    t.m0 = (band * tall + in % high) * 256;
     t.n0 = in / high * 256;
     t.n = (MODE == VOCAB_DX || MODE == VOCAB_DW) && cols - t.n0 <= 128 ? 128 : 256;
     t.k0 = t.split * per;
@@ -359,8 +364,9 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
         if (!mbar_wait(&tfull[seq & 1], seq >> 1 & 1, abort_flag, g.status)) break;
         tc_fence_after();
       }
-      // one arrival per warp: one per thread took the other CTA's 1600 cycles a tile (5 rows,
-      // 131072 x 4096: the weight gradient 264 us, @@ so)
+      // one arrival per warp, without an order of its own at cluster scope: one per thread that
+      // had it took the other CTA's warps 1600 cycles a tile (5 rows, 131072 x 4096: the
+      // weight gradient 268 us, 182 so)
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
