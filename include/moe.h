@@ -602,11 +602,15 @@ int moe_vocab_backward(const moe_vocab_config *cfg, const float *dloss, const fl
  * c zero (infinite norm) or NaN, as the formula says.
  * max_norm >= 0 (infinite: no limit), eps > 0; n <= 2^24, counts <= 2^42.
  */
+typedef struct {
+  double max_norm, eps;
+} moe_clip_config;
+
 size_t moe_grad_workspace_bytes(int32_t n);
 int moe_grad_norm(const void *const *grads, const int64_t *counts, const int32_t *dtypes, int32_t n, float *norm,
                   void *ws, moe_stream_t stream);
-int moe_grad_clip(const void *const *grads, void *const *outs, const int64_t *counts, const int32_t *dtypes,
-                  const int32_t *out_dtypes, int32_t n, double max_norm, double eps, float *norm, void *ws,
+int moe_grad_clip(const moe_clip_config *cfg, const void *const *grads, void *const *outs, const int64_t *counts,
+                  const int32_t *dtypes, const int32_t *out_dtypes, int32_t n, float *norm, void *ws,
                   moe_stream_t stream);
 
 /* Synchronises `stream`, returns the device status word recorded in `ws`

@@ -76,6 +76,10 @@ class MoeVocabConfig(ctypes.Structure):
                [(n, ctypes.c_int64) for n in ("ld_x", "ld_w", "ld_dx")]
 
 
+class MoeClipConfig(ctypes.Structure):
+    _fields_ = [("max_norm", ctypes.c_double), ("eps", ctypes.c_double)]
+
+
 _lib = None
 EXPORTS = ["moe_workspace_bytes", "moe_saved_bytes", "moe_buffer_info", "moe_padded_rows",
            "moe_quantize_weights", "moe_quantize_mx", "moe_quantize_mx_both", "moe_prepare_weights",
@@ -146,10 +150,10 @@ def lib():
         for fn, cp, n in ((L.moe_gated_forward, gap, 6), (L.moe_gated_backward, gap, 8), (L.moe_vocab_forward, vp, 6),
                           (L.moe_vocab_backward, vp, 9)):
             fn.argtypes, fn.restype = [cp] + [P] * n + [S], I
-        n32, f64 = ctypes.c_int32, ctypes.c_double
+        n32 = ctypes.c_int32
         L.moe_grad_workspace_bytes.argtypes, L.moe_grad_workspace_bytes.restype = [n32], Z
         L.moe_grad_norm.argtypes, L.moe_grad_norm.restype = [P, P, P, n32, P, P, S], I
-        L.moe_grad_clip.argtypes, L.moe_grad_clip.restype = [P, P, P, P, P, n32, f64, f64, P, P, S], I
+        L.moe_grad_clip.argtypes, L.moe_grad_clip.restype = [ctypes.POINTER(MoeClipConfig), P, P, P, P, P, n32, P, P, S], I
         _lib = L
     return _lib
 
@@ -369,8 +373,8 @@ def moe_grad_norm(grads, counts, dtypes, n, norm, ws, stream=None):
     return lib().moe_grad_norm(grads, counts, dtypes, n, _ptr(norm), _ptr(ws), _stream(stream))
 
 
-def moe_grad_clip(grads, outs, counts, dtypes, out_dtypes, n, max_norm, eps, norm, ws, stream=None):
-    return lib().moe_grad_clip(grads, outs, counts, dtypes, out_dtypes, n, max_norm, eps, _ptr(norm), _ptr(ws),
+def moe_grad_clip(cfg, grads, outs, counts, dtypes, out_dtypes, n, norm, ws, stream=None):
+    return lib().moe_grad_clip(ctypes.byref(cfg), grads, outs, counts, dtypes, out_dtypes, n, _ptr(norm), _ptr(ws),
                                _stream(stream))
 
 

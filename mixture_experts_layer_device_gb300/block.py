@@ -19,8 +19,8 @@ from operator import attrgetter
 
 import torch
 
-from . import (ACTS, GATES, MOE_ELEM_BF16, MOE_ELEM_FP16, MOE_ELEM_FP32, MOE_NORM_POST, MOE_NORM_PRE, MoeEmbedConfig,
-               MoeGatedConfig, MoeGroupedConfig, MoeNormConfig, MoeVocabConfig, _stream, check, lib, moe_get_status)
+from . import (ACTS, GATES, MOE_ELEM_BF16, MOE_ELEM_FP16, MOE_ELEM_FP32, MOE_NORM_POST, MOE_NORM_PRE, MoeClipConfig,
+               MoeEmbedConfig, MoeGatedConfig, MoeGroupedConfig, MoeNormConfig, MoeVocabConfig, _stream, check, lib, moe_get_status)
 
 _ELEM = {torch.bfloat16: MOE_ELEM_BF16, torch.float16: MOE_ELEM_FP16, torch.float32: MOE_ELEM_FP32}
 
@@ -650,8 +650,8 @@ def grad_clip(grads, max_norm, *, out=None, eps=1e-6, norm=None, stream=None):
         _bad("max_norm must not be negative, eps must be positive")
     norm = _norm_out(norm, gpu)
     ws = torch.empty(_grad_workspace(len(grads)), dtype=torch.uint8, device=norm.device)
-    rc = lib().moe_grad_clip(_host(at), _host(out_at), _host(counts), _host(types), _host(out_types), len(grads), max_norm,
-                             eps, norm.data_ptr(), ws.data_ptr(), _stream(None))
+    rc = lib().moe_grad_clip(ctypes.byref(MoeClipConfig(max_norm, eps)), _host(at), _host(out_at), _host(counts),
+                             _host(types), _host(out_types), len(grads), norm.data_ptr(), ws.data_ptr(), _stream(None))
     if rc == -1:    # of the library's checks the only one that is not made above
         _bad("tensors of the call overlap: no output shares memory with another tensor")
     check(rc)

@@ -108,7 +108,7 @@ size_t vocab_bind(moe::VocabArgs *a, bool backward, void *ws) {
     a->dz = take(high * a->width * 2);
     a->sum = reinterpret_cast<float *>(take(a->splits * rows * a->ld_sum * 4));
   } else {
-    a->part = reinterpret_cast<float2 *>(take(pad * a->parts * 8));
+    a->part = reinterpret_cast<float2 *>(take(rows * a->parts * 8));
   }
   return at + 256;
 }
@@ -245,12 +245,13 @@ int moe_grad_norm(const void *const *grads, const int64_t *counts, const int32_t
   return status_of(moe::launch_grads(g, false, 0.0, 0.0, norm, ws, sms, stream));
 }
 
-int moe_grad_clip(const void *const *grads, void *const *outs, const int64_t *counts, const int32_t *dtypes,
-                  const int32_t *out_dtypes, int32_t n, double max_norm, double eps, float *norm, void *ws,
+int moe_grad_clip(const moe_clip_config *cfg, const void *const *grads, void *const *outs, const int64_t *counts,
+                  const int32_t *dtypes, const int32_t *out_dtypes, int32_t n, float *norm, void *ws,
                   moe_stream_t stream) {
+  if (!cfg) return MOE_ERR_ARG;
   int rc = grad_check(grads, outs, counts, dtypes, out_dtypes, n, true);
   if (rc != MOE_OK) return rc;
-  if (!norm || !ws || !(max_norm >= 0.0) || !(eps > 0.0) || !isfinite(eps)) return MOE_ERR_ARG;
+  if (!norm || !ws || !(cfg->max_norm >= 0.0) || !(cfg->eps > 0.0) || !isfinite(cfg->eps)) return MOE_ERR_ARG;
   if (!aligned(norm, 4) || !aligned(ws, 16)) return MOE_ERR_ALIGN;
   const moe::GradTensors g = {n, grads, outs, counts, dtypes, out_dtypes};
   try {
@@ -260,7 +261,7 @@ int moe_grad_clip(const void *const *grads, void *const *outs, const int64_t *co
   }
   int sms;
   if ((rc = moe::host_device(&sms)) != MOE_OK) return rc;
-  return status_of(moe::launch_grads(g, true, max_norm, eps, norm, ws, sms, stream));
+  return status_of(moe::launch_grads(g, true, cfg->max_norm, cfg->eps, norm, ws, sms, stream));
 }
 
 }  // extern "C"

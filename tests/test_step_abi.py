@@ -108,7 +108,7 @@ def grads(pkg, data, counts, types, outs=None, out_types=None, max_norm=1.0, eps
     if outs is None:
         return pkg.moe_grad_norm(at(d), at(c), at(t), len(d), norm, ws, 0)
     o, ot = array("Q", outs), array("i", out_types)
-    return pkg.moe_grad_clip(at(d), at(o), at(c), at(t), at(ot), len(d), max_norm, eps, norm, ws, 0)
+    return pkg.moe_grad_clip(pkg.MoeClipConfig(max_norm, eps), at(d), at(o), at(c), at(t), at(ot), len(d), norm, ws, 0)
 
 
 def test_grad_refusals(pkg):
@@ -160,3 +160,8 @@ def test_python_functions_check_before_they_call(pkg, monkeypatch):
 def test_config_layouts_match_the_header(pkg):
     assert ctypes.sizeof(pkg.MoeGatedConfig) == 8 + 7 * 4 + 4 + 5 * 8
     assert ctypes.sizeof(pkg.MoeVocabConfig) == 16 + 6 * 4 + 3 * 8
+    assert ctypes.sizeof(pkg.MoeClipConfig) == 2 * 8
+
+
+def test_clip_without_a_config(pkg):
+    assert pkg.lib().moe_grad_clip(None, None, None, None, None, None, 0, P, P, None) == -1
