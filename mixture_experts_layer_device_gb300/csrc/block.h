@@ -171,7 +171,7 @@ struct VocabArgs {
   int *row, *place;      // [pad] row of a place, [rows] place of a row (-1: none)
   int *label;            // [pad]
   float *hit;            // [pad] the label's logit; backward: its dz
-  float2 *part;          // forward: [pad][parts] (maximum, sum of exponentials) of 128 logits
+  float2 *part;          // forward: [rows][parts] (maximum, sum of exponentials) of 128 logits
   int parts;
   float *coef_p, *coef_l, *base;  // backward: [pad] dz = coef_p 2^(z log2 e - base), less coef_l for the label
   void *xs;              // [rows rounded up to 128][ld_xs] the copy of x

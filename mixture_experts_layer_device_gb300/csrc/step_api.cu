@@ -53,7 +53,8 @@ int vocab_check(const moe_vocab_config *c, moe::VocabArgs *a) {
 }
 
 // A piece of the vocabulary: as many entries as the gradient of the logits of all rows
-// takes 512 MB for, 4096 at least.
+// takes 512 MB for, 4096 at least (8192 rows, 5735 that count, 131072 x 4096: 11.41 ms with
+// 128 MB, 11.25 with 256, 11.06 with 512, 10.97 with 1024, 11.07 with 2048).
 constexpr int64_t kPieceBytes = 512LL << 20;
 // DX: the piece's reduction is split so that the last round of tiles over the SM pairs is
 // full; a split costs a pass of its sums through memory, taken as 2 %.

@@ -161,7 +161,8 @@ __global__ void __launch_bounds__(kRowThreads) vocab_rows_kernel(const VocabArgs
 // On the way the label's logit, a dot product in fp32 whose terms are rounded to
 // nearest.  The tensor cores' sums truncate: at d = 7168 their logits are off by some
 // 4e-6 of their size, which the loss of a row that is sure of its label would consist of.
-// GROUP threads per row: 32, or the block's 256 from 2048 columns on.
+// GROUP threads per row: 32, or the block's 256 from 2048 columns on (31 rows of 8192: 9.9
+// us, 16.0 with 32; 16384 rows of 512: 9.7 with 32, 20.0 with 256; of 2048: 25 and 28).
 constexpr int kWideRow = 2048;
 
 template <typename T>
@@ -326,7 +327,8 @@ __global__ void __launch_bounds__(256) vocab_pad_kernel(const VocabArgs a) {
 // Parts are (maximum, sum of exponentials from it); where a maximum is not finite, from zero.
 MOE_DEV float from_of(float m) { return fabsf(m) <= 3.402823466e38f ? m : 0.f; }
 
-// GROUP threads per row that counts: 32, or the block's 256 for few rows.  The parts hold
+// GROUP threads per row that counts: 32, or the block's 256 for few rows with many parts (5
+// rows of 1024 parts: 6.0 us, 9.8 with 32; 16384 rows of 8: 8.1 with 32, 26.5 with 256).  The parts hold
 // all logits but the label's, z:
 //   loss = log(1 + S exp(m - z)),  lse = z + loss
 // where that is in range, which keeps a small loss's precision.
