@@ -369,9 +369,10 @@ __global__ void __launch_bounds__(256) vocab_loss_kernel(const VocabArgs a) {
       const float z = a.hit[i], others = from + logf(s);  // -inf: the label is alone
       float loss, lse;
       if (others <= z) {
-        loss = log1pf(expf(others - z));
-        lse = z + loss;
-      } else {  // also where a logit is not finite
+        const bool infinite = fabsf(z) > 3.402823466e38f;  // lse is z, and z - z no number
+        loss = infinite ? z - z : log1pf(expf(others - z));
+        lse = infinite ? z : z + loss;
+      } else {  // also where another logit is not finite, or one is NaN
         lse = others + log1pf(expf(z - others));
         loss = lse - z;
       }
