@@ -46,6 +46,8 @@ static_assert(kSmem <= 232448, "shared memory");
 template <int MODE>
 constexpr int kBand = MODE == VOCAB_LOSS ? 16 : 8;
 constexpr float kLog2e = 1.44269504088896340736f;
+// Up to here a logit times log2 e stays in fp32.
+constexpr float kMostBase = 2.3e38f;
 
 struct VocabMaps {
   CUtensorMap a, b, out;
@@ -427,7 +429,11 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
           }
           const float m = fmaxf(m0, m1);
           // a maximum that is not finite: exponentials from zero, as the join expects
-          const float base = fabsf(m) <= 3.402823466e38f ? m * kLog2e : 0.f;
+          const float base = fabsf(m) <= kMostBase ? m * kLog2e : 0.f;
+          if (fabsf(m) > kMostBase && fabsf(m) <= 3.402823466e38f) {  // m log2 e is not: from m by subtraction
+#pragma unroll
+            for (int i = 0; i < 128; ++i) z[i] -= m;
+          }
           float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int i = 0; i < 128; ++i) s[i & 3] += ex2(fmaf(z[i], kLog2e, -base));
@@ -436,7 +442,15 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
         }
       } else if constexpr (MODE == VOCAB_DZ) {
         // out through the staging by plain stores: nothing to wait for between pieces
-        const float cp = g.coef_p[row], own = g.hit[row], base = g.base[row];
+        const float cp = g.coef_p[row], own = g.hit[row];
+        float base = g.base[row], less = 0.f;
+        if (fabsf(base) > 3.402823466e38f && row < count) {  // lse log2 e: lse itself may be finite
+          const float l = g.lse_in[g.row[row]];
+          if (fabsf(l) <= 3.402823466e38f) {
+            less = l;
+            base = 0.f;
+          }
+        }
         const int label = g.label[row] - (g.v0 + t.n0);
         const gemm_detail::OutView out = gemm_detail::out_view(g.dz, g.width, (g.rows + 127L) / 128 * 128, 2);
 #pragma unroll 1
@@ -450,6 +464,10 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
           if (j == 192) release();
           if (t.n0 + j >= g.wp) continue;
           float *z = reinterpret_cast<float *>(r);
+          if (less != 0.f) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) z[i] -= less;
+          }
           // no coefficient, no term: what z holds there does not matter
 #pragma unroll
           for (int i = 0; i < 64; ++i) z[i] = cp == 0.f ? 0.f : cp * ex2(fmaf(z[i], kLog2e, -base));

@@ -36,3 +36,32 @@ def test_vocab_infinite_logits(blk, V, rows):
             want = want.to(torch.float32).cuda()
             assert torch.allclose(got[:3], want, rtol=1e-6, atol=1e-6, equal_nan=True), (label, got[:3], want)
             assert torch.equal(got[2:], got[2:3].expand(rows - 2))
+
+
+@pytest.mark.parametrize("dtype", [BF])          # fp16 does not reach such logits
+@pytest.mark.parametrize("sign", [1, -1])
+def test_vocab_logits_near_the_largest_number(blk, dtype, sign):
+    """Logits of 1.5 2^127, whose product with log2 e is no fp32 number.  lse and loss are exact
+    there (a step of fp32 is 2^104), and so is dz: 1 at the largest, 0 elsewhere."""
+    V, d, far = 700, 64, slice(256, 384)
+    x, w = torch.zeros((3, d), dtype=dtype, device="cuda"), torch.zeros((V, d), dtype=dtype, device="cuda")
+    x[0, 0], x[1, 0] = sign * 2.0 ** 64, -sign * 2.0 ** 64
+    w[far, 0] = 1.5 * 2.0 ** 63
+    w[:, 1] = 0.25
+    z = (x.to(F64) @ w.to(F64).T)
+    top = 1.5 * 2.0 ** 127
+    up = 0 if sign > 0 else 1                    # the row whose large logits are positive
+    for label in (0, 300):
+        labels = torch.full((3,), label, device="cuda")
+        loss, lse = blk.vocab_loss_forward(x, w, labels)
+        ref = torch.logsumexp(z, 1)
+        assert float(lse[up]) == top and (float(loss[up]) == top if label == 0 else 0.0 <= float(loss[up]) < 4.9)  # log 128
+        assert abs(float(lse[1 - up]) - math.log(V - 128)) < 1e-5
+        assert float(loss[1 - up]) == pytest.approx(top if label == 300 else math.log(V - 128), rel=1e-6)
+        assert abs(float(loss[2]) - math.log(V)) < 1e-5 and torch.allclose(lse.to(F64), ref, rtol=1e-6)
+        one = torch.ones(3, device="cuda")
+        dx = blk.vocab_loss_backward(None, x, w, labels, lse, dlse=one)[0]
+        assert float(dx[up, 0]) == 128 * 1.5 * 2.0 ** 63 and float(dx[up, 1]) == 32.0
+        assert float(dx[1 - up, 0]) == 0.0 and abs(float(dx[1 - up, 1]) - 0.25) < 1e-2
+        dx = blk.vocab_loss_backward(one, x, w, labels, lse)[0]
+        assert float(dx[up, 0]) == float(torch.tensor((128 if label == 0 else 127) * 1.5 * 2.0 ** 63).to(dtype))
