@@ -628,7 +628,8 @@ def grad_clip(grads, max_norm, *, out=None, eps=1e-6, norm=None, stream=None):
     """Scales all tensors of the list `grads` by min(1, max_norm / (norm + eps)), in place
     or into the list `out` of tensors of the same shapes and layouts (each of its
     gradient's type or fp32, as an optimizer's masters take them); the norm of before
-    comes back as a 0-d fp32 tensor.  No output shares memory with another tensor of the
+    comes back as a 0-d fp32 tensor.  An infinite max_norm is no limit, whatever the norm
+    but NaN.  No output shares memory with another tensor of the
     call (the same gradient twice, a view of another): refused."""
     if stream is not None:
         return _on(stream, grad_clip, list(grads), max_norm, out=None if out is None else list(out), eps=eps, norm=norm)

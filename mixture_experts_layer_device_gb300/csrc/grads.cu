@@ -242,7 +242,8 @@ __global__ void __launch_bounds__(kGradThreads, kBlocksPerSm) grad_scale_kernel(
     const double v = norm_of(part, n);
     if (threadIdx.x == 0) {
       if (blockIdx.x == 0) *norm = static_cast<float>(v);
-      const double r = max_norm / (v + eps);
+      // no limit: an infinite norm scales nothing either (inf / inf is NaN)
+      const double r = isinf(max_norm) && isinf(v) ? 1.0 : max_norm / (v + eps);
       factor = r >= 1.0 ? 1.f : static_cast<float>(r);  // NaN stays
     }
   }

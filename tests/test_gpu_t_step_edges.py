@@ -65,3 +65,22 @@ def test_vocab_logits_near_the_largest_number(blk, dtype, sign):
         assert float(dx[1 - up, 0]) == 0.0 and abs(float(dx[1 - up, 1]) - 0.25) < 1e-2
         dx = blk.vocab_loss_backward(one, x, w, labels, lse)[0]
         assert float(dx[up, 0]) == float(torch.tensor((128 if label == 0 else 127) * 1.5 * 2.0 ** 63).to(dtype))
+
+
+# ---------------------------------------------------------------- gradients
+def test_clip_without_a_limit(blk):
+    """max_norm = inf scales nothing, whatever the norm but NaN (the quotient inf / inf is one)."""
+    for bad, norm in ((math.inf, math.inf), (-math.inf, math.inf), (3e38, None), (math.nan, math.nan)):
+        grads = [torch.ones(1000, device="cuda"), torch.full((70,), 3.0, dtype=BF, device="cuda")]
+        grads[0][77] = bad
+        keep = [t.clone() for t in grads]
+        for out in (None, [torch.empty_like(t, dtype=FP) for t in grads]):
+            got = blk.grad_clip(grads, math.inf, out=out)
+            if norm is not None:
+                assert torch.allclose(got, torch.tensor(norm, device="cuda"), equal_nan=True)
+            for t, k in zip(out or grads, keep):
+                assert bool(torch.isnan(t).all()) if bad != bad else torch.equal(t, k.to(t.dtype))
+    limited = torch.ones(10, device="cuda")
+    limited[3] = math.inf
+    blk.grad_clip([limited], 3e38)               # a limit, if a large one: c = 0
+    assert float(limited[0]) == 0.0 and bool(torch.isnan(limited[3]))
