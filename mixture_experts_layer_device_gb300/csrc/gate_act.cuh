@@ -50,9 +50,10 @@ MOE_DEV void act_slope(float g, float &value, float &slope) {
     value = g * cdf;
     slope = cdf + g * __expf(-0.5f * g * g) * 0.39894228040143268f;
   } else if constexpr (ACT == MOE_ACT_GELU_TANH) {
-    const float s = sigmoidf(kTanhSlope * g * (1.0f + kTanhCube * g * g));
+    // s is 0 or 1 long before g^2 = 10^4; where g^2 itself overflows, 0 * inf would be NaN
+    const float q = kTanhCube * fminf(g * g, 1e4f), s = sigmoidf(kTanhSlope * g * (1.0f + q));
     value = g * s;
-    slope = s + value * (1.0f - s) * kTanhSlope * (1.0f + 3.0f * kTanhCube * g * g);
+    slope = s + value * (1.0f - s) * kTanhSlope * (1.0f + 3.0f * q);
   } else {
     value = g <= 0.f ? 0.f : g;
     slope = g <= 0.f ? 0.f : 1.f;

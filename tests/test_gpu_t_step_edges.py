@@ -84,3 +84,20 @@ def test_clip_without_a_limit(blk):
     limited[3] = math.inf
     blk.grad_clip([limited], 3e38)               # a limit, if a large one: c = 0
     assert float(limited[0]) == 0.0 and bool(torch.isnan(limited[3]))
+
+
+# ---------------------------------------------------------------- gated products
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh", "relu"])
+@pytest.mark.parametrize("m", [8, 9])            # rows in 16-byte pieces and element by element
+def test_gated_slopes_far_out(blk, act, m):
+    """Gates whose square leaves fp32: act(g) is g or 0, act'(g) 1 or 0.  Exact: w has one 1 per row."""
+    big = torch.tensor([1e3, 1e10, 2e19, 1e30, 3e38], dtype=F64).to(BF)
+    gates = torch.cat([big, -big]).cuda()
+    rows, K = gates.numel(), 2 * m
+    gu = torch.ones((rows, 2 * m), dtype=BF, device="cuda")
+    gu[:, :m] = gates[:, None]
+    dh = torch.full((rows, m), 0.5, dtype=BF, device="cuda")
+    w, x = torch.eye(K, dtype=BF, device="cuda")[None].contiguous(), torch.ones((rows, K), dtype=BF, device="cuda")
+    dx = blk.gated_backward(dh, x, w, torch.tensor([0, rows], dtype=torch.int32, device="cuda"), gu, act=act, need_dw=False)[0]
+    assert torch.all(dx[:5, :m] == 0.5) and torch.all(dx[5:, :m] == 0.0)
+    assert torch.equal(dx[:5, m:], 0.5 * gu[:5, :m]) and torch.all(dx[5:, m:] == 0.0)
