@@ -600,8 +600,9 @@ int moe_vocab_backward(const moe_vocab_config *cfg, const float *dloss, const fl
  * norm: one fp32 on the device.  Sums are held in 64 bits over short fp32 sums, in
  * a fixed order; no squares overflow or vanish.  A norm that is not finite makes
  * c zero (infinite norm) or NaN, as the formula says.
- * max_norm >= 0, eps > 0; n <= 2^24, counts <= 2^42.  An infinite max_norm is no
- * limit: c = 1, for an infinite norm too (a NaN among the gradients: c NaN).
+ * max_norm >= 0, eps > 0; n <= 2^24, counts <= 2^42, 2^45 bytes in all.
+ * An infinite max_norm is no limit: c = 1, for an infinite norm too (a NaN among
+ * the gradients: c NaN).
  */
 typedef struct {
   double max_norm, eps;

@@ -128,6 +128,7 @@ int grad_check(const void *const *data, void *const *outs, const int64_t *counts
                const int32_t *out_dtypes, int32_t n, bool clip) {
   if (n < 0 || (n > 0 && (!data || !counts || !dtypes || (clip && (!outs || !out_dtypes))))) return MOE_ERR_ARG;
   if (n > (1 << 24)) return MOE_ERR_SHAPE;
+  int64_t bytes = 0;
   for (int i = 0; i < n; ++i) {
     if (counts[i] < 0 || dtypes[i] < MOE_ELEM_BF16 || dtypes[i] > MOE_ELEM_FP32) return MOE_ERR_ARG;
     if (clip && out_dtypes[i] != dtypes[i] && out_dtypes[i] != MOE_ELEM_FP32) return MOE_ERR_ARG;
@@ -136,6 +137,9 @@ int grad_check(const void *const *data, void *const *outs, const int64_t *counts
     if (!data[i] || (clip && !outs[i])) return MOE_ERR_ARG;
     if (!aligned(data[i], moe::elem_bytes(dtypes[i])) || (clip && !aligned(outs[i], moe::elem_bytes(out_dtypes[i]))))
       return MOE_ERR_ALIGN;
+    // a launch's pieces of 32 KB are counted in 32 bits: the same large tensor many times over
+    bytes += counts[i] * moe::elem_bytes(dtypes[i]);
+    if (bytes > (1LL << 45)) return MOE_ERR_SHAPE;
   }
   return MOE_OK;
 }
