@@ -10,7 +10,8 @@ from torch and call the library; all arithmetic runs in its kernels.  They run
 on torch's current stream and do not synchronise; with `stream` (a stream or its
 handle) they run as under `torch.cuda.stream(stream)`: what they read has to be
 ready on it, and what they return is.  All tensors of a call are on the current
-GPU.  The autograd functions and modules over them are in module.py.
+GPU.  Where a call changes a tensor's values in place (clipping, accumulate=True) autograd
+is told.  The autograd functions and modules over them are in module.py.
 """
 import ctypes
 from array import array
@@ -97,6 +98,11 @@ def _ws(plan, device):
     if plan[2] <= 0:
         _bad("the library does not take these sizes")
     return torch.empty(plan[2], dtype=torch.uint8, device=device)
+
+
+# The library writes through addresses: autograd is told of the callers' tensors whose values
+# a call changes in place, so that a graph which has saved one refuses its stale values.
+_changed = torch.autograd.graph.increment_version
 
 
 def _on(stream, call, *args, **kw):
@@ -216,6 +222,8 @@ def grouped_backward(dy, x, w, offsets, *, dx=None, dw=None, need_dx=True, need_
     ws = _ws(plan, dy.device)
     check(lib().moe_grouped_backward(plan[1], dy.data_ptr(), x.data_ptr(), w.data_ptr(), offsets.data_ptr(), _ptr(dx),
                                      _ptr(dw), ws.data_ptr(), _stream(None)))
+    if accumulate and need_dw:
+        _changed(dw)
     return (dx, dw, ws) if return_workspace else (dx, dw)
 
 
@@ -288,6 +296,8 @@ def gated_backward(dh, x, w, offsets, gu, *, act="silu", dx=None, dw=None, need_
     ws = _ws(plan, dh.device)
     check(lib().moe_gated_backward(plan[1], dh.data_ptr(), x.data_ptr(), w.data_ptr(), offsets.data_ptr(), gu.data_ptr(),
                                    _ptr(dx), _ptr(dw), ws.data_ptr(), _stream(None)))
+    if accumulate and need_dw:
+        _changed(dw)
     return (dx, dw, ws) if return_workspace else (dx, dw)
 
 
@@ -471,6 +481,8 @@ def embed_backward(ids, dout, V, *, scale=1.0, dtable=None, grad_dtype=None, acc
     ws = _ws(plan, dout.device)
     check(lib().moe_embed_backward(plan[1], flat.data_ptr(), dout.data_ptr(), dtable.data_ptr(), ws.data_ptr(),
                                    _stream(None)))
+    if accumulate:
+        _changed(dtable)
     return dtable
 
 
@@ -561,6 +573,8 @@ def vocab_loss_backward(dloss, x, w, labels, lse, *, dlse=None, dx=None, dw=None
     dx, dw = dx if need_dx else None, dw if need_dw else None
     check(lib().moe_vocab_backward(plan[1], _ptr(dloss), _ptr(dlse), x.data_ptr(), w.data_ptr(), flat.data_ptr(),
                                    lse.data_ptr(), _ptr(dx), _ptr(dw), ws.data_ptr(), _stream(None)))
+    if accumulate and need_dw:
+        _changed(dw)
     return (dx, dw, ws) if return_workspace else (dx, dw)
 
 
@@ -656,4 +670,5 @@ def grad_clip(grads, max_norm, *, out=None, eps=1e-6, norm=None, stream=None):
     if rc == -1:    # of the library's checks the only one that is not made above
         _bad("tensors of the call overlap: no output shares memory with another tensor")
     check(rc)
+    _changed(grads if out is None else out)
     return norm

@@ -1,0 +1,47 @@
+"""CPU-only checks of how the calls that end a training step meet autograd: tensors
+changed in place, the grad mode, refused calls.  CPU tensors pose as GPU tensors
+and a stand-in for the library records its calls (as in test_block_calls.py)."""
+import pytest
+import torch
+
+from mixture_experts_layer_device_gb300 import block, module
+from test_block_calls import SIDE, Gpu, gpu, on  # noqa: F401
+from test_step_calls import FP, gpu_step  # noqa: F401
+
+
+# ---------------------------------------------------------------- changed in place
+@pytest.mark.parametrize("given", [None, SIDE], ids=["current", "stream"])
+def test_autograd_learns_of_clipped_tensors(gpu_step, given):  # noqa: F811
+    """As torch's own operations in place: what a graph has saved of such a tensor is stale."""
+    grads, out = [on(Gpu, 5, 3), on(Gpu, 4, dtype=FP)], [on(Gpu, 5, 3, dtype=FP), on(Gpu, 4, dtype=FP)]
+    before = [t._version for t in grads + out]
+    block.grad_norm(grads, stream=given)
+    assert [t._version for t in grads + out] == before
+    block.grad_clip(iter(grads), 1.0, out=iter(out), stream=given)
+    assert [t._version for t in grads] == before[:2]
+    assert all(t._version > v for t, v in zip(out, before[2:]))
+    after = [t._version for t in out]
+    block.grad_clip(grads, 1.0, stream=given)
+    assert all(t._version > v for t, v in zip(grads, before)) and [t._version for t in out] == after
+    leaf = torch.ones(4, requires_grad=True)
+    part = grads[1].as_subclass(torch.Tensor)
+    stale = (leaf * part).sum()
+    block.grad_clip(grads, 1.0, stream=given)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        stale.backward()
+
+
+@pytest.mark.parametrize("given", [None, SIDE], ids=["current", "stream"])
+def test_autograd_learns_of_what_is_added_to(gpu_step, given):  # noqa: F811
+    R, E, m, K, V = 6, 3, 4, 8, 7
+    x, w, off, dh, gu = on(Gpu, R, K), on(Gpu, E, 2 * m, K), on(Gpu, E + 1, dtype=torch.int32), on(Gpu, R, m), on(Gpu, R, 2 * m)
+    table, ids, r = on(Gpu, V, K), on(Gpu, R, dtype=torch.int64), on(Gpu, R, dtype=FP)
+    calls = [(lambda **kw: block.gated_backward(dh, x, w, off, gu, **kw), "dw", (E, 2 * m, K)),
+             (lambda **kw: block.grouped_backward(gu, x, w, off, **kw), "dw", (E, 2 * m, K)),
+             (lambda **kw: block.vocab_loss_backward(r, x, table, ids, r, **kw), "dw", (V, K)),
+             (lambda **kw: block.embed_backward(ids, x, V, **kw), "dtable", (V, K))]
+    for call, name, shape in calls:
+        t = on(Gpu, *shape, dtype=FP)
+        was = t._version
+        call(**{name: t}, accumulate=True, stream=given)
+        assert t._version > was, name
