@@ -45,3 +45,27 @@ def test_autograd_learns_of_what_is_added_to(gpu_step, given):  # noqa: F811
         was = t._version
         call(**{name: t}, accumulate=True, stream=given)
         assert t._version > was, name
+
+
+# ---------------------------------------------------------------- grad mode
+def test_inference_leaves_gate_and_up_out(monkeypatch):
+    """Without a graph nothing reads [g | u]: it is neither allocated nor written."""
+    asked = []
+
+    def forward(x, w, offsets, act, need_gu):
+        asked.append(need_gu)
+        gu = x @ w[0].T
+        return gu[:, :2] * gu[:, 2:], gu if need_gu else None
+
+    monkeypatch.setattr(block, "gated_forward", forward)
+    layer = module.GatedLinear(1, 2, 3, act="relu", dtype=torch.float32, device="cpu")
+    x, offsets = torch.randn(5, 3), torch.tensor([0, 5], dtype=torch.int32)
+    trained = layer(x, offsets)
+    assert asked == [True] and trained.requires_grad
+    for mode in (torch.no_grad, torch.inference_mode):
+        with mode():
+            h = layer(x, offsets)
+        assert asked[-1] is False and torch.equal(h, trained) and not h.requires_grad
+    layer.weight.requires_grad_(False)
+    assert not layer(x, offsets).requires_grad and asked[-1] is False
+    assert layer(x.requires_grad_(), offsets).requires_grad and asked[-1] is True
