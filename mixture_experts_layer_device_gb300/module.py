@@ -332,12 +332,13 @@ def clip_gradients(parameters, max_norm, masters=None, eps=1e-6):
     masters = list(masters)
     if len(masters) != len(parameters):
         raise ValueError("%d masters for %d parameters" % (len(masters), len(parameters)))
-    out = []
-    for p, m in zip(parameters, masters):
-        if p.grad is None:
-            m.grad = None
-            continue
-        if m.grad is None or m.grad.stride() != p.grad.stride():
-            m.grad = torch.empty_like(p.grad, dtype=torch.float32)
-        out.append(m.grad)
-    return block.grad_clip(grads, max_norm, out=out, eps=eps)
+    for i, (p, m) in enumerate(zip(parameters, masters)):
+        if m.shape != p.shape or m.dtype != torch.float32 or m.device != p.device:
+            raise ValueError("master %d is %s %s on %s, expected float32 %s on %s" %
+                             (i, m.dtype, tuple(m.shape), m.device, tuple(p.shape), p.device))
+    new = [None if p.grad is None else m.grad if m.grad is not None and m.grad.stride() == p.grad.stride() else
+           torch.empty_like(p.grad, dtype=torch.float32) for p, m in zip(parameters, masters)]
+    norm = block.grad_clip(grads, max_norm, out=[g for g in new if g is not None], eps=eps)
+    for m, g in zip(masters, new):      # a refused call has left them as they were
+        m.grad = g
+    return norm

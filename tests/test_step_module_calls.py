@@ -69,3 +69,31 @@ def test_inference_leaves_gate_and_up_out(monkeypatch):
     layer.weight.requires_grad_(False)
     assert not layer(x, offsets).requires_grad and asked[-1] is False
     assert layer(x.requires_grad_(), offsets).requires_grad and asked[-1] is True
+
+
+# ---------------------------------------------------------------- masters
+def test_a_refused_clipping_leaves_the_masters_alone(monkeypatch):
+    def refuse(grads, max_norm, out=None, eps=1e-6):
+        raise ValueError("refused")
+
+    ps = [torch.nn.Parameter(torch.zeros(n, 2)) for n in (3, 4, 5)]
+    ps[0].grad, ps[2].grad = torch.ones(3, 2), torch.ones(2, 5).t()
+    masters = [p.detach().clone().requires_grad_() for p in ps]
+    masters[1].grad, masters[2].grad = torch.ones(4, 2), torch.ones(5, 2)
+    was = [m.grad for m in masters]
+    kept = [None if g is None else g.clone() for g in was]
+
+    def unchanged():
+        return all(m.grad is g and (g is None or torch.equal(g, k)) for m, g, k in zip(masters, was, kept))
+
+    monkeypatch.setattr(block, "grad_clip", refuse)
+    with pytest.raises(ValueError, match="refused"):
+        module.clip_gradients(ps, 1.0, masters)
+    assert unchanged()
+    monkeypatch.setattr(block, "grad_clip", lambda *a, **kw: "n")
+    for bad in (torch.zeros(2, 3), torch.zeros(3, 2, dtype=torch.bfloat16), torch.zeros(3, 2, device="meta")):
+        with pytest.raises(ValueError, match="master 0"):
+            module.clip_gradients(ps, 1.0, [bad] + masters[1:])
+        assert unchanged() and bad.grad is None
+    assert module.clip_gradients(ps, 1.0, masters) == "n"
+    assert masters[1].grad is None and masters[2].grad.stride() == ps[2].grad.stride() and masters[0].grad.shape == (3, 2)
