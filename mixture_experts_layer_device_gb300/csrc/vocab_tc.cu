@@ -113,13 +113,16 @@ MOE_DEV float ex2(float x) {
   return y;
 }
 
-// LOSS: how many reduction steps one accumulator takes; the epilogue adds those sums in
-// fp32.  An accumulator truncates at every instruction: a chain of 448 of them (d = 7168)
-// left logits 1.3e-5 too low, all alike, which lse and the loss inherit.
+// How many reduction steps one accumulator takes.  An accumulator truncates at every
+// instruction, always towards zero: a chain of 448 of them (d = 7168) left logits 1.3e-5 too
+// low, all alike, which lse and the loss inherit, and one of 16384 an fp32 dw of positive
+// terms over 262144 rows 4.3e-4 of its size (2048 steps: 2.2e-7, whatever the rows).
+// LOSS and fp32 dw are joined from chains of kChain steps in fp32.  Elsewhere the result is
+// rounded to 16 bits, which is more than such a chain loses.
 constexpr int kChain = 2048;
-template <int MODE>
+template <int MODE, bool WIDE>
 MOE_DEV int chain_of(int klen) {
-  return MODE == VOCAB_LOSS ? kChain : (klen > 0 ? klen : 1);
+  return MODE == VOCAB_LOSS || (MODE == VOCAB_DW && WIDE) ? kChain : (klen > 0 ? klen : 1);
 }
 
 struct VocabTile {
@@ -299,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
       for (int u = pair; u < tiles.total && ok; u += pairs) {
         const VocabTile t = tiles.at(u);
         const uint32_t idesc = vocab_idesc<MODE>(g.dtype, t.n);
-        for (int from = 0, chain = chain_of<MODE>(t.klen); from < t.klen && ok; from += chain) {
+        for (int from = 0, chain = chain_of<MODE, WIDE>(t.klen); from < t.klen && ok; from += chain) {
           const int to = t.klen - from < chain ? t.klen : from + chain;
           if (!mbar_wait(&tempty[acc], aph ^ 1u, abort_flag, g.status)) {
             ok = false;
@@ -512,6 +515,44 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
         }
       } else {
         constexpr int STEP = WIDE ? 32 : 64;  // columns of a 128-byte piece
+        if (WIDE && t.klen > kChain) {
+          // The chains' sums meet in registers, as in LOSS, and go back to the last one's columns:
+          // kept in registers up to the stores they spilled.  (8192 rows, 131072 x 4096: 10.5 ms,
+          // 10.3 as one chain; added up in dw by TMA 10.85, and 274 us instead of 146 for 9000 rows
+          // and 5001 x 321, whose elements leave one by one.)
+          const bool mine = group * 128 < t.n;  // the narrow tile's columns are the first group's
+          float z[128];
+#pragma unroll
+          for (int i = 0; i < 128; ++i) z[i] = 0.f;
+          for (int from = 0; from < t.klen; from += kChain) {
+            if (from > 0) {
+              release();
+              ++seq;
+              if (!mbar_wait(&tfull[seq & 1], seq >> 1 & 1, abort_flag, g.status)) {
+                lost = true;
+                break;
+              }
+              tc_fence_after();
+              tb = lanes + (seq & 1) * 256 + group * 128;
+            }
+            if (!mine) continue;
+#pragma unroll
+            for (int j = 0; j < 128; j += 16) {
+              uint32_t more[16];
+              tmem_ld16_async(tb + j, more);
+              tmem_ld_wait();
+              reg_fence<16>(more);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) z[j + i] += __uint_as_float(more[i]);
+            }
+          }
+          if (lost) break;
+          if (mine) {
+#pragma unroll
+            for (int j = 0; j < 128; j += 32) tmem_st32(tb + j, reinterpret_cast<const uint32_t *>(z) + j);
+            tmem_st_wait();
+          }
+        }
         const float scale = *reinterpret_cast<const volatile float *>(g.scale);
 #pragma unroll 1
         for (int j = 0; j < 128; j += STEP) {

@@ -67,6 +67,38 @@ def test_vocab_logits_near_the_largest_number(blk, dtype, sign):
         assert float(dx[up, 0]) == float(torch.tensor((128 if label == 0 else 127) * 1.5 * 2.0 ** 63).to(dtype))
 
 
+def grows_evenly(rows):
+    """How far an fp32 sum of `rows` positive terms of one size may be off, relative to the sum:
+    chains of 2048 additions at 2^-22 of the sum so far (half of the whole on average; a tensor
+    core's truncating adder: four times a rounding), joined in fp32."""
+    return (2048 / 2 + 32) * 2.0 ** -22 + (rows / 2048 / 2 + 1) * 2.0 ** -24
+
+
+@pytest.mark.parametrize("d", [64, 33])          # dw by TMA and element by element
+@pytest.mark.parametrize("rows", [2048, 2049, 5000, 1 << 20])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_vocab_wide_gradient_of_many_rows(blk, rows, d, dtype):
+    """An fp32 dw of terms of one sign: its error does not grow with the rows.  w = 0 makes every
+    probability 2^-8, exactly, and dw[v] = 2^-8 sum_t x_t for all v."""
+    V = 256
+    g = torch.Generator(device="cuda").manual_seed(rows + d)
+    x = torch.rand((rows, d), generator=g, device="cuda").to(dtype)
+    w, labels = torch.zeros((V, d), dtype=dtype, device="cuda"), torch.zeros(rows, dtype=torch.int64, device="cuda")
+    labels[::3] = -1                             # a third does not count
+    lse = blk.vocab_loss_forward(x, w, labels)[1]
+    ref = x[labels >= 0].to(F64).sum(0) / V
+    one, n = torch.ones(rows, device="cuda"), int((labels >= 0).sum())
+    run = lambda **kw: blk.vocab_loss_backward(None, x, w, labels, lse, dlse=one, need_dx=False, **kw)[1]  # noqa: E731
+    dw = run(dw_dtype=FP)
+    # 2^-20: lse and the exponential
+    assert float((dw.to(F64) / ref - 1).abs().max()) <= grows_evenly(n) + 2.0 ** -20
+    assert torch.equal(dw, run(dw_dtype=FP))
+    acc = torch.rand((V, d), generator=g, device="cuda") * ref.float()
+    total = ref + acc.to(F64)
+    run(dw=acc, accumulate=True)
+    assert float((acc.to(F64) / total - 1).abs().max()) <= grows_evenly(n) + 2.0 ** -20
+
+
 # ---------------------------------------------------------------- gradients
 def test_clip_without_a_limit(blk):
     """max_norm = inf scales nothing, whatever the norm but NaN (the quotient inf / inf is one)."""
