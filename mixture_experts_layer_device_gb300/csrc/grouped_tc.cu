@@ -117,6 +117,28 @@ MOE_DEV uint32_t tc_idesc(int dtype, int n) {
          (DIR == GROUPED_WGRAD ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (16u << 24);
 }
 
+// How many reduction steps one accumulator takes.  It truncates at every instruction, always
+// towards zero: a chain of 16384 of them left an fp32 dw of positive terms (262144 rows of one
+// expert) 4.3e-4 of its size too low.  Chains of 8192 steps joined in fp32 lose 2.5e-6, whatever
+// the rows, at no cost; of 2048 2.2e-7, but 20000 rows of two experts of [1057, 2001] added to a
+// given dw take 285 us instead of 250 (the next tile's product stops at a chain's end while
+// elements leave).  Where the result is rounded to 16 bits that is more than a chain of up to
+// 2^18 steps loses.
+constexpr int kChain = 8192;
+template <int DIR, bool WIDE>
+MOE_DEV int chain_of(int klen) {
+  return DIR == GROUPED_WGRAD && WIDE ? kChain : (klen > 0 ? klen : 1);
+}
+
+MOE_DEV void tmem_ld16_async(uint32_t taddr, uint32_t *r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
 struct TcTile {
   int e;
   int f0;     // first output feature of the pair (A's rows)
@@ -462,39 +484,45 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
         const TcTile t = next;
         next = tiles.ahead(tiles.unit(i + 1, pair, pairs));
         if (t.klen == 0) continue;
-        if (!mbar_wait(&tempty[acc], aph ^ 1u, abort_flag, g.status)) break;
-        tc_fence_after();
-        const uint32_t dt = tmem + static_cast<uint32_t>(acc * 256);
         const uint32_t idesc = tc_idesc<DIR>(g.dtype, t.n);
-        for (int kb = 0; kb < t.klen; kb += 64 * kBlocks) {
-          if (!mbar_wait(&full[stage], ph, abort_flag, g.status)) {
+        for (int from = 0, chain = chain_of<DIR, WIDE>(t.klen); from < t.klen && ok; from += chain) {
+          const int to = t.klen - from < chain ? t.klen : from + chain;
+          if (!mbar_wait(&tempty[acc], aph ^ 1u, abort_flag, g.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa0 = smem_u32(smem + stage * kStageBytes);
-          const int left = t.klen - kb;  // steps past the end hold zeros in both operands
+          const uint32_t dt = tmem + static_cast<uint32_t>(acc * 256);
+          for (int kb = from; kb < to; kb += 64 * kBlocks) {
+            if (!mbar_wait(&full[stage], ph, abort_flag, g.status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t sa0 = smem_u32(smem + stage * kStageBytes);
+            const int left = to - kb;  // steps past the end hold zeros in both operands
 #pragma unroll
-          for (int k = 0; k < 4 * kBlocks; ++k) {
-            if (k * 16 < left) {
-              const uint32_t sa = sa0 + (k >> 2) * kBlockBytes, sb = sa + 16384;
-              const uint64_t ad = DIR == GROUPED_FWD || DIR == GROUPED_GATED ? sw128_desc(sa + 32 * (k & 3))
-                                                                              : mn_desc(sa + 2048 * (k & 3));
-              const uint64_t bd = DIR == GROUPED_WGRAD ? mn_desc(sb + 2048 * (k & 3)) : sw128_desc(sb + 32 * (k & 3));
-              mma_bf16_pair(dt, ad, bd, idesc, (kb | k) ? 1u : 0u);
+            for (int k = 0; k < 4 * kBlocks; ++k) {
+              if (k * 16 < left) {
+                const uint32_t sa = sa0 + (k >> 2) * kBlockBytes, sb = sa + 16384;
+                const uint64_t ad = DIR == GROUPED_FWD || DIR == GROUPED_GATED ? sw128_desc(sa + 32 * (k & 3))
+                                                                                : mn_desc(sa + 2048 * (k & 3));
+                const uint64_t bd = DIR == GROUPED_WGRAD ? mn_desc(sb + 2048 * (k & 3)) : sw128_desc(sb + 32 * (k & 3));
+                mma_bf16_pair(dt, ad, bd, idesc, (kb - from | k) ? 1u : 0u);
+              }
+            }
+            mma_commit_pair_mc(&empty[stage], 3);
+            if (++stage == kStages) {
+              stage = 0;
+              ph ^= 1u;
             }
           }
-          mma_commit_pair_mc(&empty[stage], 3);
-          if (++stage == kStages) {
-            stage = 0;
-            ph ^= 1u;
+          if (!ok) break;
+          mma_commit_pair_mc(&tfull[acc], 3);
+          if (++acc == 2) {
+            acc = 0;
+            aph ^= 1u;
           }
-        }
-        if (!ok) break;
-        mma_commit_pair_mc(&tfull[acc], 3);
-        if (++acc == 2) {
-          acc = 0;
-          aph ^= 1u;
         }
       }
       mma_commit_pair_mc(done, 1);
@@ -542,12 +570,11 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
       const TcTile t = next;
       next = tiles.ahead(tiles.unit(i + 1, pair, pairs));
       const int fr = t.f0 + static_cast<int>(rank) * 128 + q * 32;  // this warp's first feature
-      const uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * 256);
+      uint32_t tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * 256);
       if (t.klen > 0) {
         if (!mbar_wait(&tfull[acc], aph, abort_flag, g.status)) break;
         tc_fence_after();
       }
-      const uint32_t tempty_addr = smem_u32(&tempty[acc]);
       // one arrival per warp, without an order of its own at cluster scope: one per thread that
       // had it took the other CTA's warps some 1600 cycles a tile (60 experts of 128 rows, [4096,
       // 7168]: the weight gradient 843 us, 567 so)
@@ -556,12 +583,51 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
         __syncwarp();
         if (lane == 0) {
           if (leader) mbar_arrive(&tempty[acc]);
-          else mbar_arrive_remote_tmem(peer_smem(tempty_addr, 0));
+          else mbar_arrive_remote_tmem(peer_smem(smem_u32(&tempty[acc]), 0));
         }
       };
       bool held = t.klen > 0;  // this warp has not released the accumulator yet
       if constexpr (DIR == GROUPED_WGRAD) {
         constexpr int STEP = WIDE ? 32 : 64;  // columns of a 128-byte piece
+        if (WIDE && t.klen > kChain) {
+          // the chains' sums meet in registers and go back to the last one's columns (kept in
+          // registers up to the stores they would spill)
+          bool lost = false;
+          float z[128];
+#pragma unroll
+          for (int i = 0; i < 128; ++i) z[i] = 0.f;
+          for (int from = 0; from < t.klen; from += kChain) {
+            if (from > 0) {
+              release();
+              if (++acc == 2) {
+                acc = 0;
+                aph ^= 1u;
+              }
+              if (!mbar_wait(&tfull[acc], aph, abort_flag, g.status)) {
+                lost = true;
+                break;
+              }
+              tc_fence_after();
+              tb = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * 256);
+            }
+#pragma unroll
+            for (int j = 0; j < 128; j += 16) {
+              const int col = half * 32 + (j >> 5) * 64 + (j & 16);
+              if (col >= t.n) continue;
+              uint32_t more[16];
+              tmem_ld16_async(tb + col, more);
+              tmem_ld_wait();
+              reg_fence<16>(more);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) z[j + i] += __uint_as_float(more[i]);
+            }
+          }
+          if (lost) break;
+#pragma unroll
+          for (int j = 0; j < 128; j += 32)
+            if (half * 32 + j * 2 < t.n) tmem_st32(tb + half * 32 + j * 2, reinterpret_cast<const uint32_t *>(z) + j);
+          tmem_st_wait();
+        }
         for (int j = half * STEP; j < t.n; j += 2 * STEP) {
           uint32_t r[STEP], w[32];
           if (t.klen > 0) {

@@ -67,11 +67,11 @@ def test_vocab_logits_near_the_largest_number(blk, dtype, sign):
         assert float(dx[up, 0]) == float(torch.tensor((128 if label == 0 else 127) * 1.5 * 2.0 ** 63).to(dtype))
 
 
-def grows_evenly(rows):
+def grows_evenly(rows, chain):
     """How far an fp32 sum of `rows` positive terms of one size may be off, relative to the sum:
-    chains of 2048 additions at 2^-22 of the sum so far (half of the whole on average; a tensor
+    chains of additions at 2^-22 of the sum so far (half of the whole on average; a tensor
     core's truncating adder: four times a rounding), joined in fp32."""
-    return (2048 / 2 + 32) * 2.0 ** -22 + (rows / 2048 / 2 + 1) * 2.0 ** -24
+    return (min(rows, chain) / 2 + 32) * 2.0 ** -22 + (rows / chain / 2 + 1) * 2.0 ** -24
 
 
 @pytest.mark.parametrize("d", [64, 33])          # dw by TMA and element by element
@@ -91,12 +91,12 @@ def test_vocab_wide_gradient_of_many_rows(blk, rows, d, dtype):
     run = lambda **kw: blk.vocab_loss_backward(None, x, w, labels, lse, dlse=one, need_dx=False, **kw)[1]  # noqa: E731
     dw = run(dw_dtype=FP)
     # 2^-20: lse and the exponential
-    assert float((dw.to(F64) / ref - 1).abs().max()) <= grows_evenly(n) + 2.0 ** -20
+    assert float((dw.to(F64) / ref - 1).abs().max()) <= grows_evenly(n, 2048) + 2.0 ** -20
     assert torch.equal(dw, run(dw_dtype=FP))
     acc = torch.rand((V, d), generator=g, device="cuda") * ref.float()
     total = ref + acc.to(F64)
     run(dw=acc, accumulate=True)
-    assert float((acc.to(F64) / total - 1).abs().max()) <= grows_evenly(n) + 2.0 ** -20
+    assert float((acc.to(F64) / total - 1).abs().max()) <= grows_evenly(n, 2048) + 2.0 ** -20
 
 
 # ---------------------------------------------------------------- gradients
@@ -119,6 +119,32 @@ def test_clip_without_a_limit(blk):
 
 
 # ---------------------------------------------------------------- gated products
+@pytest.mark.parametrize("m,K", [(64, 64), (9, 33)])     # dw by TMA and element by element
+@pytest.mark.parametrize("rows", [2049, 9000, 1 << 20])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_gated_and_grouped_wide_gradients_of_many_rows(blk, rows, m, K, dtype):
+    """An fp32 dw of terms of one sign: its error does not grow with an expert's rows.  dg = du =
+    2^-8 exactly, so that dw[e] = 2^-8 sum x[r] for all its rows."""
+    g = torch.Generator(device="cuda").manual_seed(rows + m)
+    x = torch.rand((rows, K), generator=g, device="cuda").to(dtype)
+    w, gu = torch.zeros((3, 2 * m, K), dtype=dtype, device="cuda"), torch.ones((rows, 2 * m), dtype=dtype, device="cuda")
+    dh = torch.full((rows, m), 2.0 ** -8, dtype=dtype, device="cuda")
+    dy = torch.full((rows, 2 * m), 2.0 ** -8, dtype=dtype, device="cuda")
+    off = [0, 700, 700, rows]
+    offsets = torch.tensor(off, dtype=torch.int32, device="cuda")
+    ref = torch.stack([x[a:b].to(F64).sum(0) / 256 for a, b in zip(off, off[1:])])[:, None, :].expand(3, 2 * m, K)
+    tol = grows_evenly(rows, 8192) * ref
+    for back in (lambda **kw: blk.gated_backward(dh, x, w, offsets, gu, act="relu", need_dx=False, **kw)[1],
+                 lambda **kw: blk.grouped_backward(dy, x, w, offsets, need_dx=False, **kw)[1]):
+        dw = back(dw_dtype=FP)
+        assert bool(((dw.to(F64) - ref).abs() <= tol).all()) and torch.all(dw[1] == 0)
+        assert torch.equal(dw, back(dw_dtype=FP))
+        before = torch.rand((3, 2 * m, K), generator=g, device="cuda")
+        acc = before.clone()
+        back(dw=acc, accumulate=True)
+        assert bool(((acc.to(F64) - before.to(F64) - ref).abs() <= tol + 2.0 ** -22 * acc.abs()).all())
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh", "relu"])
 @pytest.mark.parametrize("m", [8, 9])            # rows in 16-byte pieces and element by element
 def test_gated_slopes_far_out(blk, act, m):
