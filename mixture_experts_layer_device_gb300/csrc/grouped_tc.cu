@@ -118,16 +118,16 @@ MOE_DEV uint32_t tc_idesc(int dtype, int n) {
 }
 
 // How many reduction steps one accumulator takes.  It truncates at every instruction, always
-// towards zero: a chain of 16384 of them left an fp32 dw of positive terms (262144 rows of one
-// expert) 4.3e-4 of its size too low.  Chains of 8192 steps joined in fp32 lose 2.5e-6, whatever
+// towards zero: a chain of 16384 of them left a dw of terms of one sign (262144 rows of one
+// expert) 4.3e-4 of its size too low.  CHAINS, for weight gradients of more rows than kChain in
+// fp32, or than kChain16 in 16 bits: chains of 8192 steps joined in fp32 lose 2.5e-6, whatever
 // the rows, at no cost; of 2048 2.2e-7, but 20000 rows of two experts of [1057, 2001] added to a
 // given dw take 285 us instead of 250 (the next tile's product stops at a chain's end while
-// elements leave).  Where the result is rounded to 16 bits that is more than a chain of up to
-// 2^18 steps loses.
-constexpr int kChain = 8192;
-template <int DIR, bool WIDE>
+// elements leave); of 65536, in front of a rounding to 16 bits, 6.7e-5.
+constexpr int kChain = 8192, kChain16 = 65536;
+template <bool WIDE, bool CHAINS>
 MOE_DEV int chain_of(int klen) {
-  return DIR == GROUPED_WGRAD && WIDE ? kChain : (klen > 0 ? klen : 1);
+  return CHAINS ? (WIDE ? kChain : kChain16) : (klen > 0 ? klen : 1);
 }
 
 MOE_DEV void tmem_ld16_async(uint32_t taddr, uint32_t *r) {
@@ -349,8 +349,8 @@ MOE_DEV void put_elements(const uint32_t *w, uint8_t *buf, O *out, long ld, int 
     }
 }
 
-// T: the operands' type; WIDE: fp32 output (y or dw).
-template <int DIR, typename T, bool WIDE>
+// T: the operands' type; WIDE: fp32 output (y or dw); CHAINS: dw from several accumulators.
+template <int DIR, typename T, bool WIDE, bool CHAINS>
 __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_constant__ TcMaps maps, const GroupedArgs g) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
         next = tiles.ahead(tiles.unit(i + 1, pair, pairs));
         if (t.klen == 0) continue;
         const uint32_t idesc = tc_idesc<DIR>(g.dtype, t.n);
-        for (int from = 0, chain = chain_of<DIR, WIDE>(t.klen); from < t.klen && ok; from += chain) {
+        for (int from = 0, chain = chain_of<WIDE, CHAINS>(t.klen); from < t.klen && ok; from += chain) {
           const int to = t.klen - from < chain ? t.klen : from + chain;
           if (!mbar_wait(&tempty[acc], aph ^ 1u, abort_flag, g.status)) {
             ok = false;
@@ -589,14 +589,14 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
       bool held = t.klen > 0;  // this warp has not released the accumulator yet
       if constexpr (DIR == GROUPED_WGRAD) {
         constexpr int STEP = WIDE ? 32 : 64;  // columns of a 128-byte piece
-        if (WIDE && t.klen > kChain) {
+        if (CHAINS && t.klen > chain_of<WIDE, CHAINS>(t.klen)) {
           // the chains' sums meet in registers and go back to the last one's columns (kept in
           // registers up to the stores they would spill)
           bool lost = false;
           float z[128];
 #pragma unroll
           for (int i = 0; i < 128; ++i) z[i] = 0.f;
-          for (int from = 0; from < t.klen; from += kChain) {
+          for (int from = 0, chain = chain_of<WIDE, CHAINS>(t.klen); from < t.klen; from += chain) {
             if (from > 0) {
               release();
               if (++acc == 2) {
@@ -612,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
             }
 #pragma unroll
             for (int j = 0; j < 128; j += 16) {
-              const int col = half * 32 + (j >> 5) * 64 + (j & 16);
+              const int col = (half + j / STEP * 2) * STEP + j % STEP;
               if (col >= t.n) continue;
               uint32_t more[16];
               tmem_ld16_async(tb + col, more);
@@ -624,8 +624,10 @@ __global__ void __launch_bounds__(kThreads, 1) grouped_tc_kernel(const __grid_co
           }
           if (lost) break;
 #pragma unroll
-          for (int j = 0; j < 128; j += 32)
-            if (half * 32 + j * 2 < t.n) tmem_st32(tb + half * 32 + j * 2, reinterpret_cast<const uint32_t *>(z) + j);
+          for (int j = 0; j < 128; j += 32) {
+            const int col = (half + j / STEP * 2) * STEP + j % STEP;
+            if (col < t.n) tmem_st32(tb + col, reinterpret_cast<const uint32_t *>(z) + j);
+          }
           tmem_st_wait();
         }
         for (int j = half * STEP; j < t.n; j += 2 * STEP) {
@@ -796,9 +798,9 @@ __global__ void __launch_bounds__(128) grouped_maps_kernel(const __grid_constant
       : "memory");
 }
 
-template <int DIR, typename T, bool WIDE>
+template <int DIR, typename T, bool WIDE, bool CHAINS>
 int tc_clusters_query() {
-  const auto kernel = grouped_tc_kernel<DIR, T, WIDE>;
+  const auto kernel = grouped_tc_kernel<DIR, T, WIDE, CHAINS>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(kSmem)) != cudaSuccess)
     return 0;
@@ -817,10 +819,10 @@ int tc_clusters_query() {
   return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
 }
 
-template <int DIR, typename T, bool WIDE>
-cudaError_t launch_tc_one(const TcMaps &maps, const GroupedArgs &g, long units, cudaStream_t s) {
+template <int DIR, typename T, bool WIDE, bool CHAINS>
+cudaError_t launch_tc_kernel(const TcMaps &maps, const GroupedArgs &g, long units, cudaStream_t s) {
   static int memo[64] = {};
-  const int most = per_device_memo(memo, tc_clusters_query<DIR, T, WIDE>);
+  const int most = per_device_memo(memo, tc_clusters_query<DIR, T, WIDE, CHAINS>);
   if (most <= 0) return cudaErrorInvalidConfiguration;
   if (units <= 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
@@ -837,7 +839,17 @@ cudaError_t launch_tc_one(const TcMaps &maps, const GroupedArgs &g, long units, 
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = g.chained ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<DIR, T, WIDE>, maps, g);
+  return cudaLaunchKernelEx(&cfg, grouped_tc_kernel<DIR, T, WIDE, CHAINS>, maps, g);
+}
+
+// CHAINS costs registers, and some time where there is one chain (32768 rows, 64 experts of
+// [4096, 4096], 16 bits: weight gradient 848 us, 815 without).
+template <int DIR, typename T, bool WIDE>
+cudaError_t launch_tc_one(const TcMaps &maps, const GroupedArgs &g, long units, cudaStream_t s) {
+  if constexpr (DIR == GROUPED_WGRAD) {
+    if (g.rows > (WIDE ? kChain : kChain16)) return launch_tc_kernel<DIR, T, WIDE, true>(maps, g, units, s);
+  }
+  return launch_tc_kernel<DIR, T, WIDE, false>(maps, g, units, s);
 }
 
 template <int DIR>

@@ -115,14 +115,15 @@ MOE_DEV float ex2(float x) {
 
 // How many reduction steps one accumulator takes.  An accumulator truncates at every
 // instruction, always towards zero: a chain of 448 of them (d = 7168) left logits 1.3e-5 too
-// low, all alike, which lse and the loss inherit, and one of 16384 an fp32 dw of positive
-// terms over 262144 rows 4.3e-4 of its size (2048 steps: 2.2e-7, whatever the rows).
-// LOSS and fp32 dw are joined from chains of kChain steps in fp32.  Elsewhere the result is
-// rounded to 16 bits, which is more than such a chain loses.
-constexpr int kChain = 2048;
-template <int MODE, bool WIDE>
+// low, all alike, which lse and the loss inherit, and one of 16384 a dw of terms of one sign over
+// 262144 rows 4.3e-4 of its size.  LOSS is joined from chains of kChain steps in fp32, and so
+// is dw (CHAINS) of more rows than that in fp32 (2.2e-7, whatever the rows), or than kChain16
+// in 16 bits (6.7e-5).  dz and dx are rounded to 16 bits, which is more than the chains of a
+// width or of a piece of the vocabulary lose.
+constexpr int kChain = 2048, kChain16 = 65536;
+template <int MODE, bool WIDE, bool CHAINS>
 MOE_DEV int chain_of(int klen) {
-  return MODE == VOCAB_LOSS || (MODE == VOCAB_DW && WIDE) ? kChain : (klen > 0 ? klen : 1);
+  return MODE == VOCAB_LOSS || (CHAINS && WIDE) ? kChain : CHAINS ? kChain16 : (klen > 0 ? klen : 1);
 }
 
 struct VocabTile {
@@ -201,8 +202,8 @@ MOE_DEV void put_elements(const uint32_t *w, uint8_t *buf, O *out, long ld, int 
     }
 }
 
-// T: the operands' type; WIDE: fp32 dw.
-template <int MODE, typename T, bool WIDE>
+// T: the operands' type; WIDE: fp32 dw; CHAINS: dw from several accumulators.
+template <int MODE, typename T, bool WIDE, bool CHAINS>
 __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_constant__ VocabMaps maps, const VocabArgs g) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
       for (int u = pair; u < tiles.total && ok; u += pairs) {
         const VocabTile t = tiles.at(u);
         const uint32_t idesc = vocab_idesc<MODE>(g.dtype, t.n);
-        for (int from = 0, chain = chain_of<MODE, WIDE>(t.klen); from < t.klen && ok; from += chain) {
+        for (int from = 0, chain = chain_of<MODE, WIDE, CHAINS>(t.klen); from < t.klen && ok; from += chain) {
           const int to = t.klen - from < chain ? t.klen : from + chain;
           if (!mbar_wait(&tempty[acc], aph ^ 1u, abort_flag, g.status)) {
             ok = false;
@@ -515,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
         }
       } else {
         constexpr int STEP = WIDE ? 32 : 64;  // columns of a 128-byte piece
-        if (WIDE && t.klen > kChain) {
+        if (CHAINS && t.klen > chain_of<MODE, WIDE, CHAINS>(t.klen)) {
           // The chains' sums meet in registers, as in LOSS, and go back to the last one's columns:
           // kept in registers up to the stores they spilled.  (8192 rows, 131072 x 4096: 10.5 ms,
           // 10.3 as one chain; added up in dw by TMA 10.85, and 274 us instead of 146 for 9000 rows
@@ -524,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
           float z[128];
 #pragma unroll
           for (int i = 0; i < 128; ++i) z[i] = 0.f;
-          for (int from = 0; from < t.klen; from += kChain) {
+          for (int from = 0, chain = chain_of<MODE, WIDE, CHAINS>(t.klen); from < t.klen; from += chain) {
             if (from > 0) {
               release();
               ++seq;
@@ -607,9 +608,9 @@ __global__ void __launch_bounds__(kThreads, 1) vocab_tc_kernel(const __grid_cons
   }
 }
 
-template <int MODE, typename T, bool WIDE>
+template <int MODE, typename T, bool WIDE, bool CHAINS>
 int vocab_clusters_query() {
-  const auto kernel = vocab_tc_kernel<MODE, T, WIDE>;
+  const auto kernel = vocab_tc_kernel<MODE, T, WIDE, CHAINS>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmem)) != cudaSuccess)
     return 0;
   cudaLaunchConfig_t cfg = {};
@@ -627,10 +628,10 @@ int vocab_clusters_query() {
   return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess ? n : 0;
 }
 
-template <int MODE, typename T, bool WIDE>
-cudaError_t launch_one(const VocabMaps &maps, const VocabArgs &g, long units, cudaStream_t s) {
+template <int MODE, typename T, bool WIDE, bool CHAINS>
+cudaError_t launch_kernel(const VocabMaps &maps, const VocabArgs &g, long units, cudaStream_t s) {
   static int memo[64] = {};
-  const int most = per_device_memo(memo, vocab_clusters_query<MODE, T, WIDE>);
+  const int most = per_device_memo(memo, vocab_clusters_query<MODE, T, WIDE, CHAINS>);
   if (most <= 0) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * static_cast<unsigned>(units < most ? units : most), 1, 1);
@@ -646,7 +647,17 @@ cudaError_t launch_one(const VocabMaps &maps, const VocabArgs &g, long units, cu
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, vocab_tc_kernel<MODE, T, WIDE>, maps, g);
+  return cudaLaunchKernelEx(&cfg, vocab_tc_kernel<MODE, T, WIDE, CHAINS>, maps, g);
+}
+
+// CHAINS costs registers, and time where there is one chain: 515 rows, 50001 x 321 with dx 169
+// us, 152 without.
+template <int MODE, typename T, bool WIDE>
+cudaError_t launch_one(const VocabMaps &maps, const VocabArgs &g, long units, cudaStream_t s) {
+  if constexpr (MODE == VOCAB_DW) {
+    if (g.rows > (WIDE ? kChain : kChain16)) return launch_kernel<MODE, T, WIDE, true>(maps, g, units, s);
+  }
+  return launch_kernel<MODE, T, WIDE, false>(maps, g, units, s);
 }
 
 template <int MODE>

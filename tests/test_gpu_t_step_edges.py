@@ -99,6 +99,26 @@ def test_vocab_wide_gradient_of_many_rows(blk, rows, d, dtype):
     assert float((acc.to(F64) / total - 1).abs().max()) <= grows_evenly(n, 2048) + 2.0 ** -20
 
 
+@pytest.mark.parametrize("m,K", [(64, 64), (16, 33), (9, 33)])     # by TMA, and element by element
+@pytest.mark.parametrize("rows", [65537, 1 << 20])
+def test_narrow_gradients_of_many_rows(blk, rows, m, K):
+    """A dw of 16 bits over many rows of one sign: its sum is off by less than its rounding.
+    Chains of 65536 steps, an instruction of 16 terms truncated by at most 2^-22 of the sum so
+    far (half of the whole on average), joined in fp32: 5e-4, and half a step of fp16."""
+    g = torch.Generator(device="cuda").manual_seed(rows + m)
+    x = torch.rand((rows, K), generator=g, device="cuda").to(HF)
+    gu, dh = torch.ones((rows, 2 * m), dtype=HF, device="cuda"), torch.full((rows, m), 2.0 ** -8, dtype=HF, device="cuda")
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    ref = x.to(F64).sum(0) / 256
+    tol = 65536 / 16 / 2 * 2.0 ** -22 + 16 * 2.0 ** -24 + 2.0 ** -11
+    dw = blk.gated_backward(dh, x, torch.zeros((1, 2 * m, K), dtype=HF, device="cuda"), off, gu, act="relu", need_dx=False)[1]
+    assert dw.dtype == HF and float((dw.to(F64) / ref - 1).abs().max()) <= tol
+    w, labels = torch.zeros((256, K), dtype=HF, device="cuda"), torch.zeros(rows, dtype=torch.int64, device="cuda")
+    lse = blk.vocab_loss_forward(x, w, labels)[1]
+    dw = blk.vocab_loss_backward(None, x, w, labels, lse, dlse=torch.ones(rows, device="cuda"), need_dx=False)[1]
+    assert dw.dtype == HF and float((dw.to(F64) / ref - 1).abs().max()) <= tol + 2.0 ** -20
+
+
 # ---------------------------------------------------------------- gradients
 def test_clip_without_a_limit(blk):
     """max_norm = inf scales nothing, whatever the norm but NaN (the quotient inf / inf is one)."""
