@@ -5,6 +5,8 @@ import math
 import pytest
 import torch
 
+from oracle import step
+
 pytestmark = pytest.mark.gpu
 
 BF, HF, FP, F64 = torch.bfloat16, torch.float16, torch.float32, torch.float64
@@ -117,6 +119,37 @@ def test_narrow_gradients_of_many_rows(blk, rows, m, K):
     lse = blk.vocab_loss_forward(x, w, labels)[1]
     dw = blk.vocab_loss_backward(None, x, w, labels, lse, dlse=torch.ones(rows, device="cuda"), need_dx=False)[1]
     assert dw.dtype == HF and float((dw.to(F64) / ref - 1).abs().max()) <= tol + 2.0 ** -20
+
+
+@pytest.mark.parametrize("cols", [1104, 1101])   # by TMA and element by element
+def test_wide_gradients_of_many_rows_and_tiles(blk, cols):
+    """Several accumulators per tile, several tiles per CTA pair, experts of one chain and of more:
+    tolerances of test_gpu_r_step.py."""
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    rand = lambda *s: torch.randn(s, generator=g, device="cuda").to(BF)  # noqa: E731
+    off, m = [0, 9000, 9000, 17192, 17200, 36000], 900
+    rows, E = off[-1], len(off) - 1
+    x, w, dh, gu = rand(rows, cols), torch.zeros((E, 2 * m, cols), dtype=BF, device="cuda"), rand(rows, m), rand(rows, 2 * m)
+    dw = blk.gated_backward(dh, x, w, torch.tensor(off, dtype=torch.int32, device="cuda"), gu, act="relu", need_dx=False,
+                            dw_dtype=FP)[1]
+    value = torch.clamp(gu[:, :m].double(), min=0.0)
+    terms = torch.cat([dh.double() * gu[:, m:].double() * (gu[:, :m] > 0), dh.double() * value], 1)
+    dgu = terms.to(BF).double()                  # as the products take it
+    for e in range(E):
+        a, b = off[e], off[e + 1]
+        ref, size = dgu[a:b].T @ x[a:b].double(), dgu[a:b].abs().T @ x[a:b].double().abs()
+        # where a product of three lies on the border of two bf16 numbers its fp32 form may round to the other
+        slack = (2.0 ** -8 * terms[a:b].abs() * ((terms[a:b].float().to(BF).double() - dgu[a:b]) != 0)).T @ x[a:b].double().abs()
+        tol = (b - a + 32) * 2.0 ** -22 * size + slack + 2.0 ** -20 * size
+        assert bool(((dw[e].double() - ref).abs() <= tol).all()), e
+    V, rows = 5000, 7000
+    x, w = rand(rows, cols), rand(V, cols) * cols ** -0.5
+    labels = torch.randint(-1, V, (rows,), generator=g, device="cuda")
+    lse = blk.vocab_loss_forward(x, w, labels)[1]
+    dloss = torch.rand(rows, generator=g, device="cuda")
+    dw = blk.vocab_loss_backward(dloss, x, w, labels, lse, need_dx=False, dw_dtype=FP)[1]
+    r = step.vocab_backward(dloss, None, x, w, labels, lse, 2.0 ** -8, cols + 32)
+    assert bool(((dw.double() - r["dw"]).abs() <= r["tol_dw"] + 2.0 ** -24 * r["dw"].abs() + 2.0 ** -25).all())
 
 
 # ---------------------------------------------------------------- gradients
