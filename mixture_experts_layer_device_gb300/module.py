@@ -322,8 +322,8 @@ class VocabLoss(torch.nn.Module):
 def clip_gradients(parameters, max_norm, masters=None, eps=1e-6):
     """Scales the gradients of `parameters` so that their common norm is at most max_norm
     (block.grad_clip) and returns the norm of before, a 0-d tensor.  With `masters`, a
-    list of fp32 tensors in the parameters' order, the gradients are left alone and the
-    masters' .grad get the scaled ones.  Parameters without a gradient are left out
+    list of fp32 tensors of the parameters' shapes and in their order, the gradients are left
+    alone and the masters' .grad get the scaled ones.  Parameters without a gradient are left out
     (their master's .grad becomes None)."""
     parameters = list(parameters)
     grads = [p.grad for p in parameters if p.grad is not None]
