@@ -142,6 +142,18 @@ def test_wide_gradients_of_many_rows_and_tiles(blk, cols):
         slack = (2.0 ** -8 * terms[a:b].abs() * ((terms[a:b].float().to(BF).double() - dgu[a:b]) != 0)).T @ x[a:b].double().abs()
         tol = (b - a + 32) * 2.0 ** -22 * size + slack + 2.0 ** -20 * size
         assert bool(((dw[e].double() - ref).abs() <= tol).all()), e
+    offsets, w = torch.tensor(off, dtype=torch.int32, device="cuda"), rand(E, 2 * m, cols)
+    dx, both = blk.gated_backward(dh, x, w, offsets, gu, act="relu", dw_dtype=FP)     # beside the data gradient
+    assert torch.equal(both, dw) and torch.equal(dx, blk.gated_backward(dh, x, w, offsets, gu, act="relu", need_dw=False)[0])
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        again = blk.gated_backward(dh, x, w, offsets, gu, act="relu", dw_dtype=FP)
+    for _ in range(2):
+        again[1].fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
     V, rows = 5000, 7000
     x, w = rand(rows, cols), rand(V, cols) * cols ** -0.5
     labels = torch.randint(-1, V, (rows,), generator=g, device="cuda")
